@@ -80,7 +80,12 @@ typedef enum mqa_kv_dtype {
      * inline, after its codes; see gqa_paged_decode. */
     MQA_KV_FP8_E4M3_PER_TOKEN_HEAD = 2,
     MQA_KV_INT8_PER_TOKEN_HEAD = 3,
-    MQA_KV_INT4_PER_TOKEN_HEAD = 4
+    MQA_KV_INT4_PER_TOKEN_HEAD = 4,
+    /* 8-bit GQA caches with one scale per (block of tokens, plane, KV head) in
+     * a tensor of their own (gqa_block_decode, gqa_window_decode,
+     * gqa_rope_append). */
+    MQA_KV_FP8_E4M3_BLOCK = 5,
+    MQA_KV_INT8_BLOCK = 6
 } mqa_kv_dtype;
 
 /* ABI version of the loaded library (MQA_ABI_VERSION at build time). */
@@ -422,6 +427,146 @@ mqa_status gqa_paged_decode(const void* q, const void* kv_cache, const int32_t* 
                             int head_size, int num_blocks, int page_size, int max_blocks,
                             mqa_kv_dtype kv_dtype, int num_kv_splits, void* workspace,
                             size_t workspace_bytes, int* device_status, void* stream);
+
+/* ---- Block-scaled caches, sliding windows, and writing the caches ---------
+ *
+ * A block-scaled GQA cache is [num_blocks, 2, page_size, num_kv_heads,
+ * head_size] codes (e4m3, or int8 in [-127, 127]) beside
+ *   kv_scales  fp32 [num_blocks, 2, page_size / scale_block, num_kv_heads]:
+ *              the scale of each block of scale_block tokens of a page, of
+ *              the K (0) or V (1) plane and of each KV head;
+ *              value = scale * code.  Scales are >= 0, zero or normal.
+ *   scale_block is a multiple of 16 that divides page_size. */
+
+/* Workspace bytes of gqa_window_decode and gqa_block_decode: 0 for
+ * num_kv_splits == 1, else batch * ceil(rows / 16) * num_kv_splits *
+ * num_kv_heads * min(rows, 16) * (head_size + 1) * 4 with rows = q_len *
+ * num_q_heads / num_kv_heads.  0 on invalid arguments. */
+size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
+                                         int num_kv_splits);
+
+/* The smallest num_kv_splits (at least 2) with which gqa_window_decode and
+ * gqa_block_decode can spread such a batch over the whole current device; -1
+ * on invalid arguments or without a device. */
+int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_heads);
+
+/* GQA paged decode under a sliding window, the first tokens staying visible.
+ *
+ * Query i of q_len sits at position p = seq_lens[b] - q_len + i (its own key
+ * and value are already in the cache) and sees key t iff
+ *   t <= p  and  (t < sinks  or  t > p - window),
+ * i.e. itself, the window - 1 keys before it and the first `sinks` keys;
+ *   x_t = scale <q, K_t>,  lse = ln sum_t e^{x_t},  out = sum_t e^{x_t - lse} V_t
+ * over the visible t.  A query without a visible key (p < 0) gets out = 0,
+ * lse = -inf.  Pages that hold no visible key are not read, nor are their
+ * block-table entries: a serving system may free them.  Bytes of tokens that
+ * no query sees never reach a result, whatever they hold; an Inf or NaN at a
+ * key reaches only the queries that see it.
+ *
+ *   q          bf16 [batch, q_len, num_q_heads, head_size] (contiguous);
+ *              query head h reads KV head h / (num_q_heads / num_kv_heads).
+ *   kv_cache, kv_dtype: MQA_KV_BF16 or MQA_KV_FP8_E4M3 as in
+ *              gqa_paged_decode, MQA_KV_FP8_E4M3_BLOCK or MQA_KV_INT8_BLOCK
+ *              with kv_scales / scale_block (else NULL / ignored).  With 8-bit
+ *              codes the query is taken in f16: entries within +-65504.
+ *   k_scale, v_scale  used by MQA_KV_FP8_E4M3 only.
+ *   window     >= 1 (2^30 and above: no window); sinks >= 0.
+ *   out        bf16 [batch, q_len, num_q_heads, head_size], fully written.
+ *   lse        fp32 [batch, q_len, num_q_heads] or NULL.
+ *   num_kv_splits  1: one thread block per request and 16 query rows, in a
+ *              fixed order (reproducible, independent of the rest of the
+ *              batch); more: the batch's visible tokens cut into units of
+ *              equal size, num_kv_splits - 1 per request on average at most.
+ *              Results are reproducible at any value.
+ *   workspace  gqa_window_decode_workspace_bytes(...) bytes; its contents do
+ *              not matter.  Calls that may overlap need one each.
+ *   head_size in {64, 128}; num_kv_heads in [1, 8]; at most 16 query heads per
+ *   KV head; q_len * num_q_heads / num_kv_heads <= 128; batch * ceil(that /
+ *   16) <= 2048; page_size a multiple of 16.  Other arguments and errors as
+ *   for mla_decode. */
+mqa_status gqa_window_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                             const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window,
+                             int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,
+                             int num_kv_heads, int head_size, int num_blocks, int page_size, int max_blocks,
+                             int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits, void* workspace,
+                             size_t workspace_bytes, int* device_status, void* stream);
+
+/* GQA paged decode over a block-scaled cache (MQA_KV_FP8_E4M3_BLOCK or
+ * MQA_KV_INT8_BLOCK): gqa_window_decode without a window. */
+mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, void* out, float* lse, int batch, int q_len,
+                            int num_q_heads, int num_kv_heads, int head_size, int num_blocks, int page_size,
+                            int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits,
+                            void* workspace, size_t workspace_bytes, int* device_status, void* stream);
+
+/* Appends the keys and values of a ragged batch of new tokens to a paged GQA
+ * cache, rotating the keys (and the queries) to their positions.
+ *
+ * Request b brings tokens query_start[b] .. query_start[b + 1] - 1 (none if
+ * equal); the last of them has position seq_lens[b] - 1, so seq_lens are the
+ * lengths that the decode entry points take next.  Token rows outside
+ * [query_start[0], query_start[batch]) are padding: neither read into the
+ * cache nor written in q_out.  With c, s the two halves of row p of cos_sin,
+ * each pair (x, y) of the first rotary_dim columns of a query or key row at
+ * position p becomes (x c - y s, y c + x s); pair i is columns (i, i +
+ * rotary_dim / 2), or (2i, 2i + 1) if interleaved.  Arithmetic in fp32.
+ *
+ *   q, k, v    bf16 [num_tokens, heads, head_size] with token strides in
+ *              elements (multiples of 8, at least a token's row: slices of a
+ *              fused projection will do); q and q_out both NULL: no queries.
+ *   q_out      bf16, token stride q_out_stride; may be q itself.
+ *   cos_sin    fp32 [max_position, rotary_dim]: cosines, then sines;
+ *              rotary_dim a multiple of 16, at most head_size.
+ *   query_start int32 [batch + 1], ascending, at most num_tokens.
+ *   kv_cache   any GQA cache of mqa_kv_dtype, laid out as the decode entry
+ *              points read it.  A value x is stored as
+ *                bf16             x;
+ *                FP8_E4M3         e4m3(x / k_scale or v_scale) (non-zero);
+ *                *_PER_TOKEN_HEAD s = max|x| / 448, 127 or 7 over the row, its
+ *                                 codes round(x / s);
+ *                *_BLOCK          s = max(s_old, max|x| / 448 or 127) over the
+ *                                 new rows of the block; where the block held
+ *                                 earlier tokens of the request and s > s_old,
+ *                                 their codes become round(code * s_old / s).
+ *                                 A block whose first token is new starts
+ *                                 from s_old = 0 whatever it held.
+ *              Codes saturate; scales below 2^-126 become 0 with codes 0.
+ *   kv_scales, scale_block  the block formats' only (else NULL / ignored).
+ *   No two requests of a call may append to the same physical block.
+ *   num_tokens 0 .. 2^24; batch up to 2^20; num_kv_heads up to 8; num_q_heads
+ *   up to 1024; page_size a multiple of 16.
+ * A request with seq_lens[b] < its new tokens, a position without a row in
+ * cos_sin or a page in the table, or a block id outside [0, num_blocks) raises
+ * MQA_ERR_DEVICE_CHECK in *device_status; the cells concerned (of a block
+ * format: the block's new tokens) are not written.  Enqueues one kernel;
+ * allocates nothing. */
+mqa_status gqa_rope_append(const void* q, const void* k, const void* v, const float* cos_sin,
+                           const int32_t* query_start, const int32_t* seq_lens, const int32_t* block_table,
+                           void* q_out, void* kv_cache, float* kv_scales, float k_scale, float v_scale,
+                           int num_tokens, int batch, int num_q_heads, int num_kv_heads, int head_size,
+                           int rotary_dim, int interleaved, int max_position, int num_blocks, int page_size,
+                           int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, long long q_stride,
+                           long long k_stride, long long v_stride, long long q_out_stride, int* device_status,
+                           void* stream);
+
+/* The same for an MLA cache (bf16 or e4m3): row [kv_c | k_pe] of each new
+ * token with its 64 k_pe columns rotated, and the rotary part q_pe of every
+ * query head rotated into the absorbed query's last 64 columns (q_pe_out
+ * with a head stride of head_size), or in place.
+ *
+ *   kv_c       bf16 [num_tokens, kv_lora_rank], k_pe bf16 [num_tokens, 64],
+ *              each with a token stride; e4m3 stores e4m3(x / k_scale).
+ *   q_pe, q_pe_out  bf16 [num_tokens, num_heads, 64] with token and head
+ *              strides; both NULL: no queries.
+ *   cos_sin    fp32 [max_position, 64].  head_size / kv_lora_rank 576/512 or
+ *              320/256.  Other arguments and errors as for gqa_rope_append. */
+mqa_status mla_rope_append(const void* kv_c, const void* k_pe, const void* q_pe, const float* cos_sin,
+                           const int32_t* query_start, const int32_t* seq_lens, const int32_t* block_table,
+                           void* q_pe_out, void* kv_cache, float k_scale, int num_tokens, int batch, int num_heads,
+                           int head_size, int kv_lora_rank, int interleaved, int max_position, int num_blocks,
+                           int page_size, int max_blocks, mqa_kv_dtype kv_dtype, long long kv_c_stride,
+                           long long k_pe_stride, long long q_pe_stride, long long q_pe_head_stride,
+                           long long q_out_stride, long long q_out_head_stride, int* device_status, void* stream);
 
 #ifdef __cplusplus
 }

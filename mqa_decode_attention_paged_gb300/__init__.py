@@ -20,8 +20,10 @@ def __getattr__(name):
     exported = {
         "mla_decode", "mla_decode_fixed_splits", "mla_decode_multi", "mla_decode_sparse", "gqa_paged_decode", "lse_merge", "num_kv_splits",
         "mla_decode_workspace_bytes", "gqa_paged_decode_workspace_bytes", "status_string", "abi_version", "device_sm_count",
-        "MqaError",
+        "gqa_window_decode", "gqa_block_decode", "gqa_window_decode_workspace_bytes", "gqa_window_num_kv_splits",
+        "gqa_rope_append", "mla_rope_append", "MqaError",
     }
     if name in exported:
-        return getattr(_load_binding(), name)
+        value = globals()[name] = getattr(_load_binding(), name)
+        return value
     raise AttributeError(name)

@@ -25,8 +25,11 @@ KV_FP8_E4M3 = 1
 KV_FP8_E4M3_PER_TOKEN_HEAD = 2
 KV_INT8_PER_TOKEN_HEAD = 3
 KV_INT4_PER_TOKEN_HEAD = 4
+KV_FP8_E4M3_BLOCK = 5
+KV_INT8_BLOCK = 6
 _KV_NAMES = {"bf16": KV_BF16, "fp8_e4m3": KV_FP8_E4M3, "fp8_e4m3_pth": KV_FP8_E4M3_PER_TOKEN_HEAD,
-             "int8_pth": KV_INT8_PER_TOKEN_HEAD, "int4_pth": KV_INT4_PER_TOKEN_HEAD}
+             "int8_pth": KV_INT8_PER_TOKEN_HEAD, "int4_pth": KV_INT4_PER_TOKEN_HEAD,
+             "fp8_e4m3_block": KV_FP8_E4M3_BLOCK, "int8_block": KV_INT8_BLOCK}
 
 LIB_PATH = _build.LIB_PATH
 
@@ -75,6 +78,21 @@ def _load() -> ctypes.CDLL:
     lib.mla_decode_noalloc.argtypes = [P, P, P, P, F, F, P, P, I, I, I, I, I, I, I, I, I, P, P]
     lib.gqa_paged_decode.restype = I
     lib.gqa_paged_decode.argtypes = [P, P, P, P, F, F, F, P, P, I, I, I, I, I, I, I, I, I, P, SZ, P, P]
+    LL = ctypes.c_longlong
+    lib.gqa_window_decode_workspace_bytes.restype = SZ
+    lib.gqa_window_decode_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gqa_window_num_kv_splits.restype = I
+    lib.gqa_window_num_kv_splits.argtypes = [I, I, I, I]
+    lib.gqa_window_decode.restype = I
+    lib.gqa_window_decode.argtypes = [P, P, P, P, P, F, F, F, I, I, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P]
+    lib.gqa_block_decode.restype = I
+    lib.gqa_block_decode.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P]
+    lib.gqa_rope_append.restype = I
+    lib.gqa_rope_append.argtypes = [P, P, P, P, P, P, P, P, P, P, F, F, I, I, I, I, I, I, I, I, I, I, I, I, I, LL, LL,
+                                    LL, LL, P, P]
+    lib.mla_rope_append.restype = I
+    lib.mla_rope_append.argtypes = [P, P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, I, LL, LL, LL, LL, LL,
+                                    LL, P, P]
     lib.mqa_lse_merge.restype = I
     lib.mqa_lse_merge.argtypes = [P, P, P, P, I, ctypes.c_longlong, I, P]
     lib.mqa_dcp_shard_max_blocks.restype = I
@@ -468,3 +486,292 @@ def mla_decode_noalloc(q, kv_cache, block_table, seq_lens, scale, k_scale=1.0, *
     if rc != OK:
         raise MqaError(rc, "mla_decode_noalloc")
     return out, lse
+
+
+def gqa_window_decode_workspace_bytes(batch: int, q_len: int, num_q_heads: int, num_kv_heads: int, head_size: int,
+                                      num_kv_splits: int) -> int:
+    return int(lib.gqa_window_decode_workspace_bytes(batch, q_len, num_q_heads, num_kv_heads, head_size,
+                                                     num_kv_splits))
+
+
+def gqa_window_num_kv_splits(batch: int, q_len: int, num_q_heads: int, num_kv_heads: int) -> int:
+    """The smallest num_kv_splits that lets gqa_window_decode / gqa_block_decode fill the current device."""
+    n = int(lib.gqa_window_num_kv_splits(batch, q_len, num_q_heads, num_kv_heads))
+    if n < 0:
+        raise ValueError("no device, or a head layout that gqa_window_decode does not serve")
+    return n
+
+
+def _on_current(dev):
+    """The stream the caller works on, for a call on device `dev`; None if `dev` is not the current device."""
+    import torch
+    return torch.cuda.current_stream(dev) if dev.index == torch.cuda.current_device() else None
+
+
+def _call_stream(stream, current, allocated):
+    """The raw stream of a call.  Tensors that the call allocated (on the current stream) are recorded on a
+    stream that the caller passes, so that their memory is not reused while that stream still works on them."""
+    import torch
+    if stream is None:
+        return current.cuda_stream
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if raw != current.cuda_stream and allocated:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(raw, device=current.device)
+        s.wait_stream(current)
+        for t in allocated:
+            t.record_stream(s)
+    return raw
+
+
+def _block_code(kv_cache, kv_scales, kv_dtype):
+    """kv_dtype code of a cache that may have block scales."""
+    import torch
+    if kv_dtype is not None or kv_scales is None:
+        return _kv_code(kv_cache, kv_dtype)
+    if kv_cache.dtype == torch.float8_e4m3fn:
+        return KV_FP8_E4M3_BLOCK
+    if kv_cache.dtype == torch.int8:
+        return KV_INT8_BLOCK
+    raise TypeError("a block-scaled kv_cache is float8_e4m3fn or int8 (or pass kv_dtype with uint8 storage)")
+
+
+def _scale_block(kv_scales, code, nb, page, hkv):
+    """Tokens per scale of kv_scales [num_blocks, 2, page / scale_block, num_kv_heads]; 0 for the other formats."""
+    import torch
+    if code not in (KV_FP8_E4M3_BLOCK, KV_INT8_BLOCK):
+        if kv_scales is not None:
+            raise ValueError("kv_scales is for the fp8_e4m3_block and int8_block caches only")
+        return 0
+    if kv_scales is None:
+        raise ValueError("kv_scales is required")
+    s = kv_scales.shape
+    if len(s) != 4 or s[0] != nb or s[1] != 2 or s[2] < 1 or page % s[2] != 0 or s[3] != hkv:
+        raise ValueError(f"kv_scales must be [{nb}, 2, page / scale_block, {hkv}], got {tuple(s)}")
+    _check(kv_scales, "kv_scales", (torch.float32,))
+    return page // s[2]
+
+
+def gqa_window_decode(q, kv_cache, block_table, seq_lens, scale, window, sinks=0, *, kv_scales=None, k_scale=1.0,
+                      v_scale=1.0, out=None, lse=None, num_kv_splits=None, workspace=None, kv_dtype=None,
+                      device_status=None, stream=None, return_lse=True):
+    """GQA paged decode under a sliding window through the C ABI: the query at position p sees key t iff t <= p and
+    (t < sinks or t > p - window).  q bf16 [B, Hq, D], or [B, q_len, Hq, D] for q_len new positions per request
+    (the last at seq_lens - 1); kv_cache [num_blocks, 2, page, Hkv, D] bf16 or e4m3 (k_scale / v_scale), or e4m3 /
+    int8 codes with kv_scales fp32 [num_blocks, 2, page / scale_block, Hkv].  Returns out like q and lse fp32 like
+    q without its last dimension.  num_kv_splits None fills the device; out / lse / workspace are allocated with
+    torch when they are not given."""
+    return _window_decode("gqa_window_decode", q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale,
+                          window, sinks, out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream,
+                          return_lse)
+
+
+def gqa_block_decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, *, out=None, lse=None, num_kv_splits=None,
+                     workspace=None, kv_dtype=None, device_status=None, stream=None, return_lse=True):
+    """GQA paged decode over a block-scaled 8-bit cache through the C ABI: kv_cache e4m3 or int8 codes
+    [num_blocks, 2, page, Hkv, D], kv_scales fp32 [num_blocks, 2, page / scale_block, Hkv].  q and the other
+    arguments as for :func:`gqa_window_decode`, without a window."""
+    return _window_decode("gqa_block_decode", q, kv_cache, kv_scales, block_table, seq_lens, scale, 1.0, 1.0, None, 0,
+                          out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse)
+
+
+def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale, window, sinks, out,
+                   lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse):
+    import torch
+    if q.dim() not in (3, 4) or kv_cache.dim() != 5:
+        raise ValueError("q must be [batch, (q_len,) heads, head_size] and kv_cache have 5 dimensions")
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    L = q.shape[1] if q.dim() == 4 else 1
+    nb, two, page, Hkv, D2 = kv_cache.shape
+    code = _block_code(kv_cache, kv_scales, kv_dtype)
+    if two != 2 or D2 != D:
+        raise ValueError(f"kv_cache must be [num_blocks, 2, page, num_kv_heads, {D}]")
+    block = _scale_block(kv_scales, code, nb, page, Hkv)
+    if name == "gqa_block_decode" and block == 0:
+        raise ValueError("gqa_block_decode reads block-scaled caches (fp8_e4m3_block, int8_block)")
+    _check_common(q, kv_cache, code, block_table, seq_lens, q if out is None else out, q.shape, lse, q.shape[:-1],
+                  workspace, device_status, extra=(("kv_scales", kv_scales),))
+    current = _on_current(q.device)
+    if current is None:
+        with torch.cuda.device(q.device):
+            return _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale,
+                                  window, sinks, out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream,
+                                  return_lse)
+    fresh = []
+    if out is None:
+        out = torch.empty_like(q)
+        fresh.append(out)
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        fresh.append(lse)
+    if num_kv_splits is None:
+        num_kv_splits = max(1, int(lib.gqa_window_num_kv_splits(B, L, Hq, Hkv)))
+    if workspace is None:
+        need = int(lib.gqa_window_decode_workspace_bytes(B, L, Hq, Hkv, D, num_kv_splits))
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            fresh.append(workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    raw = _call_stream(stream, current, fresh)
+    head = (_ptr(q), _ptr(kv_cache), _ptr(kv_scales), _ptr(block_table), _ptr(seq_lens), float(scale))
+    tail = (_ptr(out), _ptr(lse), B, L, Hq, Hkv, D, nb, page, block_table.shape[1], block, code, int(num_kv_splits),
+            _ptr(workspace), ws_bytes, _ptr(device_status), raw)
+    if window is None:
+        rc = lib.gqa_block_decode(*head, *tail)
+    else:
+        rc = lib.gqa_window_decode(*head, float(k_scale), float(v_scale), int(window), int(sinks), *tail)
+    if rc != OK:
+        raise MqaError(rc, name)
+    return out, lse
+
+
+def _check_rows(t, name, shape, dense):
+    """A bf16 tensor of shape `shape` whose last `dense` dimensions are dense (rows of a wider tensor will do);
+    returns its leading strides."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st, want = t.stride(), 1
+    for i in range(1, dense + 1):
+        if shape[-i] != 1 and st[-i] != want:
+            raise ValueError(f"the last {dense} dimension(s) of {name} must be contiguous")
+        want *= shape[-i]
+    # a dimension of one has no stride of its own: any that holds a row will do
+    out = []
+    for i in range(len(shape) - dense - 1, -1, -1):
+        s = st[i] if shape[i] > 1 else want
+        out.insert(0, s)
+        want = max(want, s * shape[i])
+    return out
+
+
+def _check_append(cos_sin, width, kv_cache, block_table, seq_lens, query_start, device_status, named):
+    import torch
+    _check(cos_sin, "cos_sin", (torch.float32,))
+    if cos_sin.dim() != 2 or (width is not None and cos_sin.shape[1] != width):
+        raise ValueError(f"cos_sin must be fp32 [max_position, {width or 'rotary_dim'}]")
+    _check(kv_cache, "kv_cache")
+    _check(block_table, "block_table", (torch.int32,))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, max_blocks]")
+    B = block_table.shape[0]
+    _check(seq_lens, "seq_lens", (torch.int32,), shape=(B,))
+    _check(query_start, "query_start", (torch.int32,), shape=(B + 1,))
+    _check(device_status, "device_status", (torch.int32,), optional=True)
+    _on_device([*named, ("cos_sin", cos_sin), ("kv_cache", kv_cache), ("block_table", block_table),
+                ("seq_lens", seq_lens), ("query_start", query_start), ("device_status", device_status)])
+    return B
+
+
+def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start, *, q=None, q_out=None,
+                    kv_scales=None, k_scale=1.0, v_scale=1.0, interleaved=False, kv_dtype=None, device_status=None,
+                    stream=None):
+    """Append new keys and values to a paged GQA cache through the C ABI, keys (and queries) rotated to their
+    positions.  k, v bf16 [T, Hkv, D] and q [T, Hq, D] may be slices of a fused projection (any token stride that
+    is a multiple of 8); request b brings tokens query_start[b] .. query_start[b + 1] - 1 (int32 [B + 1]), the last
+    at position seq_lens[b] - 1; tokens behind query_start[B] are padding.  cos_sin fp32 [max_position, rotary_dim]
+    holds cosines, then sines; interleaved pairs are columns (2i, 2i + 1).  kv_cache is any cache that the GQA
+    decode calls read, with kv_scales for the block-scaled formats; both are updated in place.  Returns the rotated
+    queries (q_out, which may be q itself; allocated when only q is given), or None."""
+    import torch
+    if k.dim() != 3 or kv_cache.dim() != 5 or cos_sin.dim() != 2:
+        raise ValueError("k must be [tokens, heads, head_size], kv_cache have 5 dimensions and cos_sin 2")
+    T, Hkv, D = k.shape
+    nb, two, page, Hkv2, row = kv_cache.shape
+    code = _block_code(kv_cache, kv_scales, kv_dtype)
+    want = {KV_FP8_E4M3_PER_TOKEN_HEAD: D + 4, KV_INT8_PER_TOKEN_HEAD: D + 4,
+            KV_INT4_PER_TOKEN_HEAD: D // 2 + 4}.get(code, D)
+    if two != 2 or Hkv2 != Hkv or row != want:
+        raise ValueError(f"kv_cache must be [num_blocks, 2, page, {Hkv}, {want}]")
+    if kv_cache.element_size() != (2 if code == KV_BF16 else 1):
+        raise TypeError(f"kv_cache must have {2 if code == KV_BF16 else 1}-byte elements, got {kv_cache.dtype}")
+    block = _scale_block(kv_scales, code, nb, page, Hkv)
+    ks, = _check_rows(k, "k", (T, Hkv, D), 2)
+    vs, = _check_rows(v, "v", (T, Hkv, D), 2)
+    qs = qos = Hq = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads, head_size]")
+        Hq = q.shape[1]
+        qs, = _check_rows(q, "q", (T, Hq, D), 2)
+        if q_out is not None:
+            qos, = _check_rows(q_out, "q_out", (T, Hq, D), 2)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    B = _check_append(cos_sin, None, kv_cache, block_table, seq_lens, query_start, device_status,
+                      (("k", k), ("v", v), ("q", q), ("q_out", q_out), ("kv_scales", kv_scales)))
+    current = _on_current(k.device)
+    if current is None:
+        with torch.cuda.device(k.device):
+            return gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start, q=q, q_out=q_out,
+                                   kv_scales=kv_scales, k_scale=k_scale, v_scale=v_scale, interleaved=interleaved,
+                                   kv_dtype=kv_dtype, device_status=device_status, stream=stream)
+    fresh = []
+    if q is not None and q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        qos = Hq * D
+        fresh.append(q_out)
+    if T == 0:
+        return q_out
+    rc = lib.gqa_rope_append(_ptr(q), _ptr(k), _ptr(v), _ptr(cos_sin), _ptr(query_start), _ptr(seq_lens),
+                             _ptr(block_table), _ptr(q_out), _ptr(kv_cache), _ptr(kv_scales), float(k_scale),
+                             float(v_scale), T, B, Hq, Hkv, D, cos_sin.shape[1], int(bool(interleaved)),
+                             cos_sin.shape[0], nb, page, block_table.shape[1], block, code, qs, ks, vs, qos,
+                             _ptr(device_status), _call_stream(stream, current, fresh))
+    if rc != OK:
+        raise MqaError(rc, "gqa_rope_append")
+    return q_out
+
+
+def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_start, *, q_pe=None, q_pe_out=None,
+                    k_scale=1.0, interleaved=False, kv_dtype=None, device_status=None, stream=None):
+    """Append new latent rows [kv_c | rotated k_pe] to a paged MLA cache (bf16, or e4m3 with k_scale) through the C
+    ABI.  kv_c bf16 [T, R] and k_pe [T, 64] may be slices of one projection; q_pe [T, H, 64] is rotated into
+    q_pe_out (for instance ``q[..., R:]`` of the absorbed query; may be q_pe itself; allocated when only q_pe is
+    given), which is returned (None without q_pe).  cos_sin fp32 [max_position, 64]; the batch is described as for
+    :func:`gqa_rope_append`."""
+    import torch
+    if kv_c.dim() != 2 or kv_cache.dim() != 3:
+        raise ValueError("kv_c must be [tokens, kv_lora_rank] and kv_cache [num_blocks, page, head_size]")
+    T, R = kv_c.shape
+    nb, page, D = kv_cache.shape
+    if D != R + 64:
+        raise ValueError(f"kv_cache must be [num_blocks, page, {R + 64}]")
+    code = _kv_code(kv_cache, kv_dtype)
+    if kv_cache.element_size() != (2 if code == KV_BF16 else 1):
+        raise TypeError(f"kv_cache must have {2 if code == KV_BF16 else 1}-byte elements, got {kv_cache.dtype}")
+    cs, = _check_rows(kv_c, "kv_c", (T, R), 1)
+    ps, = _check_rows(k_pe, "k_pe", (T, 64), 1)
+    H = qs = qhs = qos = qohs = 0
+    if q_pe is not None:
+        if q_pe.dim() != 3:
+            raise ValueError("q_pe must be [tokens, heads, 64]")
+        H = q_pe.shape[1]
+        qs, qhs = _check_rows(q_pe, "q_pe", (T, H, 64), 1)
+        if q_pe_out is not None:
+            qos, qohs = _check_rows(q_pe_out, "q_pe_out", (T, H, 64), 1)
+    elif q_pe_out is not None:
+        raise ValueError("q_pe_out without q_pe")
+    B = _check_append(cos_sin, 64, kv_cache, block_table, seq_lens, query_start, device_status,
+                      (("kv_c", kv_c), ("k_pe", k_pe), ("q_pe", q_pe), ("q_pe_out", q_pe_out)))
+    current = _on_current(kv_c.device)
+    if current is None:
+        with torch.cuda.device(kv_c.device):
+            return mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_start, q_pe=q_pe,
+                                   q_pe_out=q_pe_out, k_scale=k_scale, interleaved=interleaved, kv_dtype=kv_dtype,
+                                   device_status=device_status, stream=stream)
+    fresh = []
+    if q_pe is not None and q_pe_out is None:
+        q_pe_out = torch.empty((T, H, 64), dtype=torch.bfloat16, device=q_pe.device)
+        qos, qohs = H * 64, 64
+        fresh.append(q_pe_out)
+    if T == 0:
+        return q_pe_out
+    rc = lib.mla_rope_append(_ptr(kv_c), _ptr(k_pe), _ptr(q_pe), _ptr(cos_sin), _ptr(query_start), _ptr(seq_lens),
+                             _ptr(block_table), _ptr(q_pe_out), _ptr(kv_cache), float(k_scale), T, B, H, D, R,
+                             int(bool(interleaved)), cos_sin.shape[0], nb, page, block_table.shape[1], code, cs, ps,
+                             qs, qhs, qos, qohs, _ptr(device_status), _call_stream(stream, current, fresh))
+    if rc != OK:
+        raise MqaError(rc, "mla_rope_append")
+    return q_pe_out

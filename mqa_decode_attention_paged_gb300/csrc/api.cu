@@ -17,6 +17,7 @@
 #include "shard_merge.cuh"
 #include "dcp.cuh"
 #include "gqa_test.cuh"
+#include "api_common.cuh"
 
 namespace {
 
@@ -295,6 +296,10 @@ bool mla_tensor_map(CUtensorMap* out, const void* base, int cols, long long rows
 }
 
 }  // namespace
+
+mqa_status mqa::api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+PFN_cuTensorMapEncodeTiled_v12000 mqa::api_encode_tiled() { return encode_tiled_fn(); }
+int mqa::api_sm_count() { return sm_count_current(); }
 
 static mqa_status mla_decode_rows(const void* q, const void* kv_cache, const int32_t* block_table,
                       const int32_t* seq_lens, float scale, float k_scale, void* out, float* lse,

@@ -1,0 +1,202 @@
+// C ABI of windowed and block-scaled GQA decode: argument validation, the
+// work split and the launches.  See include/mqa_decode.h for the contract.
+#include <cmath>
+#include <cstring>
+
+#include "api_common.cuh"
+#include "gqa_win.cuh"
+
+namespace {
+
+using mqa::api_aligned;
+using mqa::api_cuda_fail;
+
+constexpr int kMaxRows = 128;  // query rows of a KV head: q_len * (num_q_heads / num_kv_heads)
+
+struct Rows {
+    int grp, rows, rb, rbn;
+};
+
+bool heads_ok(int batch, int q_len, int hq, int hkv) {
+    return batch >= 1 && q_len >= 1 && hq >= 1 && hkv >= 1 && hq % hkv == 0;
+}
+
+bool heads_served(int batch, int q_len, int hq, int hkv) {
+    const long long rows = static_cast<long long>(q_len) * (hq / hkv);
+    return hkv <= 8 && hq / hkv <= 16 && rows <= kMaxRows &&
+           batch <= mqa::kWinMaxVirtual / static_cast<int>((rows + 15) / 16);
+}
+
+Rows rows_of(int q_len, int hq, int hkv) {
+    Rows r;
+    r.grp = hq / hkv;
+    r.rows = q_len * r.grp;
+    r.rb = (r.rows + 15) / 16;
+    r.rbn = r.rows < 16 ? r.rows : 16;
+    return r;
+}
+
+// A 5D view of the cache, {line, page, panels, heads, 2 * blocks}, whose box
+// is box_tok tokens of every head of one plane: it lands as [head][panel]
+// [token][line] under the swizzle of its line (128 or 64 bytes).  Encoded per
+// call (a fraction of a microsecond): nothing is kept by an address.
+bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, int page, int blocks, int box_tok) {
+    auto fn = mqa::api_encode_tiled();
+    if (!fn) return false;
+    const int line = D * elt >= 128 ? 128 : D * elt;
+    const int inner = line / elt, panels = D / inner;
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(page),
+                                static_cast<cuuint64_t>(panels), static_cast<cuuint64_t>(hkv),
+                                static_cast<cuuint64_t>(blocks) * 2};
+    const cuuint64_t row = static_cast<cuuint64_t>(hkv) * D * elt;
+    const cuuint64_t strides[4] = {row, static_cast<cuuint64_t>(line), static_cast<cuuint64_t>(D) * elt, row * page};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(box_tok),
+                               static_cast<cuuint32_t>(panels), static_cast<cuuint32_t>(hkv), 1};
+    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    std::memset(out, 0, sizeof *out);
+    return fn(out, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5,
+              const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                  const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window, int sinks,
+                  void* out, float* lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
+                  int num_blocks, int page_size, int max_blocks, int scale_block, mqa_kv_dtype kv_dtype,
+                  int num_kv_splits, void* workspace, size_t workspace_bytes, int* device_status, void* stream) {
+    if (!q || !kv_cache || !block_table || !seq_lens || !out) return MQA_ERR_INVALID_ARG;
+    if (!api_aligned(q, 16) || !api_aligned(kv_cache, 16) || !api_aligned(out, 16) || !api_aligned(block_table, 4) ||
+        !api_aligned(seq_lens, 4) || (lse && !api_aligned(lse, 4)) ||
+        (device_status && !api_aligned(device_status, 4)))
+        return MQA_ERR_INVALID_ARG;
+    if (!heads_ok(batch, q_len, num_q_heads, num_kv_heads) || num_blocks < 1 || max_blocks < 1 || page_size < 1 ||
+        num_kv_splits < 1 || window < 1 || sinks < 0)
+        return MQA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return MQA_ERR_INVALID_ARG;
+    if (head_size != 64 && head_size != 128) return MQA_ERR_UNSUPPORTED;
+    if (!heads_served(batch, q_len, num_q_heads, num_kv_heads)) return MQA_ERR_UNSUPPORTED;
+    if (page_size % 16 != 0) return MQA_ERR_UNSUPPORTED;
+    const bool block = kv_dtype == MQA_KV_FP8_E4M3_BLOCK || kv_dtype == MQA_KV_INT8_BLOCK;
+    if (!block && kv_dtype != MQA_KV_BF16 && kv_dtype != MQA_KV_FP8_E4M3) return MQA_ERR_UNSUPPORTED;
+    if (kv_dtype == MQA_KV_FP8_E4M3 && (!std::isfinite(k_scale) || !std::isfinite(v_scale)))
+        return MQA_ERR_INVALID_ARG;
+    if (block) {
+        if (!kv_scales || !api_aligned(kv_scales, 4) || scale_block < 1) return MQA_ERR_INVALID_ARG;
+        if (scale_block % 16 != 0 || page_size % scale_block != 0) return MQA_ERR_UNSUPPORTED;
+    }
+    // positions stay clear of INT_MAX by more than a tile (128 tokens) and
+    // the tensor map's plane coordinate 2 * block + 1 stays an int
+    if (static_cast<long long>(max_blocks) * page_size > INT32_MAX - 256 ||
+        static_cast<long long>(num_blocks) * page_size > INT32_MAX)
+        return MQA_ERR_UNSUPPORTED;
+
+    const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
+    const size_t need = gqa_window_decode_workspace_bytes(batch, q_len, num_q_heads, num_kv_heads, head_size,
+                                                          num_kv_splits);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MQA_ERR_WORKSPACE_TOO_SMALL;
+    if (need > 0 && !api_aligned(workspace, 16)) return MQA_ERR_INVALID_ARG;
+    const int sms = mqa::api_sm_count();
+    if (sms < 1) return MQA_ERR_CUDA;
+
+    mqa::WinArgs a{};
+    const int elt = kv_dtype == MQA_KV_BF16 ? 2 : 1;
+    a.ts = mqa::win_subtiles(num_kv_heads);
+    // boxes of as many tokens as divide both the page and the tile
+    a.box_tok = 16;
+    while (a.box_tok < 16 * a.ts && page_size % (2 * a.box_tok) == 0) a.box_tok *= 2;
+    if (!cache_map(&a.tmap, kv_cache, elt, head_size, num_kv_heads, page_size, num_blocks, a.box_tok))
+        return api_cuda_fail(cudaErrorInvalidValue);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.kv_scales = block ? kv_scales : nullptr;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.status = device_status;
+    const bool per_tensor = kv_dtype == MQA_KV_FP8_E4M3;
+    a.sl2 = scale * (per_tensor ? k_scale : 1.0f) * mqa::kLog2e;
+    a.out_scale = per_tensor ? v_scale : 1.0f;
+    a.batch = batch;
+    a.q_len = q_len;
+    a.Hq = num_q_heads;
+    a.Hkv = num_kv_heads;
+    a.grp = r.grp;
+    a.rows = r.rows;
+    a.rb = r.rb;
+    a.rbn = r.rbn;
+    a.num_blocks = num_blocks;
+    a.page = page_size;
+    a.max_blocks = max_blocks;
+    a.window = window < mqa::kWinNoWindow ? window : mqa::kWinNoWindow;
+    a.sinks = sinks;
+    a.scale_block = block ? scale_block : 1;
+    a.scale_groups = block ? page_size / scale_block : 1;
+    const int vb = batch * r.rb;
+    if (num_kv_splits > 1) {
+        const size_t slots = static_cast<size_t>(vb) * num_kv_splits;
+        a.ws_o = static_cast<float*>(workspace);
+        a.ws_lse = a.ws_o + slots * num_kv_heads * r.rbn * head_size;
+        // units g and virtual requests v use slots g + v <= units + vb - 2
+        const long long cap = static_cast<long long>(vb) * (num_kv_splits - 1) + 1;
+        const long long fill = static_cast<long long>(sms) * mqa::win_ctas_per_sm(r.rbn);
+        a.units = static_cast<int>(fill < cap ? fill : cap);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int grid = a.units > 0 ? a.units : vb;
+    const cudaError_t e = kv_dtype == MQA_KV_BF16         ? mqa::win_stage1_bf16(a, head_size, grid, st)
+                          : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::win_stage1_int8(a, head_size, grid, st)
+                                                          : mqa::win_stage1_e4m3(a, head_size, grid, st);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    if (a.units > 0)
+        if (cudaError_t e2 = mqa::win_merge(a, head_size, st); e2 != cudaSuccess) return api_cuda_fail(e2);
+    return MQA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
+                                         int num_kv_splits) {
+    if (!heads_ok(batch, q_len, num_q_heads, num_kv_heads) || head_size < 1 || num_kv_splits < 2) return 0;
+    if (!heads_served(batch, q_len, num_q_heads, num_kv_heads)) return 0;
+    const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
+    return static_cast<size_t>(batch) * r.rb * num_kv_splits * num_kv_heads * r.rbn *
+           (static_cast<size_t>(head_size) + 1) * 4;
+}
+
+int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_heads) {
+    if (!heads_ok(batch, q_len, num_q_heads, num_kv_heads) ||
+        !heads_served(batch, q_len, num_q_heads, num_kv_heads))
+        return -1;
+    const int sms = mqa::api_sm_count();
+    if (sms < 1) return -1;
+    const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
+    const int vb = batch * r.rb, fill = sms * mqa::win_ctas_per_sm(r.rbn);
+    return 1 + (fill - 1 + vb - 1) / vb;  // the smallest budget that lets units fill the device (2 at least)
+}
+
+mqa_status gqa_window_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                             const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window,
+                             int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,
+                             int num_kv_heads, int head_size, int num_blocks, int page_size, int max_blocks,
+                             int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits, void* workspace,
+                             size_t workspace_bytes, int* device_status, void* stream) {
+    return decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale, window, sinks, out, lse,
+                  batch, q_len, num_q_heads, num_kv_heads, head_size, num_blocks, page_size, max_blocks, scale_block,
+                  kv_dtype, num_kv_splits, workspace, workspace_bytes, device_status, stream);
+}
+
+mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, void* out, float* lse, int batch, int q_len,
+                            int num_q_heads, int num_kv_heads, int head_size, int num_blocks, int page_size,
+                            int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits,
+                            void* workspace, size_t workspace_bytes, int* device_status, void* stream) {
+    if (kv_dtype != MQA_KV_FP8_E4M3_BLOCK && kv_dtype != MQA_KV_INT8_BLOCK) return MQA_ERR_UNSUPPORTED;
+    return decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, 1.0f, 1.0f, mqa::kWinNoWindow, 0, out, lse,
+                  batch, q_len, num_q_heads, num_kv_heads, head_size, num_blocks, page_size, max_blocks, scale_block,
+                  kv_dtype, num_kv_splits, workspace, workspace_bytes, device_status, stream);
+}
+
+}  // extern "C"

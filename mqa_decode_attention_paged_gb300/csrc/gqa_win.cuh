@@ -1,0 +1,106 @@
+// Windowed and block-scaled GQA paged decode: arguments, the visible-key plan
+// shared by the stage-1 kernels and the merge, and the host interface.
+//
+// A request's query rows (q_len positions x the query heads of a KV head) are
+// cut into row blocks of 16; request and row block together are one "virtual
+// request" v = b * rb + r with its own keys.  The query at position p sees
+// key t iff  t <= p and (t < sinks or t > p - window), so the keys of a row
+// block are the sinks [0, min(sinks, hi)) and the run [lo, hi), where hi is
+// its last position + 1 and lo = max(0, first position - window + 1).  They
+// are walked in tiles of TT = 16 TS consecutive tokens (TS subtiles of 16,
+// one per group of Hkv consumer warps); the tiles of all virtual requests are
+// laid end to end and cut into units of equal size, one per thread block, so
+// only tiles that hold a visible key are ever read.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace mqa {
+
+// Cache formats of the kernels.
+enum WinKind { kWinBf16 = 0, kWinE4m3 = 1, kWinInt8 = 2 };
+
+constexpr int kWinMaxVirtual = 2048;  // virtual requests whose tile prefix fits in shared memory
+constexpr int kWinNoWindow = 1 << 30;
+
+struct WinArgs {
+    CUtensorMap tmap;  // {inner, page tokens, panels, heads, 2 planes x blocks}
+    const __nv_bfloat16* q;   // [batch, q_len, Hq, D]
+    const float* kv_scales;   // [blocks, 2, page / scale_block, Hkv], or null: no block scales
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    __nv_bfloat16* out;
+    float* lse;
+    float* ws_o;    // [slots, Hkv, rbn, D], normalised partials
+    float* ws_lse;  // [slots, Hkv, rbn]
+    int* status;
+    float sl2;        // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
+    float out_scale;  // v_scale of a per-tensor e4m3 cache, else 1
+    int batch, q_len, Hq, Hkv, grp, rows;  // rows = q_len * grp: query rows of a KV head
+    int num_blocks, page, max_blocks;
+    int window, sinks;
+    int scale_block, scale_groups;  // tokens per scale, scales per page
+    int box_tok;                    // tokens of one copied box (divides the page and the tile)
+    int rb, rbn;                    // row blocks per request; rows of a (full) row block
+    int ts;                         // subtiles per tile
+    int units;                      // 0: one unit per virtual request, else the balanced unit count
+    int nslots;
+};
+
+// The tiles of one virtual request.
+struct WinVis {
+    int n;                // length of the request
+    int p_first, p_last;  // positions of the row block's first and last query token
+    int lo, hi;           // the windowed run of keys
+    int ns, w0;           // sink tiles; first tile of the run after them
+    int nt;               // tiles in all
+    __device__ __forceinline__ int tile(int j) const { return j < ns ? j : w0 + j - ns; }
+};
+
+__device__ __forceinline__ int win_len(const WinArgs& a, int b, int* status) {
+    const int n = __ldg(a.seq_lens + b);
+    const long long cap = static_cast<long long>(a.max_blocks) * a.page;
+    if (n < 0 || n > cap) {
+        report(status, MQA_ERR_DEVICE_CHECK);
+        return n < 0 ? 0 : static_cast<int>(cap);
+    }
+    return n;
+}
+
+__device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
+    WinVis v;
+    const int r0 = r * 16, r1 = min(a.rows, r0 + 16) - 1;
+    const int i0 = a.q_len == 1 ? 0 : r0 / a.grp, i1 = a.q_len == 1 ? 0 : r1 / a.grp;
+    const int tt = 16 * a.ts;
+    v.n = n;
+    v.p_first = n - a.q_len + i0;
+    v.p_last = n - a.q_len + i1;
+    v.hi = max(0, v.p_last + 1);
+    v.lo = max(0, v.p_first - a.window + 1);
+    const int s_end = min(a.sinks, v.hi);
+    v.ns = (s_end + tt - 1) / tt;
+    v.w0 = max(v.lo / tt, v.ns);
+    v.nt = v.ns + max(0, (v.hi + tt - 1) / tt - v.w0);
+    return v;
+}
+
+// Balanced mode with T tiles: units actually used.  A unit holds kWinMinTiles
+// tiles at least where there are enough, so that short work is not spread
+// over more partials than its merge is worth.
+constexpr int kWinMinTiles = 2;
+__device__ __forceinline__ int win_units(int units, int T) { return min(units, max(1, T / kWinMinTiles)); }
+
+// Subtiles per tile for Hkv KV heads: 8 consumer warps, or one per KV head
+// where Hkv does not divide 8 evenly.
+__host__ __device__ inline int win_subtiles(int hkv) { return hkv == 1 ? 8 : (hkv == 2 ? 4 : (hkv <= 4 ? 2 : 1)); }
+
+cudaError_t win_stage1_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t win_stage1_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t win_stage1_int8(const WinArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t win_merge(const WinArgs& a, int D, cudaStream_t stream);
+// Thread blocks of stage 1 resident on one SM.
+int win_ctas_per_sm(int rbn);
+
+}  // namespace mqa

@@ -1,0 +1,154 @@
+// Windowed / block-scaled GQA decode, stage 2: the partials of each row merged
+// by LogSumExp (out = sum_s w_s O_s / sum_s w_s, w_s = e^{lse_s - max lse},
+// lse = max + ln sum w; ascending units, so the result is reproducible).
+//
+// Bound by the latency of its few loads: a row has np partials of D fp32
+// values.  One warp per row where a row has few partials, a block of 8 warps
+// per row (each takes every eighth partial, then a sum through shared memory)
+// where few rows are cut into many; the host picks by the mean number of
+// partials.  Launched as a programmatic dependent of stage 1: the prefix of
+// tile counts, which needs the lengths only, is computed before the wait.
+#include "gqa_win.cuh"
+
+namespace mqa {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kInFlight = 8;  // partials of a row whose loads are issued together
+
+template <int V>
+struct Vec;
+template <>
+struct Vec<4> {
+    using T = float4;
+};
+template <>
+struct Vec<2> {
+    using T = float2;
+};
+
+// Sum of x over the block (all threads get it); `buf` holds kWarps ints.
+__device__ __forceinline__ int block_sum(int x, int* buf) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int s = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += buf[i];
+    return s;
+}
+
+// WPR: warps per row (1 or kWarps).
+template <int D, int WPR>
+__global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_constant__ WinArgs a) {
+    constexpr int V = D / 32;
+    using VecT = typename Vec<V>::T;
+    __shared__ int sums[kWarps];
+    __shared__ float part[WPR == 1 ? 1 : kWarps][D + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int v = blockIdx.x;
+    const int vb = a.batch * a.rb;
+
+    int before = 0, total = 0, mine = 0;
+    for (int i = threadIdx.x; i < vb; i += blockDim.x) {
+        const int b = a.rb == 1 ? i : i / a.rb;
+        const int nt = win_visible(a, i - b * a.rb, win_len(a, b, nullptr)).nt;
+        total += nt;
+        if (i < v) before += nt;
+        if (i == v) mine = nt;
+    }
+    total = block_sum(total, sums);
+    before = block_sum(before, sums);
+    mine = block_sum(mine, sums);
+
+    const int b = v / a.rb, r = v - b * a.rb;
+    const int item = WPR == 1 ? static_cast<int>(blockIdx.y) * kWarps + warp : static_cast<int>(blockIdx.y);
+    const int kh = item / a.rbn, jr = item - kh * a.rbn;
+    const int R = r * 16 + jr;
+    const bool row = kh < a.Hkv && R < a.rows;
+    int gf = 0, np = 0;
+    if (mine > 0) {
+        // the units that hold the first and the last of this request's tiles
+        const long long U = win_units(a.units, total);
+        gf = static_cast<int>((static_cast<long long>(before + 1) * U - 1) / total);
+        np = static_cast<int>((static_cast<long long>(before + mine) * U - 1) / total) - gf + 1;
+    }
+    pdl_wait();  // stage 1 is done (every warp waits, so that this grid ends after it)
+    if (!row || np == 1) return;  // np == 1: stage 1 wrote the output itself
+    const int i = R / a.grp;
+    const long long orow = (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
+    __nv_bfloat16* out = a.out + orow * D + V * lane;
+
+    const long long step = static_cast<long long>(a.Hkv) * a.rbn;  // rows per slot
+    const long long first = (static_cast<long long>(gf + v) * a.Hkv + kh) * a.rbn + jr;
+    float m = -INFINITY;
+    for (int s = lane; s < np; s += 32) m = fmaxf(m, a.ws_lse[first + s * step]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mu = m == -INFINITY ? 0.f : m;  // a NaN partial has a NaN weight, and so has the row
+
+    float acc[V] = {};
+    float wsum = 0.f;
+    constexpr int kStep = WPR;
+    for (int s0 = WPR == 1 ? 0 : warp; s0 < np; s0 += kInFlight * kStep) {
+        float x[kInFlight][V];
+        float w[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int s = s0 + u * kStep;
+            w[u] = 0.f;
+            if (s < np) {
+                w[u] = __expf(a.ws_lse[first + s * step] - mu);
+                *reinterpret_cast<VecT*>(x[u]) =
+                    __ldcs(reinterpret_cast<const VecT*>(a.ws_o + (first + s * step) * D + V * lane));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            wsum += w[u];
+            if (w[u] != 0.f)
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] += w[u] * x[u][k];
+        }
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) part[warp][V * lane + k] = acc[k];
+        if (lane == 0) part[warp][D] = wsum;
+        __syncthreads();
+        if (warp > 0) return;
+        for (int s = 1; s < kWarps; ++s) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] += part[s][V * lane + k];
+            wsum += part[s][D];
+        }
+    }
+    const float inv = wsum != 0.f ? 1.f / wsum : 0.f;  // 0: no visible key
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+        *reinterpret_cast<uint32_t*>(out + k) = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+    if (a.lse && lane == 0) a.lse[orow] = wsum != 0.f ? mu + logf(wsum) : -INFINITY;
+}
+
+template <int D, int WPR>
+cudaError_t launch(const WinArgs& a, cudaStream_t stream) {
+    const int items = a.Hkv * a.rbn;
+    return launch_with_pdl(win_merge_kernel<D, WPR>,
+                           dim3(a.batch * a.rb, WPR == 1 ? (items + kWarps - 1) / kWarps : items),
+                           dim3(32 * kWarps), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t win_merge(const WinArgs& a, int D, cudaStream_t stream) {
+    // a row is summed from about units / (batch * rb) + 1 partials
+    const bool many = a.units > 8 * a.batch * a.rb;
+    if (D == 128) return many ? launch<128, kWarps>(a, stream) : launch<128, 1>(a, stream);
+    return many ? launch<64, kWarps>(a, stream) : launch<64, 1>(a, stream);
+}
+
+int win_ctas_per_sm(int rbn) { return rbn <= 8 ? 2 : 1; }
+
+}  // namespace mqa

@@ -1,0 +1,345 @@
+"""GPU parity of windowed and block-scaled GQA decode (C ABI -> sm_103a
+kernels) against a 64-bit reference on the same values, with bounds derived
+from the kernels' roundings (cache_reference.py)."""
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+import mqa_decode_attention_paged_gb300 as mqa
+
+pytestmark = pytest.mark.gpu
+
+NONE = 1 << 30
+KINDS = ["bf16", "fp8_e4m3", "fp8_e4m3_block", "int8_block"]
+
+
+class Case:
+    """A paged batch on the CPU; every byte that no query may see is poisoned, and the block-table entries of pages
+    without a visible key hold invalid ids."""
+
+    def __init__(self, lens, Hq, Hkv, D, page, kv, L=1, window=NONE, sinks=0, group=16, seed=0, poison=True,
+                 extra=2):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.L, self.page, self.kv, self.window, self.sinks = lens, L, page, kv, window, sinks
+        B = len(lens)
+        pages = [-(-n // page) for n in lens]
+        nb = sum(pages) + extra
+        self.nb = nb
+        perm = torch.randperm(nb, generator=g)
+        width = max(1, max(pages)) + 1
+        bt = torch.full((B, width), -1, dtype=torch.int32)
+        at = 0
+        for b, m in enumerate(pages):
+            bt[b, :m] = perm[at:at + m].to(torch.int32)
+            at += m
+        self.q = torch.randn(B, L, Hq, D, generator=g).to(torch.bfloat16)
+        x = torch.randn(nb, 2, page, Hkv, D, generator=g)
+        self.scales, self.ks, self.vs = None, 1.0, 1.0
+        if kv == "bf16":
+            self.cache = x.to(torch.bfloat16)
+        elif kv == "fp8_e4m3":
+            self.ks, self.vs = 0.05, 0.03
+            self.cache = (x / 0.05).clamp(-448, 448).to(torch.float8_e4m3fn)
+        else:
+            x = x.view(nb, 2, page // group, group, Hkv, D)
+            x *= torch.exp(torch.randn(nb, 2, page // group, 1, Hkv, 1, generator=g))
+            s = x.abs().amax(dim=(3, 5), keepdim=True) / ref.Q_MAX[kv]
+            y = x / s
+            codes = y.round().to(torch.int8) if kv == "int8_block" else y.clamp(-448, 448).to(torch.float8_e4m3fn)
+            self.cache = codes.view(nb, 2, page, Hkv, D)
+            self.scales = s.view(nb, 2, page // group, Hkv).contiguous()
+        self.group = group
+        self.scale = D ** -0.5
+        self.bt_ref = bt.clone()
+        if poison:
+            raw = self.cache.view(torch.uint8) if kv.startswith("fp8") else self.cache
+            bad = float("nan") if kv == "bf16" else 0x7f
+            seen = torch.zeros(nb, page, dtype=torch.bool)
+            for b, n in enumerate(lens):
+                ok = torch.zeros(max(1, pages[b]) * page, dtype=torch.bool)
+                for p in range(max(0, n - L), n):
+                    t = torch.arange(p + 1)
+                    ok[t[(t < sinks) | (t > p - window)]] = True
+                for j in range(pages[b]):
+                    part = ok[j * page:(j + 1) * page]
+                    seen[bt[b, j]] = part
+                    if not part.any():
+                        bt[b, j] = (-1, nb, 1 << 30)[j % 3]
+            raw.masked_fill_(~seen[:, None, :, None, None], bad)
+            if self.scales is not None:
+                dead = ~seen.view(nb, page // group, group).any(-1)
+                self.scales.masked_fill_(dead[:, None, :, None], float("nan"))
+        self.bt = bt
+
+    def dev(self):
+        return [None if t is None else t.cuda() for t in (self.q, self.cache, self.bt, self.scales)] + [
+            torch.tensor(self.lens, dtype=torch.int32, device="cuda")]
+
+    def values(self, b, plane):
+        """(values, codes, per-token scales) of request b's tokens, float64, poisoned bytes as zeros."""
+        n = self.lens[b]
+        codes = ref.gather(self.cache, self.bt_ref, b, n, self.page, plane).nan_to_num(0.0, 0.0, 0.0)
+        Hkv = self.cache.shape[3]
+        if self.scales is not None:
+            s = ref.token_scales(self.scales, self.bt_ref, b, n, self.page, plane).nan_to_num(0.0)
+        else:
+            s = torch.full((n, Hkv), self.ks if plane == 0 else self.vs, dtype=torch.float64)
+        return codes * s[..., None], codes, s
+
+    def reference(self, rows=None):
+        for b in rows if rows is not None else range(len(self.lens)):
+            k, _, _ = self.values(b, 0)
+            v, code, s = self.values(b, 1)
+            yield b, ref.window_decode(self.q[b].double(), k, v, self.lens[b], self.scale, self.window, self.sinks,
+                                       code_v=code, s_v=s, half_p=self.kv != "bf16")
+
+    def run(self, splits=None, dev=None, **kw):
+        q, kv, bt, sc, sl = dev or self.dev()
+        B, L, Hq, D = q.shape
+        Hkv = kv.shape[3]
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full(q.shape[:3], float("nan"), device="cuda")
+        n = splits or mqa.gqa_window_num_kv_splits(B, L, Hq, Hkv)
+        ws = torch.full((max(16, mqa.gqa_window_decode_workspace_bytes(B, L, Hq, Hkv, D, n)),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = dict(out=out, lse=lse, num_kv_splits=n, workspace=ws, device_status=status, **kw)
+        if self.window >= NONE and self.sinks == 0 and sc is not None:
+            mqa.gqa_block_decode(q, kv, sc, bt, sl, self.scale, **kw)
+        else:
+            mqa.gqa_window_decode(q, kv, bt, sl, self.scale, self.window, self.sinks, kv_scales=sc, k_scale=self.ks,
+                                  v_scale=self.vs, **kw)
+        torch.cuda.synchronize()
+        return out.cpu().double(), lse.cpu().double(), int(status.item())
+
+
+def check(case, out, lse, rows=None, what=""):
+    for b, (o, l, tol_o, tol_l) in case.reference(rows):
+        dead = torch.isneginf(l)
+        assert torch.equal(torch.isneginf(lse[b]), dead), f"{what}: lse -inf pattern, request {b}"
+        assert (out[b][dead] == 0).all(), f"{what}: rows without a key, request {b}"
+        err = (out[b] - o).abs()
+        assert (err <= tol_o).all(), f"{what}: request {b} out off by {float((err / tol_o).max()):.2f} x its bound"
+        e2 = (lse[b] - l)[~dead].abs()
+        assert (e2 <= tol_l[~dead]).all(), f"{what}: request {b} lse off by {float((e2 / tol_l[~dead]).max()):.2f} x"
+
+
+def run_and_check(case, splits, what=""):
+    dev = case.dev()
+    for s in splits:
+        out, lse, status = case.run(s, dev)
+        assert status == 0, f"{what}: status {status}"
+        check(case, out, lse, what=f"{what} splits={s}")
+
+
+RAGGED = [1, 15, 16, 17, 40, 0, 100, 333]
+HEADS = [(32, 8, 128), (8, 8, 64), (16, 1, 64), (12, 4, 128), (6, 3, 128), (10, 5, 64), (14, 2, 64), (64, 8, 64)]
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+def test_window_shapes(kv, Hq, Hkv, D):
+    for window, sinks in ((1, 0), (16, 1), (33, 4), (100, 40)):
+        case = Case(RAGGED, Hq, Hkv, D, 16, kv, window=window, sinks=sinks, seed=1)
+        run_and_check(case, (1, 2, None), f"{kv} {Hq}/{Hkv}x{D} W={window} S={sinks}")
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3_block", "int8_block"])
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+def test_block_shapes(kv, Hq, Hkv, D):
+    run_and_check(Case(RAGGED, Hq, Hkv, D, 16, kv, seed=2), (1, 3, None), f"{kv} {Hq}/{Hkv}x{D}")
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("page,group", [(16, 16), (32, 16), (48, 48), (64, 32), (128, 64), (256, 256)])
+def test_pages_and_scale_blocks(kv, page, group):
+    for Hkv in (8, 2, 1):
+        case = Case([1, 47, 129, 300, 700], 4 * Hkv, Hkv, 64, page, kv, window=200, sinks=20, group=group, seed=3)
+        run_and_check(case, (1, None), f"{kv} page={page} G={group} Hkv={Hkv}")
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("L,Hq,Hkv,D", [(2, 8, 2, 128), (5, 32, 8, 64), (3, 7, 1, 128), (4, 32, 8, 128),
+                                        (8, 16, 1, 64), (128, 2, 2, 64), (17, 14, 2, 128)])
+def test_several_positions(kv, L, Hq, Hkv, D):
+    # fewer cached tokens than positions: the first rows see nothing
+    for window, sinks in ((1, 0), (24, 3), (NONE, 0)):
+        case = Case([0, 1, L - 1, L, L + 15, 130], Hq, Hkv, D, 16, kv, L=L, window=window, sinks=sinks, seed=4)
+        run_and_check(case, (1, None), f"{kv} L={L} {Hq}/{Hkv}x{D} W={window}")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3_block"])
+@pytest.mark.parametrize("bad", ["inf", "nan"])
+def test_non_finite_value_reaches_only_the_queries_that_see_it(kv, bad):
+    # the last token's V is seen by the last position only, the token that the
+    # window drops next by the first position only
+    L, n, W = 4, 90, 32
+    case = Case([n], 8, 2, 64, 16, kv, L=L, window=W, sinks=0, seed=5)
+    raw = case.cache if kv == "bf16" else case.cache.view(torch.uint8)
+    value = (float(bad) if kv == "bf16" else 0x7f)  # e4m3 has no Inf: NaN in both cases
+    for t in (n - 1, n - L - W + 1):
+        raw[case.bt[0, t // 16], 1, t % 16] = value
+    out, lse, _ = case.run(1)
+
+    # the reference takes non-finite values as zeros: right for the rows that do not see them
+    (_, (o, l, tol_o, tol_l)), = case.reference()
+    for i in (1, 2):
+        assert ((out[0, i] - o[i]).abs() <= tol_o[i]).all(), f"row {i}"
+    assert not torch.isfinite(out[0, 0]).any() and not torch.isfinite(out[0, 3]).any()
+    assert ((lse[0] - l).abs() <= tol_l).all()
+
+
+def test_scales_of_unlike_magnitude():
+    for kv in ("fp8_e4m3_block", "int8_block"):
+        case = Case([300, 90, 40], 8, 2, 128, 16, kv, seed=6, poison=False)
+        bt = case.bt
+        case.scales[bt[1, :6].long(), 1] *= 1e-7       # a whole request of tiny values
+        case.scales[bt[0, 15:18].long(), 1] *= 3e4     # late jumps
+        case.scales[bt[2, 1].long(), 1] *= 1e-20       # one tiny block between ordinary ones
+        case.scales[bt[2, 2].long(), :] = 0.0          # and one of zeros
+        case.scales[bt[0, 0].long(), 0] *= 20.0        # large logits
+        run_and_check(case, (1, 4, None), kv)
+
+
+def test_all_values_zero_and_zero_scales():
+    case = Case([50], 8, 2, 64, 16, "int8_block", seed=7, poison=False)
+    case.scales.zero_()
+    out, lse, status = case.run(None)
+    assert status == 0 and (out == 0).all()
+    assert (lse - np.log(50)).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_reproducible_and_batch_invariant(kv):
+    case = Case([700, 20, 333, 1, 512, 90], 32, 8, 128, 16, kv, window=256, sinks=4, seed=8)
+    dev = case.dev()
+    for s in (1, None):
+        a, b = case.run(s, dev), case.run(s, dev)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    one = case.run(1, dev)
+    q, cache, bt, sc, sl = dev
+    part = case.run(1, [q[[4, 1]].contiguous(), cache, bt[[4, 1]].contiguous(), sc, sl[[4, 1]].contiguous()])
+    assert torch.equal(part[0], one[0][[4, 1]]) and torch.equal(part[1], one[1][[4, 1]])
+
+
+def test_bad_block_id_and_lengths_are_reported():
+    case = Case([40, 70, 33], 8, 2, 128, 16, "int8_block", seed=9, poison=False)
+    case.bt[1, 2] = case.nb + 5
+    for s in (1, None):
+        out, lse, status = case.run(s)
+        assert status == 5 and torch.isfinite(out).all()
+        check(case, out, lse, rows=[0, 2])
+    case = Case([40, 70], 8, 2, 128, 16, "bf16", window=20, seed=9, poison=False)
+    q, kv, bt, sc, sl = case.dev()
+    for n, want in ((-3, 0), (10 ** 6, bt.shape[1] * 16)):
+        sl[1] = n
+        out, lse, status = case.run(None, [q, kv, bt, sc, sl])
+        assert status == 5
+        check(case, out, lse, rows=[0])
+
+
+def test_layouts_of_the_call():
+    case = Case([90, 7], 8, 2, 64, 16, "bf16", window=40, sinks=2, seed=10)
+    q, kv, bt, _, sl = case.dev()
+    want, lse, _ = case.run(1)
+    o3, l3 = mqa.gqa_window_decode(q[:, 0].contiguous(), kv, bt, sl, case.scale, 40, 2, num_kv_splits=1)
+    assert o3.shape == (2, 8, 64) and l3.shape == (2, 8)
+    assert torch.equal(o3.cpu().double(), want[:, 0]) and torch.equal(l3.cpu().double(), lse[:, 0])
+    o, none = mqa.gqa_window_decode(q, kv, bt, sl, case.scale, 40, 2, num_kv_splits=1, return_lse=False)
+    assert none is None and torch.equal(o.cpu().double(), want)
+    # a window wider than any length is no window
+    wide = Case([90, 7], 8, 2, 64, 16, "int8_block", window=10 ** 9, sinks=0, seed=10)
+    run_and_check(wide, (1, None))
+
+
+def test_full_batches():
+    # as many virtual requests as a call takes: single tokens and short lengths
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 40, 2048).tolist()
+    case = Case(lens, 2, 1, 64, 16, "int8_block", seed=11, poison=False)
+    out, lse, status = case.run(None)
+    assert status == 0
+    check(case, out, lse, rows=[0, 1, 2, 1023, 1024, 2046, 2047])
+    one, l1, _ = case.run(1)
+    check(case, one, l1, rows=[3, 5, 2047])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3_block"])
+def test_cells_behind_four_gigabytes(kv):
+    # blocks at the far end of a cache whose byte offsets pass 32 bits
+    small = Case([200, 33], 8, 8, 128, 16, kv, window=150, sinks=3, seed=12, poison=False)
+    per = 2 * 16 * 8 * 128 * (2 if kv == "bf16" else 1)
+    shift = (5 << 30) // per
+    q, cache, bt, sc, sl = small.dev()
+    big = torch.zeros((shift + small.nb,) + tuple(cache.shape[1:]), dtype=torch.uint8 if kv != "bf16" else cache.dtype,
+                      device="cuda")
+    big[shift:] = cache.view(torch.uint8) if kv != "bf16" else cache
+    if sc is not None:
+        far = torch.zeros((shift + small.nb,) + tuple(sc.shape[1:]), device="cuda")
+        far[shift:] = sc
+        sc = far
+    bt = torch.where(bt >= 0, bt + shift, bt)
+    out, lse, status = small.run(None, [q, big.view(cache.dtype), bt, sc, sl])
+    assert status == 0
+    check(small, out, lse)
+
+
+def test_streams_and_graphs():
+    # captured once and replayed with other lengths and queries; two graphs with workspaces of their own; a call on
+    # another stream than the current one
+    case = Case([300, 20, 150], 8, 2, 128, 16, "fp8_e4m3_block", window=64, sinks=4, seed=13, poison=False)
+    q, kv, bt, sc, sl = case.dev()
+    call = lambda **kw: mqa.gqa_window_decode(q, kv, bt, sl, case.scale, 64, 4, kv_scales=sc, **kw)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = call()
+        graphs.append((g, res))
+    for lens in ([300, 20, 150], [17, 1, 149], [0, 20, 64]):
+        case.lens = lens
+        sl.copy_(torch.tensor(lens, dtype=torch.int32))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, (out, lse) in graphs:
+            check(case, out.cpu().double(), lse.cpu().double(), what=f"replay {lens}")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    results = [call(stream=s) for _ in range(3)]
+    raw = call(stream=s.cuda_stream)
+    s.synchronize()
+    for out, lse in results + [raw]:
+        check(case, out.cpu().double(), lse.cpu().double(), what="other stream")
+
+
+def test_two_calls_at_once():
+    cases = [Case([400, 90, 33], 32, 8, 128, 16, kv, window=100, sinks=4, seed=14) for kv in ("bf16", "int8_block")]
+    devs = [c.dev() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    res = []
+    for c, d, s in zip(cases, devs, streams):
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                res.append((c, mqa.gqa_window_decode(d[0], d[1], d[2], d[4], c.scale, 100, 4, kv_scales=d[3])))
+    torch.cuda.synchronize()
+    for c, (out, lse) in res:
+        check(c, out.cpu().double(), lse.cpu().double())
+
+
+def test_random_shapes():
+    rng = np.random.default_rng(3)
+    for _ in range(40):
+        Hkv = int(rng.integers(1, 9))
+        grp, L = int(rng.integers(1, 17)), int(rng.integers(1, 8))
+        kv = KINDS[int(rng.integers(0, 4))]
+        page = int(rng.choice([16, 32, 48, 64]))
+        case = Case([int(x) for x in rng.integers(0, 500, int(rng.integers(1, 6)))], Hkv * grp, Hkv,
+                    int(rng.choice([64, 128])), page, kv, L=L, window=int(rng.choice([1, 7, 64, 300, NONE])),
+                    sinks=int(rng.choice([0, 1, 5, 70])), group=int(rng.choice([16, page])), seed=int(rng.integers(1 << 30)))
+        run_and_check(case, (1, int(rng.integers(2, 9)), None),
+                      f"{kv} Hkv={Hkv} grp={grp} L={L} page={page} lens={case.lens} W={case.window} S={case.sinks}")
