@@ -502,25 +502,31 @@ def gqa_window_num_kv_splits(batch: int, q_len: int, num_q_heads: int, num_kv_he
     return n
 
 
-def _on_current(dev):
-    """The stream the caller works on, for a call on device `dev`; None if `dev` is not the current device."""
-    import torch
-    return torch.cuda.current_stream(dev) if dev.index == torch.cuda.current_device() else None
+def _fits(t, dtype, shape, index):
+    """Whether t is what _check and _on_device ask for, in one look (the calls below run once per layer and token)."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
-def _call_stream(stream, current, allocated):
-    """The raw stream of a call.  Tensors that the call allocated (on the current stream) are recorded on a
-    stream that the caller passes, so that their memory is not reused while that stream still works on them."""
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call_stream(stream, index, allocated):
+    """The raw stream of a call on device `index`, by default the current one.  Tensors that the call allocated (on
+    the current stream) are recorded on a stream that the caller passes, so that their memory is not reused while
+    that stream still works on them."""
     import torch
+    raw = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
-        return current.cuda_stream
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if raw != current.cuda_stream and allocated:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(raw, device=current.device)
+        return raw
+    other = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if other != raw and allocated:
+        current = torch.cuda.current_stream(index)
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(other, device=current.device)
         s.wait_stream(current)
         for t in allocated:
             t.record_stream(s)
-    return raw
+    return other
 
 
 def _block_code(kv_cache, kv_scales, kv_dtype):
@@ -547,7 +553,8 @@ def _scale_block(kv_scales, code, nb, page, hkv):
     s = kv_scales.shape
     if len(s) != 4 or s[0] != nb or s[1] != 2 or s[2] < 1 or page % s[2] != 0 or s[3] != hkv:
         raise ValueError(f"kv_scales must be [{nb}, 2, page / scale_block, {hkv}], got {tuple(s)}")
-    _check(kv_scales, "kv_scales", (torch.float32,))
+    if kv_scales.dtype is not torch.float32 or not kv_scales.is_contiguous():
+        _check(kv_scales, "kv_scales", (torch.float32,))
     return page // s[2]
 
 
@@ -577,22 +584,35 @@ def gqa_block_decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, *, ou
 def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale, window, sinks, out,
                    lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse):
     import torch
-    if q.dim() not in (3, 4) or kv_cache.dim() != 5:
+    shape = q.shape
+    if len(shape) not in (3, 4) or kv_cache.dim() != 5:
         raise ValueError("q must be [batch, (q_len,) heads, head_size] and kv_cache have 5 dimensions")
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
-    L = q.shape[1] if q.dim() == 4 else 1
+    if len(shape) == 4:
+        B, L, Hq, D = shape
+    else:
+        (B, Hq, D), L = shape, 1
     nb, two, page, Hkv, D2 = kv_cache.shape
     code = _block_code(kv_cache, kv_scales, kv_dtype)
     if two != 2 or D2 != D:
         raise ValueError(f"kv_cache must be [num_blocks, 2, page, num_kv_heads, {D}]")
+    index = q.get_device()
     block = _scale_block(kv_scales, code, nb, page, Hkv)
-    if name == "gqa_block_decode" and block == 0:
+    if window is None and block == 0:
         raise ValueError("gqa_block_decode reads block-scaled caches (fp8_e4m3_block, int8_block)")
-    _check_common(q, kv_cache, code, block_table, seq_lens, q if out is None else out, q.shape, lse, q.shape[:-1],
-                  workspace, device_status, extra=(("kv_scales", kv_scales),))
-    current = _on_current(q.device)
-    if current is None:
-        with torch.cuda.device(q.device):
+    bt_shape = block_table.shape
+    if not (index >= 0 and len(bt_shape) == 2 and bt_shape[0] == B and _fits(q, torch.bfloat16, shape, index)
+            and kv_cache.is_contiguous() and kv_cache.get_device() == index
+            and kv_cache.element_size() == (2 if code == KV_BF16 else 1)
+            and _fits(block_table, torch.int32, bt_shape, index) and _fits(seq_lens, torch.int32, (B,), index)
+            and (kv_scales is None or kv_scales.get_device() == index)
+            and (out is None or _fits(out, torch.bfloat16, shape, index))
+            and (lse is None or _fits(lse, torch.float32, shape[:-1], index))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == index))
+            and (device_status is None or _fits(device_status, torch.int32, device_status.shape, index))):
+        _check_common(q, kv_cache, code, block_table, seq_lens, q if out is None else out, shape, lse, shape[:-1],
+                      workspace, device_status, extra=(("kv_scales", kv_scales),))
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale,
                                   window, sinks, out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream,
                                   return_lse)
@@ -601,24 +621,29 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
         out = torch.empty_like(q)
         fresh.append(out)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
         fresh.append(lse)
     if num_kv_splits is None:
-        num_kv_splits = max(1, int(lib.gqa_window_num_kv_splits(B, L, Hq, Hkv)))
+        num_kv_splits = max(1, lib.gqa_window_num_kv_splits(B, L, Hq, Hkv))
+    ws_bytes = 0
     if workspace is None:
-        need = int(lib.gqa_window_decode_workspace_bytes(B, L, Hq, Hkv, D, num_kv_splits))
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = lib.gqa_window_decode_workspace_bytes(B, L, Hq, Hkv, D, num_kv_splits)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
             fresh.append(workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    raw = _call_stream(stream, current, fresh)
-    head = (_ptr(q), _ptr(kv_cache), _ptr(kv_scales), _ptr(block_table), _ptr(seq_lens), float(scale))
-    tail = (_ptr(out), _ptr(lse), B, L, Hq, Hkv, D, nb, page, block_table.shape[1], block, code, int(num_kv_splits),
-            _ptr(workspace), ws_bytes, _ptr(device_status), raw)
-    if window is None:
-        rc = lib.gqa_block_decode(*head, *tail)
     else:
-        rc = lib.gqa_window_decode(*head, float(k_scale), float(v_scale), int(window), int(sinks), *tail)
+        ws_bytes = workspace.nbytes
+    raw = _call_stream(stream, index, fresh)
+    if window is None:
+        rc = lib.gqa_block_decode(q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
+                                  seq_lens.data_ptr(), scale, out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb, page,
+                                  bt_shape[1], block, code, num_kv_splits, _raw(workspace), ws_bytes,
+                                  _raw(device_status), raw)
+    else:
+        rc = lib.gqa_window_decode(q.data_ptr(), kv_cache.data_ptr(), _raw(kv_scales), block_table.data_ptr(),
+                                   seq_lens.data_ptr(), scale, k_scale, v_scale, window, sinks, out.data_ptr(),
+                                   _raw(lse), B, L, Hq, Hkv, D, nb, page, bt_shape[1], block, code, num_kv_splits,
+                                   _raw(workspace), ws_bytes, _raw(device_status), raw)
     if rc != OK:
         raise MqaError(rc, name)
     return out, lse
@@ -628,11 +653,13 @@ def _check_rows(t, name, shape, dense):
     """A bf16 tensor of shape `shape` whose last `dense` dimensions are dense (rows of a wider tensor will do);
     returns its leading strides."""
     import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st, want = t.stride(), 1
+    if st[-1] == 1 and min(shape) > 1 and (dense == 1 or st[-2] == shape[-1]):
+        return st[:-dense]
     for i in range(1, dense + 1):
         if shape[-i] != 1 and st[-i] != want:
             raise ValueError(f"the last {dense} dimension(s) of {name} must be contiguous")
@@ -643,11 +670,20 @@ def _check_rows(t, name, shape, dense):
         s = st[i] if shape[i] > 1 else want
         out.insert(0, s)
         want = max(want, s * shape[i])
-    return out
+    return tuple(out)
 
 
-def _check_append(cos_sin, width, kv_cache, block_table, seq_lens, query_start, device_status, named):
+def _check_append(index, cos_sin, width, kv_cache, block_table, seq_lens, query_start, device_status, named):
     import torch
+    bt_shape = block_table.shape
+    if (index >= 0 and len(bt_shape) == 2 and cos_sin.dim() == 2 and width in (None, cos_sin.shape[1])
+            and _fits(cos_sin, torch.float32, cos_sin.shape, index) and kv_cache.is_contiguous()
+            and kv_cache.get_device() == index and _fits(block_table, torch.int32, bt_shape, index)
+            and _fits(seq_lens, torch.int32, (bt_shape[0],), index)
+            and _fits(query_start, torch.int32, (bt_shape[0] + 1,), index)
+            and (device_status is None or _fits(device_status, torch.int32, device_status.shape, index))
+            and all(t is None or t.get_device() == index for _, t in named)):
+        return bt_shape[0]
     _check(cos_sin, "cos_sin", (torch.float32,))
     if cos_sin.dim() != 2 or (width is not None and cos_sin.shape[1] != width):
         raise ValueError(f"cos_sin must be fp32 [max_position, {width or 'rotary_dim'}]")
@@ -699,11 +735,11 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
             qos, = _check_rows(q_out, "q_out", (T, Hq, D), 2)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    B = _check_append(cos_sin, None, kv_cache, block_table, seq_lens, query_start, device_status,
+    index = k.get_device()
+    B = _check_append(index, cos_sin, None, kv_cache, block_table, seq_lens, query_start, device_status,
                       (("k", k), ("v", v), ("q", q), ("q_out", q_out), ("kv_scales", kv_scales)))
-    current = _on_current(k.device)
-    if current is None:
-        with torch.cuda.device(k.device):
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start, q=q, q_out=q_out,
                                    kv_scales=kv_scales, k_scale=k_scale, v_scale=v_scale, interleaved=interleaved,
                                    kv_dtype=kv_dtype, device_status=device_status, stream=stream)
@@ -712,13 +748,13 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
         qos = Hq * D
         fresh.append(q_out)
-    if T == 0:
+    if T == 0:  # (an empty tensor has no address)
         return q_out
-    rc = lib.gqa_rope_append(_ptr(q), _ptr(k), _ptr(v), _ptr(cos_sin), _ptr(query_start), _ptr(seq_lens),
-                             _ptr(block_table), _ptr(q_out), _ptr(kv_cache), _ptr(kv_scales), float(k_scale),
-                             float(v_scale), T, B, Hq, Hkv, D, cos_sin.shape[1], int(bool(interleaved)),
-                             cos_sin.shape[0], nb, page, block_table.shape[1], block, code, qs, ks, vs, qos,
-                             _ptr(device_status), _call_stream(stream, current, fresh))
+    rc = lib.gqa_rope_append(_raw(q), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(), query_start.data_ptr(),
+                             seq_lens.data_ptr(), block_table.data_ptr(), _raw(q_out), kv_cache.data_ptr(),
+                             _raw(kv_scales), k_scale, v_scale, T, B, Hq, Hkv, D, cos_sin.shape[1],
+                             1 if interleaved else 0, cos_sin.shape[0], nb, page, block_table.shape[1], block, code,
+                             qs, ks, vs, qos, _raw(device_status), _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "gqa_rope_append")
     return q_out
@@ -753,11 +789,11 @@ def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_
             qos, qohs = _check_rows(q_pe_out, "q_pe_out", (T, H, 64), 1)
     elif q_pe_out is not None:
         raise ValueError("q_pe_out without q_pe")
-    B = _check_append(cos_sin, 64, kv_cache, block_table, seq_lens, query_start, device_status,
+    index = kv_c.get_device()
+    B = _check_append(index, cos_sin, 64, kv_cache, block_table, seq_lens, query_start, device_status,
                       (("kv_c", kv_c), ("k_pe", k_pe), ("q_pe", q_pe), ("q_pe_out", q_pe_out)))
-    current = _on_current(kv_c.device)
-    if current is None:
-        with torch.cuda.device(kv_c.device):
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_start, q_pe=q_pe,
                                    q_pe_out=q_pe_out, k_scale=k_scale, interleaved=interleaved, kv_dtype=kv_dtype,
                                    device_status=device_status, stream=stream)
@@ -768,10 +804,11 @@ def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_
         fresh.append(q_pe_out)
     if T == 0:
         return q_pe_out
-    rc = lib.mla_rope_append(_ptr(kv_c), _ptr(k_pe), _ptr(q_pe), _ptr(cos_sin), _ptr(query_start), _ptr(seq_lens),
-                             _ptr(block_table), _ptr(q_pe_out), _ptr(kv_cache), float(k_scale), T, B, H, D, R,
-                             int(bool(interleaved)), cos_sin.shape[0], nb, page, block_table.shape[1], code, cs, ps,
-                             qs, qhs, qos, qohs, _ptr(device_status), _call_stream(stream, current, fresh))
+    rc = lib.mla_rope_append(kv_c.data_ptr(), k_pe.data_ptr(), _raw(q_pe), cos_sin.data_ptr(),
+                             query_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), _raw(q_pe_out),
+                             kv_cache.data_ptr(), k_scale, T, B, H, D, R, 1 if interleaved else 0, cos_sin.shape[0],
+                             nb, page, block_table.shape[1], code, cs, ps, qs, qhs, qos, qohs, _raw(device_status),
+                             _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "mla_rope_append")
     return q_pe_out

@@ -56,20 +56,25 @@ struct Cfg {
     __host__ __device__ static int slot_bytes(int hkv, int ts) { return 16 * ts * hkv * D * kElt; }
 };
 
-// Blocks per SM: two when a thread can live with 96 registers (up to 8 rows).
-__host__ __device__ constexpr int ctas(int nhb) { return nhb == 1 ? 2 : 1; }
+// Row splits: a row block of more than 8 rows is shared by two sets of
+// consumer warps of 8 rows each, in one thread block per SM (16 + 1 warps)
+// instead of two (8 + 1 warps each).  The second set reads and widens the same
+// tile again, but a warp then holds 8 rows' accumulators and 16 warps hide
+// each other's latencies; 16 rows to a warp (168 registers, 8 warps per SM)
+// measured 112 us where this takes 60 (32 requests x 4 positions, window
+// 4096, e4m3 blocks).
+__host__ __device__ constexpr int ctas(int rs) { return rs == 1 ? 2 : 1; }
 
 struct Layout {
     int exch, scales, ok, bars, cum, total;  // the ring of slots comes first
 };
 
 template <int D, int KIND>
-__host__ __device__ inline Layout layout(int hkv, int ts, int nhb, int nslots, int vb, int batch) {
+__host__ __device__ inline Layout layout(int hkv, int ts, int rs, int nslots, int vb, int batch) {
     Layout l;
     l.exch = nslots * Cfg<D, KIND>::slot_bytes(hkv, ts);
     // TS > 1: half of the consumer warps hand (O, m, r, l) to the other half
-    const int per_lane = nhb * (D / 16 * 4 + 6);
-    l.scales = l.exch + (ts > 1 ? hkv * (ts / 2) * per_lane * 128 : 0);
+    l.scales = l.exch + (ts > 1 ? hkv * (ts / 2) * rs * (D / 16 * 4 + 6) * 128 : 0);
     l.ok = l.scales + nslots * 32;
     l.bars = l.ok + (nslots * 4 + 7) / 8 * 8;
     l.cum = l.bars + nslots * 16;
@@ -92,6 +97,26 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
 // cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+// 16 tokens x 32 e4m3 codes times 32 e4m3 x 8 rows.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -130,24 +155,21 @@ __device__ __forceinline__ uint32_t q_f16(uint32_t v) {
     return f16_pair(f.x, f.y);
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two_codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two_codes), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// The two e4m3 codes in the low half of w as two f16 values (exact).
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
 // Bytes `sel` of u (codes + 128) as two f16 values: 1024 + u is exact in the
 // mantissa of 0x6400, minus 1152 gives the code.
 __device__ __forceinline__ uint32_t int8_pair(uint32_t u, uint32_t sel) {
     return half2_bits(__hsub2(bits_half2(__byte_perm(u, 0x64646464u, sel)), bits_half2(0x64806480u)));
 }
-// Four codes -> the f16 pairs of bytes (0, 1) and (2, 3).
-template <int KIND>
+// Four int8 codes -> the f16 pairs of bytes (0, 1) and (2, 3).
 __device__ __forceinline__ uint2 widen_adjacent(uint32_t w) {
-    if constexpr (KIND == kWinInt8) {
-        const uint32_t u = w ^ 0x80808080u;
-        return make_uint2(int8_pair(u, 0x4140), int8_pair(u, 0x4342));
-    } else {
-        return make_uint2(e4m3_pair(w & 0xffffu), e4m3_pair(w >> 16));
-    }
+    const uint32_t u = w ^ 0x80808080u;
+    return make_uint2(int8_pair(u, 0x4140), int8_pair(u, 0x4342));
 }
 // Four codes -> the f16 pairs of bytes (0, 2) and (1, 3).
 template <int KIND>
@@ -156,9 +178,18 @@ __device__ __forceinline__ uint2 widen_strided(uint32_t w) {
         const uint32_t u = w ^ 0x80808080u;
         return make_uint2(int8_pair(u, 0x4240), int8_pair(u, 0x4341));
     } else {
-        const uint32_t p = __byte_perm(w, 0u, 0x3120);
-        return make_uint2(e4m3_pair(p & 0xffffu), e4m3_pair(p >> 16));
+        return make_uint2(e4m3_pair(__byte_perm(w, 0u, 0x4420)), e4m3_pair(__byte_perm(w, 0u, 0x4431)));
     }
+}
+
+// Four fp32 values as e4m3 codes (round to nearest), lowest byte first.
+__device__ __forceinline__ uint32_t e4m3_word(const float (&x)[4]) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+    return r;
 }
 
 // Whether a word of V (two bf16 values or four e4m3 codes) holds an Inf or NaN.
@@ -250,17 +281,17 @@ __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* len
     return cum[vb];
 }
 
-// MULTI: more than one query position per request.
-template <int D, int KIND, int NHB, bool MULTI>
-__global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid_constant__ WinArgs a) {
+// MULTI: more than one query position per request; RS: row splits.
+template <int D, int KIND, int RS, bool MULTI>
+__global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(const __grid_constant__ WinArgs a) {
     using C = Cfg<D, KIND>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int Hkv = a.Hkv, TS = a.ts, NC = Hkv * TS, nslots = a.nslots;
+    const int Hkv = a.Hkv, TS = a.ts, NT = Hkv * TS, NC = NT * RS, nslots = a.nslots;
     const int vb = a.batch * a.rb;
-    const Layout lay = layout<D, KIND>(Hkv, TS, NHB, nslots, vb, a.batch);
+    const Layout lay = layout<D, KIND>(Hkv, TS, RS, nslots, vb, a.batch);
     const int sbytes = C::slot_bytes(Hkv, TS);
-    float* scale_s = reinterpret_cast<float*>(smem + lay.scales);  // [slot][consumer warp]
+    float* scale_s = reinterpret_cast<float*>(smem + lay.scales);  // [slot][subtile * Hkv + head]
     uint32_t* ok_s = reinterpret_cast<uint32_t*>(smem + lay.ok);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);
     uint64_t* empty = full + nslots;
@@ -325,11 +356,11 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
                 const bool valid = lane < nbx && id >= 0;
                 const uint32_t ok = __ballot_sync(0xffffffffu, valid);
                 const int tok = t0 + lane * a.box_tok;  // of box `lane`
-                // scale of consumer warp `lane`: subtile lane / Hkv, head lane % Hkv
+                // scale `lane`: subtile lane / Hkv, head lane % Hkv
                 const int sub = lane / Hkv, stok = t0 + sub * 16;
                 const int sbox = min(sub * 16 / a.box_tok, nbx - 1);
                 const int sid = __shfl_sync(0xffffffffu, id, sbox);
-                const bool has_scale = scaled && lane < NC && sid >= 0;
+                const bool has_scale = scaled && lane < NT && sid >= 0;
 #pragma unroll
                 for (int plane = 0; plane < 2; ++plane) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1))) {
@@ -370,24 +401,28 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
 
     // ------------------------------------------------------------- consumers
     const int g = lane >> 2, c = lane & 3;
-    const int sub = warp / Hkv, kh = warp - sub * Hkv;
+    const int rs = RS == 1 ? 0 : warp / NT, wt = RS == 1 ? warp : warp - rs * NT;
+    const int sub = wt / Hkv, kh = wt - sub * Hkv;
     const int box = sub * 16 / a.box_tok;
     // this warp's 16-token tile inside a slot, panel p at + p * panel_bytes
     const int panel_bytes = a.box_tok * C::kLine;
-    const int tile_off = box * (sbytes / (tt / a.box_tok)) + kh * C::kPanels * panel_bytes +
-                         (sub * 16 - box * a.box_tok) * C::kLine;
-    // ldmatrix rows: K (and 8-bit V) matrices are (tokens 0-7, chunk), (8-15,
-    // chunk), (0-7, chunk + 1), (8-15, chunk + 1); bf16 V swaps the middle two
-    const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
-    const int vrow = KIND == kWinBf16 ? (lane & 7) + (lane >> 4) * 8 : krow;
-    const int vch = KIND == kWinBf16 ? (lane >> 3) & 1 : kch;
-    auto at = [](int row, int ch) {  // byte offset of 16-byte chunk ch of a token row
+    const uint32_t tile = smem_u32(smem) + box * (sbytes / (tt / a.box_tok)) + kh * C::kPanels * panel_bytes +
+                          (sub * 16 - box * a.box_tok) * C::kLine;
+    // A lane's ldmatrix address of 16-byte chunks 2i, 2i + 1 of its row is
+    // (row, chunk 0 or 1) with bit 5 + flipped by i: the swizzle only xors.
+    // K (and 8-bit V) matrices are (tokens 0-7, chunk), (8-15, chunk),
+    // (0-7, chunk + 1), (8-15, chunk + 1); bf16 V swaps the middle two.
+    auto lane_at = [](int row, int ch) {
         if constexpr (C::kLine == 128) return row * 128 + ((ch ^ (row & 7)) << 4);
         return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
     };
+    const uint32_t k_at = tile + lane_at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t v_at =
+        KIND == kWinBf16 ? tile + lane_at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) : k_at;
+    constexpr int kPairs = C::kLine / 32;  // chunk pairs of one line
 
     int slot = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, slot_off = 0;
     bool aborted = false;
     // A wait that runs out is reported once; from then on the warp waits for
     // nothing and writes nothing, but still meets the other warps.
@@ -401,8 +436,10 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
     auto release = [&]() {
         __syncwarp();
         if (lane == 0 && !aborted) mbar_arrive(&empty[slot]);
+        slot_off += sbytes;
         if (++slot == nslots) {
             slot = 0;
+            slot_off = 0;
             phase ^= 1;
         }
     };
@@ -411,83 +448,119 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
         const int b = a.rb == 1 ? pc.cur : pc.cur / a.rb;
         const int rblk = pc.cur - b * a.rb;
         const WinVis vis = win_visible(a, rblk, lens[b]);
-        const int row0 = rblk * 16;
+        const int row0 = rblk * 16 + rs * 8;
+        // positions of this warp's first and last row, and the keys they see
+        const int i_last = (min(a.rows, row0 + 8) - 1) / a.grp;
+        const int p_first = MULTI ? vis.n - a.q_len + row0 / a.grp : vis.p_first;
+        const int p_last = MULTI ? vis.n - a.q_len + i_last : vis.p_last;
+        const int lo = p_first - a.window;  // the last key before the window of the first row
+        const bool idle = RS > 1 && row0 >= a.rows;
 
-        // Q^T operand (row hb * 8 + g); 8-bit kinds in the permuted order
-        uint32_t qb[NHB][C::kSteps][2];
-        int qpos[NHB][2];  // positions of rows 2c, 2c + 1
-#pragma unroll
-        for (int hb = 0; hb < NHB; ++hb) {
-            const int R = row0 + hb * 8 + g;
+        // Q^T operand (row g): bf16; f16 in the order of the int8 codes' words;
+        // or two e4m3 terms of the row scaled by a power of two, q = f (q1 +
+        // q2 / 16): 4 + 4 significant bits hold a bf16 value exactly, down to
+        // 2^-21 of the row's largest entry
+        uint32_t qb[C::kSteps][2];
+        float qf[2] = {1.f, 1.f};  // f of rows 2c, 2c + 1 (e4m3)
+        int qpos[2];               // positions of rows 2c, 2c + 1
+        {
+            const int R = row0 + g;
             const int i = MULTI ? R / a.grp : 0;
             const bool have = R < a.rows;
             const __nv_bfloat16* qr =
                 a.q + ((static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp)) * D;
+            if constexpr (KIND == kWinBf16) {
 #pragma unroll
-            for (int ks = 0; ks < C::kSteps; ++ks) {
-                if constexpr (KIND == kWinBf16) {
-                    qb[hb][ks][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c)) : 0u;
-                    qb[hb][ks][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c + 8)) : 0u;
+                for (int ks = 0; ks < C::kSteps; ++ks) {
+                    qb[ks][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c)) : 0u;
+                    qb[ks][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c + 8)) : 0u;
+                }
+            } else {
+                uint2 v[C::kSteps];  // entries 16 ks + 4c .. + 3
+#pragma unroll
+                for (int ks = 0; ks < C::kSteps; ++ks)
+                    v[ks] = have ? __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * c)) : make_uint2(0u, 0u);
+                if constexpr (KIND == kWinInt8) {
+#pragma unroll
+                    for (int ks = 0; ks < C::kSteps; ++ks) {
+                        qb[ks][0] = q_f16(v[ks].x);
+                        qb[ks][1] = q_f16(v[ks].y);
+                    }
                 } else {
-                    const uint2 v = have ? __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * c))
-                                         : make_uint2(0u, 0u);
-                    qb[hb][ks][0] = q_f16(v.x);
-                    qb[hb][ks][1] = q_f16(v.y);
+                    float top = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < C::kSteps; ++ks) {
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[ks].x << 16)),
+                                               fabsf(__uint_as_float(v[ks].x & 0xffff0000u))));
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[ks].y << 16)),
+                                               fabsf(__uint_as_float(v[ks].y & 0xffff0000u))));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // 2^e above top; the row times 2^(8 - e) stays below 256
+                    const int e = max(-100, static_cast<int>(__float_as_uint(top) >> 23) - 126);
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+                    const float f = __uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23);
+                    qf[0] = __shfl_sync(0xffffffffu, f, 8 * c);  // of row 2c: any lane with g = 2c
+                    qf[1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+#pragma unroll
+                    for (int ks = 0; ks < C::kSteps; ++ks) {
+                        float x[4] = {__uint_as_float(v[ks].x << 16) * up, __uint_as_float(v[ks].x & 0xffff0000u) * up,
+                                      __uint_as_float(v[ks].y << 16) * up, __uint_as_float(v[ks].y & 0xffff0000u) * up};
+                        const uint32_t hi = e4m3_word(x);
+                        const uint32_t h01 = e4m3_pair(hi), h23 = e4m3_pair(hi >> 16);
+                        const float2 f01 = __half22float2(bits_half2(h01)), f23 = __half22float2(bits_half2(h23));
+                        x[0] = (x[0] - f01.x) * 16.f;
+                        x[1] = (x[1] - f01.y) * 16.f;
+                        x[2] = (x[2] - f23.x) * 16.f;
+                        x[3] = (x[3] - f23.y) * 16.f;
+                        qb[ks][0] = hi;
+                        qb[ks][1] = e4m3_word(x);
+                    }
                 }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int Re = min(row0 + hb * 8 + 2 * c + e, a.rows - 1);
-                qpos[hb][e] = MULTI ? vis.n - a.q_len + Re / a.grp : vis.p_last;
+                const int Re = min(row0 + 2 * c + e, a.rows - 1);
+                qpos[e] = MULTI ? vis.n - a.q_len + Re / a.grp : vis.p_last;
             }
         }
-        float o[NHB][C::kSteps][4];
-        float m_run[NHB][2], r_run[NHB][2], l_part[NHB][2];
+        float o[C::kSteps][4];
+        // references of the sums and (8-bit) of the numerators: base-2
+        // exponents, and the logit above which they move (-inf: none yet)
+        float m_ref[2] = {0.f, 0.f}, m_thr[2] = {-INFINITY, -INFINITY};
+        float r_ref[2] = {0.f, 0.f}, r_thr[2] = {-INFINITY, -INFINITY};
+        float l_part[2] = {0.f, 0.f};
 #pragma unroll
-        for (int hb = 0; hb < NHB; ++hb) {
-#pragma unroll
-            for (int mb = 0; mb < C::kSteps; ++mb) o[hb][mb][0] = o[hb][mb][1] = o[hb][mb][2] = o[hb][mb][3] = 0.f;
-            m_run[hb][0] = m_run[hb][1] = r_run[hb][0] = r_run[hb][1] = -INFINITY;
-            l_part[hb][0] = l_part[hb][1] = 0.f;
-        }
+        for (int mb = 0; mb < C::kSteps; ++mb) o[mb][0] = o[mb][1] = o[mb][2] = o[mb][3] = 0.f;
 
         for (int j = pc.j0; j < pc.j1; ++j) {
             const int t0 = vis.tile(j) * tt + sub * 16;
-            float st[NHB][2][4];
+            float st[2][4];
             bool act = false;
             float ksc = a.sl2;
             if (wait_full()) {
-                act = ((ok_s[slot] >> box) & 1u) && t0 < vis.hi && (t0 + 15 >= vis.lo || t0 < a.sinks);
+                act = ((ok_s[slot] >> box) & 1u) && t0 <= p_last && (t0 + 15 > lo || t0 < a.sinks) && !idle;
                 if (act) {
-                    if (scaled) ksc *= scale_s[slot * 8 + warp];
-                    const uint8_t* kb = smem + slot * sbytes + tile_off;
+                    if (scaled) ksc *= scale_s[slot * 8 + wt];
+                    const uint32_t kb = k_at + slot_off;
 #pragma unroll
-                    for (int hb = 0; hb < NHB; ++hb)
+                    for (int e = 0; e < 2; ++e) st[e][0] = st[e][1] = st[e][2] = st[e][3] = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            st[hb][e][0] = st[hb][e][1] = st[hb][e][2] = st[hb][e][3] = 0.f;
-                    if constexpr (KIND == kWinBf16) {
-#pragma unroll
-                        for (int ks = 0; ks < C::kSteps; ++ks) {
-                            uint32_t af[4];
-                            ldsm_x4(af[0], af[1], af[2], af[3],
-                                    kb + (ks / 4) * panel_bytes + at(krow, (ks % 4) * 2 + kch));
-#pragma unroll
-                            for (int hb = 0; hb < NHB; ++hb)
-                                mma<KIND>(st[hb][ks & 1], af, qb[hb][ks][0], qb[hb][ks][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k2 = 0; k2 < C::kSteps / 2; ++k2) {
-                            uint32_t w[4];
-                            ldsm_x4(w[0], w[1], w[2], w[3], kb + at(krow, k2 * 2 + kch));
+                    for (int i = 0; i < C::kPanels * kPairs; ++i) {
+                        uint32_t w[4];
+                        ldsm(w, ((kb + (i / kPairs) * panel_bytes) ^ ((i % kPairs) << 5)));
+                        if constexpr (KIND == kWinBf16) {  // one 16-wide step
+                            mma<KIND>(st[i & 1], w, qb[i][0], qb[i][1]);
+                        } else if constexpr (KIND == kWinE4m3) {  // one 32-wide step, both terms of Q
+                            mma_e4m3(st[0], w, qb[2 * i][0], qb[2 * i + 1][0]);
+                            mma_e4m3(st[1], w, qb[2 * i][1], qb[2 * i + 1][1]);
+                        } else {  // two 16-wide steps
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const uint2 k0 = widen_adjacent<KIND>(w[2 * e]), k1 = widen_adjacent<KIND>(w[2 * e + 1]);
+                                const uint2 k0 = widen_adjacent(w[2 * e]), k1 = widen_adjacent(w[2 * e + 1]);
                                 const uint32_t af[4] = {k0.x, k1.x, k0.y, k1.y};
-#pragma unroll
-                                for (int hb = 0; hb < NHB; ++hb)
-                                    mma<KIND>(st[hb][e], af, qb[hb][2 * k2 + e][0], qb[hb][2 * k2 + e][1]);
+                                mma<KIND>(st[e], af, qb[2 * i + e][0], qb[2 * i + e][1]);
                             }
                         }
                     }
@@ -496,78 +569,81 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
             release();
             const bool have_v = wait_full();
             if (act && have_v) {
-                const float vsc = scaled ? scale_s[slot * 8 + warp] : 1.f;
-                const float lvs = scaled ? log2f(vsc) : 0.f;
+                const float lvs = scaled ? log2f(scale_s[slot * 8 + wt]) : 0.f;
                 // a tile at the edge of what the rows see: mask key by key
-                const bool edge = t0 + 15 > vis.p_first || (t0 + 15 >= a.sinks && t0 <= vis.p_last - a.window);
+                const bool edge = t0 + 15 > p_first || (t0 + 15 >= a.sinks && t0 <= p_last - a.window);
+                float x[4];  // token g: rows 2c, 2c + 1; token g + 8
+                const float f0 = ksc * qf[0], f1 = ksc * qf[1];
+                if constexpr (KIND == kWinE4m3) {
+                    x[0] = fmaf(st[1][0], 0.0625f, st[0][0]) * f0;
+                    x[1] = fmaf(st[1][1], 0.0625f, st[0][1]) * f1;
+                    x[2] = fmaf(st[1][2], 0.0625f, st[0][2]) * f0;
+                    x[3] = fmaf(st[1][3], 0.0625f, st[0][3]) * f1;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = (st[0][e] + st[1][e]) * ksc;
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = t0 + g + (e >> 1) * 8, p = qpos[e & 1];
+                        if (!(t <= p && (t < a.sinks || t > p - a.window))) x[e] = -INFINITY;
+                    }
+                }
                 bool grow = false;
 #pragma unroll
-                for (int hb = 0; hb < NHB; ++hb) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st[hb][0][e] = (st[hb][0][e] + st[hb][1][e]) * ksc;
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int t = t0 + g + (e >> 1) * 8, p = qpos[hb][e & 1];
-                            if (!(t <= p && (t < a.sinks || t > p - a.window))) st[hb][0][e] = -INFINITY;
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float mx = fmaxf(st[hb][0][e], st[hb][0][2 + e]);
-                        grow |= mx > m_run[hb][e] + 8.f;
-                        if (KIND != kWinBf16) grow |= mx + lvs > r_run[hb][e] + 8.f;
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const float mx = fmaxf(x[e], x[2 + e]);
+                    grow |= mx > m_thr[e];
+                    if (KIND != kWinBf16) grow |= mx + lvs > r_thr[e];
                 }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int hb = 0; hb < NHB; ++hb)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float mx = fmaxf(st[hb][0][e], st[hb][0][2 + e]);
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                            float f = 1.f;
-                            if (mx > m_run[hb][e] + 8.f) {
-                                f = ex2(m_run[hb][e] - mx);
-                                l_part[hb][e] *= f;
-                                m_run[hb][e] = mx;
-                            }
-                            if (KIND != kWinBf16) {
-                                f = 1.f;
-                                if (mx + lvs > r_run[hb][e] + 8.f) {
-                                    f = ex2(r_run[hb][e] - (mx + lvs));
-                                    r_run[hb][e] = mx + lvs;
-                                }
-                            }
-#pragma unroll
-                            for (int mb = 0; mb < C::kSteps; ++mb) {
-                                o[hb][mb][e] *= f;
-                                o[hb][mb][2 + e] *= f;
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(x[e], x[2 + e]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        float f = 1.f;
+                        if (mx > m_thr[e]) {
+                            f = m_thr[e] == -INFINITY ? 0.f : ex2(m_ref[e] - mx);
+                            l_part[e] *= f;
+                            m_ref[e] = mx;
+                            m_thr[e] = mx + 8.f;
+                        }
+                        if (KIND != kWinBf16) {
+                            f = 1.f;
+                            mx += lvs;
+                            if (mx > r_thr[e]) {
+                                f = r_thr[e] == -INFINITY ? 0.f : ex2(r_ref[e] - mx);
+                                r_ref[e] = mx;
+                                r_thr[e] = mx + 8.f;
                             }
                         }
-                }
-                uint32_t pb[NHB][2];
 #pragma unroll
-                for (int hb = 0; hb < NHB; ++hb) {
-                    const float mu0 = m_run[hb][0] == -INFINITY ? 0.f : m_run[hb][0];
-                    const float mu1 = m_run[hb][1] == -INFINITY ? 0.f : m_run[hb][1];
-                    const float p0 = ex2(st[hb][0][0] - mu0), p1 = ex2(st[hb][0][1] - mu1);
-                    const float p2 = ex2(st[hb][0][2] - mu0), p3 = ex2(st[hb][0][3] - mu1);
-                    l_part[hb][0] += p0 + p2;
-                    l_part[hb][1] += p1 + p3;
-                    if (KIND != kWinBf16) {
-                        const float d0 = r_run[hb][0] == -INFINITY ? -INFINITY : lvs - r_run[hb][0];
-                        const float d1 = r_run[hb][1] == -INFINITY ? -INFINITY : lvs - r_run[hb][1];
-                        pb[hb][0] = movmatrix_t(p_pair<KIND>(ex2(st[hb][0][0] + d0), ex2(st[hb][0][1] + d1)));
-                        pb[hb][1] = movmatrix_t(p_pair<KIND>(ex2(st[hb][0][2] + d0), ex2(st[hb][0][3] + d1)));
-                    } else {
-                        pb[hb][0] = movmatrix_t(p_pair<KIND>(p0, p1));
-                        pb[hb][1] = movmatrix_t(p_pair<KIND>(p2, p3));
+                        for (int mb = 0; mb < C::kSteps; ++mb) {
+                            o[mb][e] *= f;
+                            o[mb][2 + e] *= f;
+                        }
                     }
                 }
-                const uint8_t* vbuf = smem + slot * sbytes + tile_off;
+                // the sums take the fp32 probabilities; P.V takes them rounded
+                uint32_t pb[2];
+                {
+                    const float p0 = ex2(x[0] - m_ref[0]), p1 = ex2(x[1] - m_ref[1]);
+                    const float p2 = ex2(x[2] - m_ref[0]), p3 = ex2(x[3] - m_ref[1]);
+                    l_part[0] += p0 + p2;
+                    l_part[1] += p1 + p3;
+                    if (KIND != kWinBf16) {
+                        const float d0 = lvs - r_ref[0], d1 = lvs - r_ref[1];
+                        pb[0] = movmatrix_t(p_pair<KIND>(ex2(x[0] + d0), ex2(x[1] + d1)));
+                        pb[1] = movmatrix_t(p_pair<KIND>(ex2(x[2] + d0), ex2(x[3] + d1)));
+                    } else {
+                        pb[0] = movmatrix_t(p_pair<KIND>(p0, p1));
+                        pb[1] = movmatrix_t(p_pair<KIND>(p2, p3));
+                    }
+                }
+                const uint32_t vb_at = v_at + slot_off;
                 // V words of tokens 2c, 2c + 1 (x) and + 8 (y): bits kept
                 auto keep = [&](int p_min, int p_max) {
                     auto seen = [&](int t) { return t <= p_max && (t < a.sinks || t > p_min - a.window); };
@@ -580,9 +656,8 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
                     if constexpr (KIND == kWinBf16) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int mb = 2 * mb2 + e;
-                            ldsm_x4_t(av[e][0], av[e][1], av[e][2], av[e][3],
-                                      vbuf + (mb / 4) * panel_bytes + at(vrow, (mb % 4) * 2 + vch));
+                            const int i = 2 * mb2 + e;
+                            ldsm_t(av[e], (vb_at + (i / kPairs) * panel_bytes) ^ ((i % kPairs) << 5));
                             av[e][0] &= k.x;
                             av[e][1] &= k.x;
                             av[e][2] &= k.y;
@@ -590,30 +665,29 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
                         }
                     } else {
                         uint32_t w[4];
-                        ldsm_x4_t(w[0], w[1], w[2], w[3], vbuf + at(vrow, mb2 * 2 + vch));
+                        ldsm_t(w, vb_at ^ (mb2 << 5));
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             if constexpr (KIND == kWinE4m3) {
                                 w[2 * e] &= k.x;
                                 w[2 * e + 1] &= k.y;
                             }
-                            const uint2 lo = widen_strided<KIND>(w[2 * e]), hi = widen_strided<KIND>(w[2 * e + 1]);
-                            av[e][0] = lo.x;
-                            av[e][1] = lo.y;
-                            av[e][2] = hi.x;
-                            av[e][3] = hi.y;
+                            const uint2 lo2 = widen_strided<KIND>(w[2 * e]), hi2 = widen_strided<KIND>(w[2 * e + 1]);
+                            av[e][0] = lo2.x;
+                            av[e][1] = lo2.y;
+                            av[e][2] = hi2.x;
+                            av[e][3] = hi2.y;
                         }
                     }
                 };
-                const uint2 kp = edge ? keep(vis.p_first, vis.p_last) : make_uint2(~0u, ~0u);
+                const uint2 kp = edge ? keep(p_first, p_last) : make_uint2(~0u, ~0u);
                 bool apart = false;
-                if (MULTI && KIND != kWinInt8 && edge && vis.p_first != vis.p_last) {
+                if (MULTI && KIND != kWinInt8 && edge && p_first != p_last) {
                     // some key is seen by some rows only: is any V value Inf or NaN?
 #pragma unroll
-                    for (int i = 0; i < C::kSteps * C::kElt / 2; ++i) {
+                    for (int i = 0; i < C::kPanels * kPairs; ++i) {
                         uint32_t w[4];
-                        ldsm_x4_t(w[0], w[1], w[2], w[3],
-                                  vbuf + (i / 4) * panel_bytes + at(krow, (i % 4) * 2 + kch));
+                        ldsm_t(w, (k_at + slot_off + (i / kPairs) * panel_bytes) ^ ((i % kPairs) << 5));
                         apart |= non_finite<KIND>(w[0] & kp.x) || non_finite<KIND>(w[1] & kp.y) ||
                                  non_finite<KIND>(w[2] & kp.x) || non_finite<KIND>(w[3] & kp.y);
                     }
@@ -624,29 +698,24 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
                     for (int mb2 = 0; mb2 < C::kSteps / 2; ++mb2) {
                         uint32_t av[2][4];
                         load_v(mb2, kp, av);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int hb = 0; hb < NHB; ++hb)
-                                mma<KIND>(o[hb][2 * mb2 + e], av[e], pb[hb][0], pb[hb][1]);
+                        mma<KIND>(o[2 * mb2], av[0], pb[0], pb[1]);
+                        mma<KIND>(o[2 * mb2 + 1], av[1], pb[0], pb[1]);
                     }
                 } else {
-                    for (int p = vis.p_first; p <= vis.p_last; ++p) {  // one query position at a time
+                    for (int p = p_first; p <= p_last; ++p) {  // one query position at a time
                         const uint2 k1 = keep(p, p);
 #pragma unroll
                         for (int mb2 = 0; mb2 < C::kSteps / 2; ++mb2) {
                             uint32_t av[2][4];
                             load_v(mb2, k1, av);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
+                            for (int e = 0; e < 2; ++e) {
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma<KIND>(d, av[e], pb[0], pb[1]);
 #pragma unroll
-                                for (int hb = 0; hb < NHB; ++hb) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma<KIND>(d, av[e], pb[hb][0], pb[hb][1]);
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x)
-                                        if (qpos[hb][x & 1] == p) o[hb][2 * mb2 + e][x] += d[x];
-                                }
+                                for (int y = 0; y < 4; ++y)
+                                    if (qpos[y & 1] == p) o[2 * mb2 + e][y] += d[y];
+                            }
                         }
                     }
                 }
@@ -654,64 +723,58 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
             release();
         }
 
-        // ---- the row's sums over the warp's lanes, then over its subtiles
+        // ---- the rows' sums over the warp's lanes, then over its subtiles;
+        // references become -inf where there is none
 #pragma unroll
-        for (int hb = 0; hb < NHB; ++hb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float l = l_part[hb][e];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                l_part[hb][e] = l;
-                if (KIND == kWinBf16) r_run[hb][e] = m_run[hb][e];
-            }
+        for (int e = 0; e < 2; ++e) {
+            float l = l_part[e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            l_part[e] = l;
+            if (m_thr[e] == -INFINITY) m_ref[e] = -INFINITY;
+            if (KIND == kWinBf16)
+                r_ref[e] = m_ref[e];
+            else if (r_thr[e] == -INFINITY)
+                r_ref[e] = -INFINITY;
+        }
         if (TS > 1) {
-            constexpr int kPerLane = NHB * (C::kSteps * 4 + 6);
+            constexpr int kPerLane = C::kSteps * 4 + 6;
             float* exch = reinterpret_cast<float*>(smem + lay.exch);
             for (int half = TS / 2; half >= 1; half >>= 1) {
-                float* buf = exch + ((sub & (half - 1)) * Hkv + kh) * kPerLane * 32 + lane;
+                float* buf = exch + ((rs * (TS / 2) + (sub & (half - 1))) * Hkv + kh) * kPerLane * 32 + lane;
+                float* tail = buf + C::kSteps * 4 * 32;
                 if (sub >= half && sub < 2 * half) {
-                    float* w = buf;
 #pragma unroll
-                    for (int hb = 0; hb < NHB; ++hb) {
+                    for (int mb = 0; mb < C::kSteps; ++mb)
 #pragma unroll
-                        for (int mb = 0; mb < C::kSteps; ++mb)
+                        for (int y = 0; y < 4; ++y) buf[(mb * 4 + y) * 32] = o[mb][y];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x, w += 32) *w = o[hb][mb][x];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e, w += 96) {
-                            w[0] = m_run[hb][e];
-                            w[32] = r_run[hb][e];
-                            w[64] = l_part[hb][e];
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        tail[e * 96] = m_ref[e];
+                        tail[e * 96 + 32] = r_ref[e];
+                        tail[e * 96 + 64] = l_part[e];
                     }
                 }
                 named_bar_sync(1, 32 * NC);
                 if (sub < half) {
-                    const float* w = buf;
+                    float f0[2], f1[2];
 #pragma unroll
-                    for (int hb = 0; hb < NHB; ++hb) {
-                        const float* st2 = w + C::kSteps * 4 * 32;
-                        float f0[2], f1[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float m1 = st2[e * 96], r1 = st2[e * 96 + 32], l1 = st2[e * 96 + 64];
-                            const float m = fmaxf(m_run[hb][e], m1), r = fmaxf(r_run[hb][e], r1);
-                            const float mu = m == -INFINITY ? 0.f : m, ru = r == -INFINITY ? 0.f : r;
-                            l_part[hb][e] = l_part[hb][e] * ex2(m_run[hb][e] - mu) + l1 * ex2(m1 - mu);
-                            f0[e] = ex2(r_run[hb][e] - ru);
-                            f1[e] = ex2(r1 - ru);
-                            m_run[hb][e] = m;
-                            r_run[hb][e] = r;
-                        }
-#pragma unroll
-                        for (int mb = 0; mb < C::kSteps; ++mb)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x, w += 32)
-                                o[hb][mb][x] = o[hb][mb][x] * f0[x & 1] + *w * f1[x & 1];
-                        w += 2 * 96;
+                    for (int e = 0; e < 2; ++e) {
+                        const float m1 = tail[e * 96], r1 = tail[e * 96 + 32], l1 = tail[e * 96 + 64];
+                        const float m = fmaxf(m_ref[e], m1), r = fmaxf(r_ref[e], r1);
+                        const float mu = m == -INFINITY ? 0.f : m, ru = r == -INFINITY ? 0.f : r;
+                        l_part[e] = l_part[e] * ex2(m_ref[e] - mu) + l1 * ex2(m1 - mu);
+                        f0[e] = ex2(r_ref[e] - ru);
+                        f1[e] = ex2(r1 - ru);
+                        m_ref[e] = m;
+                        r_ref[e] = r;
                     }
+#pragma unroll
+                    for (int mb = 0; mb < C::kSteps; ++mb)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            o[mb][y] = o[mb][y] * f0[y & 1] + buf[(mb * 4 + y) * 32] * f1[y & 1];
                 }
                 named_bar_sync(1, 32 * NC);
             }
@@ -719,69 +782,64 @@ __global__ void __launch_bounds__(32 * 9, ctas(NHB)) gqa_win_kernel(const __grid
         }
         if (aborted) continue;
 
-        // ---- epilogue: rows hb * 8 + 2c + e; head dims by kind (see the top)
+        // ---- epilogue: rows 2c + e; head dims by kind (see the top)
         const int vslot = static_cast<int>(blockIdx.x) + pc.cur;
 #pragma unroll
-        for (int hb = 0; hb < NHB; ++hb)
+        for (int e = 0; e < 2; ++e) {
+            const int jr = rs * 8 + 2 * c + e, R = rblk * 16 + jr;
+            if (jr >= a.rbn || R >= a.rows) continue;
+            const float l = l_part[e];
+            // l == 0: no visible key (a NaN sum goes through to the output)
+            float f = 0.f;
+            if (l != 0.f) f = a.out_scale * (r_ref[e] == -INFINITY ? 0.f : ex2(r_ref[e] - m_ref[e])) / l;
+            const float lse = l != 0.f ? (m_ref[e] + log2f(l)) * kLn2 : -INFINITY;
+            if (pc.whole) {
+                const int i = MULTI ? R / a.grp : 0;
+                const long long orow =
+                    (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
+                __nv_bfloat16* op = a.out + orow * D;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int jr = hb * 8 + 2 * c + e, R = row0 + jr;
-                if (jr >= a.rbn || R >= a.rows) continue;
-                const float l = l_part[hb][e];
-                // l == 0: no visible key (a NaN sum goes through to the output)
-                float f = 0.f;
-                if (l != 0.f)
-                    f = a.out_scale * (r_run[hb][e] == -INFINITY ? 0.f : ex2(r_run[hb][e] - m_run[hb][e])) / l;
-                const float lse = l != 0.f ? (m_run[hb][e] + log2f(l)) * kLn2 : -INFINITY;
-                if (pc.whole) {
-                    const int i = MULTI ? R / a.grp : 0;
-                    const long long orow =
-                        (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
-                    __nv_bfloat16* op = a.out + orow * D;
-#pragma unroll
-                    for (int mb = 0; mb < C::kSteps; ++mb) {
-                        if constexpr (KIND == kWinBf16) {
-                            op[mb * 16 + g] = __float2bfloat16_rn(o[hb][mb][e] * f);
-                            op[mb * 16 + g + 8] = __float2bfloat16_rn(o[hb][mb][2 + e] * f);
-                        } else {
-                            *reinterpret_cast<uint32_t*>(op + mb * 16 + 2 * g) =
-                                pack_bf16x2(o[hb][mb][e] * f, o[hb][mb][2 + e] * f);
-                        }
+                for (int mb = 0; mb < C::kSteps; ++mb) {
+                    if constexpr (KIND == kWinBf16) {
+                        op[mb * 16 + g] = __float2bfloat16_rn(o[mb][e] * f);
+                        op[mb * 16 + g + 8] = __float2bfloat16_rn(o[mb][2 + e] * f);
+                    } else {
+                        *reinterpret_cast<uint32_t*>(op + mb * 16 + 2 * g) = pack_bf16x2(o[mb][e] * f, o[mb][2 + e] * f);
                     }
-                    if (a.lse && g == 0) a.lse[orow] = lse;
-                } else {
-                    const long long prow = (static_cast<long long>(vslot) * Hkv + kh) * a.rbn + jr;
-                    float* op = a.ws_o + prow * D;
-#pragma unroll
-                    for (int mb = 0; mb < C::kSteps; ++mb) {
-                        if constexpr (KIND == kWinBf16) {
-                            op[mb * 16 + g] = o[hb][mb][e] * f;
-                            op[mb * 16 + g + 8] = o[hb][mb][2 + e] * f;
-                        } else {
-                            *reinterpret_cast<float2*>(op + mb * 16 + 2 * g) =
-                                make_float2(o[hb][mb][e] * f, o[hb][mb][2 + e] * f);
-                        }
-                    }
-                    if (g == 0) a.ws_lse[prow] = lse;
                 }
+                if (a.lse && g == 0) a.lse[orow] = lse;
+            } else {
+                const long long prow = (static_cast<long long>(vslot) * Hkv + kh) * a.rbn + jr;
+                float* op = a.ws_o + prow * D;
+#pragma unroll
+                for (int mb = 0; mb < C::kSteps; ++mb) {
+                    if constexpr (KIND == kWinBf16) {
+                        op[mb * 16 + g] = o[mb][e] * f;
+                        op[mb * 16 + g + 8] = o[mb][2 + e] * f;
+                    } else {
+                        *reinterpret_cast<float2*>(op + mb * 16 + 2 * g) = make_float2(o[mb][e] * f, o[mb][2 + e] * f);
+                    }
+                }
+                if (g == 0) a.ws_lse[prow] = lse;
             }
+        }
     }
 }
 
-template <int D, int KIND, int NHB>
+template <int D, int KIND, int RS>
 cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     const int vb = a.batch * a.rb;
     // dynamic shared memory of one block: 227 KB, or its share of the SM's 228 KB
-    const int limit = ctas(NHB) == 1 ? 227 * 1024 : 228 * 1024 / ctas(NHB) - 1024;
+    const int limit = ctas(RS) == 1 ? 227 * 1024 : 228 * 1024 / ctas(RS) - 1024;
     int ns = kMaxSlots;
-    while (ns > 2 && layout<D, KIND>(a.Hkv, a.ts, NHB, ns, vb, a.batch).total > limit) --ns;
+    while (ns > 2 && layout<D, KIND>(a.Hkv, a.ts, RS, ns, vb, a.batch).total > limit) --ns;
     a.nslots = ns;
-    const int bytes = layout<D, KIND>(a.Hkv, a.ts, NHB, ns, vb, a.batch).total;
-    auto kern = a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true> : gqa_win_kernel<D, KIND, NHB, false>;
+    const int bytes = layout<D, KIND>(a.Hkv, a.ts, RS, ns, vb, a.batch).total;
+    auto kern = a.q_len > 1 ? gqa_win_kernel<D, KIND, RS, true> : gqa_win_kernel<D, KIND, RS, false>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e != cudaSuccess)
         return e;
-    return launch_with_pdl(kern, dim3(grid), dim3(32 * (a.Hkv * a.ts + 1)), bytes, stream, a);
+    return launch_with_pdl(kern, dim3(grid), dim3(32 * (a.Hkv * a.ts * RS + 1)), bytes, stream, a);
 }
 
 template <int KIND>

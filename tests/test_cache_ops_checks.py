@@ -213,6 +213,6 @@ def test_append_query_checks():
 
 def test_row_strides():
     x = torch.zeros(7, 12, 64, dtype=BF)
-    assert mqa._check_rows(x[:, 2:6], "k", (7, 4, 64), 2) == [768]
-    assert mqa._check_rows(x[:1, 2:6], "k", (1, 4, 64), 2) == [256]    # one token: no stride of its own
-    assert mqa._check_rows(x[..., :64].transpose(0, 1), "q_pe", (12, 7, 64), 1) == [64, 768]
+    assert mqa._check_rows(x[:, 2:6], "k", (7, 4, 64), 2) == (768,)
+    assert mqa._check_rows(x[:1, 2:6], "k", (1, 4, 64), 2) == (256,)    # one token: no stride of its own
+    assert mqa._check_rows(x[..., :64].transpose(0, 1), "q_pe", (12, 7, 64), 1) == (64, 768)

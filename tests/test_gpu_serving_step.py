@@ -12,13 +12,13 @@ from test_gpu_append import BF, table
 pytestmark = pytest.mark.gpu
 
 
-def attend(q, cache, scales, bt, lens, page, window, sinks, D, half):
+def attend(q, cache, scales, bt, lens, page, window, sinks, D, kv):
     for b, n in enumerate(lens):
         codes = [ref.gather(cache, bt, b, n, page, i) for i in (0, 1)]
         s = [ref.token_scales(scales, bt, b, n, page, i) if scales is not None
              else torch.ones(n, cache.shape[3], dtype=torch.float64) for i in (0, 1)]
         yield ref.window_decode(q[b].double(), codes[0] * s[0][..., None], codes[1] * s[1][..., None], n, D ** -0.5,
-                                window, sinks, code_v=codes[1], s_v=s[1], half_p=half)
+                                window, sinks, code_v=codes[1], s_v=s[1], half_p=kv != "bf16", e4m3_q=kv.startswith("fp8"))
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3_block", "int8_block"])
@@ -79,7 +79,7 @@ def test_prefill_then_steps(kv, L):
             if pair is None:
                 continue
             o, l = pair[0].cpu().double(), pair[1].cpu().double()
-            for b, (ro, rl, to, tl) in enumerate(attend(q.cpu(), c, s, bt, n, page, w, sk, D, kv != "bf16")):
+            for b, (ro, rl, to, tl) in enumerate(attend(q.cpu(), c, s, bt, n, page, w, sk, D, kv)):
                 assert ((o[b] - ro).abs() <= to).all(), (kv, i, b, w)
                 assert ((l[b] - rl).abs() <= tl).all(), (kv, i, b, w)
 
