@@ -439,9 +439,10 @@ mqa_status gqa_paged_decode(const void* q, const void* kv_cache, const int32_t* 
  *   scale_block is a multiple of 16 that divides page_size. */
 
 /* Workspace bytes of gqa_window_decode and gqa_block_decode: 0 for
- * num_kv_splits == 1, else batch * ceil(rows / 16) * num_kv_splits *
- * num_kv_heads * min(rows, 16) * (head_size + 1) * 4 with rows = q_len *
- * num_q_heads / num_kv_heads.  0 on invalid arguments. */
+ * num_kv_splits == 1; else with rows = q_len * num_q_heads / num_kv_heads and
+ * v = batch * ceil(rows / 16), partials p = v * num_kv_splits * num_kv_heads *
+ * min(rows, 16) of head_size + 1 fp32 (the last rounded up to 8 bytes in all)
+ * and 8 v bytes.  0 on invalid arguments. */
 size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
                                          int num_kv_splits);
 
@@ -482,8 +483,8 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
  *              not matter.  Calls that may overlap need one each.
  *   head_size in {64, 128}; num_kv_heads in [1, 8]; at most 16 query heads per
  *   KV head; q_len * num_q_heads / num_kv_heads <= 128; batch * ceil(that /
- *   16) <= 2048; page_size a multiple of 16.  Other arguments and errors as
- *   for mla_decode. */
+ *   16) <= 2048; page_size a multiple of 16; num_blocks * page_size < 2^30.
+ *   Other arguments and errors as for mla_decode. */
 mqa_status gqa_window_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
                              const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window,
                              int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,

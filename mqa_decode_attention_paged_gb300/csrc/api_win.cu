@@ -36,25 +36,24 @@ Rows rows_of(int q_len, int hq, int hkv) {
     return r;
 }
 
-// A 5D view of the cache, {line, page, panels, heads, 2 * blocks}, whose box
-// is box_tok tokens of every head of one plane: it lands as [head][panel]
-// [token][line] under the swizzle of its line (128 or 64 bytes).  Encoded per
-// call (a fraction of a microsecond): nothing is kept by an address.
-bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, int page, int blocks, int box_tok) {
+// A view of the cache, {line, rows, panels, heads} with rows over blocks,
+// planes and tokens, whose box is box_tok rows of one head: it lands as
+// [panel][row][line] under the swizzle of its line (128 or 64 bytes).  Encoded
+// per call (a fraction of a microsecond): nothing is kept by an address.
+bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, long long rows, int box_tok) {
     auto fn = mqa::api_encode_tiled();
     if (!fn) return false;
     const int line = D * elt >= 128 ? 128 : D * elt;
     const int inner = line / elt, panels = D / inner;
-    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(page),
-                                static_cast<cuuint64_t>(panels), static_cast<cuuint64_t>(hkv),
-                                static_cast<cuuint64_t>(blocks) * 2};
-    const cuuint64_t row = static_cast<cuuint64_t>(hkv) * D * elt;
-    const cuuint64_t strides[4] = {row, static_cast<cuuint64_t>(line), static_cast<cuuint64_t>(D) * elt, row * page};
-    const cuuint32_t box[5] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(box_tok),
-                               static_cast<cuuint32_t>(panels), static_cast<cuuint32_t>(hkv), 1};
-    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(panels), static_cast<cuuint64_t>(hkv)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hkv) * D * elt, static_cast<cuuint64_t>(line),
+                                   static_cast<cuuint64_t>(D) * elt};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(box_tok),
+                               static_cast<cuuint32_t>(panels), 1};
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
     std::memset(out, 0, sizeof *out);
-    return fn(out, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5,
+    return fn(out, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
               const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
               line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -85,10 +84,10 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         if (!kv_scales || !api_aligned(kv_scales, 4) || scale_block < 1) return MQA_ERR_INVALID_ARG;
         if (scale_block % 16 != 0 || page_size % scale_block != 0) return MQA_ERR_UNSUPPORTED;
     }
-    // positions stay clear of INT_MAX by more than a tile (128 tokens) and
-    // the tensor map's plane coordinate 2 * block + 1 stays an int
-    if (static_cast<long long>(max_blocks) * page_size > INT32_MAX - 256 ||
-        static_cast<long long>(num_blocks) * page_size > INT32_MAX)
+    // positions stay clear of INT_MAX by more than a tile (256 tokens), cache
+    // rows (two planes of tokens) are ints
+    if (static_cast<long long>(max_blocks) * page_size > INT32_MAX - 512 ||
+        static_cast<long long>(num_blocks) * page_size > (1 << 30) - 1)
         return MQA_ERR_UNSUPPORTED;
 
     const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
@@ -101,11 +100,15 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
 
     mqa::WinArgs a{};
     const int elt = kv_dtype == MQA_KV_BF16 ? 2 : 1;
+    const mqa::WinKind kind = kv_dtype == MQA_KV_BF16         ? mqa::kWinBf16
+                              : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::kWinInt8
+                                                              : mqa::kWinE4m3;
+    const int warp_tok = 16 * mqa::win_mblocks(kind, r.rbn <= 8 ? 1 : 2);
     a.ts = mqa::win_subtiles(num_kv_heads);
-    // boxes of as many tokens as divide both the page and the tile
-    a.box_tok = 16;
-    while (a.box_tok < 16 * a.ts && page_size % (2 * a.box_tok) == 0) a.box_tok *= 2;
-    if (!cache_map(&a.tmap, kv_cache, elt, head_size, num_kv_heads, page_size, num_blocks, a.box_tok))
+    a.tt = warp_tok * a.ts;
+    a.box_tok = page_size % warp_tok == 0 ? warp_tok : 16;  // a box lies in one page
+    if (!cache_map(&a.tmap, kv_cache, elt, head_size, num_kv_heads,
+                   2LL * num_blocks * page_size, a.box_tok))
         return api_cuda_fail(cudaErrorInvalidValue);
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.kv_scales = block ? kv_scales : nullptr;
@@ -137,16 +140,17 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         const size_t slots = static_cast<size_t>(vb) * num_kv_splits;
         a.ws_o = static_cast<float*>(workspace);
         a.ws_lse = a.ws_o + slots * num_kv_heads * r.rbn * head_size;
-        // units g and virtual requests v use slots g + v <= units + vb - 2
+        a.ws_units = reinterpret_cast<int2*>(a.ws_lse + (slots * num_kv_heads * r.rbn + 1) / 2 * 2);
+        // unit g and virtual request v use slot g + v <= units + vb - 2
         const long long cap = static_cast<long long>(vb) * (num_kv_splits - 1) + 1;
-        const long long fill = static_cast<long long>(sms) * mqa::win_ctas_per_sm(r.rbn);
+        const long long fill = static_cast<long long>(sms) * mqa::kWinCtasPerSm;
         a.units = static_cast<int>(fill < cap ? fill : cap);
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = a.units > 0 ? a.units : vb;
-    const cudaError_t e = kv_dtype == MQA_KV_BF16         ? mqa::win_stage1_bf16(a, head_size, grid, st)
-                          : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::win_stage1_int8(a, head_size, grid, st)
-                                                          : mqa::win_stage1_e4m3(a, head_size, grid, st);
+    const cudaError_t e = kind == mqa::kWinBf16   ? mqa::win_stage1_bf16(a, head_size, grid, st)
+                          : kind == mqa::kWinInt8 ? mqa::win_stage1_int8(a, head_size, grid, st)
+                                                  : mqa::win_stage1_e4m3(a, head_size, grid, st);
     if (e != cudaSuccess) return api_cuda_fail(e);
     if (a.units > 0)
         if (cudaError_t e2 = mqa::win_merge(a, head_size, st); e2 != cudaSuccess) return api_cuda_fail(e2);
@@ -162,8 +166,11 @@ size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, 
     if (!heads_ok(batch, q_len, num_q_heads, num_kv_heads) || head_size < 1 || num_kv_splits < 2) return 0;
     if (!heads_served(batch, q_len, num_q_heads, num_kv_heads)) return 0;
     const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
-    return static_cast<size_t>(batch) * r.rb * num_kv_splits * num_kv_heads * r.rbn *
-           (static_cast<size_t>(head_size) + 1) * 4;
+    // partials [slots, heads, rows] of head_size + 1 floats (padded to 8
+    // bytes), then two ints per virtual request
+    const size_t vb = static_cast<size_t>(batch) * r.rb;
+    const size_t rows = vb * num_kv_splits * num_kv_heads * r.rbn;
+    return rows * head_size * 4 + (rows + 1) / 2 * 8 + vb * 8;
 }
 
 int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_heads) {
@@ -173,7 +180,7 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
     const int sms = mqa::api_sm_count();
     if (sms < 1) return -1;
     const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
-    const int vb = batch * r.rb, fill = sms * mqa::win_ctas_per_sm(r.rbn);
+    const int vb = batch * r.rb, fill = sms * mqa::kWinCtasPerSm;
     return 1 + (fill - 1 + vb - 1) / vb;  // the smallest budget that lets units fill the device (2 at least)
 }
 

@@ -1,5 +1,5 @@
 // Windowed and block-scaled GQA paged decode: arguments, the visible-key plan
-// shared by the stage-1 kernels and the merge, and the host interface.
+// of the stage-1 kernels, and the host interface.
 //
 // A request's query rows (q_len positions x the query heads of a KV head) are
 // cut into row blocks of 16; request and row block together are one "virtual
@@ -7,10 +7,9 @@
 // key t iff  t <= p and (t < sinks or t > p - window), so the keys of a row
 // block are the sinks [0, min(sinks, hi)) and the run [lo, hi), where hi is
 // its last position + 1 and lo = max(0, first position - window + 1).  They
-// are walked in tiles of TT = 16 TS consecutive tokens (TS subtiles of 16,
-// one per group of Hkv consumer warps); the tiles of all virtual requests are
-// laid end to end and cut into units of equal size, one per thread block, so
-// only tiles that hold a visible key are ever read.
+// are walked in tiles of `tt` consecutive tokens; the tiles of all virtual
+// requests are laid end to end and cut into units of about equal size, one
+// per thread block, so only tiles that hold a visible key are ever read.
 #pragma once
 
 #include <cuda.h>
@@ -26,7 +25,7 @@ constexpr int kWinMaxVirtual = 2048;  // virtual requests whose tile prefix fits
 constexpr int kWinNoWindow = 1 << 30;
 
 struct WinArgs {
-    CUtensorMap tmap;  // {inner, page tokens, panels, heads, 2 planes x blocks}
+    CUtensorMap tmap;  // {line, rows (block, plane, token), panels, heads}
     const __nv_bfloat16* q;   // [batch, q_len, Hq, D]
     const float* kv_scales;   // [blocks, 2, page / scale_block, Hkv], or null: no block scales
     const int32_t* block_table;
@@ -35,6 +34,7 @@ struct WinArgs {
     float* lse;
     float* ws_o;    // [slots, Hkv, rbn, D], normalised partials
     float* ws_lse;  // [slots, Hkv, rbn]
+    int2* ws_units; // [batch * rb]: first and last unit of each virtual request
     int* status;
     float sl2;        // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
     float out_scale;  // v_scale of a per-tensor e4m3 cache, else 1
@@ -42,11 +42,11 @@ struct WinArgs {
     int num_blocks, page, max_blocks;
     int window, sinks;
     int scale_block, scale_groups;  // tokens per scale, scales per page
-    int box_tok;                    // tokens of one copied box (divides the page and the tile)
+    int box_tok;                    // tokens of one copied box (divides the page and a warp's tile)
     int rb, rbn;                    // row blocks per request; rows of a (full) row block
-    int ts;                         // subtiles per tile
+    int ts, tt;                     // warps that share a KV head; tokens of a tile (all of them)
     int units;                      // 0: one unit per virtual request, else the balanced unit count
-    int nslots;
+    int nslots;                     // slots of a warp's ring
 };
 
 // The tiles of one virtual request.
@@ -73,7 +73,7 @@ __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
     WinVis v;
     const int r0 = r * 16, r1 = min(a.rows, r0 + 16) - 1;
     const int i0 = a.q_len == 1 ? 0 : r0 / a.grp, i1 = a.q_len == 1 ? 0 : r1 / a.grp;
-    const int tt = 16 * a.ts;
+    const int tt = a.tt;
     v.n = n;
     v.p_first = n - a.q_len + i0;
     v.p_last = n - a.q_len + i1;
@@ -86,21 +86,41 @@ __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
     return v;
 }
 
-// Balanced mode with T tiles: units actually used.  A unit holds kWinMinTiles
-// tiles at least where there are enough, so that short work is not spread
-// over more partials than its merge is worth.
-constexpr int kWinMinTiles = 2;
-__device__ __forceinline__ int win_units(int units, int T) { return min(units, max(1, T / kWinMinTiles)); }
+// Balanced mode with T tiles: units actually used.
+__device__ __forceinline__ int win_units(int units, int T) { return min(units, max(1, T)); }
 
-// Subtiles per tile for Hkv KV heads: 8 consumer warps, or one per KV head
-// where Hkv does not divide 8 evenly.
+// First tile of unit g of U: g T / U, moved to a request's start or end where
+// one lies a tile away and units hold four tiles at least: a cut costs a
+// merge and a start, about a tile's time, so nothing further is worth the
+// imbalance.  Non-decreasing in g.
+__device__ __forceinline__ int win_unit_start(const int* cum, int vb, int T, int U, int g) {
+    if (g >= U) return T;
+    const int x = static_cast<int>(static_cast<long long>(g) * T / U);
+    int lo = 0, hi = vb - 1;  // the last virtual request starting at or before x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int near = T / U >= 4 ? 1 : 0;
+    if (x - cum[lo] <= near) return cum[lo];
+    return cum[lo + 1] - x <= near ? cum[lo + 1] : x;
+}
+
+// Warps that share a KV head: 8 warps in all, or one per KV head where Hkv
+// does not divide 8 evenly.
 __host__ __device__ inline int win_subtiles(int hkv) { return hkv == 1 ? 8 : (hkv == 2 ? 4 : (hkv <= 4 ? 2 : 1)); }
+
+// 16-token MMA blocks of a warp's tile: two over 8-bit codes with up to 8
+// rows, else one.
+__host__ __device__ constexpr int win_mblocks(int kind, int nhb) { return kind != kWinBf16 && nhb == 1 ? 2 : 1; }
 
 cudaError_t win_stage1_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_int8(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_merge(const WinArgs& a, int D, cudaStream_t stream);
-// Thread blocks of stage 1 resident on one SM.
-int win_ctas_per_sm(int rbn);
+constexpr int kWinCtasPerSm = 2;  // thread blocks of stage 1 resident on one SM
 
 }  // namespace mqa

@@ -9,31 +9,38 @@
 // twice that per 8-bit byte, far below the tensor rate), and, with an 8-bit
 // cache, the instructions that widen the codes.
 //
-// One thread block = up to 8 consumer warps + 1 producer warp, two blocks per
-// SM for up to 8 rows.  The producer copies the K and then the V plane of a
-// tile (16 TS tokens, all KV heads) into a ring of slots with 5D tensor
-// copies whose box lands head after head, each head a dense tile of 16-token
-// rows under the 128-byte (64-byte) swizzle, so ldmatrix over eight tokens is
-// free of bank conflicts and nothing is padded.  Block scales ride along as
-// 4-byte asynchronous copies counted on the same barrier.  Consumer warp w
-// takes KV head w % Hkv and subtile w / Hkv of every tile.
-//   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows per
-//     row group), O^T = V^T P^T (16 head dims x 8 rows).
-//   * 8-bit codes stay codes in shared memory.  K: one ldmatrix gives a lane
-//     four consecutive codes of a token; the reduction order inside a
-//     16-wide step is permuted alike in Q.  V: ldmatrix.trans over byte
-//     pairs gives a lane two head dims of two tokens; a byte permute makes
-//     the two f16 pairs, so accumulator rows g and g + 8 are head dims 2g and
-//     2g + 1 and V is never written back widened.
-//   * Online softmax in base 2; the reference maximum moves only when a logit
-//     exceeds it by more than 8, which a warp vote finds without reductions.
-//     The numerators keep a reference of their own for x + log2(s_v): the
-//     weights of P.V stay within the f16 range whatever the scales'
-//     magnitude, and no rescaling of V is needed.
+// One thread block = up to 8 warps, two blocks per SM (128 registers a
+// thread).  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
+// feeds itself: it keeps a ring of slots in shared memory, copies its own
+// head's K rows and then V rows of a tile into it with tensor copies (16 or 32
+// token rows of one head, 128-byte or 64-byte swizzle: ldmatrix over eight
+// tokens is free of bank conflicts and nothing is padded), and refills a slot
+// as soon as it has read it.  There is no producer warp (whose registers
+// would cost every thread 32) and no barrier between warps but a meeting
+// every kMeet tiles, which keeps the heads of a token row together: a probe
+// that only copies reads 6.9 TB/s with such per-head boxes and three 2 KB
+// slots, but 3.9 TB/s where six slots let the warps drift apart.  Block ids
+// are fetched 16 or 32 tiles at a time, one lane per tile, across requests.
+//   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows),
+//     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.  With two
+//     groups Q lies in shared memory instead of registers.
+//   * 8-bit codes stay codes in shared memory and are widened to f16 in
+//     registers.  K: four consecutive codes of a token to a lane; Q has the
+//     same order.  V: ldmatrix.trans over byte pairs gives a lane two head dims
+//     of two tokens; byte permutes make the two f16 pairs, so accumulator rows
+//     g and g + 8 are head dims 2g and 2g + 1.  (The warp-level e4m3 MMA is no
+//     way around the widening: with K as codes and Q in two e4m3 terms the
+//     kernel ran 507 instructions per 16 tokens and head, 399 us against
+//     ## on the batch of 256 with lognormal lengths.)
+//   * Online softmax in base 2; the reference moves only when a logit exceeds
+//     it by more than 8, which a warp vote finds without reductions.  Over
+//     8-bit caches the numerators keep a reference of their own for x +
+//     log2(s_v): the weights of P.V stay within the f16 range whatever the
+//     scales' magnitude, and V is not rescaled.
 //   * Masked keys: their logits are replaced by -inf, and V bits of keys that
-//     no row of the block sees are cleared in registers, so stale or non-finite
+//     no row of the warp sees are cleared in registers, so stale or non-finite
 //     bytes never reach an accumulator (int8 codes are always finite).  Where
-//     a key is seen by some rows only and its V holds an Inf or NaN, the rows
+//     a key is seen by some rows only and a V value is Inf or NaN, the rows
 //     are summed apart.
 #pragma once
 
@@ -45,49 +52,54 @@
 namespace mqa {
 namespace win {
 
-constexpr int kMaxSlots = 12;
+constexpr int kMaxSlots = 4;
+constexpr int kDesc = 64;   // box descriptions kept per warp: the chunk being copied and the one before
+constexpr int kMeet = 8;    // tiles between meetings of a block's warps
+constexpr float kNone = -3e38f;  // reference before the first logit
 
-template <int D, int KIND>
+template <int D, int KIND, int NHB>
 struct Cfg {
     static constexpr int kElt = KIND == kWinBf16 ? 2 : 1;
     static constexpr int kLine = D * kElt >= 128 ? 128 : D * kElt;  // bytes of one swizzled line
     static constexpr int kPanels = D * kElt / kLine;
     static constexpr int kSteps = D / 16;
-    __host__ __device__ static int slot_bytes(int hkv, int ts) { return 16 * ts * hkv * D * kElt; }
+    static constexpr int kMT = win_mblocks(KIND, NHB);
+    static constexpr int kTok = 16 * kMT;            // tokens of a warp's tile
+    static constexpr int kSlot = kTok * D * kElt;    // bytes of a slot (one plane of it)
+    static constexpr int kQBytes = NHB == 1 ? 0 : 16 * D * 2;  // a warp's Q
+    static constexpr int kExch = (16 + 6 * NHB) * 128;         // one warp's hand-over buffer
 };
-
-// Row splits: a row block of more than 8 rows is shared by two sets of
-// consumer warps of 8 rows each, in one thread block per SM (16 + 1 warps)
-// instead of two (8 + 1 warps each).  The second set reads and widens the same
-// tile again, but a warp then holds 8 rows' accumulators and 16 warps hide
-// each other's latencies; 16 rows to a warp (168 registers, 8 warps per SM)
-// measured 112 us where this takes 60 (32 requests x 4 positions, window
-// 4096, e4m3 blocks).
-__host__ __device__ constexpr int ctas(int rs) { return rs == 1 ? 2 : 1; }
 
 struct Layout {
-    int exch, scales, ok, bars, cum, total;  // the ring of slots comes first
+    int q, exch, scales, desc, bars, cum, total;  // the warps' rings come first
 };
 
-template <int D, int KIND>
-__host__ __device__ inline Layout layout(int hkv, int ts, int rs, int nslots, int vb, int batch) {
+template <int D, int KIND, int NHB>
+__host__ __device__ inline Layout layout(int hkv, int ts, int nslots, int vb, int batch) {
+    using C = Cfg<D, KIND, NHB>;
+    const int nc = hkv * ts;
     Layout l;
-    l.exch = nslots * Cfg<D, KIND>::slot_bytes(hkv, ts);
-    // TS > 1: half of the consumer warps hand (O, m, r, l) to the other half
-    l.scales = l.exch + (ts > 1 ? hkv * (ts / 2) * rs * (D / 16 * 4 + 6) * 128 : 0);
-    l.ok = l.scales + nslots * 32;
-    l.bars = l.ok + (nslots * 4 + 7) / 8 * 8;
-    l.cum = l.bars + nslots * 16;
+    l.q = nc * nslots * C::kSlot;
+    l.exch = l.q + nc * C::kQBytes;
+    l.scales = l.exch + (ts > 1 ? nc / 2 * C::kExch : 0);
+    l.desc = l.scales + nc * kMaxSlots * 8;
+    l.bars = l.desc + nc * kDesc * 16;
+    l.cum = l.bars + nc * kMaxSlots * 8;
     l.total = l.cum + 4 * (vb + 1 + batch) + 1024;  // + alignment of the base
     return l;
 }
 
-__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int y, int plane, uint64_t* bar) {
+// Box of one head from cache row `row` on.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const void* tmap, int row, int head, uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %2, %2, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(tmap), "r"(0), "r"(y), "r"(plane), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %2, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(row), "r"(head), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
@@ -108,15 +120,6 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
-}
-
-// 16 tokens x 32 e4m3 codes times 32 e4m3 x 8 rows.
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -166,10 +169,15 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
 __device__ __forceinline__ uint32_t int8_pair(uint32_t u, uint32_t sel) {
     return half2_bits(__hsub2(bits_half2(__byte_perm(u, 0x64646464u, sel)), bits_half2(0x64806480u)));
 }
-// Four int8 codes -> the f16 pairs of bytes (0, 1) and (2, 3).
+// Four codes -> the f16 pairs of bytes (0, 1) and (2, 3).
+template <int KIND>
 __device__ __forceinline__ uint2 widen_adjacent(uint32_t w) {
-    const uint32_t u = w ^ 0x80808080u;
-    return make_uint2(int8_pair(u, 0x4140), int8_pair(u, 0x4342));
+    if constexpr (KIND == kWinInt8) {
+        const uint32_t u = w ^ 0x80808080u;
+        return make_uint2(int8_pair(u, 0x4140), int8_pair(u, 0x4342));
+    } else {
+        return make_uint2(e4m3_pair(w), e4m3_pair(w >> 16));
+    }
 }
 // Four codes -> the f16 pairs of bytes (0, 2) and (1, 3).
 template <int KIND>
@@ -182,16 +190,6 @@ __device__ __forceinline__ uint2 widen_strided(uint32_t w) {
     }
 }
 
-// Four fp32 values as e4m3 codes (round to nearest), lowest byte first.
-__device__ __forceinline__ uint32_t e4m3_word(const float (&x)[4]) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
-        : "=r"(r)
-        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
-    return r;
-}
-
 // Whether a word of V (two bf16 values or four e4m3 codes) holds an Inf or NaN.
 template <int KIND>
 __device__ __forceinline__ bool non_finite(uint32_t w) {
@@ -201,65 +199,15 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
            (x & 0xff000000u) == 0x7f000000u;
 }
 
-// Walks the (virtual request, tile range) pieces of a unit.
-struct Pieces {
-    int p, p1, v, per_seq, done;
-    int j0, j1, cur, whole;
-    __device__ __forceinline__ void init(const int* cum, int vb, int units, int T, int g) {
-        per_seq = units == 0;
-        done = 0;
-        p = p1 = 0;
-        v = 0;
-        if (per_seq) {
-            v = g;
-            return;
-        }
-        const int U = win_units(units, T);
-        if (g >= U) return;
-        p = static_cast<int>(static_cast<long long>(g) * T / U);
-        p1 = static_cast<int>(static_cast<long long>(g + 1) * T / U);
-        int lo = 0, hi = vb - 1;  // the last virtual request starting at or before p
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= p)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        v = lo;
-    }
-    // The next piece: tiles [j0, j1) of virtual request cur.
-    __device__ __forceinline__ bool next(const int* cum) {
-        if (per_seq) {
-            if (done) return false;
-            done = 1;
-            cur = v;
-            j0 = 0;
-            j1 = cum[v + 1] - cum[v];
-            whole = 1;
-            return true;
-        }
-        if (p >= p1) return false;
-        while (cum[v + 1] <= p) ++v;  // skip virtual requests without keys
-        const int end = min(p1, cum[v + 1]);
-        cur = v;
-        j0 = p - cum[v];
-        j1 = end - cum[v];
-        whole = j0 == 0 && end == cum[v + 1];
-        p = end;
-        return true;
-    }
-};
-
 // cum[0 .. vb]: exclusive prefix of the virtual requests' tile counts; lens:
 // clamped lengths.  Every thread of the block calls it; returns the total.
 __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* lens) {
     const int vb = a.batch * a.rb;
-    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) lens[b] = win_len(a, b, a.status);
-    __syncthreads();
     for (int v = threadIdx.x; v < vb; v += blockDim.x) {
-        const int b = a.rb == 1 ? v : v / a.rb;
-        cum[v + 1] = win_visible(a, v - b * a.rb, lens[b]).nt;
+        const int b = a.rb == 1 ? v : v / a.rb, r = v - b * a.rb;
+        const int n = win_len(a, b, a.status);
+        if (r == 0) lens[b] = n;
+        cum[v + 1] = win_visible(a, r, n).nt;
     }
     if (threadIdx.x == 0) cum[0] = 0;
     __syncthreads();
@@ -281,133 +229,154 @@ __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* len
     return cum[vb];
 }
 
-// MULTI: more than one query position per request; RS: row splits.
-template <int D, int KIND, int RS, bool MULTI>
-__global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(const __grid_constant__ WinArgs a) {
-    using C = Cfg<D, KIND>;
+// A box of tokens: x first token, y its row of the K plane (-1: nothing to
+// copy; the V plane is a page of rows further), z the virtual request and the
+// flags below, w the index of its first K scale.
+constexpr int kFirst = 1 << 16, kLast = 1 << 17, kWhole = 1 << 18;  // of the tile in the unit's run of its request
+constexpr int kNextScale = 1 << 19;  // the box's second 16 tokens have the next scale
+
+// MULTI: more than one query position per request.
+template <int D, int KIND, int NHB, bool MULTI>
+__global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __grid_constant__ WinArgs a) {
+    using C = Cfg<D, KIND, NHB>;
+    constexpr int MT = C::kMT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int Hkv = a.Hkv, TS = a.ts, NT = Hkv * TS, NC = NT * RS, nslots = a.nslots;
+    const int Hkv = a.Hkv, TS = a.ts, NC = Hkv * TS, nslots = a.nslots;
     const int vb = a.batch * a.rb;
-    const Layout lay = layout<D, KIND>(Hkv, TS, RS, nslots, vb, a.batch);
-    const int sbytes = C::slot_bytes(Hkv, TS);
-    float* scale_s = reinterpret_cast<float*>(smem + lay.scales);  // [slot][subtile * Hkv + head]
-    uint32_t* ok_s = reinterpret_cast<uint32_t*>(smem + lay.ok);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);
-    uint64_t* empty = full + nslots;
+    const Layout lay = layout<D, KIND, NHB>(Hkv, TS, nslots, vb, a.batch);
     int* cum = reinterpret_cast<int*>(smem + lay.cum);
     int* lens = cum + vb + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp / Hkv, kh = warp - sub * Hkv;
     const bool scaled = KIND != kWinBf16 && a.kv_scales != nullptr;
+    const uint32_t ring = smem_u32(smem) + warp * nslots * C::kSlot;
+    float* scale_s = reinterpret_cast<float*>(smem + lay.scales) + warp * kMaxSlots * 2;  // [slot][MMA block]
+    int4* desc_s = reinterpret_cast<int4*>(smem + lay.desc) + warp * kDesc;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars) + warp * kMaxSlots;
+    const int nb = C::kTok / a.box_tok;  // boxes of a warp's tile (1 or 2)
 
-    if (threadIdx.x == 0) {
-        prefetch_tmap(&a.tmap);
-        for (int s = 0; s < nslots; ++s) {
-            mbar_init(&full[s], scaled ? 33 : 1);
-            mbar_init(&empty[s], NC);
-        }
+    if (lane == 0) {
+        if (warp == 0) prefetch_tmap(&a.tmap);
+        // a fill: each box's bytes, and its scales
+        for (int s = 0; s < nslots; ++s) mbar_init(&full[s], scaled ? 2 * nb : nb);
         fence_mbar_init();
     }
     pdl_wait();
     pdl_launch_dependents();
     const int T = build_prefix(a, cum, lens);  // contains __syncthreads
-    const int tt = 16 * TS;
-    Pieces pc;
-    pc.init(cum, vb, a.units, T, blockIdx.x);
 
-    if (warp == NC) {
-        // ------------------------------------------------------------ producer
-        const int nbx = tt / a.box_tok;  // boxes per tile (1 .. 8), lane l < nbx copies box l
-        const int bbytes = sbytes / nbx;
-        const int per = 32 / nbx;  // tiles whose block ids one load of the warp holds
-        const int lt = lane / nbx, lb = lane - lt * nbx;
-        int slot = 0;
-        uint32_t phase = 0;
-        uint32_t used = 0, parity = 0;  // slots ever filled, and the parity of their last fill
-        bool dead = false;
-        while (!dead && pc.next(cum)) {
-            const int b = a.rb == 1 ? pc.cur : pc.cur / a.rb;
-            const WinVis vis = win_visible(a, pc.cur - b * a.rb, lens[b]);
-            const int s_end = min(a.sinks, vis.hi);
-            const int32_t* bt = a.block_table + static_cast<long long>(b) * a.max_blocks;
-            // block id of box lb of tile j + lt, -1 where the box holds no visible key
-            auto load_ids = [&](int j) {
-                if (lt >= per || j + lt >= pc.j1) return -1;
-                const int tok = vis.tile(j + lt) * tt + lb * a.box_tok;
-                const bool need = tok < vis.hi && (tok + a.box_tok > vis.lo || tok < s_end);
-                if (!need) return -1;
-                const int id = __ldg(bt + tok / a.page);
-                if (id < 0 || id >= a.num_blocks) {
-                    report(a.status, MQA_ERR_DEVICE_CHECK);
-                    return -1;
-                }
-                return id;
-            };
-            int ids = load_ids(pc.j0), next_ids = load_ids(pc.j0 + per);
-            int base = pc.j0;
-            for (int j = pc.j0; !dead && j < pc.j1; ++j) {
-                if (j == base + per) {
-                    base = j;
-                    ids = next_ids;
-                    next_ids = load_ids(base + per);
-                }
-                const int t0 = vis.tile(j) * tt;
-                const int id = __shfl_sync(0xffffffffu, ids, ((j - base) * nbx + lane) & 31);
-                const bool valid = lane < nbx && id >= 0;
-                const uint32_t ok = __ballot_sync(0xffffffffu, valid);
-                const int tok = t0 + lane * a.box_tok;  // of box `lane`
-                // scale `lane`: subtile lane / Hkv, head lane % Hkv
-                const int sub = lane / Hkv, stok = t0 + sub * 16;
-                const int sbox = min(sub * 16 / a.box_tok, nbx - 1);
-                const int sid = __shfl_sync(0xffffffffu, id, sbox);
-                const bool has_scale = scaled && lane < NT && sid >= 0;
-#pragma unroll
-                for (int plane = 0; plane < 2; ++plane) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1))) {
-                        report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-                        dead = true;
-                        break;
-                    }
-                    if (lane == 0) {
-                        ok_s[slot] = ok;
-                        mbar_arrive_expect_tx(&full[slot], __popc(ok) * bbytes);
-                    }
-                    __syncwarp();
-                    if (valid)
-                        tma_load_5d(smem + slot * sbytes + lane * bbytes, &a.tmap, tok % a.page, id * 2 + plane,
-                                    &full[slot]);
-                    if (scaled) {
-                        if (has_scale)
-                            cp_async_4(scale_s + slot * 8 + lane,
-                                       a.kv_scales + ((static_cast<long long>(sid) * 2 + plane) * a.scale_groups +
-                                                      (stok % a.page) / a.scale_block) * Hkv + (lane - sub * Hkv));
-                        cp_async_arrive(&full[slot]);
-                    }
-                    used |= 1u << slot;
-                    parity = (parity & ~(1u << slot)) | (phase << slot);
-                    if (++slot == nslots) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
+    // this block's tiles [p0, p1)
+    int p0, p1;
+    if (a.units == 0) {
+        p0 = cum[blockIdx.x];
+        p1 = cum[blockIdx.x + 1];
+    } else {
+        const int U = win_units(a.units, T);
+        const int x = win_unit_start(cum, vb, T, U, static_cast<int>(blockIdx.x) + (lane & 1));
+        p0 = __shfl_sync(0xffffffffu, x, 0);
+        p1 = __shfl_sync(0xffffffffu, x, 1);
+    }
+    // virtual requests without a key: out = 0, lse = -inf
+    for (int v = blockIdx.x; v < vb; v += gridDim.x) {
+        if (cum[v + 1] > cum[v]) continue;
+        const int b = v / a.rb, r0 = (v - b * a.rb) * 16, rows = min(a.rows - r0, 16);
+        for (int i = threadIdx.x; i < Hkv * rows * (D / 8); i += blockDim.x) {
+            const int h = i / (rows * (D / 8)), R = r0 + i / (D / 8) % rows, qi = R / a.grp;
+            const long long orow = (static_cast<long long>(b) * a.q_len + qi) * a.Hq + h * a.grp + R - qi * a.grp;
+            *reinterpret_cast<uint4*>(a.out + orow * D + i % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse && i % (D / 8) == 0) a.lse[orow] = -INFINITY;
         }
-        // no copy of this block may be in flight when it ends
-        for (int s = 0; s < nslots; ++s)
-            if ((used >> s) & 1u)
-                if (!mbar_wait(&full[s], (parity >> s) & 1u)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-        return;
+        if (a.units > 0 && threadIdx.x == 0) a.ws_units[v] = make_int2(0, 0);
     }
 
-    // ------------------------------------------------------------- consumers
+    // ---- copying.  Boxes are described 32 at a time, a lane each (across
+    // requests), in shared memory for the copies and for the reader; the block
+    // ids of the next 32 are fetched meanwhile.
+    const int boxes = (p1 - p0) * nb;
+    int next_id = -1;
+    // Box i of this block's run: where it lies; false where no row sees a key of it.
+    auto locate = [&](int i, int4& d) {
+        const int P = p0 + i / nb;
+        int lo = 0, hi = vb - 1;  // the last virtual request starting at or before P
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cum[mid] <= P)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int b = a.rb == 1 ? lo : lo / a.rb;
+        const WinVis vis = win_visible(a, lo - b * a.rb, lens[b]);
+        const int c0 = cum[lo], c1 = cum[lo + 1];
+        d.x = vis.tile(P - c0) * a.tt + sub * C::kTok + i % nb * a.box_tok;
+        d.z = lo | (P == max(c0, p0) ? kFirst : 0) | (P + 1 == min(c1, p1) ? kLast : 0) |
+              (c0 >= p0 && c1 <= p1 ? kWhole : 0);
+        d.y = b;
+        // only boxes with a visible key are read, and only their block ids
+        return d.x < vis.hi && (d.x + a.box_tok > vis.lo || d.x < min(a.sinks, vis.hi));
+    };
+    auto fetch_id = [&](int i) {
+        int4 d;
+        next_id = -1;
+        if (i < boxes && locate(i, d)) {
+            next_id = __ldg(a.block_table + static_cast<long long>(d.y) * a.max_blocks + d.x / a.page);
+            if (next_id < 0 || next_id >= a.num_blocks) next_id = -2;
+        }
+    };
+    auto describe = [&](int i) {  // box i, whose id has been fetched
+        int4 d;
+        if (i < boxes) {
+            locate(i, d);
+            if (next_id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
+            const int in_page = d.x % a.page;
+            d.y = next_id < 0 ? -1 : next_id * 2 * a.page + in_page;
+            if (scaled) {
+                d.w = (next_id * 2 * a.scale_groups + in_page / a.scale_block) * Hkv + kh;
+                if ((in_page + 16) / a.scale_block != in_page / a.scale_block) d.z |= kNextScale;
+            }
+            desc_s[i & (kDesc - 1)] = d;
+        }
+        __syncwarp();
+    };
+    const int loads = 2 * (p1 - p0);  // planes to copy: K, V, K, V ..
+    int issued = 0, i_slot = 0;
+    // After a wait ran out (`copy` false) boxes are still described, so that
+    // the warp keeps meeting the others, but nothing is copied.
+    auto issue = [&](bool copy) {
+        const int first = (issued >> 1) * nb, plane = issued & 1;
+        if (plane == 0 && (first & 31) == 0) {
+            describe(first + lane);
+            fetch_id(first + 32 + lane);
+        }
+        if (lane < nb && copy) {
+            const int4 d = desc_s[(first + lane) & (kDesc - 1)];
+            constexpr int kBox16 = 16 * D * C::kElt;  // bytes of 16 tokens
+            const int bytes = nb == 1 ? C::kSlot : kBox16;
+            if (d.y >= 0) {
+                mbar_arrive_expect_tx(&full[i_slot], bytes);
+                tma_load_rows(ring + i_slot * C::kSlot + lane * kBox16, &a.tmap, d.y + plane * a.page, kh,
+                              &full[i_slot]);
+                if (scaled) {
+                    const float* sp = a.kv_scales + d.w + plane * (a.scale_groups * Hkv);
+                    float* dst = scale_s + i_slot * 2 + lane;
+                    cp_async_4(dst, sp);
+                    if (MT == 2 && nb == 1) cp_async_4(dst + 1, sp + (d.z & kNextScale ? Hkv : 0));
+                    cp_async_arrive(&full[i_slot]);
+                }
+            } else {
+                mbar_arrive(&full[i_slot]);
+                if (scaled) mbar_arrive(&full[i_slot]);
+            }
+        }
+        ++issued;
+        if (++i_slot == nslots) i_slot = 0;
+    };
+    fetch_id(lane);
+    for (int s = 0; s < nslots && issued < loads; ++s) issue(true);
+
+    // ---- reading
     const int g = lane >> 2, c = lane & 3;
-    const int rs = RS == 1 ? 0 : warp / NT, wt = RS == 1 ? warp : warp - rs * NT;
-    const int sub = wt / Hkv, kh = wt - sub * Hkv;
-    const int box = sub * 16 / a.box_tok;
-    // this warp's 16-token tile inside a slot, panel p at + p * panel_bytes
-    const int panel_bytes = a.box_tok * C::kLine;
-    const uint32_t tile = smem_u32(smem) + box * (sbytes / (tt / a.box_tok)) + kh * C::kPanels * panel_bytes +
-                          (sub * 16 - box * a.box_tok) * C::kLine;
     // A lane's ldmatrix address of 16-byte chunks 2i, 2i + 1 of its row is
     // (row, chunk 0 or 1) with bit 5 + flipped by i: the swizzle only xors.
     // K (and 8-bit V) matrices are (tokens 0-7, chunk), (8-15, chunk),
@@ -416,240 +385,263 @@ __global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(co
         if constexpr (C::kLine == 128) return row * 128 + ((ch ^ (row & 7)) << 4);
         return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
     };
-    const uint32_t k_at = tile + lane_at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t k_at = ring + lane_at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
     const uint32_t v_at =
-        KIND == kWinBf16 ? tile + lane_at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) : k_at;
-    constexpr int kPairs = C::kLine / 32;  // chunk pairs of one line
+        KIND == kWinBf16 ? ring + lane_at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) : k_at;
+    constexpr int kPairs = C::kLine / 32;         // chunk pairs of one line
+    constexpr int kPanel = C::kTok * C::kLine;    // bytes of one panel of a slot
+    // Q in shared memory (two row groups): 16 rows of 2 D bytes, chunks xored
+    // by the row; matrices (rows 0-7, chunk), (0-7, chunk + 1), (8-15, ..)
+    const uint32_t q_base = smem_u32(smem) + lay.q + warp * C::kQBytes;
+    const uint32_t q_at =
+        q_base + ((lane & 7) + (lane >> 4) * 8) * (2 * D) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 
     int slot = 0;
-    uint32_t phase = 0, slot_off = 0;
+    uint32_t phase = 0;
     bool aborted = false;
+    int copied = 0;  // fills issued when the warp gave up
     // A wait that runs out is reported once; from then on the warp waits for
-    // nothing and writes nothing, but still meets the other warps.
+    // nothing, copies and writes nothing, but still meets the other warps.
     auto wait_full = [&]() {
-        if (aborted) return false;
-        if (__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) return true;
+        if (aborted) return;
+        if (__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) return;
         report(a.status, MQA_ERR_DEVICE_TIMEOUT);
         aborted = true;
-        return false;
+        copied = issued;
     };
-    auto release = [&]() {
+    auto refill = [&]() {  // the slot has been read
         __syncwarp();
-        if (lane == 0 && !aborted) mbar_arrive(&empty[slot]);
-        slot_off += sbytes;
         if (++slot == nslots) {
             slot = 0;
-            slot_off = 0;
             phase ^= 1;
         }
+        if (issued < loads) issue(!aborted);
     };
 
-    while (pc.next(cum)) {
-        const int b = a.rb == 1 ? pc.cur : pc.cur / a.rb;
-        const int rblk = pc.cur - b * a.rb;
-        const WinVis vis = win_visible(a, rblk, lens[b]);
-        const int row0 = rblk * 16 + rs * 8;
-        // positions of this warp's first and last row, and the keys they see
-        const int i_last = (min(a.rows, row0 + 8) - 1) / a.grp;
-        const int p_first = MULTI ? vis.n - a.q_len + row0 / a.grp : vis.p_first;
-        const int p_last = MULTI ? vis.n - a.q_len + i_last : vis.p_last;
-        const int lo = p_first - a.window;  // the last key before the window of the first row
-        const bool idle = RS > 1 && row0 >= a.rows;
+    int p_first = 0, p_last = 0;  // positions of the row block's first and last row
+    uint32_t qb[NHB == 1 ? C::kSteps : 1][2];
+    float o[NHB][C::kSteps][4];
+    float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
 
-        // Q^T operand (row g): bf16; f16 in the order of the int8 codes' words;
-        // or two e4m3 terms of the row scaled by a power of two, q = f (q1 +
-        // q2 / 16): 4 + 4 significant bits hold a bf16 value exactly, down to
-        // 2^-21 of the row's largest entry
-        uint32_t qb[C::kSteps][2];
-        float qf[2] = {1.f, 1.f};  // f of rows 2c, 2c + 1 (e4m3)
-        int qpos[2];               // positions of rows 2c, 2c + 1
-        {
-            const int R = row0 + g;
-            const int i = MULTI ? R / a.grp : 0;
-            const bool have = R < a.rows;
-            const __nv_bfloat16* qr =
-                a.q + ((static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp)) * D;
-            if constexpr (KIND == kWinBf16) {
+    for (int tile = 0; tile < p1 - p0; ++tile) {
+        if ((tile & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
+        const int4 d = desc_s[(tile * nb) & (kDesc - 1)];
+        const int t0 = d.x, v = d.z & 0xffff;
+        const int b = a.rb == 1 ? v : v / a.rb;
+        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
+        const int n = lens[b];
+
+        if (d.z & kFirst) {
+            p_first = MULTI ? n - a.q_len + row0 / a.grp : n - 1;
+            p_last = MULTI ? n - a.q_len + (min(a.rows, row0 + 16) - 1) / a.grp : n - 1;
+            if (a.units > 0 && threadIdx.x == 0) {
+                // every request's first and last unit, for the merge
+                int2* u = a.ws_units + v;
+                const int P = p0 + tile;
+                if (P == cum[v]) u->x = blockIdx.x;
+                if (cum[v + 1] <= p1) u->y = blockIdx.x;
+            }
 #pragma unroll
-                for (int ks = 0; ks < C::kSteps; ++ks) {
-                    qb[ks][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c)) : 0u;
-                    qb[ks][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c + 8)) : 0u;
-                }
-            } else {
-                uint2 v[C::kSteps];  // entries 16 ks + 4c .. + 3
-#pragma unroll
-                for (int ks = 0; ks < C::kSteps; ++ks)
-                    v[ks] = have ? __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * c)) : make_uint2(0u, 0u);
-                if constexpr (KIND == kWinInt8) {
+            for (int hb = 0; hb < NHB; ++hb) {
+                // Q^T operand (row g): bf16, or f16 in the order of the codes' words
+                uint32_t w[C::kSteps][2];
+                const int R = row0 + hb * 8 + g;
+                const int i = MULTI ? R / a.grp : 0;
+                const bool have = R < a.rows;
+                const __nv_bfloat16* qr =
+                    a.q + ((static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp)) * D;
+                if constexpr (KIND == kWinBf16) {
 #pragma unroll
                     for (int ks = 0; ks < C::kSteps; ++ks) {
-                        qb[ks][0] = q_f16(v[ks].x);
-                        qb[ks][1] = q_f16(v[ks].y);
+                        w[ks][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c)) : 0u;
+                        w[ks][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c + 8)) : 0u;
                     }
                 } else {
-                    float top = 0.f;
 #pragma unroll
-                    for (int ks = 0; ks < C::kSteps; ++ks) {
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[ks].x << 16)),
-                                               fabsf(__uint_as_float(v[ks].x & 0xffff0000u))));
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[ks].y << 16)),
-                                               fabsf(__uint_as_float(v[ks].y & 0xffff0000u))));
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // 2^e above top; the row times 2^(8 - e) stays below 256
-                    const int e = max(-100, static_cast<int>(__float_as_uint(top) >> 23) - 126);
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
-                    const float f = __uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23);
-                    qf[0] = __shfl_sync(0xffffffffu, f, 8 * c);  // of row 2c: any lane with g = 2c
-                    qf[1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-#pragma unroll
-                    for (int ks = 0; ks < C::kSteps; ++ks) {
-                        float x[4] = {__uint_as_float(v[ks].x << 16) * up, __uint_as_float(v[ks].x & 0xffff0000u) * up,
-                                      __uint_as_float(v[ks].y << 16) * up, __uint_as_float(v[ks].y & 0xffff0000u) * up};
-                        const uint32_t hi = e4m3_word(x);
-                        const uint32_t h01 = e4m3_pair(hi), h23 = e4m3_pair(hi >> 16);
-                        const float2 f01 = __half22float2(bits_half2(h01)), f23 = __half22float2(bits_half2(h23));
-                        x[0] = (x[0] - f01.x) * 16.f;
-                        x[1] = (x[1] - f01.y) * 16.f;
-                        x[2] = (x[2] - f23.x) * 16.f;
-                        x[3] = (x[3] - f23.y) * 16.f;
-                        qb[ks][0] = hi;
-                        qb[ks][1] = e4m3_word(x);
+                    for (int ks = 0; ks < C::kSteps; ++ks) {  // entries 16 ks + 4c .. + 3
+                        const uint2 u = have ? __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * c))
+                                             : make_uint2(0u, 0u);
+                        w[ks][0] = q_f16(u.x);
+                        w[ks][1] = q_f16(u.y);
                     }
                 }
-            }
+                if constexpr (NHB == 1) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int Re = min(row0 + 2 * c + e, a.rows - 1);
-                qpos[e] = MULTI ? vis.n - a.q_len + Re / a.grp : vis.p_last;
+                    for (int ks = 0; ks < C::kSteps; ++ks) {
+                        qb[ks][0] = w[ks][0];
+                        qb[ks][1] = w[ks][1];
+                    }
+                } else {
+                    // words 0 and 1 are chunks 2 ks and 2 ks + 1
+                    const int row = hb * 8 + g;
+                    const uint32_t at = q_base + row * (2 * D) + 4 * c;
+                    if (hb == 0) __syncwarp();  // the last reads of the previous request's Q
+#pragma unroll
+                    for (int ks = 0; ks < C::kSteps; ++ks)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) st_shared(at + (((2 * ks + e) ^ g) << 4), w[ks][e]);
+                    if (hb == NHB - 1) __syncwarp();
+                }
+#pragma unroll
+                for (int mb = 0; mb < C::kSteps; ++mb)
+                    o[hb][mb][0] = o[hb][mb][1] = o[hb][mb][2] = o[hb][mb][3] = 0.f;
+                m_ref[hb][0] = m_ref[hb][1] = r_ref[hb][0] = r_ref[hb][1] = kNone;
+                l_part[hb][0] = l_part[hb][1] = 0.f;
             }
         }
-        float o[C::kSteps][4];
-        // references of the sums and (8-bit) of the numerators: base-2
-        // exponents, and the logit above which they move (-inf: none yet)
-        float m_ref[2] = {0.f, 0.f}, m_thr[2] = {-INFINITY, -INFINITY};
-        float r_ref[2] = {0.f, 0.f}, r_thr[2] = {-INFINITY, -INFINITY};
-        float l_part[2] = {0.f, 0.f};
-#pragma unroll
-        for (int mb = 0; mb < C::kSteps; ++mb) o[mb][0] = o[mb][1] = o[mb][2] = o[mb][3] = 0.f;
 
-        for (int j = pc.j0; j < pc.j1; ++j) {
-            const int t0 = vis.tile(j) * tt + sub * 16;
-            float st[2][4];
-            bool act = false;
-            float ksc = a.sl2;
-            if (wait_full()) {
-                act = ((ok_s[slot] >> box) & 1u) && t0 <= p_last && (t0 + 15 > lo || t0 < a.sinks) && !idle;
-                if (act) {
-                    if (scaled) ksc *= scale_s[slot * 8 + wt];
-                    const uint32_t kb = k_at + slot_off;
+        // which of the tile's 16-token blocks hold a key for the warp's rows
+        bool act[MT];
+        bool any = false;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) st[e][0] = st[e][1] = st[e][2] = st[e][3] = 0.f;
+        for (int m = 0; m < MT; ++m) {
+            const int t = t0 + 16 * m;
+            const int id = MT == 1 || nb == 1 || m == 0 ? d.y : desc_s[(tile * 2 + 1) & (kDesc - 1)].y;
+            act[m] = id >= 0 && t <= p_last && (t + 15 > p_first - a.window || t < a.sinks);
+            any |= act[m];
+        }
+        float x[MT][NHB][4];  // logits of token g (rows 2c, 2c + 1) and of token g + 8
+        wait_full();
+        if (any && !aborted) {
+            const uint32_t kb = k_at + slot * C::kSlot;
 #pragma unroll
-                    for (int i = 0; i < C::kPanels * kPairs; ++i) {
-                        uint32_t w[4];
-                        ldsm(w, ((kb + (i / kPairs) * panel_bytes) ^ ((i % kPairs) << 5)));
-                        if constexpr (KIND == kWinBf16) {  // one 16-wide step
-                            mma<KIND>(st[i & 1], w, qb[i][0], qb[i][1]);
-                        } else if constexpr (KIND == kWinE4m3) {  // one 32-wide step, both terms of Q
-                            mma_e4m3(st[0], w, qb[2 * i][0], qb[2 * i + 1][0]);
-                            mma_e4m3(st[1], w, qb[2 * i][1], qb[2 * i + 1][1]);
-                        } else {  // two 16-wide steps
+            for (int m = 0; m < MT; ++m) {
+                float st[NHB][2][4];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint2 k0 = widen_adjacent(w[2 * e]), k1 = widen_adjacent(w[2 * e + 1]);
-                                const uint32_t af[4] = {k0.x, k1.x, k0.y, k1.y};
-                                mma<KIND>(st[e], af, qb[2 * i + e][0], qb[2 * i + e][1]);
-                            }
+                for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) st[hb][e][0] = st[hb][e][1] = st[hb][e][2] = st[hb][e][3] = 0.f;
+#pragma unroll
+                for (int i = 0; i < C::kPanels * kPairs; ++i) {
+                    uint32_t w[4];
+                    ldsm(w, (kb + (i / kPairs) * kPanel + m * 16 * C::kLine) ^ ((i % kPairs) << 5));
+                    constexpr int kE = KIND == kWinBf16 ? 1 : 2;  // 16-wide steps
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        const int ks = kE * i + e;
+                        uint32_t af[4] = {w[0], w[1], w[2], w[3]};
+                        if constexpr (KIND != kWinBf16) {
+                            const uint2 k0 = widen_adjacent<KIND>(w[2 * e]), k1 = widen_adjacent<KIND>(w[2 * e + 1]);
+                            af[0] = k0.x;
+                            af[1] = k1.x;
+                            af[2] = k0.y;
+                            af[3] = k1.y;
+                        }
+                        if constexpr (NHB == 1) {
+                            mma<KIND>(st[0][ks & 1], af, qb[ks][0], qb[ks][1]);
+                        } else {
+                            uint32_t q1[4];
+                            ldsm(q1, q_at ^ (ks << 5));
+#pragma unroll
+                            for (int hb = 0; hb < NHB; ++hb)
+                                mma<KIND>(st[hb][ks & 1], af, q1[2 * hb], q1[2 * hb + 1]);
                         }
                     }
                 }
+                const float ksc = scaled ? a.sl2 * scale_s[slot * 2 + m] : a.sl2;
+#pragma unroll
+                for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[m][hb][e] = (st[hb][0][e] + st[hb][1][e]) * ksc;
             }
-            release();
-            const bool have_v = wait_full();
-            if (act && have_v) {
-                const float lvs = scaled ? log2f(scale_s[slot * 8 + wt]) : 0.f;
-                // a tile at the edge of what the rows see: mask key by key
-                const bool edge = t0 + 15 > p_first || (t0 + 15 >= a.sinks && t0 <= p_last - a.window);
-                float x[4];  // token g: rows 2c, 2c + 1; token g + 8
-                const float f0 = ksc * qf[0], f1 = ksc * qf[1];
-                if constexpr (KIND == kWinE4m3) {
-                    x[0] = fmaf(st[1][0], 0.0625f, st[0][0]) * f0;
-                    x[1] = fmaf(st[1][1], 0.0625f, st[0][1]) * f1;
-                    x[2] = fmaf(st[1][2], 0.0625f, st[0][2]) * f0;
-                    x[3] = fmaf(st[1][3], 0.0625f, st[0][3]) * f1;
-                } else {
+        }
+        refill();
+        wait_full();
+        if (any && !aborted) {
+            float lvs[MT];
+            bool edge[MT];  // at the edge of what the rows see: mask key by key
+            bool grow = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = (st[0][e] + st[1][e]) * ksc;
-                }
-                if (edge) {
+            for (int m = 0; m < MT; ++m) {
+                const int t = t0 + 16 * m;
+                lvs[m] = scaled ? __log2f(scale_s[slot * 2 + m]) : 0.f;
+                edge[m] = !act[m] || t + 15 > p_first || (t + 15 >= a.sinks && t <= p_last - a.window);
+                if (edge[m]) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = t0 + g + (e >> 1) * 8, p = qpos[e & 1];
-                        if (!(t <= p && (t < a.sinks || t > p - a.window))) x[e] = -INFINITY;
-                    }
-                }
-                bool grow = false;
+                    for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mx = fmaxf(x[e], x[2 + e]);
-                    grow |= mx > m_thr[e];
-                    if (KIND != kWinBf16) grow |= mx + lvs > r_thr[e];
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = t + g + (e >> 1) * 8;
+                            const int R = min(row0 + hb * 8 + 2 * c + (e & 1), a.rows - 1);
+                            const int p = MULTI ? n - a.q_len + R / a.grp : n - 1;
+                            if (!act[m] || !(key <= p && (key < a.sinks || key > p - a.window)))
+                                x[m][hb][e] = -INFINITY;
+                        }
+                    if (!act[m]) lvs[m] = 0.f;
                 }
-                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(x[e], x[2 + e]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float mx = fmaxf(x[m][hb][e], x[m][hb][2 + e]);
+                        grow |= mx > m_ref[hb][e] + 8.f;
+                        if (KIND != kWinBf16) grow |= mx + lvs[m] > r_ref[hb][e] + 8.f;
+                    }
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = -INFINITY, mr = -INFINITY;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const float y = fmaxf(x[m][hb][e], x[m][hb][2 + e]);
+                            mx = fmaxf(mx, y);
+                            mr = fmaxf(mr, y + lvs[m]);
+                        }
+#pragma unroll
+                        for (int s = 4; s <= 16; s <<= 1) {
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+                            if (KIND != kWinBf16) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, s));
+                        }
                         float f = 1.f;
-                        if (mx > m_thr[e]) {
-                            f = m_thr[e] == -INFINITY ? 0.f : ex2(m_ref[e] - mx);
-                            l_part[e] *= f;
-                            m_ref[e] = mx;
-                            m_thr[e] = mx + 8.f;
+                        if (mx > m_ref[hb][e] + 8.f) {
+                            f = ex2(m_ref[hb][e] - mx);
+                            l_part[hb][e] *= f;
+                            m_ref[hb][e] = mx;
                         }
                         if (KIND != kWinBf16) {
                             f = 1.f;
-                            mx += lvs;
-                            if (mx > r_thr[e]) {
-                                f = r_thr[e] == -INFINITY ? 0.f : ex2(r_ref[e] - mx);
-                                r_ref[e] = mx;
-                                r_thr[e] = mx + 8.f;
+                            if (mr > r_ref[hb][e] + 8.f) {
+                                f = ex2(r_ref[hb][e] - mr);
+                                r_ref[hb][e] = mr;
                             }
                         }
 #pragma unroll
                         for (int mb = 0; mb < C::kSteps; ++mb) {
-                            o[mb][e] *= f;
-                            o[mb][2 + e] *= f;
+                            o[hb][mb][e] *= f;
+                            o[hb][mb][2 + e] *= f;
                         }
                     }
-                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int t = t0 + 16 * m;
                 // the sums take the fp32 probabilities; P.V takes them rounded
-                uint32_t pb[2];
-                {
-                    const float p0 = ex2(x[0] - m_ref[0]), p1 = ex2(x[1] - m_ref[1]);
-                    const float p2 = ex2(x[2] - m_ref[0]), p3 = ex2(x[3] - m_ref[1]);
-                    l_part[0] += p0 + p2;
-                    l_part[1] += p1 + p3;
+                uint32_t pb[NHB][2];
+#pragma unroll
+                for (int hb = 0; hb < NHB; ++hb) {
+                    const float e0 = ex2(x[m][hb][0] - m_ref[hb][0]), e1 = ex2(x[m][hb][1] - m_ref[hb][1]);
+                    const float e2 = ex2(x[m][hb][2] - m_ref[hb][0]), e3 = ex2(x[m][hb][3] - m_ref[hb][1]);
+                    l_part[hb][0] += e0 + e2;
+                    l_part[hb][1] += e1 + e3;
                     if (KIND != kWinBf16) {
-                        const float d0 = lvs - r_ref[0], d1 = lvs - r_ref[1];
-                        pb[0] = movmatrix_t(p_pair<KIND>(ex2(x[0] + d0), ex2(x[1] + d1)));
-                        pb[1] = movmatrix_t(p_pair<KIND>(ex2(x[2] + d0), ex2(x[3] + d1)));
+                        const float d0 = lvs[m] - r_ref[hb][0], d1 = lvs[m] - r_ref[hb][1];
+                        pb[hb][0] = movmatrix_t(p_pair<KIND>(ex2(x[m][hb][0] + d0), ex2(x[m][hb][1] + d1)));
+                        pb[hb][1] = movmatrix_t(p_pair<KIND>(ex2(x[m][hb][2] + d0), ex2(x[m][hb][3] + d1)));
                     } else {
-                        pb[0] = movmatrix_t(p_pair<KIND>(p0, p1));
-                        pb[1] = movmatrix_t(p_pair<KIND>(p2, p3));
+                        pb[hb][0] = movmatrix_t(p_pair<KIND>(e0, e1));
+                        pb[hb][1] = movmatrix_t(p_pair<KIND>(e2, e3));
                     }
                 }
-                const uint32_t vb_at = v_at + slot_off;
+                const uint32_t vb_at = v_at + slot * C::kSlot + m * 16 * C::kLine;
                 // V words of tokens 2c, 2c + 1 (x) and + 8 (y): bits kept
                 auto keep = [&](int p_min, int p_max) {
-                    auto seen = [&](int t) { return t <= p_max && (t < a.sinks || t > p_min - a.window); };
-                    const int t = t0 + 2 * c;
-                    return make_uint2((seen(t) ? 0xffffu : 0u) | (seen(t + 1) ? 0xffff0000u : 0u),
-                                      (seen(t + 8) ? 0xffffu : 0u) | (seen(t + 9) ? 0xffff0000u : 0u));
+                    auto seen = [&](int key) { return key <= p_max && (key < a.sinks || key > p_min - a.window); };
+                    const int key = t + 2 * c;
+                    return make_uint2((seen(key) ? 0xffffu : 0u) | (seen(key + 1) ? 0xffff0000u : 0u),
+                                      (seen(key + 8) ? 0xffffu : 0u) | (seen(key + 9) ? 0xffff0000u : 0u));
                 };
                 // operand A of head dims 16 mb ..: rows g and g + 8
                 auto load_v = [&](int mb2, uint2 k, uint32_t (&av)[2][4]) {  // blocks 2 mb2, 2 mb2 + 1
@@ -657,7 +649,7 @@ __global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(co
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int i = 2 * mb2 + e;
-                            ldsm_t(av[e], (vb_at + (i / kPairs) * panel_bytes) ^ ((i % kPairs) << 5));
+                            ldsm_t(av[e], (vb_at + (i / kPairs) * kPanel) ^ ((i % kPairs) << 5));
                             av[e][0] &= k.x;
                             av[e][1] &= k.x;
                             av[e][2] &= k.y;
@@ -680,14 +672,16 @@ __global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(co
                         }
                     }
                 };
-                const uint2 kp = edge ? keep(p_first, p_last) : make_uint2(~0u, ~0u);
+                uint2 kp = make_uint2(~0u, ~0u);
+                if (edge[m]) kp = act[m] ? keep(p_first, p_last) : make_uint2(0u, 0u);
                 bool apart = false;
-                if (MULTI && KIND != kWinInt8 && edge && p_first != p_last) {
+                if (MULTI && KIND != kWinInt8 && edge[m] && act[m] && p_first != p_last) {
                     // some key is seen by some rows only: is any V value Inf or NaN?
 #pragma unroll
                     for (int i = 0; i < C::kPanels * kPairs; ++i) {
                         uint32_t w[4];
-                        ldsm_t(w, (k_at + slot_off + (i / kPairs) * panel_bytes) ^ ((i % kPairs) << 5));
+                        ldsm_t(w, (k_at + slot * C::kSlot + m * 16 * C::kLine + (i / kPairs) * kPanel) ^
+                                      ((i % kPairs) << 5));
                         apart |= non_finite<KIND>(w[0] & kp.x) || non_finite<KIND>(w[1] & kp.y) ||
                                  non_finite<KIND>(w[2] & kp.x) || non_finite<KIND>(w[3] & kp.y);
                     }
@@ -698,8 +692,11 @@ __global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(co
                     for (int mb2 = 0; mb2 < C::kSteps / 2; ++mb2) {
                         uint32_t av[2][4];
                         load_v(mb2, kp, av);
-                        mma<KIND>(o[2 * mb2], av[0], pb[0], pb[1]);
-                        mma<KIND>(o[2 * mb2 + 1], av[1], pb[0], pb[1]);
+#pragma unroll
+                        for (int hb = 0; hb < NHB; ++hb) {
+                            mma<KIND>(o[hb][2 * mb2], av[0], pb[hb][0], pb[hb][1]);
+                            mma<KIND>(o[hb][2 * mb2 + 1], av[1], pb[hb][0], pb[hb][1]);
+                        }
                     }
                 } else {
                     for (int p = p_first; p <= p_last; ++p) {  // one query position at a time
@@ -709,137 +706,159 @@ __global__ void __launch_bounds__(32 * (8 * RS + 1), ctas(RS)) gqa_win_kernel(co
                             uint32_t av[2][4];
                             load_v(mb2, k1, av);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma<KIND>(d, av[e], pb[0], pb[1]);
+                            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    if (qpos[y & 1] == p) o[2 * mb2 + e][y] += d[y];
-                            }
+                                for (int hb = 0; hb < NHB; ++hb) {
+                                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma<KIND>(s, av[e], pb[hb][0], pb[hb][1]);
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        const int R = min(row0 + hb * 8 + 2 * c + (y & 1), a.rows - 1);
+                                        if (n - a.q_len + R / a.grp == p) o[hb][2 * mb2 + e][y] += s[y];
+                                    }
+                                }
                         }
                     }
                 }
             }
-            release();
         }
+        refill();
+        if (!(d.z & kLast)) continue;
 
-        // ---- the rows' sums over the warp's lanes, then over its subtiles;
-        // references become -inf where there is none
+        // ---- the rows' sums over the warp's lanes, then over the warps of
+        // the head; references become -inf where there is none
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float l = l_part[e];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            l_part[e] = l;
-            if (m_thr[e] == -INFINITY) m_ref[e] = -INFINITY;
-            if (KIND == kWinBf16)
-                r_ref[e] = m_ref[e];
-            else if (r_thr[e] == -INFINITY)
-                r_ref[e] = -INFINITY;
-        }
+        for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = l_part[hb][e];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                l_part[hb][e] = l;
+                if (KIND == kWinBf16) r_ref[hb][e] = m_ref[hb][e];
+                if (m_ref[hb][e] == kNone) m_ref[hb][e] = -INFINITY;
+                if (r_ref[hb][e] == kNone) r_ref[hb][e] = -INFINITY;
+            }
         if (TS > 1) {
-            constexpr int kPerLane = C::kSteps * 4 + 6;
-            float* exch = reinterpret_cast<float*>(smem + lay.exch);
             for (int half = TS / 2; half >= 1; half >>= 1) {
-                float* buf = exch + ((rs * (TS / 2) + (sub & (half - 1))) * Hkv + kh) * kPerLane * 32 + lane;
-                float* tail = buf + C::kSteps * 4 * 32;
-                if (sub >= half && sub < 2 * half) {
+                // warp sub + half hands its state to warp sub, 16 values of a
+                // row group at a time
+                float* buf = reinterpret_cast<float*>(smem + lay.exch) +
+                             ((sub & (half - 1)) * Hkv + kh) * (C::kExch / 4) + lane;
+                float* tail = buf + 16 * 32;
+                const bool gives = sub >= half && sub < 2 * half, takes = sub < half;
+                float f0[NHB][2], f1[NHB][2];
 #pragma unroll
-                    for (int mb = 0; mb < C::kSteps; ++mb)
+                for (int part = 0; part < NHB * C::kSteps / 4; ++part) {
+                    const int hb = part / (C::kSteps / 4), m0 = part % (C::kSteps / 4) * 4;
+                    if (gives) {
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) buf[(mb * 4 + y) * 32] = o[mb][y];
+                        for (int y = 0; y < 16; ++y) buf[y * 32] = o[hb][m0 + y / 4][y % 4];
+                        if (part == 0)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        tail[e * 96] = m_ref[e];
-                        tail[e * 96 + 32] = r_ref[e];
-                        tail[e * 96 + 64] = l_part[e];
+                            for (int y = 0; y < 2 * NHB; ++y) {
+                                tail[y * 96] = m_ref[y / 2][y % 2];
+                                tail[y * 96 + 32] = r_ref[y / 2][y % 2];
+                                tail[y * 96 + 64] = l_part[y / 2][y % 2];
+                            }
                     }
-                }
-                named_bar_sync(1, 32 * NC);
-                if (sub < half) {
-                    float f0[2], f1[2];
+                    named_bar_sync(1, 32 * NC);
+                    if (takes) {
+                        if (part == 0)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float m1 = tail[e * 96], r1 = tail[e * 96 + 32], l1 = tail[e * 96 + 64];
-                        const float m = fmaxf(m_ref[e], m1), r = fmaxf(r_ref[e], r1);
-                        const float mu = m == -INFINITY ? 0.f : m, ru = r == -INFINITY ? 0.f : r;
-                        l_part[e] = l_part[e] * ex2(m_ref[e] - mu) + l1 * ex2(m1 - mu);
-                        f0[e] = ex2(r_ref[e] - ru);
-                        f1[e] = ex2(r1 - ru);
-                        m_ref[e] = m;
-                        r_ref[e] = r;
+                            for (int y = 0; y < 2 * NHB; ++y) {
+                                const int h = y / 2, e = y % 2;
+                                const float m1 = tail[y * 96], r1 = tail[y * 96 + 32], l1 = tail[y * 96 + 64];
+                                const float m = fmaxf(m_ref[h][e], m1), r = fmaxf(r_ref[h][e], r1);
+                                const float mu = m == -INFINITY ? 0.f : m, ru = r == -INFINITY ? 0.f : r;
+                                l_part[h][e] = l_part[h][e] * ex2(m_ref[h][e] - mu) + l1 * ex2(m1 - mu);
+                                f0[h][e] = ex2(r_ref[h][e] - ru);
+                                f1[h][e] = ex2(r1 - ru);
+                                m_ref[h][e] = m;
+                                r_ref[h][e] = r;
+                            }
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            o[hb][m0 + y / 4][y % 4] =
+                                o[hb][m0 + y / 4][y % 4] * f0[hb][y & 1] + buf[y * 32] * f1[hb][y & 1];
                     }
-#pragma unroll
-                    for (int mb = 0; mb < C::kSteps; ++mb)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            o[mb][y] = o[mb][y] * f0[y & 1] + buf[(mb * 4 + y) * 32] * f1[y & 1];
+                    named_bar_sync(1, 32 * NC);
                 }
-                named_bar_sync(1, 32 * NC);
             }
             if (sub > 0) continue;
         }
         if (aborted) continue;
 
-        // ---- epilogue: rows 2c + e; head dims by kind (see the top)
-        const int vslot = static_cast<int>(blockIdx.x) + pc.cur;
+        // ---- epilogue: rows hb * 8 + 2c + e; head dims by kind (see the top)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int jr = rs * 8 + 2 * c + e, R = rblk * 16 + jr;
-            if (jr >= a.rbn || R >= a.rows) continue;
-            const float l = l_part[e];
-            // l == 0: no visible key (a NaN sum goes through to the output)
-            float f = 0.f;
-            if (l != 0.f) f = a.out_scale * (r_ref[e] == -INFINITY ? 0.f : ex2(r_ref[e] - m_ref[e])) / l;
-            const float lse = l != 0.f ? (m_ref[e] + log2f(l)) * kLn2 : -INFINITY;
-            if (pc.whole) {
-                const int i = MULTI ? R / a.grp : 0;
-                const long long orow =
-                    (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
-                __nv_bfloat16* op = a.out + orow * D;
+        for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
-                for (int mb = 0; mb < C::kSteps; ++mb) {
-                    if constexpr (KIND == kWinBf16) {
-                        op[mb * 16 + g] = __float2bfloat16_rn(o[mb][e] * f);
-                        op[mb * 16 + g + 8] = __float2bfloat16_rn(o[mb][2 + e] * f);
-                    } else {
-                        *reinterpret_cast<uint32_t*>(op + mb * 16 + 2 * g) = pack_bf16x2(o[mb][e] * f, o[mb][2 + e] * f);
+            for (int e = 0; e < 2; ++e) {
+                const int jr = hb * 8 + 2 * c + e, R = row0 + jr;
+                if (jr >= a.rbn || R >= a.rows) continue;
+                const float l = l_part[hb][e];
+                // l == 0: no visible key (a NaN sum goes through to the output)
+                float f = 0.f;
+                if (l != 0.f)
+                    f = a.out_scale * (r_ref[hb][e] == -INFINITY ? 0.f : ex2(r_ref[hb][e] - m_ref[hb][e])) / l;
+                const float lse = l != 0.f ? (m_ref[hb][e] + log2f(l)) * kLn2 : -INFINITY;
+                if (d.z & kWhole) {
+                    const int i = MULTI ? R / a.grp : 0;
+                    const long long orow =
+                        (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
+                    __nv_bfloat16* op = a.out + orow * D;
+#pragma unroll
+                    for (int mb = 0; mb < C::kSteps; ++mb) {
+                        if constexpr (KIND == kWinBf16) {
+                            op[mb * 16 + g] = __float2bfloat16_rn(o[hb][mb][e] * f);
+                            op[mb * 16 + g + 8] = __float2bfloat16_rn(o[hb][mb][2 + e] * f);
+                        } else {
+                            *reinterpret_cast<uint32_t*>(op + mb * 16 + 2 * g) =
+                                pack_bf16x2(o[hb][mb][e] * f, o[hb][mb][2 + e] * f);
+                        }
                     }
-                }
-                if (a.lse && g == 0) a.lse[orow] = lse;
-            } else {
-                const long long prow = (static_cast<long long>(vslot) * Hkv + kh) * a.rbn + jr;
-                float* op = a.ws_o + prow * D;
+                    if (a.lse && g == 0) a.lse[orow] = lse;
+                } else {
+                    const long long prow =
+                        (static_cast<long long>(static_cast<int>(blockIdx.x) + v) * Hkv + kh) * a.rbn + jr;
+                    float* op = a.ws_o + prow * D;
 #pragma unroll
-                for (int mb = 0; mb < C::kSteps; ++mb) {
-                    if constexpr (KIND == kWinBf16) {
-                        op[mb * 16 + g] = o[mb][e] * f;
-                        op[mb * 16 + g + 8] = o[mb][2 + e] * f;
-                    } else {
-                        *reinterpret_cast<float2*>(op + mb * 16 + 2 * g) = make_float2(o[mb][e] * f, o[mb][2 + e] * f);
+                    for (int mb = 0; mb < C::kSteps; ++mb) {
+                        if constexpr (KIND == kWinBf16) {
+                            op[mb * 16 + g] = o[hb][mb][e] * f;
+                            op[mb * 16 + g + 8] = o[hb][mb][2 + e] * f;
+                        } else {
+                            *reinterpret_cast<float2*>(op + mb * 16 + 2 * g) =
+                                make_float2(o[hb][mb][e] * f, o[hb][mb][2 + e] * f);
+                        }
                     }
+                    if (g == 0) a.ws_lse[prow] = lse;
                 }
-                if (g == 0) a.ws_lse[prow] = lse;
             }
-        }
     }
+    // a warp that gave up lets its copies in flight land before it ends
+    // (bounded like every wait; a landed fill's phase answers at once)
+    if (aborted)
+        for (int s = 0; s < nslots && s < copied; ++s) {
+            const int fills = (copied - s + nslots - 1) / nslots;
+            mbar_wait(&full[s], (fills - 1) & 1);
+        }
 }
 
-template <int D, int KIND, int RS>
+template <int D, int KIND, int NHB>
 cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     const int vb = a.batch * a.rb;
-    // dynamic shared memory of one block: 227 KB, or its share of the SM's 228 KB
-    const int limit = ctas(RS) == 1 ? 227 * 1024 : 228 * 1024 / ctas(RS) - 1024;
+    constexpr int limit = 228 * 1024 / kWinCtasPerSm - 1024;  // a block's share of the SM's shared memory
     int ns = kMaxSlots;
-    while (ns > 2 && layout<D, KIND>(a.Hkv, a.ts, RS, ns, vb, a.batch).total > limit) --ns;
+    while (ns > 2 && layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total > limit) --ns;
     a.nslots = ns;
-    const int bytes = layout<D, KIND>(a.Hkv, a.ts, RS, ns, vb, a.batch).total;
-    auto kern = a.q_len > 1 ? gqa_win_kernel<D, KIND, RS, true> : gqa_win_kernel<D, KIND, RS, false>;
+    const int bytes = layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total;
+    auto kern = a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true> : gqa_win_kernel<D, KIND, NHB, false>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e != cudaSuccess)
         return e;
-    return launch_with_pdl(kern, dim3(grid), dim3(32 * (a.Hkv * a.ts * RS + 1)), bytes, stream, a);
+    return launch_with_pdl(kern, dim3(grid), dim3(32 * a.Hkv * a.ts), bytes, stream, a);
 }
 
 template <int KIND>

@@ -6,8 +6,8 @@
 // values.  One warp per row where a row has few partials, a block of 8 warps
 // per row (each takes every eighth partial, then a sum through shared memory)
 // where few rows are cut into many; the host picks by the mean number of
-// partials.  Launched as a programmatic dependent of stage 1: the prefix of
-// tile counts, which needs the lengths only, is computed before the wait.
+// partials.  Stage 1 left each request's first and last unit in the
+// workspace; a request of one unit was written by it and is skipped.
 #include "gqa_win.cuh"
 
 namespace mqa {
@@ -27,56 +27,22 @@ struct Vec<2> {
     using T = float2;
 };
 
-// Sum of x over the block (all threads get it); `buf` holds kWarps ints.
-__device__ __forceinline__ int block_sum(int x, int* buf) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += buf[i];
-    return s;
-}
-
 // WPR: warps per row (1 or kWarps).
 template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_constant__ WinArgs a) {
     constexpr int V = D / 32;
     using VecT = typename Vec<V>::T;
-    __shared__ int sums[kWarps];
     __shared__ float part[WPR == 1 ? 1 : kWarps][D + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v = blockIdx.x;
-    const int vb = a.batch * a.rb;
-
-    int before = 0, total = 0, mine = 0;
-    for (int i = threadIdx.x; i < vb; i += blockDim.x) {
-        const int b = a.rb == 1 ? i : i / a.rb;
-        const int nt = win_visible(a, i - b * a.rb, win_len(a, b, nullptr)).nt;
-        total += nt;
-        if (i < v) before += nt;
-        if (i == v) mine = nt;
-    }
-    total = block_sum(total, sums);
-    before = block_sum(before, sums);
-    mine = block_sum(mine, sums);
-
     const int b = v / a.rb, r = v - b * a.rb;
     const int item = WPR == 1 ? static_cast<int>(blockIdx.y) * kWarps + warp : static_cast<int>(blockIdx.y);
     const int kh = item / a.rbn, jr = item - kh * a.rbn;
     const int R = r * 16 + jr;
-    const bool row = kh < a.Hkv && R < a.rows;
-    int gf = 0, np = 0;
-    if (mine > 0) {
-        // the units that hold the first and the last of this request's tiles
-        const long long U = win_units(a.units, total);
-        gf = static_cast<int>((static_cast<long long>(before + 1) * U - 1) / total);
-        np = static_cast<int>((static_cast<long long>(before + mine) * U - 1) / total) - gf + 1;
-    }
     pdl_wait();  // stage 1 is done (every warp waits, so that this grid ends after it)
-    if (!row || np == 1) return;  // np == 1: stage 1 wrote the output itself
+    const int2 units = a.ws_units[v];
+    const int gf = units.x, np = units.y - units.x + 1;
+    if (np == 1 || kh >= a.Hkv || R >= a.rows) return;
     const int i = R / a.grp;
     const long long orow = (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
     __nv_bfloat16* out = a.out + orow * D + V * lane;
@@ -148,7 +114,4 @@ cudaError_t win_merge(const WinArgs& a, int D, cudaStream_t stream) {
     if (D == 128) return many ? launch<128, kWarps>(a, stream) : launch<128, 1>(a, stream);
     return many ? launch<64, kWarps>(a, stream) : launch<64, 1>(a, stream);
 }
-
-int win_ctas_per_sm(int rbn) { return rbn <= 8 ? 2 : 1; }
-
 }  // namespace mqa

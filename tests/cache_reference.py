@@ -16,14 +16,12 @@ Q_MAX = {"fp8_e4m3_block": 448.0, "int8_block": 127.0, "fp8_e4m3_pth": 448.0, "i
 
 # ------------------------------------------------------------------ decode
 
-def window_decode(q, k, v, n, scale, window, sinks, *, code_v=None, s_v=None, half_p=False, e4m3_q=False):
+def window_decode(q, k, v, n, scale, window, sinks, *, code_v=None, s_v=None, half_p=False):
     """One request.  q [L, Hq, D], k and v [n, Hkv, D] (float64, values); code_v, s_v: V as codes and per-token
     scales where it is held in 8 bits.  Returns out [L, Hq, D], lse [L, Hq] and their error bounds.
 
     The bounds: the logits are fp32 sums of exact products, off by ex = 2^-21 sum|q k| scale (a sum of up to 128
-    terms in any order, twice over) + the query's rounding, 2^-25 per subnormal entry for bf16 -> f16 and at most
-    2^-21 of the row's largest entry per entry for two e4m3 terms (each entry, scaled so that the largest is in
-    [128, 256), is off by half the second term's subnormal step, 2^-10 / 16); the base-2
+    terms in any order, twice over) + the bf16 -> f16 conversion's 2^-25 per subnormal entry; the base-2
     exponentials and the sums over n keys and up to n partials add 2^-20 + n 2^-24; P is rounded to bf16 (2^-8) or
     f16 (2^-11, or 2^-25 of the largest weight where it is subnormal); the output to bf16 (2^-8)."""
     L, Hq, D = q.shape
@@ -49,8 +47,7 @@ def window_decode(q, k, v, n, scale, window, sinks, *, code_v=None, s_v=None, ha
             ex += 2 ** -20 + len(t) * 2 ** -24
             weight = (w @ vv.abs()) / total
             if half_p:
-                off = float(q[i, h].abs().max()) * 2 ** -21 if e4m3_q else 2 ** -25
-                ex += D * off * float(kk.abs().max()) * abs(scale)
+                ex += D * 2 ** -25 * float(kk.abs().max()) * abs(scale)
                 ws = w * s_v[t, h // grp] if s_v is not None else w
                 codes = code_v[t, h // grp] if code_v is not None else vv
                 extra = weight * 2 ** -11 + 2 ** -25 * float(ws.max()) * codes.abs().sum(0) / total

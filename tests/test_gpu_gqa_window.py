@@ -92,7 +92,7 @@ class Case:
             k, _, _ = self.values(b, 0)
             v, code, s = self.values(b, 1)
             yield b, ref.window_decode(self.q[b].double(), k, v, self.lens[b], self.scale, self.window, self.sinks,
-                                       code_v=code, s_v=s, half_p=self.kv != "bf16", e4m3_q=self.kv.startswith("fp8"))
+                                       code_v=code, s_v=s, half_p=self.kv != "bf16")
 
     def run(self, splits=None, dev=None, **kw):
         q, kv, bt, sc, sl = dev or self.dev()

@@ -18,7 +18,7 @@ def attend(q, cache, scales, bt, lens, page, window, sinks, D, kv):
         s = [ref.token_scales(scales, bt, b, n, page, i) if scales is not None
              else torch.ones(n, cache.shape[3], dtype=torch.float64) for i in (0, 1)]
         yield ref.window_decode(q[b].double(), codes[0] * s[0][..., None], codes[1] * s[1][..., None], n, D ** -0.5,
-                                window, sinks, code_v=codes[1], s_v=s[1], half_p=kv != "bf16", e4m3_q=kv.startswith("fp8"))
+                                window, sinks, code_v=codes[1], s_v=s[1], half_p=kv != "bf16")
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3_block", "int8_block"])
