@@ -199,6 +199,9 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
            (x & 0xff000000u) == 0x7f000000u;
 }
 
+// The rest of a wait that did not end at once.
+static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity); }
+
 // cum[0 .. vb]: exclusive prefix of the virtual requests' tile counts; lens:
 // clamped lengths.  Every thread of the block calls it; returns the total.
 __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* lens) {
@@ -234,6 +237,9 @@ __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* len
 // flags below, w the index of its first K scale.
 constexpr int kFirst = 1 << 16, kLast = 1 << 17, kWhole = 1 << 18;  // of the tile in the unit's run of its request
 constexpr int kNextScale = 1 << 19;  // the box's second 16 tokens have the next scale
+// of the tile's two 16-token blocks: holds a key that the rows see, and one
+// that some row does not see
+constexpr int kAct = 1 << 20, kEdge = 1 << 22;
 
 // MULTI: more than one query position per request.
 template <int D, int KIND, int NHB, bool MULTI>
@@ -325,31 +331,37 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         }
     };
     auto describe = [&](int i) {  // box i, whose id has been fetched
-        int4 d;
+        int4 d = make_int4(0, -1, 0, 0);
         if (i < boxes) {
             locate(i, d);
             if (next_id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
-            const int in_page = d.x % a.page;
+            const int v = d.z & 0xffff, b = d.y, in_page = d.x % a.page;
             d.y = next_id < 0 ? -1 : next_id * 2 * a.page + in_page;
             if (scaled) {
                 d.w = (next_id * 2 * a.scale_groups + in_page / a.scale_block) * Hkv + kh;
                 if ((in_page + 16) / a.scale_block != in_page / a.scale_block) d.z |= kNextScale;
             }
-            desc_s[i & (kDesc - 1)] = d;
+            const WinVis vis = win_visible(a, a.rb == 1 ? 0 : v - b * a.rb, lens[b]);
+            for (int m = 0; m < a.box_tok / 16; ++m) {
+                const int t = d.x + 16 * m, bit = nb == 1 ? m : i & 1;
+                const bool act = d.y >= 0 && t <= vis.p_last && (t + 15 > vis.p_first - a.window || t < a.sinks);
+                const bool edge = !act || t + 15 > vis.p_first || (t + 15 >= a.sinks && t <= vis.p_last - a.window);
+                d.z |= (act ? kAct << bit : 0) | (edge ? kEdge << bit : 0);
+            }
         }
+        if (nb == 2) d.z |= __shfl_xor_sync(0xffffffffu, d.z, 1) & (3 * kAct | 3 * kEdge);
+        if (i < boxes) desc_s[i & (kDesc - 1)] = d;
         __syncwarp();
     };
     const int loads = 2 * (p1 - p0);  // planes to copy: K, V, K, V ..
     int issued = 0, i_slot = 0;
-    // After a wait ran out (`copy` false) boxes are still described, so that
-    // the warp keeps meeting the others, but nothing is copied.
-    auto issue = [&](bool copy) {
+    auto issue = [&]() {
         const int first = (issued >> 1) * nb, plane = issued & 1;
         if (plane == 0 && (first & 31) == 0) {
             describe(first + lane);
             fetch_id(first + 32 + lane);
         }
-        if (lane < nb && copy) {
+        if (lane < nb) {
             const int4 d = desc_s[(first + lane) & (kDesc - 1)];
             constexpr int kBox16 = 16 * D * C::kElt;  // bytes of 16 tokens
             const int bytes = nb == 1 ? C::kSlot : kBox16;
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         if (++i_slot == nslots) i_slot = 0;
     };
     fetch_id(lane);
-    for (int s = 0; s < nslots && issued < loads; ++s) issue(true);
+    for (int s = 0; s < nslots && issued < loads; ++s) issue();
 
     // ---- reading
     const int g = lane >> 2, c = lane & 3;
@@ -398,16 +410,10 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 
     int slot = 0;
     uint32_t phase = 0;
-    bool aborted = false;
-    int copied = 0;  // fills issued when the warp gave up
-    // A wait that runs out is reported once; from then on the warp waits for
-    // nothing, copies and writes nothing, but still meets the other warps.
+    // False (for the whole warp) if the wait ran out.
     auto wait_full = [&]() {
-        if (aborted) return;
-        if (__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) return;
-        report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-        aborted = true;
-        copied = issued;
+        if (__all_sync(0xffffffffu, mbar_try_wait(&full[slot], phase))) return true;
+        return __all_sync(0xffffffffu, wait_long(&full[slot], phase)) != 0;
     };
     auto refill = [&]() {  // the slot has been read
         __syncwarp();
@@ -415,24 +421,31 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             slot = 0;
             phase ^= 1;
         }
-        if (issued < loads) issue(!aborted);
+        if (issued < loads) issue();
     };
 
+    constexpr int kParts = NHB * C::kSteps / 4;  // of a warp's hand-over to another
+    const int tiles = p1 - p0;
+    int tile = 0, n = 0;
     int p_first = 0, p_last = 0;  // positions of the row block's first and last row
+    int r_first = 0;              // rows of the first row's position before it
+    // position of row jr of the row block (rows behind the last have its position)
+    auto row_position = [&](int jr) { return MULTI ? min(p_first + (r_first + jr) / a.grp, p_last) : p_last; };
     uint32_t qb[NHB == 1 ? C::kSteps : 1][2];
     float o[NHB][C::kSteps][4];
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
 
-    for (int tile = 0; tile < p1 - p0; ++tile) {
+    for (; tile < tiles; ++tile) {
         if ((tile & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
         const int4 d = desc_s[(tile * nb) & (kDesc - 1)];
-        const int t0 = d.x, v = d.z & 0xffff;
-        const int b = a.rb == 1 ? v : v / a.rb;
-        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
-        const int n = lens[b];
+        const int t0 = d.x;
 
         if (d.z & kFirst) {
+            const int v = d.z & 0xffff, b = a.rb == 1 ? v : v / a.rb;
+            const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
+            n = lens[b];
             p_first = MULTI ? n - a.q_len + row0 / a.grp : n - 1;
+            r_first = MULTI ? row0 % a.grp : 0;
             p_last = MULTI ? n - a.q_len + (min(a.rows, row0 + 16) - 1) / a.grp : n - 1;
             if (a.units > 0 && threadIdx.x == 0) {
                 // every request's first and last unit, for the merge
@@ -490,19 +503,10 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             }
         }
 
-        // which of the tile's 16-token blocks hold a key for the warp's rows
-        bool act[MT];
-        bool any = false;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int t = t0 + 16 * m;
-            const int id = MT == 1 || nb == 1 || m == 0 ? d.y : desc_s[(tile * 2 + 1) & (kDesc - 1)].y;
-            act[m] = id >= 0 && t <= p_last && (t + 15 > p_first - a.window || t < a.sinks);
-            any |= act[m];
-        }
+        const bool any = d.z & (3 * kAct);
         float x[MT][NHB][4];  // logits of token g (rows 2c, 2c + 1) and of token g + 8
-        wait_full();
-        if (any && !aborted) {
+        if (!wait_full()) break;
+        if (any) {
             const uint32_t kb = k_at + slot * C::kSlot;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -546,39 +550,58 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             }
         }
         refill();
-        wait_full();
-        if (any && !aborted) {
+        if (!wait_full()) break;
+        if (any) {
             float lvs[MT];
-            bool edge[MT];  // at the edge of what the rows see: mask key by key
-            bool grow = false;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int t = t0 + 16 * m;
-                lvs[m] = scaled ? __log2f(scale_s[slot * 2 + m]) : 0.f;
-                edge[m] = !act[m] || t + 15 > p_first || (t + 15 >= a.sinks && t <= p_last - a.window);
-                if (edge[m]) {
+            for (int m = 0; m < MT; ++m) lvs[m] = scaled ? __log2f(scale_s[slot * 2 + m]) : 0.f;
+            if (d.z & (3 * kEdge)) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (!(d.z & (kEdge << m))) continue;
+                    const bool act = d.z & (kAct << m);
+                    const int t = t0 + 16 * m;
+                    if (!act) lvs[m] = 0.f;
 #pragma unroll
                     for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = t + g + (e >> 1) * 8;
-                            const int R = min(row0 + hb * 8 + 2 * c + (e & 1), a.rows - 1);
-                            const int p = MULTI ? n - a.q_len + R / a.grp : n - 1;
-                            if (!act[m] || !(key <= p && (key < a.sinks || key > p - a.window)))
+                        for (int e = 0; e < 4; ++e) {  // mask key by key
+                            const int key = t + g + (e >> 1) * 8, p = row_position(hb * 8 + 2 * c + (e & 1));
+                            if (!act || !(key <= p && (key < a.sinks || key > p - a.window)))
                                 x[m][hb][e] = -INFINITY;
                         }
-                    if (!act[m]) lvs[m] = 0.f;
+                    if (KIND != kWinInt8) {
+                        // V rows that no row sees become zeros: whatever bytes
+                        // they hold (int8 codes are finite anyway)
+                        for (int r = 0; r < 16; ++r) {
+                            const int key = t + r;
+                            if (act && key <= p_last && (key < a.sinks || key > p_first - a.window)) continue;
+#pragma unroll
+                            for (int q = 0; q < C::kPanels; ++q)
+                                if (4 * lane < C::kLine)
+                                    st_shared(ring + slot * C::kSlot + q * kPanel + (16 * m + r) * C::kLine + 4 * lane,
+                                              0u);
+                        }
+                    }
                 }
+                if (KIND != kWinInt8) {
+                    fence_proxy_async_smem();  // before the slot's next copy
+                    __syncwarp();
+                }
+            }
+            // the largest excess over a reference, in base-2 exponents
+            float over = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float mx = fmaxf(x[m][hb][e], x[m][hb][2 + e]);
-                        grow |= mx > m_ref[hb][e] + 8.f;
-                        if (KIND != kWinBf16) grow |= mx + lvs[m] > r_ref[hb][e] + 8.f;
+                        over = fmaxf(over, mx - m_ref[hb][e]);
+                        if (KIND != kWinBf16) over = fmaxf(over, mx + (lvs[m] - r_ref[hb][e]));
                     }
-            }
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__any_sync(0xffffffffu, over > 8.f)) {
 #pragma unroll
                 for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
@@ -636,31 +659,26 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                     }
                 }
                 const uint32_t vb_at = v_at + slot * C::kSlot + m * 16 * C::kLine;
-                // V words of tokens 2c, 2c + 1 (x) and + 8 (y): bits kept
-                auto keep = [&](int p_min, int p_max) {
-                    auto seen = [&](int key) { return key <= p_max && (key < a.sinks || key > p_min - a.window); };
-                    const int key = t + 2 * c;
-                    return make_uint2((seen(key) ? 0xffffu : 0u) | (seen(key + 1) ? 0xffff0000u : 0u),
-                                      (seen(key + 8) ? 0xffffu : 0u) | (seen(key + 9) ? 0xffff0000u : 0u));
-                };
                 // operand A of head dims 16 mb ..: rows g and g + 8
-                auto load_v = [&](int mb2, uint2 k, uint32_t (&av)[2][4]) {  // blocks 2 mb2, 2 mb2 + 1
+                auto load_v = [&](int mb2, uint32_t (&av)[2][4], bool masked, uint2 k) {  // blocks 2 mb2, 2 mb2 + 1
                     if constexpr (KIND == kWinBf16) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int i = 2 * mb2 + e;
                             ldsm_t(av[e], (vb_at + (i / kPairs) * kPanel) ^ ((i % kPairs) << 5));
-                            av[e][0] &= k.x;
-                            av[e][1] &= k.x;
-                            av[e][2] &= k.y;
-                            av[e][3] &= k.y;
+                            if (masked) {
+                                av[e][0] &= k.x;
+                                av[e][1] &= k.x;
+                                av[e][2] &= k.y;
+                                av[e][3] &= k.y;
+                            }
                         }
                     } else {
                         uint32_t w[4];
                         ldsm_t(w, vb_at ^ (mb2 << 5));
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            if constexpr (KIND == kWinE4m3) {
+                            if (masked) {
                                 w[2 * e] &= k.x;
                                 w[2 * e + 1] &= k.y;
                             }
@@ -672,18 +690,16 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                         }
                     }
                 };
-                uint2 kp = make_uint2(~0u, ~0u);
-                if (edge[m]) kp = act[m] ? keep(p_first, p_last) : make_uint2(0u, 0u);
                 bool apart = false;
-                if (MULTI && KIND != kWinInt8 && edge[m] && act[m] && p_first != p_last) {
+                if (MULTI && KIND != kWinInt8 && (d.z & (kEdge << m)) && p_first != p_last) {
                     // some key is seen by some rows only: is any V value Inf or NaN?
 #pragma unroll
                     for (int i = 0; i < C::kPanels * kPairs; ++i) {
                         uint32_t w[4];
                         ldsm_t(w, (k_at + slot * C::kSlot + m * 16 * C::kLine + (i / kPairs) * kPanel) ^
                                       ((i % kPairs) << 5));
-                        apart |= non_finite<KIND>(w[0] & kp.x) || non_finite<KIND>(w[1] & kp.y) ||
-                                 non_finite<KIND>(w[2] & kp.x) || non_finite<KIND>(w[3] & kp.y);
+                        apart |= non_finite<KIND>(w[0]) || non_finite<KIND>(w[1]) || non_finite<KIND>(w[2]) ||
+                                 non_finite<KIND>(w[3]);
                     }
                     apart = __any_sync(0xffffffffu, apart);
                 }
@@ -691,7 +707,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 #pragma unroll
                     for (int mb2 = 0; mb2 < C::kSteps / 2; ++mb2) {
                         uint32_t av[2][4];
-                        load_v(mb2, kp, av);
+                        load_v(mb2, av, false, make_uint2(0u, 0u));
 #pragma unroll
                         for (int hb = 0; hb < NHB; ++hb) {
                             mma<KIND>(o[hb][2 * mb2], av[0], pb[hb][0], pb[hb][1]);
@@ -700,11 +716,15 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                     }
                 } else {
                     for (int p = p_first; p <= p_last; ++p) {  // one query position at a time
-                        const uint2 k1 = keep(p, p);
+                        auto seen = [&](int key) { return key <= p && (key < a.sinks || key > p - a.window); };
+                        const int key = t + 2 * c;  // V words hold tokens 2c, 2c + 1 (and + 8)
+                        const uint2 k = make_uint2(
+                            (seen(key) ? 0xffffu : 0u) | (seen(key + 1) ? 0xffff0000u : 0u),
+                            (seen(key + 8) ? 0xffffu : 0u) | (seen(key + 9) ? 0xffff0000u : 0u));
 #pragma unroll
                         for (int mb2 = 0; mb2 < C::kSteps / 2; ++mb2) {
                             uint32_t av[2][4];
-                            load_v(mb2, k1, av);
+                            load_v(mb2, av, true, k);
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -712,10 +732,9 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                                     float s[4] = {0.f, 0.f, 0.f, 0.f};
                                     mma<KIND>(s, av[e], pb[hb][0], pb[hb][1]);
 #pragma unroll
-                                    for (int y = 0; y < 4; ++y) {
-                                        const int R = min(row0 + hb * 8 + 2 * c + (y & 1), a.rows - 1);
-                                        if (n - a.q_len + R / a.grp == p) o[hb][2 * mb2 + e][y] += s[y];
-                                    }
+                                    for (int y = 0; y < 4; ++y)
+                                        if (row_position(hb * 8 + 2 * c + (y & 1)) == p)
+                                            o[hb][2 * mb2 + e][y] += s[y];
                                 }
                         }
                     }
@@ -750,7 +769,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                 const bool gives = sub >= half && sub < 2 * half, takes = sub < half;
                 float f0[NHB][2], f1[NHB][2];
 #pragma unroll
-                for (int part = 0; part < NHB * C::kSteps / 4; ++part) {
+                for (int part = 0; part < kParts; ++part) {
                     const int hb = part / (C::kSteps / 4), m0 = part % (C::kSteps / 4) * 4;
                     if (gives) {
 #pragma unroll
@@ -788,9 +807,10 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             }
             if (sub > 0) continue;
         }
-        if (aborted) continue;
 
         // ---- epilogue: rows hb * 8 + 2c + e; head dims by kind (see the top)
+        const int v = d.z & 0xffff, b = a.rb == 1 ? v : v / a.rb;
+        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
 #pragma unroll
         for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
@@ -837,13 +857,24 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                 }
             }
     }
-    // a warp that gave up lets its copies in flight land before it ends
-    // (bounded like every wait; a landed fill's phase answers at once)
-    if (aborted)
-        for (int s = 0; s < nslots && s < copied; ++s) {
-            const int fills = (copied - s + nslots - 1) / nslots;
+    if (tile < tiles) {
+        // A wait ran out: report it, meet the other warps wherever they
+        // expect it, write nothing more, and let the copies in flight land
+        // (bounded like every wait; a landed fill's phase answers at once).
+        report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+        for (int t = tile; t < tiles; ++t) {
+            if (t > tile && (t & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
+            int4 d;
+            locate(t * nb, d);
+            if (d.z & kLast)
+                for (int half = TS / 2; half >= 1; half >>= 1)
+                    for (int part = 0; part < 2 * kParts; ++part) named_bar_sync(1, 32 * NC);
+        }
+        for (int s = 0; s < nslots && s < issued; ++s) {
+            const int fills = (issued - s + nslots - 1) / nslots;
             mbar_wait(&full[s], (fills - 1) & 1);
         }
+    }
 }
 
 template <int D, int KIND, int NHB>
