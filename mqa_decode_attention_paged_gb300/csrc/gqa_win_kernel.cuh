@@ -122,19 +122,22 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// d = a b + d, or a b if `first`, on 16-bit operands (bf16, else f16).  No
+// memory is touched: the compiler may schedule it freely.
 template <int KIND>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                    bool first = false) {
+    const float c0 = first ? 0.f : d[0], c1 = first ? 0.f : d[1], c2 = first ? 0.f : d[2], c3 = first ? 0.f : d[3];
     if constexpr (KIND == kWinBf16)
-        mma_bf16_16816(d, a, b0, b1);
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
-        mma_f16(d, a, b0, b1);
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // Transpose of an 8x8 matrix of 16-bit values in the MMA fragment layout.
@@ -508,45 +511,52 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         if (!wait_full()) break;
         if (any) {
             const uint32_t kb = k_at + slot * C::kSlot;
+            // one chain of MMAs per (block, row group); two where there is one
+            constexpr int kChains = MT * NHB == 1 ? 2 : 1;
+            constexpr int kE = KIND == kWinBf16 ? 1 : 2;  // 16-wide steps of a chunk pair
+            float st[kChains][MT][NHB][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float st[NHB][2][4];
+            for (int i = 0; i < C::kPanels * kPairs; ++i) {
+                uint32_t w[MT][4];
 #pragma unroll
-                for (int hb = 0; hb < NHB; ++hb)
+                for (int m = 0; m < MT; ++m)
+                    ldsm(w[m], (kb + (i / kPairs) * kPanel + m * 16 * C::kLine) ^ ((i % kPairs) << 5));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) st[hb][e][0] = st[hb][e][1] = st[hb][e][2] = st[hb][e][3] = 0.f;
+                for (int e = 0; e < kE; ++e) {
+                    const int ks = kE * i + e;
+                    uint32_t q1[4];
+                    if constexpr (NHB == 1) {
+                        q1[0] = qb[ks][0];
+                        q1[1] = qb[ks][1];
+                    } else {
+                        ldsm(q1, q_at ^ (ks << 5));
+                    }
 #pragma unroll
-                for (int i = 0; i < C::kPanels * kPairs; ++i) {
-                    uint32_t w[4];
-                    ldsm(w, (kb + (i / kPairs) * kPanel + m * 16 * C::kLine) ^ ((i % kPairs) << 5));
-                    constexpr int kE = KIND == kWinBf16 ? 1 : 2;  // 16-wide steps
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) {
-                        const int ks = kE * i + e;
-                        uint32_t af[4] = {w[0], w[1], w[2], w[3]};
+                    for (int m = 0; m < MT; ++m) {
+                        uint32_t af[4] = {w[m][0], w[m][1], w[m][2], w[m][3]};
                         if constexpr (KIND != kWinBf16) {
-                            const uint2 k0 = widen_adjacent<KIND>(w[2 * e]), k1 = widen_adjacent<KIND>(w[2 * e + 1]);
+                            const uint2 k0 = widen_adjacent<KIND>(w[m][2 * e]);
+                            const uint2 k1 = widen_adjacent<KIND>(w[m][2 * e + 1]);
                             af[0] = k0.x;
                             af[1] = k1.x;
                             af[2] = k0.y;
                             af[3] = k1.y;
                         }
-                        if constexpr (NHB == 1) {
-                            mma<KIND>(st[0][ks & 1], af, qb[ks][0], qb[ks][1]);
-                        } else {
-                            uint32_t q1[4];
-                            ldsm(q1, q_at ^ (ks << 5));
 #pragma unroll
-                            for (int hb = 0; hb < NHB; ++hb)
-                                mma<KIND>(st[hb][ks & 1], af, q1[2 * hb], q1[2 * hb + 1]);
-                        }
+                        for (int hb = 0; hb < NHB; ++hb)
+                            mma<KIND>(st[ks % kChains][m][hb], af, q1[2 * hb], q1[2 * hb + 1], ks < kChains);
                     }
                 }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
                 const float ksc = scaled ? a.sl2 * scale_s[slot * 2 + m] : a.sl2;
 #pragma unroll
                 for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[m][hb][e] = (st[hb][0][e] + st[hb][1][e]) * ksc;
+                    for (int e = 0; e < 4; ++e)
+                        x[m][hb][e] =
+                            (kChains == 1 ? st[0][m][hb][e] : st[0][m][hb][e] + st[kChains - 1][m][hb][e]) * ksc;
             }
         }
         refill();
@@ -729,8 +739,8 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
                                 for (int hb = 0; hb < NHB; ++hb) {
-                                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma<KIND>(s, av[e], pb[hb][0], pb[hb][1]);
+                                    float s[4];
+                                    mma<KIND>(s, av[e], pb[hb][0], pb[hb][1], true);
 #pragma unroll
                                     for (int y = 0; y < 4; ++y)
                                         if (row_position(hb * 8 + 2 * c + (y & 1)) == p)
