@@ -502,6 +502,9 @@ def gqa_window_num_kv_splits(batch: int, q_len: int, num_q_heads: int, num_kv_he
     return n
 
 
+_PTH_CODES = (KV_FP8_E4M3_PER_TOKEN_HEAD, KV_INT8_PER_TOKEN_HEAD, KV_INT4_PER_TOKEN_HEAD)
+
+
 def _fits(t, dtype, shape, index):
     """Whether t is what _check and _on_device ask for, in one look (the calls below run once per layer and token)."""
     return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
@@ -658,7 +661,7 @@ def _check_rows(t, name, shape, dense):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st, want = t.stride(), 1
-    if st[-1] == 1 and min(shape) > 1 and (dense == 1 or st[-2] == shape[-1]):
+    if st[-1] == 1 and (dense == 1 or st[-2] == shape[-1]) and 1 not in shape and 0 not in shape:
         return st[:-dense]
     for i in range(1, dense + 1):
         if shape[-i] != 1 and st[-i] != want:
@@ -679,11 +682,14 @@ def _check_append(index, cos_sin, width, kv_cache, block_table, seq_lens, query_
     if (index >= 0 and len(bt_shape) == 2 and cos_sin.dim() == 2 and width in (None, cos_sin.shape[1])
             and _fits(cos_sin, torch.float32, cos_sin.shape, index) and kv_cache.is_contiguous()
             and kv_cache.get_device() == index and _fits(block_table, torch.int32, bt_shape, index)
-            and _fits(seq_lens, torch.int32, (bt_shape[0],), index)
+            and _fits(seq_lens, torch.int32, bt_shape[:1], index)
             and _fits(query_start, torch.int32, (bt_shape[0] + 1,), index)
-            and (device_status is None or _fits(device_status, torch.int32, device_status.shape, index))
-            and all(t is None or t.get_device() == index for _, t in named)):
-        return bt_shape[0]
+            and (device_status is None or _fits(device_status, torch.int32, device_status.shape, index))):
+        for _, t in named:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return bt_shape[0]
     _check(cos_sin, "cos_sin", (torch.float32,))
     if cos_sin.dim() != 2 or (width is not None and cos_sin.shape[1] != width):
         raise ValueError(f"cos_sin must be fp32 [max_position, {width or 'rotary_dim'}]")
@@ -716,8 +722,7 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
     T, Hkv, D = k.shape
     nb, two, page, Hkv2, row = kv_cache.shape
     code = _block_code(kv_cache, kv_scales, kv_dtype)
-    want = {KV_FP8_E4M3_PER_TOKEN_HEAD: D + 4, KV_INT8_PER_TOKEN_HEAD: D + 4,
-            KV_INT4_PER_TOKEN_HEAD: D // 2 + 4}.get(code, D)
+    want = D if code not in _PTH_CODES else D // 2 + 4 if code == KV_INT4_PER_TOKEN_HEAD else D + 4
     if two != 2 or Hkv2 != Hkv or row != want:
         raise ValueError(f"kv_cache must be [num_blocks, 2, page, {Hkv}, {want}]")
     if kv_cache.element_size() != (2 if code == KV_BF16 else 1):

@@ -2,6 +2,7 @@
 // See include/mqa_decode.h for the contract of every function.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -299,7 +300,20 @@ bool mla_tensor_map(CUtensorMap* out, const void* base, int cols, long long rows
 
 mqa_status mqa::api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
 PFN_cuTensorMapEncodeTiled_v12000 mqa::api_encode_tiled() { return encode_tiled_fn(); }
-int mqa::api_sm_count() { return sm_count_current(); }
+int mqa::api_sm_count() {
+    // a property of the device: looked up once for each
+    constexpr int kDevices = 64;
+    static std::atomic<int> count[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    if (dev < 0 || dev >= kDevices) return sm_count_current();
+    int n = count[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        n = sm_count_current();
+        if (n > 0) count[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 static mqa_status mla_decode_rows(const void* q, const void* kv_cache, const int32_t* block_table,
                       const int32_t* seq_lens, float scale, float k_scale, void* out, float* lse,

@@ -135,13 +135,16 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
         return e4m3_code(a) | e4m3_code(b) << 8 | e4m3_code(c) << 16 | e4m3_code(d) << 24;
     }
 }
-// The eight codes of y / s (s = 0: zeros).
+// The eight codes of y / s, given inv = 1 / s (0 where s = 0: zeros).  The
+// product is within 2^-23 of the quotient, relative: another code only where
+// the quotient is that near the border between two.
 template <bool INT8>
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float s) {
-    if (s == 0.f) return make_uint2(0u, 0u);
-    return make_uint2(codes4<INT8>(y[0] / s, y[1] / s, y[2] / s, y[3] / s),
-                      codes4<INT8>(y[4] / s, y[5] / s, y[6] / s, y[7] / s));
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+    if (inv == 0.f) return make_uint2(0u, 0u);  // (a product could be -0)
+    return make_uint2(codes4<INT8>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                      codes4<INT8>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
 }
+__device__ __forceinline__ float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
 
 __device__ __forceinline__ float amax16(const float (&y0)[8], const float (&y1)[8]) {
     float m = 0.f;
@@ -164,15 +167,15 @@ __device__ __host__ constexpr int row_bytes() {
 // call it.
 template <int D, int FMT>
 __device__ __forceinline__ void store_row(uint8_t* row, bool store, const float (&y0)[8], const float (&y1)[8],
-                                          int c0, int c1, int l, float tensor_scale) {
+                                          int c0, int c1, int l, float tensor_inv) {
     if constexpr (FMT == MQA_KV_BF16) {
         if (!store) return;
         *reinterpret_cast<uint4*>(row + 2 * c0) = pack8(y0);
         *reinterpret_cast<uint4*>(row + 2 * c1) = pack8(y1);
     } else if constexpr (FMT == MQA_KV_FP8_E4M3) {
         if (!store) return;
-        *reinterpret_cast<uint2*>(row + c0) = codes8<false>(y0, tensor_scale);
-        *reinterpret_cast<uint2*>(row + c1) = codes8<false>(y1, tensor_scale);
+        *reinterpret_cast<uint2*>(row + c0) = codes8<false>(y0, tensor_inv);
+        *reinterpret_cast<uint2*>(row + c1) = codes8<false>(y1, tensor_inv);
     } else {
         constexpr float top = FMT == MQA_KV_FP8_E4M3_PER_TOKEN_HEAD ? kE4m3Max
                               : FMT == MQA_KV_INT8_PER_TOKEN_HEAD   ? kInt8Max
@@ -183,12 +186,13 @@ __device__ __forceinline__ void store_row(uint8_t* row, bool store, const float 
         float s = m / top;
         if (s < kTinyScale) s = 0.f;
         if (!store) return;
+        const float inv = inverse(s);
         if constexpr (FMT == MQA_KV_INT4_PER_TOKEN_HEAD) {
             auto word = [&](const float (&y)[8]) {
                 uint32_t w = 0u;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    w |= (static_cast<uint32_t>(s == 0.f ? 0 : int_code(y[i] / s, kInt4Max)) & 0xfu) << (4 * i);
+                    w |= (static_cast<uint32_t>(int_code(y[i] * inv, kInt4Max)) & 0xfu) << (4 * i);
                 return w;
             };
             *reinterpret_cast<uint32_t*>(row + c0 / 2) = word(y0);
@@ -196,7 +200,7 @@ __device__ __forceinline__ void store_row(uint8_t* row, bool store, const float 
             if (l == 0) *reinterpret_cast<float*>(row + D / 2) = s;
         } else {
             constexpr bool int8 = FMT == MQA_KV_INT8_PER_TOKEN_HEAD;
-            const uint2 a = codes8<int8>(y0, s), b = codes8<int8>(y1, s);
+            const uint2 a = codes8<int8>(y0, inv), b = codes8<int8>(y1, inv);
             reinterpret_cast<uint32_t*>(row + c0)[0] = a.x;  // rows of D + 4 bytes: 4-byte alignment
             reinterpret_cast<uint32_t*>(row + c0)[1] = a.y;
             reinterpret_cast<uint32_t*>(row + c1)[0] = b.x;
@@ -265,7 +269,8 @@ __device__ __forceinline__ void append_rows(const GqaAppendArgs& a, int t, int r
             const int h = r - a.Hq;  // key rows, then value rows
             const bool v = h >= a.Hkv;
             uint8_t* row = cell + (static_cast<long long>(v) * a.t.page * a.Hkv + (v ? h - a.Hkv : h)) * row_bytes<D, FMT>();
-            store_row<D, FMT>(row, h >= 0 && r < rows && id >= 0, y0, y1, ch.c0, ch.c1, l, v ? a.v_scale : a.k_scale);
+            store_row<D, FMT>(row, h >= 0 && r < rows && id >= 0, y0, y1, ch.c0, ch.c1, l,
+                              FMT == MQA_KV_FP8_E4M3 ? 1.f / (v ? a.v_scale : a.k_scale) : 0.f);
         }
     }
 }
@@ -368,7 +373,7 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
         if (rot && i < m) rotate(y0, y1, an, a.t.interleaved);
     };
     float amax = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = rl; i - rl < m; i += RPI) {
         float y0[8], y1[8];
         values(i, y0, y1);
@@ -388,39 +393,40 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
                             rescale4<INT8>(w.w, ratio));
         }
     }
-#pragma unroll 2
+    const float inv = inverse(s_new);
+#pragma unroll 4
     for (int i = rl; i - rl < m; i += RPI) {
         float y0[8], y1[8];
         values(i, y0, y1);
         if (i >= m) continue;
         uint8_t* row = cell + (had + i) * row_step;
-        *reinterpret_cast<uint2*>(row + ch.c0) = codes8<INT8>(y0, s_new);
-        *reinterpret_cast<uint2*>(row + ch.c1) = codes8<INT8>(y1, s_new);
+        *reinterpret_cast<uint2*>(row + ch.c0) = codes8<INT8>(y0, inv);
+        *reinterpret_cast<uint2*>(row + ch.c1) = codes8<INT8>(y1, inv);
     }
     if (lane == 0) *sp = s_new;
 }
 
-// Warp tasks: [0, row_tasks) rows of tokens, then (block formats) blocks.
+// Warp tasks: (block formats) blocks, which take longest, then rows of tokens.
 template <int D, int FMT>
 __global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppendArgs a, const int groups,
                                                                  const long long row_tasks,
                                                                  const long long block_tasks) {
     const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
-    if (w < row_tasks) {
-        const int t = static_cast<int>(w / groups);
-        append_rows<D, FMT>(a, t, static_cast<int>(w - static_cast<long long>(t) * groups) * rows_per_warp<D>(), lane);
-        return;
-    }
     if constexpr (block_format<FMT>()) {
-        const long long k = w - row_tasks;
-        if (k >= block_tasks) return;
-        const long long task = k / (2 * a.Hkv);
-        const int ph = static_cast<int>(k - task * 2 * a.Hkv);
-        append_block<D, FMT>(a, task, ph / a.Hkv, ph % a.Hkv, lane);
+        if (w < block_tasks) {
+            const long long task = w / (2 * a.Hkv);
+            const int ph = static_cast<int>(w - task * 2 * a.Hkv);
+            append_block<D, FMT>(a, task, ph / a.Hkv, ph % a.Hkv, lane);
+            return;
+        }
+        w -= block_tasks;
     }
+    if (w >= row_tasks) return;
+    const int t = static_cast<int>(w / groups);
+    append_rows<D, FMT>(a, t, static_cast<int>(w - static_cast<long long>(t) * groups) * rows_per_warp<D>(), lane);
 }
 
 // MLA: a token's 64-column pieces: R / 64 of kv_c, k_pe, then H of q_pe (4
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(32 * kWarps) mla_append_kernel(const MlaAppend
             *reinterpret_cast<uint4*>(dst + ch.c1) = pack8(y1);
         } else {
             store_row<D, FP8 ? MQA_KV_FP8_E4M3 : MQA_KV_BF16>(cell + r * 64 * (FP8 ? 1 : 2), id >= 0, y0, y1, ch.c0,
-                                                              ch.c1, l, a.k_scale);
+                                                              ch.c1, l, FP8 ? 1.f / a.k_scale : 0.f);
         }
     }
 }
