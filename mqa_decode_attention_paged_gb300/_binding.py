@@ -10,6 +10,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 from . import build as _build
 
 OK = 0
@@ -138,7 +140,6 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
@@ -178,7 +179,6 @@ def _on_device(named):
 
 def _check_common(q, kv_cache, code, block_table, seq_lens, out, out_shape, lse, lse_shape, workspace,
                   device_status, extra=()):
-    import torch
     _check(q, "q", (torch.bfloat16,))
     _check(kv_cache, "kv_cache", elt=2 if code == KV_BF16 else 1)
     _check(block_table, "block_table", (torch.int32,))
@@ -195,7 +195,6 @@ def _check_common(q, kv_cache, code, block_table, seq_lens, out, out_shape, lse,
 
 
 def _kv_code(kv_cache, kv_dtype):
-    import torch
     if kv_dtype is not None:
         return _KV_NAMES[kv_dtype] if isinstance(kv_dtype, str) else int(kv_dtype)
     if kv_cache.dtype == torch.bfloat16:
@@ -228,7 +227,6 @@ def mla_decode_fixed_splits(q, kv_cache, block_table, seq_lens, scale, k_scale=1
 
 def _mla_decode(fn, name, q, kv_cache, block_table, seq_lens, scale, k_scale, out, lse, num_kv_splits, workspace,
                 kv_lora_rank, kv_dtype, device_status, stream, return_lse):
-    import torch
     B, H, D = q.shape
     nb, page, D2 = kv_cache.shape
     if D2 != D:
@@ -259,7 +257,6 @@ def mla_decode_multi(q, kv_cache, block_table, seq_lens, scale, k_scale=1.0, *, 
     """Multi-token MLA decode through the C ABI.  q [B, q_len, H, D] bf16 (query i of
     request b sits at position seq_lens[b] - q_len + i and sees the keys up to it);
     returns out [B, q_len, H, R] bf16 and lse [B, q_len, H] fp32."""
-    import torch
     B, Lq, H, D = q.shape
     nb, page, D2 = kv_cache.shape
     if D2 != D:
@@ -291,7 +288,6 @@ def mla_decode_sparse(q, kv_cache, block_table, seq_lens, indices, scale, k_scal
     """Sparse (top-k) MLA decode through the C ABI.  q [B, H, D] bf16, indices [B, topk]
     int32 logical positions (entries outside [0, seq_lens[b]) select nothing); returns
     out [B, H, R] bf16 and lse [B, H] fp32."""
-    import torch
     B, H, D = q.shape
     nb, page, D2 = kv_cache.shape
     if D2 != D:
@@ -329,7 +325,6 @@ def gqa_paged_decode(q, kv_cache, block_table, seq_lens, scale, k_scale=1.0, v_s
     kv_dtype "fp8_e4m3_pth" / "int8_pth", uint8 [num_blocks, 2, page, Hkv,
     D + 4] rows of D codes followed by their fp32 scale, or "int4_pth", uint8
     [..., D / 2 + 4] rows of packed 4-bit codes followed by the scale."""
-    import torch
     B, Hq, D = q.shape
     nb, two, page, Hkv, D2 = kv_cache.shape
     code = _kv_code(kv_cache, kv_dtype)
@@ -362,7 +357,6 @@ def lse_merge(shard_out, shard_lse, *, out=None, lse=None, stream=None, return_l
     parallelism, after the caller has gathered the shards): shard_out bf16
     [G, ..., head_dim], shard_lse fp32 [G, ...]; returns (out [..., head_dim]
     bf16, lse [...] fp32)."""
-    import torch
     G = shard_out.shape[0]
     D = shard_out.shape[-1]
     lead = tuple(shard_out.shape[1:-1])
@@ -442,7 +436,6 @@ def dcp_scale_shard(shard_out, gathered_lse, rank, *, scaled=None, lse=None, sca
     reduce-scatter over the ranks (C ABI ``mqa_dcp_scale_shard``):
     shard_out bf16 [B, H, D], gathered_lse fp32 [G, B, H]; returns (scaled
     [G, B, H / G, D] fp32 or bf16, merged lse [B, H] fp32)."""
-    import torch
     B, H, D = shard_out.shape
     G = gathered_lse.shape[0]
     if H % G != 0:
@@ -518,7 +511,6 @@ def _call_stream(stream, index, allocated):
     """The raw stream of a call on device `index`, by default the current one.  Tensors that the call allocated (on
     the current stream) are recorded on a stream that the caller passes, so that their memory is not reused while
     that stream still works on them."""
-    import torch
     raw = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
         return raw
@@ -534,7 +526,6 @@ def _call_stream(stream, index, allocated):
 
 def _block_code(kv_cache, kv_scales, kv_dtype):
     """kv_dtype code of a cache that may have block scales."""
-    import torch
     if kv_dtype is not None or kv_scales is None:
         return _kv_code(kv_cache, kv_dtype)
     if kv_cache.dtype == torch.float8_e4m3fn:
@@ -546,7 +537,6 @@ def _block_code(kv_cache, kv_scales, kv_dtype):
 
 def _scale_block(kv_scales, code, nb, page, hkv):
     """Tokens per scale of kv_scales [num_blocks, 2, page / scale_block, num_kv_heads]; 0 for the other formats."""
-    import torch
     if code not in (KV_FP8_E4M3_BLOCK, KV_INT8_BLOCK):
         if kv_scales is not None:
             raise ValueError("kv_scales is for the fp8_e4m3_block and int8_block caches only")
@@ -586,7 +576,6 @@ def gqa_block_decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, *, ou
 
 def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale, window, sinks, out,
                    lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse):
-    import torch
     shape = q.shape
     if len(shape) not in (3, 4) or kv_cache.dim() != 5:
         raise ValueError("q must be [batch, (q_len,) heads, head_size] and kv_cache have 5 dimensions")
@@ -655,14 +644,15 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
 def _check_rows(t, name, shape, dense):
     """A bf16 tensor of shape `shape` whose last `dense` dimensions are dense (rows of a wider tensor will do);
     returns its leading strides."""
-    import torch
+    st = t.stride()
+    if (t.dtype is torch.bfloat16 and t.shape == shape and st[-1] == 1 and (dense == 1 or st[-2] == shape[-1])
+            and 1 not in shape and 0 not in shape):
+        return st[:-dense]
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st, want = t.stride(), 1
-    if st[-1] == 1 and (dense == 1 or st[-2] == shape[-1]) and 1 not in shape and 0 not in shape:
-        return st[:-dense]
+    want = 1
     for i in range(1, dense + 1):
         if shape[-i] != 1 and st[-i] != want:
             raise ValueError(f"the last {dense} dimension(s) of {name} must be contiguous")
@@ -677,7 +667,6 @@ def _check_rows(t, name, shape, dense):
 
 
 def _check_append(index, cos_sin, width, kv_cache, block_table, seq_lens, query_start, device_status, named):
-    import torch
     bt_shape = block_table.shape
     if (index >= 0 and len(bt_shape) == 2 and cos_sin.dim() == 2 and width in (None, cos_sin.shape[1])
             and _fits(cos_sin, torch.float32, cos_sin.shape, index) and kv_cache.is_contiguous()
@@ -716,7 +705,6 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
     holds cosines, then sines; interleaved pairs are columns (2i, 2i + 1).  kv_cache is any cache that the GQA
     decode calls read, with kv_scales for the block-scaled formats; both are updated in place.  Returns the rotated
     queries (q_out, which may be q itself; allocated when only q is given), or None."""
-    import torch
     if k.dim() != 3 or kv_cache.dim() != 5 or cos_sin.dim() != 2:
         raise ValueError("k must be [tokens, heads, head_size], kv_cache have 5 dimensions and cos_sin 2")
     T, Hkv, D = k.shape
@@ -772,7 +760,6 @@ def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_
     q_pe_out (for instance ``q[..., R:]`` of the absorbed query; may be q_pe itself; allocated when only q_pe is
     given), which is returned (None without q_pe).  cos_sin fp32 [max_position, 64]; the batch is described as for
     :func:`gqa_rope_append`."""
-    import torch
     if kv_c.dim() != 2 or kv_cache.dim() != 3:
         raise ValueError("kv_c must be [tokens, kv_lora_rank] and kv_cache [num_blocks, page, head_size]")
     T, R = kv_c.shape

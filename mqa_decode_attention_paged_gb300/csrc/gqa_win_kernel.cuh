@@ -47,6 +47,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "gqa_win.cuh"
 
 namespace mqa {
@@ -887,6 +889,21 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     }
 }
 
+// Lets `kern` (one of the two of this instance) use all of a block's shared
+// memory, once per device.
+template <int D, int KIND, int NHB>
+cudaError_t allow_smem(const void* kern, bool multi) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[2][kDevices];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kDevices;
+    if (known && done[multi][dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (known && e == cudaSuccess) done[multi][dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
 template <int D, int KIND, int NHB>
 cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     const int vb = a.batch * a.rb;
@@ -896,9 +913,7 @@ cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     a.nslots = ns;
     const int bytes = layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total;
     auto kern = a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true> : gqa_win_kernel<D, KIND, NHB, false>;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        e != cudaSuccess)
-        return e;
+    if (cudaError_t e = allow_smem<D, KIND, NHB>(reinterpret_cast<const void*>(kern), a.q_len > 1); e != cudaSuccess) return e;
     return launch_with_pdl(kern, dim3(grid), dim3(32 * a.Hkv * a.ts), bytes, stream, a);
 }
 
