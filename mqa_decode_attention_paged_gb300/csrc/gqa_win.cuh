@@ -86,8 +86,15 @@ __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
     return v;
 }
 
-// Balanced mode with T tiles: units actually used.
-__device__ __forceinline__ int win_units(int units, int T) { return min(units, max(1, T)); }
+// Balanced mode with T tiles, the longest request's being `longest`: units
+// actually used.  Where the units are enough and no request is more than two
+// tiles above an equal share, a unit is a request (returned as 0): cutting
+// requests would cost more, in starts and partials to merge, than it evens
+// out (256 windows of five tiles on 304 units: 25 us instead of 31).
+__device__ __forceinline__ int win_units(int units, int vb, int T, int longest) {
+    const int U = min(units, max(1, T));
+    return vb <= units && longest <= T / U + 2 ? 0 : U;
+}
 
 // First tile of unit g of U: g T / U, moved to a request's start or end where
 // one lies a tile away and units hold four tiles at least: a cut costs a

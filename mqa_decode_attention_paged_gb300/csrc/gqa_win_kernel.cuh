@@ -87,7 +87,7 @@ __host__ __device__ inline Layout layout(int hkv, int ts, int nslots, int vb, in
     l.desc = l.scales + nc * kMaxSlots * 8;
     l.bars = l.desc + nc * kDesc * 16;
     l.cum = l.bars + nc * kMaxSlots * 8;
-    l.total = l.cum + 4 * (vb + 1 + batch) + 1024;  // + alignment of the base
+    l.total = l.cum + 4 * (vb + 2 + batch) + 1024;  // + alignment of the base
     return l;
 }
 
@@ -207,8 +207,9 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
 // The rest of a wait that did not end at once.
 static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity); }
 
-// cum[0 .. vb]: exclusive prefix of the virtual requests' tile counts; lens:
-// clamped lengths.  Every thread of the block calls it; returns the total.
+// cum[0 .. vb]: exclusive prefix of the virtual requests' tile counts, then the
+// largest count; lens: clamped lengths.  Every thread of the block calls it;
+// returns the total.
 __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* lens) {
     const int vb = a.batch * a.rb;
     for (int v = threadIdx.x; v < vb; v += blockDim.x) {
@@ -220,10 +221,11 @@ __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* len
     if (threadIdx.x == 0) cum[0] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
-        int running = 0;
+        int running = 0, longest = 0;
         for (int base = 0; base < vb; base += 32) {
             const int i = base + static_cast<int>(threadIdx.x);
             int x = i < vb ? cum[i + 1] : 0;
+            longest = max(longest, x);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, x, o);
@@ -232,6 +234,8 @@ __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* len
             if (i < vb) cum[i + 1] = running + x;
             running += __shfl_sync(0xffffffffu, x, 31);
         }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (threadIdx.x == 0) cum[vb + 1] = longest;
     }
     __syncthreads();
     return cum[vb];
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     const int vb = a.batch * a.rb;
     const Layout lay = layout<D, KIND, NHB>(Hkv, TS, nslots, vb, a.batch);
     int* cum = reinterpret_cast<int*>(smem + lay.cum);
-    int* lens = cum + vb + 1;
+    int* lens = cum + vb + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp / Hkv, kh = warp - sub * Hkv;
     const bool scaled = KIND != kWinBf16 && a.kv_scales != nullptr;
@@ -279,11 +283,11 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 
     // this block's tiles [p0, p1)
     int p0, p1;
-    if (a.units == 0) {
-        p0 = cum[blockIdx.x];
-        p1 = cum[blockIdx.x + 1];
+    const int U = a.units == 0 ? 0 : win_units(a.units, vb, T, cum[vb + 1]);
+    if (U == 0) {  // a unit is a request
+        p0 = cum[min(static_cast<int>(blockIdx.x), vb)];
+        p1 = cum[min(static_cast<int>(blockIdx.x) + 1, vb)];
     } else {
-        const int U = win_units(a.units, T);
         const int x = win_unit_start(cum, vb, T, U, static_cast<int>(blockIdx.x) + (lane & 1));
         p0 = __shfl_sync(0xffffffffu, x, 0);
         p1 = __shfl_sync(0xffffffffu, x, 1);
