@@ -31,24 +31,43 @@ constexpr int kWarps = 4;
 constexpr float kE4m3Max = 448.f, kInt8Max = 127.f, kInt4Max = 7.f;
 constexpr float kTinyScale = 1.1754943508222875e-38f;  // 2^-126: scales are zero or normal
 
-// Request of token t: the last b with query_start[b] <= t; -1 before the first
-// request, batch behind the last.  A warp counts 32 entries at a time.
-__device__ __forceinline__ int find_request(const AppendBatch& a, int t, int lane) {
-    int n = 0;
-#pragma unroll 4
-    for (int base = 0; base <= a.batch; base += 32) {
-        const int i = base + lane;
-        n += __popc(__ballot_sync(0xffffffffu, i <= a.batch && __ldg(a.query_start + i) <= t));
+// The request that token t belongs to, with its entries; false for padding.
+// query_start ascends: a warp narrows the candidates to 32 by samples, then
+// reads those with their lengths, so that a batch of up to 32 (1024) requests
+// costs one (two) dependent loads.
+struct Owner {
+    int b, q0, q1, len;
+};
+__device__ __forceinline__ bool find_owner(const AppendBatch& a, int t, int lane, Owner& o) {
+    int lo = 0, n = a.batch;
+    while (n > 32) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const int m = __popc(__ballot_sync(0xffffffffu, at < n && __ldg(a.query_start + lo + at) <= t));
+        if (m == 0) return false;
+        lo += (m - 1) * step;
+        n = min(step, n - (m - 1) * step);
     }
-    return n - 1;
+    int q0 = 0, q1 = 0, len = 0;
+    if (lane < n) {
+        q0 = __ldg(a.query_start + lo + lane);
+        q1 = __ldg(a.query_start + lo + lane + 1);
+        len = __ldg(a.seq_lens + lo + lane);
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane < n && q0 <= t && t < q1);
+    if (hit == 0) return false;
+    const int s = __ffs(hit) - 1;
+    o.b = lo + s;
+    o.q0 = __shfl_sync(0xffffffffu, q0, s);
+    o.q1 = __shfl_sync(0xffffffffu, q1, s);
+    o.len = __shfl_sync(0xffffffffu, len, s);
+    return true;
 }
 
-// Position of token t of request b, or -1 (reported) where the request's
+// Position of token t of request o, or -1 (reported) where the request's
 // length does not hold its new tokens or the position has no angle or page.
-__device__ __forceinline__ int position(const AppendBatch& a, int b, int t) {
-    const int q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1), len = __ldg(a.seq_lens + b);
-    const long long p = static_cast<long long>(len) - q1 + t;
-    if (q0 < 0 || q1 > a.tokens || len < static_cast<long long>(q1) - q0 || p < 0 || p >= a.max_position ||
+__device__ __forceinline__ int position(const AppendBatch& a, const Owner& o, int t) {
+    const long long p = static_cast<long long>(o.len) - o.q1 + t;
+    if (o.q0 < 0 || o.q1 > a.tokens || o.len < static_cast<long long>(o.q1) - o.q0 || p >= a.max_position ||
         p >= static_cast<long long>(a.max_blocks) * a.page) {
         report(a.status, MQA_ERR_DEVICE_CHECK);
         return -1;
@@ -244,13 +263,13 @@ __device__ __forceinline__ void append_rows(const GqaAppendArgs& a, int t, int r
         x0[it] = *reinterpret_cast<const uint4*>(src + ch.c0);
         x1[it] = *reinterpret_cast<const uint4*>(src + ch.c1);
     }
-    const int b = find_request(a.t, t, lane);
-    if (b < 0 || b >= a.t.batch) return;  // padding: no request's token
-    const int p = position(a.t, b, t);
+    Owner own;
+    if (!find_owner(a.t, t, lane, own)) return;  // padding: no request's token
+    const int p = position(a.t, own, t);
     if (p < 0) return;
     Angles an;
     if (ch.rot) load_angles(an, a.t, p, l);
-    const int id = BLOCK ? -1 : block_id(a.t, b, p);
+    const int id = BLOCK ? -1 : block_id(a.t, own.b, p);
     uint8_t* cell = a.cache + (static_cast<long long>(id) * 2 * a.t.page + p % a.t.page) * a.Hkv * row_bytes<D, FMT>();
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
@@ -292,60 +311,103 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
     return codes4<INT8>(f[0], f[1], f[2], f[3]);
 }
 
-// Block-scaled formats: block of tokens number `task` of those the batch
-// touches, one plane and head (one warp).
-template <int D, int FMT>
-__device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long task, int plane, int head, int lane) {
-    constexpr int LPR = D / 16, RPI = 32 / LPR;
-    constexpr bool INT8 = FMT == MQA_KV_INT8_BLOCK;
-    constexpr float top = INT8 ? kInt8Max : kE4m3Max;
-    const int G = a.scale_block;
-    // request and block: the prefix of the requests' block counts
+// A request's share of a block of tokens: its new positions [pa, pe) of the
+// block starting at position `first`, the first of them token t.
+struct Share {
+    int b, first, pa, pe, t;
+};
+__device__ __forceinline__ bool share_of(const AppendBatch& a, const Owner& o, int p0, int first, int G, Share& s) {
+    const long long last = static_cast<long long>(first) + G;
+    s.b = o.b;
+    s.first = first;
+    s.pa = max(p0, first);
+    s.pe = static_cast<int>(last < o.len ? last : static_cast<long long>(o.len));
+    s.t = o.q0 + s.pa - p0;
+    if (s.pe > a.max_position || s.pe > static_cast<long long>(a.max_blocks) * a.page) {
+        report(a.status, MQA_ERR_DEVICE_CHECK);
+        return false;
+    }
+    return true;
+}
+
+// The share that starts with token t, if one does.
+__device__ __forceinline__ bool share_at_token(const AppendBatch& a, int t, int G, int lane, Share& s) {
+    Owner o;
+    if (!find_owner(a, t, lane, o)) return false;
+    const long long p0 = static_cast<long long>(o.len) - (static_cast<long long>(o.q1) - o.q0);
+    if (o.q0 < 0 || o.q1 > a.tokens || p0 < 0) {
+        if (t == o.q0) report(a.status, MQA_ERR_DEVICE_CHECK);
+        return false;
+    }
+    const int p = static_cast<int>(p0) + (t - o.q0);
+    if (t != o.q0 && p % G != 0) return false;
+    return share_of(a, o, static_cast<int>(p0), p / G * G, G, s);
+}
+
+// Share number `task` of the batch, by the prefix of the requests' counts.
+__device__ __forceinline__ bool share_by_number(const AppendBatch& a, long long task, int G, int lane, Share& s) {
     long long running = 0;
-    int b = -1, q0 = 0, n = 0, p0 = 0, kth = 0;
-    for (int base = 0; base < a.t.batch && b < 0; base += 32) {
+    for (int base = 0; base < a.batch; base += 32) {
         const int i = base + lane;
-        int c = 0, i0 = 0, ni = 0, pi = 0;
-        if (i < a.t.batch) {
-            i0 = __ldg(a.t.query_start + i);
-            const int i1 = __ldg(a.t.query_start + i + 1), len = __ldg(a.t.seq_lens + i);
-            if (i1 > i0) {
-                if (i0 < 0 || i1 > a.t.tokens || len < static_cast<long long>(i1) - i0) {
-                    report(a.t.status, MQA_ERR_DEVICE_CHECK);
+        Owner o{i, 0, 0, 0};
+        int c = 0, p0 = 0;
+        if (i < a.batch) {
+            o.q0 = __ldg(a.query_start + i);
+            o.q1 = __ldg(a.query_start + i + 1);
+            o.len = __ldg(a.seq_lens + i);
+            if (o.q1 > o.q0) {
+                if (o.q0 < 0 || o.q1 > a.tokens || o.len < static_cast<long long>(o.q1) - o.q0) {
+                    report(a.status, MQA_ERR_DEVICE_CHECK);
                 } else {
-                    ni = i1 - i0;
-                    pi = len - ni;
-                    c = (len - 1) / G - pi / G + 1;
+                    p0 = o.len - (o.q1 - o.q0);
+                    c = (o.len - 1) / G - p0 / G + 1;
                 }
             }
         }
         int x = c;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += u;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += u;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, running + x > task && running + x - c <= task);
         if (hit) {
-            const int s = __ffs(hit) - 1;
-            b = base + s;
-            q0 = __shfl_sync(0xffffffffu, i0, s);
-            n = __shfl_sync(0xffffffffu, ni, s);
-            p0 = __shfl_sync(0xffffffffu, pi, s);
-            kth = static_cast<int>(task - running) - __shfl_sync(0xffffffffu, x - c, s);
+            const int l = __ffs(hit) - 1;
+            o.b = base + l;
+            o.q0 = __shfl_sync(0xffffffffu, o.q0, l);
+            o.q1 = __shfl_sync(0xffffffffu, o.q1, l);
+            o.len = __shfl_sync(0xffffffffu, o.len, l);
+            p0 = __shfl_sync(0xffffffffu, p0, l);
+            const int kth = static_cast<int>(task - running) - __shfl_sync(0xffffffffu, x - c, l);
+            return share_of(a, o, p0, (p0 / G + kth) * G, G, s);
         }
         running += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (b < 0) return;  // fewer blocks than the grid allows for
-    const int first = (p0 / G + kth) * G;                                // position of the block's first slot
-    const long long last = static_cast<long long>(first) + G;
-    const int pa = max(p0, first);                                       // new positions [pa, pe)
-    const int pe = static_cast<int>(last < static_cast<long long>(p0) + n ? last : static_cast<long long>(p0) + n);
-    if (pe > a.t.max_position || pe > static_cast<long long>(a.t.max_blocks) * a.t.page) {
-        report(a.t.status, MQA_ERR_DEVICE_CHECK);
+    return false;  // fewer shares than the grid allows for
+}
+
+// How a share is found: at the token that starts it, or by its number in the
+// batch; and by how many warps of a thread block it is then done.
+struct ShareMode {
+    bool by_token;
+    int warps;  // 1 or kWarps
+};
+
+// Block-scaled formats: one share, one plane and head, rows dealt to
+// mode.warps warps (a warp alone, or a whole thread block).
+template <int D, int FMT>
+__device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long task, ShareMode mode, int plane, int head,
+                                             int lane, float* exchange) {
+    constexpr int LPR = D / 16, RPI = 32 / LPR;
+    constexpr bool INT8 = FMT == MQA_KV_INT8_BLOCK;
+    constexpr float top = INT8 ? kInt8Max : kE4m3Max;
+    const int G = a.scale_block;
+    Share sh;
+    if (!(mode.by_token ? share_at_token(a.t, static_cast<int>(task), G, lane, sh)
+                   : share_by_number(a.t, task, G, lane, sh)))
         return;
-    }
-    const int id = block_id(a.t, b, first);
+    const int first = sh.first, pa = sh.pa, pe = sh.pe;
+    const int id = block_id(a.t, sh.b, first);
     if (id < 0) return;
     const int had = pa - first, m = pe - pa;
     const int slot = first % a.t.page;
@@ -354,11 +416,12 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
     uint8_t* cell = a.cache + (((static_cast<long long>(id) * 2 + plane) * a.t.page + slot) * a.Hkv + head) * D;
     const long long row_step = static_cast<long long>(a.Hkv) * D;
 
-    const int l = lane % LPR, rl = lane / LPR;
+    const int warp = mode.warps == 1 ? 0 : threadIdx.x >> 5;
+    const int l = lane % LPR, rl = lane / LPR + warp * RPI, step = RPI * mode.warps;
     const Chunks ch = chunks_of(l, a.t.rotary, a.t.interleaved);
     const bool rot = plane == 0 && ch.rot;
     const long long stride = plane ? a.v_stride : a.k_stride;
-    const __nv_bfloat16* src = (plane ? a.v : a.k) + (q0 + pa - p0) * stride + head * D;
+    const __nv_bfloat16* src = (plane ? a.v : a.k) + sh.t * stride + head * D;
     // values of new row i of the block (zeros past the end)
     auto values = [&](int i, float (&y0)[8], float (&y1)[8]) {
         uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
@@ -374,19 +437,24 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
     };
     float amax = 0.f;
 #pragma unroll 4
-    for (int i = rl; i - rl < m; i += RPI) {
+    for (int i = rl; i - lane / LPR < m; i += step) {
         float y0[8], y1[8];
         values(i, y0, y1);
         amax = fmaxf(amax, amax16(y0, y1));
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (mode.warps > 1) {  // (every warp has read s_old by the time it meets the others)
+        if (lane == 0) exchange[warp] = amax;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, exchange[w]);
+    }
     float s_new = amax / top;
     if (s_new < kTinyScale) s_new = 0.f;
     s_new = fmaxf(s_new, s_old);
     if (s_new > s_old && had > 0) {  // the codes the block held, at the new scale
         const float ratio = s_old / s_new;
-        for (int i = rl; i < had; i += RPI) {
+        for (int i = rl; i < had; i += step) {
             uint4* p = reinterpret_cast<uint4*>(cell + i * row_step + 16 * l);
             const uint4 w = *p;
             *p = make_uint4(rescale4<INT8>(w.x, ratio), rescale4<INT8>(w.y, ratio), rescale4<INT8>(w.z, ratio),
@@ -395,7 +463,7 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
     }
     const float inv = inverse(s_new);
 #pragma unroll 4
-    for (int i = rl; i - rl < m; i += RPI) {
+    for (int i = rl; i - lane / LPR < m; i += step) {
         float y0[8], y1[8];
         values(i, y0, y1);
         if (i >= m) continue;
@@ -403,26 +471,29 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
         *reinterpret_cast<uint2*>(row + ch.c0) = codes8<INT8>(y0, inv);
         *reinterpret_cast<uint2*>(row + ch.c1) = codes8<INT8>(y1, inv);
     }
-    if (lane == 0) *sp = s_new;
+    if (lane == 0 && warp == 0) *sp = s_new;
 }
 
 // Warp tasks: (block formats) blocks, which take longest, then rows of tokens.
 template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppendArgs a, const int groups,
+__global__ void __launch_bounds__(32 * kWarps, 6) gqa_append_kernel(const GqaAppendArgs a, const int groups,
                                                                  const long long row_tasks,
-                                                                 const long long block_tasks) {
+                                                                 const long long block_tasks, const ShareMode mode) {
+    __shared__ float exchange[kWarps];
     const int lane = threadIdx.x & 31;
     long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
     if constexpr (block_format<FMT>()) {
-        if (w < block_tasks) {
-            const long long task = w / (2 * a.Hkv);
-            const int ph = static_cast<int>(w - task * 2 * a.Hkv);
-            append_block<D, FMT>(a, task, ph / a.Hkv, ph % a.Hkv, lane);
+        // (whole thread blocks where several warps share a task)
+        const long long k = mode.warps == 1 ? w : blockIdx.x;
+        if (k < block_tasks) {
+            const long long task = k / (2 * a.Hkv);
+            const int ph = static_cast<int>(k - task * 2 * a.Hkv);
+            append_block<D, FMT>(a, task, mode, ph / a.Hkv, ph % a.Hkv, lane, exchange);
             return;
         }
-        w -= block_tasks;
+        w -= block_tasks * mode.warps;
     }
     if (w >= row_tasks) return;
     const int t = static_cast<int>(w / groups);
@@ -432,7 +503,7 @@ __global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppend
 // MLA: a token's 64-column pieces: R / 64 of kv_c, k_pe, then H of q_pe (4
 // lanes a piece).
 template <bool FP8>
-__global__ void __launch_bounds__(32 * kWarps) mla_append_kernel(const MlaAppendArgs a, const int groups,
+__global__ void __launch_bounds__(32 * kWarps, 6) mla_append_kernel(const MlaAppendArgs a, const int groups,
                                                                  const long long row_tasks) {
     constexpr int D = 64, LPR = 4, RPI = 8;
     const int lane = threadIdx.x & 31;
@@ -457,13 +528,13 @@ __global__ void __launch_bounds__(32 * kWarps) mla_append_kernel(const MlaAppend
         x0[it] = *reinterpret_cast<const uint4*>(src + ch.c0);
         x1[it] = *reinterpret_cast<const uint4*>(src + ch.c1);
     }
-    const int b = find_request(a.t, t, lane);
-    if (b < 0 || b >= a.t.batch) return;  // padding
-    const int p = position(a.t, b, t);
+    Owner own;
+    if (!find_owner(a.t, t, lane, own)) return;  // padding
+    const int p = position(a.t, own, t);
     if (p < 0) return;
     Angles an;
     load_angles(an, a.t, p, l);
-    const int id = r0 <= nc ? block_id(a.t, b, p) : -1;
+    const int id = r0 <= nc ? block_id(a.t, own.b, p) : -1;
     uint8_t* cell = a.cache + (static_cast<long long>(id) * a.t.page + p % a.t.page) * (a.R + 64) * (FP8 ? 1 : 2);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
@@ -491,15 +562,24 @@ cudaError_t launch(const GqaAppendArgs& a, cudaStream_t stream) {
     const int groups = (rows + rows_per_warp<D>() - 1) / rows_per_warp<D>();
     const long long row_tasks = static_cast<long long>(a.t.tokens) * groups;
     long long block_tasks = 0;
+    ShareMode mode{false, 1};
     if (BLOCK) {
-        // blocks touched: a request with n new tokens touches at most n, and
-        // at most (n - 1) / G + 2
+        // One task per plane, head and share of a block.  With few new tokens
+        // per request a token is the start of a share more often than not, and
+        // a warp finds its request by a search; with many, shares are numbered
+        // by the prefix of the requests' counts (a request with n new tokens
+        // touches at most n blocks, and at most (n - 1) / G + 2).
         const long long T = a.t.tokens, bound = T / a.scale_block + 2LL * a.t.batch;
-        block_tasks = (T < bound ? T : bound) * 2 * a.Hkv;
+        mode.by_token = T <= bound;
+        // Shares of more than 16 rows go to four warps: a warp alone would
+        // wait for 16 loads in turn, twice (a prefill of 7.4 thousand tokens in
+        // 64-token blocks: 48 us, and 33 us of it for the blocks alone).
+        mode.warps = !mode.by_token && a.scale_block > 16 ? kWarps : 1;
+        block_tasks = (mode.by_token ? T : bound) * 2 * a.Hkv;
     }
-    const long long grid = (row_tasks + block_tasks + kWarps - 1) / kWarps;
+    const long long grid = (row_tasks + block_tasks * mode.warps + kWarps - 1) / kWarps;
     return launch_with_pdl(gqa_append_kernel<D, FMT>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), 0, stream,
-                           a, groups > 0 ? groups : 1, row_tasks, block_tasks);
+                           a, groups > 0 ? groups : 1, row_tasks, block_tasks, mode);
 }
 
 template <int D>
