@@ -17,8 +17,7 @@
 // Block-scaled formats: one warp owns one (block of tokens, plane, head).  It
 // takes the largest magnitude of the new values, s = max(s_old, amax / Q) (s_old
 // only where the block already held tokens), rescales the codes it held by
-// s_old / s if the scale grew, and stores the new codes x / s.  The new rows
-// are read twice, the second time from cache.
+// s_old / s if the scale grew, and stores the new codes x / s.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -140,19 +139,24 @@ __device__ __forceinline__ void rotate(float (&y0)[8], float (&y1)[8], const Ang
     }
 }
 
-__device__ __forceinline__ uint32_t e4m3_code(float x) {
-    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
-}
 __device__ __forceinline__ int int_code(float x, float top) { return __float2int_rn(fminf(fmaxf(x, -top), top)); }
-// Four 8-bit codes, lowest first; INT8 selects the format.
+// Four 8-bit codes, lowest first; INT8 selects the format.  (int8: |x| is at
+// most 127 and a rounding, so that saturation to -128 does not come up.)
 template <bool INT8>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    uint32_t r;
     if constexpr (INT8) {
-        return (int_code(a, kInt8Max) & 0xffu) | (int_code(b, kInt8Max) & 0xffu) << 8 |
-               (int_code(c, kInt8Max) & 0xffu) << 16 | (int_code(d, kInt8Max) & 0xffu) << 24;
+        asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\t"
+            "cvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+            : "=r"(r)
+            : "r"(__float2int_rn(a)), "r"(__float2int_rn(b)), "r"(__float2int_rn(c)), "r"(__float2int_rn(d)));
     } else {
-        return e4m3_code(a) | e4m3_code(b) << 8 | e4m3_code(c) << 16 | e4m3_code(d) << 24;
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
     }
+    return r;
 }
 // The eight codes of y / s, given inv = 1 / s (0 where s = 0: zeros).  The
 // product is within 2^-23 of the quotient, relative: another code only where
@@ -407,41 +411,59 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
                    : share_by_number(a.t, task, G, lane, sh)))
         return;
     const int first = sh.first, pa = sh.pa, pe = sh.pe;
-    const int id = block_id(a.t, sh.b, first);
-    if (id < 0) return;
     const int had = pa - first, m = pe - pa;
-    const int slot = first % a.t.page;
-    float* sp = a.scales + ((static_cast<long long>(id) * 2 + plane) * (a.t.page / G) + slot / G) * a.Hkv + head;
-    const float s_old = had > 0 ? *sp : 0.f;
-    uint8_t* cell = a.cache + (((static_cast<long long>(id) * 2 + plane) * a.t.page + slot) * a.Hkv + head) * D;
-    const long long row_step = static_cast<long long>(a.Hkv) * D;
-
     const int warp = mode.warps == 1 ? 0 : threadIdx.x >> 5;
     const int l = lane % LPR, rl = lane / LPR + warp * RPI, step = RPI * mode.warps;
     const Chunks ch = chunks_of(l, a.t.rotary, a.t.interleaved);
     const bool rot = plane == 0 && ch.rot;
     const long long stride = plane ? a.v_stride : a.k_stride;
     const __nv_bfloat16* src = (plane ? a.v : a.k) + sh.t * stride + head * D;
-    // values of new row i of the block (zeros past the end)
-    auto values = [&](int i, float (&y0)[8], float (&y1)[8]) {
-        uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
-        Angles an;
-        if (i < m) {
-            u0 = *reinterpret_cast<const uint4*>(src + i * stride + ch.c0);
-            u1 = *reinterpret_cast<const uint4*>(src + i * stride + ch.c1);
-            if (rot) load_angles(an, a.t, pa + i, l);
-        }
+    // up to kKeep new rows per lane are read once and kept; the rest twice
+    constexpr int kKeep = 4;
+    uint4 x0[kKeep], x1[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        const int i = rl + k * step;
+        x0[k] = x1[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (i >= m) continue;
+        x0[k] = *reinterpret_cast<const uint4*>(src + i * stride + ch.c0);
+        x1[k] = *reinterpret_cast<const uint4*>(src + i * stride + ch.c1);
+    }
+    const int id = block_id(a.t, sh.b, first);
+    if (id < 0) return;
+    const int slot = first % a.t.page;
+    float* sp = a.scales + ((static_cast<long long>(id) * 2 + plane) * (a.t.page / G) + slot / G) * a.Hkv + head;
+    const float s_old = had > 0 ? *sp : 0.f;
+    uint8_t* cell = a.cache + (((static_cast<long long>(id) * 2 + plane) * a.t.page + slot) * a.Hkv + head) * D;
+    const long long row_step = static_cast<long long>(a.Hkv) * D;
+
+    // values of new row i < m, given its chunks
+    auto values = [&](int i, uint4 u0, uint4 u1, float (&y0)[8], float (&y1)[8]) {
         unpack8(y0, u0);
         unpack8(y1, u1);
-        if (rot && i < m) rotate(y0, y1, an, a.t.interleaved);
+        if (rot) {
+            Angles an;
+            load_angles(an, a.t, pa + i, l);
+            rotate(y0, y1, an, a.t.interleaved);
+        }
     };
     float amax = 0.f;
-#pragma unroll 4
-    for (int i = rl; i - lane / LPR < m; i += step) {
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        const int i = rl + k * step;
+        if (i >= m) continue;
         float y0[8], y1[8];
-        values(i, y0, y1);
+        values(i, x0[k], x1[k], y0, y1);
         amax = fmaxf(amax, amax16(y0, y1));
     }
+#pragma unroll 2
+    for (int i = rl + kKeep * step; i < m; i += step) {
+        float y0[8], y1[8];
+        values(i, *reinterpret_cast<const uint4*>(src + i * stride + ch.c0),
+               *reinterpret_cast<const uint4*>(src + i * stride + ch.c1), y0, y1);
+        amax = fmaxf(amax, amax16(y0, y1));
+    }
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (mode.warps > 1) {  // (every warp has read s_old by the time it meets the others)
@@ -462,14 +484,25 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
         }
     }
     const float inv = inverse(s_new);
-#pragma unroll 4
-    for (int i = rl; i - lane / LPR < m; i += step) {
-        float y0[8], y1[8];
-        values(i, y0, y1);
-        if (i >= m) continue;
+    auto store = [&](int i, const float (&y0)[8], const float (&y1)[8]) {
         uint8_t* row = cell + (had + i) * row_step;
         *reinterpret_cast<uint2*>(row + ch.c0) = codes8<INT8>(y0, inv);
         *reinterpret_cast<uint2*>(row + ch.c1) = codes8<INT8>(y1, inv);
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        const int i = rl + k * step;
+        if (i >= m) continue;
+        float y0[8], y1[8];
+        values(i, x0[k], x1[k], y0, y1);
+        store(i, y0, y1);
+    }
+#pragma unroll 2
+    for (int i = rl + kKeep * step; i < m; i += step) {
+        float y0[8], y1[8];
+        values(i, *reinterpret_cast<const uint4*>(src + i * stride + ch.c0),
+               *reinterpret_cast<const uint4*>(src + i * stride + ch.c1), y0, y1);
+        store(i, y0, y1);
     }
     if (lane == 0 && warp == 0) *sp = s_new;
 }
