@@ -65,6 +65,19 @@ mqa_status mqa_test_mla_warp_gives_up(const void* q, const void* kv_cache, const
                                       size_t workspace_bytes, int* device_status, void* stream, int unit,
                                       int warp);
 
+/* A gqa_window_decode (k_scale = v_scale = 1) in which work unit
+ * `withhold_unit` copies none of its tiles: its warps wait in vain, meet each
+ * other all the same and return.  Arguments as for gqa_window_decode;
+ * withhold_unit >= 0 (with num_kv_splits == 1, unit b is request b where 16
+ * query rows hold a request). */
+mqa_status mqa_test_gqa_window_withheld(const void* q, const void* kv_cache, const float* kv_scales,
+                                        const int32_t* block_table, const int32_t* seq_lens, float scale, int window,
+                                        int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,
+                                        int num_kv_heads, int head_size, int num_blocks, int page_size,
+                                        int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits,
+                                        void* workspace, size_t workspace_bytes, int* device_status, void* stream,
+                                        int withhold_unit);
+
 #ifdef __cplusplus
 }
 #endif

@@ -628,14 +628,14 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
     raw = _call_stream(stream, index, fresh)
     if window is None:
         rc = lib.gqa_block_decode(q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
-                                  seq_lens.data_ptr(), scale, out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb, page,
-                                  bt_shape[1], block, code, num_kv_splits, _raw(workspace), ws_bytes,
+                                  seq_lens.data_ptr(), float(scale), out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb,
+                                  page, bt_shape[1], block, code, int(num_kv_splits), _raw(workspace), ws_bytes,
                                   _raw(device_status), raw)
     else:
         rc = lib.gqa_window_decode(q.data_ptr(), kv_cache.data_ptr(), _raw(kv_scales), block_table.data_ptr(),
-                                   seq_lens.data_ptr(), scale, k_scale, v_scale, window, sinks, out.data_ptr(),
-                                   _raw(lse), B, L, Hq, Hkv, D, nb, page, bt_shape[1], block, code, num_kv_splits,
-                                   _raw(workspace), ws_bytes, _raw(device_status), raw)
+                                   seq_lens.data_ptr(), float(scale), float(k_scale), float(v_scale), int(window),
+                                   int(sinks), out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb, page, bt_shape[1],
+                                   block, code, int(num_kv_splits), _raw(workspace), ws_bytes, _raw(device_status), raw)
     if rc != OK:
         raise MqaError(rc, name)
     return out, lse
@@ -745,7 +745,7 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
         return q_out
     rc = lib.gqa_rope_append(_raw(q), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(), query_start.data_ptr(),
                              seq_lens.data_ptr(), block_table.data_ptr(), _raw(q_out), kv_cache.data_ptr(),
-                             _raw(kv_scales), k_scale, v_scale, T, B, Hq, Hkv, D, cos_sin.shape[1],
+                             _raw(kv_scales), float(k_scale), float(v_scale), T, B, Hq, Hkv, D, cos_sin.shape[1],
                              1 if interleaved else 0, cos_sin.shape[0], nb, page, block_table.shape[1], block, code,
                              qs, ks, vs, qos, _raw(device_status), _call_stream(stream, index, fresh))
     if rc != OK:
@@ -798,7 +798,7 @@ def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_
         return q_pe_out
     rc = lib.mla_rope_append(kv_c.data_ptr(), k_pe.data_ptr(), _raw(q_pe), cos_sin.data_ptr(),
                              query_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), _raw(q_pe_out),
-                             kv_cache.data_ptr(), k_scale, T, B, H, D, R, 1 if interleaved else 0, cos_sin.shape[0],
+                             kv_cache.data_ptr(), float(k_scale), T, B, H, D, R, 1 if interleaved else 0, cos_sin.shape[0],
                              nb, page, block_table.shape[1], code, cs, ps, qs, qhs, qos, qohs, _raw(device_status),
                              _call_stream(stream, index, fresh))
     if rc != OK:

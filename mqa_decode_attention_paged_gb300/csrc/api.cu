@@ -300,6 +300,7 @@ bool mla_tensor_map(CUtensorMap* out, const void* base, int cols, long long rows
 
 mqa_status mqa::api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
 PFN_cuTensorMapEncodeTiled_v12000 mqa::api_encode_tiled() { return encode_tiled_fn(); }
+bool mqa::api_test_hooks() { return test_hooks_enabled(); }
 int mqa::api_sm_count() {
     // a property of the device: looked up once for each
     constexpr int kDevices = 64;

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "../../include/mqa_decode_testing.h"
 #include "api_common.cuh"
 #include "gqa_win.cuh"
 
@@ -63,7 +64,9 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
                   const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window, int sinks,
                   void* out, float* lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
                   int num_blocks, int page_size, int max_blocks, int scale_block, mqa_kv_dtype kv_dtype,
-                  int num_kv_splits, void* workspace, size_t workspace_bytes, int* device_status, void* stream) {
+                  int num_kv_splits, void* workspace, size_t workspace_bytes, int* device_status, void* stream,
+                  int withhold = -1) {
+    // withhold >= 0 only from the test hook mqa_test_gqa_window_withheld
     if (!q || !kv_cache || !block_table || !seq_lens || !out) return MQA_ERR_INVALID_ARG;
     if (!api_aligned(q, 16) || !api_aligned(kv_cache, 16) || !api_aligned(out, 16) || !api_aligned(block_table, 4) ||
         !api_aligned(seq_lens, 4) || (lse && !api_aligned(lse, 4)) ||
@@ -133,6 +136,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     a.max_blocks = max_blocks;
     a.window = window < mqa::kWinNoWindow ? window : mqa::kWinNoWindow;
     a.sinks = sinks;
+    a.withhold = withhold;
     a.scale_block = block ? scale_block : 1;
     a.scale_groups = block ? page_size / scale_block : 1;
     const int vb = batch * r.rb;
@@ -204,6 +208,20 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
     return decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, 1.0f, 1.0f, mqa::kWinNoWindow, 0, out, lse,
                   batch, q_len, num_q_heads, num_kv_heads, head_size, num_blocks, page_size, max_blocks, scale_block,
                   kv_dtype, num_kv_splits, workspace, workspace_bytes, device_status, stream);
+}
+
+mqa_status mqa_test_gqa_window_withheld(const void* q, const void* kv_cache, const float* kv_scales,
+                                        const int32_t* block_table, const int32_t* seq_lens, float scale, int window,
+                                        int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,
+                                        int num_kv_heads, int head_size, int num_blocks, int page_size,
+                                        int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits,
+                                        void* workspace, size_t workspace_bytes, int* device_status, void* stream,
+                                        int withhold_unit) {
+    if (!mqa::api_test_hooks()) return MQA_ERR_UNSUPPORTED;
+    if (withhold_unit < 0) return MQA_ERR_INVALID_ARG;
+    return decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, 1.0f, 1.0f, window, sinks, out, lse, batch,
+                  q_len, num_q_heads, num_kv_heads, head_size, num_blocks, page_size, max_blocks, scale_block,
+                  kv_dtype, num_kv_splits, workspace, workspace_bytes, device_status, stream, withhold_unit);
 }
 
 }  // extern "C"

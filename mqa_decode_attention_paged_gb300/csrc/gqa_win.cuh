@@ -47,6 +47,7 @@ struct WinArgs {
     int ts, tt;                     // warps that share a KV head; tokens of a tile (all of them)
     int units;                      // 0: one unit per virtual request, else the balanced unit count
     int nslots;                     // slots of a warp's ring
+    int withhold;  // test hook of the bounded waits: this unit copies nothing (-1 in every product call)
 };
 
 // The tiles of one virtual request.

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             describe(first + lane);
             fetch_id(first + 32 + lane);
         }
-        if (lane < nb) {
+        if (lane < nb && static_cast<int>(blockIdx.x) != a.withhold) {
             const int4 d = desc_s[(first + lane) & (kDesc - 1)];
             constexpr int kBox16 = 16 * D * C::kElt;  // bytes of 16 tokens
             const int bytes = nb == 1 ? C::kSlot : kBox16;
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         }
         for (int s = 0; s < nslots && s < issued; ++s) {
             const int fills = (issued - s + nslots - 1) / nslots;
-            mbar_wait(&full[s], (fills - 1) & 1);
+            if (!mbar_wait(&full[s], (fills - 1) & 1)) break;
         }
     }
 }

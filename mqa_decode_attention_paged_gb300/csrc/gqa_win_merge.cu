@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_con
     const int2 units = a.ws_units[v];
     const int gf = units.x, np = units.y - units.x + 1;
     if (np == 1 || kh >= a.Hkv || R >= a.rows) return;
+    // (a unit that gave up may have left this entry unwritten)
+    if (units.x < 0 || units.y < units.x || units.y >= a.units) return;
     const int i = R / a.grp;
     const long long orow = (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
     __nv_bfloat16* out = a.out + orow * D + V * lane;

@@ -316,6 +316,37 @@ def test_streams_and_graphs():
         check(case, out.cpu().double(), lse.cpu().double(), what="other stream")
 
 
+@pytest.mark.parametrize("kv,Hkv", [("bf16", 8), ("int8_block", 2), ("fp8_e4m3_block", 1)])
+def test_a_wait_that_runs_out_is_reported(kv, Hkv, monkeypatch):
+    # one unit copies nothing: its bounded waits (2 s) run out, every block returns (also where warps of a head meet
+    # to hand over their sums, and where requests are cut and merged), the status says so, and the context goes on
+    monkeypatch.setenv("MQA_ENABLE_TEST_HOOKS", "1")
+    import ctypes
+    from mqa_decode_attention_paged_gb300 import _binding as binding
+    P, I, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    fn = binding.lib.mqa_test_gqa_window_withheld
+    fn.restype = I
+    fn.argtypes = [P, P, P, P, P, F, I, I, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P, I]
+    case = Case([900, 300, 40], 4 * Hkv, Hkv, 64, 16, kv, window=700, sinks=4, seed=16, poison=False)
+    q, cache, bt, sc, sl = case.dev()
+    B, L, Hq, D = q.shape
+    code = binding._KV_NAMES[kv]
+    for splits in (1, 3):
+        out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:3], float("nan"), device="cuda")
+        ws = torch.full((max(16, mqa.gqa_window_decode_workspace_bytes(B, L, Hq, Hkv, D, splits)),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        rc = fn(q.data_ptr(), cache.data_ptr(), None if sc is None else sc.data_ptr(), bt.data_ptr(), sl.data_ptr(),
+                case.scale, 700, 4, out.data_ptr(), lse.data_ptr(), B, L, Hq, Hkv, D, case.nb, 16, bt.shape[1], 16,
+                code, splits, ws.data_ptr(), ws.numel(), status.data_ptr(), torch.cuda.current_stream().cuda_stream, 0)
+        assert rc == binding.OK
+        torch.cuda.synchronize()
+        assert int(status.item()) == binding.ERR_DEVICE_TIMEOUT
+        if splits == 1:
+            check(case, out.cpu().double(), lse.cpu().double(), rows=[1, 2])
+    run_and_check(case, (1, None))
+
+
 def test_two_calls_at_once():
     cases = [Case([400, 90, 33], 32, 8, 128, 16, kv, window=100, sinks=4, seed=14) for kv in ("bf16", "int8_block")]
     devs = [c.dev() for c in cases]
