@@ -108,7 +108,12 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
                                                               : mqa::kWinE4m3;
     const int warp_tok = 16 * mqa::win_mblocks(kind, r.rbn <= 8 ? 1 : 2);
     a.ts = mqa::win_subtiles(num_kv_heads);
-    a.tt = warp_tok * a.ts;
+    a.tt_log = 0;
+    while ((1 << a.tt_log) < warp_tok * a.ts) ++a.tt_log;  // (both are powers of two)
+    a.page_div = mqa::FastDiv::of(page_size);
+    a.scale_div = mqa::FastDiv::of(block ? scale_block : 1);
+    a.grp_div = mqa::FastDiv::of(r.grp);
+    a.rb_div = mqa::FastDiv::of(r.rb);
     a.box_tok = page_size % warp_tok == 0 ? warp_tok : 16;  // a box lies in one page
     if (!cache_map(&a.tmap, kv_cache, elt, head_size, num_kv_heads,
                    2LL * num_blocks * page_size, a.box_tok))

@@ -24,6 +24,21 @@ enum WinKind { kWinBf16 = 0, kWinE4m3 = 1, kWinInt8 = 2 };
 constexpr int kWinMaxVirtual = 2048;  // virtual requests whose tile prefix fits in shared memory
 constexpr int kWinNoWindow = 1 << 30;
 
+// Exact division of 0 <= n < 2^31 by a divisor known on the host: with l =
+// ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(m, n) + n)
+// >> l (Granlund and Montgomery, "Division by invariant integers").
+struct FastDiv {
+    uint32_t m, l;
+    static FastDiv of(int d) {
+        uint32_t l = 0;
+        while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
+        return {static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - static_cast<uint64_t>(d))) / static_cast<uint64_t>(d) + 1), l};
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return static_cast<int>((__umulhi(m, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> l);
+    }
+};
+
 struct WinArgs {
     CUtensorMap tmap;  // {line, rows (block, plane, token), panels, heads}
     const __nv_bfloat16* q;   // [batch, q_len, Hq, D]
@@ -44,7 +59,8 @@ struct WinArgs {
     int scale_block, scale_groups;  // tokens per scale, scales per page
     int box_tok;                    // tokens of one copied box (divides the page and a warp's tile)
     int rb, rbn;                    // row blocks per request; rows of a (full) row block
-    int ts, tt;                     // warps that share a KV head; tokens of a tile (all of them)
+    int ts, tt_log;                 // warps that share a KV head; log2 of a tile's tokens (all of them)
+    FastDiv page_div, scale_div, grp_div, rb_div;
     int units;                      // 0: one unit per virtual request, else the balanced unit count
     int nslots;                     // slots of a warp's ring
     int withhold;  // test hook of the bounded waits: this unit copies nothing (-1 in every product call)
@@ -73,17 +89,17 @@ __device__ __forceinline__ int win_len(const WinArgs& a, int b, int* status) {
 __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
     WinVis v;
     const int r0 = r * 16, r1 = min(a.rows, r0 + 16) - 1;
-    const int i0 = a.q_len == 1 ? 0 : r0 / a.grp, i1 = a.q_len == 1 ? 0 : r1 / a.grp;
-    const int tt = a.tt;
+    const int i0 = a.q_len == 1 ? 0 : a.grp_div(r0), i1 = a.q_len == 1 ? 0 : a.grp_div(r1);
+    const int tl = a.tt_log, up = (1 << tl) - 1;
     v.n = n;
     v.p_first = n - a.q_len + i0;
     v.p_last = n - a.q_len + i1;
     v.hi = max(0, v.p_last + 1);
     v.lo = max(0, v.p_first - a.window + 1);
     const int s_end = min(a.sinks, v.hi);
-    v.ns = (s_end + tt - 1) / tt;
-    v.w0 = max(v.lo / tt, v.ns);
-    v.nt = v.ns + max(0, (v.hi + tt - 1) / tt - v.w0);
+    v.ns = (s_end + up) >> tl;
+    v.w0 = max(v.lo >> tl, v.ns);
+    v.nt = v.ns + max(0, ((v.hi + up) >> tl) - v.w0);
     return v;
 }
 
@@ -97,13 +113,15 @@ __device__ __forceinline__ int win_units(int units, int vb, int T, int longest) 
     return vb <= units && longest <= T / U + 2 ? 0 : U;
 }
 
-// First tile of unit g of U: g T / U, moved to a request's start or end where
-// one lies a tile away and units hold four tiles at least: a cut costs a
-// merge and a start, about a tile's time, so nothing further is worth the
-// imbalance.  Non-decreasing in g.
+// First tile of unit g of U (shares of T / U tiles, the first T % U of them one
+// more), moved to a request's start or end where one lies a tile away and
+// units hold four tiles at least: a cut costs a merge and a start, about a
+// tile's time, so nothing further is worth the imbalance.  Non-decreasing in
+// g.
 __device__ __forceinline__ int win_unit_start(const int* cum, int vb, int T, int U, int g) {
     if (g >= U) return T;
-    const int x = static_cast<int>(static_cast<long long>(g) * T / U);
+    const int share = T / U;
+    const int x = g * share + min(g, T - share * U);
     int lo = 0, hi = vb - 1;  // the last virtual request starting at or before x
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -112,7 +130,7 @@ __device__ __forceinline__ int win_unit_start(const int* cum, int vb, int T, int
         else
             hi = mid - 1;
     }
-    const int near = T / U >= 4 ? 1 : 0;
+    const int near = share >= 4 ? 1 : 0;
     if (x - cum[lo] <= near) return cum[lo];
     return cum[lo + 1] - x <= near ? cum[lo + 1] : x;
 }

@@ -55,7 +55,8 @@ namespace mqa {
 namespace win {
 
 constexpr int kMaxSlots = 4;
-constexpr int kDesc = 64;   // box descriptions kept per warp: the chunk being copied and the one before
+constexpr int kChunk = 16;  // boxes described together
+constexpr int kDesc = 64;   // box descriptions kept per warp: at most three chunks are in use
 constexpr int kMeet = 8;    // tiles between meetings of a block's warps
 constexpr float kNone = -3e38f;  // reference before the first logit
 
@@ -213,7 +214,7 @@ static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) { 
 __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* lens) {
     const int vb = a.batch * a.rb;
     for (int v = threadIdx.x; v < vb; v += blockDim.x) {
-        const int b = a.rb == 1 ? v : v / a.rb, r = v - b * a.rb;
+        const int b = a.rb == 1 ? v : a.rb_div(v), r = v - b * a.rb;
         const int n = win_len(a, b, a.status);
         if (r == 0) lens[b] = n;
         cum[v + 1] = win_visible(a, r, n).nt;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     // virtual requests without a key: out = 0, lse = -inf
     for (int v = blockIdx.x; v < vb; v += gridDim.x) {
         if (cum[v + 1] > cum[v]) continue;
-        const int b = v / a.rb, r0 = (v - b * a.rb) * 16, rows = min(a.rows - r0, 16);
+        const int b = a.rb_div(v), r0 = (v - b * a.rb) * 16, rows = min(a.rows - r0, 16);
         for (int i = threadIdx.x; i < Hkv * rows * (D / 8); i += blockDim.x) {
             const int h = i / (rows * (D / 8)), R = r0 + i / (D / 8) % rows, qi = R / a.grp;
             const long long orow = (static_cast<long long>(b) * a.q_len + qi) * a.Hq + h * a.grp + R - qi * a.grp;
@@ -305,71 +306,77 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         if (a.units > 0 && threadIdx.x == 0) a.ws_units[v] = make_int2(0, 0);
     }
 
-    // ---- copying.  Boxes are described 32 at a time, a lane each (across
-    // requests), in shared memory for the copies and for the reader; the block
-    // ids of the next 32 are fetched meanwhile.
+    // ---- copying.  Boxes are described kChunk at a time, a lane each (across
+    // requests), in shared memory for the copies and for the reader: locate()
+    // writes all but the block ids, and fetches those; complete() puts them in
+    // when the chunk's turn comes, a chunk later.
     const int boxes = (p1 - p0) * nb;
-    int next_id = -1;
-    // Box i of this block's run: where it lies; false where no row sees a key of it.
-    auto locate = [&](int i, int4& d) {
-        const int P = p0 + i / nb;
-        int lo = 0, hi = vb - 1;  // the last virtual request starting at or before P
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= P)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const int b = a.rb == 1 ? lo : lo / a.rb;
-        const WinVis vis = win_visible(a, lo - b * a.rb, lens[b]);
-        const int c0 = cum[lo], c1 = cum[lo + 1];
-        d.x = vis.tile(P - c0) * a.tt + sub * C::kTok + i % nb * a.box_tok;
-        d.z = lo | (P == max(c0, p0) ? kFirst : 0) | (P + 1 == min(c1, p1) ? kLast : 0) |
-              (c0 >= p0 && c1 <= p1 ? kWhole : 0);
-        d.y = b;
-        // only boxes with a visible key are read, and only their block ids
-        return d.x < vis.hi && (d.x + a.box_tok > vis.lo || d.x < min(a.sinks, vis.hi));
-    };
-    auto fetch_id = [&](int i) {
-        int4 d;
-        next_id = -1;
-        if (i < boxes && locate(i, d)) {
-            next_id = __ldg(a.block_table + static_cast<long long>(d.y) * a.max_blocks + d.x / a.page);
-            if (next_id < 0 || next_id >= a.num_blocks) next_id = -2;
-        }
-    };
-    auto describe = [&](int i) {  // box i, whose id has been fetched
-        int4 d = make_int4(0, -1, 0, 0);
-        if (i < boxes) {
-            locate(i, d);
-            if (next_id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
-            const int v = d.z & 0xffff, b = d.y, in_page = d.x % a.page;
-            d.y = next_id < 0 ? -1 : next_id * 2 * a.page + in_page;
-            if (scaled) {
-                d.w = (next_id * 2 * a.scale_groups + in_page / a.scale_block) * Hkv + kh;
-                if ((in_page + 16) / a.scale_block != in_page / a.scale_block) d.z |= kNextScale;
+    int located = 0, completed = 0;  // boxes
+    int id = -1;                     // block id of box located - kChunk + lane; -2: not a block
+    auto locate = [&]() {
+        const int i = located + lane;
+        int4 d = make_int4(0, 0, 0, 0);
+        id = -1;
+        if (lane < kChunk && i < boxes) {
+            const int P = p0 + (nb == 1 ? i : i >> 1);
+            int lo = 0, hi = vb - 1;  // the last virtual request starting at or before P
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cum[mid] <= P)
+                    lo = mid;
+                else
+                    hi = mid - 1;
             }
-            const WinVis vis = win_visible(a, a.rb == 1 ? 0 : v - b * a.rb, lens[b]);
-            for (int m = 0; m < a.box_tok / 16; ++m) {
+            const int b = a.rb == 1 ? lo : a.rb_div(lo);
+            const WinVis vis = win_visible(a, lo - b * a.rb, lens[b]);
+            const int c0 = cum[lo], c1 = cum[lo + 1];
+            d.x = (vis.tile(P - c0) << a.tt_log) + sub * C::kTok + (nb == 1 ? 0 : i & 1) * 16;
+            d.z = lo | (P == max(c0, p0) ? kFirst : 0) | (P + 1 == min(c1, p1) ? kLast : 0) |
+                  (c0 >= p0 && c1 <= p1 ? kWhole : 0);
+            const int page = a.page_div(d.x);
+            d.y = d.x - page * a.page;
+            for (int m = 0; m < (nb == 1 ? MT : 1); ++m) {
                 const int t = d.x + 16 * m, bit = nb == 1 ? m : i & 1;
-                const bool act = d.y >= 0 && t <= vis.p_last && (t + 15 > vis.p_first - a.window || t < a.sinks);
+                const bool act = t <= vis.p_last && (t + 15 > vis.p_first - a.window || t < a.sinks);
                 const bool edge = !act || t + 15 > vis.p_first || (t + 15 >= a.sinks && t <= vis.p_last - a.window);
                 d.z |= (act ? kAct << bit : 0) | (edge ? kEdge << bit : 0);
             }
+            if (scaled) {
+                d.w = a.scale_div(d.y);
+                if (MT == 2 && nb == 1 && a.scale_div(d.y + 16) != d.w) d.z |= kNextScale;
+            }
+            // only boxes with a visible key are read, and only their block ids
+            if (d.z & (3 * kAct)) {
+                id = __ldg(a.block_table + static_cast<long long>(b) * a.max_blocks + page);
+                if (id < 0 || id >= a.num_blocks) id = -2;
+            }
+        }
+        if (lane < kChunk && i < boxes) desc_s[i & (kDesc - 1)] = d;
+        located += kChunk;
+    };
+    auto complete = [&]() {
+        const int i = completed + lane;
+        int4 d = make_int4(0, -1, 0, 0);
+        if (lane < kChunk && i < boxes) {
+            d = desc_s[i & (kDesc - 1)];
+            if (id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
+            if (id < 0) {  // nothing to read: no block of it counts
+                if (d.z & (3 * kAct)) d.z = (d.z & ~(3 * kAct)) | ((d.z & (3 * kAct)) / kAct * kEdge);
+                d.y = -1;
+            } else {
+                d.y += id * 2 * a.page;
+                d.w = (id * 2 * a.scale_groups + d.w) * Hkv + kh;
+            }
         }
         if (nb == 2) d.z |= __shfl_xor_sync(0xffffffffu, d.z, 1) & (3 * kAct | 3 * kEdge);
-        if (i < boxes) desc_s[i & (kDesc - 1)] = d;
+        if (lane < kChunk && i < boxes) desc_s[i & (kDesc - 1)] = d;
         __syncwarp();
+        completed += kChunk;
     };
     const int loads = 2 * (p1 - p0);  // planes to copy: K, V, K, V ..
     int issued = 0, i_slot = 0;
     auto issue = [&]() {
         const int first = (issued >> 1) * nb, plane = issued & 1;
-        if (plane == 0 && (first & 31) == 0) {
-            describe(first + lane);
-            fetch_id(first + 32 + lane);
-        }
         if (lane < nb && static_cast<int>(blockIdx.x) != a.withhold) {
             const int4 d = desc_s[(first + lane) & (kDesc - 1)];
             constexpr int kBox16 = 16 * D * C::kElt;  // bytes of 16 tokens
@@ -393,8 +400,6 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         ++issued;
         if (++i_slot == nslots) i_slot = 0;
     };
-    fetch_id(lane);
-    for (int s = 0; s < nslots && issued < loads; ++s) issue();
 
     // ---- reading
     const int g = lane >> 2, c = lane & 3;
@@ -439,23 +444,32 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     int p_first = 0, p_last = 0;  // positions of the row block's first and last row
     int r_first = 0;              // rows of the first row's position before it
     // position of row jr of the row block (rows behind the last have its position)
-    auto row_position = [&](int jr) { return MULTI ? min(p_first + (r_first + jr) / a.grp, p_last) : p_last; };
+    auto row_position = [&](int jr) { return MULTI ? min(p_first + a.grp_div(r_first + jr), p_last) : p_last; };
     uint32_t qb[NHB == 1 ? C::kSteps : 1][2];
     float o[NHB][C::kSteps][4];
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
 
     for (; tile < tiles; ++tile) {
+        // boxes are complete two tiles ahead, which is how far copies run
+        // ahead of the reader (the first time round: locate, complete, start)
+        if (tile == 0) locate();
+        if (completed < min(boxes, (tile + 3) * nb)) {
+            complete();
+            locate();
+        }
+        if (tile == 0)
+            for (int s = 0; s < nslots && issued < loads; ++s) issue();
         if ((tile & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
         const int4 d = desc_s[(tile * nb) & (kDesc - 1)];
         const int t0 = d.x;
 
         if (d.z & kFirst) {
-            const int v = d.z & 0xffff, b = a.rb == 1 ? v : v / a.rb;
+            const int v = d.z & 0xffff, b = a.rb == 1 ? v : a.rb_div(v);
             const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
             n = lens[b];
-            p_first = MULTI ? n - a.q_len + row0 / a.grp : n - 1;
-            r_first = MULTI ? row0 % a.grp : 0;
-            p_last = MULTI ? n - a.q_len + (min(a.rows, row0 + 16) - 1) / a.grp : n - 1;
+            p_first = MULTI ? n - a.q_len + a.grp_div(row0) : n - 1;
+            r_first = MULTI ? row0 - a.grp_div(row0) * a.grp : 0;
+            p_last = MULTI ? n - a.q_len + a.grp_div(min(a.rows, row0 + 16) - 1) : n - 1;
             if (a.units > 0 && threadIdx.x == 0) {
                 // every request's first and last unit, for the merge
                 int2* u = a.ws_units + v;
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                 // Q^T operand (row g): bf16, or f16 in the order of the codes' words
                 uint32_t w[C::kSteps][2];
                 const int R = row0 + hb * 8 + g;
-                const int i = MULTI ? R / a.grp : 0;
+                const int i = MULTI ? a.grp_div(R) : 0;
                 const bool have = R < a.rows;
                 const __nv_bfloat16* qr =
                     a.q + ((static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp)) * D;
@@ -825,7 +839,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         }
 
         // ---- epilogue: rows hb * 8 + 2c + e; head dims by kind (see the top)
-        const int v = d.z & 0xffff, b = a.rb == 1 ? v : v / a.rb;
+        const int v = d.z & 0xffff, b = a.rb == 1 ? v : a.rb_div(v);
         const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
 #pragma unroll
         for (int hb = 0; hb < NHB; ++hb)
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                     f = a.out_scale * (r_ref[hb][e] == -INFINITY ? 0.f : ex2(r_ref[hb][e] - m_ref[hb][e])) / l;
                 const float lse = l != 0.f ? (m_ref[hb][e] + log2f(l)) * kLn2 : -INFINITY;
                 if (d.z & kWhole) {
-                    const int i = MULTI ? R / a.grp : 0;
+                    const int i = MULTI ? a.grp_div(R) : 0;
                     const long long orow =
                         (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
                     __nv_bfloat16* op = a.out + orow * D;
@@ -880,9 +894,11 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         report(a.status, MQA_ERR_DEVICE_TIMEOUT);
         for (int t = tile; t < tiles; ++t) {
             if (t > tile && (t & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
-            int4 d;
-            locate(t * nb, d);
-            if (d.z & kLast)
+            if (completed < min(boxes, (t + 3) * nb)) {
+                complete();
+                locate();
+            }
+            if (desc_s[(t * nb) & (kDesc - 1)].z & kLast)
                 for (int half = TS / 2; half >= 1; half >>= 1)
                     for (int part = 0; part < 2 * kParts; ++part) named_bar_sync(1, 32 * NC);
         }

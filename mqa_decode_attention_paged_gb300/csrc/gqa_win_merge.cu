@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_con
     __shared__ float part[WPR == 1 ? 1 : kWarps][D + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v = blockIdx.x;
-    const int b = v / a.rb, r = v - b * a.rb;
+    const int b = a.rb_div(v), r = v - b * a.rb;
     const int item = WPR == 1 ? static_cast<int>(blockIdx.y) * kWarps + warp : static_cast<int>(blockIdx.y);
     const int kh = item / a.rbn, jr = item - kh * a.rbn;
     const int R = r * 16 + jr;
@@ -45,12 +45,28 @@ __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_con
     if (np == 1 || kh >= a.Hkv || R >= a.rows) return;
     // (a unit that gave up may have left this entry unwritten)
     if (units.x < 0 || units.y < units.x || units.y >= a.units) return;
-    const int i = R / a.grp;
+    const int i = a.grp_div(R);
     const long long orow = (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);
     __nv_bfloat16* out = a.out + orow * D + V * lane;
 
     const long long step = static_cast<long long>(a.Hkv) * a.rbn;  // rows per slot
     const long long first = (static_cast<long long>(gf + v) * a.Hkv + kh) * a.rbn + jr;
+    // the first partials' loads are in flight before their weights are known
+    float x[kInFlight][V], ls[kInFlight];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int s = s0 + u * WPR;
+            ls[u] = -INFINITY;
+            if (s < np) {
+                ls[u] = a.ws_lse[first + s * step];
+                *reinterpret_cast<VecT*>(x[u]) =
+                    __ldcs(reinterpret_cast<const VecT*>(a.ws_o + (first + s * step) * D + V * lane));
+            }
+        }
+    };
+    const int start = WPR == 1 ? 0 : warp;
+    load(start);
     float m = -INFINITY;
     for (int s = lane; s < np; s += 32) m = fmaxf(m, a.ws_lse[first + s * step]);
 #pragma unroll
@@ -59,26 +75,15 @@ __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_con
 
     float acc[V] = {};
     float wsum = 0.f;
-    constexpr int kStep = WPR;
-    for (int s0 = WPR == 1 ? 0 : warp; s0 < np; s0 += kInFlight * kStep) {
-        float x[kInFlight][V];
-        float w[kInFlight];
+    for (int s0 = start; s0 < np; s0 += kInFlight * WPR) {
+        if (s0 > start) load(s0);
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int s = s0 + u * kStep;
-            w[u] = 0.f;
-            if (s < np) {
-                w[u] = __expf(a.ws_lse[first + s * step] - mu);
-                *reinterpret_cast<VecT*>(x[u]) =
-                    __ldcs(reinterpret_cast<const VecT*>(a.ws_o + (first + s * step) * D + V * lane));
-            }
-        }
+            const float w = __expf(ls[u] - mu);
+            wsum += w;
+            if (w != 0.f)
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            wsum += w[u];
-            if (w[u] != 0.f)
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] += w[u] * x[u][k];
+                for (int k = 0; k < V; ++k) acc[k] += w * x[u][k];
         }
     }
     if (WPR > 1) {
