@@ -17,10 +17,18 @@
 // tokens is free of bank conflicts and nothing is padded), and refills a slot
 // as soon as it has read it.  There is no producer warp (whose registers
 // would cost every thread 32) and no barrier between warps but a meeting
-// every kMeet tiles, which keeps the heads of a token row together: a probe
-// that only copies reads 6.9 TB/s with such per-head boxes and three 2 KB
-// slots, but 3.9 TB/s where six slots let the warps drift apart.  Block ids
-// are fetched 16 or 32 tiles at a time, one lane per tile, across requests.
+// every kMeet tiles, so that the heads of a token row are read near each other:
+// a probe that only copies reads 6.9 TB/s with such per-head boxes and three
+// 2 KB slots, but 3.9 TB/s where six slots let the warps drift apart (in this
+// kernel 1, 2, 8 and 64 tiles between meetings are within 3 % of each other).
+// Boxes are described 16 at a time, a lane each, across requests.
+//
+// Measured (batch of 256, lognormal lengths, 32/8 heads x 128, 16-token pages,
+// e4m3 with a scale per page and head): 262 us, 6.3 TB/s of the 6.67 a copy
+// reaches; 64 windows of 16384 tokens over bf16: 661 us, 6.5 TB/s.  Short
+// windows are bound by the start (5 us until the first copies are issued) and
+// the merge; 9 to 16 rows per KV head by instructions (about 730 per 16 tokens
+// and head).
 //   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows),
 //     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.  With two
 //     groups Q lies in shared memory instead of registers.
@@ -29,19 +37,18 @@
 //     same order.  V: ldmatrix.trans over byte pairs gives a lane two head dims
 //     of two tokens; byte permutes make the two f16 pairs, so accumulator rows
 //     g and g + 8 are head dims 2g and 2g + 1.  (The warp-level e4m3 MMA is no
-//     way around the widening: with K as codes and Q in two e4m3 terms the
-//     kernel ran 507 instructions per 16 tokens and head, 399 us against
-//     ## on the batch of 256 with lognormal lengths.)
+//     way around the widening of K: with Q in two e4m3 terms it took 399 us
+//     where f16 took 342, on 256 requests of lognormal length.)
 //   * Online softmax in base 2; the reference moves only when a logit exceeds
 //     it by more than 8, which a warp vote finds without reductions.  Over
 //     8-bit caches the numerators keep a reference of their own for x +
 //     log2(s_v): the weights of P.V stay within the f16 range whatever the
 //     scales' magnitude, and V is not rescaled.
-//   * Masked keys: their logits are replaced by -inf, and V bits of keys that
-//     no row of the warp sees are cleared in registers, so stale or non-finite
-//     bytes never reach an accumulator (int8 codes are always finite).  Where
-//     a key is seen by some rows only and a V value is Inf or NaN, the rows
-//     are summed apart.
+//   * Masked keys: their logits are replaced by -inf, and at the edges of what
+//     the rows see V rows of keys that none sees are cleared in the slot, so
+//     stale or non-finite bytes never reach an accumulator (int8 codes are
+//     always finite).  Where a key is seen by some rows only and a V value is
+//     Inf or NaN, the rows are summed apart.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -90,6 +97,10 @@ __host__ __device__ inline Layout layout(int hkv, int ts, int nslots, int vb, in
     l.cum = l.bars + nc * kMaxSlots * 8;
     l.total = l.cum + 4 * (vb + 2 + batch) + 1024;  // + alignment of the base
     return l;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // Box of one head from cache row `row` on.
@@ -284,7 +295,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 
     // this block's tiles [p0, p1)
     int p0, p1;
-    const int U = a.units == 0 ? 0 : win_units(a.units, vb, T, cum[vb + 1]);
+    const int U = a.units == 0 ? 0 : win_units(a, vb, T, cum[vb + 1]);
     if (U == 0) {  // a unit is a request
         p0 = cum[min(static_cast<int>(blockIdx.x), vb)];
         p1 = cum[min(static_cast<int>(blockIdx.x) + 1, vb)];
@@ -351,7 +362,15 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                 if (id < 0 || id >= a.num_blocks) id = -2;
             }
         }
-        if (lane < kChunk && i < boxes) desc_s[i & (kDesc - 1)] = d;
+        if (lane < kChunk && i < boxes) {
+            desc_s[i & (kDesc - 1)] = d;
+            if (d.z & kFirst) {  // the request's query will be wanted soon
+                const int v = d.z & 0xffff, qb0 = a.rb == 1 ? v : a.rb_div(v);
+                const char* q0 = reinterpret_cast<const char*>(
+                    a.q + (static_cast<long long>(qb0) * a.q_len * a.Hq + kh * a.grp) * D);
+                for (int o = 0; o < a.grp * D * 2; o += 128) prefetch_l2(q0 + o);
+            }
+        }
         located += kChunk;
     };
     auto complete = [&]() {
@@ -450,10 +469,10 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
 
     for (; tile < tiles; ++tile) {
-        // boxes are complete two tiles ahead, which is how far copies run
+        // boxes are complete as many tiles ahead as copies run
         // ahead of the reader (the first time round: locate, complete, start)
         if (tile == 0) locate();
-        if (completed < min(boxes, (tile + 3) * nb)) {
+        if (completed < min(boxes, (tile + kMaxSlots / 2 + 1) * nb)) {
             complete();
             locate();
         }
@@ -894,7 +913,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         report(a.status, MQA_ERR_DEVICE_TIMEOUT);
         for (int t = tile; t < tiles; ++t) {
             if (t > tile && (t & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
-            if (completed < min(boxes, (t + 3) * nb)) {
+            if (completed < min(boxes, (t + kMaxSlots / 2 + 1) * nb)) {
                 complete();
                 locate();
             }
