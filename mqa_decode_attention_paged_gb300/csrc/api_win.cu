@@ -106,7 +106,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     const mqa::WinKind kind = kv_dtype == MQA_KV_BF16         ? mqa::kWinBf16
                               : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::kWinInt8
                                                               : mqa::kWinE4m3;
-    const int warp_tok = 16 * mqa::win_mblocks(kind, r.rbn <= 8 ? 1 : 2);
+    const int warp_tok = 16 * mqa::win_mblocks(kind, r.rbn <= 8 ? 1 : 2, head_size);
     a.ts = mqa::win_subtiles(num_kv_heads);
     a.tt_log = 0;
     while ((1 << a.tt_log) < warp_tok * a.ts) ++a.tt_log;  // (both are powers of two)
@@ -114,7 +114,8 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     a.scale_div = mqa::FastDiv::of(block ? scale_block : 1);
     a.grp_div = mqa::FastDiv::of(r.grp);
     a.rb_div = mqa::FastDiv::of(r.rb);
-    a.box_tok = page_size % warp_tok == 0 ? warp_tok : 16;  // a box lies in one page
+    a.box_tok = warp_tok;  // a box lies in one page
+    while (page_size % a.box_tok != 0) a.box_tok /= 2;
     if (!cache_map(&a.tmap, kv_cache, elt, head_size, num_kv_heads,
                    2LL * num_blocks * page_size, a.box_tok))
         return api_cuda_fail(cudaErrorInvalidValue);

@@ -142,9 +142,12 @@ __device__ __forceinline__ int win_unit_start(const int* cum, int vb, int T, int
 // does not divide 8 evenly.
 __host__ __device__ inline int win_subtiles(int hkv) { return hkv == 1 ? 8 : (hkv == 2 ? 4 : (hkv <= 4 ? 2 : 1)); }
 
-// 16-token MMA blocks of a warp's tile: two over 8-bit codes with up to 8
-// rows, else one.
-__host__ __device__ constexpr int win_mblocks(int kind, int nhb) { return kind != kWinBf16 && nhb == 1 ? 2 : 1; }
+// 16-token MMA blocks of a warp's tile, as many as the registers carry beside
+// the accumulators: with head size 128 two over 8-bit codes with up to 8 rows
+// (one row group), else one; with head size 64 twice as many.
+__host__ __device__ constexpr int win_mblocks(int kind, int nhb, int D) {
+    return (kind != kWinBf16 && nhb == 1 ? 2 : 1) * (128 / D);
+}
 
 cudaError_t win_stage1_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream);

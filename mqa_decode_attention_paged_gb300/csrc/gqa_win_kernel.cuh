@@ -73,7 +73,7 @@ struct Cfg {
     static constexpr int kLine = D * kElt >= 128 ? 128 : D * kElt;  // bytes of one swizzled line
     static constexpr int kPanels = D * kElt / kLine;
     static constexpr int kSteps = D / 16;
-    static constexpr int kMT = win_mblocks(KIND, NHB);
+    static constexpr int kMT = win_mblocks(KIND, NHB, D);
     static constexpr int kTok = 16 * kMT;            // tokens of a warp's tile
     static constexpr int kSlot = kTok * D * kElt;    // bytes of a slot (one plane of it)
     static constexpr int kQBytes = NHB == 1 ? 0 : 16 * D * 2;  // a warp's Q
@@ -92,7 +92,7 @@ __host__ __device__ inline Layout layout(int hkv, int ts, int nslots, int vb, in
     l.q = nc * nslots * C::kSlot;
     l.exch = l.q + nc * C::kQBytes;
     l.scales = l.exch + (ts > 1 ? nc / 2 * C::kExch : 0);
-    l.desc = l.scales + nc * kMaxSlots * 8;
+    l.desc = l.scales + nc * kMaxSlots * 16;
     l.bars = l.desc + nc * kDesc * 16;
     l.cum = l.bars + nc * kMaxSlots * 8;
     l.total = l.cum + 4 * (vb + 2 + batch) + 1024;  // + alignment of the base
@@ -256,11 +256,12 @@ __device__ __forceinline__ int build_prefix(const WinArgs& a, int* cum, int* len
 // A box of tokens: x first token, y its row of the K plane (-1: nothing to
 // copy; the V plane is a page of rows further), z the virtual request and the
 // flags below, w the index of its first K scale.
-constexpr int kFirst = 1 << 16, kLast = 1 << 17, kWhole = 1 << 18;  // of the tile in the unit's run of its request
-constexpr int kNextScale = 1 << 19;  // the box's second 16 tokens have the next scale
-// of the tile's two 16-token blocks: holds a key that the rows see, and one
-// that some row does not see
-constexpr int kAct = 1 << 20, kEdge = 1 << 22;
+constexpr int kVMask = kWinMaxVirtual - 1;
+constexpr int kFirst = 1 << 11, kLast = 1 << 12, kWhole = 1 << 13;  // of the tile in the unit's run of its request
+// of the tile's 16-token blocks (up to four): holds a key that the rows see,
+// and one that some row does not see
+constexpr int kAct = 1 << 14, kEdge = 1 << 18, kBlocks = 15;
+constexpr int kSteps2 = 22;  // bits 22 + 2j: scales from the box's first to that of its 16 tokens number j + 1
 
 // MULTI: more than one query position per request.
 template <int D, int KIND, int NHB, bool MULTI>
@@ -278,10 +279,11 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     const int sub = warp / Hkv, kh = warp - sub * Hkv;
     const bool scaled = KIND != kWinBf16 && a.kv_scales != nullptr;
     const uint32_t ring = smem_u32(smem) + warp * nslots * C::kSlot;
-    float* scale_s = reinterpret_cast<float*>(smem + lay.scales) + warp * kMaxSlots * 2;  // [slot][MMA block]
+    float* scale_s = reinterpret_cast<float*>(smem + lay.scales) + warp * kMaxSlots * 4;  // [slot][MMA block]
     int4* desc_s = reinterpret_cast<int4*>(smem + lay.desc) + warp * kDesc;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars) + warp * kMaxSlots;
-    const int nb = C::kTok / a.box_tok;  // boxes of a warp's tile (1 or 2)
+    const int nb = C::kTok / a.box_tok;  // boxes of a warp's tile (1, 2 or 4)
+    const int nb_log = nb >> 1;
 
     if (lane == 0) {
         if (warp == 0) prefetch_tmap(&a.tmap);
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         int4 d = make_int4(0, 0, 0, 0);
         id = -1;
         if (lane < kChunk && i < boxes) {
-            const int P = p0 + (nb == 1 ? i : i >> 1);
+            const int P = p0 + (i >> nb_log), k = i & (nb - 1);  // tile, box of it
             int lo = 0, hi = vb - 1;  // the last virtual request starting at or before P
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -341,23 +343,21 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             const int b = a.rb == 1 ? lo : a.rb_div(lo);
             const WinVis vis = win_visible(a, lo - b * a.rb, lens[b]);
             const int c0 = cum[lo], c1 = cum[lo + 1];
-            d.x = (vis.tile(P - c0) << a.tt_log) + sub * C::kTok + (nb == 1 ? 0 : i & 1) * 16;
+            d.x = (vis.tile(P - c0) << a.tt_log) + sub * C::kTok + k * a.box_tok;
             d.z = lo | (P == max(c0, p0) ? kFirst : 0) | (P + 1 == min(c1, p1) ? kLast : 0) |
                   (c0 >= p0 && c1 <= p1 ? kWhole : 0);
             const int page = a.page_div(d.x);
             d.y = d.x - page * a.page;
-            for (int m = 0; m < (nb == 1 ? MT : 1); ++m) {
-                const int t = d.x + 16 * m, bit = nb == 1 ? m : i & 1;
+            if (scaled) d.w = a.scale_div(d.y);
+            for (int m = 0; m < a.box_tok / 16; ++m) {
+                const int t = d.x + 16 * m, bit = k * (a.box_tok / 16) + m;
                 const bool act = t <= vis.p_last && (t + 15 > vis.p_first - a.window || t < a.sinks);
                 const bool edge = !act || t + 15 > vis.p_first || (t + 15 >= a.sinks && t <= vis.p_last - a.window);
                 d.z |= (act ? kAct << bit : 0) | (edge ? kEdge << bit : 0);
-            }
-            if (scaled) {
-                d.w = a.scale_div(d.y);
-                if (MT == 2 && nb == 1 && a.scale_div(d.y + 16) != d.w) d.z |= kNextScale;
+                if (scaled && m > 0) d.z |= (a.scale_div(d.y + 16 * m) - d.w) << (kSteps2 - 2 + 2 * m);
             }
             // only boxes with a visible key are read, and only their block ids
-            if (d.z & (3 * kAct)) {
+            if (d.z & (kBlocks * kAct)) {
                 id = __ldg(a.block_table + static_cast<long long>(b) * a.max_blocks + page);
                 if (id < 0 || id >= a.num_blocks) id = -2;
             }
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         if (lane < kChunk && i < boxes) {
             desc_s[i & (kDesc - 1)] = d;
             if (d.z & kFirst) {  // the request's query will be wanted soon
-                const int v = d.z & 0xffff, qb0 = a.rb == 1 ? v : a.rb_div(v);
+                const int v = d.z & kVMask, qb0 = a.rb == 1 ? v : a.rb_div(v);
                 const char* q0 = reinterpret_cast<const char*>(
                     a.q + (static_cast<long long>(qb0) * a.q_len * a.Hq + kh * a.grp) * D);
                 for (int o = 0; o < a.grp * D * 2; o += 128) prefetch_l2(q0 + o);
@@ -380,14 +380,16 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             d = desc_s[i & (kDesc - 1)];
             if (id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
             if (id < 0) {  // nothing to read: no block of it counts
-                if (d.z & (3 * kAct)) d.z = (d.z & ~(3 * kAct)) | ((d.z & (3 * kAct)) / kAct * kEdge);
+                d.z = (d.z & ~(kBlocks * kAct)) | ((d.z & (kBlocks * kAct)) / kAct * kEdge);
                 d.y = -1;
             } else {
                 d.y += id * 2 * a.page;
                 d.w = (id * 2 * a.scale_groups + d.w) * Hkv + kh;
             }
         }
-        if (nb == 2) d.z |= __shfl_xor_sync(0xffffffffu, d.z, 1) & (3 * kAct | 3 * kEdge);
+        // every box of a tile carries the flags of all its blocks
+        for (int s = 1; s < nb; s <<= 1)
+            d.z |= __shfl_xor_sync(0xffffffffu, d.z, s) & (kBlocks * kAct | kBlocks * kEdge);
         if (lane < kChunk && i < boxes) desc_s[i & (kDesc - 1)] = d;
         __syncwarp();
         completed += kChunk;
@@ -398,17 +400,19 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         const int first = (issued >> 1) * nb, plane = issued & 1;
         if (lane < nb && static_cast<int>(blockIdx.x) != a.withhold) {
             const int4 d = desc_s[(first + lane) & (kDesc - 1)];
-            constexpr int kBox16 = 16 * D * C::kElt;  // bytes of 16 tokens
-            const int bytes = nb == 1 ? C::kSlot : kBox16;
+            const int bytes = C::kSlot >> nb_log;
             if (d.y >= 0) {
                 mbar_arrive_expect_tx(&full[i_slot], bytes);
-                tma_load_rows(ring + i_slot * C::kSlot + lane * kBox16, &a.tmap, d.y + plane * a.page, kh,
+                tma_load_rows(ring + i_slot * C::kSlot + lane * bytes, &a.tmap, d.y + plane * a.page, kh,
                               &full[i_slot]);
                 if (scaled) {
                     const float* sp = a.kv_scales + d.w + plane * (a.scale_groups * Hkv);
-                    float* dst = scale_s + i_slot * 2 + lane;
+                    float* dst = scale_s + i_slot * 4 + (lane * MT >> nb_log);
                     cp_async_4(dst, sp);
-                    if (MT == 2 && nb == 1) cp_async_4(dst + 1, sp + (d.z & kNextScale ? Hkv : 0));
+#pragma unroll
+                    for (int m = 1; m < MT; ++m)
+                        if (16 * m < a.box_tok)
+                            cp_async_4(dst + m, sp + ((d.z >> (kSteps2 - 2 + 2 * m)) & 3) * Hkv);
                     cp_async_arrive(&full[i_slot]);
                 }
             } else {
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         const int t0 = d.x;
 
         if (d.z & kFirst) {
-            const int v = d.z & 0xffff, b = a.rb == 1 ? v : a.rb_div(v);
+            const int v = d.z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
             const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
             n = lens[b];
             p_first = MULTI ? n - a.q_len + a.grp_div(row0) : n - 1;
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             }
         }
 
-        const bool any = d.z & (3 * kAct);
+        const bool any = d.z & (kBlocks * kAct);
         float x[MT][NHB][4];  // logits of token g (rows 2c, 2c + 1) and of token g + 8
         if (!wait_full()) break;
         if (any) {
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const float ksc = scaled ? a.sl2 * scale_s[slot * 2 + m] : a.sl2;
+                const float ksc = scaled ? a.sl2 * scale_s[slot * 4 + m] : a.sl2;
 #pragma unroll
                 for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
@@ -603,8 +607,8 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         if (any) {
             float lvs[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) lvs[m] = scaled ? __log2f(scale_s[slot * 2 + m]) : 0.f;
-            if (d.z & (3 * kEdge)) {
+            for (int m = 0; m < MT; ++m) lvs[m] = scaled ? __log2f(scale_s[slot * 4 + m]) : 0.f;
+            if (d.z & (kBlocks * kEdge)) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     if (!(d.z & (kEdge << m))) continue;
@@ -858,7 +862,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         }
 
         // ---- epilogue: rows hb * 8 + 2c + e; head dims by kind (see the top)
-        const int v = d.z & 0xffff, b = a.rb == 1 ? v : a.rb_div(v);
+        const int v = d.z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
         const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
 #pragma unroll
         for (int hb = 0; hb < NHB; ++hb)
