@@ -116,6 +116,10 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -626,14 +630,13 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                     if (KIND != kWinInt8) {
                         // V rows that no row sees become zeros: whatever bytes
                         // they hold (int8 codes are finite anyway)
-                        for (int r = 0; r < 16; ++r) {
-                            const int key = t + r;
-                            if (act && key <= p_last && (key < a.sinks || key > p_first - a.window)) continue;
+                        const int r = lane >> 1, key = t + r;  // two lanes a row
+                        if (!(act && key <= p_last && (key < a.sinks || key > p_first - a.window))) {
+                            const uint32_t row = ring + slot * C::kSlot + (16 * m + r) * C::kLine + (lane & 1) * (C::kLine / 2);
 #pragma unroll
                             for (int q = 0; q < C::kPanels; ++q)
-                                if (4 * lane < C::kLine)
-                                    st_shared(ring + slot * C::kSlot + q * kPanel + (16 * m + r) * C::kLine + 4 * lane,
-                                              0u);
+#pragma unroll
+                                for (int b16 = 0; b16 < C::kLine / 2; b16 += 16) st_shared_zero16(row + q * kPanel + b16);
                         }
                     }
                 }
