@@ -467,11 +467,23 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 
     constexpr int kParts = NHB * C::kSteps / 4;  // of a warp's hand-over to another
     const int tiles = p1 - p0;
-    int tile = 0, n = 0;
-    int p_first = 0, p_last = 0;  // positions of the row block's first and last row
-    int r_first = 0;              // rows of the first row's position before it
-    // position of row jr of the row block (rows behind the last have its position)
-    auto row_position = [&](int jr) { return MULTI ? min(p_first + a.grp_div(r_first + jr), p_last) : p_last; };
+    int tile = 0;
+    // Positions of a row block's rows, worked out where they are wanted (the
+    // first tile and the edges): of the first and last row, and of row jr (rows
+    // behind the last have its position).
+    struct Rows {
+        int first, last, skip;  // skip: rows of the first row's position before it
+        __device__ __forceinline__ int at(const WinArgs& a, int jr) const {
+            return MULTI ? min(first + a.grp_div(skip + jr), last) : last;
+        }
+    };
+    auto rows_of = [&](int z) {
+        const int v = z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
+        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16, n = lens[b];
+        if (!MULTI) return Rows{n - 1, n - 1, 0};
+        const int i0 = a.grp_div(row0);
+        return Rows{n - a.q_len + i0, n - a.q_len + a.grp_div(min(a.rows, row0 + 16) - 1), row0 - i0 * a.grp};
+    };
     uint32_t qb[NHB == 1 ? C::kSteps : 1][2];
     float o[NHB][C::kSteps][4];
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
@@ -493,10 +505,6 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         if (d.z & kFirst) {
             const int v = d.z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
             const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
-            n = lens[b];
-            p_first = MULTI ? n - a.q_len + a.grp_div(row0) : n - 1;
-            r_first = MULTI ? row0 - a.grp_div(row0) * a.grp : 0;
-            p_last = MULTI ? n - a.q_len + a.grp_div(min(a.rows, row0 + 16) - 1) : n - 1;
             if (a.units > 0 && threadIdx.x == 0) {
                 // every request's first and last unit, for the merge
                 int2* u = a.ws_units + v;
@@ -613,6 +621,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 #pragma unroll
             for (int m = 0; m < MT; ++m) lvs[m] = scaled ? __log2f(scale_s[slot * 4 + m]) : 0.f;
             if (d.z & (kBlocks * kEdge)) {
+                const Rows rows = rows_of(d.z);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     if (!(d.z & (kEdge << m))) continue;
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                     for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {  // mask key by key
-                            const int key = t + g + (e >> 1) * 8, p = row_position(hb * 8 + 2 * c + (e & 1));
+                            const int key = t + g + (e >> 1) * 8, p = rows.at(a, hb * 8 + 2 * c + (e & 1));
                             if (!act || !(key <= p && (key < a.sinks || key > p - a.window)))
                                 x[m][hb][e] = -INFINITY;
                         }
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                         // V rows that no row sees become zeros: whatever bytes
                         // they hold (int8 codes are finite anyway)
                         const int r = lane >> 1, key = t + r;  // two lanes a row
-                        if (!(act && key <= p_last && (key < a.sinks || key > p_first - a.window))) {
+                        if (!(act && key <= rows.last && (key < a.sinks || key > rows.first - a.window))) {
                             const uint32_t row = ring + slot * C::kSlot + (16 * m + r) * C::kLine + (lane & 1) * (C::kLine / 2);
 #pragma unroll
                             for (int q = 0; q < C::kPanels; ++q)
@@ -747,7 +756,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                     }
                 };
                 bool apart = false;
-                if (MULTI && KIND != kWinInt8 && (d.z & (kEdge << m)) && p_first != p_last) {
+                if (MULTI && KIND != kWinInt8 && (d.z & (kEdge << m))) {
                     // some key is seen by some rows only: is any V value Inf or NaN?
 #pragma unroll
                     for (int i = 0; i < C::kPanels * kPairs; ++i) {
@@ -771,7 +780,8 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                         }
                     }
                 } else {
-                    for (int p = p_first; p <= p_last; ++p) {  // one query position at a time
+                    const Rows rows = rows_of(d.z);
+                    for (int p = rows.first; p <= rows.last; ++p) {  // one query position at a time
                         auto seen = [&](int key) { return key <= p && (key < a.sinks || key > p - a.window); };
                         const int key = t + 2 * c;  // V words hold tokens 2c, 2c + 1 (and + 8)
                         const uint2 k = make_uint2(
@@ -789,7 +799,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                                     mma<KIND>(s, av[e], pb[hb][0], pb[hb][1], true);
 #pragma unroll
                                     for (int y = 0; y < 4; ++y)
-                                        if (row_position(hb * 8 + 2 * c + (y & 1)) == p)
+                                        if (rows.at(a, hb * 8 + 2 * c + (y & 1)) == p)
                                             o[hb][2 * mb2 + e][y] += s[y];
                                 }
                         }
