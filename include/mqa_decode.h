@@ -483,8 +483,9 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
  *              not matter.  Calls that may overlap need one each.
  *   head_size in {64, 128}; num_kv_heads in [1, 8]; at most 16 query heads per
  *   KV head; q_len * num_q_heads / num_kv_heads <= 128; batch * ceil(that /
- *   16) <= 2048; page_size a multiple of 16; num_blocks * page_size < 2^30.
- *   Other arguments and errors as for mla_decode. */
+ *   16) <= 2048; page_size a multiple of 16; num_blocks * page_size < 2^30;
+ *   batch * ceil(that / 16) * (max_blocks * page_size / 16 + 2) < 2^29.  Other
+ *   arguments and errors as for mla_decode. */
 mqa_status gqa_window_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
                              const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window,
                              int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,
@@ -533,7 +534,9 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
  *                                 from s_old = 0 whatever it held.
  *              Codes saturate; scales below 2^-126 become 0 with codes 0.
  *   kv_scales, scale_block  the block formats' only (else NULL / ignored).
- *   No two requests of a call may append to the same physical block.
+ *   A call may append to a physical block through one entry of the block
+ *   table only.  Infinities and NaN among the new values make the values of
+ *   their row (of a block format: of their block, plane and head) undefined.
  *   num_tokens 0 .. 2^24; batch up to 2^20; num_kv_heads up to 8; num_q_heads
  *   up to 1024; page_size a multiple of 16.
  * A request with seq_lens[b] < its new tokens, a position without a row in

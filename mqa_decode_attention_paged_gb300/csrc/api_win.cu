@@ -94,6 +94,9 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         return MQA_ERR_UNSUPPORTED;
 
     const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
+    const int vb = batch * r.rb;
+    // the batch's tiles (16 tokens at least, an edge or two more) are counted in ints
+    if (vb * ((static_cast<long long>(max_blocks) * page_size >> 4) + 2) > INT32_MAX / 4) return MQA_ERR_UNSUPPORTED;
     const size_t need = gqa_window_decode_workspace_bytes(batch, q_len, num_q_heads, num_kv_heads, head_size,
                                                           num_kv_splits);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MQA_ERR_WORKSPACE_TOO_SMALL;
@@ -145,7 +148,6 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     a.withhold = withhold;
     a.scale_block = block ? scale_block : 1;
     a.scale_groups = block ? page_size / scale_block : 1;
-    const int vb = batch * r.rb;
     if (num_kv_splits > 1) {
         const size_t slots = static_cast<size_t>(vb) * num_kv_splits;
         a.ws_o = static_cast<float*>(workspace);

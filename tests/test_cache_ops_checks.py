@@ -40,6 +40,8 @@ INV, UNS, SMALL = mqa.ERR_INVALID_ARG, mqa.ERR_UNSUPPORTED, mqa.ERR_WORKSPACE_TO
     (dict(B=257, L=32), UNS),                      # 257 requests x 8 row blocks
     (dict(P=8), UNS), (dict(P=24), UNS), (dict(kvd=2), UNS), (dict(kvd=4), UNS), (dict(kvd=9), UNS),
     (dict(nb=1 << 27, P=16), UNS), (dict(maxb=1 << 27, P=16), UNS),
+    (dict(B=2048, maxb=1 << 18), UNS),             # 2048 x (2^18 + 2) boxes of 16 tokens
+    (dict(B=2048, maxb=(1 << 18) - 3, S=4), SMALL),  # served as far as this check goes
     (dict(kvd=5), INV), (dict(kvd=6, sc=FAKE + 2), INV), (dict(kvd=6, sc=FAKE, G=0), INV),
     (dict(kvd=6, sc=FAKE, G=24, P=48), UNS), (dict(kvd=5, sc=FAKE, G=32, P=16), UNS),
     (dict(S=4), SMALL),
