@@ -447,7 +447,8 @@ size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, 
                                          int num_kv_splits);
 
 /* The smallest num_kv_splits (at least 2) with which gqa_window_decode and
- * gqa_block_decode can spread such a batch over the whole current device; -1
+ * gqa_block_decode can spread such a batch over the whole current device,
+ * whatever the head size; -1
  * on invalid arguments or without a device. */
 int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_heads);
 

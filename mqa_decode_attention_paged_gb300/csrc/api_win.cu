@@ -109,7 +109,8 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     const mqa::WinKind kind = kv_dtype == MQA_KV_BF16         ? mqa::kWinBf16
                               : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::kWinInt8
                                                               : mqa::kWinE4m3;
-    const int warp_tok = 16 * mqa::win_mblocks(kind, r.rbn <= 8 ? 1 : 2, head_size);
+    const int nhb = r.rbn <= 8 ? 1 : 2;
+    const int warp_tok = 16 * mqa::win_mblocks(kind, nhb, head_size);
     a.ts = mqa::win_subtiles(num_kv_heads);
     a.tt_log = 0;
     while ((1 << a.tt_log) < warp_tok * a.ts) ++a.tt_log;  // (both are powers of two)
@@ -117,8 +118,8 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     a.scale_div = mqa::FastDiv::of(block ? scale_block : 1);
     a.grp_div = mqa::FastDiv::of(r.grp);
     a.rb_div = mqa::FastDiv::of(r.rb);
-    a.box_tok = warp_tok;  // a box lies in one page
-    while (page_size % a.box_tok != 0) a.box_tok /= 2;
+    a.box_tok = head_size * elt > 128 ? 16 : warp_tok;  // two panels: a box is an MMA block
+    while (page_size % a.box_tok != 0) a.box_tok /= 2;  // a box lies in one page
     if (!cache_map(&a.tmap, kv_cache, elt, head_size, num_kv_heads,
                    2LL * num_blocks * page_size, a.box_tok))
         return api_cuda_fail(cudaErrorInvalidValue);
@@ -155,7 +156,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         a.ws_units = reinterpret_cast<int2*>(a.ws_lse + (slots * num_kv_heads * r.rbn + 1) / 2 * 2);
         // unit g and virtual request v use slot g + v <= units + vb - 2
         const long long cap = static_cast<long long>(vb) * (num_kv_splits - 1) + 1;
-        const long long fill = static_cast<long long>(sms) * mqa::kWinCtasPerSm;
+        const long long fill = static_cast<long long>(sms) * mqa::win_ctas_per_sm(nhb, head_size);
         a.units = static_cast<int>(fill < cap ? fill : cap);
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -192,7 +193,7 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
     const int sms = mqa::api_sm_count();
     if (sms < 1) return -1;
     const Rows r = rows_of(q_len, num_q_heads, num_kv_heads);
-    const int vb = batch * r.rb, fill = sms * mqa::kWinCtasPerSm;
+    const int vb = batch * r.rb, fill = sms * mqa::kWinMaxCtasPerSm;
     return 1 + (fill - 1 + vb - 1) / vb;  // the smallest budget that lets units fill the device (2 at least)
 }
 

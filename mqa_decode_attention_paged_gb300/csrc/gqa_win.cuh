@@ -142,17 +142,22 @@ __device__ __forceinline__ int win_unit_start(const int* cum, int vb, int T, int
 // does not divide 8 evenly.
 __host__ __device__ inline int win_subtiles(int hkv) { return hkv == 1 ? 8 : (hkv == 2 ? 4 : (hkv <= 4 ? 2 : 1)); }
 
+// Thread blocks of stage 1 resident on one SM: one where 9 to 16 rows meet head
+// size 128 (32 windows of 4096, 16 rows, e4m3: 74 us against 92 with two; with
+// head size 64 300 windows of 128 with 12 rows take 57 us with one, 39 with two).
+__host__ __device__ constexpr int win_ctas_per_sm(int nhb, int D) { return nhb == 1 || D == 64 ? 2 : 1; }
+constexpr int kWinMaxCtasPerSm = 2;
+
 // 16-token MMA blocks of a warp's tile, as many as the registers carry beside
-// the accumulators: with head size 128 two over 8-bit codes with up to 8 rows
-// (one row group), else one; with head size 64 twice as many.
+// the accumulators.
 __host__ __device__ constexpr int win_mblocks(int kind, int nhb, int D) {
-    return (kind != kWinBf16 && nhb == 1 ? 2 : 1) * (128 / D);
+    if (D == 64) return kind != kWinBf16 && nhb == 1 ? 4 : 2;
+    return kind != kWinBf16 || nhb == 2 ? 2 : 1;
 }
 
 cudaError_t win_stage1_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_int8(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_merge(const WinArgs& a, int D, cudaStream_t stream);
-constexpr int kWinCtasPerSm = 2;  // thread blocks of stage 1 resident on one SM
 
 }  // namespace mqa

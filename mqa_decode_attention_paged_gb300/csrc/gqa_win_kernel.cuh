@@ -10,7 +10,8 @@
 // cache, the instructions that widen the codes.
 //
 // One thread block = up to 8 warps, two blocks per SM (128 registers a
-// thread).  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
+// thread), or one where 9 to 16 rows meet head size 128 (accumulators and Q
+// alone are 96 registers).  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
 // feeds itself: it keeps a ring of slots in shared memory, copies its own
 // head's K rows and then V rows of a tile into it with tensor copies (16 or 32
 // token rows of one head, 128-byte or 64-byte swizzle: ldmatrix over eight
@@ -27,11 +28,12 @@
 // e4m3 with a scale per page and head): 262 us, 6.3 TB/s of the 6.67 a copy
 // reaches; 64 windows of 16384 tokens over bf16: 661 us, 6.5 TB/s.  Short
 // windows are bound by the start (5 us until the first copies are issued) and
-// the merge; 9 to 16 rows per KV head by instructions (about 730 per 16 tokens
-// and head).
+// the merge; 9 to 16 rows per KV head by instructions (32 windows of 4096 over
+// e4m3, 16 rows, head size 128: 74 us; with two blocks per SM, half the tokens
+// per step and Q in shared memory it was 92 us and 730 instructions per 16
+// tokens and head).
 //   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows),
-//     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.  With two
-//     groups Q lies in shared memory instead of registers.
+//     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.
 //   * 8-bit codes stay codes in shared memory and are widened to f16 in
 //     registers.  K: four consecutive codes of a token to a lane; Q has the
 //     same order.  V: ldmatrix.trans over byte pairs gives a lane two head dims
@@ -76,12 +78,11 @@ struct Cfg {
     static constexpr int kMT = win_mblocks(KIND, NHB, D);
     static constexpr int kTok = 16 * kMT;            // tokens of a warp's tile
     static constexpr int kSlot = kTok * D * kElt;    // bytes of a slot (one plane of it)
-    static constexpr int kQBytes = NHB == 1 ? 0 : 16 * D * 2;  // a warp's Q
     static constexpr int kExch = (16 + 6 * NHB) * 128;         // one warp's hand-over buffer
 };
 
 struct Layout {
-    int q, exch, scales, desc, bars, cum, total;  // the warps' rings come first
+    int exch, scales, desc, bars, cum, total;  // the warps' rings come first
 };
 
 template <int D, int KIND, int NHB>
@@ -89,8 +90,7 @@ __host__ __device__ inline Layout layout(int hkv, int ts, int nslots, int vb, in
     using C = Cfg<D, KIND, NHB>;
     const int nc = hkv * ts;
     Layout l;
-    l.q = nc * nslots * C::kSlot;
-    l.exch = l.q + nc * C::kQBytes;
+    l.exch = nc * nslots * C::kSlot;
     l.scales = l.exch + (ts > 1 ? nc / 2 * C::kExch : 0);
     l.desc = l.scales + nc * kMaxSlots * 16;
     l.bars = l.desc + nc * kDesc * 16;
@@ -269,7 +269,7 @@ constexpr int kSteps2 = 22;  // bits 22 + 2j: scales from the box's first to tha
 
 // MULTI: more than one query position per request.
 template <int D, int KIND, int NHB, bool MULTI>
-__global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __grid_constant__ WinArgs a) {
+__global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(const __grid_constant__ WinArgs a) {
     using C = Cfg<D, KIND, NHB>;
     constexpr int MT = C::kMT;
     extern __shared__ uint8_t smem_raw[];
@@ -442,13 +442,9 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
     const uint32_t v_at =
         KIND == kWinBf16 ? ring + lane_at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) : k_at;
     constexpr int kPairs = C::kLine / 32;         // chunk pairs of one line
-    constexpr int kPanel = C::kTok * C::kLine;    // bytes of one panel of a slot
-    // Q in shared memory (two row groups): 16 rows of 2 D bytes, chunks xored
-    // by the row; matrices (rows 0-7, chunk), (0-7, chunk + 1), (8-15, ..)
-    const uint32_t q_base = smem_u32(smem) + lay.q + warp * C::kQBytes;
-    const uint32_t q_at =
-        q_base + ((lane & 7) + (lane >> 4) * 8) * (2 * D) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
-
+    // A slot holds one 16-token block after the other, panel by panel (with one
+    // panel that is also what larger boxes write)
+    constexpr int kPanel = 16 * C::kLine, kBlock = C::kPanels * kPanel;
     int slot = 0;
     uint32_t phase = 0;
     // False (for the whole warp) if the wait ran out.
@@ -484,7 +480,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
         const int i0 = a.grp_div(row0);
         return Rows{n - a.q_len + i0, n - a.q_len + a.grp_div(min(a.rows, row0 + 16) - 1), row0 - i0 * a.grp};
     };
-    uint32_t qb[NHB == 1 ? C::kSteps : 1][2];
+    uint32_t qb[NHB][C::kSteps][2];
     float o[NHB][C::kSteps][4];
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
 
@@ -515,7 +511,6 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 #pragma unroll
             for (int hb = 0; hb < NHB; ++hb) {
                 // Q^T operand (row g): bf16, or f16 in the order of the codes' words
-                uint32_t w[C::kSteps][2];
                 const int R = row0 + hb * 8 + g;
                 const int i = MULTI ? a.grp_div(R) : 0;
                 const bool have = R < a.rows;
@@ -524,34 +519,17 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                 if constexpr (KIND == kWinBf16) {
 #pragma unroll
                     for (int ks = 0; ks < C::kSteps; ++ks) {
-                        w[ks][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c)) : 0u;
-                        w[ks][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c + 8)) : 0u;
+                        qb[hb][ks][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c)) : 0u;
+                        qb[hb][ks][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * c + 8)) : 0u;
                     }
                 } else {
 #pragma unroll
                     for (int ks = 0; ks < C::kSteps; ++ks) {  // entries 16 ks + 4c .. + 3
                         const uint2 u = have ? __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * c))
                                              : make_uint2(0u, 0u);
-                        w[ks][0] = q_f16(u.x);
-                        w[ks][1] = q_f16(u.y);
+                        qb[hb][ks][0] = q_f16(u.x);
+                        qb[hb][ks][1] = q_f16(u.y);
                     }
-                }
-                if constexpr (NHB == 1) {
-#pragma unroll
-                    for (int ks = 0; ks < C::kSteps; ++ks) {
-                        qb[ks][0] = w[ks][0];
-                        qb[ks][1] = w[ks][1];
-                    }
-                } else {
-                    // words 0 and 1 are chunks 2 ks and 2 ks + 1
-                    const int row = hb * 8 + g;
-                    const uint32_t at = q_base + row * (2 * D) + 4 * c;
-                    if (hb == 0) __syncwarp();  // the last reads of the previous request's Q
-#pragma unroll
-                    for (int ks = 0; ks < C::kSteps; ++ks)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) st_shared(at + (((2 * ks + e) ^ g) << 4), w[ks][e]);
-                    if (hb == NHB - 1) __syncwarp();
                 }
 #pragma unroll
                 for (int mb = 0; mb < C::kSteps; ++mb)
@@ -575,17 +553,10 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                 uint32_t w[MT][4];
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    ldsm(w[m], (kb + (i / kPairs) * kPanel + m * 16 * C::kLine) ^ ((i % kPairs) << 5));
+                    ldsm(w[m], (kb + (i / kPairs) * kPanel + m * kBlock) ^ ((i % kPairs) << 5));
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
                     const int ks = kE * i + e;
-                    uint32_t q1[4];
-                    if constexpr (NHB == 1) {
-                        q1[0] = qb[ks][0];
-                        q1[1] = qb[ks][1];
-                    } else {
-                        ldsm(q1, q_at ^ (ks << 5));
-                    }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         uint32_t af[4] = {w[m][0], w[m][1], w[m][2], w[m][3]};
@@ -599,7 +570,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                         }
 #pragma unroll
                         for (int hb = 0; hb < NHB; ++hb)
-                            mma<KIND>(st[ks % kChains][m][hb], af, q1[2 * hb], q1[2 * hb + 1], ks < kChains);
+                            mma<KIND>(st[ks % kChains][m][hb], af, qb[hb][ks][0], qb[hb][ks][1], ks < kChains);
                     }
                 }
             }
@@ -641,7 +612,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                         // they hold (int8 codes are finite anyway)
                         const int r = lane >> 1, key = t + r;  // two lanes a row
                         if (!(act && key <= rows.last && (key < a.sinks || key > rows.first - a.window))) {
-                            const uint32_t row = ring + slot * C::kSlot + (16 * m + r) * C::kLine + (lane & 1) * (C::kLine / 2);
+                            const uint32_t row = ring + slot * C::kSlot + m * kBlock + r * C::kLine + (lane & 1) * (C::kLine / 2);
 #pragma unroll
                             for (int q = 0; q < C::kPanels; ++q)
 #pragma unroll
@@ -723,7 +694,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
                         pb[hb][1] = movmatrix_t(p_pair<KIND>(e2, e3));
                     }
                 }
-                const uint32_t vb_at = v_at + slot * C::kSlot + m * 16 * C::kLine;
+                const uint32_t vb_at = v_at + slot * C::kSlot + m * kBlock;
                 // operand A of head dims 16 mb ..: rows g and g + 8
                 auto load_v = [&](int mb2, uint32_t (&av)[2][4], bool masked, uint2 k) {  // blocks 2 mb2, 2 mb2 + 1
                     if constexpr (KIND == kWinBf16) {
@@ -761,7 +732,7 @@ __global__ void __launch_bounds__(256, kWinCtasPerSm) gqa_win_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < C::kPanels * kPairs; ++i) {
                         uint32_t w[4];
-                        ldsm_t(w, (k_at + slot * C::kSlot + m * 16 * C::kLine + (i / kPairs) * kPanel) ^
+                        ldsm_t(w, (k_at + slot * C::kSlot + m * kBlock + (i / kPairs) * kPanel) ^
                                       ((i % kPairs) << 5));
                         apart |= non_finite<KIND>(w[0]) || non_finite<KIND>(w[1]) || non_finite<KIND>(w[2]) ||
                                  non_finite<KIND>(w[3]);
@@ -963,7 +934,7 @@ cudaError_t allow_smem(const void* kern, bool multi) {
 template <int D, int KIND, int NHB>
 cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     const int vb = a.batch * a.rb;
-    constexpr int limit = 228 * 1024 / kWinCtasPerSm - 1024;  // a block's share of the SM's shared memory
+    constexpr int limit = 228 * 1024 / win_ctas_per_sm(NHB, D) - 1024;  // a block's share of the SM's shared memory
     int ns = kMaxSlots;
     while (ns > 2 && layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total > limit) --ns;
     a.nslots = ns;
