@@ -60,6 +60,24 @@ bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, long
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether requests are too short to be worth cutting: the window (or the block
+// table's width) bounds the bytes of one, which its own block would read in
+// `own` us at most, while cutting evens the reading out over the device and
+// costs partials and a merge, about 4 us.  (One multiprocessor takes in 70 GB/s
+// of bf16, 35 GB/s of codes, which it widens; two blocks on it take 1.6 times
+// as long as one.)  Measured whole / cut, head size 128, bf16: 150 windows of
+// 128 and 512 tokens 25 / 30 and 57 / 66 us, 64 windows of 32, 256 and 512
+// 13 / 14, 27 / 26 and 43 / 36 us; head size 64, int8: 256 windows of 128 22 / 25
+// us, one window of 256 19 / 12 us.
+bool whole_requests(const mqa::WinArgs& a, int elt, int head_size, int sms) {
+    const long long tt = 1LL << a.tt_log, all = (static_cast<long long>(a.max_blocks) * a.page + tt - 1) / tt;
+    const long long seen = (a.sinks + tt - 1) / tt + (static_cast<long long>(a.window) + a.q_len - 2 + tt) / tt + 1;
+    const double bytes = static_cast<double>(seen < all ? seen : all) * tt * 2 * a.Hkv * head_size * elt;
+    const int vb = a.batch * a.rb;
+    const double own = bytes / (elt == 2 ? 70e3 : 35e3) * (vb > sms ? 1.6 : 1.0);
+    return own <= vb * bytes / 6.5e6 + 4.0;
+}
+
 mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
                   const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window, int sinks,
                   void* out, float* lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
@@ -158,6 +176,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         const long long cap = static_cast<long long>(vb) * (num_kv_splits - 1) + 1;
         const long long fill = static_cast<long long>(sms) * mqa::win_ctas_per_sm(nhb, head_size);
         a.units = static_cast<int>(fill < cap ? fill : cap);
+        if (vb <= fill && whole_requests(a, elt, head_size, sms)) a.units = 0;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = a.units > 0 ? a.units : vb;

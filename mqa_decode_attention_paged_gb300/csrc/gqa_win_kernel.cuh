@@ -485,15 +485,18 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
 
     for (; tile < tiles; ++tile) {
-        // boxes are complete as many tiles ahead as copies run
-        // ahead of the reader (the first time round: locate, complete, start)
-        if (tile == 0) locate();
-        if (completed < min(boxes, (tile + kMaxSlots / 2 + 1) * nb)) {
-            complete();
+        // boxes are complete as many tiles ahead as copies run ahead of the
+        // reader; the first time round the copies start before the second
+        // chunk is located
+        for (int step = tile == 0 ? 0 : completed < min(boxes, (tile + kMaxSlots / 2 + 1) * nb) ? 1 : 2; step < 2;
+             ++step) {
+            if (step == 1) {
+                complete();
+                if (tile == 0)
+                    for (int s = 0; s < nslots && issued < loads; ++s) issue();
+            }
             locate();
         }
-        if (tile == 0)
-            for (int s = 0; s < nslots && issued < loads; ++s) issue();
         if ((tile & (kMeet - 1)) == kMeet - 1) named_bar_sync(1, 32 * NC);
         const int4 d = desc_s[(tile * nb) & (kDesc - 1)];
         const int t0 = d.x;
