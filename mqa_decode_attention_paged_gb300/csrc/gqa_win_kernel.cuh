@@ -551,29 +551,42 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
             constexpr int kChains = MT * NHB == 1 ? 2 : 1;
             constexpr int kE = KIND == kWinBf16 ? 1 : 2;  // 16-wide steps of a chunk pair
             float st[kChains][MT][NHB][4];
+            // blocks two by two; a pair without a visible key is passed over
 #pragma unroll
-            for (int i = 0; i < C::kPanels * kPairs; ++i) {
-                uint32_t w[MT][4];
+            for (int m0 = 0; m0 < MT; m0 += 2) {
+                const int m1 = m0 + 2 < MT ? m0 + 2 : MT;
+                if (MT > 2 && !(d.z & (3 * kAct << m0))) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    ldsm(w[m], (kb + (i / kPairs) * kPanel + m * kBlock) ^ ((i % kPairs) << 5));
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int ks = kE * i + e;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint32_t af[4] = {w[m][0], w[m][1], w[m][2], w[m][3]};
-                        if constexpr (KIND != kWinBf16) {
-                            const uint2 k0 = widen_adjacent<KIND>(w[m][2 * e]);
-                            const uint2 k1 = widen_adjacent<KIND>(w[m][2 * e + 1]);
-                            af[0] = k0.x;
-                            af[1] = k1.x;
-                            af[2] = k0.y;
-                            af[3] = k1.y;
-                        }
+                    for (int m = m0; m < m1; ++m)
 #pragma unroll
                         for (int hb = 0; hb < NHB; ++hb)
-                            mma<KIND>(st[ks % kChains][m][hb], af, qb[hb][ks][0], qb[hb][ks][1], ks < kChains);
+                            st[0][m][hb][0] = st[0][m][hb][1] = st[0][m][hb][2] = st[0][m][hb][3] = 0.f;
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < C::kPanels * kPairs; ++i) {
+                    uint32_t w[MT][4];
+#pragma unroll
+                    for (int m = m0; m < m1; ++m)
+                        ldsm(w[m], (kb + (i / kPairs) * kPanel + m * kBlock) ^ ((i % kPairs) << 5));
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        const int ks = kE * i + e;
+#pragma unroll
+                        for (int m = m0; m < m1; ++m) {
+                            uint32_t af[4] = {w[m][0], w[m][1], w[m][2], w[m][3]};
+                            if constexpr (KIND != kWinBf16) {
+                                const uint2 k0 = widen_adjacent<KIND>(w[m][2 * e]);
+                                const uint2 k1 = widen_adjacent<KIND>(w[m][2 * e + 1]);
+                                af[0] = k0.x;
+                                af[1] = k1.x;
+                                af[2] = k0.y;
+                                af[3] = k1.y;
+                            }
+#pragma unroll
+                            for (int hb = 0; hb < NHB; ++hb)
+                                mma<KIND>(st[ks % kChains][m][hb], af, qb[hb][ks][0], qb[hb][ks][1], ks < kChains);
+                        }
                     }
                 }
             }
@@ -679,6 +692,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+                if (MT > 2 && !(d.z & (3 * kAct << (m & ~1)))) continue;
                 const int t = t0 + 16 * m;
                 // the sums take the fp32 probabilities; P.V takes them rounded
                 uint32_t pb[NHB][2];
