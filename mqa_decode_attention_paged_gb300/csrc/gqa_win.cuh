@@ -116,26 +116,12 @@ __device__ __forceinline__ int win_units(const WinArgs& a, int vb, int T, int lo
     return vb <= a.units && longest <= share + max(2, share / 4) ? 0 : U;
 }
 
-// First tile of unit g of U (shares of T / U tiles, the first T % U of them one
-// more), moved to a request's start or end where one lies a tile away and
-// units hold four tiles at least: a cut costs a merge and a start, about a
-// tile's time, so nothing further is worth the imbalance.  Non-decreasing in
-// g.
-__device__ __forceinline__ int win_unit_start(const int* cum, int vb, int T, int U, int g) {
-    if (g >= U) return T;
+// First tile of unit g of U: shares of T / U tiles, the first T % U of them one
+// more.  (Moving a cut to a request's boundary where one lies a tile away
+// changes nothing: 50.6 and 50.7 us on 64 windows of 1024 over bf16.)
+__device__ __forceinline__ int win_unit_start(int T, int U, int g) {
     const int share = T / U;
-    const int x = g * share + min(g, T - share * U);
-    int lo = 0, hi = vb - 1;  // the last virtual request starting at or before x
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= x)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    const int near = share >= 4 ? 1 : 0;
-    if (x - cum[lo] <= near) return cum[lo];
-    return cum[lo + 1] - x <= near ? cum[lo + 1] : x;
+    return g * share + min(g, T - share * U);
 }
 
 // Warps that share a KV head: 8 warps in all, or one per KV head where Hkv

@@ -306,9 +306,9 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
         p0 = cum[min(static_cast<int>(blockIdx.x), vb)];
         p1 = cum[min(static_cast<int>(blockIdx.x) + 1, vb)];
     } else {
-        const int x = win_unit_start(cum, vb, T, U, static_cast<int>(blockIdx.x) + (lane & 1));
-        p0 = __shfl_sync(0xffffffffu, x, 0);
-        p1 = __shfl_sync(0xffffffffu, x, 1);
+        const int u = min(static_cast<int>(blockIdx.x), U);
+        p0 = win_unit_start(T, U, u);
+        p1 = win_unit_start(T, U, min(u + 1, U));
     }
     // virtual requests without a key: out = 0, lse = -inf
     for (int v = blockIdx.x; v < vb; v += gridDim.x) {
