@@ -63,19 +63,21 @@ bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, long
 // Whether requests are too short to be worth cutting: the window (or the block
 // table's width) bounds the bytes of one, which its own block would read in
 // `own` us at most, while cutting evens the reading out over the device and
-// costs partials and a merge, about 4 us.  (One multiprocessor takes in 70 GB/s
-// of bf16, 35 GB/s of codes, which it widens; two blocks on it take 1.6 times
-// as long as one.)  Measured whole / cut, head size 128, bf16: 150 windows of
-// 128 and 512 tokens 25 / 30 and 57 / 66 us, 64 windows of 32, 256 and 512
-// 13 / 14, 27 / 26 and 43 / 36 us; head size 64, int8: 256 windows of 128 22 / 25
-// us, one window of 256 19 / 12 us.
+// costs partials and a merge, about 4 us.  One multiprocessor takes in 70 GB/s
+// of bf16, 35 GB/s of codes, which it widens; two blocks on it take 2.6 (1.6)
+// times as long as one.  Longer windows hold requests of unlike lengths more
+// often than not, and are cut whatever their number.  Measured whole / cut in
+// us, 32/8 heads x 128, bf16, windows of 128, 512 and 1024 tokens: 150 requests
+// 21 / 27, 54 / 62 and 97 / 109, 200 requests 30 / 34, 95 / 79 and 176 / 140, 304
+// requests 37 / 46, 105 / 114 and 200 / 209; 64/8 heads x 64, int8, window 128:
+// 100, 150, 200 and 256 requests 12 / 14, 13 / 19, 17 / 24, 18 / 25.
 bool whole_requests(const mqa::WinArgs& a, int elt, int head_size, int sms) {
     const long long tt = 1LL << a.tt_log, all = (static_cast<long long>(a.max_blocks) * a.page + tt - 1) / tt;
     const long long seen = (a.sinks + tt - 1) / tt + (static_cast<long long>(a.window) + a.q_len - 2 + tt) / tt + 1;
     const double bytes = static_cast<double>(seen < all ? seen : all) * tt * 2 * a.Hkv * head_size * elt;
     const int vb = a.batch * a.rb;
-    const double own = bytes / (elt == 2 ? 70e3 : 35e3) * (vb > sms ? 1.6 : 1.0);
-    return own <= vb * bytes / 6.5e6 + 4.0;
+    const double own = bytes / (elt == 2 ? 70e3 : 35e3), pair = vb <= sms ? 1.0 : elt == 2 ? 2.6 : 1.6;
+    return own <= 100.0 && own * pair <= vb * bytes / 6.5e6 + 4.0;
 }
 
 mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,

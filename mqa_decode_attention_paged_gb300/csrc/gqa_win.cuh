@@ -106,11 +106,9 @@ __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
 // Balanced mode with T tiles, the longest request's being `longest`: units
 // actually used; 0 where a unit is a request.  Where the units are enough for
 // the requests and none is much longer than an equal share, cutting would
-// cost more, in starts, partials and their merge, than it evens out: 256
-// windows of 1024 (512, 128) tokens over int8 take 96 (56, 24) us whole and 103
-// (58, 26) us cut on 304 units; 200 of 1024 take 95 us whole and 83 us cut.
-// (Much fewer requests than units leave multiprocessors to single blocks, and
-// one with two blocks then takes twice as long: an SM takes in 60 GB/s.)
+// cost more, in starts and partials, than it evens out: 256 windows of 128 (512,
+// 1024) tokens over int8, 64/8 heads x 64, take 21 (38, 62) us whole and 25
+// (43, 64) us cut on 304 units.
 __device__ __forceinline__ int win_units(const WinArgs& a, int vb, int T, int longest) {
     const int U = min(a.units, max(1, T)), share = T / U;
     return vb <= a.units && longest <= share + max(2, share / 4) ? 0 : U;
