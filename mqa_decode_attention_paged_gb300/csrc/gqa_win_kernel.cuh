@@ -25,12 +25,12 @@
 // Boxes are described 16 at a time, a lane each, across requests.
 //
 // Measured (batch of 256, lognormal lengths, 32/8 heads x 128, 16-token pages,
-// e4m3 with a scale per page and head): 262 us, 6.3 TB/s of the 6.67 a copy
+// e4m3 with a scale per page and head): 259 us, 6.4 TB/s of the 6.67 a copy
 // reaches; 64 windows of 16384 tokens over bf16: 661 us, 6.5 TB/s.  Short
-// windows are bound by the start (5 us until the first copies are issued) and
+// windows are bound by the start (4.3 us until the copies are issued) and
 // the merge; 9 to 16 rows per KV head by instructions (32 windows of 4096 over
-// e4m3, 16 rows, head size 128: 74 us; with two blocks per SM, half the tokens
-// per step and Q in shared memory it was 92 us and 730 instructions per 16
+// e4m3, 16 rows, head size 128: 69 us; with two blocks per SM, half the tokens
+// per step and Q in shared memory it was 89 us and 730 instructions per 16
 // tokens and head).
 //   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows),
 //     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.
