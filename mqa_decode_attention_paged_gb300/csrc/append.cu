@@ -605,7 +605,7 @@ cudaError_t launch(const GqaAppendArgs& a, cudaStream_t stream) {
         const long long T = a.t.tokens, bound = T / a.scale_block + 2LL * a.t.batch;
         mode.by_token = T <= bound;
         // Shares of more than 16 rows go to four warps: a warp alone would
-        // wait for 16 loads in turn, twice (a prefill of 7.4 thousand tokens in
+        // wait for 16 loads in turn, twice (a prefill of 8.7 thousand tokens in
         // 64-token blocks: 48 us, and 33 us of it for the blocks alone).
         mode.warps = !mode.by_token && a.scale_block > 16 ? kWarps : 1;
         block_tasks = (mode.by_token ? T : bound) * 2 * a.Hkv;

@@ -374,3 +374,58 @@ def test_random_shapes():
                     sinks=int(rng.choice([0, 1, 5, 70])), group=int(rng.choice([16, page])), seed=int(rng.integers(1 << 30)))
         run_and_check(case, (1, int(rng.integers(2, 9)), None),
                       f"{kv} Hkv={Hkv} grp={grp} L={L} page={page} lens={case.lens} W={case.window} S={case.sinks}")
+
+
+def widen(case, columns=2048):
+    """The same batch under a block table made for far longer requests: nothing says that they are short."""
+    case.bt = torch.cat([case.bt, torch.full((len(case.lens), columns), -1, dtype=torch.int32)], 1)
+    return case
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("L,Hq,Hkv,D", [(1, 32, 8, 128), (1, 16, 1, 64), (1, 12, 4, 128), (4, 32, 8, 128),
+                                        (5, 32, 8, 64), (17, 14, 2, 128), (3, 6, 3, 64)])
+def test_short_requests_that_are_cut(kv, L, Hq, Hkv, D):
+    # nothing but the lengths on the device says that requests are short: they are cut and merged
+    for window, sinks in ((NONE, 0), (3000, 7)):
+        case = widen(Case([0, 1, L + 1, L + 15, 130, 333, 700], Hq, Hkv, D, 16, kv, L=L, window=window, sinks=sinks,
+                          seed=17))
+        run_and_check(case, (2, 3, None), f"{kv} L={L} {Hq}/{Hkv}x{D} W={window}")
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (32, 2, 128)])
+def test_more_requests_than_blocks(kv, Hq, Hkv, D):
+    # units that hold several requests and parts of others, under a small window
+    lens = np.random.default_rng(5).integers(0, 120, 330).tolist()
+    for window, sinks in ((1, 0), (24, 3)):
+        case = Case(lens, Hq, Hkv, D, 16, kv, window=window, sinks=sinks, seed=18)
+        for s in (2, None):
+            out, lse, status = case.run(s)
+            assert status == 0
+            check(case, out, lse, rows=[*range(0, 330, 7), 328, 329], what=f"{kv} W={window} splits={s}")
+
+
+def test_graphs_of_cut_requests():
+    # two captured calls over one batch, each with its own partials, replayed together on two streams
+    case = widen(Case([700, 20, 1500], 8, 2, 128, 16, "int8_block", seed=19, poison=False))
+    q, kv, bt, sc, sl = case.dev()
+    graphs = []
+    for _ in range(2):
+        mqa.gqa_block_decode(q, kv, sc, bt, sl, case.scale)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = mqa.gqa_block_decode(q, kv, sc, bt, sl, case.scale)
+        graphs.append((g, res, torch.cuda.Stream()))
+    for lens in ([700, 20, 1500], [1, 0, 900], [333, 20, 17]):
+        case.lens = lens
+        sl.copy_(torch.tensor(lens, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for g, _, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for _, (out, lse), _ in graphs:
+            check(case, out.cpu().double(), lse.cpu().double(), what=f"replay {lens}")
