@@ -21,12 +21,14 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "api_common.cuh"
 #include "append.cuh"
 
 namespace mqa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtas = 6;  // thread blocks per SM that the registers are limited for
 constexpr float kE4m3Max = 448.f, kInt8Max = 127.f, kInt4Max = 7.f;
 constexpr float kTinyScale = 1.1754943508222875e-38f;  // 2^-126: scales are zero or normal
 
@@ -348,50 +350,46 @@ __device__ __forceinline__ bool share_at_token(const AppendBatch& a, int t, int 
     return share_of(a, o, static_cast<int>(p0), p / G * G, G, s);
 }
 
-// Share number `task` of the batch, by the prefix of the requests' counts.
+// Share number `task`: request b's shares are numbered from query_start[b] / G
+// + 2 b on, which leaves room for the (n - 1) / G + 2 that its n tokens touch
+// at most and ascends without a sum over the batch.  The request is found as in
+// find_owner.
 __device__ __forceinline__ bool share_by_number(const AppendBatch& a, long long task, int G, int lane, Share& s) {
-    long long running = 0;
-    for (int base = 0; base < a.batch; base += 32) {
-        const int i = base + lane;
-        Owner o{i, 0, 0, 0};
-        int c = 0, p0 = 0;
-        if (i < a.batch) {
-            o.q0 = __ldg(a.query_start + i);
-            o.q1 = __ldg(a.query_start + i + 1);
-            o.len = __ldg(a.seq_lens + i);
-            if (o.q1 > o.q0) {
-                if (o.q0 < 0 || o.q1 > a.tokens || o.len < static_cast<long long>(o.q1) - o.q0) {
-                    report(a.status, MQA_ERR_DEVICE_CHECK);
-                } else {
-                    p0 = o.len - (o.q1 - o.q0);
-                    c = (o.len - 1) / G - p0 / G + 1;
-                }
-            }
-        }
-        int x = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += u;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, running + x > task && running + x - c <= task);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            o.b = base + l;
-            o.q0 = __shfl_sync(0xffffffffu, o.q0, l);
-            o.q1 = __shfl_sync(0xffffffffu, o.q1, l);
-            o.len = __shfl_sync(0xffffffffu, o.len, l);
-            p0 = __shfl_sync(0xffffffffu, p0, l);
-            const int kth = static_cast<int>(task - running) - __shfl_sync(0xffffffffu, x - c, l);
-            return share_of(a, o, p0, (p0 / G + kth) * G, G, s);
-        }
-        running += __shfl_sync(0xffffffffu, x, 31);
+    auto number = [&](int b) { return __ldg(a.query_start + b) / G + 2LL * b; };
+    int lo = 0, n = a.batch;
+    while (n > 32) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const int m = __popc(__ballot_sync(0xffffffffu, at < n && number(lo + at) <= task));
+        if (m == 0) return false;
+        lo += (m - 1) * step;
+        n = min(step, n - (m - 1) * step);
     }
-    return false;  // fewer shares than the grid allows for
+    Owner o{lo + lane, 0, 0, 0};
+    long long at = 0;
+    if (lane < n) {
+        o.q0 = __ldg(a.query_start + o.b);
+        o.q1 = __ldg(a.query_start + o.b + 1);
+        o.len = __ldg(a.seq_lens + o.b);
+        at = o.q0 / G + 2LL * o.b;
+    }
+    const int m = __popc(__ballot_sync(0xffffffffu, lane < n && at <= task));
+    if (m == 0) return false;
+    o.b = __shfl_sync(0xffffffffu, o.b, m - 1);
+    o.q0 = __shfl_sync(0xffffffffu, o.q0, m - 1);
+    o.q1 = __shfl_sync(0xffffffffu, o.q1, m - 1);
+    o.len = __shfl_sync(0xffffffffu, o.len, m - 1);
+    if (o.q1 <= o.q0) return false;  // no new tokens
+    if (o.q0 < 0 || o.q1 > a.tokens || o.len < static_cast<long long>(o.q1) - o.q0) {
+        report(a.status, MQA_ERR_DEVICE_CHECK);
+        return false;
+    }
+    const int p0 = o.len - (o.q1 - o.q0);
+    const long long kth = task - __shfl_sync(0xffffffffu, at, m - 1);
+    if (kth < 0 || kth > (o.len - 1) / G - p0 / G) return false;
+    return share_of(a, o, p0, (p0 / G + static_cast<int>(kth)) * G, G, s);
 }
 
-// How a share is found: at the token that starts it, or by its number in the
-// batch; and by how many warps of a thread block it is then done.
+// How a share is found: at the token that starts it, or by its number; and by how many warps of a thread block it is then done.
 struct ShareMode {
     bool by_token;
     int warps;  // 1 or kWarps
@@ -509,7 +507,7 @@ __device__ __forceinline__ void append_block(const GqaAppendArgs& a, long long t
 
 // Warp tasks: (block formats) blocks, which take longest, then rows of tokens.
 template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kWarps, 6) gqa_append_kernel(const GqaAppendArgs a, const int groups,
+__global__ void __launch_bounds__(32 * kWarps, kCtas) gqa_append_kernel(const GqaAppendArgs a, const int groups,
                                                                  const long long row_tasks,
                                                                  const long long block_tasks, const ShareMode mode) {
     __shared__ float exchange[kWarps];
@@ -536,7 +534,7 @@ __global__ void __launch_bounds__(32 * kWarps, 6) gqa_append_kernel(const GqaApp
 // MLA: a token's 64-column pieces: R / 64 of kv_c, k_pe, then H of q_pe (4
 // lanes a piece).
 template <bool FP8>
-__global__ void __launch_bounds__(32 * kWarps, 6) mla_append_kernel(const MlaAppendArgs a, const int groups,
+__global__ void __launch_bounds__(32 * kWarps, kCtas) mla_append_kernel(const MlaAppendArgs a, const int groups,
                                                                  const long long row_tasks) {
     constexpr int D = 64, LPR = 4, RPI = 8;
     const int lane = threadIdx.x & 31;
@@ -597,17 +595,18 @@ cudaError_t launch(const GqaAppendArgs& a, cudaStream_t stream) {
     long long block_tasks = 0;
     ShareMode mode{false, 1};
     if (BLOCK) {
-        // One task per plane, head and share of a block.  With few new tokens
-        // per request a token is the start of a share more often than not, and
-        // a warp finds its request by a search; with many, shares are numbered
-        // by the prefix of the requests' counts (a request with n new tokens
-        // touches at most n blocks, and at most (n - 1) / G + 2).
+        // One task per plane, head and share of a block, or per token where
+        // that is less (a request with n new tokens touches at most n blocks,
+        // and at most (n - 1) / G + 2).
         const long long T = a.t.tokens, bound = T / a.scale_block + 2LL * a.t.batch;
         mode.by_token = T <= bound;
-        // Shares of more than 16 rows go to four warps: a warp alone would
-        // wait for 16 loads in turn, twice (a prefill of 8.7 thousand tokens in
-        // 64-token blocks: 48 us, and 33 us of it for the blocks alone).
-        mode.warps = !mode.by_token && a.scale_block > 16 ? kWarps : 1;
+        // Shares of some length go to four warps while there are not enough of
+        // them to fill the device's: a warp alone waits for its rows' loads in
+        // turn, twice.  Blocks of 64 tokens, 8 heads x 128, int8, one warp / four:
+        // 32 runs of 64 (100) new tokens 17 (20) / 13 (13) us, 128 runs of 64
+        // 25 / 27 us, 1024 runs 137 / 195 us.
+        const long long warps = static_cast<long long>(api_sm_count()) * kCtas * kWarps;
+        mode.warps = T > 8 * bound && bound * 2 * a.Hkv <= warps ? kWarps : 1;
         block_tasks = (mode.by_token ? T : bound) * 2 * a.Hkv;
     }
     const long long grid = (row_tasks + block_tasks * mode.warps + kWarps - 1) / kWarps;

@@ -433,3 +433,46 @@ def test_block_scaled_many_requests(kv):
     _, got, got_s, status = run(bt, q, k, v, cache, scales=scales)
     assert status == 0
     check_block_append(bt, k, v, False, kv, 16, cache, scales, got, got_s)
+
+
+@pytest.mark.parametrize("page,group", [(16, 16), (64, 32)])
+def test_block_scaled_batches_of_short_runs(page, group):
+    # more than 32 x 32 requests of a few tokens each: several rounds of search, by number and by token
+    rng = np.random.default_rng(6)
+    for counts in ([3, 4, 5, 17], [0, 1, 1, 2]):
+        new = rng.choice(counts, 1100).tolist()
+        bt = Batch(new, rng.integers(0, 70, 1100).tolist(), page, pad=3, seed=12, rot=64)
+        q, k, v = fused(bt, 1, 1, 64, False)
+        cache, scales = block_case(bt, 1, 64, "int8_block", group)
+        _, got, got_s, status = run(bt, q, k, v, cache, scales=scales)
+        assert status == 0
+        check_block_append(bt, k, v, False, "int8_block", group, cache, scales, got, got_s)
+
+
+def test_block_scaled_bad_requests_are_reported_by_number():
+    # long runs (shares found by number): one request shorter than its new tokens, one beyond its pages
+    for bad in (0, 1):
+        bt = Batch([40, 50, 45], [5, 0, 20], 16, seed=13, rot=64)
+        q, k, v = fused(bt, 2, 1, 64, False)
+        cache, scales = block_case(bt, 1, 64, "int8_block", 16)
+        lens = list(bt.lens)
+        bt.lens[1] = 49 if bad == 0 else 16 * bt.bt.shape[1] + 1
+        bt.cs = table(16 * bt.bt.shape[1] + 2, 64)
+        _, got, got_s, status = run(bt, q, k, v, cache, scales=scales)
+        assert status == 5
+        bt.lens = lens
+        ok = torch.zeros(bt.nb, dtype=torch.bool)
+        ok[bt.bt[[0, 2]][bt.bt[[0, 2]] >= 0].long()] = True
+        for b in (0, 2):
+            p0 = bt.lens[b] - bt.new[b]
+            for p in range(p0, bt.lens[b]):
+                blk, slot = bt.where(b, p)
+                t = int(bt.qs[b]) + p - p0
+                s = float(got_s[blk, 1, 0, 0])
+                check_codes(got[blk, 1, slot, 0].double(), v[t, 0].double(), torch.zeros(64, dtype=torch.float64), s,
+                            "int8_block", f"request {b} position {p}")
+        if bad == 0:  # its pages keep their bytes
+            own = bt.bt[1][bt.bt[1] >= 0].long()
+            assert torch.equal(got[own], cache[own]) and torch.equal(got_s[own], scales[own])
+        assert torch.equal(got[~ok & ~torch.isin(torch.arange(bt.nb), bt.bt[1].long())],
+                           cache[~ok & ~torch.isin(torch.arange(bt.nb), bt.bt[1].long())])
