@@ -524,7 +524,8 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
  *   kv_cache   any GQA cache of mqa_kv_dtype, laid out as the decode entry
  *              points read it.  A value x is stored as
  *                bf16             x;
- *                FP8_E4M3         e4m3(x / k_scale or v_scale) (non-zero);
+ *                FP8_E4M3         e4m3(x / k_scale or v_scale) (of magnitude
+ *                                 2^-126 .. 2^126);
  *                *_PER_TOKEN_HEAD s = max|x| / 448, 127 or 7 over the row, its
  *                                 codes round(x / s);
  *                *_BLOCK          s = max(s_old, max|x| / 448 or 127) over the

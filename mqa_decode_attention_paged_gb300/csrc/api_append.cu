@@ -12,6 +12,9 @@ using mqa::api_aligned;
 // Row strides are multiples of 8 elements (16-byte loads) and hold a row.
 bool stride_ok(long long s, long long least) { return s >= least && s % 8 == 0; }
 
+// A per-tensor scale that can be divided by: its reciprocal is a normal number.
+bool scale_ok(float s) { return std::fabs(s) >= 0x1p-126f && std::fabs(s) <= 0x1p126f; }
+
 // The checks the two entry points share; MQA_OK if the call may go on.
 mqa_status check_batch(const mqa::AppendBatch& t) {
     if (!t.cos_sin || !t.block_table || !t.seq_lens || !t.query_start) return MQA_ERR_INVALID_ARG;
@@ -60,9 +63,7 @@ mqa_status gqa_rope_append(const void* q, const void* k, const void* v, const fl
         const long long q_row = static_cast<long long>(num_q_heads) * head_size;
         if (!stride_ok(q_stride, q_row) || !stride_ok(q_out_stride, q_row)) return MQA_ERR_INVALID_ARG;
     }
-    if (kv_dtype == MQA_KV_FP8_E4M3 &&
-        (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f || v_scale == 0.f))
-        return MQA_ERR_INVALID_ARG;
+    if (kv_dtype == MQA_KV_FP8_E4M3 && (!scale_ok(k_scale) || !scale_ok(v_scale))) return MQA_ERR_INVALID_ARG;
     if (kv_dtype == MQA_KV_FP8_E4M3_BLOCK || kv_dtype == MQA_KV_INT8_BLOCK) {
         if (!kv_scales || !api_aligned(kv_scales, 4) || scale_block < 1) return MQA_ERR_INVALID_ARG;
         if (scale_block % 16 != 0 || page_size % scale_block != 0) return MQA_ERR_UNSUPPORTED;
@@ -111,7 +112,7 @@ mqa_status mla_rope_append(const void* kv_c, const void* k_pe, const void* q_pe,
     if (q_pe && (!stride_ok(q_pe_head_stride, 64) || !stride_ok(q_out_head_stride, 64) ||
                  !stride_ok(q_pe_stride, 64) || !stride_ok(q_out_stride, 64)))
         return MQA_ERR_INVALID_ARG;
-    if (kv_dtype == MQA_KV_FP8_E4M3 && (!std::isfinite(k_scale) || k_scale == 0.f)) return MQA_ERR_INVALID_ARG;
+    if (kv_dtype == MQA_KV_FP8_E4M3 && !scale_ok(k_scale)) return MQA_ERR_INVALID_ARG;
     if (num_tokens == 0) return MQA_OK;
     a.kv_c = static_cast<const __nv_bfloat16*>(kv_c);
     a.k_pe = static_cast<const __nv_bfloat16*>(k_pe);

@@ -92,7 +92,8 @@ def _gqa_append(**kw):
     (dict(rot=0), INV), (dict(rot=8), UNS), (dict(rot=144), INV), (dict(D=96), UNS), (dict(Hkv=9), UNS),
     (dict(P=24), UNS), (dict(kvd=7), UNS), (dict(T=(1 << 24) + 1), UNS), (dict(nb=1 << 27), UNS),
     (dict(sq=1016), INV), (dict(sk=248), INV), (dict(sv=260), INV), (dict(so=1028), INV),
-    (dict(kvd=1, ks=0.0), INV), (dict(kvd=1, vs=float("nan")), INV),
+    (dict(kvd=1, ks=0.0), INV), (dict(kvd=1, vs=float("nan")), INV), (dict(kvd=1, ks=1e-39), INV),
+    (dict(kvd=1, vs=-2e38), INV), (dict(kvd=1, ks=float("inf")), INV),
     (dict(kvd=5), INV), (dict(kvd=6, sc=FAKE, G=8), UNS), (dict(kvd=6, sc=FAKE, G=32), UNS),
     (dict(kvd=6, sc=FAKE, G=0), INV),
     (dict(T=0), mqa.OK),                           # nothing to append: nothing is enqueued
@@ -117,7 +118,7 @@ def _mla_append(**kw):
     (dict(c=FAKE + 8), INV), (dict(p=FAKE + 8), INV), (dict(q=FAKE + 8), INV), (dict(qo=FAKE + 8), INV),
     (dict(H=0), INV), (dict(D=512, R=448), UNS), (dict(kvd=3), UNS), (dict(kvd=5), UNS), (dict(P=20), UNS),
     (dict(sc=504), INV), (dict(sp=60), INV), (dict(sh=60), INV), (dict(soh=68), INV), (dict(kvd=1, ks=0.0), INV),
-    (dict(T=0), mqa.OK)])
+    (dict(kvd=1, ks=1e-40), INV), (dict(kvd=1, ks=float("nan")), INV), (dict(T=0), mqa.OK)])
 def test_mla_append_validation(kw, code):
     assert _mla_append(**kw) == code
 
