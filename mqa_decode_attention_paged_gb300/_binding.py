@@ -498,8 +498,13 @@ def gqa_window_num_kv_splits(batch: int, q_len: int, num_q_heads: int, num_kv_he
 _PTH_CODES = (KV_FP8_E4M3_PER_TOKEN_HEAD, KV_INT8_PER_TOKEN_HEAD, KV_INT4_PER_TOKEN_HEAD)
 
 
+# The calls below run once per layer and token.  Each first asks in one expression whether every tensor is the usual
+# kind; only if one is not, _check and its like find out whether the call is wrong, and say how.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _fits(t, dtype, shape, index):
-    """Whether t is what _check and _on_device ask for, in one look (the calls below run once per layer and token)."""
+    """Whether t is what _check and _on_device ask for."""
     return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
@@ -592,18 +597,20 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
     if window is None and block == 0:
         raise ValueError("gqa_block_decode reads block-scaled caches (fp8_e4m3_block, int8_block)")
     bt_shape = block_table.shape
-    if not (index >= 0 and len(bt_shape) == 2 and bt_shape[0] == B and _fits(q, torch.bfloat16, shape, index)
+    if not (index >= 0 and len(bt_shape) == 2 and bt_shape[0] == B and q.dtype is _BF16 and q.is_contiguous()
             and kv_cache.is_contiguous() and kv_cache.get_device() == index
             and kv_cache.element_size() == (2 if code == KV_BF16 else 1)
-            and _fits(block_table, torch.int32, bt_shape, index) and _fits(seq_lens, torch.int32, (B,), index)
+            and block_table.dtype is _I32 and block_table.get_device() == index and block_table.is_contiguous()
+            and seq_lens.dtype is _I32 and seq_lens.shape == bt_shape[:1] and seq_lens.get_device() == index
+            and seq_lens.is_contiguous()
             and (kv_scales is None or kv_scales.get_device() == index)
-            and (out is None or _fits(out, torch.bfloat16, shape, index))
-            and (lse is None or _fits(lse, torch.float32, shape[:-1], index))
+            and (out is None or _fits(out, _BF16, shape, index))
+            and (lse is None or _fits(lse, _F32, shape[:-1], index))
             and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == index))
-            and (device_status is None or _fits(device_status, torch.int32, device_status.shape, index))):
+            and (device_status is None or _fits(device_status, _I32, device_status.shape, index))):
         _check_common(q, kv_cache, code, block_table, seq_lens, q if out is None else out, shape, lse, shape[:-1],
                       workspace, device_status, extra=(("kv_scales", kv_scales),))
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale,
                                   window, sinks, out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream,
@@ -644,15 +651,11 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
 def _check_rows(t, name, shape, dense):
     """A bf16 tensor of shape `shape` whose last `dense` dimensions are dense (rows of a wider tensor will do);
     returns its leading strides."""
-    st = t.stride()
-    if (t.dtype is torch.bfloat16 and t.shape == shape and st[-1] == 1 and (dense == 1 or st[-2] == shape[-1])
-            and 1 not in shape and 0 not in shape):
-        return st[:-dense]
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    want = 1
+    st, want = t.stride(), 1
     for i in range(1, dense + 1):
         if shape[-i] != 1 and st[-i] != want:
             raise ValueError(f"the last {dense} dimension(s) of {name} must be contiguous")
@@ -666,19 +669,29 @@ def _check_rows(t, name, shape, dense):
     return tuple(out)
 
 
-def _check_append(index, cos_sin, width, kv_cache, block_table, seq_lens, query_start, device_status, named):
+def _head_rows(t, T, width, index):
+    """Token stride of bf16 [T, heads, width] on device `index`, dense within a token; 0 if t is anything else."""
+    s, st = t.shape, t.stride()
+    if (t.dtype is _BF16 and s[0] == T and s[2] == width and st[1] == width and st[2] == 1
+            and t.get_device() == index):
+        return st[0]
+    return 0
+
+
+def _usual_batch(index, cos_sin, kv_cache, block_table, seq_lens, query_start, device_status):
+    """Whether the tensors that describe an append's batch are the usual kind, on device `index`."""
     bt_shape = block_table.shape
-    if (index >= 0 and len(bt_shape) == 2 and cos_sin.dim() == 2 and width in (None, cos_sin.shape[1])
-            and _fits(cos_sin, torch.float32, cos_sin.shape, index) and kv_cache.is_contiguous()
-            and kv_cache.get_device() == index and _fits(block_table, torch.int32, bt_shape, index)
-            and _fits(seq_lens, torch.int32, bt_shape[:1], index)
-            and _fits(query_start, torch.int32, (bt_shape[0] + 1,), index)
-            and (device_status is None or _fits(device_status, torch.int32, device_status.shape, index))):
-        for _, t in named:
-            if t is not None and t.get_device() != index:
-                break
-        else:
-            return bt_shape[0]
+    return (index >= 0 and len(bt_shape) == 2 and kv_cache.is_contiguous() and kv_cache.get_device() == index
+            and cos_sin.dtype is _F32 and cos_sin.get_device() == index and cos_sin.is_contiguous()
+            and block_table.dtype is _I32 and block_table.get_device() == index and block_table.is_contiguous()
+            and seq_lens.dtype is _I32 and seq_lens.shape == bt_shape[:1] and seq_lens.get_device() == index
+            and seq_lens.is_contiguous()
+            and query_start.dtype is _I32 and query_start.shape == (bt_shape[0] + 1,)
+            and query_start.get_device() == index and query_start.is_contiguous()
+            and (device_status is None or _fits(device_status, _I32, device_status.shape, index)))
+
+
+def _check_append(cos_sin, width, kv_cache, block_table, seq_lens, query_start, device_status, named):
     _check(cos_sin, "cos_sin", (torch.float32,))
     if cos_sin.dim() != 2 or (width is not None and cos_sin.shape[1] != width):
         raise ValueError(f"cos_sin must be fp32 [max_position, {width or 'rotary_dim'}]")
@@ -692,7 +705,6 @@ def _check_append(index, cos_sin, width, kv_cache, block_table, seq_lens, query_
     _check(device_status, "device_status", (torch.int32,), optional=True)
     _on_device([*named, ("cos_sin", cos_sin), ("kv_cache", kv_cache), ("block_table", block_table),
                 ("seq_lens", seq_lens), ("query_start", query_start), ("device_status", device_status)])
-    return B
 
 
 def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start, *, q=None, q_out=None,
@@ -705,10 +717,11 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
     holds cosines, then sines; interleaved pairs are columns (2i, 2i + 1).  kv_cache is any cache that the GQA
     decode calls read, with kv_scales for the block-scaled formats; both are updated in place.  Returns the rotated
     queries (q_out, which may be q itself; allocated when only q is given), or None."""
-    if k.dim() != 3 or kv_cache.dim() != 5 or cos_sin.dim() != 2:
+    shape, rows, table = k.shape, kv_cache.shape, cos_sin.shape
+    if len(shape) != 3 or len(rows) != 5 or len(table) != 2:
         raise ValueError("k must be [tokens, heads, head_size], kv_cache have 5 dimensions and cos_sin 2")
-    T, Hkv, D = k.shape
-    nb, two, page, Hkv2, row = kv_cache.shape
+    T, Hkv, D = shape
+    nb, two, page, Hkv2, row = rows
     code = _block_code(kv_cache, kv_scales, kv_dtype)
     want = D if code not in _PTH_CODES else D // 2 + 4 if code == KV_INT4_PER_TOKEN_HEAD else D + 4
     if two != 2 or Hkv2 != Hkv or row != want:
@@ -716,22 +729,35 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
     if kv_cache.element_size() != (2 if code == KV_BF16 else 1):
         raise TypeError(f"kv_cache must have {2 if code == KV_BF16 else 1}-byte elements, got {kv_cache.dtype}")
     block = _scale_block(kv_scales, code, nb, page, Hkv)
-    ks, = _check_rows(k, "k", (T, Hkv, D), 2)
-    vs, = _check_rows(v, "v", (T, Hkv, D), 2)
+    index = k.get_device()
     qs = qos = Hq = 0
     if q is not None:
-        if q.dim() != 3:
+        q_shape = q.shape
+        if len(q_shape) != 3:
             raise ValueError("q must be [tokens, heads, head_size]")
-        Hq = q.shape[1]
-        qs, = _check_rows(q, "q", (T, Hq, D), 2)
-        if q_out is not None:
-            qos, = _check_rows(q_out, "q_out", (T, Hq, D), 2)
+        Hq = q_shape[1]
     elif q_out is not None:
         raise ValueError("q_out without q")
-    index = k.get_device()
-    B = _check_append(index, cos_sin, None, kv_cache, block_table, seq_lens, query_start, device_status,
+    # (a dimension of one has no stride of its own: not the usual kind)
+    ks, vs = k.stride(), v.stride()
+    if (T > 1 and Hkv > 1 and k.dtype is _BF16 and ks[1] == D and ks[2] == 1
+            and v.dtype is _BF16 and v.shape == shape and vs[1] == D and vs[2] == 1 and v.get_device() == index
+            and (kv_scales is None or kv_scales.get_device() == index)
+            and _usual_batch(index, cos_sin, kv_cache, block_table, seq_lens, query_start, device_status)
+            and (q is None or Hq > 1 and (qs := _head_rows(q, T, D, index))
+                 and (q_out is None or q_out.shape == q_shape and (qos := _head_rows(q_out, T, D, index))))):
+        ks, vs = ks[0], vs[0]
+    else:
+        ks, = _check_rows(k, "k", (T, Hkv, D), 2)
+        vs, = _check_rows(v, "v", (T, Hkv, D), 2)
+        if q is not None:
+            qs, = _check_rows(q, "q", (T, Hq, D), 2)
+            if q_out is not None:
+                qos, = _check_rows(q_out, "q_out", (T, Hq, D), 2)
+        _check_append(cos_sin, None, kv_cache, block_table, seq_lens, query_start, device_status,
                       (("k", k), ("v", v), ("q", q), ("q_out", q_out), ("kv_scales", kv_scales)))
-    if index != torch.cuda.current_device():
+    B, max_blocks = block_table.shape
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start, q=q, q_out=q_out,
                                    kv_scales=kv_scales, k_scale=k_scale, v_scale=v_scale, interleaved=interleaved,
@@ -745,8 +771,8 @@ def gqa_rope_append(k, v, cos_sin, kv_cache, block_table, seq_lens, query_start,
         return q_out
     rc = lib.gqa_rope_append(_raw(q), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(), query_start.data_ptr(),
                              seq_lens.data_ptr(), block_table.data_ptr(), _raw(q_out), kv_cache.data_ptr(),
-                             _raw(kv_scales), float(k_scale), float(v_scale), T, B, Hq, Hkv, D, cos_sin.shape[1],
-                             1 if interleaved else 0, cos_sin.shape[0], nb, page, block_table.shape[1], block, code,
+                             _raw(kv_scales), float(k_scale), float(v_scale), T, B, Hq, Hkv, D, table[1],
+                             1 if interleaved else 0, table[0], nb, page, max_blocks, block, code,
                              qs, ks, vs, qos, _raw(device_status), _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "gqa_rope_append")
@@ -760,31 +786,49 @@ def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_
     q_pe_out (for instance ``q[..., R:]`` of the absorbed query; may be q_pe itself; allocated when only q_pe is
     given), which is returned (None without q_pe).  cos_sin fp32 [max_position, 64]; the batch is described as for
     :func:`gqa_rope_append`."""
-    if kv_c.dim() != 2 or kv_cache.dim() != 3:
+    shape, rows, table = kv_c.shape, kv_cache.shape, cos_sin.shape
+    if len(shape) != 2 or len(rows) != 3:
         raise ValueError("kv_c must be [tokens, kv_lora_rank] and kv_cache [num_blocks, page, head_size]")
-    T, R = kv_c.shape
-    nb, page, D = kv_cache.shape
+    T, R = shape
+    nb, page, D = rows
     if D != R + 64:
         raise ValueError(f"kv_cache must be [num_blocks, page, {R + 64}]")
     code = _kv_code(kv_cache, kv_dtype)
     if kv_cache.element_size() != (2 if code == KV_BF16 else 1):
         raise TypeError(f"kv_cache must have {2 if code == KV_BF16 else 1}-byte elements, got {kv_cache.dtype}")
-    cs, = _check_rows(kv_c, "kv_c", (T, R), 1)
-    ps, = _check_rows(k_pe, "k_pe", (T, 64), 1)
+    index = kv_c.get_device()
     H = qs = qhs = qos = qohs = 0
     if q_pe is not None:
-        if q_pe.dim() != 3:
+        q_shape = q_pe.shape
+        if len(q_shape) != 3:
             raise ValueError("q_pe must be [tokens, heads, 64]")
-        H = q_pe.shape[1]
-        qs, qhs = _check_rows(q_pe, "q_pe", (T, H, 64), 1)
-        if q_pe_out is not None:
-            qos, qohs = _check_rows(q_pe_out, "q_pe_out", (T, H, 64), 1)
+        H = q_shape[1]
     elif q_pe_out is not None:
         raise ValueError("q_pe_out without q_pe")
-    index = kv_c.get_device()
-    B = _check_append(index, cos_sin, 64, kv_cache, block_table, seq_lens, query_start, device_status,
+    cs, ps = kv_c.stride(), k_pe.stride()
+    if (T > 1 and kv_c.dtype is _BF16 and cs[1] == 1 and k_pe.dtype is _BF16 and k_pe.shape == (T, 64) and ps[1] == 1
+            and k_pe.get_device() == index and len(table) == 2 and table[1] == 64
+            and _usual_batch(index, cos_sin, kv_cache, block_table, seq_lens, query_start, device_status)
+            and (q_pe is None or H > 1 and q_pe.dtype is _BF16 and q_shape[0] == T and q_shape[2] == 64
+                 and (qst := q_pe.stride())[2] == 1 and q_pe.get_device() == index
+                 and (q_pe_out is None or q_pe_out.dtype is _BF16 and q_pe_out.shape == q_shape
+                      and (qost := q_pe_out.stride())[2] == 1 and q_pe_out.get_device() == index))):
+        cs, ps = cs[0], ps[0]
+        if q_pe is not None:
+            qs, qhs, _ = qst
+            if q_pe_out is not None:
+                qos, qohs, _ = qost
+    else:
+        cs, = _check_rows(kv_c, "kv_c", (T, R), 1)
+        ps, = _check_rows(k_pe, "k_pe", (T, 64), 1)
+        if q_pe is not None:
+            qs, qhs = _check_rows(q_pe, "q_pe", (T, H, 64), 1)
+            if q_pe_out is not None:
+                qos, qohs = _check_rows(q_pe_out, "q_pe_out", (T, H, 64), 1)
+        _check_append(cos_sin, 64, kv_cache, block_table, seq_lens, query_start, device_status,
                       (("kv_c", kv_c), ("k_pe", k_pe), ("q_pe", q_pe), ("q_pe_out", q_pe_out)))
-    if index != torch.cuda.current_device():
+    B, max_blocks = block_table.shape
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_start, q_pe=q_pe,
                                    q_pe_out=q_pe_out, k_scale=k_scale, interleaved=interleaved, kv_dtype=kv_dtype,
@@ -798,8 +842,8 @@ def mla_rope_append(kv_c, k_pe, cos_sin, kv_cache, block_table, seq_lens, query_
         return q_pe_out
     rc = lib.mla_rope_append(kv_c.data_ptr(), k_pe.data_ptr(), _raw(q_pe), cos_sin.data_ptr(),
                              query_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), _raw(q_pe_out),
-                             kv_cache.data_ptr(), float(k_scale), T, B, H, D, R, 1 if interleaved else 0, cos_sin.shape[0],
-                             nb, page, block_table.shape[1], code, cs, ps, qs, qhs, qos, qohs, _raw(device_status),
+                             kv_cache.data_ptr(), float(k_scale), T, B, H, D, R, 1 if interleaved else 0, table[0],
+                             nb, page, max_blocks, code, cs, ps, qs, qhs, qos, qohs, _raw(device_status),
                              _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "mla_rope_append")
