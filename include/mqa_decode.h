@@ -440,9 +440,9 @@ mqa_status gqa_paged_decode(const void* q, const void* kv_cache, const int32_t* 
 
 /* Workspace bytes of gqa_window_decode and gqa_block_decode: 0 for
  * num_kv_splits == 1; else with rows = q_len * num_q_heads / num_kv_heads and
- * v = batch * ceil(rows / 16), partials p = v * num_kv_splits * num_kv_heads *
- * min(rows, 16) of head_size + 1 fp32 (the last rounded up to 8 bytes in all)
- * and 8 v bytes.  0 on invalid arguments. */
+ * r = ceil(rows / 24) blocks of query rows, v = batch * r, partials p = v *
+ * num_kv_splits * num_kv_heads * ceil(rows / r) of head_size + 1 fp32 (the last
+ * rounded up to 8 bytes in all) and 8 v bytes.  0 on invalid arguments. */
 size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
                                          int num_kv_splits);
 
@@ -475,8 +475,8 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
  *   window     >= 1 (2^30 and above: no window); sinks >= 0.
  *   out        bf16 [batch, q_len, num_q_heads, head_size], fully written.
  *   lse        fp32 [batch, q_len, num_q_heads] or NULL.
- *   num_kv_splits  1: one thread block per request and 16 query rows, in a
- *              fixed order (reproducible, independent of the rest of the
+ *   num_kv_splits  1: one thread block per request and block of query rows, in
+ *              a fixed order (reproducible, independent of the rest of the
  *              batch); more: the batch's visible tokens cut into units of
  *              equal size, num_kv_splits - 1 per request on average at most.
  *              Results are reproducible at any value.

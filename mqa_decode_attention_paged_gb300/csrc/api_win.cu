@@ -32,8 +32,8 @@ Rows rows_of(int q_len, int hq, int hkv) {
     Rows r;
     r.grp = hq / hkv;
     r.rows = q_len * r.grp;
-    r.rb = (r.rows + 15) / 16;
-    r.rbn = r.rows < 16 ? r.rows : 16;
+    r.rb = (r.rows + mqa::kWinMaxRows - 1) / mqa::kWinMaxRows;
+    r.rbn = (r.rows + r.rb - 1) / r.rb;  // (the last block has a row at least)
     return r;
 }
 
@@ -129,7 +129,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     const mqa::WinKind kind = kv_dtype == MQA_KV_BF16         ? mqa::kWinBf16
                               : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::kWinInt8
                                                               : mqa::kWinE4m3;
-    const int nhb = r.rbn <= 8 ? 1 : 2;
+    const int nhb = mqa::win_row_groups(r.rbn);
     const int warp_tok = 16 * mqa::win_mblocks(kind, nhb, head_size);
     a.ts = mqa::win_subtiles(num_kv_heads);
     a.tt_log = 0;

@@ -2,7 +2,7 @@
 // of the stage-1 kernels, and the host interface.
 //
 // A request's query rows (q_len positions x the query heads of a KV head) are
-// cut into row blocks of 16; request and row block together are one "virtual
+// cut into row blocks of up to 24; request and row block together are one "virtual
 // request" v = b * rb + r with its own keys.  The query at position p sees
 // key t iff  t <= p and (t < sinks or t > p - window), so the keys of a row
 // block are the sinks [0, min(sinks, hi)) and the run [lo, hi), where hi is
@@ -58,7 +58,7 @@ struct WinArgs {
     int window, sinks;
     int scale_block, scale_groups;  // tokens per scale, scales per page
     int box_tok;                    // tokens of one copied box (divides the page and a warp's tile)
-    int rb, rbn;                    // row blocks per request; rows of a (full) row block
+    int rb, rbn;                    // row blocks per request; rows of a (full) row block, up to kWinMaxRows
     int ts, tt_log;                 // warps that share a KV head; log2 of a tile's tokens (all of them)
     FastDiv page_div, scale_div, grp_div, rb_div;
     int units;                      // 0: one unit per virtual request, else the balanced unit count
@@ -88,7 +88,7 @@ __device__ __forceinline__ int win_len(const WinArgs& a, int b, int* status) {
 
 __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
     WinVis v;
-    const int r0 = r * 16, r1 = min(a.rows, r0 + 16) - 1;
+    const int r0 = r * a.rbn, r1 = min(a.rows, r0 + a.rbn) - 1;
     const int i0 = a.q_len == 1 ? 0 : a.grp_div(r0), i1 = a.q_len == 1 ? 0 : a.grp_div(r1);
     const int tl = a.tt_log, up = (1 << tl) - 1;
     v.n = n;
@@ -126,15 +126,22 @@ __device__ __forceinline__ int win_unit_start(int T, int U, int g) {
 // does not divide 8 evenly.
 __host__ __device__ inline int win_subtiles(int hkv) { return hkv == 1 ? 8 : (hkv == 2 ? 4 : (hkv <= 4 ? 2 : 1)); }
 
-// Thread blocks of stage 1 resident on one SM: one where 9 to 16 rows meet head
-// size 128 (32 windows of 4096, 16 rows, e4m3: 74 us against 92 with two; with
+// Query rows of a row block at most, and row groups of 8 that they make.  (Four
+// groups spill with head size 128: 32 rows take 86 us as one block, 72 as two,
+// 16 requests of 4096 tokens, e4m3.)
+constexpr int kWinMaxRows = 24;
+__host__ __device__ constexpr int win_row_groups(int rbn) { return (rbn + 7) / 8; }
+
+// Thread blocks of stage 1 resident on one SM: one where more than 8 rows meet
+// head size 128 (32 windows of 4096, 16 rows, e4m3: 74 us against 92 with two; with
 // head size 64 300 windows of 128 with 12 rows take 57 us with one, 39 with two).
-__host__ __device__ constexpr int win_ctas_per_sm(int nhb, int D) { return nhb == 1 || D == 64 ? 2 : 1; }
+__host__ __device__ constexpr int win_ctas_per_sm(int nhb, int D) { return nhb == 1 || (D == 64 && nhb == 2) ? 2 : 1; }
 constexpr int kWinMaxCtasPerSm = 2;
 
 // 16-token MMA blocks of a warp's tile, as many as the registers carry beside
 // the accumulators.
 __host__ __device__ constexpr int win_mblocks(int kind, int nhb, int D) {
+    if (nhb == 3) return D == 64 ? 4 : kind == kWinBf16 ? 1 : 2;
     if (D == 64) return kind != kWinBf16 && nhb == 1 ? 4 : 2;
     return kind != kWinBf16 || nhb == 2 ? 2 : 1;
 }

@@ -5,13 +5,13 @@
 // with s_k, s_v the scales of the token block and head (1 for bf16).
 //
 // What bounds it: the bytes of the visible keys and values, read once (a
-// row block of up to 16 rows does 8 multiply-adds per byte of bf16 cache and
+// row block of up to 24 rows does 12 multiply-adds per byte of bf16 cache and
 // twice that per 8-bit byte, far below the tensor rate), and, with an 8-bit
 // cache, the instructions that widen the codes.
 //
 // One thread block = up to 8 warps, two blocks per SM (128 registers a
-// thread), or one where 9 to 16 rows meet head size 128 (accumulators and Q
-// alone are 96 registers).  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
+// thread), or one where more than 8 rows meet head size 128 (accumulators and Q
+// of 16 rows alone are 96 registers) or more than 16 head size 64.  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
 // feeds itself: it keeps a ring of slots in shared memory, copies its own
 // head's K rows and then V rows of a tile into it with tensor copies (16 or 32
 // token rows of one head, 128-byte or 64-byte swizzle: ldmatrix over eight
@@ -31,7 +31,9 @@
 // the merge; 9 to 16 rows per KV head by instructions (32 windows of 4096 over
 // e4m3, 16 rows, head size 128: 69 us; with two blocks per SM, half the tokens
 // per step and Q in shared memory it was 89 us and 730 instructions per 16
-// tokens and head).
+// tokens and head).  17 to 24 rows are one row block: 32 windows of 2000, 20
+// rows, take 60 (bf16) and 60 (e4m3) us, as two blocks of 16 and 4 rows they took
+// 95 and 73.
 //   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows),
 //     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.
 //   * 8-bit codes stay codes in shared memory and are widened to f16 in
@@ -78,7 +80,14 @@ struct Cfg {
     static constexpr int kMT = win_mblocks(KIND, NHB, D);
     static constexpr int kTok = 16 * kMT;            // tokens of a warp's tile
     static constexpr int kSlot = kTok * D * kElt;    // bytes of a slot (one plane of it)
-    static constexpr int kExch = (16 + 6 * NHB) * 128;         // one warp's hand-over buffer
+    // A lane hands its accumulators to another warp 16 at a time, or all at once
+    // where eight full rings, four warps' buffers and 26 KB for the rest fit
+    // (42 requests, 35 rows of one KV head, int8: 47 -> 42 us)
+    static constexpr int kAll = 4 * NHB * kSteps, kTail = 6 * NHB;
+    static constexpr bool kRoom = 8 * kMaxSlots * kSlot + 4 * (kAll + kTail) * 128 + 26 * 1024 <=
+                                  228 * 1024 / win_ctas_per_sm(NHB, D);
+    static constexpr int kHanded = kRoom ? kAll : 16;
+    static constexpr int kExch = (kHanded + kTail) * 128;  // one warp's hand-over buffer
 };
 
 struct Layout {
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
     // virtual requests without a key: out = 0, lse = -inf
     for (int v = blockIdx.x; v < vb; v += gridDim.x) {
         if (cum[v + 1] > cum[v]) continue;
-        const int b = a.rb_div(v), r0 = (v - b * a.rb) * 16, rows = min(a.rows - r0, 16);
+        const int b = a.rb_div(v), r0 = (v - b * a.rb) * a.rbn, rows = min(a.rows - r0, a.rbn);
         for (int i = threadIdx.x; i < Hkv * rows * (D / 8); i += blockDim.x) {
             const int h = i / (rows * (D / 8)), R = r0 + i / (D / 8) % rows, qi = R / a.grp;
             const long long orow = (static_cast<long long>(b) * a.q_len + qi) * a.Hq + h * a.grp + R - qi * a.grp;
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
         if (issued < loads) issue();
     };
 
-    constexpr int kParts = NHB * C::kSteps / 4;  // of a warp's hand-over to another
+    constexpr int kParts = 4 * NHB * C::kSteps / C::kHanded;  // of a warp's hand-over to another
     const int tiles = p1 - p0;
     int tile = 0;
     // Positions of a row block's rows, worked out where they are wanted (the
@@ -475,10 +484,10 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
     };
     auto rows_of = [&](int z) {
         const int v = z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
-        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16, n = lens[b];
+        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * a.rbn, n = lens[b];
         if (!MULTI) return Rows{n - 1, n - 1, 0};
         const int i0 = a.grp_div(row0);
-        return Rows{n - a.q_len + i0, n - a.q_len + a.grp_div(min(a.rows, row0 + 16) - 1), row0 - i0 * a.grp};
+        return Rows{n - a.q_len + i0, n - a.q_len + a.grp_div(min(a.rows, row0 + a.rbn) - 1), row0 - i0 * a.grp};
     };
     uint32_t qb[NHB][C::kSteps][2];
     float o[NHB][C::kSteps][4];
@@ -503,7 +512,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
 
         if (d.z & kFirst) {
             const int v = d.z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
-            const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
+            const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * a.rbn;
             if (a.units > 0 && threadIdx.x == 0) {
                 // every request's first and last unit, for the merge
                 int2* u = a.ws_units + v;
@@ -815,19 +824,20 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
             }
         if (TS > 1) {
             for (int half = TS / 2; half >= 1; half >>= 1) {
-                // warp sub + half hands its state to warp sub, 16 values of a
-                // row group at a time
+                // warp sub + half hands its state to warp sub
                 float* buf = reinterpret_cast<float*>(smem + lay.exch) +
                              ((sub & (half - 1)) * Hkv + kh) * (C::kExch / 4) + lane;
-                float* tail = buf + 16 * 32;
+                float* tail = buf + C::kHanded * 32;
                 const bool gives = sub >= half && sub < 2 * half, takes = sub < half;
                 float f0[NHB][2], f1[NHB][2];
 #pragma unroll
                 for (int part = 0; part < kParts; ++part) {
-                    const int hb = part / (C::kSteps / 4), m0 = part % (C::kSteps / 4) * 4;
                     if (gives) {
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) buf[y * 32] = o[hb][m0 + y / 4][y % 4];
+                        for (int y = 0; y < C::kHanded; ++y) {
+                            const int i = part * C::kHanded + y;
+                            buf[y * 32] = o[i / (4 * C::kSteps)][i / 4 % C::kSteps][i % 4];
+                        }
                         if (part == 0)
 #pragma unroll
                             for (int y = 0; y < 2 * NHB; ++y) {
@@ -852,9 +862,11 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
                                 r_ref[h][e] = r;
                             }
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            o[hb][m0 + y / 4][y % 4] =
-                                o[hb][m0 + y / 4][y % 4] * f0[hb][y & 1] + buf[y * 32] * f1[hb][y & 1];
+                        for (int y = 0; y < C::kHanded; ++y) {
+                            const int i = part * C::kHanded + y, hb = i / (4 * C::kSteps);
+                            float& x = o[hb][i / 4 % C::kSteps][i % 4];
+                            x = x * f0[hb][i & 1] + buf[y * 32] * f1[hb][i & 1];
+                        }
                     }
                     named_bar_sync(1, 32 * NC);
                 }
@@ -864,7 +876,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
 
         // ---- epilogue: rows hb * 8 + 2c + e; head dims by kind (see the top)
         const int v = d.z & kVMask, b = a.rb == 1 ? v : a.rb_div(v);
-        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * 16;
+        const int row0 = a.rb == 1 ? 0 : (v - b * a.rb) * a.rbn;
 #pragma unroll
         for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
@@ -956,16 +968,25 @@ cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     while (ns > 2 && layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total > limit) --ns;
     a.nslots = ns;
     const int bytes = layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total;
-    auto kern = a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true> : gqa_win_kernel<D, KIND, NHB, false>;
+    // (more than 16 rows of a KV head are several positions')
+    auto kern = NHB > 2 || a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true>
+                                       : gqa_win_kernel<D, KIND, NHB <= 2 ? NHB : 1, false>;
     if (cudaError_t e = allow_smem<D, KIND, NHB>(reinterpret_cast<const void*>(kern), a.q_len > 1); e != cudaSuccess) return e;
     return launch_with_pdl(kern, dim3(grid), dim3(32 * a.Hkv * a.ts), bytes, stream, a);
 }
 
+template <int D, int KIND>
+cudaError_t dispatch_rows(const WinArgs& a, int grid, cudaStream_t stream) {
+    switch (win_row_groups(a.rbn)) {
+        case 1: return launch<D, KIND, 1>(a, grid, stream);
+        case 2: return launch<D, KIND, 2>(a, grid, stream);
+        default: return launch<D, KIND, 3>(a, grid, stream);
+    }
+}
+
 template <int KIND>
 cudaError_t dispatch(const WinArgs& a, int D, int grid, cudaStream_t stream) {
-    if (D == 128)
-        return a.rbn <= 8 ? launch<128, KIND, 1>(a, grid, stream) : launch<128, KIND, 2>(a, grid, stream);
-    return a.rbn <= 8 ? launch<64, KIND, 1>(a, grid, stream) : launch<64, KIND, 2>(a, grid, stream);
+    return D == 128 ? dispatch_rows<128, KIND>(a, grid, stream) : dispatch_rows<64, KIND>(a, grid, stream);
 }
 
 }  // namespace win

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_con
     const int b = a.rb_div(v), r = v - b * a.rb;
     const int item = WPR == 1 ? static_cast<int>(blockIdx.y) * kWarps + warp : static_cast<int>(blockIdx.y);
     const int kh = item / a.rbn, jr = item - kh * a.rbn;
-    const int R = r * 16 + jr;
+    const int R = r * a.rbn + jr;
     pdl_wait();  // stage 1 is done (every warp waits, so that this grid ends after it)
     const int2 units = a.ws_units[v];
     const int gf = units.x, np = units.y - units.x + 1;

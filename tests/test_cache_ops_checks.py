@@ -128,8 +128,9 @@ def test_workspace_bytes():
     assert f(3, 1, 32, 8, 128, 1) == 0
     assert f(3, 1, 32, 8, 128, 5) == 3 * 5 * 8 * 4 * 129 * 4 + 3 * 8
     assert f(1, 1, 1, 1, 64, 3) == 3 * 64 * 4 + 16 + 8
-    # 5 positions x 4 heads = 20 rows of a KV head: two row blocks of 16
-    assert f(3, 5, 32, 8, 64, 2) == 3 * 2 * 2 * 8 * 16 * 65 * 4 + 6 * 8
+    # 5 positions x 4 heads = 20 rows of a KV head: one row block; 7 x 4 = 28: two of 14
+    assert f(3, 5, 32, 8, 64, 2) == 3 * 2 * 8 * 20 * 65 * 4 + 3 * 8
+    assert f(3, 7, 32, 8, 64, 2) == 3 * 2 * 2 * 8 * 14 * 65 * 4 + 6 * 8
     assert f(0, 1, 32, 8, 128, 5) == 0 and f(3, 1, 33, 8, 128, 5) == 0 and f(3, 40, 32, 8, 128, 5) == 0
 
 

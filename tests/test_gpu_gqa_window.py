@@ -429,3 +429,28 @@ def test_graphs_of_cut_requests():
         torch.cuda.synchronize()
         for _, (out, lse), _ in graphs:
             check(case, out.cpu().double(), lse.cpu().double(), what=f"replay {lens}")
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("L,Hq,Hkv,D", [(5, 32, 8, 128), (12, 2, 1, 128), (5, 7, 1, 128), (9, 10, 5, 64), (24, 1, 1, 64),
+                                        (25, 4, 4, 128), (7, 28, 4, 64)])
+def test_blocks_of_many_rows(kv, L, Hq, Hkv, D):
+    # 17 to 24 rows in one block, more in blocks of unlike sizes; whole and cut, with values that some rows must not see
+    for window, sinks in ((9, 2), (NONE, 0)):
+        case = Case([0, L - 1, L + 2, 60, 500], Hq, Hkv, D, 32, kv, L=L, window=window, sinks=sinks, group=16, seed=20)
+        run_and_check(case, (1, None), f"{kv} L={L} {Hq}/{Hkv}x{D} W={window}")
+        run_and_check(widen(case), (3,), f"{kv} L={L} {Hq}/{Hkv}x{D} W={window} cut")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3_block"])
+def test_non_finite_value_among_many_rows(kv):
+    # 20 rows of a block: the last token's V is NaN and seen by the last position only
+    L, n = 5, 90
+    case = Case([n], 8, 2, 64, 16, kv, L=L, window=32, sinks=0, seed=21)
+    raw = case.cache if kv == "bf16" else case.cache.view(torch.uint8)
+    raw[case.bt[0, (n - 1) // 16], 1, (n - 1) % 16] = float("nan") if kv == "bf16" else 0x7f
+    out, lse, _ = case.run(1)
+    (_, (o, l, tol_o, tol_l)), = case.reference()
+    assert ((out[0, :L - 1] - o[:L - 1]).abs() <= tol_o[:L - 1]).all()
+    assert not torch.isfinite(out[0, L - 1]).any()
+    assert ((lse[0] - l).abs() <= tol_l).all()
