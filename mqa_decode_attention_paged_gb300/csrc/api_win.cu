@@ -66,18 +66,19 @@ bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, long
 // costs partials and a merge, about 4 us.  One multiprocessor takes in 70 GB/s
 // of bf16, 35 GB/s of codes, which it widens; two blocks on it take 2.6 (1.6)
 // times as long as one.  Longer windows hold requests of unlike lengths more
-// often than not, and are cut whatever their number.  Measured whole / cut in
-// us, 32/8 heads x 128, bf16, windows of 128, 512 and 1024 tokens: 150 requests
-// 21 / 27, 54 / 62 and 97 / 109, 200 requests 30 / 34, 95 / 79 and 176 / 140, 304
-// requests 37 / 46, 105 / 114 and 200 / 209; 64/8 heads x 64, int8, window 128:
-// 100, 150, 200 and 256 requests 12 / 14, 13 / 19, 17 / 24, 18 / 25.
+// often than not, and are cut (60 us).  Measured whole / cut in us, 32/8 heads x
+// 128, bf16, windows of 128, 512 and 1024 tokens: 150 requests 21 / 27, 54 / 61
+// and 96 / 103, 200 requests 30 / 32, 95 / 77 and 176 / 135, 304 requests 37 / 44,
+// 106 / 110 and 202 / 196 (of 1 to 3000 tokens: 36 / 44, 102 / 102, 181 / 167);
+// 64/8 heads x 64, int8, window 128: 100, 150, 200 and 256 requests 12 / 14, 13 /
+// 19, 17 / 24, 18 / 25.
 bool whole_requests(const mqa::WinArgs& a, int elt, int head_size, int sms) {
     const long long tt = 1LL << a.tt_log, all = (static_cast<long long>(a.max_blocks) * a.page + tt - 1) / tt;
     const long long seen = (a.sinks + tt - 1) / tt + (static_cast<long long>(a.window) + a.q_len - 2 + tt) / tt + 1;
     const double bytes = static_cast<double>(seen < all ? seen : all) * tt * 2 * a.Hkv * head_size * elt;
     const int vb = a.batch * a.rb;
     const double own = bytes / (elt == 2 ? 70e3 : 35e3), pair = vb <= sms ? 1.0 : elt == 2 ? 2.6 : 1.6;
-    return own <= 100.0 && own * pair <= vb * bytes / 6.5e6 + 4.0;
+    return own * pair <= 60.0 && own * pair <= vb * bytes / 6.5e6 + 4.0;
 }
 
 mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
@@ -177,11 +178,17 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         // unit g and virtual request v use slot g + v <= units + vb - 2
         const long long cap = static_cast<long long>(vb) * (num_kv_splits - 1) + 1;
         const long long fill = static_cast<long long>(sms) * mqa::win_ctas_per_sm(nhb, head_size);
-        a.units = static_cast<int>(fill < cap ? fill : cap);
+        // One unit per multiprocessor over bf16 (a block then has a ring of four
+        // slots; one request of 8000 or 60000 tokens, 32/8 heads x 128: 13 and 45
+        // us, with two units 17 and 55), and over codes where two would leave more
+        // than 100 partials a row (one request of 8000, 64/8 heads: 13, 19 us).
+        const long long units = kind == mqa::kWinBf16 || fill > 100LL * vb ? sms : fill;
+        a.units = static_cast<int>(units < cap ? units : cap);
         if (vb <= fill && whole_requests(a, elt, head_size, sms)) a.units = 0;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = a.units > 0 ? a.units : vb;
+    a.alone = grid <= sms;
     const cudaError_t e = kind == mqa::kWinBf16   ? mqa::win_stage1_bf16(a, head_size, grid, st)
                           : kind == mqa::kWinInt8 ? mqa::win_stage1_int8(a, head_size, grid, st)
                                                   : mqa::win_stage1_e4m3(a, head_size, grid, st);

@@ -63,6 +63,7 @@ struct WinArgs {
     FastDiv page_div, scale_div, grp_div, rb_div;
     int units;                      // 0: one unit per virtual request, else the balanced unit count
     int nslots;                     // slots of a warp's ring
+    bool alone;                     // no more blocks than multiprocessors: each may take one's shared memory
     int withhold;  // test hook of the bounded waits: this unit copies nothing (-1 in every product call)
 };
 

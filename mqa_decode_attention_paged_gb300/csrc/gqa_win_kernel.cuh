@@ -963,7 +963,7 @@ cudaError_t allow_smem(const void* kern, bool multi) {
 template <int D, int KIND, int NHB>
 cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     const int vb = a.batch * a.rb;
-    constexpr int limit = 228 * 1024 / win_ctas_per_sm(NHB, D) - 1024;  // a block's share of the SM's shared memory
+    const int limit = 228 * 1024 / (a.alone ? 1 : win_ctas_per_sm(NHB, D)) - 1024;  // a block's share of an SM's
     int ns = kMaxSlots;
     while (ns > 2 && layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total > limit) --ns;
     a.nslots = ns;
