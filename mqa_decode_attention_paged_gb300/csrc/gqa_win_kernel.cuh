@@ -10,8 +10,10 @@
 // cache, the instructions that widen the codes.
 //
 // One thread block = up to 8 warps, two blocks per SM (128 registers a
-// thread), or one where more than 8 rows meet head size 128 (accumulators and Q
-// of 16 rows alone are 96 registers) or more than 16 head size 64.  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
+// thread; over bf16 one reads at full rate, and that is what is launched where
+// requests are cut), or one where more than 8 rows meet head size 128
+// (accumulators and Q of 16 rows alone are 96 registers) or more than 16 head
+// size 64.  Warp w takes KV head w % Hkv and part w / Hkv of every tile, and
 // feeds itself: it keeps a ring of slots in shared memory, copies its own
 // head's K rows and then V rows of a tile into it with tensor copies (16 or 32
 // token rows of one head, 128-byte or 64-byte swizzle: ldmatrix over eight
