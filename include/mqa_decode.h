@@ -448,8 +448,7 @@ size_t gqa_window_decode_workspace_bytes(int batch, int q_len, int num_q_heads, 
 
 /* The smallest num_kv_splits (at least 2) with which gqa_window_decode and
  * gqa_block_decode can spread such a batch over the whole current device,
- * whatever the head size; -1
- * on invalid arguments or without a device. */
+ * whatever the head size; -1 on invalid arguments or without a device. */
 int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_heads);
 
 /* GQA paged decode under a sliding window, the first tokens staying visible.
@@ -478,8 +477,9 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
  *   num_kv_splits  1: one thread block per request and block of query rows, in
  *              a fixed order (reproducible, independent of the rest of the
  *              batch); more: the batch's visible tokens cut into units of
- *              equal size, num_kv_splits - 1 per request on average at most.
- *              Results are reproducible at any value.
+ *              equal size, num_kv_splits - 1 per request on average at most
+ *              (requests that the window or the width of the block table makes
+ *              short stay whole).  Results are reproducible at any value.
  *   workspace  gqa_window_decode_workspace_bytes(...) bytes; its contents do
  *              not matter.  Calls that may overlap need one each.
  *   head_size in {64, 128}; num_kv_heads in [1, 8]; at most 16 query heads per

@@ -28,9 +28,9 @@
 //
 // Measured (batch of 256, lognormal lengths, 32/8 heads x 128, 16-token pages,
 // e4m3 with a scale per page and head): 259 us, 6.4 TB/s of the 6.67 a copy
-// reaches; 64 windows of 16384 tokens over bf16: 661 us, 6.5 TB/s.  Short
-// windows are bound by the start (4.3 us until the copies are issued) and
-// the merge; 9 to 16 rows per KV head by instructions (32 windows of 4096 over
+// reaches; 64 windows of 16384 tokens over bf16: 594 us, 7.2 TB/s (reads alone
+// run faster than a copy).  Short windows are bound by the start (4.3 us until
+// the copies are issued) and the merge; 9 to 16 rows per KV head by instructions (32 windows of 4096 over
 // e4m3, 16 rows, head size 128: 69 us; with two blocks per SM, half the tokens
 // per step and Q in shared memory it was 89 us and 730 instructions per 16
 // tokens and head).  17 to 24 rows are one row block: 32 windows of 2000, 20
