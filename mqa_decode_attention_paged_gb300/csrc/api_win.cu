@@ -108,9 +108,9 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
         if (!kv_scales || !api_aligned(kv_scales, 4) || scale_block < 1) return MQA_ERR_INVALID_ARG;
         if (scale_block % 16 != 0 || page_size % scale_block != 0) return MQA_ERR_UNSUPPORTED;
     }
-    // positions stay clear of INT_MAX by more than a tile (256 tokens), cache
-    // rows (two planes of tokens) are ints
-    if (static_cast<long long>(max_blocks) * page_size > INT32_MAX - 512 ||
+    // positions stay clear of INT_MAX by more than a tile (512 tokens at most),
+    // cache rows (two planes of tokens) are ints
+    if (static_cast<long long>(max_blocks) * page_size > INT32_MAX - 1024 ||
         static_cast<long long>(num_blocks) * page_size > (1 << 30) - 1)
         return MQA_ERR_UNSUPPORTED;
 

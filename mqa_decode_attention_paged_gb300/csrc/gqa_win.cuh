@@ -2,8 +2,8 @@
 // of the stage-1 kernels, and the host interface.
 //
 // A request's query rows (q_len positions x the query heads of a KV head) are
-// cut into row blocks of up to 24; request and row block together are one "virtual
-// request" v = b * rb + r with its own keys.  The query at position p sees
+// cut into row blocks of up to 24; request and row block together are one
+// "virtual request" v = b * rb + r with its own keys.  The query at position p sees
 // key t iff  t <= p and (t < sinks or t > p - window), so the keys of a row
 // block are the sinks [0, min(sinks, hi)) and the run [lo, hi), where hi is
 // its last position + 1 and lo = max(0, first position - window + 1).  They
