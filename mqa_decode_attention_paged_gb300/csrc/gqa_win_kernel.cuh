@@ -54,7 +54,9 @@
 //     the rows see V rows of keys that none sees are cleared in the slot, so
 //     stale or non-finite bytes never reach an accumulator (int8 codes are
 //     always finite).  Where a key is seen by some rows only and a V value is
-//     Inf or NaN, the rows are summed apart.
+//     Inf or NaN, the rows are summed apart; where a V scale is, the numerators'
+//     reference of the rows that see it becomes NaN, and the scale counts as 1
+//     (the weight of a masked key would be e^{-inf + inf}).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -634,6 +636,16 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
                             if (!act || !(key <= p && (key < a.sinks || key > p - a.window)))
                                 x[m][hb][e] = -INFINITY;
                         }
+                    if (MULTI && KIND != kWinBf16 && !(lvs[m] < INFINITY)) {
+                        // an Inf or NaN scale, for the rows that see a key of
+                        // it alone: their sums become NaN by way of the reference
+#pragma unroll
+                        for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (fmaxf(x[m][hb][e], x[m][hb][2 + e]) > -INFINITY) r_ref[hb][e] = NAN;
+                        lvs[m] = 0.f;
+                    }
                     if (KIND != kWinInt8) {
                         // V rows that no row sees become zeros: whatever bytes
                         // they hold (int8 codes are finite anyway)

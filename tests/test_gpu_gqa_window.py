@@ -454,3 +454,61 @@ def test_non_finite_value_among_many_rows(kv):
     assert ((out[0, :L - 1] - o[:L - 1]).abs() <= tol_o[:L - 1]).all()
     assert not torch.isfinite(out[0, L - 1]).any()
     assert ((lse[0] - l).abs() <= tol_l).all()
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3_block", "int8_block"])
+@pytest.mark.parametrize("bad", ["inf", "nan"])
+@pytest.mark.parametrize("L,Hq,Hkv,D", [(4, 8, 2, 64), (4, 8, 2, 128), (4, 8, 4, 128), (5, 40, 8, 128), (9, 8, 1, 64),
+                                        (3, 20, 2, 64)])
+def test_non_finite_value_scale_reaches_only_the_queries_that_see_it(kv, bad, L, Hq, Hkv, D):
+    # the last token starts a scale block whose V scale (of the first head) is Inf or NaN: the last position alone
+    # sees it; the first positions of the batch see no key at all or keys of that block only
+    n = 97
+    grp = Hq // Hkv
+    for lens, cut in (([n], False), ([n, 40, 1], True)):
+        case = Case(lens, Hq, Hkv, D, 16, kv, L=L, seed=22, poison=False)
+        want = dict(case.reference())  # (before the scale is planted: rows that do not see it)
+        case.scales[case.bt[0, 6], 1, :, 0] = float(bad)
+        if cut:
+            widen(case)
+        for splits in ((1,) if not cut else (3, None)):
+            out, lse, status = case.run(splits)
+            assert status == 0
+            for b, (o, l, tol_o, tol_l) in want.items():
+                ok = torch.ones(L, Hq, dtype=torch.bool)
+                if b == 0:
+                    ok[L - 1, :grp] = False
+                    assert not torch.isfinite(out[0, L - 1, :grp]).any(), f"{kv} {bad} splits={splits}"
+                assert ((out[b] - o).abs() <= tol_o)[ok].all(), f"{kv} {bad} splits={splits} request {b}"
+                dead = torch.isneginf(l)
+                assert torch.equal(torch.isneginf(lse[b]), dead) and (out[b][dead] == 0).all()
+                assert ((lse[b] - l).abs() <= tol_l)[~dead].all(), f"{kv} {bad} splits={splits} request {b}"
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3_block", "int8_block"])
+def test_appended_infinity_reaches_only_the_queries_that_see_it(kv):
+    # the scale as gqa_rope_append stores it: of four new tokens the last starts a scale block and holds an Inf
+    from test_gpu_append import table
+    L, old, Hq, Hkv, D = 4, 13, 8, 2, 64
+    case = Case([old + L - 1], Hq, Hkv, D, 16, kv, L=L, seed=23, poison=False)
+    q, cache, bt, sc, _ = case.dev()
+    bt[0, 1] = case.nb - 1 if int(bt[0, 0]) != case.nb - 1 else case.nb - 2
+    k, v = torch.randn(L, Hkv, D).to(torch.bfloat16), torch.randn(L, Hkv, D).to(torch.bfloat16)
+    v[L - 1, 0, 5] = float("inf")
+    lens = torch.tensor([old + L], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    rq = mqa.gqa_rope_append(k.cuda(), v.cuda(), table(32, D).cuda(), cache, bt, lens, starts,
+                             q=q[0].contiguous(), kv_scales=sc)
+    torch.cuda.synchronize()
+    assert torch.isinf(sc[bt[0, 1].item(), 1, 0, 0]) and torch.isfinite(sc[bt[0, 1].item(), 1, 0, 1])
+    case.cache, case.scales, case.q, case.lens = cache.cpu(), sc.cpu(), rq.cpu()[None], [old + L]
+    case.bt = case.bt_ref = bt.cpu()
+    grp = Hq // Hkv
+    case.scales[bt[0, 1].item(), 1, 0, 0] = 1.0  # for the rows that do not see it
+    (_, (o, l, tol_o, tol_l)), = case.reference()
+    for splits in (1, None):
+        out, lse, status = case.run(splits, [rq[None], cache, bt, sc, lens])
+        assert status == 0
+        assert ((out[0] - o).abs() <= tol_o)[:L - 1].all() and ((out[0] - o).abs() <= tol_o)[:, grp:].all()
+        assert not torch.isfinite(out[0, L - 1, :grp]).any()
+        assert ((lse[0] - l).abs() <= tol_l).all()
