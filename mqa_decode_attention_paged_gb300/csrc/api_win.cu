@@ -165,7 +165,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     a.num_blocks = num_blocks;
     a.page = page_size;
     a.max_blocks = max_blocks;
-    a.window = window < mqa::kWinNoWindow ? window : mqa::kWinNoWindow;
+    a.window = window < mqa::kWinNoWindow ? window : mqa::kWinUnbounded;
     a.sinks = sinks;
     a.withhold = withhold;
     a.scale_block = block ? scale_block : 1;

@@ -22,7 +22,10 @@ namespace mqa {
 enum WinKind { kWinBf16 = 0, kWinE4m3 = 1, kWinInt8 = 2 };
 
 constexpr int kWinMaxVirtual = 2048;  // virtual requests whose tile prefix fits in shared memory
-constexpr int kWinNoWindow = 1 << 30;
+constexpr int kWinNoWindow = 1 << 30;  // windows from here on are none
+// .. and the kernels take this one: beyond every position (lengths are at most
+// INT32_MAX - 1024), and a position, -128 at least, minus it is an int
+constexpr int kWinUnbounded = INT32_MAX - 1024;
 
 // Exact division of 0 <= n < 2^31 by a divisor known on the host: with l =
 // ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(m, n) + n)

@@ -512,3 +512,24 @@ def test_appended_infinity_reaches_only_the_queries_that_see_it(kv):
         assert ((out[0] - o).abs() <= tol_o)[:L - 1].all() and ((out[0] - o).abs() <= tol_o)[:, grp:].all()
         assert not torch.isfinite(out[0, L - 1, :grp]).any()
         assert ((lse[0] - l).abs() <= tol_l).all()
+
+
+def test_no_window_beyond_two_to_the_thirty_keys():
+    # one request of 2^30 + 2^16 tokens through a table that repeats a page: the first page holds the keys that count
+    page, columns, D = 1 << 16, (1 << 14) + 1, 64
+    cache = torch.zeros(2, 2, page, 1, D, dtype=torch.int8, device="cuda")
+    cache[0, 0], cache[0, 1] = 1, 100  # logits 25, values 100; the other page: logits 0, values 0
+    sc = torch.ones(2, 2, 1, 1, device="cuda")
+    bt = torch.ones(1, columns, dtype=torch.int32, device="cuda")
+    bt[0, 0] = 0
+    n = columns * page
+    sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = torch.ones(1, 1, D, dtype=torch.bfloat16, device="cuda")
+    # the weight of the first page's keys is 1 - 2.3e-7; lse is off by a few thousand fp32 additions
+    want = 25 + np.log(page + (n - page) * np.exp(-25.0))
+    for call in (lambda: mqa.gqa_block_decode(q, cache, sc, bt, sl, 25 / D),
+                 lambda: mqa.gqa_window_decode(q, cache, bt, sl, 25 / D, NONE, kv_scales=sc),
+                 lambda: mqa.gqa_window_decode(q, cache, bt, sl, 25 / D, (1 << 31) - 1, kv_scales=sc)):
+        out, lse = call()
+        assert (out.cpu().double() - 100).abs().max() <= 100 * 2 ** -8
+        assert abs(float(lse) - want) <= 4096 * 2 ** -24 + 2 ** -20 * want
