@@ -512,6 +512,11 @@ def _raw(t):
     return None if t is None else t.data_ptr()
 
 
+def _c_int(x):
+    """x as a C int, the nearest where it has none (ctypes would take it modulo 2^32)."""
+    return max(-(1 << 31), min(int(x), (1 << 31) - 1))
+
+
 def _call_stream(stream, index, allocated):
     """The raw stream of a call on device `index`, by default the current one.  Tensors that the call allocated (on
     the current stream) are recorded on a stream that the caller passes, so that their memory is not reused while
@@ -640,8 +645,8 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
                                   _raw(device_status), raw)
     else:
         rc = lib.gqa_window_decode(q.data_ptr(), kv_cache.data_ptr(), _raw(kv_scales), block_table.data_ptr(),
-                                   seq_lens.data_ptr(), float(scale), float(k_scale), float(v_scale), int(window),
-                                   int(sinks), out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb, page, bt_shape[1],
+                                   seq_lens.data_ptr(), float(scale), float(k_scale), float(v_scale), _c_int(window),
+                                   _c_int(sinks), out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb, page, bt_shape[1],
                                    block, code, int(num_kv_splits), _raw(workspace), ws_bytes, _raw(device_status), raw)
     if rc != OK:
         raise MqaError(rc, name)

@@ -533,3 +533,17 @@ def test_no_window_beyond_two_to_the_thirty_keys():
         out, lse = call()
         assert (out.cpu().double() - 100).abs().max() <= 100 * 2 ** -8
         assert abs(float(lse) - want) <= 4096 * 2 ** -24 + 2 ** -20 * want
+
+
+def test_windows_and_sinks_wider_than_an_int():
+    case = Case([90, 7, 300], 8, 2, 64, 16, "bf16", seed=24, poison=False)
+    q, kv, bt, _, sl = case.dev()
+    want = mqa.gqa_window_decode(q, kv, bt, sl, case.scale, NONE)
+    for window, sinks in (((1 << 32) + 5, 0), ((1 << 63) + 1, 0), ((1 << 33) + 1, 3), (1, (1 << 32) + 2),
+                          (1, (1 << 31) - 1)):
+        got = mqa.gqa_window_decode(q, kv, bt, sl, case.scale, window, sinks, num_kv_splits=1)
+        check(case, got[0].cpu().double(), got[1].cpu().double(), what=f"W={window} S={sinks}")
+    check(case, want[0].cpu().double(), want[1].cpu().double())
+    for window, sinks in ((-(1 << 32) + 5, 0), (5, -(1 << 32) + 5), (0, 0), (5, -1)):
+        with pytest.raises(mqa.MqaError):
+            mqa.gqa_window_decode(q, kv, bt, sl, case.scale, window, sinks)
