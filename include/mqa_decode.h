@@ -563,7 +563,9 @@ mqa_status gqa_rope_append(const void* q, const void* k, const void* v, const fl
  *   kv_c       bf16 [num_tokens, kv_lora_rank], k_pe bf16 [num_tokens, 64],
  *              each with a token stride; e4m3 stores e4m3(x / k_scale).
  *   q_pe, q_pe_out  bf16 [num_tokens, num_heads, 64] with token and head
- *              strides; both NULL: no queries.
+ *              strides; both NULL: no queries.  The rows of q_pe_out do not
+ *              overlap: the token stride holds a token's heads, or the head
+ *              stride a head's tokens.
  *   cos_sin    fp32 [max_position, 64].  head_size / kv_lora_rank 576/512 or
  *              320/256.  Other arguments and errors as for gqa_rope_append. */
 mqa_status mla_rope_append(const void* kv_c, const void* k_pe, const void* q_pe, const float* cos_sin,

@@ -112,6 +112,10 @@ mqa_status mla_rope_append(const void* kv_c, const void* k_pe, const void* q_pe,
     if (q_pe && (!stride_ok(q_pe_head_stride, 64) || !stride_ok(q_out_head_stride, 64) ||
                  !stride_ok(q_pe_stride, 64) || !stride_ok(q_out_stride, 64)))
         return MQA_ERR_INVALID_ARG;
+    // rows that are written lie apart: a token's heads within its stride, or a head's tokens within the head's
+    if (q_pe && q_out_stride < (num_heads - 1) * q_out_head_stride + 64 &&
+        q_out_head_stride < (num_tokens - 1) * q_out_stride + 64)
+        return MQA_ERR_INVALID_ARG;
     if (kv_dtype == MQA_KV_FP8_E4M3 && !scale_ok(k_scale)) return MQA_ERR_INVALID_ARG;
     if (num_tokens == 0) return MQA_OK;
     a.kv_c = static_cast<const __nv_bfloat16*>(kv_c);

@@ -221,3 +221,10 @@ def test_row_strides():
     assert mqa._check_rows(x[:, 2:6], "k", (7, 4, 64), 2) == (768,)
     assert mqa._check_rows(x[:1, 2:6], "k", (1, 4, 64), 2) == (256,)    # one token: no stride of its own
     assert mqa._check_rows(x[..., :64].transpose(0, 1), "q_pe", (12, 7, 64), 1) == (64, 768)
+
+
+def test_mla_append_refuses_overlapping_output_rows():
+    # two heads' or two tokens' rows of q_pe_out in the same place: which one stays would be left to chance
+    assert _mla_append(so=64, soh=64) == INV
+    assert _mla_append(so=576, soh=576) == INV
+    assert _mla_append(T=3, H=2, so=64, soh=128) == INV  # the third token meets the second head

@@ -476,3 +476,28 @@ def test_block_scaled_bad_requests_are_reported_by_number():
             assert torch.equal(got[own], cache[own]) and torch.equal(got_s[own], scales[own])
         assert torch.equal(got[~ok & ~torch.isin(torch.arange(bt.nb), bt.bt[1].long())],
                            cache[~ok & ~torch.isin(torch.arange(bt.nb), bt.bt[1].long())])
+
+
+def test_mla_query_rows_in_any_order():
+    # q_pe_out with a token's heads side by side, and with a head's tokens side by side; inputs that overlap
+    bt = Batch([1, 4], [3, 30], 16, seed=14)
+    R, H = 512, 3
+    cs, tb, sl, qs = bt.dev()
+    a = bt.randn(bt.T, R + 64).to(BF).cuda()
+    base = bt.randn(H + bt.T, 64).to(BF).cuda()
+    q = base.as_strided((bt.T, H, 64), (64, 64, 1))
+    want = None
+    for out in (torch.zeros(bt.T, H, 64, dtype=BF, device="cuda"),
+                torch.zeros(H, bt.T, 64, dtype=BF, device="cuda").transpose(0, 1),
+                torch.zeros(bt.T, H, R + 64, dtype=BF, device="cuda")[..., R:]):
+        cache = torch.zeros(bt.nb, 16, R + 64, dtype=BF, device="cuda")
+        got = mqa.mla_rope_append(a[:, :R], a[:, R:], cs, cache, tb, sl, qs, q_pe=q, q_pe_out=out)
+        torch.cuda.synchronize()
+        assert got is out
+        if want is None:
+            want = out.clone()
+            for t, _, p in bt.tokens():
+                check_rows(out.cpu()[t], q.cpu()[t], bt.cs[p], False, f"q token {t}")
+        assert torch.equal(out, want)
+    with pytest.raises(mqa.MqaError):
+        mqa.mla_rope_append(a[:, :R], a[:, R:], cs, cache, tb, sl, qs, q_pe=q, q_pe_out=q)
