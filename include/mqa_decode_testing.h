@@ -68,8 +68,9 @@ mqa_status mqa_test_mla_warp_gives_up(const void* q, const void* kv_cache, const
 /* A gqa_window_decode (k_scale = v_scale = 1) in which work unit
  * `withhold_unit` copies none of its tiles: its warps wait in vain, meet each
  * other all the same and return.  Arguments as for gqa_window_decode;
- * withhold_unit >= 0 (with num_kv_splits == 1, unit b is request b where 16
- * query rows hold a request). */
+ * withhold_unit >= 0 (with num_kv_splits == 1, unit b is request b where a
+ * row block of 24 query rows holds a request).  Outputs of the requests that
+ * the unit holds a part of are undefined. */
 mqa_status mqa_test_gqa_window_withheld(const void* q, const void* kv_cache, const float* kv_scales,
                                         const int32_t* block_table, const int32_t* seq_lens, float scale, int window,
                                         int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,

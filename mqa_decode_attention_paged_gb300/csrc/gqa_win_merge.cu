@@ -43,7 +43,8 @@ __global__ void __launch_bounds__(32 * kWarps) win_merge_kernel(const __grid_con
     const int2 units = a.ws_units[v];
     const int gf = units.x, np = units.y - units.x + 1;
     if (np == 1 || kh >= a.Hkv || R >= a.rows) return;
-    // (a unit that gave up may have left this entry unwritten)
+    // (a unit that gave up may have left this entry unwritten, or partials: the
+    // row is then undefined, and the status word says so)
     if (units.x < 0 || units.y < units.x || units.y >= a.units) return;
     const int i = a.grp_div(R);
     const long long orow = (static_cast<long long>(b) * a.q_len + i) * a.Hq + kh * a.grp + (R - i * a.grp);

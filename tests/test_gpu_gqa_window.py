@@ -547,3 +547,35 @@ def test_windows_and_sinks_wider_than_an_int():
     for window, sinks in ((-(1 << 32) + 5, 0), (5, -(1 << 32) + 5), (0, 0), (5, -1)):
         with pytest.raises(mqa.MqaError):
             mqa.gqa_window_decode(q, kv, bt, sl, case.scale, window, sinks)
+
+
+@pytest.mark.parametrize("kv,Hkv,L", [("bf16", 8, 3), ("bf16", 1, 5), ("fp8_e4m3_block", 1, 3), ("int8_block", 2, 5),
+                                      ("fp8_e4m3_block", 4, 5)])
+def test_a_wait_that_runs_out_among_cut_requests(kv, Hkv, L, monkeypatch):
+    # two and three row groups, requests that are cut and merged: the first unit, inside request 0, copies nothing;
+    # the others are exact, and so is the next call
+    monkeypatch.setenv("MQA_ENABLE_TEST_HOOKS", "1")
+    import ctypes
+    from mqa_decode_attention_paged_gb300 import _binding as binding
+    P, I, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    fn = binding.lib.mqa_test_gqa_window_withheld
+    fn.restype = I
+    fn.argtypes = [P, P, P, P, P, F, I, I, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P, I]
+    case = widen(Case([6000, 300, 40], 4 * Hkv, Hkv, 64, 16, kv, L=L, window=5000, sinks=4, seed=25, poison=False))
+    q, cache, bt, sc, sl = case.dev()
+    B, _, Hq, D = q.shape
+    out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:3], float("nan"), device="cuda")
+    ws = torch.full((mqa.gqa_window_decode_workspace_bytes(B, L, Hq, Hkv, D, 3),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rc = fn(q.data_ptr(), cache.data_ptr(), None if sc is None else sc.data_ptr(), bt.data_ptr(), sl.data_ptr(),
+            case.scale, 5000, 4, out.data_ptr(), lse.data_ptr(), B, L, Hq, Hkv, D, case.nb, 16, bt.shape[1], 16,
+            binding._KV_NAMES[kv], 3, ws.data_ptr(), ws.numel(), status.data_ptr(),
+            torch.cuda.current_stream().cuda_stream, 0)
+    assert rc == binding.OK
+    torch.cuda.synchronize()
+    assert int(status.item()) == binding.ERR_DEVICE_TIMEOUT
+    units = ws.cpu()[-8 * B:].view(torch.int32).view(B, 2)  # each request's first and last unit
+    assert units[0, 0] == 0 and units[0, 1] > 0 and units[1, 0] > 0
+    check(case, out.cpu().double(), lse.cpu().double(), rows=[1, 2])
+    run_and_check(case, (3,))
