@@ -110,3 +110,79 @@ def test_mla_append_feeds_the_decode():
         bound = 2 ** -8 * (p @ k[:, :R].abs()) + 2 ** -8 * o.abs() + 1e-4
         assert ((out[b].cpu().double() - o).abs() <= bound).all()
         assert (lse[b].cpu().double() - torch.logsumexp(x, -1)).abs().max() <= 1e-3
+
+
+def half_step(x, kv, s):
+    """What a value x may lose in a cache of scale s: half a step of its code, and the rounding of the quotient."""
+    if kv.startswith("fp8"):
+        return torch.maximum(x.abs() * 2 ** -4, s * 2 ** -10) + x.abs() * 2 ** -20
+    return s / 2 + x.abs() * 2 ** -20
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "fp8_e4m3_pth", "int8_pth", "int4_pth"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (32, 8, 128), (3, 3, 128)])
+def test_appended_rows_read_back_by_the_decode(kv, Hq, Hkv, D):
+    # requests of one token: out is the value, lse the key's column that a query of a single one picks (scale 1)
+    torch.manual_seed(2)
+    B, page, grp = 40, 16, Hq // Hkv
+    row, dtype = {"bf16": (D, BF), "fp8_e4m3": (D, torch.uint8), "int4_pth": (D // 2 + 4, torch.uint8)}.get(
+        kv, (D + 4, torch.uint8))
+    cache = torch.zeros(B, 2, page, Hkv, row, dtype=dtype, device="cuda")
+    if kv == "fp8_e4m3":
+        cache = cache.view(torch.float8_e4m3fn)
+    name = kv if kv.endswith("pth") else None
+    ks, vs = (0.05, 0.03) if kv == "fp8_e4m3" else (1.0, 1.0)
+    cs = table(9, D)[8:]  # one angle row, not that of position 0
+    bt = torch.randperm(B).to(torch.int32)[:, None]
+    k, v = torch.randn(B, Hkv, D).to(BF), torch.randn(B, Hkv, D).to(BF)
+    ones = torch.ones(B, dtype=torch.int32, device="cuda")
+    mqa.gqa_rope_append(k.cuda(), v.cuda(), cs.cuda(), cache, bt.cuda(), ones,
+                        torch.arange(B + 1, dtype=torch.int32, device="cuda"), k_scale=ks, v_scale=vs, kv_dtype=name)
+    col = (torch.arange(B)[:, None] * 5 + torch.arange(Hq) * 3) % D
+    q = torch.zeros(B, Hq, D).scatter_(2, col[..., None], 1.0).to(BF)
+    out, lse = mqa.gqa_paged_decode(q.cuda(), cache, bt.cuda(), ones, 1.0, ks, vs, kv_dtype=name)
+    torch.cuda.synchronize()
+    out, lse = out.cpu().double(), lse.cpu().double()
+    for b in range(B):
+        kr, mag = ref.rotate(k[b].double(), cs[0].double(), False)
+        for h in range(Hq):
+            kk, vv, m = kr[h // grp], v[b, h // grp].double(), mag[h // grp]
+            if kv == "bf16":
+                ek, ev = kk.abs() * 2 ** -8, torch.zeros_like(vv)
+            elif kv == "fp8_e4m3":
+                ek, ev = half_step(kk, kv, torch.tensor(ks)), half_step(vv, kv, torch.tensor(vs))
+            else:
+                ek, ev = (half_step(x, kv, x.abs().max() / ref.Q_MAX[kv] * (1 + 2 ** -20)) for x in (kk, vv))
+            assert ((out[b, h] - vv).abs() <= ev + (vv.abs() + ev) * 2 ** -8).all(), (kv, b, h)
+            c = int(col[b, h])
+            assert abs(lse[b, h] - kk[c]) <= ek[c] + m[c] * 2 ** -21 + kk[c].abs() * 2 ** -20 + 1e-6, (kv, b, h)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("R,H", [(512, 16), (512, 128), (256, 16)])
+def test_appended_latent_rows_read_back_by_the_decode(fp8, R, H):
+    torch.manual_seed(3)
+    B, page, ks = 24, 16, 0.05 if fp8 else 1.0
+    cache = torch.zeros(B, page, R + 64, dtype=torch.uint8 if fp8 else BF, device="cuda")
+    if fp8:
+        cache = cache.view(torch.float8_e4m3fn)
+    cs = table(9, 64)[8:]
+    bt = torch.randperm(B).to(torch.int32)[:, None]
+    a = torch.randn(B, R + 64).to(BF)
+    ones = torch.ones(B, dtype=torch.int32, device="cuda")
+    da = a.cuda()
+    mqa.mla_rope_append(da[:, :R], da[:, R:], cs.cuda(), cache, bt.cuda(), ones,
+                        torch.arange(B + 1, dtype=torch.int32, device="cuda"), k_scale=ks)
+    col = (torch.arange(B)[:, None] * 5 + torch.arange(H) * 37) % (R + 64)
+    q = torch.zeros(B, H, R + 64).scatter_(2, col[..., None], 1.0).to(BF)
+    out, lse = mqa.mla_decode(q.cuda(), cache, bt.cuda(), ones, 1.0, ks)
+    torch.cuda.synchronize()
+    out, lse = out.cpu().double(), lse.cpu().double()
+    for b in range(B):
+        turned, mag = ref.rotate(a[b, None, R:].double(), cs[0].double(), False)
+        x = torch.cat([a[b, :R].double(), turned[0]])
+        m = torch.cat([torch.zeros(R, dtype=torch.float64), mag[0]])
+        e = half_step(x, "fp8_e4m3", torch.tensor(ks)) if fp8 else x.abs() * 2 ** -8
+        e += m * 2 ** -21
+        assert ((out[b] - x[:R]).abs() <= e[:R] + (x[:R].abs() + e[:R]) * 2 ** -8).all(), b
+        assert ((lse[b] - x[col[b]]).abs() <= e[col[b]] + x[col[b]].abs() * 2 ** -20 + 1e-6).all(), b
