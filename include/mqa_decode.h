@@ -462,14 +462,16 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
  * lse = -inf.  Pages that hold no visible key are not read, nor are their
  * block-table entries: a serving system may free them.  Bytes of tokens that
  * no query sees never reach a result, whatever they hold; an Inf or NaN at a
- * key reaches only the queries that see it.
+ * key, or in a scale, reaches only the queries that see that key, or a key of
+ * that scale.
  *
  *   q          bf16 [batch, q_len, num_q_heads, head_size] (contiguous);
  *              query head h reads KV head h / (num_q_heads / num_kv_heads).
  *   kv_cache, kv_dtype: MQA_KV_BF16 or MQA_KV_FP8_E4M3 as in
  *              gqa_paged_decode, MQA_KV_FP8_E4M3_BLOCK or MQA_KV_INT8_BLOCK
  *              with kv_scales / scale_block (else NULL / ignored).  With 8-bit
- *              codes the query is taken in f16: entries within +-65504.
+ *              codes the query is taken in f16: entries within +-65504, those
+ *              below 2^-14 in magnitude to the nearest multiple of 2^-24.
  *   k_scale, v_scale  used by MQA_KV_FP8_E4M3 only.
  *   window     >= 1 (2^30 and above: no window); sinks >= 0.
  *   out        bf16 [batch, q_len, num_q_heads, head_size], fully written.
@@ -485,8 +487,10 @@ int gqa_window_num_kv_splits(int batch, int q_len, int num_q_heads, int num_kv_h
  *   head_size in {64, 128}; num_kv_heads in [1, 8]; at most 16 query heads per
  *   KV head; q_len * num_q_heads / num_kv_heads <= 128; batch * ceil(that /
  *   16) <= 2048; page_size a multiple of 16; num_blocks * page_size < 2^30;
- *   batch * ceil(that / 16) * (max_blocks * page_size / 16 + 2) < 2^29.  Other
- *   arguments and errors as for mla_decode. */
+ *   batch * ceil(that / 24) * (max_blocks * page_size / 16 + 2) < 2^29.  Other
+ *   arguments and errors as for mla_decode; where a wait ran out
+ *   (MQA_ERR_DEVICE_TIMEOUT in *device_status) the outputs of the requests
+ *   concerned are undefined. */
 mqa_status gqa_window_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
                              const int32_t* seq_lens, float scale, float k_scale, float v_scale, int window,
                              int sinks, void* out, float* lse, int batch, int q_len, int num_q_heads,
@@ -517,7 +521,8 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
  *   q, k, v    bf16 [num_tokens, heads, head_size] with token strides in
  *              elements (multiples of 8, at least a token's row: slices of a
  *              fused projection will do); q and q_out both NULL: no queries.
- *   q_out      bf16, token stride q_out_stride; may be q itself.
+ *   q_out      bf16, token stride q_out_stride; may be q itself, and
+ *              overlaps no other argument.
  *   cos_sin    fp32 [max_position, rotary_dim]: cosines, then sines;
  *              rotary_dim a multiple of 16, at most head_size.
  *   query_start int32 [batch + 1], ascending, at most num_tokens.
@@ -535,6 +540,9 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
  *                                 A block whose first token is new starts
  *                                 from s_old = 0 whatever it held.
  *              Codes saturate; scales below 2^-126 become 0 with codes 0.
+ *              A quotient is x times the fp32 reciprocal of its scale, within
+ *              2^-23 of x / s relative: a value that near the border between
+ *              two codes may take either.
  *   kv_scales, scale_block  the block formats' only (else NULL / ignored).
  *   A call may append to a physical block through one entry of the block
  *   table only.  Infinities and NaN among the new values make the values of
@@ -544,8 +552,8 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
  * A request with seq_lens[b] < its new tokens, a position without a row in
  * cos_sin or a page in the table, or a block id outside [0, num_blocks) raises
  * MQA_ERR_DEVICE_CHECK in *device_status; the cells concerned (of a block
- * format: the block's new tokens) are not written.  Enqueues one kernel;
- * allocates nothing. */
+ * format: the block's new tokens) are not written, nor, without a position, are
+ * the token's rows of q_out.  Enqueues one kernel; allocates nothing. */
 mqa_status gqa_rope_append(const void* q, const void* k, const void* v, const float* cos_sin,
                            const int32_t* query_start, const int32_t* seq_lens, const int32_t* block_table,
                            void* q_out, void* kv_cache, float* kv_scales, float k_scale, float v_scale,

@@ -24,6 +24,8 @@ bool heads_ok(int batch, int q_len, int hq, int hkv) {
 
 bool heads_served(int batch, int q_len, int hq, int hkv) {
     const long long rows = static_cast<long long>(q_len) * (hq / hkv);
+    // (the limit on batches counts 16 rows to a block, as the header states it;
+    // blocks of 24 rows are fewer, so that the prefix always fits)
     return hkv <= 8 && hq / hkv <= 16 && rows <= kMaxRows &&
            batch <= mqa::kWinMaxVirtual / static_cast<int>((rows + 15) / 16);
 }
@@ -68,10 +70,17 @@ bool cache_map(CUtensorMap* out, const void* base, int elt, int D, int hkv, long
 // times as long as one.  Longer windows hold requests of unlike lengths more
 // often than not, and are cut (60 us).  Measured whole / cut in us, 32/8 heads x
 // 128, bf16, windows of 128, 512 and 1024 tokens: 150 requests 21 / 27, 54 / 61
-// and 96 / 103, 200 requests 30 / 32, 95 / 77 and 176 / 135, 304 requests 37 / 44,
-// 106 / 110 and 202 / 196 (of 1 to 3000 tokens: 36 / 44, 102 / 102, 181 / 167);
-// 64/8 heads x 64, int8, window 128: 100, 150, 200 and 256 requests 12 / 14, 13 /
-// 19, 17 / 24, 18 / 25.
+// and 97 / 104, 200 requests 30 / 33, 95 / 78 and 178 / 135, 304 requests 37 / 44,
+// 106 / 110 and 197 / 197 (of 1 to 3000 tokens: 36 / 43, 101 / 101, 179 / 167);
+// 64/8 heads x 64, int8, window 128: 100, 150, 200 and 256 requests 13 / 14, 13 /
+// 19, 18 / 24, 18 / 24.  These two layouts gave the rates.  Elsewhere (windows
+// of 128 and 512): 32/8 x 128, int8, 64 requests 15 / 13 and 36 / 24, 150 17 / 23
+// and 37 / 42, 200 24 / 26 and 54 / 51, 304 27 / 35 and 63 / 73; 8/1 x 128, int8,
+// 45 requests 9 / 10 and 12 / 11, 150 10 / 14 and 12 / 14; 8/2 x 128, bf16, 45
+// requests 9 / 9 and 14 / 12, 150 9 / 13 and 19 / 23.  Of all these the rule takes
+// the slower side by more than 5 %, 1 to 5 us, at 128 tokens with 200 requests of
+// 8 KV heads x 128 and with 45 of one or two over int8, and at 512 tokens with 150
+// requests over codes.
 bool whole_requests(const mqa::WinArgs& a, int elt, int head_size, int sms) {
     const long long tt = 1LL << a.tt_log, all = (static_cast<long long>(a.max_blocks) * a.page + tt - 1) / tt;
     const long long seen = (a.sinks + tt - 1) / tt + (static_cast<long long>(a.window) + a.q_len - 2 + tt) / tt + 1;

@@ -111,8 +111,8 @@ __device__ __forceinline__ WinVis win_visible(const WinArgs& a, int r, int n) {
 // actually used; 0 where a unit is a request.  Where the units are enough for
 // the requests and none is much longer than an equal share, cutting would
 // cost more, in starts and partials, than it evens out: 256 windows of 128 (512,
-// 1024) tokens over int8, 64/8 heads x 64, take 21 (38, 62) us whole and 25
-// (43, 64) us cut on 304 units.
+// 1024) tokens over int8, 64/8 heads x 64, take 18 (38, 62) us whole and 24
+// (43, 63) us cut on 304 units.
 __device__ __forceinline__ int win_units(const WinArgs& a, int vb, int T, int longest) {
     const int U = min(a.units, max(1, T)), share = T / U;
     return vb <= a.units && longest <= share + max(2, share / 4) ? 0 : U;
@@ -137,7 +137,7 @@ constexpr int kWinMaxRows = 24;
 __host__ __device__ constexpr int win_row_groups(int rbn) { return (rbn + 7) / 8; }
 
 // Thread blocks of stage 1 resident on one SM: one where more than 8 rows meet
-// head size 128 (32 windows of 4096, 16 rows, e4m3: 74 us against 92 with two; with
+// head size 128 (32 windows of 4096, 16 rows, e4m3: 69 us against 92 with two; with
 // head size 64 300 windows of 128 with 12 rows take 57 us with one, 39 with two).
 __host__ __device__ constexpr int win_ctas_per_sm(int nhb, int D) { return nhb == 1 || (D == 64 && nhb == 2) ? 2 : 1; }
 constexpr int kWinMaxCtasPerSm = 2;

@@ -30,12 +30,12 @@
 // e4m3 with a scale per page and head): 259 us, 6.4 TB/s of the 6.67 a copy
 // reaches; 64 windows of 16384 tokens over bf16: 594 us, 7.2 TB/s (reads alone
 // run faster than a copy).  Short windows are bound by the start (4.3 us until
-// the copies are issued) and the merge; 9 to 16 rows per KV head by instructions (32 windows of 4096 over
-// e4m3, 16 rows, head size 128: 69 us; with two blocks per SM, half the tokens
-// per step and Q in shared memory it was 89 us and 730 instructions per 16
-// tokens and head).  17 to 24 rows are one row block: 32 windows of 2000, 20
-// rows, take 60 (bf16) and 60 (e4m3) us, as two blocks of 16 and 4 rows they took
-// 95 and 73.
+// the copies are issued) and the merge; 9 to 16 rows per KV head by instructions
+// (32 windows of 4096 over e4m3, 16 rows, head size 128: 69 us; with two blocks
+// per SM, half the tokens per step and Q in shared memory it was 92 us and 730
+// instructions per 16 tokens and head).  17 to 24 rows are one row block: 32
+// windows of 2000, 20 rows, take 59 (bf16), 54 (e4m3) and 49 (int8) us; as two
+// blocks of 16 and 4 rows bf16 took 95 and e4m3 73.
 //   * Tokens are the MMA's M dimension: S^T = K Q^T (16 tokens x 8 rows),
 //     O^T = V^T P^T (16 head dims x 8 rows); NHB row groups of 8.
 //   * 8-bit codes stay codes in shared memory and are widened to f16 in
@@ -86,7 +86,7 @@ struct Cfg {
     static constexpr int kSlot = kTok * D * kElt;    // bytes of a slot (one plane of it)
     // A lane hands its accumulators to another warp 16 at a time, or all at once
     // where eight full rings, four warps' buffers and 26 KB for the rest fit
-    // (42 requests, 35 rows of one KV head, int8: 47 -> 42 us)
+    // (42 requests, 35 rows of one KV head, int8: 48 -> 42 us)
     static constexpr int kAll = 4 * NHB * kSteps, kTail = 6 * NHB;
     static constexpr bool kRoom = 8 * kMaxSlots * kSlot + 4 * (kAll + kTail) * 128 + 26 * 1024 <=
                                   228 * 1024 / win_ctas_per_sm(NHB, D);
