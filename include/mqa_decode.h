@@ -584,6 +584,134 @@ mqa_status mla_rope_append(const void* kv_c, const void* k_pe, const void* q_pe,
                            long long k_pe_stride, long long q_pe_stride, long long q_pe_head_stride,
                            long long q_out_stride, long long q_out_head_stride, int* device_status, void* stream);
 
+/* ---- Shaped logits, prompts, and pages ------------------------------------
+ *
+ * gqa_window_decode with shaped logits: of query head h at position p and key t
+ *   x_t = cap tanh(scale <q, K_t> / cap) - slopes[h] |p - t|
+ * (softcap = cap; 0: the scaled product itself; slopes NULL: no bias).
+ *
+ *   softcap    0, or 2^-20 .. 2^60.
+ *   slopes     fp32 [num_q_heads] or NULL.
+ *   kv_dtype, window (2^30 and above: none), sinks, workspace
+ *   (gqa_window_decode_workspace_bytes) and every other argument, limit and
+ *   error as for gqa_window_decode. */
+mqa_status gqa_score_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, float k_scale, float v_scale, float softcap,
+                            const float* slopes, int window, int sinks, void* out, float* lse, int batch, int q_len,
+                            int num_q_heads, int num_kv_heads, int head_size, int num_blocks, int page_size,
+                            int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits,
+                            void* workspace, size_t workspace_bytes, int* device_status, void* stream);
+
+/* Workspace bytes of gqa_prefill with num_kv_splits > 1 on the current device
+ * (whatever the batch); 0 on invalid arguments or without a device. */
+size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_size);
+
+/* GQA attention of a ragged batch of new tokens (prompts, chunks of prompts,
+ * single tokens) over a paged cache that holds their keys and values already
+ * (gqa_rope_append writes them).
+ *
+ * Request b brings tokens query_start[b] .. query_start[b + 1] - 1 (none if
+ * equal); the last of them has position seq_lens[b] - 1.  The query at position
+ * p >= 0 sees key t < seq_lens[b] iff
+ *   (t <= p or t < prefix_lens[b])  and  (t < sinks or t > p - window)
+ * (a prefix whose tokens see each other in both directions; none: causal), and
+ * a query with p < 0 sees none.  x_t as for gqa_score_decode;
+ *   lse = ln sum_t e^{x_t},  out = sum_t e^{x_t - lse} V_t
+ * over the keys seen; out = 0, lse = -inf where there are none.  Rows of
+ * tokens outside [query_start[0], query_start[batch]) are padding: not written.
+ * Blocks that no new token sees are not read, nor are their block-table
+ * entries.  Bytes of tokens that none of the request's new tokens sees never
+ * reach a result, whatever they hold, nor do those of other requests; an Inf
+ * or NaN among the values of a token that one of them sees may reach all of
+ * the request's new tokens.
+ *
+ *   q          bf16 [num_tokens, num_q_heads, head_size], with a token stride in
+ *              elements (a multiple of 8, at least a token's row).
+ *   kv_cache, kv_scales, scale_block, kv_dtype, k_scale, v_scale  as for
+ *              gqa_window_decode; the query stays bf16 whatever the cache, values of
+ *              block-scaled caches (scale * code) are rounded to bf16.
+ *   query_start int32 [batch + 1], ascending, at most num_tokens.
+ *   prefix_lens int32 [batch] or NULL; taken within [0, seq_lens[b]].
+ *   softcap, slopes, window, sinks  as for gqa_score_decode.
+ *   out        bf16 [num_tokens, num_q_heads, head_size] (contiguous).
+ *   lse        fp32 [num_tokens, num_q_heads] or NULL.
+ *   num_kv_splits  1: no request's keys are cut (a token's result does not
+ *              depend on the rest of the batch); more: work is cut into one
+ *              share for each multiprocessor, which needs the workspace.
+ *              Reproducible either way.
+ *   workspace  gqa_prefill_workspace_bytes(...) bytes, or NULL with
+ *              num_kv_splits 1; contents do not matter.  Calls that may overlap
+ *              need one each.
+ *   head_size in {64, 128}; num_kv_heads and query heads per KV head up to 128;
+ *   num_tokens 0 .. 2^24; batch up to 8192; page_size a multiple of 16;
+ *   max_blocks * page_size and num_blocks * page_size < 2^30.  query_start that
+ *   descends or leaves [0, num_tokens], or a length out of range, raises
+ *   MQA_ERR_DEVICE_CHECK (values are then taken into range), as does a block
+ *   id outside [0, num_blocks) (its tokens are not seen). */
+mqa_status gqa_prefill(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* query_start, const int32_t* prefix_lens, float scale,
+                       float k_scale, float v_scale, float softcap, const float* slopes, int window, int sinks,
+                       void* out, float* lse, int num_tokens, int batch, int num_q_heads, int num_kv_heads,
+                       int head_size, int num_blocks, int page_size, int max_blocks, int scale_block,
+                       mqa_kv_dtype kv_dtype, long long q_stride, int num_kv_splits, void* workspace,
+                       size_t workspace_bytes, int* device_status, void* stream);
+
+/* Page counts.  refs [num_blocks] says how many holders (rows of a block table
+ * and whatever else the caller counts) each block has; 0: free.
+ *
+ * Caches are given as HOST arrays of device pointers and of bytes per page: any
+ * tensors whose first dimension is a block (of every layer, K and V caches of
+ * each format, MLA caches, block scales); up to 256, not overlapping, each
+ * 16-byte aligned with pages of a multiple of 4 bytes, up to 2^30. */
+
+size_t mqa_pages_fork_workspace_bytes(int new_rows);
+size_t mqa_pages_compact_workspace_bytes(int num_blocks);
+
+/* New rows of a block table from parents: beams that are reordered, several
+ * samples of one prompt, requests that end.
+ *
+ * New row r has the length and the pages of row parents[r]; -1: an empty row.
+ * Pages stay shared, but a partly filled last page belongs to the first child
+ * only: every other one gets a free page with a copy of its data (in all caches),
+ * the lowest ids in the order of the rows.  With c(p) the children of row p, the
+ * count of its full pages changes by c(p) - 1, that of a partly filled last page by
+ * (c(p) > 0) - 1; a fresh page's is 1.  Pages that become free in this call may
+ * be taken by it.  (A row without children is freed: parents of -1 free.)
+ *
+ *   block_table int32 [rows, max_blocks], seq_lens int32 [rows], refs int32
+ *              [num_blocks]; entries behind a row's last page are not read.
+ *   parents    int32 [new_rows] in [-1, rows).
+ *   new_table  int32 [new_rows, max_blocks], fully written, -1 behind a row's last
+ *              page; new_lens int32 [new_rows]; new_refs int32 [num_blocks] (may
+ *              be refs itself).  Outputs overlap nothing else.
+ *   rows, new_rows up to 8192; page_size a multiple of 16.
+ *   MQA_ERR_DEVICE_CHECK in *device_status: a parent or length out of range
+ *   (an empty row; the length is taken into range), a block id outside
+ *   [0, num_blocks) (kept, not counted), or too few free pages (the last rows that
+ *   need one have -1 in its place). */
+mqa_status mqa_pages_fork(const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                          const int32_t* refs, int32_t* new_table, int32_t* new_lens, int32_t* new_refs, int rows,
+                          int new_rows, int max_blocks, int num_blocks, int page_size, void* const* caches,
+                          const size_t* page_bytes, int num_caches, void* workspace, size_t workspace_bytes,
+                          int* device_status, void* stream);
+
+/* Moves live pages (refs > 0) to the lowest ids: with L of them, those with ids
+ * >= L go, in ascending order, to the free ids below L.
+ *
+ *   new_table  the table with its entries renamed (those behind a row's last page
+ *              as they were); may be block_table itself.
+ *   new_refs   the counts by new ids; may be refs itself.
+ *   moved      int32 [num_blocks]: new id of each page, -1 for free ones (for
+ *              tables that the call does not get).
+ *   num_live   int32 [1]: L.
+ *   Data of pages from L on stays as it was.  Other arguments and errors as for
+ *   mqa_pages_fork (a table entry that is no live page is kept, and reported). */
+mqa_status mqa_pages_compact(const int32_t* block_table, const int32_t* seq_lens, const int32_t* refs,
+                             int32_t* new_table, int32_t* new_refs, int32_t* moved, int32_t* num_live, int rows,
+                             int max_blocks, int num_blocks, int page_size, void* const* caches,
+                             const size_t* page_bytes, int num_caches, void* workspace, size_t workspace_bytes,
+                             int* device_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

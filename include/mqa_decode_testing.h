@@ -79,6 +79,15 @@ mqa_status mqa_test_gqa_window_withheld(const void* q, const void* kv_cache, con
                                         void* workspace, size_t workspace_bytes, int* device_status, void* stream,
                                         int withhold_unit);
 
+/* A causal bf16-cache gqa_prefill (num_kv_splits 1, no shaping, window or
+ * prefix, no lse) in which no key of request `withhold_request` (>= 0) is
+ * copied: results of the thread blocks that work on it are undefined. */
+mqa_status mqa_test_gqa_prefill_withheld(const void* q, const void* kv_cache, const int32_t* block_table,
+                                         const int32_t* seq_lens, const int32_t* query_start, float scale, void* out,
+                                         int num_tokens, int batch, int num_q_heads, int num_kv_heads, int head_size,
+                                         int num_blocks, int page_size, int max_blocks, long long q_stride,
+                                         int* device_status, void* stream, int withhold_request);
+
 #ifdef __cplusplus
 }
 #endif

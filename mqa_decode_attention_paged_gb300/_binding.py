@@ -87,6 +87,21 @@ def _load() -> ctypes.CDLL:
     lib.gqa_window_decode.argtypes = [P, P, P, P, P, F, F, F, I, I, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P]
     lib.gqa_block_decode.restype = I
     lib.gqa_block_decode.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P]
+    lib.gqa_score_decode.restype = I
+    lib.gqa_score_decode.argtypes = [P, P, P, P, P, F, F, F, F, P, I, I, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, P, P]
+    lib.gqa_prefill_workspace_bytes.restype = SZ
+    lib.gqa_prefill_workspace_bytes.argtypes = [I, I, I]
+    lib.gqa_prefill.restype = I
+    lib.gqa_prefill.argtypes = [P, P, P, P, P, P, P, F, F, F, F, P, I, I, P, P, I, I, I, I, I, I, I, I, I, I, LL, I, P, SZ,
+                                P, P]
+    lib.mqa_pages_fork_workspace_bytes.restype = SZ
+    lib.mqa_pages_fork_workspace_bytes.argtypes = [I]
+    lib.mqa_pages_compact_workspace_bytes.restype = SZ
+    lib.mqa_pages_compact_workspace_bytes.argtypes = [I]
+    lib.mqa_pages_fork.restype = I
+    lib.mqa_pages_fork.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P, P, I, P, SZ, P, P]
+    lib.mqa_pages_compact.restype = I
+    lib.mqa_pages_compact.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, P, I, P, SZ, P, P]
     lib.gqa_rope_append.restype = I
     lib.gqa_rope_append.argtypes = [P, P, P, P, P, P, P, P, P, P, F, F, I, I, I, I, I, I, I, I, I, I, I, I, I, LL, LL,
                                     LL, LL, P, P]
@@ -502,14 +517,33 @@ def gqa_window_num_kv_splits(batch: int, q_len: int, num_q_heads: int, num_kv_he
     return n
 
 
-# The calls that run once per layer and token, with their own checks, live in a module that imports torch at once;
+def gqa_prefill_workspace_bytes(num_q_heads: int, num_kv_heads: int, head_size: int) -> int:
+    """Workspace bytes of gqa_prefill on the current device, unless num_kv_splits is 1."""
+    return int(lib.gqa_prefill_workspace_bytes(num_q_heads, num_kv_heads, head_size))
+
+
+def pages_fork_workspace_bytes(new_rows: int) -> int:
+    return int(lib.mqa_pages_fork_workspace_bytes(new_rows))
+
+
+def pages_compact_workspace_bytes(num_blocks: int) -> int:
+    return int(lib.mqa_pages_compact_workspace_bytes(num_blocks))
+
+
+# The calls that run once per layer and token, with their own checks, live in modules that import torch at once;
 # this one does without (the planner, the versions and the sizes above need no tensors).
-_CACHE_OPS = frozenset(("gqa_window_decode", "gqa_block_decode", "gqa_rope_append", "mla_rope_append", "_check_rows"))
+_CACHE_OPS = frozenset(("gqa_window_decode", "gqa_block_decode", "gqa_score_decode", "gqa_rope_append", "mla_rope_append",
+                        "_check_rows"))
+_PROMPT_OPS = frozenset(("gqa_prefill", "pages_fork", "pages_compact"))
 
 
 def __getattr__(name):
     if name in _CACHE_OPS:
         from . import _cache_ops
         value = globals()[name] = getattr(_cache_ops, name)
+        return value
+    if name in _PROMPT_OPS:
+        from . import _prompt_ops
+        value = globals()[name] = getattr(_prompt_ops, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

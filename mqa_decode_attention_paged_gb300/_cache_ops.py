@@ -7,6 +7,7 @@ import torch
 from ._binding import (KV_BF16, KV_FP8_E4M3_BLOCK, KV_FP8_E4M3_PER_TOKEN_HEAD, KV_INT4_PER_TOKEN_HEAD, KV_INT8_BLOCK,
                        KV_INT8_PER_TOKEN_HEAD, OK, MqaError, _check, _check_common, _kv_code, _on_device, lib)
 
+_NO_WINDOW = 1 << 30  # a window from here on is none
 _PTH_CODES = (KV_FP8_E4M3_PER_TOKEN_HEAD, KV_INT8_PER_TOKEN_HEAD, KV_INT4_PER_TOKEN_HEAD)
 
 
@@ -96,8 +97,19 @@ def gqa_block_decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, *, ou
                           out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse)
 
 
+def gqa_score_decode(q, kv_cache, block_table, seq_lens, scale, *, softcap=0.0, slopes=None, window=None, sinks=0,
+                     kv_scales=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, num_kv_splits=None, workspace=None,
+                     kv_dtype=None, device_status=None, stream=None, return_lse=True):
+    """GQA paged decode with shaped logits through the C ABI: the query of head h at position p gives key t the logit
+    cap tanh(scale q.K_t / cap) - slopes[h] |p - t| (softcap 0: not capped; slopes, fp32 [Hq], None: no bias).
+    window None: no window; q and the other arguments as for :func:`gqa_window_decode`."""
+    return _window_decode("gqa_score_decode", q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale,
+                          _NO_WINDOW if window is None else window, sinks, out, lse, num_kv_splits, workspace, kv_dtype,
+                          device_status, stream, return_lse, float(softcap), slopes)
+
+
 def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale, window, sinks, out,
-                   lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse):
+                   lse, num_kv_splits, workspace, kv_dtype, device_status, stream, return_lse, softcap=None, slopes=None):
     shape = q.shape
     if len(shape) not in (3, 4) or kv_cache.dim() != 5:
         raise ValueError("q must be [batch, (q_len,) heads, head_size] and kv_cache have 5 dimensions")
@@ -121,17 +133,19 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
             and seq_lens.dtype is _I32 and seq_lens.shape == bt_shape[:1] and seq_lens.get_device() == index
             and seq_lens.is_contiguous()
             and (kv_scales is None or kv_scales.get_device() == index)
+            and (slopes is None or _fits(slopes, _F32, (Hq,), index))
             and (out is None or _fits(out, _BF16, shape, index))
             and (lse is None or _fits(lse, _F32, shape[:-1], index))
             and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == index))
             and (device_status is None or _fits(device_status, _I32, device_status.shape, index))):
         _check_common(q, kv_cache, code, block_table, seq_lens, q if out is None else out, shape, lse, shape[:-1],
-                      workspace, device_status, extra=(("kv_scales", kv_scales),))
+                      workspace, device_status, extra=(("kv_scales", kv_scales), ("slopes", slopes)))
+        _check(slopes, "slopes", (torch.float32,), shape=(Hq,), optional=True)
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale,
                                   window, sinks, out, lse, num_kv_splits, workspace, kv_dtype, device_status, stream,
-                                  return_lse)
+                                  return_lse, softcap, slopes)
     fresh = []
     if out is None:
         out = torch.empty_like(q)
@@ -154,6 +168,12 @@ def _window_decode(name, q, kv_cache, kv_scales, block_table, seq_lens, scale, k
         rc = lib.gqa_block_decode(q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
                                   seq_lens.data_ptr(), float(scale), out.data_ptr(), _raw(lse), B, L, Hq, Hkv, D, nb,
                                   page, bt_shape[1], block, code, int(num_kv_splits), _raw(workspace), ws_bytes,
+                                  _raw(device_status), raw)
+    elif softcap is not None:
+        rc = lib.gqa_score_decode(q.data_ptr(), kv_cache.data_ptr(), _raw(kv_scales), block_table.data_ptr(),
+                                  seq_lens.data_ptr(), float(scale), float(k_scale), float(v_scale), softcap,
+                                  _raw(slopes), _c_int(window), _c_int(sinks), out.data_ptr(), _raw(lse), B, L, Hq, Hkv,
+                                  D, nb, page, bt_shape[1], block, code, int(num_kv_splits), _raw(workspace), ws_bytes,
                                   _raw(device_status), raw)
     else:
         rc = lib.gqa_window_decode(q.data_ptr(), kv_cache.data_ptr(), _raw(kv_scales), block_table.data_ptr(),

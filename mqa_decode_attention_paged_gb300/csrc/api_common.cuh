@@ -23,4 +23,8 @@ bool api_test_hooks();
 
 inline bool api_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// A cap of logits: none, or far enough from the ends of the fp32 range that it
+// and its reciprocal are normal numbers.
+inline bool api_softcap_ok(float cap) { return cap == 0.f || (cap >= 0x1p-20f && cap <= 0x1p60f); }
+
 }  // namespace mqa

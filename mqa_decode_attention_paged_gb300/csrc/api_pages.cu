@@ -1,0 +1,140 @@
+// C ABI of the page operations: argument validation and the launches.  See
+// include/mqa_decode.h for the contract.
+#include "api_common.cuh"
+#include "pages.cuh"
+
+namespace {
+
+using mqa::api_aligned;
+using mqa::api_cuda_fail;
+
+// The caches as pools.
+mqa_status pools_of(mqa::PagePools& p, void* const* caches, const size_t* page_bytes, int n, int num_blocks) {
+    if (n < 0 || (n > 0 && (!caches || !page_bytes))) return MQA_ERR_INVALID_ARG;
+    if (n > mqa::kMaxPools) return MQA_ERR_UNSUPPORTED;
+    long long chunks = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!caches[i] || !api_aligned(caches[i], 16) || page_bytes[i] < 4) return MQA_ERR_INVALID_ARG;
+        if (page_bytes[i] % 4 != 0 || page_bytes[i] > (1ull << 30)) return MQA_ERR_UNSUPPORTED;
+        for (int k = 0; k < i; ++k) {  // (two pools in one place would be copied by two blocks at once)
+            const uintptr_t x = reinterpret_cast<uintptr_t>(caches[i]), y = reinterpret_cast<uintptr_t>(caches[k]);
+            if (x < y + page_bytes[k] * num_blocks && y < x + page_bytes[i] * num_blocks) return MQA_ERR_INVALID_ARG;
+        }
+        p.pool[i].base = static_cast<char*>(caches[i]);
+        p.pool[i].bytes = static_cast<long long>(page_bytes[i]);
+        p.first[i] = static_cast<int>(chunks);
+        chunks += (p.pool[i].bytes + mqa::kPageChunk - 1) / mqa::kPageChunk;
+    }
+    p.first[n] = static_cast<int>(chunks);
+    p.n = n;
+    return MQA_OK;
+}
+
+bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return a < b + ny && b < a + nx;
+}
+
+mqa_status sizes_ok(int rows, int new_rows, int max_blocks, int num_blocks, int page_size) {
+    if (rows < 1 || new_rows < 1 || max_blocks < 1 || num_blocks < 1 || page_size < 1) return MQA_ERR_INVALID_ARG;
+    if (page_size % 16 != 0 || rows > mqa::kPagesMaxRows || new_rows > mqa::kPagesMaxRows || num_blocks > (1 << 30))
+        return MQA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(max_blocks) * page_size > INT32_MAX - 1024) return MQA_ERR_UNSUPPORTED;
+    return MQA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mqa_pages_fork_workspace_bytes(int new_rows) {
+    return new_rows < 1 || new_rows > mqa::kPagesMaxRows ? 0 : mqa::fork_workspace_bytes(new_rows);
+}
+
+size_t mqa_pages_compact_workspace_bytes(int num_blocks) {
+    return num_blocks < 1 || num_blocks > (1 << 30) ? 0 : mqa::compact_workspace_bytes(num_blocks);
+}
+
+mqa_status mqa_pages_fork(const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                          const int32_t* refs, int32_t* new_table, int32_t* new_lens, int32_t* new_refs, int rows,
+                          int new_rows, int max_blocks, int num_blocks, int page_size, void* const* caches,
+                          const size_t* page_bytes, int num_caches, void* workspace, size_t workspace_bytes,
+                          int* device_status, void* stream) {
+    if (!block_table || !seq_lens || !parents || !refs || !new_table || !new_lens || !new_refs) return MQA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                          static_cast<const void*>(parents), static_cast<const void*>(refs),
+                          static_cast<const void*>(new_table), static_cast<const void*>(new_lens),
+                          static_cast<const void*>(new_refs), static_cast<const void*>(device_status)})
+        if (!api_aligned(p, 4)) return MQA_ERR_INVALID_ARG;
+    if (const mqa_status s = sizes_ok(rows, new_rows, max_blocks, num_blocks, page_size); s != MQA_OK) return s;
+    const size_t old_table = static_cast<size_t>(rows) * max_blocks * 4, table = static_cast<size_t>(new_rows) * max_blocks * 4;
+    if (overlap(block_table, old_table, new_table, table) || overlap(seq_lens, rows * 4ull, new_lens, new_rows * 4ull) ||
+        (refs != new_refs && overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)))
+        return MQA_ERR_INVALID_ARG;
+    mqa::PagePools pools{};
+    if (const mqa_status s = pools_of(pools, caches, page_bytes, num_caches, num_blocks); s != MQA_OK) return s;
+    if (!workspace || workspace_bytes < mqa::fork_workspace_bytes(new_rows)) return MQA_ERR_WORKSPACE_TOO_SMALL;
+    if (!api_aligned(workspace, 16)) return MQA_ERR_INVALID_ARG;
+    const int sms = mqa::api_sm_count();
+    if (sms < 1) return MQA_ERR_CUDA;
+    mqa::PagesArgs a{};
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.parents = parents;
+    a.refs = refs;
+    a.new_table = new_table;
+    a.new_lens = new_lens;
+    a.new_refs = new_refs;
+    a.ws = static_cast<int32_t*>(workspace);
+    a.status = device_status;
+    a.rows = rows;
+    a.new_rows = new_rows;
+    a.width = max_blocks;
+    a.num_blocks = num_blocks;
+    a.page = page_size;
+    const cudaError_t e = mqa::pages_fork(a, pools, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MQA_OK : api_cuda_fail(e);
+}
+
+mqa_status mqa_pages_compact(const int32_t* block_table, const int32_t* seq_lens, const int32_t* refs,
+                             int32_t* new_table, int32_t* new_refs, int32_t* moved, int32_t* num_live, int rows,
+                             int max_blocks, int num_blocks, int page_size, void* const* caches,
+                             const size_t* page_bytes, int num_caches, void* workspace, size_t workspace_bytes,
+                             int* device_status, void* stream) {
+    if (!block_table || !seq_lens || !refs || !new_table || !new_refs || !moved || !num_live) return MQA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                          static_cast<const void*>(refs), static_cast<const void*>(new_table),
+                          static_cast<const void*>(new_refs), static_cast<const void*>(moved),
+                          static_cast<const void*>(num_live), static_cast<const void*>(device_status)})
+        if (!api_aligned(p, 4)) return MQA_ERR_INVALID_ARG;
+    if (const mqa_status s = sizes_ok(rows, rows, max_blocks, num_blocks, page_size); s != MQA_OK) return s;
+    const size_t table = static_cast<size_t>(rows) * max_blocks * 4;
+    if ((block_table != new_table && overlap(block_table, table, new_table, table)) ||
+        (refs != new_refs && overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)) ||
+        overlap(moved, num_blocks * 4ull, refs, num_blocks * 4ull) || overlap(moved, num_blocks * 4ull, new_refs, num_blocks * 4ull))
+        return MQA_ERR_INVALID_ARG;
+    mqa::PagePools pools{};
+    if (const mqa_status s = pools_of(pools, caches, page_bytes, num_caches, num_blocks); s != MQA_OK) return s;
+    if (!workspace || workspace_bytes < mqa::compact_workspace_bytes(num_blocks)) return MQA_ERR_WORKSPACE_TOO_SMALL;
+    if (!api_aligned(workspace, 16)) return MQA_ERR_INVALID_ARG;
+    const int sms = mqa::api_sm_count();
+    if (sms < 1) return MQA_ERR_CUDA;
+    mqa::PagesArgs a{};
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.refs = refs;
+    a.new_table = new_table;
+    a.new_refs = new_refs;
+    a.moved = moved;
+    a.num_live = num_live;
+    a.ws = static_cast<int32_t*>(workspace);
+    a.status = device_status;
+    a.rows = a.new_rows = rows;
+    a.width = max_blocks;
+    a.num_blocks = num_blocks;
+    a.page = page_size;
+    const cudaError_t e = mqa::pages_compact(a, pools, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MQA_OK : api_cuda_fail(e);
+}
+
+}  // extern "C"

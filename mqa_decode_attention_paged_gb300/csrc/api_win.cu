@@ -95,7 +95,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
                   void* out, float* lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_size,
                   int num_blocks, int page_size, int max_blocks, int scale_block, mqa_kv_dtype kv_dtype,
                   int num_kv_splits, void* workspace, size_t workspace_bytes, int* device_status, void* stream,
-                  int withhold = -1) {
+                  int withhold = -1, float softcap = 0.f, const float* slopes = nullptr) {
     // withhold >= 0 only from the test hook mqa_test_gqa_window_withheld
     if (!q || !kv_cache || !block_table || !seq_lens || !out) return MQA_ERR_INVALID_ARG;
     if (!api_aligned(q, 16) || !api_aligned(kv_cache, 16) || !api_aligned(out, 16) || !api_aligned(block_table, 4) ||
@@ -163,6 +163,9 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     const bool per_tensor = kv_dtype == MQA_KV_FP8_E4M3;
     a.sl2 = scale * (per_tensor ? k_scale : 1.0f) * mqa::kLog2e;
     a.out_scale = per_tensor ? v_scale : 1.0f;
+    a.cap2 = softcap * mqa::kLog2e;
+    a.inv_cap2 = softcap > 0.f ? 1.f / a.cap2 : 0.f;
+    a.slopes = slopes;
     a.batch = batch;
     a.q_len = q_len;
     a.Hq = num_q_heads;
@@ -198,9 +201,11 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = a.units > 0 ? a.units : vb;
     a.alone = grid <= sms;
-    const cudaError_t e = kind == mqa::kWinBf16   ? mqa::win_stage1_bf16(a, head_size, grid, st)
-                          : kind == mqa::kWinInt8 ? mqa::win_stage1_int8(a, head_size, grid, st)
-                                                  : mqa::win_stage1_e4m3(a, head_size, grid, st);
+    const bool shaped = softcap > 0.f || slopes;
+    const auto stage1 = kind == mqa::kWinBf16   ? (shaped ? mqa::win_shaped_bf16 : mqa::win_stage1_bf16)
+                        : kind == mqa::kWinInt8 ? (shaped ? mqa::win_shaped_int8 : mqa::win_stage1_int8)
+                                                : (shaped ? mqa::win_shaped_e4m3 : mqa::win_stage1_e4m3);
+    const cudaError_t e = stage1(a, head_size, grid, st);
     if (e != cudaSuccess) return api_cuda_fail(e);
     if (a.units > 0)
         if (cudaError_t e2 = mqa::win_merge(a, head_size, st); e2 != cudaSuccess) return api_cuda_fail(e2);
@@ -254,6 +259,18 @@ mqa_status gqa_block_decode(const void* q, const void* kv_cache, const float* kv
     return decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, 1.0f, 1.0f, mqa::kWinNoWindow, 0, out, lse,
                   batch, q_len, num_q_heads, num_kv_heads, head_size, num_blocks, page_size, max_blocks, scale_block,
                   kv_dtype, num_kv_splits, workspace, workspace_bytes, device_status, stream);
+}
+
+mqa_status gqa_score_decode(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, float k_scale, float v_scale, float softcap,
+                            const float* slopes, int window, int sinks, void* out, float* lse, int batch, int q_len,
+                            int num_q_heads, int num_kv_heads, int head_size, int num_blocks, int page_size,
+                            int max_blocks, int scale_block, mqa_kv_dtype kv_dtype, int num_kv_splits,
+                            void* workspace, size_t workspace_bytes, int* device_status, void* stream) {
+    if (!mqa::api_softcap_ok(softcap) || !api_aligned(slopes, 4)) return MQA_ERR_INVALID_ARG;
+    return decode(q, kv_cache, kv_scales, block_table, seq_lens, scale, k_scale, v_scale, window, sinks, out, lse,
+                  batch, q_len, num_q_heads, num_kv_heads, head_size, num_blocks, page_size, max_blocks, scale_block,
+                  kv_dtype, num_kv_splits, workspace, workspace_bytes, device_status, stream, -1, softcap, slopes);
 }
 
 mqa_status mqa_test_gqa_window_withheld(const void* q, const void* kv_cache, const float* kv_scales,

@@ -1,0 +1,953 @@
+// Attention of a ragged batch of new tokens over a paged GQA cache that holds
+// their keys and values already (see gqa_prefill.cuh for cells and pieces).
+// For the query row of a token at position p and query head h, over the keys t
+// that it sees (t < max(p + 1, prefix), and t < sinks or t > p - window),
+//   x_t = cap tanh(scale s_k <q, K_t> / cap) - slope_h |p - t|,
+//   out = sum_t e^{x_t - lse} s_v V_t,   lse = ln sum_t e^{x_t}
+// with s_k, s_v the scales of the token block and head (1 for bf16); no cap:
+// the scaled product itself; no slopes: no bias.
+//
+// One thread block per multiprocessor.  Two tiles of 128 query rows share every
+// block of 128 keys; roles by warp:
+//   0-3, 4-7   softmax of tile 0 and 1: one row a thread
+//   8          copies K and V blocks (tensor copies of box_tok tokens of one
+//              head, 128-byte swizzle) into a ring
+//   9          issues the tensor-core products: S_i = Q_i K^T (M = 128 rows, N =
+//              128 keys) and O_i += P_i V, for the two tiles in turn, so that one
+//              tile's softmax runs beside the other's products
+//   10         copies the queries
+//   11..       make blocks ready: clear V rows that no row of the cell sees
+//              (whatever bytes they hold: 0 * NaN), and widen 8-bit codes to bf16
+// TMEM (512 columns): O_0, O_1 (D fp32 columns each), S_0, S_1 (128 each); P_i
+// (bf16) overwrites S_i.
+//
+// Softmax in base 2; a row's reference moves only when a logit exceeds it by
+// more than 8 (P stays below 2^8, sums are fp32), so O is rarely rescaled, and
+// the tile's own softmax warps do that.  P is rounded to bf16 for the tensor
+// cores, the denominator sums the unrounded values.  8-bit codes widen to bf16
+// exactly; K scales multiply the logits, V values code * s_v are rounded to
+// bf16 once, as an output is.
+#pragma once
+
+#include <atomic>
+
+#include "gqa_prefill.cuh"
+#include "tc_ptx.cuh"
+
+namespace mqa {
+namespace pre {
+
+constexpr float kNone = -3e38f;  // reference before the first logit
+
+template <int D, int KIND>
+struct Cfg {
+    static constexpr bool kCodes = KIND != kWinBf16;
+    static constexpr int kPanels = D / 64;                        // 64-column panels of a bf16 tile
+    static constexpr int kPanel = kPreBlock * 128;                // bytes of one
+    static constexpr int kTile = kPanels * kPanel;                // bytes of a bf16 tile of 128 rows
+    static constexpr int kRaw = kCodes ? kPreBlock * D : 0;       // bytes of a block of codes
+    static constexpr int kStages = kCodes ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);  // bf16 ring
+    static constexpr int kRawStages = kCodes ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int kHelpers = kCodes ? 5 : 1;  // warps 11..
+    static constexpr int kThreads = 32 * (11 + kHelpers);
+    // registers a thread: 64 K by the launch, moved between the warpgroups
+    static constexpr int kRegsSoftmax = kCodes ? 184 : 208, kRegsRest = kCodes ? 72 : 80;
+    static constexpr int kInfo = 16;  // blocks whose validity and scales are kept
+};
+
+struct Shared {
+    uint64_t kv_full[8];   // copies landed (a raw stage's for codes)
+    uint64_t kv_free[8];   // codes: read by the helpers; bf16: see ready / used
+    uint64_t ready[8];     // a bf16 stage may be multiplied
+    uint64_t used[8];      // .. and was
+    uint64_t q_full, q_free;
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2], drain;
+    long long scan[16];
+    long long total;
+    int b[2], u[2], h[2], j[2];  // start and end of the block's share
+    uint32_t tmem;
+    int failed;
+    uint32_t valid[16];      // 16-token groups of a block that were copied
+    float scale[16][2][8];   // their K and V scales
+};
+
+template <int D, int KIND>
+constexpr int smem_bytes() {
+    using C = Cfg<D, KIND>;
+    return 2 * C::kTile + C::kStages * C::kTile + C::kRawStages * C::kRaw + 1024 + static_cast<int>(sizeof(Shared));
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void st_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- pairs of fp32 values, one instruction for both
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, "
+        "%1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, "
+        "%1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 "
+        "w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// x := cap2 tanh(x / cap2).  For |y| <= 1, tanh(y) = y (c0 + .. + c5 y^10), least
+// squares towards the smallest absolute error, 2.4e-7 (of logits capped at 50:
+// 1.7e-5 in base 2, far below the 2^-9 of P's rounding); beyond, 1 - 2 / (1 + e^{2y}).
+__device__ __forceinline__ float2 cap_near(float2 x, float cap2, float inv) {
+    const float2 y = mul2(x, both(inv)), z = mul2(y, y);
+    float2 w = fma2(z, both(-0.002839464694f), both(0.01611417904f));
+    w = fma2(w, z, both(-0.05097286030f));
+    w = fma2(w, z, both(0.1325352489f));
+    w = fma2(w, z, both(-0.3332400322f));
+    w = fma2(w, z, both(0.9999968409f));
+    return mul2(mul2(y, both(cap2)), w);
+}
+
+// ---- codes
+__device__ __forceinline__ float2 half2_f32(uint32_t h) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Two codes in the low half of w -> two fp32 values (exact).
+template <int KIND>
+__device__ __forceinline__ float2 code_pair(uint32_t w) {
+    if constexpr (KIND == kWinE4m3) {
+        return half2_f32(e4m3x2_to_f16x2(w));
+    } else {
+        // 1024 + (code + 128) is exact in the mantissa of f16 0x6400
+        const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+        return __half22float2(h);
+    }
+}
+
+// Walks the pieces of a thread block's share; the same in every role.
+struct Pieces {
+    PreReq req;
+    PreCell cell;
+    int b, u, h, j0, j1, cells;
+    int eb, eu, eh, ej;
+    int jn;  // first block of the next piece
+
+    __device__ __forceinline__ void load(const PreArgs& a) {
+        req = pre_request(a, b, nullptr);
+        cells = (req.cnt + 2 * a.tile_tok - 1) / (2 * a.tile_tok);
+    }
+    __device__ __forceinline__ void init(const PreArgs& a, const Shared& s) {
+        b = s.b[0];
+        u = s.u[0];
+        h = s.h[0] - 1;
+        jn = s.j[0];
+        eb = s.b[1];
+        eu = s.u[1];
+        eh = s.h[1];
+        ej = s.j[1];
+        if (b < a.batch) {
+            load(a);
+            cell = pre_cell(a, req, u);
+        }
+    }
+    // The next piece: blocks [j0, j1) of cell (b, u), head h.
+    __device__ __forceinline__ bool next(const PreArgs& a) {
+        if (b >= a.batch) return false;
+        if (++h == a.Hkv) {
+            h = 0;
+            if (++u >= cells) {
+                u = 0;
+                do {
+                    if (++b >= a.batch) return false;
+                    load(a);
+                } while (cells == 0);
+            }
+            cell = pre_cell(a, req, u);
+        }
+        j0 = jn;
+        jn = 0;
+        const bool last = b == eb && u == eu && h == eh;
+        if (last && ej == 0) return false;
+        if (last || (b == eb && u == eu && h > eh) || (b == eb && u > eu) || b > eb) {
+            if (!last) return false;
+            j1 = ej;
+            b = a.batch;  // nothing after it (cell, h and the fields above stay)
+            return true;
+        }
+        j1 = cell.nt;
+        return true;
+    }
+};
+
+// The rows of tile i in a cell, and what they see.
+struct TileView {
+    int cnt;      // tokens
+    int lo_first, lo_last, lim_first, lim_last;
+    __device__ __forceinline__ TileView(const PreArgs& a, const PreCell& c, int i) {
+        const int t0 = i * a.tile_tok;
+        cnt = min(a.tile_tok, c.cnt - t0);
+        const int p0 = c.p0 + t0, p1 = p0 + cnt - 1;
+        lo_first = p0 - a.window + 1;
+        lo_last = p1 - a.window + 1;
+        lim_first = p0 < 0 ? 0 : max(p0 + 1, c.pre);
+        lim_last = p1 < 0 ? 0 : max(p1 + 1, c.pre);
+    }
+    // whether a row sees a key of the block from token t on
+    __device__ __forceinline__ bool active(const PreArgs& a, int t) const {
+        return cnt > 0 && t < lim_last && (t + kPreBlock > lo_first || t < a.sinks);
+    }
+    // whether every row sees all of it
+    __device__ __forceinline__ bool whole(const PreArgs& a, int t) const {
+        return t + kPreBlock <= lim_first && (t >= lo_last || t + kPreBlock <= a.sinks);
+    }
+};
+
+__device__ __forceinline__ long long block_sum(Shared& s, long long v) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (lane == 0) s.scan[warp] = v;
+    __syncthreads();
+    long long t = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += s.scan[w];
+    return t;
+}
+// Exclusive prefix over the block's threads; total in `all`.
+__device__ __forceinline__ long long block_scan(Shared& s, long long v, long long& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s.scan[warp] = x;
+    __syncthreads();
+    long long before = 0, t = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+        if (w == warp) before = t;
+        t += s.scan[w];
+    }
+    all = t;
+    return before + x - v;
+}
+
+// The thread block's share: start and end in s.  Cuts inside a (cell, head) lie
+// `grain` blocks apart, so that no piece is shorter than what a partial costs.
+__device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
+    const int tid = threadIdx.x, nthr = blockDim.x, c = blockIdx.x;
+    // first[b]: cells of the requests before b
+    int before = 0;
+    for (int base = 0; base < a.batch; base += nthr) {
+        const int b = base + tid;
+        int k = 0;
+        if (b < a.batch) {
+            const PreReq r = pre_request(a, b, c == 0 ? a.status : nullptr);
+            k = a.cell_div(r.cnt + 2 * a.tile_tok - 1);
+        }
+        long long all;
+        const int at = before + static_cast<int>(block_scan(s, k, all));
+        if (b < a.batch) first[b] = at;
+        before += static_cast<int>(all);
+    }
+    if (tid < 2) {
+        s.b[tid] = a.batch;
+        s.u[tid] = s.h[tid] = s.j[tid] = 0;
+    }
+    __syncthreads();
+    const int cells = before;
+    auto find = [&](int i, int& b, int& u, int& nt) {
+        int lo = 0, hi = a.batch - 1;  // the last request whose cells begin at or before i (empty ones lie before)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= i)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        b = lo;
+        u = i - first[lo];
+        nt = pre_cell(a, pre_request(a, b, nullptr), u).nt;
+    };
+    long long w = 0;
+    for (int i = tid; i < cells; i += nthr) {
+        int b, u, nt;
+        find(i, b, u, nt);
+        w += nt + kPreCellCost;
+    }
+    const long long total = block_sum(s, w) * a.Hkv;
+    const long long share = total / a.grid;
+    const int grain = !a.cut ? 1 << 30 : share >= 32 ? 1 : share >= 8 ? 2 : 4;
+    const long long x[2] = {total * c / a.grid, total * (c + 1) / a.grid};
+    long long base = 0;
+    for (int i0 = 0; i0 < cells && base <= x[1]; i0 += nthr) {
+        const int i = i0 + tid;
+        int b = 0, u = 0, nt = 0;
+        if (i < cells) find(i, b, u, nt);
+        const int per = i < cells ? nt + kPreCellCost : 0;
+        long long all;
+        const long long at = base + block_scan(s, static_cast<long long>(per) * a.Hkv, all);
+        base += all;
+        for (int e = 0; e < 2; ++e) {
+            if (per == 0 || x[e] < at || x[e] >= at + static_cast<long long>(per) * a.Hkv || (e == 1 && c + 1 == a.grid)) continue;
+            int h = static_cast<int>((x[e] - at) / per);
+            const int y = static_cast<int>(x[e] - at - static_cast<long long>(h) * per);
+            // the nearest cut: a multiple of the grain, or an end
+            int j = max(0, y - kPreCellCost);
+            if (grain >= nt)
+                j = 2 * y <= per ? 0 : nt;
+            else
+                j = (j + grain / 2) / grain * grain;
+            int cb = b, cu = u;
+            if (j > 0 && j + (grain + 1) / 2 >= nt) {  // the start of what follows
+                j = 0;
+                if (++h == a.Hkv) {
+                    h = 0;
+                    ++cu;  // past the request's last cell: normalised below
+                }
+            }
+            s.b[e] = cb;
+            s.u[e] = cu;
+            s.h[e] = h;
+            s.j[e] = j;
+        }
+        __syncthreads();
+    }
+    __syncthreads();
+    if (tid == 0) {
+        for (int e = 0; e < 2; ++e)
+            while (s.b[e] < a.batch) {
+                const int k = (s.b[e] + 1 < a.batch ? first[s.b[e] + 1] : cells) - first[s.b[e]];
+                if (s.u[e] < k) break;
+                ++s.b[e];
+                s.u[e] = 0;
+            }
+        if (s.b[0] == s.b[1] && s.u[0] == s.u[1] && s.h[0] == s.h[1] && s.j[0] == s.j[1]) s.b[0] = a.batch;  // nothing
+    }
+    __syncthreads();
+}
+
+// P of 32 logits (base 2, x - m) as bf16 pairs; their sum is added to l.
+template <bool SHAPED>
+__device__ __forceinline__ void numerators(const uint32_t (&s)[32], float sl2, float m, float2 (&l)[2], uint32_t (&p)[16]) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float2 x = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+        const float2 y = SHAPED ? add2(x, both(-m)) : fma2(x, both(sl2), both(-m));
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        l[k & 1] = add2(l[k & 1], e);
+        p[k] = pack_bf16x2(e.x, e.y);
+    }
+}
+
+// (16-byte stores: that is how outputs are aligned)
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+template <int D, int KIND, bool SHAPED>
+__global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
+    using C = Cfg<D, KIND>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t q_s = smem_u32(smem), kv_s = q_s + 2 * C::kTile, raw_s = kv_s + C::kStages * C::kTile;
+    Shared& s = *reinterpret_cast<Shared*>(smem + (2 + C::kStages) * C::kTile + C::kRawStages * C::kRaw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool scaled = C::kCodes && a.kv_scales != nullptr;
+    constexpr int kCopyStages = C::kCodes ? C::kRawStages : C::kStages;
+
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&a.q_map);
+        prefetch_tmap(&a.kv_map);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&s.kv_full[i], scaled ? 9 : 1);
+            mbar_init(&s.kv_free[i], C::kHelpers);
+            mbar_init(&s.ready[i], C::kHelpers);
+            mbar_init(&s.used[i], 1);
+        }
+        mbar_init(&s.q_full, 1);
+        mbar_init(&s.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 128);
+            mbar_init(&s.o_done[i], 1);
+            mbar_init(&s.o_free[i], 128);
+        }
+        mbar_init(&s.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&s.tmem, 512);
+    pdl_wait();
+    pdl_launch_dependents();
+    plan(a, s, reinterpret_cast<int*>(smem + 2 * C::kTile));  // the ring is not in use yet
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    const uint32_t t_o = tmem, t_s = tmem + 2 * D;  // tile i: t_o + i D, t_s + 128 i
+
+    Pieces pc;
+    pc.init(a, s);
+    bool ok = true;
+
+    if (warp == 8) {
+        // ------------------------------------------------ copies of K and V
+        set_regs_down<C::kRegsRest>();
+        const int nb = kPreBlock / a.box_tok;
+        int kvc = 0;  // blocks of K or V copied
+        while (ok && pc.next(a)) {
+            const int b = pc.b < a.batch ? pc.b : pc.eb;
+            if (b == a.withhold) break;
+            // lane k < nb: box k of a block; its block id is fetched a block ahead
+            auto want = [&](int j, int& off) {
+                const int t = pc.cell.block(j) * kPreBlock + lane * a.box_tok;
+                if (lane >= nb || t >= pc.cell.hi || !(t + a.box_tok > pc.cell.lo || t < pc.cell.s_end)) return -1;
+                const int page = a.page_div(t);
+                off = t - page * a.page;
+                const int id = __ldg(a.block_table + static_cast<long long>(b) * a.max_blocks + page);
+                return id < 0 || id >= a.num_blocks ? -2 : id;
+            };
+            int off = 0, off_next = 0, id_next = pc.j0 < pc.j1 ? want(pc.j0, off_next) : -1;
+            for (int j = pc.j0; j < pc.j1 && ok; ++j) {
+                const int id = id_next;
+                off = off_next;
+                if (j + 1 < pc.j1) id_next = want(j + 1, off_next);
+                if (id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
+                const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
+                const int per = a.box_tok / 16;
+                uint32_t groups = 0;
+                for (int k = 0; k < nb; ++k)
+                    if ((have >> k) & 1u) groups |= ((1u << per) - 1u) << (k * per);
+                const int g_id = __shfl_sync(0xffffffffu, id, lane / per);
+                const int g_off = __shfl_sync(0xffffffffu, off, lane / per) + lane % per * 16;
+                const int slot = (kvc >> 1) % C::kInfo;
+                for (int plane = 0; plane < 2; ++plane, ++kvc) {
+                    const int st = kvc % kCopyStages;
+                    uint64_t* free = C::kCodes ? &s.kv_free[st] : &s.used[st];
+                    if (!mbar_wait(free, (kvc / kCopyStages & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (plane == 0) s.valid[slot] = groups;
+                        mbar_arrive_expect_tx(&s.kv_full[st], __popc(have) * a.box_tok * D * (C::kCodes ? 1 : 2));
+                    }
+                    __syncwarp();
+                    if (id >= 0) {
+                        const int row = id * 2 * a.page + plane * a.page + off;
+                        if constexpr (C::kCodes) {
+                            tma_load(raw_s + st * C::kRaw + lane * a.box_tok * D, &a.kv_map, 0, pc.h, row, &s.kv_full[st]);
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < C::kPanels; ++p)
+                                tma_load(kv_s + st * C::kTile + p * C::kPanel + lane * a.box_tok * 128, &a.kv_map, p * 64, pc.h, row,
+                                         &s.kv_full[st]);
+                        }
+                    }
+                    if (scaled && lane < 8) {
+                        if (g_id >= 0) {
+                            cp_async_4(&s.scale[slot][plane][lane],
+                                       a.kv_scales + (static_cast<long long>(g_id * 2 + plane) * a.scale_groups + a.scale_div(g_off)) * a.Hkv + pc.h);
+                            cp_async_arrive(&s.kv_full[st]);
+                        } else {
+                            s.scale[slot][plane][lane] = 0.f;
+                            mbar_arrive(&s.kv_full[st]);
+                        }
+                    }
+                }
+            }
+        }
+        if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+        // no copy may be in flight at the end
+        for (int q = max(kvc - kCopyStages, 0); q < kvc; ++q)
+            if (!mbar_wait(&s.kv_full[q % kCopyStages], q / kCopyStages & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+    } else if (warp == 10) {
+        // ------------------------------------------------ copies of queries
+        set_regs_down<C::kRegsRest>();
+        int n = 0;
+        while (ok && pc.next(a)) {
+            if (pc.j1 <= pc.j0) continue;
+            if (n > 0 && !mbar_wait(&s.q_free, (n - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                const int tiles = pc.cell.cnt > a.tile_tok ? 2 : 1;
+                mbar_arrive_expect_tx(&s.q_full, tiles * a.tile_rows * D * 2);
+                for (int i = 0; i < tiles; ++i)
+                    for (int p = 0; p < C::kPanels; ++p)
+                        tma_load(q_s + i * C::kTile + p * C::kPanel, &a.q_map, p * 64, pc.h * a.grp,
+                                 pc.cell.row0 + i * a.tile_tok, &s.q_full);
+            }
+            ++n;
+        }
+        if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+        if (n > 0 && !mbar_wait(&s.q_full, (n - 1) & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+    } else if (warp == 9) {
+        // ------------------------------------------------ tensor-core products
+        set_regs_down<C::kRegsRest>();
+        if (lane == 0) {
+            constexpr uint32_t kIdQK = umma_idesc_bf16(128, kPreBlock, 0), kIdPV = umma_idesc_bf16(128, D, 1);
+            const uint64_t qd = umma_desc(q_s, 16, 1024), kd = umma_desc(kv_s, 16, 1024), vd = umma_desc(kv_s, C::kPanel, 1024);
+            int kvc = 0, n = 0;                      // K or V blocks, pieces with blocks
+            int pn[2] = {0, 0}, on[2] = {0, 0};      // P blocks, pieces with a product, of each tile
+            while (ok && pc.next(a)) {
+                if (pc.j1 <= pc.j0) continue;
+                const TileView v0(a, pc.cell, 0), v1(a, pc.cell, 1);
+                if (!mbar_wait(&s.q_full, n & 1)) {
+                    ok = false;
+                    break;
+                }
+                ++n;
+                int st = 0;
+                auto wait_block = [&](int q) {  // K or V block number q
+                    st = q % C::kStages;
+                    if (!mbar_wait(&s.ready[st], q / C::kStages & 1)) return false;
+                    tc_fence_after();
+                    return true;
+                };
+                auto qk = [&](int i) {
+                    const uint64_t aq = qd + static_cast<uint64_t>((i * C::kTile) >> 4), bk = kd + static_cast<uint64_t>((st * C::kTile) >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kPanel + (k & 3) * 32) >> 4);
+                        umma_bf16(t_s + i * 128, aq + o, bk + o, kIdQK, k > 0);
+                    }
+                    umma_commit(&s.s_full[i]);
+                };
+                bool begun[2] = {false, false};
+                const int jn = pc.j1 - pc.j0;
+                if (!wait_block(kvc)) {
+                    ok = false;
+                    break;
+                }
+                {
+                    const int t = pc.cell.block(pc.j0) * kPreBlock;
+                    if (v0.active(a, t)) qk(0);
+                    if (v1.active(a, t)) qk(1);
+                }
+                umma_commit(&s.used[st]);
+                if (jn == 1) umma_commit(&s.q_free);
+                for (int jj = 0; jj < jn && ok; ++jj) {
+                    const int t = pc.cell.block(pc.j0 + jj) * kPreBlock;
+                    const bool more = jj + 1 < jn;
+                    const int tn = more ? pc.cell.block(pc.j0 + jj + 1) * kPreBlock : 0;
+                    const int qv = kvc + 2 * jj + 1, qk_next = qv + 1;
+                    bool have_v = false, have_k = false;
+                    int vst = 0, kst = 0;
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        const TileView& v = i == 0 ? v0 : v1;
+                        if (v.active(a, t)) {
+                            if (!have_v) {
+                                ok = wait_block(qv);
+                                vst = st;
+                                have_v = true;
+                            }
+                            if (ok) ok = mbar_wait(&s.p_full[i], pn[i] & 1);
+                            ++pn[i];
+                            if (ok && !begun[i] && on[i] > 0) ok = mbar_wait(&s.o_free[i], (on[i] - 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t bv = vd + static_cast<uint64_t>((vst * C::kTile) >> 4);
+#pragma unroll
+                            for (int k = 0; k < kPreBlock / 16; ++k)
+                                umma_bf16_ta(t_o + i * D, t_s + i * 128 + k * 8, bv + static_cast<uint64_t>((k * 16 * 128) >> 4),
+                                             kIdPV, begun[i] || k > 0);
+                            umma_commit(&s.o_done[i]);
+                            if (!begun[i]) ++on[i];
+                            begun[i] = true;
+                        }
+                        if (more && v.active(a, tn)) {
+                            if (!have_k) {
+                                ok = wait_block(qk_next);
+                                kst = st;
+                                have_k = true;
+                            }
+                            if (!ok) break;
+                            st = kst;
+                            qk(i);
+                        }
+                    }
+                    if (!ok) break;
+                    if (!have_v) {
+                        ok = wait_block(qv);
+                        vst = st;
+                    }
+                    if (ok) umma_commit(&s.used[vst]);
+                    if (more) {
+                        if (ok && !have_k) {
+                            ok = wait_block(qk_next);
+                            kst = st;
+                        }
+                        if (ok) umma_commit(&s.used[kst]);
+                        if (jj + 2 == jn) umma_commit(&s.q_free);
+                    }
+                }
+                kvc += 2 * jn;
+            }
+            if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+            // no product may be in flight at the end
+            umma_commit(&s.drain);
+            if (!mbar_wait(&s.drain, 0)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+        }
+    } else if (warp >= 11) {
+        // ------------------------------------------------ making blocks ready
+        set_regs_down<C::kRegsRest>();
+        const int w = warp - 11;
+        int kvc = 0;
+        while (ok && pc.next(a)) {
+            for (int j = pc.j0; j < pc.j1 && ok; ++j) {
+                const int t0 = pc.cell.block(j) * kPreBlock, hi = pc.cell.hi, lo = pc.cell.lo, se = pc.cell.s_end;
+                for (int plane = 0; plane < 2; ++plane, ++kvc) {
+                    const int st = kvc % C::kStages, rst = kvc % kCopyStages, slot = (kvc >> 1) % C::kInfo;
+                    if (!mbar_wait(&s.kv_full[rst], kvc / kCopyStages & 1) ||
+                        (C::kCodes && !mbar_wait(&s.used[st], (kvc / C::kStages & 1) ^ 1))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t groups = s.valid[slot];
+                    const bool all = groups == 0xffu && t0 + kPreBlock <= hi && (t0 >= lo || t0 + kPreBlock <= se);
+                    auto seen = [&](int r) {
+                        const int t = t0 + r;
+                        return ((groups >> (r >> 4)) & 1u) && t < hi && (t >= lo || t < se);
+                    };
+                    const uint32_t dst = kv_s + st * C::kTile;
+                    if constexpr (!C::kCodes) {
+                        if (plane == 1 && !all) {
+                            // two rows at a time, a 16-byte chunk a lane (the swizzle only permutes a row's chunks)
+                            constexpr int kChunks = D / 8;  // chunks of a row
+                            for (int i = lane; i < kPreBlock * kChunks; i += 32) {
+                                const int r = i / kChunks, ch = i % kChunks;
+                                if (!seen(r)) st_zero16(dst + (ch >> 3) * C::kPanel + r * 128 + (ch & 7) * 16);
+                            }
+                            fence_proxy_async_smem();
+                        }
+                    } else {
+                        // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one
+                        constexpr int kQ = D / 16;
+                        const uint32_t src = raw_s + rst * C::kRaw;
+                        for (int i = w; i < kPreBlock / 8 * (kQ / 4); i += C::kHelpers) {
+                            const int r = i / (kQ / 4) * 8 + (lane & 7), q = i % (kQ / 4) * 4 + (lane >> 3);
+                            const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
+                            uint4 c = make_uint4(0, 0, 0, 0);
+                            const bool use = plane == 0 || all || seen(r);
+                            if (use) c = ld_shared16(src + at);
+                            const float f = plane == 1 && scaled && use ? s.scale[slot][1][r >> 4] : 1.f;
+                            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float2 x = code_pair<KIND>(in[k] & 0xffffu), y = code_pair<KIND>(in[k] >> 16);
+                                if (plane == 1) {
+                                    x = mul2(x, both(f));
+                                    y = mul2(y, both(f));
+                                }
+                                o[2 * k] = pack_bf16x2(x.x, x.y);
+                                o[2 * k + 1] = pack_bf16x2(y.x, y.y);
+                            }
+                            const uint32_t row = dst + (q >> 2) * C::kPanel + r * 128;
+                            const int ch = (q & 3) * 2;
+                            st_shared16(row + ((ch ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                            st_shared16(row + (((ch + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&s.ready[st]);
+                        if (C::kCodes) mbar_arrive(&s.kv_free[rst]);
+                    }
+                }
+            }
+        }
+        if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+    } else {
+        // ------------------------------------------------ softmax of tile i
+        set_regs_up<C::kRegsSoftmax>();
+        const int i = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t my_s = t_s + i * 128 + lanes, my_o = t_o + i * D + lanes;
+        const int tk = a.grp_div(r), g = r - tk * a.grp;  // token of the tile, head of the group
+        int sn = 0, pieces = 0, kvb = 0;  // blocks of this tile; pieces; blocks of the thread block
+        int head = 0, begun = 0, m_row0 = 0, m_cnt = 0, m_h = 0;
+        while (ok && pc.next(a)) {
+            const PreCell& cell = pc.cell;
+            const TileView view(a, cell, i);
+            const int p = cell.p0 + i * a.tile_tok + tk;
+            const bool row = tk < view.cnt && r < a.tile_rows;
+            const int lim = row && p >= 0 ? max(p + 1, cell.pre) : 0, lo = p - a.window + 1;
+            float slope2 = 0.f;
+            if (SHAPED && a.slopes && row) slope2 = __ldg(a.slopes + pc.h * a.grp + g) * kLog2e;
+            float m = kNone;
+            float2 l[2] = {both(0.f), both(0.f)};
+            int nact = 0;
+            for (int j = pc.j0; j < pc.j1; ++j, ++kvb) {
+                const int t0 = cell.block(j) * kPreBlock;
+                if (!view.active(a, t0)) continue;
+                if (!mbar_wait(&s.s_full[i], sn & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
+                const uint32_t groups = s.valid[kvb % C::kInfo];
+                tmem_wait_ld();
+                if (SHAPED) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float f = scaled ? a.sl2 * s.scale[kvb % C::kInfo][0][k] : a.sl2;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            uint32_t* y = &x[k >> 1][(k & 1) * 16 + e];
+                            const float2 z = mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), both(f));
+                            y[0] = __float_as_uint(z.x);
+                            y[1] = __float_as_uint(z.y);
+                        }
+                    }
+                    if (a.cap2 > 0.f) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float top = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(x[k][e])));
+                            // (a NaN passes the comparison of the others and stays one)
+                            if (top <= a.cap2) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 z = cap_near(make_float2(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])), a.cap2, a.inv_cap2);
+                                    x[k][e] = __float_as_uint(z.x);
+                                    x[k][e + 1] = __float_as_uint(z.y);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float y = __uint_as_float(x[k][e]) * a.inv_cap2;
+                                    x[k][e] = __float_as_uint(a.cap2 - __fdividef(2.f * a.cap2, 1.f + ex2(2.f * kLog2e * y)));
+                                }
+                            }
+                        }
+                    }
+                    if (a.slopes) {
+                        const float far = static_cast<float>(p - t0);
+#pragma unroll
+                        for (int e = 0; e < 128; ++e) {
+                            uint32_t& y = x[e >> 5][e & 31];
+                            y = __float_as_uint(fmaf(-slope2, fabsf(far - static_cast<float>(e)), __uint_as_float(y)));
+                        }
+                    }
+                }
+                if (groups != 0xffu || !view.whole(a, t0)) {
+                    // key t0 + e counts iff e < lim - t0 and (e >= lo - t0 or e < sinks - t0), its group was copied
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
+                        const int t = t0 + 32 * k;
+                        uint32_t bits = below(lim - t) & (~below(lo - t) | below(a.sinks - t));
+                        bits &= ((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) x[k][e] = 0xff800000u;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])));
+                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (!SHAPED) mx *= a.sl2;
+                const bool move = mx > m + 8.f;
+                if (nact == 0) {
+                    if (move) m = mx;
+                } else if (__any_sync(0xffffffffu, move)) {
+                    float f = 1.f;
+                    if (move) {
+                        f = ex2(m - mx);
+                        m = mx;
+                    }
+                    l[0] = mul2(l[0], both(f));
+                    l[1] = mul2(l[1], both(f));
+                    // the product before must be in O
+                    if (!mbar_wait(&s.o_done[i], (sn - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(my_o + k, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(my_o + k, o);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[16];
+                    numerators<SHAPED>(x[k], a.sl2, m, l, o);
+                    tmem_st16(my_s + 16 * k, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&s.p_full[i]);
+                ++sn;
+                ++nact;
+            }
+            if (!ok) break;
+            if (nact > 0) {
+                if (!mbar_wait(&s.o_done[i], (sn - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+            }
+            // ---- the piece's result
+            const float sum = l[0].x + l[0].y + l[1].x + l[1].y;
+            const bool part = pc.j0 > 0 || pc.j1 < cell.nt;
+            if (pieces == 0 && pc.j0 > 0) head = pc.j1 < cell.nt ? 2 : 1;
+            begun = pc.j0 == 0 && pc.j1 < cell.nt;
+            if (begun) {
+                m_row0 = cell.row0;
+                m_cnt = cell.cnt;
+                m_h = pc.h;
+            }
+            const int token = cell.row0 + i * a.tile_tok + tk;
+            const long long orow = static_cast<long long>(token) * a.Hq + pc.h * a.grp + g;
+            const long long prow = (2LL * blockIdx.x + (pc.j0 > 0 ? 0 : 1)) * kPreSlotRows + i * kPreTile + r;
+            // sum == 0: no visible key (a NaN goes through to the output)
+            const float f = part ? a.out_scale : sum == 0.f ? 0.f : a.out_scale / sum;
+            if (row) {
+                if (part) {
+                    *reinterpret_cast<float2*>(a.ws_ml + 2 * prow) = make_float2(sum == 0.f ? -INFINITY : m, sum);
+                } else if (a.lse) {
+                    a.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < D; k += 32) {
+                uint32_t o[32];
+                if (nact > 0) {
+                    tmem_ld32(my_o + k, o);
+                    tmem_wait_ld();
+                }
+                if (nact == 0 || sum == 0.f) {  // (O may hold anything)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (!row) continue;
+                if (part) {
+                    float* op = a.ws_o + prow * D + k;
+#pragma unroll
+                    for (int q = 0; q < 32; q += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[q + e]) * f);
+                        st_global32(op + q, v);
+                    }
+                } else {
+                    __nv_bfloat16* op = a.out + orow * D + k;
+#pragma unroll
+                    for (int q = 0; q < 32; q += 16) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = pack_bf16x2(__uint_as_float(o[q + 2 * e]) * f, __uint_as_float(o[q + 2 * e + 1]) * f);
+                        st_global32(op + q, v);
+                    }
+                }
+            }
+            if (nact > 0) {
+                tc_fence_before();
+                mbar_arrive(&s.o_free[i]);
+            }
+            ++pieces;
+        }
+        if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+        if (threadIdx.x == 0 && a.cut) {
+            a.ws_meta[2 * blockIdx.x] = make_int4(ok ? begun : 0, pieces == 0 ? 3 : head, m_row0, m_cnt);
+            a.ws_meta[2 * blockIdx.x + 1] = make_int4(m_h, 0, 0, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int KIND, bool SHAPED>
+cudaError_t launch(const PreArgs& a, cudaStream_t stream) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices];
+    constexpr int bytes = smem_bytes<D, KIND>();
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    auto kern = gqa_prefill_kernel<D, KIND, SHAPED>;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kDevices;
+    if (!known || !done[dev].load(std::memory_order_relaxed)) {
+        if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); e != cudaSuccess) return e;
+        if (known) done[dev].store(true, std::memory_order_relaxed);
+    }
+    return launch_with_pdl(kern, dim3(a.grid), dim3(Cfg<D, KIND>::kThreads), bytes, stream, a);
+}
+
+template <int KIND, bool SHAPED>
+cudaError_t dispatch(const PreArgs& a, int D, cudaStream_t stream) {
+    return D == 128 ? launch<128, KIND, SHAPED>(a, stream) : launch<64, KIND, SHAPED>(a, stream);
+}
+
+}  // namespace pre
+}  // namespace mqa

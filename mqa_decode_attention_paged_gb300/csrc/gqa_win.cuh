@@ -56,6 +56,8 @@ struct WinArgs {
     int* status;
     float sl2;        // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
     float out_scale;  // v_scale of a per-tensor e4m3 cache, else 1
+    float cap2, inv_cap2;  // softcap * log2(e) and its reciprocal, or 0 (shaped logits only, like the next)
+    const float* slopes;   // [Hq], or null
     int batch, q_len, Hq, Hkv, grp, rows;  // rows = q_len * grp: query rows of a KV head
     int num_blocks, page, max_blocks;
     int window, sinks;
@@ -153,6 +155,9 @@ __host__ __device__ constexpr int win_mblocks(int kind, int nhb, int D) {
 cudaError_t win_stage1_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_stage1_int8(const WinArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t win_shaped_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t win_shaped_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t win_shaped_int8(const WinArgs& a, int D, int grid, cudaStream_t stream);
 cudaError_t win_merge(const WinArgs& a, int D, cudaStream_t stream);
 
 }  // namespace mqa

@@ -4,7 +4,7 @@
 namespace mqa {
 
 cudaError_t win_stage1_bf16(const WinArgs& a, int D, int grid, cudaStream_t stream) {
-    return win::dispatch<kWinBf16>(a, D, grid, stream);
+    return win::dispatch<kWinBf16, false>(a, D, grid, stream);
 }
 
 }  // namespace mqa

@@ -4,7 +4,7 @@
 namespace mqa {
 
 cudaError_t win_stage1_e4m3(const WinArgs& a, int D, int grid, cudaStream_t stream) {
-    return win::dispatch<kWinE4m3>(a, D, grid, stream);
+    return win::dispatch<kWinE4m3, false>(a, D, grid, stream);
 }
 
 }  // namespace mqa

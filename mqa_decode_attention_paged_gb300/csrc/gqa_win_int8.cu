@@ -4,7 +4,7 @@
 namespace mqa {
 
 cudaError_t win_stage1_int8(const WinArgs& a, int D, int grid, cudaStream_t stream) {
-    return win::dispatch<kWinInt8>(a, D, grid, stream);
+    return win::dispatch<kWinInt8, false>(a, D, grid, stream);
 }
 
 }  // namespace mqa

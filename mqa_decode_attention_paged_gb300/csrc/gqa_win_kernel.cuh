@@ -280,8 +280,15 @@ constexpr int kFirst = 1 << 11, kLast = 1 << 12, kWhole = 1 << 13;  // of the ti
 constexpr int kAct = 1 << 14, kEdge = 1 << 18, kBlocks = 15;
 constexpr int kSteps2 = 22;  // bits 22 + 2j: scales from the box's first to that of its 16 tokens number j + 1
 
-// MULTI: more than one query position per request.
-template <int D, int KIND, int NHB, bool MULTI>
+// A base-2 logit x capped: cap2 tanh(x / cap2), as 1 - 2 / (1 + e^{2y}) (within 2^-23 of the
+// cap; infinities become +-cap2, a NaN stays one).
+__device__ __forceinline__ float capped(float x, float cap2, float inv_cap2) {
+    return cap2 - __fdividef(2.f * cap2, 1.f + ex2(2.f * kLog2e * inv_cap2 * x));
+}
+
+// MULTI: more than one query position per request.  SHAPED: logits capped by
+// a.cap2 (if > 0) and biased by -slope |p - t| (if a.slopes), in that order.
+template <int D, int KIND, int NHB, bool MULTI, bool SHAPED>
 __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(const __grid_constant__ WinArgs a) {
     using C = Cfg<D, KIND, NHB>;
     constexpr int MT = C::kMT;
@@ -496,6 +503,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
     uint32_t qb[NHB][C::kSteps][2];
     float o[NHB][C::kSteps][4];
     float m_ref[NHB][2], r_ref[NHB][2], l_part[NHB][2];
+    float slope2[SHAPED ? NHB : 1][2] = {};  // of rows 2c, 2c + 1 of each row group, in base 2
 
     for (; tile < tiles; ++tile) {
         // boxes are complete as many tiles ahead as copies run ahead of the
@@ -552,6 +560,14 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
                     o[hb][mb][0] = o[hb][mb][1] = o[hb][mb][2] = o[hb][mb][3] = 0.f;
                 m_ref[hb][0] = m_ref[hb][1] = r_ref[hb][0] = r_ref[hb][1] = kNone;
                 l_part[hb][0] = l_part[hb][1] = 0.f;
+                if (SHAPED && a.slopes) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int Re = row0 + hb * 8 + 2 * c + e;
+                        slope2[SHAPED ? hb : 0][e] =
+                            Re < a.rows ? __ldg(a.slopes + kh * a.grp + Re - (MULTI ? a.grp_div(Re) * a.grp : 0)) * kLog2e : 0.f;
+                    }
+                }
             }
         }
 
@@ -612,6 +628,31 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
                     for (int e = 0; e < 4; ++e)
                         x[m][hb][e] =
                             (kChains == 1 ? st[0][m][hb][e] : st[0][m][hb][e] + st[kChains - 1][m][hb][e]) * ksc;
+            }
+            if (SHAPED) {
+                if (a.cap2 > 0.f)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[m][hb][e] = capped(x[m][hb][e], a.cap2, a.inv_cap2);
+                if (a.slopes) {
+                    const Rows rows = rows_of(d.z);
+#pragma unroll
+                    for (int hb = 0; hb < NHB; ++hb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // (t <= p where t is seen)
+                            const int ahead = t0 + g - rows.at(a, hb * 8 + 2 * c + e);
+                            const float far = static_cast<float>(ahead), sl = slope2[SHAPED ? hb : 0][e];
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) {
+                                x[m][hb][e] = fmaf(sl, far + static_cast<float>(16 * m), x[m][hb][e]);
+                                x[m][hb][2 + e] = fmaf(sl, far + static_cast<float>(16 * m + 8), x[m][hb][2 + e]);
+                            }
+                        }
+                }
             }
         }
         refill();
@@ -961,7 +1002,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
 
 // Lets `kern` (one of the two of this instance) use all of a block's shared
 // memory, once per device.
-template <int D, int KIND, int NHB>
+template <int D, int KIND, int NHB, bool SHAPED>
 cudaError_t allow_smem(const void* kern, bool multi) {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[2][kDevices];
@@ -974,7 +1015,7 @@ cudaError_t allow_smem(const void* kern, bool multi) {
     return e;
 }
 
-template <int D, int KIND, int NHB>
+template <int D, int KIND, int NHB, bool SHAPED>
 cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     const int vb = a.batch * a.rb;
     const int limit = 228 * 1024 / (a.alone ? 1 : win_ctas_per_sm(NHB, D)) - 1024;  // a block's share of an SM's
@@ -983,24 +1024,24 @@ cudaError_t launch(WinArgs a, int grid, cudaStream_t stream) {
     a.nslots = ns;
     const int bytes = layout<D, KIND, NHB>(a.Hkv, a.ts, ns, vb, a.batch).total;
     // (more than 16 rows of a KV head are several positions')
-    auto kern = NHB > 2 || a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true>
-                                       : gqa_win_kernel<D, KIND, NHB <= 2 ? NHB : 1, false>;
-    if (cudaError_t e = allow_smem<D, KIND, NHB>(reinterpret_cast<const void*>(kern), a.q_len > 1); e != cudaSuccess) return e;
+    auto kern = NHB > 2 || a.q_len > 1 ? gqa_win_kernel<D, KIND, NHB, true, SHAPED>
+                                       : gqa_win_kernel<D, KIND, NHB <= 2 ? NHB : 1, false, SHAPED>;
+    if (cudaError_t e = allow_smem<D, KIND, NHB, SHAPED>(reinterpret_cast<const void*>(kern), a.q_len > 1); e != cudaSuccess) return e;
     return launch_with_pdl(kern, dim3(grid), dim3(32 * a.Hkv * a.ts), bytes, stream, a);
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool SHAPED>
 cudaError_t dispatch_rows(const WinArgs& a, int grid, cudaStream_t stream) {
     switch (win_row_groups(a.rbn)) {
-        case 1: return launch<D, KIND, 1>(a, grid, stream);
-        case 2: return launch<D, KIND, 2>(a, grid, stream);
-        default: return launch<D, KIND, 3>(a, grid, stream);
+        case 1: return launch<D, KIND, 1, SHAPED>(a, grid, stream);
+        case 2: return launch<D, KIND, 2, SHAPED>(a, grid, stream);
+        default: return launch<D, KIND, 3, SHAPED>(a, grid, stream);
     }
 }
 
-template <int KIND>
+template <int KIND, bool SHAPED>
 cudaError_t dispatch(const WinArgs& a, int D, int grid, cudaStream_t stream) {
-    return D == 128 ? dispatch_rows<128, KIND>(a, grid, stream) : dispatch_rows<64, KIND>(a, grid, stream);
+    return D == 128 ? dispatch_rows<128, KIND, SHAPED>(a, grid, stream) : dispatch_rows<64, KIND, SHAPED>(a, grid, stream);
 }
 
 }  // namespace win

@@ -1,0 +1,234 @@
+"""gqa_prefill against attention in 64 bits (attention_reference.py): formats, head layouts, page sizes, ragged
+lengths from no token to long ones, windows, sinks, prefixes, caps and biases, cut and uncut."""
+import itertools
+import os
+
+import pytest
+import torch
+
+import mqa_decode_attention_paged_gb300 as mqa
+from attention_reference import NO_WINDOW, Paged, attention, judge
+
+pytestmark = pytest.mark.gpu
+
+
+def slopes_of(Hq):
+    return torch.exp2(-8.0 * torch.arange(1, Hq + 1, device="cuda") / Hq).float()
+
+
+def batch(new, old, Hq, D, pad=0, seed=1, size=1.0, fused=False, lead=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    T = sum(new) + pad + lead
+    if fused:
+        q = (torch.randn(T, Hq + 4, D, generator=g, device="cuda") * size).to(torch.bfloat16)[:, 2:2 + Hq]
+    else:
+        q = (torch.randn(T, Hq, D, generator=g, device="cuda") * size).to(torch.bfloat16)
+    starts = torch.tensor([lead] + [lead + s for s in itertools.accumulate(new)], dtype=torch.int32, device="cuda")
+    return q, starts, [a + b for a, b in zip(new, old)]
+
+
+def run(new, old, Hq=8, Hkv=2, D=128, page=16, kv="bf16", group=0, window=NO_WINDOW, sinks=0, prefix=None, cap=0.0,
+        slopes=False, splits=None, pad=0, size=1.0, fused=False, lead=0, value=1.0, scale=None, seed=1):
+    q, starts, lens = batch(new, old, Hq, D, pad, seed, size, fused, lead)
+    c = Paged(lens, Hkv, D, page, kv, seed, group, value=value)
+    scale = D ** -0.5 if scale is None else scale
+    sl = slopes_of(Hq) if slopes else None
+    pre = None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    out = torch.full((q.shape[0], Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], Hq), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, scale, softcap=cap, slopes=sl, window=window, sinks=sinks,
+                    prefix_lens=pre, kv_scales=c.scales, k_scale=c.k_scale, v_scale=c.v_scale, out=out, lse=lse,
+                    num_kv_splits=splits, device_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    at = lead
+    for b, k in enumerate(new):
+        if k:
+            ref = attention(q[at:at + k], c.K[b], c.V[b], lens[b] - k, scale, cap, sl, window, sinks,
+                            min(max(prefix[b], 0), lens[b]) if prefix else 0)
+            judge(out[at:at + k], lse[at:at + k], ref, f"request {b}")
+        at += k
+    for x in (out[:lead], out[at:], lse[:lead], lse[at:]):
+        assert bool((x == 7.0).all()), "padding rows are left as they were"
+    return out, lse
+
+
+@pytest.mark.parametrize("splits", [1, None])
+@pytest.mark.parametrize("kv,group", [("bf16", 0), ("fp8_e4m3", 0), ("fp8_e4m3_block", 16), ("int8_block", 32)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_formats(kv, group, D, splits):
+    run([37, 1, 300, 0, 129], [0, 500, 70, 10, 1], D=D, page=32, kv=kv, group=group, splits=splits, pad=3)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 2), (6, 2), (7, 1), (32, 8), (10, 5), (16, 1), (48, 3), (71, 1), (128, 1), (40, 40)])
+def test_heads(Hq, Hkv):
+    run([1, 150, 3], [5, 40, 0], Hq=Hq, Hkv=Hkv, pad=1)
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 80, 128, 144, 256, 1024])
+def test_pages(page):
+    run([200, 5], [90, 700], page=page)
+    run([200, 5], [90, 700], page=page, kv="int8_block", D=64)
+
+
+@pytest.mark.parametrize("new,old", [([1], [0]), ([1], [127]), ([1], [128]), ([32], [0]), ([33], [0]), ([64], [64]),
+                                     ([65], [63]), ([127, 128, 129], [1, 0, 255]), ([1] * 40, list(range(40))),
+                                     ([0, 0, 5, 0], [0, 3, 0, 9]), ([2000], [3000]), ([3], [9000])])
+def test_lengths(new, old):
+    for splits in (1, None):
+        run(new, old, splits=splits)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 5), (16, 0), (100, 4), (128, 128), (129, 130), (333, 1), (1000, 17)])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (2, 2)])
+def test_windows(window, sinks, Hq, Hkv):
+    run([300, 1, 40], [200, 700, 0], Hq=Hq, Hkv=Hkv, window=window, sinks=sinks)
+    run([300, 1, 40], [200, 700, 0], Hq=Hq, Hkv=Hkv, window=window, sinks=sinks, kv="fp8_e4m3_block", group=16, D=64)
+
+
+@pytest.mark.parametrize("window", [NO_WINDOW, 90])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_prefixes(slopes, window):
+    run([300, 1, 40, 200], [0, 700, 100, 50], prefix=[250, 0, 1000, -4], slopes=slopes, window=window)
+    run([300, 40], [0, 100], prefix=[129, 110], Hq=4, Hkv=4, slopes=slopes, window=window, sinks=3, kv="int8_block")
+
+
+@pytest.mark.parametrize("cap", [5.0, 15.0, 50.0, 1e9])
+@pytest.mark.parametrize("size", [0.5, 4.0, 40.0])
+def test_caps(cap, size):
+    run([200, 1], [60, 300], cap=cap, size=size)
+    run([200, 1], [60, 300], cap=cap, size=size, slopes=True, kv="fp8_e4m3", D=64)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8_block"])
+def test_distance_bias(kv):
+    run([200, 1, 5], [60, 3000, 9], slopes=True, kv=kv)
+    run([200, 1, 5], [60, 3000, 9], slopes=True, kv=kv, window=70, sinks=2, Hq=6, Hkv=3)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-6, 3.0])
+def test_scales(scale):
+    run([150], [30], scale=scale)
+
+
+def test_large_logits_move_the_reference():
+    # logits of hundreds: rows' references move often, in both tiles
+    run([260], [500], size=20.0, scale=1.0)
+    run([260], [500], size=20.0, scale=1.0, kv="fp8_e4m3_block", D=64)
+
+
+def test_fused_projection_and_padding():
+    run([70, 1, 9], [10, 90, 0], fused=True, pad=9, lead=5)
+    run([1], [90], Hq=1, Hkv=1, fused=True)
+
+
+def test_values_of_unlike_magnitude():
+    run([200], [60], value=1e-6)
+    run([200], [60], value=1e4, scale=1e-9)
+
+
+def test_many_requests():
+    run([1 + i % 3 for i in range(700)], [i % 90 for i in range(700)], Hq=4, Hkv=1, D=64)
+
+
+def test_queries_before_the_first_position():
+    # fewer tokens in the sequence than new ones: the first queries see nothing
+    q, starts, _ = batch([6], [0], 8, 128)
+    c = Paged([4], 2, 128, 16, "bf16")
+    out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, prefix_lens=torch.tensor([3], dtype=torch.int32, device="cuda"))
+    judge(out, lse, attention(q, c.K[0], c.V[0], -2, 0.1, prefix=3))
+    assert bool((out[:2] == 0).all()) and bool((lse[:2] == -float("inf")).all())
+
+
+def test_an_empty_sequence_and_an_empty_batch():
+    q, starts, _ = batch([3], [0], 8, 128)
+    c = Paged([0], 2, 128, 16, "bf16")
+    for splits in (1, None):
+        out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, num_kv_splits=splits)
+        assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+    none = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, lse = mqa.gqa_prefill(q[:0], c.cache, c.table, c.seq_lens, none, 0.1)
+    assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+
+
+def test_uncut_results_do_not_depend_on_the_batch():
+    q, starts, lens = batch([37, 200, 90], [10, 300, 5], 8, 128)
+    c = Paged(lens, 2, 128, 16, "bf16")
+    out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, num_kv_splits=1)
+    one = torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+    o1, l1 = mqa.gqa_prefill(q[37:237].contiguous(), c.cache, c.table[1:2].contiguous(), c.seq_lens[1:2].contiguous(), one, 0.1,
+                             num_kv_splits=1)
+    assert torch.equal(out[37:237], o1) and torch.equal(lse[37:237], l1)
+
+
+def test_reproducible():
+    q, starts, lens = batch([64, 1, 700], [9000, 4000, 0], 32, 128)
+    c = Paged(lens, 8, 128, 64, "bf16")
+    ref = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1)
+    for _ in range(5):
+        got = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_bad_block_ids_and_lengths():
+    q, starts, lens = batch([40, 40], [100, 100], 8, 128)
+    c = Paged(lens, 2, 128, 16, "bf16")
+    for bad in (-1, c.cache.shape[0], 2 ** 31 - 1):
+        table = c.table.clone()
+        table[0, 3] = bad
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = mqa.gqa_prefill(q, c.cache, table, c.seq_lens, starts, 0.1, device_status=status)
+        assert int(status) == 5
+        judge(out[40:], lse[40:], attention(q[40:], c.K[1], c.V[1], 100, 0.1))
+        # the block's tokens are not seen
+        K, V = (torch.cat([x[:48], x[64:]]) for x in (c.K[0], c.V[0]))
+        ref = attention(q[:40], K, V, 84, 0.1)
+        judge(out[:40], lse[:40], ref)
+    for lengths, start in (([10 ** 6, 140], None), ([-5, 140], None), ([140, 140], [0, 90, 80]), ([140, 140], [-3, 40, 80]),
+                           ([140, 140], [0, 40, 1000])):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        st = starts if start is None else torch.tensor(start, dtype=torch.int32, device="cuda")
+        mqa.gqa_prefill(q, c.cache, c.table, torch.tensor(lengths, dtype=torch.int32, device="cuda"), st, 0.1,
+                        device_status=status)
+        assert int(status) == 5
+
+
+def test_captured_and_replayed_on_two_streams():
+    q, starts, lens = batch([64, 3], [3000, 100], 32, 128)
+    c = Paged(lens, 8, 128, 64, "bf16")
+    want = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1)
+    outs = []
+    for _ in range(2):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1)
+        outs.append((g, s, got))
+    for g, s, got in outs:
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, got in outs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_wait_that_runs_out(monkeypatch):
+    import ctypes
+    from mqa_decode_attention_paged_gb300 import _binding as b
+    monkeypatch.setenv("MQA_ENABLE_TEST_HOOKS", "1")
+    q, starts, lens = batch([64, 64], [200, 100], 8, 128)
+    c = Paged(lens, 2, 128, 16, "bf16")
+    out = torch.zeros_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    P = ctypes.c_void_p
+    fn = b.lib.mqa_test_gqa_prefill_withheld
+    fn.argtypes = [P] * 5 + [ctypes.c_float, P] + [ctypes.c_int] * 8 + [ctypes.c_longlong, P, P, ctypes.c_int]
+    rc = fn(q.data_ptr(), c.cache.data_ptr(), c.table.data_ptr(), c.seq_lens.data_ptr(), starts.data_ptr(), 0.1,
+            out.data_ptr(), 128, 2, 8, 2, 128, c.cache.shape[0], 16, c.table.shape[1], q.stride(0), status.data_ptr(),
+            torch.cuda.current_stream().cuda_stream, 1)
+    torch.cuda.synchronize()
+    assert rc == 0 and int(status) == 6
+    run([37], [10])  # the context goes on
