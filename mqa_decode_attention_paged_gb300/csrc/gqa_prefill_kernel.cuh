@@ -15,7 +15,8 @@
 //   9          issues the tensor-core products: S_i = Q_i K^T (M = 128 rows, N =
 //              128 keys) and O_i += P_i V, for the two tiles in turn, so that one
 //              tile's softmax runs beside the other's products
-//   10         copies the queries
+//   10         walks the thread block's pieces, describes them for the others in a
+//              ring in shared memory, and copies their queries
 //   11..       make blocks ready: clear V rows that no row of the cell sees
 //              (whatever bytes they hold: 0 * NaN), and widen 8-bit codes to bf16
 // TMEM (512 columns): O_0, O_1 (D fp32 columns each), S_0, S_1 (128 each); P_i
@@ -55,18 +56,29 @@ struct Cfg {
     static constexpr int kInfo = 16;  // blocks whose validity and scales are kept
 };
 
+// A piece: blocks [j0, j1) of a cell's keys for one KV head (see PreCell).
+struct Piece {
+    int row0, cnt, p0, pre;
+    int hi, lo, s_end, ns;
+    int w0, nt, j0, j1;
+    int b, h, more, unused;  // more: 0 behind the last piece
+    __device__ __forceinline__ int block(int j) const { return j < ns ? j : w0 + j - ns; }
+};
+constexpr int kPieces = 4;  // described ahead
+
 struct Shared {
     uint64_t kv_full[8];   // copies landed (a raw stage's for codes)
     uint64_t kv_free[8];   // codes: read by the helpers; bf16: see ready / used
     uint64_t ready[8];     // a bf16 stage may be multiplied
     uint64_t used[8];      // .. and was
     uint64_t q_full, q_free;
+    uint64_t piece_full[kPieces], piece_free[kPieces];
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2], drain;
     long long scan[16];
     long long total;
     int b[2], u[2], h[2], j[2];  // start and end of the block's share
     uint32_t tmem;
-    int failed;
+    Piece piece[kPieces];
     uint32_t valid[16];      // 16-token groups of a block that were copied
     float scale[16][2][8];   // their K and V scales
 };
@@ -138,19 +150,26 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// x := cap2 tanh(x / cap2).  For |y| <= 1, tanh(y) = y (c0 + .. + c5 y^10), least
-// squares towards the smallest absolute error, 2.4e-7 (of logits capped at 50:
-// 1.7e-5 in base 2, far below the 2^-9 of P's rounding); beyond, 1 - 2 / (1 + e^{2y}).
-__device__ __forceinline__ float2 cap_near(float2 x, float cap2, float inv) {
-    const float2 y = mul2(x, both(inv)), z = mul2(y, y);
-    float2 w = fma2(z, both(-0.002839464694f), both(0.01611417904f));
-    w = fma2(w, z, both(-0.05097286030f));
-    w = fma2(w, z, both(0.1325352489f));
-    w = fma2(w, z, both(-0.3332400322f));
-    w = fma2(w, z, both(0.9999968409f));
-    return mul2(mul2(y, both(cap2)), w);
+// Three-way maxima, of the values and of their magnitudes.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
+// cap2 tanh(y) / y for |y| <= 1 (see kTanh).
+__device__ __forceinline__ float2 tanh_over(const float (&c)[6], float2 y) {
+    const float2 z = mul2(y, y);
+    float2 w = fma2(z, both(c[5]), both(c[4]));
+#pragma unroll
+    for (int k = 3; k >= 0; --k) w = fma2(w, z, both(c[k]));
+    return w;
+}
 // ---- codes
 __device__ __forceinline__ float2 half2_f32(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -168,7 +187,7 @@ __device__ __forceinline__ float2 code_pair(uint32_t w) {
     }
 }
 
-// Walks the pieces of a thread block's share; the same in every role.
+// Walks the pieces of a thread block's share.
 struct Pieces {
     PreReq req;
     PreCell cell;
@@ -227,7 +246,7 @@ struct Pieces {
 struct TileView {
     int cnt;      // tokens
     int lo_first, lo_last, lim_first, lim_last;
-    __device__ __forceinline__ TileView(const PreArgs& a, const PreCell& c, int i) {
+    __device__ __forceinline__ TileView(const PreArgs& a, const Piece& c, int i) {
         const int t0 = i * a.tile_tok;
         cnt = min(a.tile_tok, c.cnt - t0);
         const int p0 = c.p0 + t0, p1 = p0 + cnt - 1;
@@ -371,13 +390,13 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
     __syncthreads();
 }
 
-// P of 32 logits (base 2, x - m) as bf16 pairs; their sum is added to l.
-template <bool SHAPED>
+// P of 32 logits as bf16 pairs; their sum is added to l.  FORM 0: logits are sl2 s, 1: s, 2: s is less m already.
+template <int FORM>
 __device__ __forceinline__ void numerators(const uint32_t (&s)[32], float sl2, float m, float2 (&l)[2], uint32_t (&p)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const float2 x = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-        const float2 y = SHAPED ? add2(x, both(-m)) : fma2(x, both(sl2), both(-m));
+        const float2 y = FORM == 2 ? x : FORM == 1 ? add2(x, both(-m)) : fma2(x, both(sl2), both(-m));
         const float2 e = make_float2(ex2(y.x), ex2(y.y));
         l[k & 1] = add2(l[k & 1], e);
         p[k] = pack_bf16x2(e.x, e.y);
@@ -419,6 +438,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             mbar_init(&s.o_free[i], 128);
         }
         mbar_init(&s.drain, 1);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&s.piece_full[i], 1);
+            mbar_init(&s.piece_free[i], 2 + C::kHelpers + 8);  // the warps that read it
+        }
         fence_mbar_init();
     }
     if (warp == 9) tmem_alloc(&s.tmem, 512);
@@ -432,25 +455,36 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     const uint32_t tmem = s.tmem;
     const uint32_t t_o = tmem, t_s = tmem + 2 * D;  // tile i: t_o + i D, t_s + 128 i
 
-    Pieces pc;
-    pc.init(a, s);
     bool ok = true;
+    // Piece number n, once it is described; false behind the last one (or where the wait ran out).
+    auto piece = [&](int n) -> const Piece* {
+        const Piece* pc = &s.piece[n % kPieces];
+        if (!mbar_wait(&s.piece_full[n % kPieces], n / kPieces & 1)) {
+            ok = false;
+            return nullptr;
+        }
+        return pc->more ? pc : nullptr;
+    };
+    auto piece_done = [&](int n) { mbar_arrive(&s.piece_free[n % kPieces]); };
 
     if (warp == 8) {
         // ------------------------------------------------ copies of K and V
         set_regs_down<C::kRegsRest>();
-        const int nb = kPreBlock / a.box_tok;
+        const int nb = kPreBlock / a.box_tok, per = a.box_tok / 16;
         int kvc = 0;  // blocks of K or V copied
-        while (ok && pc.next(a)) {
-            const int b = pc.b < a.batch ? pc.b : pc.eb;
-            if (b == a.withhold) break;
+        for (int n = 0; ok; ++n) {
+            const Piece* pp = piece(n);
+            if (!pp) break;
+            const Piece pc = *pp;
+            if (pc.b == a.withhold) break;
+            const int32_t* table = a.block_table + static_cast<long long>(pc.b) * a.max_blocks;
             // lane k < nb: box k of a block; its block id is fetched a block ahead
             auto want = [&](int j, int& off) {
-                const int t = pc.cell.block(j) * kPreBlock + lane * a.box_tok;
-                if (lane >= nb || t >= pc.cell.hi || !(t + a.box_tok > pc.cell.lo || t < pc.cell.s_end)) return -1;
+                const int t = pc.block(j) * kPreBlock + lane * a.box_tok;
+                if (lane >= nb || t >= pc.hi || !(t + a.box_tok > pc.lo || t < pc.s_end)) return -1;
                 const int page = a.page_div(t);
                 off = t - page * a.page;
-                const int id = __ldg(a.block_table + static_cast<long long>(b) * a.max_blocks + page);
+                const int id = __ldg(table + page);
                 return id < 0 || id >= a.num_blocks ? -2 : id;
             };
             int off = 0, off_next = 0, id_next = pc.j0 < pc.j1 ? want(pc.j0, off_next) : -1;
@@ -460,12 +494,17 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 if (j + 1 < pc.j1) id_next = want(j + 1, off_next);
                 if (id == -2) report(a.status, MQA_ERR_DEVICE_CHECK);
                 const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-                const int per = a.box_tok / 16;
-                uint32_t groups = 0;
-                for (int k = 0; k < nb; ++k)
-                    if ((have >> k) & 1u) groups |= ((1u << per) - 1u) << (k * per);
-                const int g_id = __shfl_sync(0xffffffffu, id, lane / per);
-                const int g_off = __shfl_sync(0xffffffffu, off, lane / per) + lane % per * 16;
+                uint32_t groups = 0xffu;
+                if (have != (1u << nb) - 1u) {
+                    groups = 0;
+                    for (int k = 0; k < nb; ++k)
+                        if ((have >> k) & 1u) groups |= ((1u << per) - 1u) << (k * per);
+                }
+                int g_id = 0, g_off = 0;
+                if (scaled) {
+                    g_id = __shfl_sync(0xffffffffu, id, lane / per);
+                    g_off = __shfl_sync(0xffffffffu, off, lane / per) + lane % per * 16;
+                }
                 const int slot = (kvc >> 1) % C::kInfo;
                 for (int plane = 0; plane < 2; ++plane, ++kvc) {
                     const int st = kvc % kCopyStages;
@@ -502,49 +541,75 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) piece_done(n);
         }
         if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
         // no copy may be in flight at the end
         for (int q = max(kvc - kCopyStages, 0); q < kvc; ++q)
             if (!mbar_wait(&s.kv_full[q % kCopyStages], q / kCopyStages & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
     } else if (warp == 10) {
-        // ------------------------------------------------ copies of queries
+        // ------------------------------------------------ pieces and queries
         set_regs_down<C::kRegsRest>();
-        int n = 0;
-        while (ok && pc.next(a)) {
-            if (pc.j1 <= pc.j0) continue;
-            if (n > 0 && !mbar_wait(&s.q_free, (n - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) {
-                const int tiles = pc.cell.cnt > a.tile_tok ? 2 : 1;
+        if (lane == 0) {
+            Pieces pw;
+            pw.init(a, s);
+            int n = 0, queries = 0, head = 3, begun = 0, row0 = 0, cnt = 0, h = 0;
+            for (bool more = true; more && ok; ++n) {
+                more = pw.next(a);
+                if (n >= kPieces && !mbar_wait(&s.piece_free[n % kPieces], (n / kPieces & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                Piece& pc = s.piece[n % kPieces];
+                const PreCell& c = pw.cell;
+                pc = {c.row0, c.cnt, c.p0, c.pre, c.hi, c.lo, c.s_end, c.ns, c.w0, c.nt, pw.j0, pw.j1, pw.b < a.batch ? pw.b : pw.eb, pw.h, more, 0};
+                mbar_arrive(&s.piece_full[n % kPieces]);
+                if (!more) break;
+                if (n == 0) head = pw.j0 == 0 ? 0 : pw.j1 < c.nt ? 2 : 1;
+                begun = pw.j0 == 0 && pw.j1 < c.nt;
+                row0 = c.row0;
+                cnt = c.cnt;
+                h = pw.h;
+                if (pw.j1 <= pw.j0) continue;
+                if (queries > 0 && !mbar_wait(&s.q_free, (queries - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const int tiles = cnt > a.tile_tok ? 2 : 1;
                 mbar_arrive_expect_tx(&s.q_full, tiles * a.tile_rows * D * 2);
                 for (int i = 0; i < tiles; ++i)
                     for (int p = 0; p < C::kPanels; ++p)
-                        tma_load(q_s + i * C::kTile + p * C::kPanel, &a.q_map, p * 64, pc.h * a.grp,
-                                 pc.cell.row0 + i * a.tile_tok, &s.q_full);
+                        tma_load(q_s + i * C::kTile + p * C::kPanel, &a.q_map, p * 64, h * a.grp, row0 + i * a.tile_tok, &s.q_full);
+                ++queries;
             }
-            ++n;
+            if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+            if (queries > 0 && !mbar_wait(&s.q_full, (queries - 1) & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+            if (a.cut) {
+                a.ws_meta[2 * blockIdx.x] = make_int4(begun, head, row0, cnt);
+                a.ws_meta[2 * blockIdx.x + 1] = make_int4(h, 0, 0, 0);
+            }
         }
-        if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-        if (n > 0 && !mbar_wait(&s.q_full, (n - 1) & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
     } else if (warp == 9) {
         // ------------------------------------------------ tensor-core products
         set_regs_down<C::kRegsRest>();
         if (lane == 0) {
             constexpr uint32_t kIdQK = umma_idesc_bf16(128, kPreBlock, 0), kIdPV = umma_idesc_bf16(128, D, 1);
             const uint64_t qd = umma_desc(q_s, 16, 1024), kd = umma_desc(kv_s, 16, 1024), vd = umma_desc(kv_s, C::kPanel, 1024);
-            int kvc = 0, n = 0;                      // K or V blocks, pieces with blocks
+            int kvc = 0, qn = 0;                     // K or V blocks, pieces with blocks
             int pn[2] = {0, 0}, on[2] = {0, 0};      // P blocks, pieces with a product, of each tile
-            while (ok && pc.next(a)) {
+            for (int n = 0; ok; ++n) {
+                const Piece* pp = piece(n);
+                if (!pp) break;
+                const Piece pc = *pp;
+                piece_done(n);
                 if (pc.j1 <= pc.j0) continue;
-                const TileView v0(a, pc.cell, 0), v1(a, pc.cell, 1);
-                if (!mbar_wait(&s.q_full, n & 1)) {
+                const TileView v0(a, pc, 0), v1(a, pc, 1);
+                if (!mbar_wait(&s.q_full, qn & 1)) {
                     ok = false;
                     break;
                 }
-                ++n;
+                ++qn;
                 int st = 0;
                 auto wait_block = [&](int q) {  // K or V block number q
                     st = q % C::kStages;
@@ -568,16 +633,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     break;
                 }
                 {
-                    const int t = pc.cell.block(pc.j0) * kPreBlock;
+                    const int t = pc.block(pc.j0) * kPreBlock;
                     if (v0.active(a, t)) qk(0);
                     if (v1.active(a, t)) qk(1);
                 }
                 umma_commit(&s.used[st]);
                 if (jn == 1) umma_commit(&s.q_free);
                 for (int jj = 0; jj < jn && ok; ++jj) {
-                    const int t = pc.cell.block(pc.j0 + jj) * kPreBlock;
+                    const int t = pc.block(pc.j0 + jj) * kPreBlock;
                     const bool more = jj + 1 < jn;
-                    const int tn = more ? pc.cell.block(pc.j0 + jj + 1) * kPreBlock : 0;
+                    const int tn = more ? pc.block(pc.j0 + jj + 1) * kPreBlock : 0;
                     const int qv = kvc + 2 * jj + 1, qk_next = qv + 1;
                     bool have_v = false, have_k = false;
                     int vst = 0, kst = 0;
@@ -641,9 +706,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         set_regs_down<C::kRegsRest>();
         const int w = warp - 11;
         int kvc = 0;
-        while (ok && pc.next(a)) {
+        for (int n = 0; ok; ++n) {
+            const Piece* pp = piece(n);
+            if (!pp) break;
+            const Piece pc = *pp;
+            __syncwarp();
+            if (lane == 0) piece_done(n);
             for (int j = pc.j0; j < pc.j1 && ok; ++j) {
-                const int t0 = pc.cell.block(j) * kPreBlock, hi = pc.cell.hi, lo = pc.cell.lo, se = pc.cell.s_end;
+                const int t0 = pc.block(j) * kPreBlock, hi = pc.hi, lo = pc.lo, se = pc.s_end;
                 for (int plane = 0; plane < 2; ++plane, ++kvc) {
                     const int st = kvc % C::kStages, rst = kvc % kCopyStages, slot = (kvc >> 1) % C::kInfo;
                     if (!mbar_wait(&s.kv_full[rst], kvc / kCopyStages & 1) ||
@@ -714,21 +784,22 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t my_s = t_s + i * 128 + lanes, my_o = t_o + i * D + lanes;
         const int tk = a.grp_div(r), g = r - tk * a.grp;  // token of the tile, head of the group
-        int sn = 0, pieces = 0, kvb = 0;  // blocks of this tile; pieces; blocks of the thread block
-        int head = 0, begun = 0, m_row0 = 0, m_cnt = 0, m_h = 0;
-        while (ok && pc.next(a)) {
-            const PreCell& cell = pc.cell;
-            const TileView view(a, cell, i);
-            const int p = cell.p0 + i * a.tile_tok + tk;
+        int sn = 0, kvb = 0;  // blocks of this tile, of the thread block
+        for (int n = 0; ok; ++n) {
+            const Piece* pc = piece(n);
+            if (!pc) break;
+            const TileView view(a, *pc, i);
+            const int p = pc->p0 + i * a.tile_tok + tk;
             const bool row = tk < view.cnt && r < a.tile_rows;
-            const int lim = row && p >= 0 ? max(p + 1, cell.pre) : 0, lo = p - a.window + 1;
+            const int lim = row && p >= 0 ? max(p + 1, pc->pre) : 0, lo = p - a.window + 1;
             float slope2 = 0.f;
-            if (SHAPED && a.slopes && row) slope2 = __ldg(a.slopes + pc.h * a.grp + g) * kLog2e;
+            if (SHAPED && a.slopes && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
             float m = kNone;
             float2 l[2] = {both(0.f), both(0.f)};
             int nact = 0;
-            for (int j = pc.j0; j < pc.j1; ++j, ++kvb) {
-                const int t0 = cell.block(j) * kPreBlock;
+            const int j1 = pc->j1;
+            for (int j = pc->j0; j < j1; ++j, ++kvb) {
+                const int t0 = pc->block(j) * kPreBlock;
                 if (!view.active(a, t0)) continue;
                 if (!mbar_wait(&s.s_full[i], sn & 1)) {
                     ok = false;
@@ -739,39 +810,61 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 const uint32_t groups = s.valid[kvb % C::kInfo];
+                const bool edge = groups != 0xffu || !view.whole(a, t0);
                 tmem_wait_ld();
-                if (SHAPED) {
+                auto pair = [&](int k, int e) { return make_float2(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])); };
+                auto put = [&](int k, int e, float2 z) {
+                    x[k][e] = __float_as_uint(z.x);
+                    x[k][e + 1] = __float_as_uint(z.y);
+                };
+                // key t0 + e counts iff e < lim - t0 and (e >= lo - t0 or e < sinks - t0), its group was copied; else it becomes v
+                auto clear = [&](uint32_t v) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float f = scaled ? a.sl2 * s.scale[kvb % C::kInfo][0][k] : a.sl2;
+                    for (int k = 0; k < 4; ++k) {
+                        auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
+                        const int t = t0 + 32 * k;
+                        uint32_t bits = below(lim - t) & (~below(lo - t) | below(a.sinks - t));
+                        bits &= ((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            uint32_t* y = &x[k >> 1][(k & 1) * 16 + e];
-                            const float2 z = mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), both(f));
-                            y[0] = __float_as_uint(z.x);
-                            y[1] = __float_as_uint(z.y);
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) x[k][e] = v;
                     }
-                    if (a.cap2 > 0.f) {
+                };
+                // Where every key is seen and only a cap shapes the logits, it is
+                // monotone: the maximum is the largest product's, and the polynomial's
+                // last step subtracts the reference as well.
+                bool late = false;
+                if (SHAPED) {
+                    const bool cap = a.cap2 > 0.f;
+                    const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
+                    float top = 0.f;
+                    if (edge && cap) clear(0u);  // (what lies there must not choose the formula)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float top = 0.f;
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(x[k][e])));
-                            // (a NaN passes the comparison of the others and stays one)
-                            if (top <= a.cap2) {
+                        for (int e = 0; e < 32; e += 2) {
+                            const float f = scaled ? unit * s.scale[kvb % C::kInfo][0][2 * k + e / 16] : unit;
+                            const float2 y = mul2(pair(k, e), both(f));
+                            put(k, e, y);
+                            if (cap) top = max3_abs(top, y.x, y.y);
+                        }
+                    if (cap) {
+                        late = !edge && !a.slopes && __all_sync(0xffffffffu, top <= 1.f || !row);
+                        if (!late) {
+                            if (top <= 1.f) {  // (a NaN passes the comparison of the others and stays one)
 #pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    const float2 z = cap_near(make_float2(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])), a.cap2, a.inv_cap2);
-                                    x[k][e] = __float_as_uint(z.x);
-                                    x[k][e + 1] = __float_as_uint(z.y);
-                                }
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) put(k, e, mul2(pair(k, e), tanh_over(a.tanh_c, pair(k, e))));
                             } else {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float y = __uint_as_float(x[k][e]) * a.inv_cap2;
-                                    x[k][e] = __float_as_uint(a.cap2 - __fdividef(2.f * a.cap2, 1.f + ex2(2.f * kLog2e * y)));
-                                }
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) {
+                                        const float2 y = pair(k, e), near = mul2(y, tanh_over(a.tanh_c, y));
+                                        put(k, e, make_float2(fabsf(y.x) <= 1.f ? near.x : tanh_far(a.cap2, y.x),
+                                                              fabsf(y.y) <= 1.f ? near.y : tanh_far(a.cap2, y.y)));
+                                    }
                             }
                         }
                     }
@@ -784,27 +877,15 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         }
                     }
                 }
-                if (groups != 0xffu || !view.whole(a, t0)) {
-                    // key t0 + e counts iff e < lim - t0 and (e >= lo - t0 or e < sinks - t0), its group was copied
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
-                        const int t = t0 + 32 * k;
-                        uint32_t bits = below(lim - t) & (~below(lo - t) | below(a.sinks - t));
-                        bits &= ((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) x[k][e] = 0xff800000u;
-                    }
-                }
+                if (edge) clear(0xff800000u);
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])));
-                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    for (int e = 0; e < 32; e += 2) top[k] = max3(top[k], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+                float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                 if (!SHAPED) mx *= a.sl2;
+                if (late) mx *= tanh_over(a.tanh_c, both(mx)).x;
                 const bool move = mx > m + 8.f;
                 if (nact == 0) {
                     if (move) m = mx;
@@ -832,11 +913,22 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         tmem_st16(my_o + k, o);
                     }
                 }
+                if (late) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t o[16];
-                    numerators<SHAPED>(x[k], a.sl2, m, l, o);
-                    tmem_st16(my_s + 16 * k, o);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) put(k, e, fma2(pair(k, e), tanh_over(a.tanh_c, pair(k, e)), both(-m)));
+                        numerators<2>(x[k], a.sl2, m, l, o);
+                        tmem_st16(my_s + 16 * k, o);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[16];
+                        numerators<SHAPED ? 1 : 0>(x[k], a.sl2, m, l, o);
+                        tmem_st16(my_s + 16 * k, o);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -854,17 +946,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             }
             // ---- the piece's result
             const float sum = l[0].x + l[0].y + l[1].x + l[1].y;
-            const bool part = pc.j0 > 0 || pc.j1 < cell.nt;
-            if (pieces == 0 && pc.j0 > 0) head = pc.j1 < cell.nt ? 2 : 1;
-            begun = pc.j0 == 0 && pc.j1 < cell.nt;
-            if (begun) {
-                m_row0 = cell.row0;
-                m_cnt = cell.cnt;
-                m_h = pc.h;
-            }
-            const int token = cell.row0 + i * a.tile_tok + tk;
-            const long long orow = static_cast<long long>(token) * a.Hq + pc.h * a.grp + g;
-            const long long prow = (2LL * blockIdx.x + (pc.j0 > 0 ? 0 : 1)) * kPreSlotRows + i * kPreTile + r;
+            const int j0 = pc->j0;
+            const bool part = j0 > 0 || j1 < pc->nt;
+            const int token = pc->row0 + i * a.tile_tok + tk;
+            const long long orow = static_cast<long long>(token) * a.Hq + pc->h * a.grp + g;
+            const long long prow = (2LL * blockIdx.x + (j0 > 0 ? 0 : 1)) * kPreSlotRows + i * kPreTile + r;
+            __syncwarp();
+            if (lane == 0) piece_done(n);
             // sum == 0: no visible key (a NaN goes through to the output)
             const float f = part ? a.out_scale : sum == 0.f ? 0.f : a.out_scale / sum;
             if (row) {
@@ -911,13 +999,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 tc_fence_before();
                 mbar_arrive(&s.o_free[i]);
             }
-            ++pieces;
         }
         if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-        if (threadIdx.x == 0 && a.cut) {
-            a.ws_meta[2 * blockIdx.x] = make_int4(ok ? begun : 0, pieces == 0 ? 3 : head, m_row0, m_cnt);
-            a.ws_meta[2 * blockIdx.x + 1] = make_int4(m_h, 0, 0, 0);
-        }
     }
     tc_fence_before();
     __syncthreads();

@@ -42,6 +42,12 @@ struct FastDiv {
     }
 };
 
+// Caps of logits, in base 2: cap2 tanh(x / cap2).
+// tanh(y) / y for |y| <= 1: c0 + c1 y^2 + .. + c5 y^10, coefficients of least
+// squares towards the smallest absolute error of tanh, 2.4e-7 (of logits capped at
+// 50: 1.7e-5 in base 2, far below the 2^-9 of P's rounding).
+constexpr float kTanh[6] = {0.9999968409f, -0.3332400322f, 0.1325352489f, -0.05097286030f, 0.01611417904f, -0.002839464694f};
+
 struct WinArgs {
     CUtensorMap tmap;  // {line, rows (block, plane, token), panels, heads}
     const __nv_bfloat16* q;   // [batch, q_len, Hq, D]
@@ -57,6 +63,7 @@ struct WinArgs {
     float sl2;        // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
     float out_scale;  // v_scale of a per-tensor e4m3 cache, else 1
     float cap2, inv_cap2;  // softcap * log2(e) and its reciprocal, or 0 (shaped logits only, like the next)
+    float tanh_c[6];       // cap2 times kTanh
     const float* slopes;   // [Hq], or null
     int batch, q_len, Hq, Hkv, grp, rows;  // rows = q_len * grp: query rows of a KV head
     int num_blocks, page, max_blocks;
@@ -71,6 +78,13 @@ struct WinArgs {
     bool alone;                     // no more blocks than multiprocessors: each may take one's shared memory
     int withhold;  // test hook of the bounded waits: this unit copies nothing (-1 in every product call)
 };
+
+// cap2 tanh(y) for |y| > 1: 1 - 2 / (1 + e^{2y}) (infinities become +-cap2, a NaN
+// stays one).  Its error is absolute, 2^-23 of the cap: near 0 the polynomial's is
+// relative, 2^-18 of the logit, which is what a cap far above the logits needs.
+__device__ __forceinline__ float tanh_far(float cap2, float y) {
+    return cap2 - __fdividef(2.f * cap2, 1.f + ex2(2.f * kLog2e * y));
+}
 
 // The tiles of one virtual request.
 struct WinVis {

@@ -280,10 +280,13 @@ constexpr int kFirst = 1 << 11, kLast = 1 << 12, kWhole = 1 << 13;  // of the ti
 constexpr int kAct = 1 << 14, kEdge = 1 << 18, kBlocks = 15;
 constexpr int kSteps2 = 22;  // bits 22 + 2j: scales from the box's first to that of its 16 tokens number j + 1
 
-// A base-2 logit x capped: cap2 tanh(x / cap2), as 1 - 2 / (1 + e^{2y}) (within 2^-23 of the
-// cap; infinities become +-cap2, a NaN stays one).
-__device__ __forceinline__ float capped(float x, float cap2, float inv_cap2) {
-    return cap2 - __fdividef(2.f * cap2, 1.f + ex2(2.f * kLog2e * inv_cap2 * x));
+// A base-2 logit x capped.
+__device__ __forceinline__ float capped(const WinArgs& a, float x) {
+    const float y = x * a.inv_cap2, z = y * y;
+    float w = a.tanh_c[5];
+#pragma unroll
+    for (int k = 4; k >= 0; --k) w = fmaf(w, z, a.tanh_c[k]);
+    return fabsf(y) <= 1.f ? y * w : tanh_far(a.cap2, y);
 }
 
 // MULTI: more than one query position per request.  SHAPED: logits capped by
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(c
 #pragma unroll
                         for (int hb = 0; hb < NHB; ++hb)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) x[m][hb][e] = capped(x[m][hb][e], a.cap2, a.inv_cap2);
+                            for (int e = 0; e < 4; ++e) x[m][hb][e] = capped(a, x[m][hb][e]);
                 if (a.slopes) {
                     const Rows rows = rows_of(d.z);
 #pragma unroll

@@ -96,11 +96,13 @@ def attention(q, K, V, first, scale, cap=0.0, slopes=None, window=NO_WINDOW, sin
     P = torch.where(some[..., None], torch.exp(x - lse[..., None]), 0.0).nan_to_num(0.0)
     out = torch.einsum("whgn,nhd->whgd", P, V)
     mass = torch.einsum("whgn,nhd->whgd", P, V.abs())
-    # Logits: D products summed in fp32 (D 2^-24 of their absolute sum), a cap within 2^-21 of it, a bias of two fp32
+    # Logits: D products summed in fp32 (D 2^-24 of their absolute sum), a cap within 2^-21 of it or 2^-18 of the
+    # logit, whichever is less (a polynomial's errors), a bias of two fp32
     # roundings, exp and log within 2^-21.  Numerators and, of scaled codes, values rounded to bf16 (2^-8 each of the
     # weighted absolute sum, which logits' errors change by as much again), the output to bf16 (2^-8).
-    dx = torch.where(seen[:, None, None], D * 2.0 ** -24 * size + bias.abs() * 2.0 ** -22, 0.0)
-    dx = (P * dx).sum(-1) * 4 + (dx.amax(-1) if n else 0.0) * 0.25 + abs(cap) * 2.0 ** -21 + 2.0 ** -20
+    capped = torch.minimum((x + bias).abs() * 2.0 ** -18, torch.tensor(abs(cap) * 2.0 ** -21, device=q.device))
+    dx = torch.where(seen[:, None, None], D * 2.0 ** -24 * size + bias.abs() * 2.0 ** -22 + capped, 0.0)
+    dx = (P * dx).sum(-1) * 4 + (dx.amax(-1) if n else 0.0) * 0.25 + 2.0 ** -20
     out_tol = out.abs() * 2.0 ** -8 + mass * (2 * 2.0 ** -8 + 2 * dx[..., None]) + 1e-30
     if half_codes is not None:
         # f16 numerators P s_v are kept relative to one that is at most the largest, so those below 2^-14 of it are off

@@ -94,7 +94,7 @@ def test_prefixes(slopes, window):
     run([300, 40], [0, 100], prefix=[129, 110], Hq=4, Hkv=4, slopes=slopes, window=window, sinks=3, kv="int8_block")
 
 
-@pytest.mark.parametrize("cap", [5.0, 15.0, 50.0, 1e9])
+@pytest.mark.parametrize("cap", [5.0, 15.0, 50.0, 1e4, 1e9])
 @pytest.mark.parametrize("size", [0.5, 4.0, 40.0])
 def test_caps(cap, size):
     run([200, 1], [60, 300], cap=cap, size=size)

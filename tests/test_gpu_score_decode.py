@@ -49,10 +49,11 @@ def test_windows(window, sinks):
     run([1, 99, 100, 5000], window=window, sinks=sinks, cap=20.0, slopes=True, kv="fp8_e4m3_block", size=3.0)
 
 
+@pytest.mark.parametrize("cap", [1e-3, 50.0, 1e4, 1e9])
 @pytest.mark.parametrize("size", [0.1, 30.0, 300.0])
-def test_caps_over_the_range(size):
-    run([300, 70], cap=50.0, size=size)
-    run([300, 70], cap=50.0, size=size, kv="fp8_e4m3", L=4)
+def test_caps_over_the_range(size, cap):
+    run([300, 70], cap=cap, size=size)
+    run([300, 70], cap=cap, size=size, kv="fp8_e4m3", L=4)
 
 
 def test_without_shaping_it_is_the_windowed_call():
