@@ -7,7 +7,7 @@
 // of 128 rows.  Its keys are walked in blocks of 128 tokens (those of the sinks,
 // then the run from the first row's window to the last row's limit).  The
 // (cell, head) pairs are laid end to end, each with its number of blocks plus
-// kCellCost as weight, and cut into one equal share per thread block; what a
+// cell_cost as weight, and cut into one equal share per thread block; what a
 // thread block has of one (cell, head) is a piece.  Pieces that hold a whole
 // (cell, head) write its result, the others partials that a second kernel
 // merges.
@@ -23,7 +23,6 @@ constexpr int kPreBlock = 128;  // keys of a block
 constexpr int kPreTile = 128;   // query rows of a tile
 constexpr int kPreMaxBatch = 8192;
 constexpr int kPreNoWindow = 1 << 30;
-constexpr int kPreCellCost = 1;  // start and end of a (cell, head), in blocks
 
 struct PreArgs {
     CUtensorMap q_map;   // {D, Hq, num_tokens}, box {64, grp, tile_tok}
@@ -51,6 +50,7 @@ struct PreArgs {
     int scale_block, scale_groups;
     int box_tok;
     FastDiv page_div, scale_div, grp_div, cell_div;  // cell_div: by 2 * tile_tok
+    int cell_cost;  // start and end of a (cell, head), in blocks
     int grid;
     bool cut;  // whether (cell, head) pairs may be cut
     int withhold;  // test hook of the bounded waits: no key of this request is copied (-1 in every product call)
@@ -125,7 +125,7 @@ inline size_t pre_workspace_bytes(int grid, int D) {
            static_cast<size_t>(grid) * 2 * kPreSlotRows * (D + 2) * sizeof(float);
 }
 
-cudaError_t pre_stage1_bf16(const PreArgs& a, int D, bool shaped, cudaStream_t stream);
+cudaError_t pre_stage1_bf16(const PreArgs& a, int D, cudaStream_t stream);
 cudaError_t pre_stage1_e4m3(const PreArgs& a, int D, cudaStream_t stream);
 cudaError_t pre_stage1_int8(const PreArgs& a, int D, cudaStream_t stream);
 cudaError_t pre_merge(const PreArgs& a, int D, cudaStream_t stream);

@@ -3,8 +3,6 @@
 
 namespace mqa {
 
-cudaError_t pre_stage1_bf16(const PreArgs& a, int D, bool shaped, cudaStream_t stream) {
-    return shaped ? pre::dispatch<kWinBf16, true>(a, D, stream) : pre::dispatch<kWinBf16, false>(a, D, stream);
-}
+cudaError_t pre_stage1_bf16(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinBf16>(a, D, stream); }
 
 }  // namespace mqa

@@ -38,6 +38,8 @@
 namespace mqa {
 namespace pre {
 
+enum Mode { kPlain = 0, kScaled = 1, kBiased = 2 };
+
 constexpr float kNone = -3e38f;  // reference before the first logit
 
 template <int D, int KIND>
@@ -112,6 +114,38 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(v));
+    return v;
+}
+// Tensor-core products issued by the lane whose `on` is set.  The whole warp runs
+// the code around them, converged (its waits end in a vote), so that descriptors
+// stay in uniform registers: in a branch of one lane each product took 80 to 130
+// cycles to issue, and a prompt of 15999 tokens 2323 us instead of 1745.
+__device__ __forceinline__ void umma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void umma_done(uint32_t on, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
 }
 
 template <int N>
@@ -336,7 +370,7 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
     for (int i = tid; i < cells; i += nthr) {
         int b, u, nt;
         find(i, b, u, nt);
-        w += nt + kPreCellCost;
+        w += nt + a.cell_cost;
     }
     const long long total = block_sum(s, w) * a.Hkv;
     const long long share = total / a.grid;
@@ -347,7 +381,7 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
         const int i = i0 + tid;
         int b = 0, u = 0, nt = 0;
         if (i < cells) find(i, b, u, nt);
-        const int per = i < cells ? nt + kPreCellCost : 0;
+        const int per = i < cells ? nt + a.cell_cost : 0;
         long long all;
         const long long at = base + block_scan(s, static_cast<long long>(per) * a.Hkv, all);
         base += all;
@@ -356,7 +390,7 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
             int h = static_cast<int>((x[e] - at) / per);
             const int y = static_cast<int>(x[e] - at - static_cast<long long>(h) * per);
             // the nearest cut: a multiple of the grain, or an end
-            int j = max(0, y - kPreCellCost);
+            int j = max(0, y - a.cell_cost);
             if (grain >= nt)
                 j = 2 * y <= per ? 0 : nt;
             else
@@ -390,13 +424,13 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
     __syncthreads();
 }
 
-// P of 32 logits as bf16 pairs; their sum is added to l.  FORM 0: logits are sl2 s, 1: s, 2: s is less m already.
-template <int FORM>
+// P of 32 logits (sl2 s if PLAIN, else s) as bf16 pairs; their sum is added to l.
+template <bool PLAIN>
 __device__ __forceinline__ void numerators(const uint32_t (&s)[32], float sl2, float m, float2 (&l)[2], uint32_t (&p)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const float2 x = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-        const float2 y = FORM == 2 ? x : FORM == 1 ? add2(x, both(-m)) : fma2(x, both(sl2), both(-m));
+        const float2 y = PLAIN ? fma2(x, both(sl2), both(-m)) : add2(x, both(-m));
         const float2 e = make_float2(ex2(y.x), ex2(y.y));
         l[k & 1] = add2(l[k & 1], e);
         p[k] = pack_bf16x2(e.x, e.y);
@@ -409,7 +443,9 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
     reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
-template <int D, int KIND, bool SHAPED>
+// MODE: kPlain (scores times one positive scale), kScaled (scales of token
+// blocks, or a scale <= 0, and a cap if there is one), kBiased (and slopes).
+template <int D, int KIND, int MODE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
     using C = Cfg<D, KIND>;
     extern __shared__ uint8_t smem_raw[];
@@ -593,114 +629,102 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     } else if (warp == 9) {
         // ------------------------------------------------ tensor-core products
         set_regs_down<C::kRegsRest>();
-        if (lane == 0) {
-            constexpr uint32_t kIdQK = umma_idesc_bf16(128, kPreBlock, 0), kIdPV = umma_idesc_bf16(128, D, 1);
-            const uint64_t qd = umma_desc(q_s, 16, 1024), kd = umma_desc(kv_s, 16, 1024), vd = umma_desc(kv_s, C::kPanel, 1024);
-            int kvc = 0, qn = 0;                     // K or V blocks, pieces with blocks
-            int pn[2] = {0, 0}, on[2] = {0, 0};      // P blocks, pieces with a product, of each tile
-            for (int n = 0; ok; ++n) {
-                const Piece* pp = piece(n);
-                if (!pp) break;
-                const Piece pc = *pp;
-                piece_done(n);
-                if (pc.j1 <= pc.j0) continue;
-                const TileView v0(a, pc, 0), v1(a, pc, 1);
-                if (!mbar_wait(&s.q_full, qn & 1)) {
-                    ok = false;
-                    break;
-                }
-                ++qn;
-                int st = 0;
-                auto wait_block = [&](int q) {  // K or V block number q
-                    st = q % C::kStages;
-                    if (!mbar_wait(&s.ready[st], q / C::kStages & 1)) return false;
-                    tc_fence_after();
-                    return true;
-                };
-                auto qk = [&](int i) {
-                    const uint64_t aq = qd + static_cast<uint64_t>((i * C::kTile) >> 4), bk = kd + static_cast<uint64_t>((st * C::kTile) >> 4);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kPanel + (k & 3) * 32) >> 4);
-                        umma_bf16(t_s + i * 128, aq + o, bk + o, kIdQK, k > 0);
-                    }
-                    umma_commit(&s.s_full[i]);
-                };
-                bool begun[2] = {false, false};
-                const int jn = pc.j1 - pc.j0;
-                if (!wait_block(kvc)) {
-                    ok = false;
-                    break;
-                }
-                {
-                    const int t = pc.block(pc.j0) * kPreBlock;
-                    if (v0.active(a, t)) qk(0);
-                    if (v1.active(a, t)) qk(1);
-                }
-                umma_commit(&s.used[st]);
-                if (jn == 1) umma_commit(&s.q_free);
-                for (int jj = 0; jj < jn && ok; ++jj) {
-                    const int t = pc.block(pc.j0 + jj) * kPreBlock;
-                    const bool more = jj + 1 < jn;
-                    const int tn = more ? pc.block(pc.j0 + jj + 1) * kPreBlock : 0;
-                    const int qv = kvc + 2 * jj + 1, qk_next = qv + 1;
-                    bool have_v = false, have_k = false;
-                    int vst = 0, kst = 0;
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        const TileView& v = i == 0 ? v0 : v1;
-                        if (v.active(a, t)) {
-                            if (!have_v) {
-                                ok = wait_block(qv);
-                                vst = st;
-                                have_v = true;
-                            }
-                            if (ok) ok = mbar_wait(&s.p_full[i], pn[i] & 1);
-                            ++pn[i];
-                            if (ok && !begun[i] && on[i] > 0) ok = mbar_wait(&s.o_free[i], (on[i] - 1) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t bv = vd + static_cast<uint64_t>((vst * C::kTile) >> 4);
-#pragma unroll
-                            for (int k = 0; k < kPreBlock / 16; ++k)
-                                umma_bf16_ta(t_o + i * D, t_s + i * 128 + k * 8, bv + static_cast<uint64_t>((k * 16 * 128) >> 4),
-                                             kIdPV, begun[i] || k > 0);
-                            umma_commit(&s.o_done[i]);
-                            if (!begun[i]) ++on[i];
-                            begun[i] = true;
-                        }
-                        if (more && v.active(a, tn)) {
-                            if (!have_k) {
-                                ok = wait_block(qk_next);
-                                kst = st;
-                                have_k = true;
-                            }
-                            if (!ok) break;
-                            st = kst;
-                            qk(i);
-                        }
-                    }
-                    if (!ok) break;
-                    if (!have_v) {
-                        ok = wait_block(qv);
-                        vst = st;
-                    }
-                    if (ok) umma_commit(&s.used[vst]);
-                    if (more) {
-                        if (ok && !have_k) {
-                            ok = wait_block(qk_next);
-                            kst = st;
-                        }
-                        if (ok) umma_commit(&s.used[kst]);
-                        if (jj + 2 == jn) umma_commit(&s.q_free);
-                    }
-                }
-                kvc += 2 * jn;
+        constexpr uint32_t kIdQK = umma_idesc_bf16(128, kPreBlock, 0), kIdPV = umma_idesc_bf16(128, D, 1);
+        const uint64_t qd = umma_desc(q_s, 16, 1024), kd = umma_desc(kv_s, 16, 1024), vd = umma_desc(kv_s, C::kPanel, 1024);
+        const uint32_t on = elect_lane();
+        int st = 0, ph = 0;          // stage and phase of the next K or V block that is waited for
+        int qn = 0;                  // pieces with blocks
+        int pn0 = 0, pn1 = 0;        // P blocks of each tile
+        int on0 = 0, on1 = 0;        // pieces with a product of each tile
+        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+        auto wait_block = [&](int& at) {  // the next K or V block
+            at = st;
+            ok = wait(&s.ready[st], ph);
+            if (++st == C::kStages) {
+                st = 0;
+                ph ^= 1;
             }
-            if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-            // no product may be in flight at the end
-            umma_commit(&s.drain);
-            if (!mbar_wait(&s.drain, 0)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+            tc_fence_after();
+        };
+        auto qk = [&](int i, int at) {
+            const uint64_t aq = qd + static_cast<uint64_t>((i * C::kTile) >> 4), bk = kd + static_cast<uint64_t>((at * C::kTile) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kPanel + (k & 3) * 32) >> 4);
+                umma_ss(on, t_s + i * 128, aq + o, bk + o, kIdQK, k > 0);
+            }
+            umma_done(on, &s.s_full[i]);
+        };
+        auto pv = [&](int i, int at, bool begun) {
+            const uint64_t bv = vd + static_cast<uint64_t>((at * C::kTile) >> 4);
+#pragma unroll
+            for (int k = 0; k < kPreBlock / 16; ++k)
+                umma_ts(on, t_o + i * D, t_s + i * 128 + k * 8, bv + static_cast<uint64_t>((k * 16 * 128) >> 4), kIdPV, begun || k > 0);
+            umma_done(on, &s.o_done[i]);
+        };
+        for (int n = 0; ok; ++n) {
+            const Piece* pp = piece(n);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !pp) break;
+            const Piece pc = *pp;
+            __syncwarp();
+            if (lane == 0) piece_done(n);
+            __syncwarp();
+            if (pc.j1 <= pc.j0) continue;
+            const TileView v0(a, pc, 0), v1(a, pc, 1);
+            ok = wait(&s.q_full, qn++ & 1);
+            if (!ok) break;
+            int kst = 0, vst = 0;
+            wait_block(kst);
+            if (!ok) break;
+            int t = pc.block(pc.j0) * kPreBlock;
+            bool a0 = v0.active(a, t), a1 = v1.active(a, t);  // tiles that the block has to do with
+            bool begun0 = false, begun1 = false;
+            if (a0) qk(0, kst);
+            if (a1) qk(1, kst);
+            umma_done(on, &s.used[kst]);
+            if (pc.j1 - pc.j0 == 1) umma_done(on, &s.q_free);
+            for (int j = pc.j0; j < pc.j1; ++j) {
+                const bool more = j + 1 < pc.j1;
+                t = more ? pc.block(j + 1) * kPreBlock : 0;
+                const bool n0 = more && v0.active(a, t), n1 = more && v1.active(a, t);
+                wait_block(vst);  // V of this block
+                if (!ok) break;
+                if (a0) {
+                    ok = wait(&s.p_full[0], pn0++ & 1) && (begun0 || on0 == 0 || wait(&s.o_free[0], (on0 - 1) & 1));
+                    if (!ok) break;
+                    on0 += !begun0;
+                    tc_fence_after();
+                    pv(0, vst, begun0);
+                    begun0 = true;
+                }
+                if (more) {
+                    wait_block(kst);  // K of the next one
+                    if (!ok) break;
+                    if (n0) qk(0, kst);
+                }
+                if (a1) {
+                    ok = wait(&s.p_full[1], pn1++ & 1) && (begun1 || on1 == 0 || wait(&s.o_free[1], (on1 - 1) & 1));
+                    if (!ok) break;
+                    on1 += !begun1;
+                    tc_fence_after();
+                    pv(1, vst, begun1);
+                    begun1 = true;
+                }
+                umma_done(on, &s.used[vst]);
+                if (more) {
+                    if (n1) qk(1, kst);
+                    umma_done(on, &s.used[kst]);
+                    if (j + 2 == pc.j1) umma_done(on, &s.q_free);
+                }
+                a0 = n0;
+                a1 = n1;
+            }
         }
+        if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+        // no product may be in flight at the end
+        umma_done(on, &s.drain);
+        if (!mbar_wait(&s.drain, 0)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
     } else if (warp >= 11) {
         // ------------------------------------------------ making blocks ready
         set_regs_down<C::kRegsRest>();
@@ -793,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             const bool row = tk < view.cnt && r < a.tile_rows;
             const int lim = row && p >= 0 ? max(p + 1, pc->pre) : 0, lo = p - a.window + 1;
             float slope2 = 0.f;
-            if (SHAPED && a.slopes && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
+            if (MODE == kBiased && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
             float m = kNone;
             float2 l[2] = {both(0.f), both(0.f)};
             int nact = 0;
@@ -818,74 +842,70 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     x[k][e + 1] = __float_as_uint(z.y);
                 };
                 // key t0 + e counts iff e < lim - t0 and (e >= lo - t0 or e < sinks - t0), its group was copied; else it becomes v
-                auto clear = [&](uint32_t v) {
+                auto clear = [&](int k, uint32_t v) {
+                    auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
+                    const int t = t0 + 32 * k;
+                    uint32_t bits = below(lim - t) & (~below(lo - t) | below(a.sinks - t));
+                    bits &= ((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
-                        const int t = t0 + 32 * k;
-                        uint32_t bits = below(lim - t) & (~below(lo - t) | below(a.sinks - t));
-                        bits &= ((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) x[k][e] = v;
-                    }
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) x[k][e] = v;
                 };
-                // Where every key is seen and only a cap shapes the logits, it is
-                // monotone: the maximum is the largest product's, and the polynomial's
-                // last step subtracts the reference as well.
-                bool late = false;
-                if (SHAPED) {
-                    const bool cap = a.cap2 > 0.f;
-                    const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
-                    float top = 0.f;
-                    if (edge && cap) clear(0u);  // (what lies there must not choose the formula)
+                float top[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (MODE != kPlain) {
+                        const bool cap = a.cap2 > 0.f;
+                        const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
+                        float far = 0.f;  // the largest magnitude under the tanh
+                        if (edge && cap) clear(k, 0u);  // (what lies where no key is seen must not choose the formula)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float f = scaled ? unit * s.scale[kvb % C::kInfo][0][2 * k + e / 16] : unit;
+                            const float f = C::kCodes && scaled ? unit * s.scale[kvb % C::kInfo][0][2 * k + e / 16] : unit;
                             const float2 y = mul2(pair(k, e), both(f));
                             put(k, e, y);
-                            if (cap) top = max3_abs(top, y.x, y.y);
+                            far = max3_abs(far, y.x, y.y);
                         }
-                    if (cap) {
-                        late = !edge && !a.slopes && __all_sync(0xffffffffu, top <= 1.f || !row);
-                        if (!late) {
-                            if (top <= 1.f) {  // (a NaN passes the comparison of the others and stays one)
+                        if (cap) {
+                            if (far <= 1.f) {  // (a NaN passes the comparison of the others and stays one)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
+                                for (int e = 0; e < 32; e += 8) {  // four chains at a time
+                                    float2 z[4], w[4];
 #pragma unroll
-                                    for (int e = 0; e < 32; e += 2) put(k, e, mul2(pair(k, e), tanh_over(a.tanh_c, pair(k, e))));
+                                    for (int c = 0; c < 4; ++c) {
+                                        z[c] = mul2(pair(k, e + 2 * c), pair(k, e + 2 * c));
+                                        w[c] = fma2(z[c], both(a.tanh_c[5]), both(a.tanh_c[4]));
+                                    }
+#pragma unroll
+                                    for (int q = 3; q >= 0; --q)
+#pragma unroll
+                                        for (int c = 0; c < 4; ++c) w[c] = fma2(w[c], z[c], both(a.tanh_c[q]));
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) put(k, e + 2 * c, mul2(pair(k, e + 2 * c), w[c]));
+                                }
                             } else {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 2) {
-                                        const float2 y = pair(k, e), near = mul2(y, tanh_over(a.tanh_c, y));
-                                        put(k, e, make_float2(fabsf(y.x) <= 1.f ? near.x : tanh_far(a.cap2, y.x),
-                                                              fabsf(y.y) <= 1.f ? near.y : tanh_far(a.cap2, y.y)));
-                                    }
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 y = pair(k, e), near = mul2(y, tanh_over(a.tanh_c, y));
+                                    put(k, e, make_float2(fabsf(y.x) <= 1.f ? near.x : tanh_far(a.cap2, y.x),
+                                                          fabsf(y.y) <= 1.f ? near.y : tanh_far(a.cap2, y.y)));
+                                }
                             }
                         }
-                    }
-                    if (a.slopes) {
-                        const float far = static_cast<float>(p - t0);
+                        if constexpr (MODE == kBiased) {
+                            const float d = static_cast<float>(p - t0 - 32 * k);
 #pragma unroll
-                        for (int e = 0; e < 128; ++e) {
-                            uint32_t& y = x[e >> 5][e & 31];
-                            y = __float_as_uint(fmaf(-slope2, fabsf(far - static_cast<float>(e)), __uint_as_float(y)));
+                            for (int e = 0; e < 32; ++e)
+                                x[k][e] = __float_as_uint(fmaf(-slope2, fabsf(d - static_cast<float>(e)), __uint_as_float(x[k][e])));
                         }
                     }
-                }
-                if (edge) clear(0xff800000u);
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
+                    if (edge) clear(k, 0xff800000u);
+                    top[k] = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) top[k] = max3(top[k], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+                }
                 float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-                if (!SHAPED) mx *= a.sl2;
-                if (late) mx *= tanh_over(a.tanh_c, both(mx)).x;
+                if (MODE == kPlain) mx *= a.sl2;
                 const bool move = mx > m + 8.f;
                 if (nact == 0) {
                     if (move) m = mx;
@@ -913,22 +933,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         tmem_st16(my_o + k, o);
                     }
                 }
-                if (late) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) put(k, e, fma2(pair(k, e), tanh_over(a.tanh_c, pair(k, e)), both(-m)));
-                        numerators<2>(x[k], a.sl2, m, l, o);
-                        tmem_st16(my_s + 16 * k, o);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[16];
-                        numerators<SHAPED ? 1 : 0>(x[k], a.sl2, m, l, o);
-                        tmem_st16(my_s + 16 * k, o);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[16];
+                    numerators<MODE == kPlain>(x[k], a.sl2, m, l, o);
+                    tmem_st16(my_s + 16 * k, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1010,13 +1019,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     }
 }
 
-template <int D, int KIND, bool SHAPED>
+template <int D, int KIND, int MODE>
 cudaError_t launch(const PreArgs& a, cudaStream_t stream) {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[kDevices];
     constexpr int bytes = smem_bytes<D, KIND>();
     static_assert(bytes <= 227 * 1024, "shared memory");
-    auto kern = gqa_prefill_kernel<D, KIND, SHAPED>;
+    auto kern = gqa_prefill_kernel<D, KIND, MODE>;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const bool known = dev >= 0 && dev < kDevices;
@@ -1027,9 +1036,18 @@ cudaError_t launch(const PreArgs& a, cudaStream_t stream) {
     return launch_with_pdl(kern, dim3(a.grid), dim3(Cfg<D, KIND>::kThreads), bytes, stream, a);
 }
 
-template <int KIND, bool SHAPED>
+template <int KIND, int MODE>
+cudaError_t dispatch_size(const PreArgs& a, int D, cudaStream_t stream) {
+    return D == 128 ? launch<128, KIND, MODE>(a, stream) : launch<64, KIND, MODE>(a, stream);
+}
+
+template <int KIND>
 cudaError_t dispatch(const PreArgs& a, int D, cudaStream_t stream) {
-    return D == 128 ? launch<128, KIND, SHAPED>(a, stream) : launch<64, KIND, SHAPED>(a, stream);
+    if (a.slopes) return dispatch_size<KIND, kBiased>(a, D, stream);
+    // (the plain kernel takes the maximum before it scales)
+    if constexpr (KIND != kWinInt8)
+        if (a.cap2 == 0.f && !a.kv_scales && a.sl2 > 0.f) return dispatch_size<KIND, kPlain>(a, D, stream);
+    return dispatch_size<KIND, kScaled>(a, D, stream);
 }
 
 }  // namespace pre
