@@ -38,7 +38,7 @@
 namespace mqa {
 namespace pre {
 
-enum Mode { kPlain = 0, kScaled = 1, kBiased = 2 };
+enum Mode { kPlain, kScaled, kShaped };
 
 constexpr float kNone = -3e38f;  // reference before the first logit
 
@@ -155,6 +155,11 @@ __device__ __forceinline__ void set_regs_up() {
 template <int N>
 __device__ __forceinline__ void set_regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A wait of the whole warp, which is converged after it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
 // ---- pairs of fp32 values, one instruction for both
@@ -424,13 +429,92 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
     __syncthreads();
 }
 
-// P of 32 logits (sl2 s if PLAIN, else s) as bf16 pairs; their sum is added to l.
-template <bool PLAIN>
-__device__ __forceinline__ void numerators(const uint32_t (&s)[32], float sl2, float m, float2 (&l)[2], uint32_t (&p)[16]) {
+__device__ __forceinline__ float2 get2(const uint32_t (&x)[32], int e) {
+    return make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+}
+__device__ __forceinline__ void put2(uint32_t (&x)[32], int e, float2 v) {
+    x[e] = __float_as_uint(v.x);
+    x[e + 1] = __float_as_uint(v.y);
+}
+// Values whose bit is not set become v.
+__device__ __forceinline__ void keep(uint32_t (&x)[32], uint32_t bits, float v) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!((bits >> e) & 1u)) x[e] = __float_as_uint(v);
+}
+__device__ __forceinline__ float chunk_max(const uint32_t (&x)[32]) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) top[e / 2 & 1] = max3(top[e / 2 & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    return fmaxf(top[0], top[1]);
+}
+
+// Logits (base 2) of 32 keys from their products: times sl2 and the scales f of
+// the two groups of 16, capped, less slope2 |d - e| (both_ways: some keys may lie
+// behind the query), masked by `bits` at the edges.
+__device__ __forceinline__ void shape_chunk(const PreArgs& a, uint32_t (&x)[32], float2 f, bool edge, uint32_t bits, bool bias,
+                                            float slope2, int d, bool both_ways) {
+    const bool cap = a.cap2 > 0.f;
+    const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
+    if (edge && cap) keep(x, bits, 0.f);  // (what lies where no key is seen must not choose the formula)
+    float far = 0.f;                      // the largest magnitude under the tanh
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 y = mul2(get2(x, e), both(unit * (e < 16 ? f.x : f.y)));
+        put2(x, e, y);
+        far = max3_abs(far, y.x, y.y);
+    }
+    if (cap) {
+        if (far <= 1.f) {  // (a NaN passes the comparison of the others and stays one)
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {  // eight chains at a time
+                float2 z[8], w[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    z[c] = mul2(get2(x, e + 2 * c), get2(x, e + 2 * c));
+                    w[c] = fma2(z[c], both(a.tanh_c[5]), both(a.tanh_c[4]));
+                }
+#pragma unroll
+                for (int q = 3; q >= 0; --q)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) w[c] = fma2(w[c], z[c], both(a.tanh_c[q]));
+#pragma unroll
+                for (int c = 0; c < 8; ++c) put2(x, e + 2 * c, mul2(get2(x, e + 2 * c), w[c]));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float2 y = get2(x, e), near = mul2(y, tanh_over(a.tanh_c, y));
+                put2(x, e, make_float2(fabsf(y.x) <= 1.f ? near.x : tanh_far(a.cap2, y.x),
+                                       fabsf(y.y) <= 1.f ? near.y : tanh_far(a.cap2, y.y)));
+            }
+        }
+    }
+    if (bias) {
+        // Every key that is seen lies at or before the query but for a prefix: slope2
+        // e - slope2 d then (a row sees its own key at distance 0, beside which the
+        // rounding of a far key's bias is nothing).
+        if (!both_ways) {
+            const float base = -slope2 * static_cast<float>(d);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+                put2(x, e, fma2(make_float2(static_cast<float>(e), static_cast<float>(e + 1)), both(slope2), add2(get2(x, e), both(base))));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                x[e] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(d) - static_cast<float>(e)), __uint_as_float(x[e])));
+        }
+    }
+    if (edge) keep(x, bits, -INFINITY);
+}
+
+// P of 32 keys as bf16 pairs from logits x (times f, a scale for each 16 of them,
+// if MULTIPLY); their sum is added to l.
+template <bool MULTIPLY>
+__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float m, float2 (&l)[2], uint32_t (&p)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        const float2 x = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-        const float2 y = PLAIN ? fma2(x, both(sl2), both(-m)) : add2(x, both(-m));
+        const float2 y = MULTIPLY ? fma2(get2(x, 2 * k), both(k < 8 ? f.x : f.y), both(-m)) : add2(get2(x, 2 * k), both(-m));
         const float2 e = make_float2(ex2(y.x), ex2(y.y));
         l[k & 1] = add2(l[k & 1], e);
         p[k] = pack_bf16x2(e.x, e.y);
@@ -443,8 +527,11 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
     reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
-// MODE: kPlain (scores times one positive scale), kScaled (scales of token
-// blocks, or a scale <= 0, and a cap if there is one), kBiased (and slopes).
+// MODE: kPlain (one positive scale), kScaled (non-negative scales of token blocks),
+// kShaped (a cap, slopes, any scale).  The first two keep a row's 128 products in
+// registers and fold the scale into the exponent; with the shaping's temporaries
+// they would spill and its code, four times over, leave the instruction cache (a
+// capped prompt of 15999 tokens: 3160 us), so kShaped goes through TMEM in chunks.
 template <int D, int KIND, int MODE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
     using C = Cfg<D, KIND>;
@@ -636,10 +723,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         int qn = 0;                  // pieces with blocks
         int pn0 = 0, pn1 = 0;        // P blocks of each tile
         int on0 = 0, on1 = 0;        // pieces with a product of each tile
-        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
         auto wait_block = [&](int& at) {  // the next K or V block
             at = st;
-            ok = wait(&s.ready[st], ph);
+            ok = warp_wait(&s.ready[st], ph);
             if (++st == C::kStages) {
                 st = 0;
                 ph ^= 1;
@@ -672,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             __syncwarp();
             if (pc.j1 <= pc.j0) continue;
             const TileView v0(a, pc, 0), v1(a, pc, 1);
-            ok = wait(&s.q_full, qn++ & 1);
+            ok = warp_wait(&s.q_full, qn++ & 1);
             if (!ok) break;
             int kst = 0, vst = 0;
             wait_block(kst);
@@ -691,7 +777,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 wait_block(vst);  // V of this block
                 if (!ok) break;
                 if (a0) {
-                    ok = wait(&s.p_full[0], pn0++ & 1) && (begun0 || on0 == 0 || wait(&s.o_free[0], (on0 - 1) & 1));
+                    ok = warp_wait(&s.p_full[0], pn0++ & 1) && (begun0 || on0 == 0 || warp_wait(&s.o_free[0], (on0 - 1) & 1));
                     if (!ok) break;
                     on0 += !begun0;
                     tc_fence_after();
@@ -704,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     if (n0) qk(0, kst);
                 }
                 if (a1) {
-                    ok = wait(&s.p_full[1], pn1++ & 1) && (begun1 || on1 == 0 || wait(&s.o_free[1], (on1 - 1) & 1));
+                    ok = warp_wait(&s.p_full[1], pn1++ & 1) && (begun1 || on1 == 0 || warp_wait(&s.o_free[1], (on1 - 1) & 1));
                     if (!ok) break;
                     on1 += !begun1;
                     tc_fence_after();
@@ -817,7 +903,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             const bool row = tk < view.cnt && r < a.tile_rows;
             const int lim = row && p >= 0 ? max(p + 1, pc->pre) : 0, lo = p - a.window + 1;
             float slope2 = 0.f;
-            if (MODE == kBiased && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
+            if (MODE == kShaped && a.slopes && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
             float m = kNone;
             float2 l[2] = {both(0.f), both(0.f)};
             int nact = 0;
@@ -825,87 +911,68 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             for (int j = pc->j0; j < j1; ++j, ++kvb) {
                 const int t0 = pc->block(j) * kPreBlock;
                 if (!view.active(a, t0)) continue;
-                if (!mbar_wait(&s.s_full[i], sn & 1)) {
+                if (!warp_wait(&s.s_full[i], sn & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t x[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 const uint32_t groups = s.valid[kvb % C::kInfo];
                 const bool edge = groups != 0xffu || !view.whole(a, t0);
-                tmem_wait_ld();
-                auto pair = [&](int k, int e) { return make_float2(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])); };
-                auto put = [&](int k, int e, float2 z) {
-                    x[k][e] = __float_as_uint(z.x);
-                    x[k][e + 1] = __float_as_uint(z.y);
-                };
-                // key t0 + e counts iff e < lim - t0 and (e >= lo - t0 or e < sinks - t0), its group was copied; else it becomes v
-                auto clear = [&](int k, uint32_t v) {
+                // of keys t0 + 32 k + e, e < 32: bit e set where it counts, t < lim and (t >= lo or t < sinks), its group copied
+                auto seen = [&](int k) {
                     auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
                     const int t = t0 + 32 * k;
-                    uint32_t bits = below(lim - t) & (~below(lo - t) | below(a.sinks - t));
-                    bits &= ((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) x[k][e] = v;
+                    return below(lim - t) & (~below(lo - t) | below(a.sinks - t)) &
+                           (((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u));
                 };
-                float top[4];
+                uint32_t x[MODE == kShaped ? 1 : 4][32];
+                float mx = -INFINITY;
+                if constexpr (MODE == kShaped) {
+                    // in chunks of 32 keys, through TMEM: the logits take S's place
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        tmem_ld32(my_s + 32 * k, x[0]);
+                        tmem_wait_ld();
+                        const float2 f = scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1])
+                                                : both(1.f);
+                        shape_chunk(a, x[0], f, edge, edge ? seen(k) : 0u, a.slopes != nullptr, slope2, p - t0 - 32 * k, pc->pre > 0);
+                        mx = fmaxf(mx, chunk_max(x[0]));
+                        tmem_st32(my_s + 32 * k, x[0]);
+                    }
+                    tmem_wait_st();
+                } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (MODE != kPlain) {
-                        const bool cap = a.cap2 > 0.f;
-                        const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
-                        float far = 0.f;  // the largest magnitude under the tanh
-                        if (edge && cap) clear(k, 0u);  // (what lies where no key is seen must not choose the formula)
+                    for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
+                    tmem_wait_ld();
+                    if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float f = C::kCodes && scaled ? unit * s.scale[kvb % C::kInfo][0][2 * k + e / 16] : unit;
-                            const float2 y = mul2(pair(k, e), both(f));
-                            put(k, e, y);
-                            far = max3_abs(far, y.x, y.y);
-                        }
-                        if (cap) {
-                            if (far <= 1.f) {  // (a NaN passes the comparison of the others and stays one)
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (MODE == kScaled) {
 #pragma unroll
-                                for (int e = 0; e < 32; e += 8) {  // four chains at a time
-                                    float2 z[4], w[4];
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c) {
-                                        z[c] = mul2(pair(k, e + 2 * c), pair(k, e + 2 * c));
-                                        w[c] = fma2(z[c], both(a.tanh_c[5]), both(a.tanh_c[4]));
-                                    }
-#pragma unroll
-                                    for (int q = 3; q >= 0; --q)
-#pragma unroll
-                                        for (int c = 0; c < 4; ++c) w[c] = fma2(w[c], z[c], both(a.tanh_c[q]));
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c) put(k, e + 2 * c, mul2(pair(k, e + 2 * c), w[c]));
-                                }
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    const float2 y = pair(k, e), near = mul2(y, tanh_over(a.tanh_c, y));
-                                    put(k, e, make_float2(fabsf(y.x) <= 1.f ? near.x : tanh_far(a.cap2, y.x),
-                                                          fabsf(y.y) <= 1.f ? near.y : tanh_far(a.cap2, y.y)));
-                                }
+                                for (int e = 0; e < 32; e += 2)
+                                    put2(x[k], e, mul2(get2(x[k], e), both(a.sl2 * s.scale[kvb % C::kInfo][0][2 * k + e / 16])));
                             }
-                        }
-                        if constexpr (MODE == kBiased) {
-                            const float d = static_cast<float>(p - t0 - 32 * k);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[k][e] = __float_as_uint(fmaf(-slope2, fabsf(d - static_cast<float>(e)), __uint_as_float(x[k][e])));
+                            keep(x[k], seen(k), -INFINITY);
                         }
                     }
-                    if (edge) clear(k, 0xff800000u);
-                    top[k] = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) top[k] = max3(top[k], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (MODE == kScaled) {  // (scales are not negative)
+                            const float2 f = edge ? both(1.f)
+                                                  : mul2(make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]), both(a.sl2));
+                            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 y = get2(x[k], e);
+                                top[e / 16] = max3(top[e / 16], y.x, y.y);
+                            }
+                            mx = max3(mx, top[0] * f.x, top[1] * f.y);
+                        } else {
+                            mx = fmaxf(mx, chunk_max(x[k]));
+                        }
+                    }
+                    if (MODE == kPlain) mx *= a.sl2;
                 }
-                float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-                if (MODE == kPlain) mx *= a.sl2;
                 const bool move = mx > m + 8.f;
                 if (nact == 0) {
                     if (move) m = mx;
@@ -918,7 +985,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     l[0] = mul2(l[0], both(f));
                     l[1] = mul2(l[1], both(f));
                     // the product before must be in O
-                    if (!mbar_wait(&s.o_done[i], (sn - 1) & 1)) {
+                    if (!warp_wait(&s.o_done[i], (sn - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -933,11 +1000,26 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         tmem_st16(my_o + k, o);
                     }
                 }
+                // (P of chunk k lies in columns 16 k .. 16 k + 15: chunks that were read before)
+                if constexpr (MODE == kShaped) {
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        tmem_ld32(my_s + 32 * k, x[0]);
+                        tmem_wait_ld();
+                        uint32_t o[16];
+                        numerators<false>(x[0], both(1.f), m, l, o);
+                        tmem_st16(my_s + 16 * k, o);
+                    }
+                } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t o[16];
-                    numerators<MODE == kPlain>(x[k], a.sl2, m, l, o);
-                    tmem_st16(my_s + 16 * k, o);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[16];
+                        float2 f = both(a.sl2);
+                        if constexpr (MODE == kScaled)
+                            f = edge ? both(1.f) : mul2(make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]), both(a.sl2));
+                        numerators<true>(x[k], f, m, l, o);
+                        tmem_st16(my_s + 16 * k, o);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -947,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             }
             if (!ok) break;
             if (nact > 0) {
-                if (!mbar_wait(&s.o_done[i], (sn - 1) & 1)) {
+                if (!warp_wait(&s.o_done[i], (sn - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -1043,11 +1125,11 @@ cudaError_t dispatch_size(const PreArgs& a, int D, cudaStream_t stream) {
 
 template <int KIND>
 cudaError_t dispatch(const PreArgs& a, int D, cudaStream_t stream) {
-    if (a.slopes) return dispatch_size<KIND, kBiased>(a, D, stream);
-    // (the plain kernel takes the maximum before it scales)
-    if constexpr (KIND != kWinInt8)
-        if (a.cap2 == 0.f && !a.kv_scales && a.sl2 > 0.f) return dispatch_size<KIND, kPlain>(a, D, stream);
-    return dispatch_size<KIND, kScaled>(a, D, stream);
+    if (a.slopes || a.cap2 > 0.f || !(a.sl2 > 0.f)) return dispatch_size<KIND, kShaped>(a, D, stream);
+    if constexpr (KIND != kWinBf16)
+        if (a.kv_scales) return dispatch_size<KIND, kScaled>(a, D, stream);
+    if constexpr (KIND != kWinInt8) return dispatch_size<KIND, kPlain>(a, D, stream);
+    return cudaErrorInvalidValue;  // (int8 codes always have scales)
 }
 
 }  // namespace pre
