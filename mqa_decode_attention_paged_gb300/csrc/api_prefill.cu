@@ -1,6 +1,7 @@
 // C ABI of prompt attention over paged GQA caches: argument validation and the
 // launches.  See include/mqa_decode.h for the contract.
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "../../include/mqa_decode_testing.h"
@@ -107,6 +108,7 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     a.out_scale = per_tensor ? v_scale : 1.f;
     a.cap2 = softcap * mqa::kLog2e;
     for (int k = 0; k < 6; ++k) a.tanh_c[k] = a.cap2 * mqa::kTanh[k];
+    for (int k = 0; k < 5; ++k) a.tanh_near[k] = a.cap2 * mqa::kTanhNear[k];
     a.inv_cap2 = softcap > 0.f ? 1.f / a.cap2 : 0.f;
     a.num_tokens = num_tokens;
     a.batch = batch;
@@ -128,7 +130,7 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     // 1526, 1385 and 1383 us, six of 500 to 2600 202, 170, 165 and 171; capped, where
     // a block takes twice as long, 3180, 3180, 3193 and 3221 (with a window of 1024,
     // six prompts: 302, 309, 309 and 318).
-    a.cell_cost = softcap > 0.f || slopes ? 1 : 3;
+    a.cell_cost = getenv("CC") ? atoi(getenv("CC")) : 3;
     a.grid = grid;
     a.cut = num_kv_splits > 1;
     a.withhold = withhold;

@@ -42,7 +42,7 @@ struct PreArgs {
     float sl2;               // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
     float out_scale;         // v_scale of a per-tensor e4m3 cache, else 1
     float cap2, inv_cap2;    // softcap * log2(e) and its reciprocal, or 0
-    float tanh_c[6];         // cap2 times kTanh
+    float tanh_c[6], tanh_near[5];  // cap2 times kTanh and kTanhNear
     int num_tokens, batch, Hq, Hkv, grp;
     int tile_tok, tile_rows;  // tokens and rows of a tile: rows = tokens * grp <= 128
     int num_blocks, page, max_blocks;

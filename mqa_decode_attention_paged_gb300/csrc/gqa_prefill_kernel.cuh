@@ -17,7 +17,7 @@
 //              tile's softmax runs beside the other's products
 //   10         walks the thread block's pieces, describes them for the others in a
 //              ring in shared memory, and copies their queries
-//   11..       make blocks ready: clear V rows that no row of the cell sees
+//   11 (8-bit caches: 12-15)  make blocks ready: clear V rows that no row of the cell sees
 //              (whatever bytes they hold: 0 * NaN), and widen 8-bit codes to bf16
 // TMEM (512 columns): O_0, O_1 (D fp32 columns each), S_0, S_1 (128 each); P_i
 // (bf16) overwrites S_i.
@@ -31,6 +31,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "gqa_prefill.cuh"
 #include "tc_ptx.cuh"
@@ -38,7 +39,7 @@
 namespace mqa {
 namespace pre {
 
-enum Mode { kPlain, kScaled, kShaped };
+enum Mode { kPlain, kScaled, kCapped, kBiased, kBoth };
 
 constexpr float kNone = -3e38f;  // reference before the first logit
 
@@ -51,10 +52,10 @@ struct Cfg {
     static constexpr int kRaw = kCodes ? kPreBlock * D : 0;       // bytes of a block of codes
     static constexpr int kStages = kCodes ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);  // bf16 ring
     static constexpr int kRawStages = kCodes ? (D == 128 ? 4 : 6) : 0;
-    static constexpr int kHelpers = kCodes ? 5 : 1;  // warps 11..
-    static constexpr int kThreads = 32 * (11 + kHelpers);
+    static constexpr int kHelper = kCodes ? 12 : 11, kHelpers = kCodes ? 4 : 1;  // first of them, how many
+    static constexpr int kThreads = 32 * (kHelper + kHelpers);
     // registers a thread: 64 K by the launch, moved between the warpgroups
-    static constexpr int kRegsSoftmax = kCodes ? 184 : 208, kRegsRest = kCodes ? 72 : 80;
+    static constexpr int kRegsSoftmax = kCodes ? 200 : 216, kRegsRest = kCodes ? 56 : 72;
     static constexpr int kInfo = 16;  // blocks whose validity and scales are kept
 };
 
@@ -201,14 +202,20 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     return d;
 }
 
-// cap2 tanh(y) / y for |y| <= 1 (see kTanh).
-__device__ __forceinline__ float2 tanh_over(const float (&c)[6], float2 y) {
+// cap2 tanh(y) / y by the polynomial c.
+template <int N>
+__device__ __forceinline__ float2 tanh_over(const float (&c)[N], float2 y) {
     const float2 z = mul2(y, y);
-    float2 w = fma2(z, both(c[5]), both(c[4]));
+    float2 w = both(c[N - 1]);
 #pragma unroll
-    for (int k = 3; k >= 0; --k) w = fma2(w, z, both(c[k]));
+    for (int k = N - 2; k >= 0; --k) w = fma2(w, z, both(c[k]));
     return w;
 }
+// One y = x / cap2, capped.
+__device__ __forceinline__ float capped(const PreArgs& a, float y) {
+    return fabsf(y) <= 1.f ? y * tanh_over(a.tanh_c, both(y)).x : tanh_far(a.cap2, y);
+}
+
 // ---- codes
 __device__ __forceinline__ float2 half2_f32(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -442,6 +449,19 @@ __device__ __forceinline__ void keep(uint32_t (&x)[32], uint32_t bits, float v) 
     for (int e = 0; e < 32; ++e)
         if (!((bits >> e) & 1u)) x[e] = __float_as_uint(v);
 }
+// The largest value of each 16 whose bit is set.
+__device__ __forceinline__ float2 group_max(const uint32_t (&x)[32], uint32_t bits) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 32; ++e) top[e / 16] = fmaxf(top[e / 16], (bits >> e) & 1u ? __uint_as_float(x[e]) : -INFINITY);
+    return make_float2(top[0], top[1]);
+}
+__device__ __forceinline__ float2 group_max(const uint32_t (&x)[32]) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) top[e / 16] = max3(top[e / 16], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    return make_float2(top[0], top[1]);
+}
 __device__ __forceinline__ float chunk_max(const uint32_t (&x)[32]) {
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -449,72 +469,53 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&x)[32]) {
     return fmaxf(top[0], top[1]);
 }
 
-// Logits (base 2) of 32 keys from their products: times sl2 and the scales f of
-// the two groups of 16, capped, less slope2 |d - e| (both_ways: some keys may lie
-// behind the query), masked by `bits` at the edges.
-__device__ __forceinline__ void shape_chunk(const PreArgs& a, uint32_t (&x)[32], float2 f, bool edge, uint32_t bits, bool bias,
-                                            float slope2, int d, bool both_ways) {
-    const bool cap = a.cap2 > 0.f;
-    const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
-    if (edge && cap) keep(x, bits, 0.f);  // (what lies where no key is seen must not choose the formula)
-    float far = 0.f;                      // the largest magnitude under the tanh
+// y[32] := cap2 tanh(y), eight polynomials at a time.
+template <int N>
+__device__ __forceinline__ void cap_chunk(const float (&c)[N], uint32_t (&x)[32]) {
+    constexpr int kChains = 8;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        const float2 y = mul2(get2(x, e), both(unit * (e < 16 ? f.x : f.y)));
-        put2(x, e, y);
-        far = max3_abs(far, y.x, y.y);
-    }
-    if (cap) {
-        if (far <= 1.f) {  // (a NaN passes the comparison of the others and stays one)
+    for (int e = 0; e < 32; e += 2 * kChains) {
+        float2 z[kChains], w[kChains];
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {  // eight chains at a time
-                float2 z[8], w[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    z[c] = mul2(get2(x, e + 2 * c), get2(x, e + 2 * c));
-                    w[c] = fma2(z[c], both(a.tanh_c[5]), both(a.tanh_c[4]));
-                }
-#pragma unroll
-                for (int q = 3; q >= 0; --q)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) w[c] = fma2(w[c], z[c], both(a.tanh_c[q]));
-#pragma unroll
-                for (int c = 0; c < 8; ++c) put2(x, e + 2 * c, mul2(get2(x, e + 2 * c), w[c]));
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float2 y = get2(x, e), near = mul2(y, tanh_over(a.tanh_c, y));
-                put2(x, e, make_float2(fabsf(y.x) <= 1.f ? near.x : tanh_far(a.cap2, y.x),
-                                       fabsf(y.y) <= 1.f ? near.y : tanh_far(a.cap2, y.y)));
-            }
+        for (int k = 0; k < kChains; ++k) {
+            z[k] = mul2(get2(x, e + 2 * k), get2(x, e + 2 * k));
+            w[k] = fma2(z[k], both(c[N - 1]), both(c[N - 2]));
         }
-    }
-    if (bias) {
-        // Every key that is seen lies at or before the query but for a prefix: slope2
-        // e - slope2 d then (a row sees its own key at distance 0, beside which the
-        // rounding of a far key's bias is nothing).
-        if (!both_ways) {
-            const float base = -slope2 * static_cast<float>(d);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-                put2(x, e, fma2(make_float2(static_cast<float>(e), static_cast<float>(e + 1)), both(slope2), add2(get2(x, e), both(base))));
-        } else {
+        for (int q = N - 3; q >= 0; --q)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                x[e] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(d) - static_cast<float>(e)), __uint_as_float(x[e])));
-        }
+            for (int k = 0; k < kChains; ++k) w[k] = fma2(w[k], z[k], both(c[q]));
+#pragma unroll
+        for (int k = 0; k < kChains; ++k) put2(x, e + 2 * k, mul2(get2(x, e + 2 * k), w[k]));
     }
-    if (edge) keep(x, bits, -INFINITY);
 }
 
-// P of 32 keys as bf16 pairs from logits x (times f, a scale for each 16 of them,
-// if MULTIPLY); their sum is added to l.
-template <bool MULTIPLY>
-__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float m, float2 (&l)[2], uint32_t (&p)[16]) {
+// Logits (base 2) of 32 keys from their products, whatever the shaping: times sl2
+// and the scales f of the two groups of 16, capped (mid: all within the reach of
+// kTanh), less slope2 |d - e|; -inf where `bits` has no bit.
+__device__ __forceinline__ void shape_any(const PreArgs& a, uint32_t (&x)[32], float2 f, bool mid, float slope2, int d, uint32_t bits) {
+    const bool cap = a.cap2 > 0.f;
+    const float unit = cap ? a.sl2 * a.inv_cap2 : a.sl2;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) put2(x, e, mul2(get2(x, e), both(unit * (e < 16 ? f.x : f.y))));
+    if (cap && mid) cap_chunk(a.tanh_c, x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        float y = __uint_as_float(x[e]);
+        if (cap && !mid) y = capped(a, y);
+        x[e] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(d - e)), y));
+    }
+    keep(x, bits, -INFINITY);
+}
+
+// P of 32 keys as bf16 pairs from x f + add, a scale f for each 16 of them, and +
+// slope2 e for key e if BIAS.  Their sum is added to l.
+template <bool BIAS>
+__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float add, float slope2, float2 (&l)[2], uint32_t (&p)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        const float2 y = MULTIPLY ? fma2(get2(x, 2 * k), both(k < 8 ? f.x : f.y), both(-m)) : add2(get2(x, 2 * k), both(-m));
+        float2 y = fma2(get2(x, 2 * k), both(k < 8 ? f.x : f.y), both(add));
+        if (BIAS) y = make_float2(fmaf(slope2, 2.f * k, y.x), fmaf(slope2, 2.f * k + 1.f, y.y));
         const float2 e = make_float2(ex2(y.x), ex2(y.y));
         l[k & 1] = add2(l[k & 1], e);
         p[k] = pack_bf16x2(e.x, e.y);
@@ -528,10 +529,11 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
 }
 
 // MODE: kPlain (one positive scale), kScaled (non-negative scales of token blocks),
-// kShaped (a cap, slopes, any scale).  The first two keep a row's 128 products in
-// registers and fold the scale into the exponent; with the shaping's temporaries
-// they would spill and its code, four times over, leave the instruction cache (a
-// capped prompt of 15999 tokens: 3160 us), so kShaped goes through TMEM in chunks.
+// kCapped, kBiased (slopes, or a scale <= 0), kBoth.  All keep a row's 128 products
+// in registers; what is rare (a logit beyond 0.75 of its cap, keys behind the query,
+// steep biases, scales <= 0) is shaped in a loop of its own through TMEM, so that
+// the code that runs stays short: with every case in line a capped prompt of 15999
+// tokens took 3509 us, a biased one 3728, a third of it waits for instructions.
 template <int D, int KIND, int MODE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
     using C = Cfg<D, KIND>;
@@ -540,7 +542,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     const uint32_t q_s = smem_u32(smem), kv_s = q_s + 2 * C::kTile, raw_s = kv_s + C::kStages * C::kTile;
     Shared& s = *reinterpret_cast<Shared*>(smem + (2 + C::kStages) * C::kTile + C::kRawStages * C::kRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool scaled = C::kCodes && a.kv_scales != nullptr;
+    const bool scaled = C::kCodes && MODE != kPlain && a.kv_scales != nullptr;
+    constexpr bool kCap = MODE == kCapped || MODE == kBoth, kBias = MODE == kBiased || MODE == kBoth;
     constexpr int kCopyStages = C::kCodes ? C::kRawStages : C::kStages;
 
     if (threadIdx.x == 0) {
@@ -811,10 +814,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         // no product may be in flight at the end
         umma_done(on, &s.drain);
         if (!mbar_wait(&s.drain, 0)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-    } else if (warp >= 11) {
+    } else if (warp >= C::kHelper) {
         // ------------------------------------------------ making blocks ready
         set_regs_down<C::kRegsRest>();
-        const int w = warp - 11;
+        const int w = warp - C::kHelper;
         int kvc = 0;
         for (int n = 0; ok; ++n) {
             const Piece* pp = piece(n);
@@ -849,33 +852,52 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                             fence_proxy_async_smem();
                         }
                     } else {
-                        // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one
-                        constexpr int kQ = D / 16;
+                        // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one; four at a time
+                        constexpr int kQ4 = D / 64, kUnits = kPreBlock / 8 * kQ4 / C::kHelpers;
                         const uint32_t src = raw_s + rst * C::kRaw;
-                        for (int i = w; i < kPreBlock / 8 * (kQ / 4); i += C::kHelpers) {
-                            const int r = i / (kQ / 4) * 8 + (lane & 7), q = i % (kQ / 4) * 4 + (lane >> 3);
-                            const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
-                            uint4 c = make_uint4(0, 0, 0, 0);
-                            const bool use = plane == 0 || all || seen(r);
-                            if (use) c = ld_shared16(src + at);
-                            const float f = plane == 1 && scaled && use ? s.scale[slot][1][r >> 4] : 1.f;
-                            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-                            uint32_t o[8];
+                        auto widen = [&](auto whole, auto times) {
+#pragma unroll 1
+                            for (int u0 = 0; u0 < kUnits; u0 += 4) {
+                                uint4 c[4];
+                                float f[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                float2 x = code_pair<KIND>(in[k] & 0xffffu), y = code_pair<KIND>(in[k] >> 16);
-                                if (plane == 1) {
-                                    x = mul2(x, both(f));
-                                    y = mul2(y, both(f));
+                                for (int u = 0; u < 4; ++u) {
+                                    const int i = (u0 + u) * C::kHelpers + w, r = i / kQ4 * 8 + (lane & 7), q = i % kQ4 * 4 + (lane >> 3);
+                                    const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
+                                    const bool use = decltype(whole)::value || seen(r);
+                                    c[u] = use ? ld_shared16(src + at) : make_uint4(0, 0, 0, 0);
+                                    f[u] = decltype(times)::value && use && scaled && plane == 1 ? s.scale[slot][1][r >> 4] : 1.f;
                                 }
-                                o[2 * k] = pack_bf16x2(x.x, x.y);
-                                o[2 * k + 1] = pack_bf16x2(y.x, y.y);
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const int i = (u0 + u) * C::kHelpers + w, r = i / kQ4 * 8 + (lane & 7), q = i % kQ4 * 4 + (lane >> 3);
+                                    const uint32_t in[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+                                    uint32_t o[8];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        float2 x = code_pair<KIND>(in[k] & 0xffffu), y = code_pair<KIND>(in[k] >> 16);
+                                        if constexpr (decltype(times)::value) {
+                                            x = mul2(x, both(f[u]));
+                                            y = mul2(y, both(f[u]));
+                                        }
+                                        o[2 * k] = pack_bf16x2(x.x, x.y);
+                                        o[2 * k + 1] = pack_bf16x2(y.x, y.y);
+                                    }
+                                    const uint32_t row = dst + (q >> 2) * C::kPanel + r * 128;
+                                    const int ch = (q & 3) * 2;
+                                    st_shared16(row + ((ch ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                                    st_shared16(row + (((ch + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+                                }
                             }
-                            const uint32_t row = dst + (q >> 2) * C::kPanel + r * 128;
-                            const int ch = (q & 3) * 2;
-                            st_shared16(row + ((ch ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-                            st_shared16(row + (((ch + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
-                        }
+                        };
+                        using Yes = std::true_type;
+                        using No = std::false_type;
+                        if (plane == 1 && !all)
+                            widen(No{}, Yes{});
+                        else if (scaled)  // (K's codes by 1: one loop for both planes stays in the instruction cache)
+                            widen(Yes{}, Yes{});
+                        else
+                            widen(Yes{}, No{});
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
@@ -887,6 +909,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             }
         }
         if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+    } else if (warp == 11) {
+        set_regs_down<C::kRegsRest>();  // (with its warpgroup)
     } else {
         // ------------------------------------------------ softmax of tile i
         set_regs_up<C::kRegsSoftmax>();
@@ -903,7 +927,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             const bool row = tk < view.cnt && r < a.tile_rows;
             const int lim = row && p >= 0 ? max(p + 1, pc->pre) : 0, lo = p - a.window + 1;
             float slope2 = 0.f;
-            if (MODE == kShaped && a.slopes && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
+            if (kBias && a.slopes && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
+            // where a bias changes by more than 64 over 32 keys, rows take the largest logit itself
+            const bool steep = kBias && __any_sync(0xffffffffu, !(fabsf(slope2) * 31.f <= 64.f));
             float m = kNone;
             float2 l[2] = {both(0.f), both(0.f)};
             int nact = 0;
@@ -925,53 +951,93 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     return below(lim - t) & (~below(lo - t) | below(a.sinks - t)) &
                            (((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u));
                 };
-                uint32_t x[MODE == kShaped ? 1 : 4][32];
+                uint32_t x[4][32];
                 float mx = -INFINITY;
-                if constexpr (MODE == kShaped) {
-                    // in chunks of 32 keys, through TMEM: the logits take S's place
+                auto scales = [&](int k) {  // of the two groups of chunk k
+                    return scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f);
+                };
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
+                tmem_wait_ld();
+                bool rare = false, mid = false;
+                if constexpr (kCap) {
+                    float size = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float wide[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            wide[e / 16] = max3_abs(wide[e / 16], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+                        const float2 f = scales(k);
+                        size = max3(size, wide[0] * f.x, wide[1] * f.y);
+                    }
+                    size *= fabsf(a.sl2) * a.inv_cap2;  // (a NaN passes the comparisons of the others and stays one)
+                    rare = __any_sync(0xffffffffu, row && size > 0.75f);
+                    mid = !__any_sync(0xffffffffu, row && size > 1.f);
+                }
+                if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
+                if constexpr (kCap || kBias) rare |= !(a.sl2 > 0.f);
+                if (__builtin_expect(rare, 0)) {
+                    // in chunks through TMEM: the logits take S's place
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         tmem_ld32(my_s + 32 * k, x[0]);
                         tmem_wait_ld();
-                        const float2 f = scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1])
-                                                : both(1.f);
-                        shape_chunk(a, x[0], f, edge, edge ? seen(k) : 0u, a.slopes != nullptr, slope2, p - t0 - 32 * k, pc->pre > 0);
+                        shape_any(a, x[0], scales(k), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
                         mx = fmaxf(mx, chunk_max(x[0]));
                         tmem_st32(my_s + 32 * k, x[0]);
                     }
                     tmem_wait_st();
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
-                    tmem_wait_ld();
-                    if (edge) {
+                    // With a bias, instead of the largest logit a bound of it: the largest
+                    // product of each 32 keys less the bias of the nearest (at most 64 too
+                    // large, see `steep`; numerators of 2^-64 lose nothing in bf16 or fp32).
+                    float b[4];
+                    if (!kCap && edge) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if constexpr (MODE == kScaled) {
+                            if constexpr (MODE != kPlain) {  // scaled first: a scale of 0 times -inf is no logit
+                                const float2 f = mul2(scales(k), both(a.sl2));
 #pragma unroll
-                                for (int e = 0; e < 32; e += 2)
-                                    put2(x[k], e, mul2(get2(x[k], e), both(a.sl2 * s.scale[kvb % C::kInfo][0][2 * k + e / 16])));
+                                for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
                             }
                             keep(x[k], seen(k), -INFINITY);
                         }
                     }
+                    if (kCap && edge) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (MODE == kScaled) {  // (scales are not negative)
-                            const float2 f = edge ? both(1.f)
-                                                  : mul2(make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]), both(a.sl2));
-                            float top[2] = {-INFINITY, -INFINITY};
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = mul2(scales(k), both(a.sl2)), top = group_max(x[k], seen(k));
+                            b[k] = fmaxf(top.x * f.x, top.y * f.y);
+                        }
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 y = get2(x[k], e);
-                                top[e / 16] = max3(top[e / 16], y.x, y.y);
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (C::kCodes && MODE != kPlain) {
+                                const float2 f = edge ? both(1.f) : mul2(scales(k), both(a.sl2)), top = group_max(x[k]);
+                                b[k] = fmaxf(top.x * f.x, top.y * f.y);
+                            } else {
+                                b[k] = chunk_max(x[k]);
                             }
-                            mx = max3(mx, top[0] * f.x, top[1] * f.y);
-                        } else {
-                            mx = fmaxf(mx, chunk_max(x[k]));
+                        }
+                        if constexpr (!(C::kCodes && MODE != kPlain) && MODE != kPlain) {
+                            const float f = !kCap && edge ? 1.f : a.sl2;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) b[k] *= f;
                         }
                     }
+                    if constexpr (kBias) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int d = p - t0 - 32 * k;  // distance of the chunk's first key
+                            const float near = slope2 * static_cast<float>(d < 0 ? -d : max(0, d - 31)), far = slope2 * static_cast<float>(max(abs(d), abs(d - 31)));
+                            if (kCap && b[k] > -INFINITY) b[k] = b[k] * a.inv_cap2 * tanh_over(a.tanh_near, both(b[k] * a.inv_cap2)).x;
+                            b[k] -= fminf(near, far);
+                        }
+                    }
+                    mx = max3(fmaxf(b[0], b[1]), b[2], b[3]);
                     if (MODE == kPlain) mx *= a.sl2;
+                    if (kCap && !kBias && mx > -INFINITY) mx = mx * a.inv_cap2 * tanh_over(a.tanh_near, both(mx * a.inv_cap2)).x;
                 }
                 const bool move = mx > m + 8.f;
                 if (nact == 0) {
@@ -1001,23 +1067,42 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     }
                 }
                 // (P of chunk k lies in columns 16 k .. 16 k + 15: chunks that were read before)
-                if constexpr (MODE == kShaped) {
+                if (__builtin_expect(rare, 0)) {
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
+                        uint32_t o[16];
                         tmem_ld32(my_s + 32 * k, x[0]);
                         tmem_wait_ld();
-                        uint32_t o[16];
-                        numerators<false>(x[0], both(1.f), m, l, o);
+                        numerators<false>(x[0], both(1.f), -m, 0.f, l, o);
                         tmem_st16(my_s + 16 * k, o);
                     }
                 } else {
+                    if constexpr (kCap) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = mul2(scales(k), both(a.sl2 * a.inv_cap2));
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
+                            cap_chunk(a.tanh_near, x[k]);
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) keep(x[k], seen(k), -INFINITY);
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t o[16];
                         float2 f = both(a.sl2);
-                        if constexpr (MODE == kScaled)
-                            f = edge ? both(1.f) : mul2(make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]), both(a.sl2));
-                        numerators<true>(x[k], f, m, l, o);
+                        if constexpr (kCap)
+                            f = both(1.f);
+                        else if constexpr (MODE != kPlain)
+                            f = edge ? both(1.f) : C::kCodes ? mul2(scales(k), both(a.sl2)) : f;
+                        // With a bias: every key that is seen lies at or before the query, slope2 e -
+                        // slope2 d (a row sees its own key at distance 0, beside which the rounding
+                        // of a far key's bias is nothing).
+                        const float add = kBias ? fmaf(-slope2, static_cast<float>(p - t0 - 32 * k), -m) : -m;
+                        numerators<kBias>(x[k], f, add, slope2, l, o);
                         tmem_st16(my_s + 16 * k, o);
                     }
                 }
@@ -1125,7 +1210,8 @@ cudaError_t dispatch_size(const PreArgs& a, int D, cudaStream_t stream) {
 
 template <int KIND>
 cudaError_t dispatch(const PreArgs& a, int D, cudaStream_t stream) {
-    if (a.slopes || a.cap2 > 0.f || !(a.sl2 > 0.f)) return dispatch_size<KIND, kShaped>(a, D, stream);
+    if (a.cap2 > 0.f) return a.slopes ? dispatch_size<KIND, kBoth>(a, D, stream) : dispatch_size<KIND, kCapped>(a, D, stream);
+    if (a.slopes || !(a.sl2 > 0.f)) return dispatch_size<KIND, kBiased>(a, D, stream);
     if constexpr (KIND != kWinBf16)
         if (a.kv_scales) return dispatch_size<KIND, kScaled>(a, D, stream);
     if constexpr (KIND != kWinInt8) return dispatch_size<KIND, kPlain>(a, D, stream);

@@ -43,10 +43,11 @@ struct FastDiv {
 };
 
 // Caps of logits, in base 2: cap2 tanh(x / cap2).
-// tanh(y) / y for |y| <= 1: c0 + c1 y^2 + .. + c5 y^10, coefficients of least
-// squares towards the smallest absolute error of tanh, 2.4e-7 (of logits capped at
-// 50: 1.7e-5 in base 2, far below the 2^-9 of P's rounding).
+// tanh(y) / y: c0 + c1 y^2 + .., coefficients of least squares towards the smallest
+// absolute error of tanh.  kTanh for |y| <= 1: 2.4e-7 (of logits capped at 50: 1.7e-5
+// in base 2, far below the 2^-9 of P's rounding); kTanhNear for |y| <= 0.75: 1.9e-7.
 constexpr float kTanh[6] = {0.9999968409f, -0.3332400322f, 0.1325352489f, -0.05097286030f, 0.01611417904f, -0.002839464694f};
+constexpr float kTanhNear[5] = {0.9999971986f, -0.3332307637f, 0.1322609186f, -0.04928044975f, 0.01231883466f};
 
 struct WinArgs {
     CUtensorMap tmap;  // {line, rows (block, plane, token), panels, heads}
