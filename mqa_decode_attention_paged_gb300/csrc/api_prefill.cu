@@ -131,6 +131,10 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     // a block takes twice as long, 3180, 3180, 3193 and 3221 (with a window of 1024,
     // six prompts: 302, 309, 309 and 318).
     a.cell_cost = getenv("CC") ? atoi(getenv("CC")) : 3;
+    const double unit = softcap > 0.f ? static_cast<double>(a.sl2) * a.inv_cap2 : 0.0;
+    double power = unit;
+    for (int k = 0; k < 5; ++k, power *= unit * unit) a.tanh_raw[k] = static_cast<float>(a.cap2 * mqa::kTanhNear[k] * power);
+    a.tiny_unit = std::fabs(unit) < 1e-4 || std::fabs(unit) > 1.0;
     a.grid = grid;
     a.cut = num_kv_splits > 1;
     a.withhold = withhold;

@@ -928,8 +928,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             const int lim = row && p >= 0 ? max(p + 1, pc->pre) : 0, lo = p - a.window + 1;
             float slope2 = 0.f;
             if (kBias && a.slopes && row) slope2 = __ldg(a.slopes + pc->h * a.grp + g) * kLog2e;
-            // where a bias changes by more than 64 over 32 keys, rows take the largest logit itself
-            const bool steep = kBias && __any_sync(0xffffffffu, !(fabsf(slope2) * 31.f <= 64.f));
+            // where a bias falls by more than 64 over 32 keys (or rises), rows take the largest logit itself
+            const bool steep = kBias && __any_sync(0xffffffffu, !(slope2 >= 0.f && slope2 * 31.f <= 64.f));
             float m = kNone;
             float2 l[2] = {both(0.f), both(0.f)};
             int nact = 0;
@@ -952,13 +952,40 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                            (((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u));
                 };
                 uint32_t x[4][32];
-                float mx = -INFINITY;
                 auto scales = [&](int k) {  // of the two groups of chunk k
                     return scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f);
                 };
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 tmem_wait_ld();
+                // The row's reference after a block whose largest logit is mx (or less); false if a wait ran out.
+                auto refer = [&](float mx) {
+                    const bool move = mx > m + 8.f;
+                    if (nact == 0) {
+                        if (move) m = mx;
+                    } else if (__any_sync(0xffffffffu, move)) {
+                        float f = 1.f;
+                        if (move) {
+                            f = ex2(m - mx);
+                            m = mx;
+                        }
+                        l[0] = mul2(l[0], both(f));
+                        l[1] = mul2(l[1], both(f));
+                        // the product before must be in O
+                        if (!warp_wait(&s.o_done[i], (sn - 1) & 1)) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(my_o + k, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(my_o + k, o);
+                        }
+                    }
+                    return true;
+                };
                 bool rare = false, mid = false;
                 if constexpr (kCap) {
                     float size = 0.f;
@@ -972,26 +999,35 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         size = max3(size, wide[0] * f.x, wide[1] * f.y);
                     }
                     size *= fabsf(a.sl2) * a.inv_cap2;  // (a NaN passes the comparisons of the others and stays one)
-                    rare = __any_sync(0xffffffffu, row && size > 0.75f);
+                    rare = a.tiny_unit || __any_sync(0xffffffffu, row && size > 0.75f);
                     mid = !__any_sync(0xffffffffu, row && size > 1.f);
                 }
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
                 if constexpr (kCap || kBias) rare |= !(a.sl2 > 0.f);
                 if (__builtin_expect(rare, 0)) {
-                    // in chunks through TMEM: the logits take S's place
+                    // in chunks through TMEM: the logits take S's place, then P theirs (that of
+                    // chunk k in columns 16 k .. 16 k + 15, of chunks that were read before)
+                    float mx = -INFINITY;
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        tmem_ld32(my_s + 32 * k, x[0]);
+                        uint32_t y[32];
+                        tmem_ld32(my_s + 32 * k, y);
                         tmem_wait_ld();
-                        shape_any(a, x[0], scales(k), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
-                        mx = fmaxf(mx, chunk_max(x[0]));
-                        tmem_st32(my_s + 32 * k, x[0]);
+                        shape_any(a, y, scales(k), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
+                        mx = fmaxf(mx, chunk_max(y));
+                        tmem_st32(my_s + 32 * k, y);
                     }
                     tmem_wait_st();
+                    ok = refer(mx);
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t y[32], o[16];
+                        tmem_ld32(my_s + 32 * k, y);
+                        tmem_wait_ld();
+                        numerators<false>(y, both(1.f), -m, 0.f, l, o);
+                        tmem_st16(my_s + 16 * k, o);
+                    }
                 } else {
-                    // With a bias, instead of the largest logit a bound of it: the largest
-                    // product of each 32 keys less the bias of the nearest (at most 64 too
-                    // large, see `steep`; numerators of 2^-64 lose nothing in bf16 or fp32).
                     float b[4];
                     if (!kCap && edge) {
 #pragma unroll
@@ -1007,83 +1043,49 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     if (kCap && edge) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float2 f = mul2(scales(k), both(a.sl2)), top = group_max(x[k], seen(k));
+                            const float2 f = scales(k), top = group_max(x[k], seen(k));
                             b[k] = fmaxf(top.x * f.x, top.y * f.y);
                         }
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if constexpr (C::kCodes && MODE != kPlain) {
-                                const float2 f = edge ? both(1.f) : mul2(scales(k), both(a.sl2)), top = group_max(x[k]);
+                                const float2 f = !kCap && edge ? both(1.f) : scales(k), top = group_max(x[k]);
                                 b[k] = fmaxf(top.x * f.x, top.y * f.y);
                             } else {
                                 b[k] = chunk_max(x[k]);
                             }
                         }
-                        if constexpr (!(C::kCodes && MODE != kPlain) && MODE != kPlain) {
-                            const float f = !kCap && edge ? 1.f : a.sl2;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) b[k] *= f;
-                        }
                     }
+                    // (of logits, and of products that are not scaled yet; with a cap of what it takes)
+                    const float unit = MODE == kPlain || kCap || !edge ? a.sl2 : 1.f;
+                    float mx;
                     if constexpr (kBias) {
+                        // Instead of the largest logit a bound of it: the largest product of
+                        // each 32 keys less the bias of the nearest (at most 64 too large, see
+                        // `steep`; numerators of 2^-64 lose nothing in bf16 or fp32).
+                        const float d = static_cast<float>(p - t0);  // distance of the block's first key
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int d = p - t0 - 32 * k;  // distance of the chunk's first key
-                            const float near = slope2 * static_cast<float>(d < 0 ? -d : max(0, d - 31)), far = slope2 * static_cast<float>(max(abs(d), abs(d - 31)));
+                            b[k] *= unit;
                             if (kCap && b[k] > -INFINITY) b[k] = b[k] * a.inv_cap2 * tanh_over(a.tanh_near, both(b[k] * a.inv_cap2)).x;
-                            b[k] -= fminf(near, far);
+                            b[k] = fmaf(-slope2, fmaxf(0.f, d - (32.f * k + 31.f)), b[k]);
                         }
+                        mx = max3(fmaxf(b[0], b[1]), b[2], b[3]);
+                    } else {
+                        mx = max3(fmaxf(b[0], b[1]), b[2], b[3]) * unit;
+                        if (kCap && mx > -INFINITY) mx = mx * a.inv_cap2 * tanh_over(a.tanh_near, both(mx * a.inv_cap2)).x;
                     }
-                    mx = max3(fmaxf(b[0], b[1]), b[2], b[3]);
-                    if (MODE == kPlain) mx *= a.sl2;
-                    if (kCap && !kBias && mx > -INFINITY) mx = mx * a.inv_cap2 * tanh_over(a.tanh_near, both(mx * a.inv_cap2)).x;
-                }
-                const bool move = mx > m + 8.f;
-                if (nact == 0) {
-                    if (move) m = mx;
-                } else if (__any_sync(0xffffffffu, move)) {
-                    float f = 1.f;
-                    if (move) {
-                        f = ex2(m - mx);
-                        m = mx;
-                    }
-                    l[0] = mul2(l[0], both(f));
-                    l[1] = mul2(l[1], both(f));
-                    // the product before must be in O
-                    if (!warp_wait(&s.o_done[i], (sn - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < D; k += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(my_o + k, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st16(my_o + k, o);
-                    }
-                }
-                // (P of chunk k lies in columns 16 k .. 16 k + 15: chunks that were read before)
-                if (__builtin_expect(rare, 0)) {
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[16];
-                        tmem_ld32(my_s + 32 * k, x[0]);
-                        tmem_wait_ld();
-                        numerators<false>(x[0], both(1.f), -m, 0.f, l, o);
-                        tmem_st16(my_s + 16 * k, o);
-                    }
-                } else {
+                    ok = refer(mx);
                     if constexpr (kCap) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float2 f = mul2(scales(k), both(a.sl2 * a.inv_cap2));
+                            if (scaled) {
+                                const float2 f = scales(k);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
-                            cap_chunk(a.tanh_near, x[k]);
+                                for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
+                            }
+                            cap_chunk(a.tanh_raw, x[k]);
                         }
                         if (edge) {
 #pragma unroll
@@ -1106,6 +1108,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         tmem_st16(my_s + 16 * k, o);
                     }
                 }
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&s.p_full[i]);
