@@ -83,7 +83,7 @@ struct Shared {
     uint32_t tmem;
     Piece piece[kPieces];
     uint32_t valid[16];      // 16-token groups of a block that were copied
-    float scale[16][2][8];   // their K and V scales
+    alignas(16) float scale[16][2][8];  // their K and V scales
 };
 
 template <int D, int KIND>
@@ -220,16 +220,17 @@ __device__ __forceinline__ float capped(const PreArgs& a, float y) {
 __device__ __forceinline__ float2 half2_f32(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Two codes in the low half of w -> two fp32 values (exact).
-template <int KIND>
+// Two codes, bytes 2 i and 2 i + 1 of w, as two fp32 values (exact).
+template <int KIND, int I>
 __device__ __forceinline__ float2 code_pair(uint32_t w) {
     if constexpr (KIND == kWinE4m3) {
-        return half2_f32(e4m3x2_to_f16x2(w));
+        return half2_f32(e4m3x2_to_f16x2(I ? w >> 16 : w & 0xffffu));
     } else {
-        // 1024 + (code + 128) is exact in the mantissa of f16 0x6400
-        const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-        return __half22float2(h);
+        // 2^23 + (code + 128) is exact in the mantissa of 0x4b000000
+        const uint32_t u = w ^ 0x80808080u;
+        return add2(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + 2 * I)),
+                                __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + 2 * I))),
+                    both(-8388736.f));
     }
 }
 
@@ -875,7 +876,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                     uint32_t o[8];
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) {
-                                        float2 x = code_pair<KIND>(in[k] & 0xffffu), y = code_pair<KIND>(in[k] >> 16);
+                                        float2 x = code_pair<KIND, 0>(in[k]), y = code_pair<KIND, 1>(in[k]);
                                         if constexpr (decltype(times)::value) {
                                             x = mul2(x, both(f[u]));
                                             y = mul2(y, both(f[u]));
@@ -952,8 +953,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                            (((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u));
                 };
                 uint32_t x[4][32];
-                auto scales = [&](int k) {  // of the two groups of chunk k
-                    return scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f);
+                float4 ks[2] = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
+                if (scaled && !kCap) {
+                    ks[0] = *reinterpret_cast<const float4*>(&s.scale[kvb % C::kInfo][0][0]);
+                    ks[1] = *reinterpret_cast<const float4*>(&s.scale[kvb % C::kInfo][0][4]);
+                }
+                auto scales = [&](int k) {  // of the two groups of chunk k (with a cap from shared memory: registers)
+                    if (kCap && scaled) return make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]);
+                    return k & 1 ? make_float2(ks[k >> 1].z, ks[k >> 1].w) : make_float2(ks[k >> 1].x, ks[k >> 1].y);
                 };
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
@@ -1013,7 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         uint32_t y[32];
                         tmem_ld32(my_s + 32 * k, y);
                         tmem_wait_ld();
-                        shape_any(a, y, scales(k), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
+                        shape_any(a, y, scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
                         mx = fmaxf(mx, chunk_max(y));
                         tmem_st32(my_s + 32 * k, y);
                     }
