@@ -2,7 +2,7 @@
 with their checks of arguments.  Reached through the package, like the calls of :mod:`._binding`."""
 from __future__ import annotations
 
-import ctypes
+from array import array
 
 import torch
 
@@ -100,16 +100,24 @@ def gqa_prefill(q, kv_cache, block_table, seq_lens, query_start, scale, *, softc
 
 
 def _pools(caches, num_blocks, index):
-    """Host arrays of the caches' addresses and bytes per page."""
-    n = len(caches)
-    for i, t in enumerate(caches):
-        if t.dim() < 1 or t.shape[0] != num_blocks or not t.is_contiguous() or t.get_device() != index:
+    """Addresses and bytes per page of the caches, as arrays of 64-bit words for the C ABI."""
+    addresses, sizes = array("Q"), array("Q")
+    for t in caches:
+        s = t.shape
+        if not (len(s) > 0 and s[0] == num_blocks and t.get_device() == index and t.is_contiguous()):
+            i = len(addresses)
             _check(t, f"caches[{i}]")
-            if t.dim() < 1 or t.shape[0] != num_blocks:
-                raise ValueError(f"caches[{i}] must have {num_blocks} pages in its first dimension, got {tuple(t.shape)}")
+            if len(s) < 1 or s[0] != num_blocks:
+                raise ValueError(f"caches[{i}] must have {num_blocks} pages in its first dimension, got {tuple(s)}")
             raise ValueError(f"caches[{i}] is on {t.device}, the call runs on cuda:{index}")
-    return ((ctypes.c_void_p * n)(*(t.data_ptr() for t in caches)),
-            (ctypes.c_size_t * n)(*(t.nbytes // num_blocks for t in caches)))
+        addresses.append(t.data_ptr())
+        sizes.append(t.nbytes // num_blocks)
+    return addresses, sizes
+
+
+def _int32(t, shape, index):
+    """Whether t is None or an int32 tensor of that shape on device `index`, contiguous."""
+    return t is None or (t.dtype is _I32 and t.shape == shape and t.get_device() == index and t.is_contiguous())
 
 
 def _check_pages(block_table, seq_lens, refs, named, workspace, device_status):
@@ -139,15 +147,20 @@ def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_t
     [num_blocks, ...] whose pages are copied, in place (of every layer; block scales are tensors of their own).
     Returns new_table [new_rows, max_blocks], new_lens [new_rows] and new_refs [num_blocks] (new_refs may be refs
     itself; allocated with torch when not given)."""
-    caches = list(caches)
-    N = parents.shape[0] if parents.dim() == 1 else -1
-    if N < 0:
+    if parents.dim() != 1:
         raise ValueError("parents must be int32 [new_rows]")
-    width = block_table.shape[-1]
-    index = _check_pages(block_table, seq_lens, refs,
-                         (("parents", parents, (N,)), ("new_table", new_table, (N, width)),
-                          ("new_lens", new_lens, (N,)), ("new_refs", new_refs, refs.shape)), workspace, device_status)
-    nb = refs.shape[0]
+    shape, N, index = block_table.shape, parents.shape[0], block_table.get_device()
+    if not (index >= 0 and len(shape) == 2 and refs.dim() == 1 and _int32(block_table, shape, index)
+            and _int32(seq_lens, shape[:1], index) and _int32(parents, (N,), index) and _int32(refs, refs.shape, index)
+            and _int32(new_table, (N, shape[1]), index) and _int32(new_lens, (N,), index)
+            and _int32(new_refs, refs.shape, index)
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == index))
+            and (device_status is None or _fits(device_status, _I32, device_status.shape, index))):
+        index = _check_pages(block_table, seq_lens, refs,
+                             (("parents", parents, (N,)), ("new_table", new_table, (N, shape[-1])),
+                              ("new_lens", new_lens, (N,)), ("new_refs", new_refs, refs.shape)), workspace,
+                             device_status)
+    width, nb = shape[1], refs.shape[0]
     addresses, sizes = _pools(caches, nb, index)
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
@@ -163,11 +176,11 @@ def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_t
         return t
 
     new_table, new_lens, new_refs = given(new_table, N, width), given(new_lens, N), given(new_refs, nb)
-    if workspace is None:
-        workspace = given(None, max(16, lib.mqa_pages_fork_workspace_bytes(N) // 4))
-    rc = lib.mqa_pages_fork(_raw(block_table), _raw(seq_lens), _raw(parents), _raw(refs), _raw(new_table),
-                            _raw(new_lens), _raw(new_refs), block_table.shape[0], N, width, nb, int(page_size),
-                            addresses, sizes, len(caches), _raw(workspace), workspace.nbytes, _raw(device_status),
+    workspace = given(workspace, max(16, lib.mqa_pages_fork_workspace_bytes(N) // 4))
+    rc = lib.mqa_pages_fork(block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(), refs.data_ptr(),
+                            new_table.data_ptr(), new_lens.data_ptr(), new_refs.data_ptr(), shape[0], N, width, nb,
+                            int(page_size), addresses.buffer_info()[0], sizes.buffer_info()[0], len(addresses),
+                            workspace.data_ptr(), workspace.nbytes, _raw(device_status),
                             _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "mqa_pages_fork")
@@ -180,11 +193,17 @@ def pages_compact(block_table, seq_lens, refs, caches, page_size, *, new_table=N
     new_table (the renamed table; may be block_table itself), new_refs (may be refs itself), moved int32 [num_blocks]
     (each page's new id, -1 for free ones) and num_live int32 [1], allocated with torch when not given.  Arguments as
     for :func:`pages_fork`."""
-    caches = list(caches)
-    nb = refs.shape[0] if refs.dim() == 1 else 0
-    index = _check_pages(block_table, seq_lens, refs,
-                         (("new_table", new_table, block_table.shape), ("new_refs", new_refs, refs.shape),
-                          ("moved", moved, refs.shape), ("num_live", num_live, (1,))), workspace, device_status)
+    shape, index = block_table.shape, block_table.get_device()
+    if not (index >= 0 and len(shape) == 2 and refs.dim() == 1 and _int32(block_table, shape, index)
+            and _int32(seq_lens, shape[:1], index) and _int32(refs, refs.shape, index) and _int32(new_table, shape, index)
+            and _int32(new_refs, refs.shape, index) and _int32(moved, refs.shape, index)
+            and _int32(num_live, (1,), index)
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == index))
+            and (device_status is None or _fits(device_status, _I32, device_status.shape, index))):
+        index = _check_pages(block_table, seq_lens, refs,
+                             (("new_table", new_table, shape), ("new_refs", new_refs, refs.shape),
+                              ("moved", moved, refs.shape), ("num_live", num_live, (1,))), workspace, device_status)
+    nb = refs.shape[0]
     addresses, sizes = _pools(caches, nb, index)
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
@@ -199,13 +218,13 @@ def pages_compact(block_table, seq_lens, refs, caches, page_size, *, new_table=N
             fresh.append(t)
         return t
 
-    new_table, new_refs = given(new_table, *block_table.shape), given(new_refs, nb)
+    new_table, new_refs = given(new_table, *shape), given(new_refs, nb)
     moved, num_live = given(moved, nb), given(num_live, 1)
-    if workspace is None:
-        workspace = given(None, max(16, lib.mqa_pages_compact_workspace_bytes(nb) // 4))
-    rc = lib.mqa_pages_compact(_raw(block_table), _raw(seq_lens), _raw(refs), _raw(new_table), _raw(new_refs),
-                               _raw(moved), _raw(num_live), *block_table.shape, nb, int(page_size), addresses, sizes,
-                               len(caches), _raw(workspace), workspace.nbytes, _raw(device_status),
+    workspace = given(workspace, max(16, lib.mqa_pages_compact_workspace_bytes(nb) // 4))
+    rc = lib.mqa_pages_compact(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), new_table.data_ptr(),
+                               new_refs.data_ptr(), moved.data_ptr(), num_live.data_ptr(), shape[0], shape[1], nb,
+                               int(page_size), addresses.buffer_info()[0], sizes.buffer_info()[0], len(addresses),
+                               workspace.data_ptr(), workspace.nbytes, _raw(device_status),
                                _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "mqa_pages_compact")

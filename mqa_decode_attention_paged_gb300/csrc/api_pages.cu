@@ -1,5 +1,8 @@
 // C ABI of the page operations: argument validation and the launches.  See
 // include/mqa_decode.h for the contract.
+#include <algorithm>
+#include <utility>
+
 #include "api_common.cuh"
 #include "pages.cuh"
 
@@ -13,18 +16,21 @@ mqa_status pools_of(mqa::PagePools& p, void* const* caches, const size_t* page_b
     if (n < 0 || (n > 0 && (!caches || !page_bytes))) return MQA_ERR_INVALID_ARG;
     if (n > mqa::kMaxPools) return MQA_ERR_UNSUPPORTED;
     long long chunks = 0;
+    std::pair<uintptr_t, uintptr_t> places[mqa::kMaxPools];
     for (int i = 0; i < n; ++i) {
         if (!caches[i] || !api_aligned(caches[i], 16) || page_bytes[i] < 4) return MQA_ERR_INVALID_ARG;
         if (page_bytes[i] % 4 != 0 || page_bytes[i] > (1ull << 30)) return MQA_ERR_UNSUPPORTED;
-        for (int k = 0; k < i; ++k) {  // (two pools in one place would be copied by two blocks at once)
-            const uintptr_t x = reinterpret_cast<uintptr_t>(caches[i]), y = reinterpret_cast<uintptr_t>(caches[k]);
-            if (x < y + page_bytes[k] * num_blocks && y < x + page_bytes[i] * num_blocks) return MQA_ERR_INVALID_ARG;
-        }
+        const uintptr_t at = reinterpret_cast<uintptr_t>(caches[i]);
+        places[i] = {at, at + page_bytes[i] * static_cast<size_t>(num_blocks)};
         p.pool[i].base = static_cast<char*>(caches[i]);
         p.pool[i].bytes = static_cast<long long>(page_bytes[i]);
         p.first[i] = static_cast<int>(chunks);
         chunks += (p.pool[i].bytes + mqa::kPageChunk - 1) / mqa::kPageChunk;
     }
+    // (two pools in one place would be copied by two blocks at once)
+    std::sort(places, places + n);
+    for (int i = 1; i < n; ++i)
+        if (places[i].first < places[i - 1].second) return MQA_ERR_INVALID_ARG;
     p.first[n] = static_cast<int>(chunks);
     p.n = n;
     return MQA_OK;

@@ -1,7 +1,6 @@
 // C ABI of prompt attention over paged GQA caches: argument validation and the
 // launches.  See include/mqa_decode.h for the contract.
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 
 #include "../../include/mqa_decode_testing.h"
@@ -74,10 +73,11 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     // a token's row of q: dense, 16-byte aligned
     if (q_stride % 8 != 0 || q_stride < static_cast<long long>(num_q_heads) * head_size || q_stride > (1LL << 36))
         return MQA_ERR_INVALID_ARG;
+    if (num_kv_splits > 1 && !workspace) return MQA_ERR_WORKSPACE_TOO_SMALL;
     const int grid = grid_of();
     if (grid < 1) return MQA_ERR_CUDA;
     const size_t need = num_kv_splits > 1 ? mqa::pre_workspace_bytes(grid, head_size) : 0;
-    if (need > 0 && (!workspace || workspace_bytes < need)) return MQA_ERR_WORKSPACE_TOO_SMALL;
+    if (need > 0 && workspace_bytes < need) return MQA_ERR_WORKSPACE_TOO_SMALL;
     if (need > 0 && !api_aligned(workspace, 16)) return MQA_ERR_INVALID_ARG;
     if (num_tokens == 0) return MQA_OK;
 
@@ -128,9 +128,8 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     // What a (cell, head) takes beside its blocks (Q's copy, the first product, the
     // output), in blocks: with 1, 2, 3 and 4 one prompt of 15999 tokens takes 1740,
     // 1526, 1385 and 1383 us, six of 500 to 2600 202, 170, 165 and 171; capped, where
-    // a block takes twice as long, 3180, 3180, 3193 and 3221 (with a window of 1024,
-    // six prompts: 302, 309, 309 and 318).
-    a.cell_cost = getenv("CC") ? atoi(getenv("CC")) : 3;
+    // a block takes longer, 2 and 3 are within 2 % of each other.
+    a.cell_cost = 3;
     const double unit = softcap > 0.f ? static_cast<double>(a.sl2) * a.inv_cap2 : 0.0;
     double power = unit;
     for (int k = 0; k < 5; ++k, power *= unit * unit) a.tanh_raw[k] = static_cast<float>(a.cap2 * mqa::kTanhNear[k] * power);
