@@ -52,6 +52,7 @@ struct Cfg {
     static constexpr int kRaw = kCodes ? kPreBlock * D : 0;       // bytes of a block of codes
     static constexpr int kStages = kCodes ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);  // bf16 ring
     static constexpr int kRawStages = kCodes ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int kQ = D == 64 ? 2 : 1;  // cells whose queries are held
     static constexpr int kHelper = kCodes ? 12 : 11, kHelpers = kCodes ? 4 : 1;  // first of them, how many
     static constexpr int kThreads = 32 * (kHelper + kHelpers);
     // registers a thread: 64 K by the launch, moved between the warpgroups
@@ -74,7 +75,7 @@ struct Shared {
     uint64_t kv_free[8];   // codes: read by the helpers; bf16: see ready / used
     uint64_t ready[8];     // a bf16 stage may be multiplied
     uint64_t used[8];      // .. and was
-    uint64_t q_full, q_free;
+    uint64_t q_full[2], q_free[2];
     uint64_t piece_full[kPieces], piece_free[kPieces];
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2], drain;
     long long scan[16];
@@ -89,7 +90,7 @@ struct Shared {
 template <int D, int KIND>
 constexpr int smem_bytes() {
     using C = Cfg<D, KIND>;
-    return 2 * C::kTile + C::kStages * C::kTile + C::kRawStages * C::kRaw + 1024 + static_cast<int>(sizeof(Shared));
+    return 2 * C::kQ * C::kTile + C::kStages * C::kTile + C::kRawStages * C::kRaw + 1024 + static_cast<int>(sizeof(Shared));
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
@@ -98,6 +99,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void* tmap, int x, 
             dst),
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+__device__ __forceinline__ void tma_prefetch(const void* tmap, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(x), "r"(y), "r"(z) : "memory");
 }
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -523,10 +527,17 @@ __device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, fl
     }
 }
 
-// (16-byte stores: that is how outputs are aligned)
-__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+// 32 bytes, in one store where `wide` says that they are aligned to it (rows lie
+// apart, so that a warp's store takes a cycle for each lane whatever its width).
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 // MODE: kPlain (one positive scale), kScaled (non-negative scales of token blocks),
@@ -540,8 +551,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     using C = Cfg<D, KIND>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t q_s = smem_u32(smem), kv_s = q_s + 2 * C::kTile, raw_s = kv_s + C::kStages * C::kTile;
-    Shared& s = *reinterpret_cast<Shared*>(smem + (2 + C::kStages) * C::kTile + C::kRawStages * C::kRaw);
+    const uint32_t q_s = smem_u32(smem), kv_s = q_s + 2 * C::kQ * C::kTile, raw_s = kv_s + C::kStages * C::kTile;
+    Shared& s = *reinterpret_cast<Shared*>(smem + (2 * C::kQ + C::kStages) * C::kTile + C::kRawStages * C::kRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool scaled = C::kCodes && MODE != kPlain && a.kv_scales != nullptr;
     constexpr bool kCap = MODE == kCapped || MODE == kBoth, kBias = MODE == kBiased || MODE == kBoth;
@@ -556,9 +567,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             mbar_init(&s.ready[i], C::kHelpers);
             mbar_init(&s.used[i], 1);
         }
-        mbar_init(&s.q_full, 1);
-        mbar_init(&s.q_free, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_free[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 128);
             mbar_init(&s.o_done[i], 1);
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     if (warp == 9) tmem_alloc(&s.tmem, 512);
     pdl_wait();
     pdl_launch_dependents();
-    plan(a, s, reinterpret_cast<int*>(smem + 2 * C::kTile));  // the ring is not in use yet
+    plan(a, s, reinterpret_cast<int*>(smem + 2 * C::kQ * C::kTile));  // the ring is not in use yet
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -681,9 +692,29 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         if (lane == 0) {
             Pieces pw;
             pw.init(a, s);
-            int n = 0, queries = 0, head = 3, begun = 0, row0 = 0, cnt = 0, h = 0;
-            for (bool more = true; more && ok; ++n) {
-                more = pw.next(a);
+            int queries = 0, head = 3, begun = 0, row0 = 0, cnt = 0, h = 0;
+            // queries of the last described piece with blocks, not copied yet: a piece is
+            // described (and its queries fetched towards L2) before the one before it gets
+            // its queries, which waits for the products of the one before that
+            int q_row = 0, q_cnt = 0, q_head = 0;
+            auto copy_queries = [&]() {
+                if (q_cnt == 0) return;
+                const int qs = queries % C::kQ;
+                if (queries >= C::kQ && !mbar_wait(&s.q_free[qs], (queries / C::kQ & 1) ^ 1)) {
+                    ok = false;
+                    return;
+                }
+                const int tiles = q_cnt > a.tile_tok ? 2 : 1;
+                mbar_arrive_expect_tx(&s.q_full[qs], tiles * a.tile_rows * D * 2);
+                for (int i = 0; i < tiles; ++i)
+                    for (int p = 0; p < C::kPanels; ++p)
+                        tma_load(q_s + (2 * qs + i) * C::kTile + p * C::kPanel, &a.q_map, p * 64, q_head * a.grp, q_row + i * a.tile_tok,
+                                 &s.q_full[qs]);
+                ++queries;
+                q_cnt = 0;
+            };
+            for (int n = 0; ok; ++n) {
+                const bool more = pw.next(a);
                 if (n >= kPieces && !mbar_wait(&s.piece_free[n % kPieces], (n / kPieces & 1) ^ 1)) {
                     ok = false;
                     break;
@@ -699,19 +730,19 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 cnt = c.cnt;
                 h = pw.h;
                 if (pw.j1 <= pw.j0) continue;
-                if (queries > 0 && !mbar_wait(&s.q_free, (queries - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const int tiles = cnt > a.tile_tok ? 2 : 1;
-                mbar_arrive_expect_tx(&s.q_full, tiles * a.tile_rows * D * 2);
-                for (int i = 0; i < tiles; ++i)
-                    for (int p = 0; p < C::kPanels; ++p)
-                        tma_load(q_s + i * C::kTile + p * C::kPanel, &a.q_map, p * 64, h * a.grp, row0 + i * a.tile_tok, &s.q_full);
-                ++queries;
+                if (queries > 0)
+                    for (int i = 0; i < (cnt > a.tile_tok ? 2 : 1); ++i)
+                        for (int p = 0; p < C::kPanels; ++p) tma_prefetch(&a.q_map, p * 64, h * a.grp, row0 + i * a.tile_tok);
+                copy_queries();
+                q_row = row0;
+                q_cnt = cnt;
+                q_head = h;
+                if (queries == 0) copy_queries();
             }
+            if (ok) copy_queries();
             if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
-            if (queries > 0 && !mbar_wait(&s.q_full, (queries - 1) & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
+            for (int q = max(queries - C::kQ, 0); q < queries; ++q)  // no copy may be in flight at the end
+                if (!mbar_wait(&s.q_full[q % C::kQ], q / C::kQ & 1)) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
             if (a.cut) {
                 a.ws_meta[2 * blockIdx.x] = make_int4(begun, head, row0, cnt);
                 a.ws_meta[2 * blockIdx.x + 1] = make_int4(h, 0, 0, 0);
@@ -724,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         const uint64_t qd = umma_desc(q_s, 16, 1024), kd = umma_desc(kv_s, 16, 1024), vd = umma_desc(kv_s, C::kPanel, 1024);
         const uint32_t on = elect_lane();
         int st = 0, ph = 0;          // stage and phase of the next K or V block that is waited for
-        int qn = 0;                  // pieces with blocks
+        int qn = 0, qs = 0;          // pieces with blocks, where the queries of this one lie
         int pn0 = 0, pn1 = 0;        // P blocks of each tile
         int on0 = 0, on1 = 0;        // pieces with a product of each tile
         auto wait_block = [&](int& at) {  // the next K or V block
@@ -737,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             tc_fence_after();
         };
         auto qk = [&](int i, int at) {
-            const uint64_t aq = qd + static_cast<uint64_t>((i * C::kTile) >> 4), bk = kd + static_cast<uint64_t>((at * C::kTile) >> 4);
+            const uint64_t aq = qd + static_cast<uint64_t>(((2 * qs + i) * C::kTile) >> 4), bk = kd + static_cast<uint64_t>((at * C::kTile) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kPanel + (k & 3) * 32) >> 4);
@@ -762,7 +793,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             __syncwarp();
             if (pc.j1 <= pc.j0) continue;
             const TileView v0(a, pc, 0), v1(a, pc, 1);
-            ok = warp_wait(&s.q_full, qn++ & 1);
+            qs = qn % C::kQ;
+            ok = warp_wait(&s.q_full[qs], qn++ / C::kQ & 1);
             if (!ok) break;
             int kst = 0, vst = 0;
             wait_block(kst);
@@ -773,7 +805,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             if (a0) qk(0, kst);
             if (a1) qk(1, kst);
             umma_done(on, &s.used[kst]);
-            if (pc.j1 - pc.j0 == 1) umma_done(on, &s.q_free);
+            if (pc.j1 - pc.j0 == 1) umma_done(on, &s.q_free[qs]);
             for (int j = pc.j0; j < pc.j1; ++j) {
                 const bool more = j + 1 < pc.j1;
                 t = more ? pc.block(j + 1) * kPreBlock : 0;
@@ -805,7 +837,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 if (more) {
                     if (n1) qk(1, kst);
                     umma_done(on, &s.used[kst]);
-                    if (j + 2 == pc.j1) umma_done(on, &s.q_free);
+                    if (j + 2 == pc.j1) umma_done(on, &s.q_free[qs]);
                 }
                 a0 = n0;
                 a1 = n1;
@@ -843,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     };
                     const uint32_t dst = kv_s + st * C::kTile;
                     if constexpr (!C::kCodes) {
-                        if (plane == 1 && !all) {
+                        if ((plane == 1 || kCap) && !all) {  // (K too where its products choose the cap's formula)
                             // two rows at a time, a 16-byte chunk a lane (the swizzle only permutes a row's chunks)
                             constexpr int kChunks = D / 8;  // chunks of a row
                             for (int i = lane; i < kPreBlock * kChunks; i += 32) {
@@ -893,7 +925,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         };
                         using Yes = std::true_type;
                         using No = std::false_type;
-                        if (plane == 1 && !all)
+                        if ((plane == 1 || kCap) && !all)
                             widen(No{}, Yes{});
                         else if (scaled)  // (K's codes by 1: one loop for both planes stays in the instruction cache)
                             widen(Yes{}, Yes{});
@@ -1139,6 +1171,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             const long long prow = (2LL * blockIdx.x + (j0 > 0 ? 0 : 1)) * kPreSlotRows + i * kPreTile + r;
             __syncwarp();
             if (lane == 0) piece_done(n);
+            const bool wide = (reinterpret_cast<uintptr_t>(part ? static_cast<void*>(a.ws_o) : a.out) & 31) == 0;
             // sum == 0: no visible key (a NaN goes through to the output)
             const float f = part ? a.out_scale : sum == 0.f ? 0.f : a.out_scale / sum;
             if (row) {
@@ -1167,7 +1200,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         uint32_t v[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[q + e]) * f);
-                        st_global32(op + q, v);
+                        st_global32(op + q, v, wide);
                     }
                 } else {
                     __nv_bfloat16* op = a.out + orow * D + k;
@@ -1177,7 +1210,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             v[e] = pack_bf16x2(__uint_as_float(o[q + 2 * e]) * f, __uint_as_float(o[q + 2 * e + 1]) * f);
-                        st_global32(op + q, v);
+                        st_global32(op + q, v, wide);
                     }
                 }
             }
