@@ -70,7 +70,7 @@ struct Piece {
 };
 constexpr int kPieces = 4;  // described ahead
 
-struct Shared {
+struct alignas(16) Shared {  // (what follows it is read 16 bytes at a time)
     uint64_t kv_full[8];   // copies landed (a raw stage's for codes)
     uint64_t kv_free[8];   // codes: read by the helpers; bf16: see ready / used
     uint64_t ready[8];     // a bf16 stage may be multiplied
@@ -84,13 +84,16 @@ struct Shared {
     uint32_t tmem;
     Piece piece[kPieces];
     uint32_t valid[16];      // 16-token groups of a block that were copied
-    alignas(16) float scale[16][2][8];  // their K and V scales
+};
+// What block-scaled caches have beside: K and V scales of the groups.
+struct alignas(16) Extra {
+    float scale[16][2][8];
 };
 
 template <int D, int KIND>
 constexpr int smem_bytes() {
     using C = Cfg<D, KIND>;
-    return 2 * C::kQ * C::kTile + C::kStages * C::kTile + C::kRawStages * C::kRaw + 1024 + static_cast<int>(sizeof(Shared));
+    return (2 * C::kQ + C::kStages) * C::kTile + C::kRawStages * C::kRaw + static_cast<int>(sizeof(Shared) + (C::kCodes ? sizeof(Extra) : 0));
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
@@ -527,8 +530,7 @@ __device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, fl
     }
 }
 
-// 32 bytes, in one store where `wide` says that they are aligned to it (rows lie
-// apart, so that a warp's store takes a cycle for each lane whatever its width).
+// 32 bytes, in one store where `wide` says that they are aligned to it.
 __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8], bool wide) {
     if (wide) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -537,6 +539,81 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8], boo
     } else {
         reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// Four lanes' rows of 128 bytes, v[8 u ..] the 32 bytes u of the lane's own row: after
+// it v[8 j ..] are bytes 32 q .. of row j of the four, q = lane % 4.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[32]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+    for (int u = 0; u < 4; u += 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t x = v[8 * u + e], y = v[8 * u + 8 + e];
+            const uint32_t z = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+            v[8 * u + e] = odd ? z : x;
+            v[8 * u + 8 + e] = odd ? y : z;
+        }
+    // now pairs of rows: v[0 ..], v[8 ..] bytes 32 (q & 1) .., v[16 ..], v[24 ..] bytes 64 + 32 (q & 1) ..
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const uint32_t x = v[e], y = v[16 + e];
+        const uint32_t z = __shfl_xor_sync(0xffffffffu, high ? x : y, 2);
+        v[e] = high ? z : x;
+        v[16 + e] = high ? y : z;
+    }
+}
+
+// A row's D columns of O (at TMEM o_at) times f: bf16 to row orow of out, or a
+// partial's fp32 to row prow; row < 0: nowhere.  f == 0: zeros, whatever O holds.
+// The whole warp calls it.  Four lanes write whole lines of their rows in turn: what
+// bounds the stores is their number of requests (32 bytes of 32 rows a store took
+// 4500 cycles a tile).  (Four warps of their own for it kept the next cell's first
+// products waiting longer than the softmax did: 148 and 168 us, by rows and by lines,
+// where this takes 137, six prompts with a window of 1024.)
+template <int D>
+__device__ __forceinline__ void write_rows(const PreArgs& a, uint32_t o_at, bool part, float f, long long row) {
+    const int q = threadIdx.x & 3;
+    const bool wide = (reinterpret_cast<uintptr_t>(part ? static_cast<void*>(a.ws_o) : a.out) & 31) == 0;
+    long long to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) to[j] = __shfl_sync(0xffffffffu, row, (threadIdx.x & 28) + j);
+    if (part) {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_at + k, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
+            transpose4(o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t v[8] = {o[8 * j], o[8 * j + 1], o[8 * j + 2], o[8 * j + 3], o[8 * j + 4], o[8 * j + 5], o[8 * j + 6], o[8 * j + 7]};
+                if (to[j] >= 0) st_global32(a.ws_o + to[j] * D + k + 8 * q, v, wide);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 64) {
+            uint32_t v[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[32];
+                tmem_ld32(o_at + k + 32 * h, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[16 * h + e] = f == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+            }
+            transpose4(v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w[8] = {v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3], v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+                if (to[j] >= 0) st_global32(a.out + to[j] * D + k + 16 * q, w, wide);
+            }
+        }
     }
 }
 
@@ -549,10 +626,10 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8], boo
 template <int D, int KIND, int MODE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
     using C = Cfg<D, KIND>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t q_s = smem_u32(smem), kv_s = q_s + 2 * C::kQ * C::kTile, raw_s = kv_s + C::kStages * C::kTile;
     Shared& s = *reinterpret_cast<Shared*>(smem + (2 * C::kQ + C::kStages) * C::kTile + C::kRawStages * C::kRaw);
+    Extra& ex = *reinterpret_cast<Extra*>(&s + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool scaled = C::kCodes && MODE != kPlain && a.kv_scales != nullptr;
     constexpr bool kCap = MODE == kCapped || MODE == kBoth, kBias = MODE == kBiased || MODE == kBoth;
@@ -573,7 +650,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 128);
             mbar_init(&s.o_done[i], 1);
-            mbar_init(&s.o_free[i], 128);
+            mbar_init(&s.o_free[i], 4);
+
         }
         mbar_init(&s.drain, 1);
         for (int i = 0; i < kPieces; ++i) {
@@ -669,11 +747,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     }
                     if (scaled && lane < 8) {
                         if (g_id >= 0) {
-                            cp_async_4(&s.scale[slot][plane][lane],
+                            cp_async_4(&ex.scale[slot][plane][lane],
                                        a.kv_scales + (static_cast<long long>(g_id * 2 + plane) * a.scale_groups + a.scale_div(g_off)) * a.Hkv + pc.h);
                             cp_async_arrive(&s.kv_full[st]);
                         } else {
-                            s.scale[slot][plane][lane] = 0.f;
+                            ex.scale[slot][plane][lane] = 0.f;
                             mbar_arrive(&s.kv_full[st]);
                         }
                     }
@@ -899,7 +977,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                     const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
                                     const bool use = decltype(whole)::value || seen(r);
                                     c[u] = use ? ld_shared16(src + at) : make_uint4(0, 0, 0, 0);
-                                    f[u] = decltype(times)::value && use && scaled && plane == 1 ? s.scale[slot][1][r >> 4] : 1.f;
+                                    f[u] = decltype(times)::value && use && scaled && plane == 1 ? ex.scale[slot][1][r >> 4] : 1.f;
                                 }
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
@@ -987,11 +1065,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 uint32_t x[4][32];
                 float4 ks[2] = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
                 if (scaled && !kCap) {
-                    ks[0] = *reinterpret_cast<const float4*>(&s.scale[kvb % C::kInfo][0][0]);
-                    ks[1] = *reinterpret_cast<const float4*>(&s.scale[kvb % C::kInfo][0][4]);
+                    ks[0] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][0]);
+                    ks[1] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][4]);
                 }
                 auto scales = [&](int k) {  // of the two groups of chunk k (with a cap from shared memory: registers)
-                    if (kCap && scaled) return make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]);
+                    if (kCap && scaled) return make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]);
                     return k & 1 ? make_float2(ks[k >> 1].z, ks[k >> 1].w) : make_float2(ks[k >> 1].x, ks[k >> 1].y);
                 };
 #pragma unroll
@@ -1052,7 +1130,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         uint32_t y[32];
                         tmem_ld32(my_s + 32 * k, y);
                         tmem_wait_ld();
-                        shape_any(a, y, scaled ? make_float2(s.scale[kvb % C::kInfo][0][2 * k], s.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
+                        shape_any(a, y, scaled ? make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
                         mx = fmaxf(mx, chunk_max(y));
                         tmem_st32(my_s + 32 * k, y);
                     }
@@ -1155,25 +1233,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 ++nact;
             }
             if (!ok) break;
-            if (nact > 0) {
-                if (!warp_wait(&s.o_done[i], (sn - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-            }
             // ---- the piece's result
             const float sum = l[0].x + l[0].y + l[1].x + l[1].y;
             const int j0 = pc->j0;
             const bool part = j0 > 0 || j1 < pc->nt;
-            const int token = pc->row0 + i * a.tile_tok + tk;
-            const long long orow = static_cast<long long>(token) * a.Hq + pc->h * a.grp + g;
+            const long long orow = static_cast<long long>(pc->row0 + i * a.tile_tok + tk) * a.Hq + pc->h * a.grp + g;
             const long long prow = (2LL * blockIdx.x + (j0 > 0 ? 0 : 1)) * kPreSlotRows + i * kPreTile + r;
-            __syncwarp();
-            if (lane == 0) piece_done(n);
-            const bool wide = (reinterpret_cast<uintptr_t>(part ? static_cast<void*>(a.ws_o) : a.out) & 31) == 0;
             // sum == 0: no visible key (a NaN goes through to the output)
-            const float f = part ? a.out_scale : sum == 0.f ? 0.f : a.out_scale / sum;
+            const float f = sum == 0.f ? 0.f : part ? a.out_scale : a.out_scale / sum;
             if (row) {
                 if (part) {
                     *reinterpret_cast<float2*>(a.ws_ml + 2 * prow) = make_float2(sum == 0.f ? -INFINITY : m, sum);
@@ -1181,42 +1248,18 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     a.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
                 }
             }
-#pragma unroll
-            for (int k = 0; k < D; k += 32) {
-                uint32_t o[32];
-                if (nact > 0) {
-                    tmem_ld32(my_o + k, o);
-                    tmem_wait_ld();
-                }
-                if (nact == 0 || sum == 0.f) {  // (O may hold anything)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-                if (!row) continue;
-                if (part) {
-                    float* op = a.ws_o + prow * D + k;
-#pragma unroll
-                    for (int q = 0; q < 32; q += 8) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[q + e]) * f);
-                        st_global32(op + q, v, wide);
-                    }
-                } else {
-                    __nv_bfloat16* op = a.out + orow * D + k;
-#pragma unroll
-                    for (int q = 0; q < 32; q += 16) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = pack_bf16x2(__uint_as_float(o[q + 2 * e]) * f, __uint_as_float(o[q + 2 * e + 1]) * f);
-                        st_global32(op + q, v, wide);
-                    }
-                }
+            if (nact > 0 && !warp_wait(&s.o_done[i], (sn - 1) & 1)) {
+                ok = false;
+                break;
             }
+            tc_fence_after();
+            write_rows<D>(a, my_o, part, f, !row ? -1 : part ? prow : orow);
+            __syncwarp();
+            if (lane == 0) piece_done(n);
             if (nact > 0) {
                 tc_fence_before();
-                mbar_arrive(&s.o_free[i]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.o_free[i]);
             }
         }
         if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
