@@ -628,8 +628,7 @@ size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_s
  *   q          bf16 [num_tokens, num_q_heads, head_size], with a token stride in
  *              elements (a multiple of 8, at least a token's row).
  *   kv_cache, kv_scales, scale_block, kv_dtype, k_scale, v_scale  as for
- *              gqa_window_decode; the query stays bf16 whatever the cache, values of
- *              block-scaled caches (scale * code) are rounded to bf16.
+ *              gqa_window_decode; the query stays bf16 whatever the cache.
  *   query_start int32 [batch + 1], ascending, at most num_tokens.
  *   prefix_lens int32 [batch] or NULL; taken within [0, seq_lens[b]].
  *   softcap, slopes, window, sinks  as for gqa_score_decode.

@@ -107,8 +107,8 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     a.sl2 = scale * (per_tensor ? k_scale : 1.f) * mqa::kLog2e;
     a.out_scale = per_tensor ? v_scale : 1.f;
     a.cap2 = softcap * mqa::kLog2e;
-    for (int k = 0; k < 6; ++k) a.tanh_c[k] = a.cap2 * mqa::kTanh[k];
-    for (int k = 0; k < 5; ++k) a.tanh_near[k] = a.cap2 * mqa::kTanhNear[k];
+    for (int k = 0; k < mqa::kTanhTerms; ++k) a.tanh_c[k] = a.cap2 * mqa::kTanh[k];
+    for (int k = 0; k < mqa::kTanhNearTerms; ++k) a.tanh_near[k] = a.cap2 * mqa::kTanhNear[k];
     a.inv_cap2 = softcap > 0.f ? 1.f / a.cap2 : 0.f;
     a.num_tokens = num_tokens;
     a.batch = batch;
@@ -132,7 +132,7 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     a.cell_cost = 3;
     const double unit = softcap > 0.f ? static_cast<double>(a.sl2) * a.inv_cap2 : 0.0;
     double power = unit;
-    for (int k = 0; k < 5; ++k, power *= unit * unit) a.tanh_raw[k] = static_cast<float>(a.cap2 * mqa::kTanhNear[k] * power);
+    for (int k = 0; k < mqa::kTanhNearTerms; ++k, power *= unit * unit) a.tanh_raw[k] = static_cast<float>(a.cap2 * mqa::kTanhNear[k] * power);
     a.tiny_unit = std::fabs(unit) < 1e-4 || std::fabs(unit) > 1.0;
     a.grid = grid;
     a.cut = num_kv_splits > 1;

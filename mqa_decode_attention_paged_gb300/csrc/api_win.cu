@@ -164,7 +164,7 @@ mqa_status decode(const void* q, const void* kv_cache, const float* kv_scales, c
     a.sl2 = scale * (per_tensor ? k_scale : 1.0f) * mqa::kLog2e;
     a.out_scale = per_tensor ? v_scale : 1.0f;
     a.cap2 = softcap * mqa::kLog2e;
-    for (int k = 0; k < 6; ++k) a.tanh_c[k] = a.cap2 * mqa::kTanh[k];
+    for (int k = 0; k < mqa::kTanhTerms; ++k) a.tanh_c[k] = a.cap2 * mqa::kTanh[k];
     a.inv_cap2 = softcap > 0.f ? 1.f / a.cap2 : 0.f;
     a.slopes = slopes;
     a.batch = batch;

@@ -42,8 +42,8 @@ struct PreArgs {
     float sl2;               // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
     float out_scale;         // v_scale of a per-tensor e4m3 cache, else 1
     float cap2, inv_cap2;    // softcap * log2(e) and its reciprocal, or 0
-    float tanh_c[6], tanh_near[5];  // cap2 times kTanh and kTanhNear
-    float tanh_raw[5];              // the latter in products: coefficient k times (sl2 / cap2)^(2 k + 1)
+    float tanh_c[kTanhTerms], tanh_near[kTanhNearTerms];  // cap2 times kTanh and kTanhNear
+    float tanh_raw[kTanhNearTerms];             // the latter in products: coefficient k times (sl2 / cap2)^(2 k + 1)
     bool tiny_unit;                 // .. where these leave the fp32 range
     int num_tokens, batch, Hq, Hkv, grp;
     int tile_tok, tile_rows;  // tokens and rows of a tile: rows = tokens * grp <= 128

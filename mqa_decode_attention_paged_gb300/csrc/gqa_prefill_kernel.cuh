@@ -26,8 +26,8 @@
 // more than 8 (P stays below 2^8, sums are fp32), so O is rarely rescaled, and
 // the tile's own softmax warps do that.  P is rounded to bf16 for the tensor
 // cores, the denominator sums the unrounded values.  8-bit codes widen to bf16
-// exactly; K scales multiply the logits, V values code * s_v are rounded to
-// bf16 once, as an output is.
+// exactly; K scales multiply the logits, V scales the numerators before they are
+// rounded.
 #pragma once
 
 #include <atomic>
@@ -517,15 +517,18 @@ __device__ __forceinline__ void shape_any(const PreArgs& a, uint32_t (&x)[32], f
 }
 
 // P of 32 keys as bf16 pairs from x f + add, a scale f for each 16 of them, and +
-// slope2 e for key e if BIAS.  Their sum is added to l.
-template <bool BIAS>
-__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float add, float slope2, float2 (&l)[2], uint32_t (&p)[16]) {
+// slope2 e for key e if BIAS.  Their sum is added to l; with TIMES P is multiplied
+// by V's scales v of the two groups after that (codes are V's operand then, so that
+// there is one rounding, of P v: bf16 has the range of any scale).
+template <bool BIAS, bool TIMES>
+__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float add, float slope2, float2 v, float2 (&l)[2], uint32_t (&p)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         float2 y = fma2(get2(x, 2 * k), both(k < 8 ? f.x : f.y), both(add));
         if (BIAS) y = make_float2(fmaf(slope2, 2.f * k, y.x), fmaf(slope2, 2.f * k + 1.f, y.y));
-        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        float2 e = make_float2(ex2(y.x), ex2(y.y));
         l[k & 1] = add2(l[k & 1], e);
+        if (TIMES) e = mul2(e, both(k < 8 ? v.x : v.y));
         p[k] = pack_bf16x2(e.x, e.y);
     }
 }
@@ -619,7 +622,7 @@ __device__ __forceinline__ void write_rows(const PreArgs& a, uint32_t o_at, bool
 
 // MODE: kPlain (one positive scale), kScaled (non-negative scales of token blocks),
 // kCapped, kBiased (slopes, or a scale <= 0), kBoth.  All keep a row's 128 products
-// in registers; what is rare (a logit beyond 0.75 of its cap, keys behind the query,
+// in registers; what is rare (a product beyond 0.6 of its cap, keys behind the query,
 // steep biases, scales <= 0) is shaped in a loop of its own through TMEM, so that
 // the code that runs stays short: with every case in line a capped prompt of 15999
 // tokens took 3509 us, a biased one 3728, a third of it waits for instructions.
@@ -633,6 +636,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool scaled = C::kCodes && MODE != kPlain && a.kv_scales != nullptr;
     constexpr bool kCap = MODE == kCapped || MODE == kBoth, kBias = MODE == kBiased || MODE == kBoth;
+    constexpr bool kTimes = C::kCodes && MODE != kPlain;
     constexpr int kCopyStages = C::kCodes ? C::kRawStages : C::kStages;
 
     if (threadIdx.x == 0) {
@@ -746,12 +750,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         }
                     }
                     if (scaled && lane < 8) {
-                        if (g_id >= 0) {
-                            cp_async_4(&ex.scale[slot][plane][lane],
-                                       a.kv_scales + (static_cast<long long>(g_id * 2 + plane) * a.scale_groups + a.scale_div(g_off)) * a.Hkv + pc.h);
+                        // (V's with K's: the softmax wants both)
+                        if (plane == 0 && g_id >= 0) {
+                            const float* from = a.kv_scales + (static_cast<long long>(g_id * 2) * a.scale_groups + a.scale_div(g_off)) * a.Hkv + pc.h;
+                            cp_async_4(&ex.scale[slot][0][lane], from);
+                            cp_async_4(&ex.scale[slot][1][lane], from + a.scale_groups * a.Hkv);
                             cp_async_arrive(&s.kv_full[st]);
                         } else {
-                            ex.scale[slot][plane][lane] = 0.f;
+                            if (plane == 0) ex.scale[slot][0][lane] = ex.scale[slot][1][lane] = 0.f;
                             mbar_arrive(&s.kv_full[st]);
                         }
                     }
@@ -966,18 +972,15 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one; four at a time
                         constexpr int kQ4 = D / 64, kUnits = kPreBlock / 8 * kQ4 / C::kHelpers;
                         const uint32_t src = raw_s + rst * C::kRaw;
-                        auto widen = [&](auto whole, auto times) {
+                        auto widen = [&](auto whole) {
 #pragma unroll 1
                             for (int u0 = 0; u0 < kUnits; u0 += 4) {
                                 uint4 c[4];
-                                float f[4];
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
                                     const int i = (u0 + u) * C::kHelpers + w, r = i / kQ4 * 8 + (lane & 7), q = i % kQ4 * 4 + (lane >> 3);
                                     const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
-                                    const bool use = decltype(whole)::value || seen(r);
-                                    c[u] = use ? ld_shared16(src + at) : make_uint4(0, 0, 0, 0);
-                                    f[u] = decltype(times)::value && use && scaled && plane == 1 ? ex.scale[slot][1][r >> 4] : 1.f;
+                                    c[u] = decltype(whole)::value || seen(r) ? ld_shared16(src + at) : make_uint4(0, 0, 0, 0);
                                 }
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
@@ -986,11 +989,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                     uint32_t o[8];
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) {
-                                        float2 x = code_pair<KIND, 0>(in[k]), y = code_pair<KIND, 1>(in[k]);
-                                        if constexpr (decltype(times)::value) {
-                                            x = mul2(x, both(f[u]));
-                                            y = mul2(y, both(f[u]));
-                                        }
+                                        const float2 x = code_pair<KIND, 0>(in[k]), y = code_pair<KIND, 1>(in[k]);
                                         o[2 * k] = pack_bf16x2(x.x, x.y);
                                         o[2 * k + 1] = pack_bf16x2(y.x, y.y);
                                     }
@@ -1001,14 +1000,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                 }
                             }
                         };
-                        using Yes = std::true_type;
-                        using No = std::false_type;
                         if ((plane == 1 || kCap) && !all)
-                            widen(No{}, Yes{});
-                        else if (scaled)  // (K's codes by 1: one loop for both planes stays in the instruction cache)
-                            widen(Yes{}, Yes{});
+                            widen(std::false_type{});
                         else
-                            widen(Yes{}, No{});
+                            widen(std::true_type{});
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
@@ -1075,6 +1070,20 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 tmem_wait_ld();
+                // V's scales of the two groups of chunk k; 1 where there are none, 0 where no key of a group is seen by the row
+                // (an Inf or NaN scale reaches the rows that see a key of it)
+                auto v_scales = [&](int k) {
+                    float2 v = both(1.f);
+                    if (kTimes && scaled) {
+                        v = *reinterpret_cast<const float2*>(&ex.scale[kvb % C::kInfo][1][2 * k]);
+                        if (edge) {
+                            const uint32_t bits = seen(k);
+                            if (!(bits & 0xffffu)) v.x = 0.f;
+                            if (!(bits >> 16)) v.y = 0.f;
+                        }
+                    }
+                    return v;
+                };
                 // The row's reference after a block whose largest logit is mx (or less); false if a wait ran out.
                 auto refer = [&](float mx) {
                     const bool move = mx > m + 8.f;
@@ -1116,7 +1125,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         size = max3(size, wide[0] * f.x, wide[1] * f.y);
                     }
                     size *= fabsf(a.sl2) * a.inv_cap2;  // (a NaN passes the comparisons of the others and stays one)
-                    rare = a.tiny_unit || __any_sync(0xffffffffu, row && size > 0.75f);
+                    rare = a.tiny_unit || __any_sync(0xffffffffu, row && size > 0.6f);
                     mid = !__any_sync(0xffffffffu, row && size > 1.f);
                 }
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
@@ -1141,7 +1150,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         uint32_t y[32], o[16];
                         tmem_ld32(my_s + 32 * k, y);
                         tmem_wait_ld();
-                        numerators<false>(y, both(1.f), -m, 0.f, l, o);
+                        numerators<false, kTimes>(y, both(1.f), -m, 0.f, v_scales(k), l, o);
                         tmem_st16(my_s + 16 * k, o);
                     }
                 } else {
@@ -1221,7 +1230,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         // slope2 d (a row sees its own key at distance 0, beside which the rounding
                         // of a far key's bias is nothing).
                         const float add = kBias ? fmaf(-slope2, static_cast<float>(p - t0 - 32 * k), -m) : -m;
-                        numerators<kBias>(x[k], f, add, slope2, l, o);
+                        numerators<kBias, kTimes>(x[k], f, add, slope2, v_scales(k), l, o);
                         tmem_st16(my_s + 16 * k, o);
                     }
                 }

@@ -44,10 +44,12 @@ struct FastDiv {
 
 // Caps of logits, in base 2: cap2 tanh(x / cap2).
 // tanh(y) / y: c0 + c1 y^2 + .., coefficients of least squares towards the smallest
-// absolute error of tanh.  kTanh for |y| <= 1: 2.4e-7 (of logits capped at 50: 1.7e-5
-// in base 2, far below the 2^-9 of P's rounding); kTanhNear for |y| <= 0.75: 1.9e-7.
-constexpr float kTanh[6] = {0.9999968409f, -0.3332400322f, 0.1325352489f, -0.05097286030f, 0.01611417904f, -0.002839464694f};
-constexpr float kTanhNear[5] = {0.9999971986f, -0.3332307637f, 0.1322609186f, -0.04928044975f, 0.01231883466f};
+// absolute error of tanh, 2e-8 (of logits capped at 50: 1.4e-6 in base 2): kTanh for
+// |y| <= 1, kTanhNear for |y| <= 0.6.
+constexpr int kTanhTerms = 7, kTanhNearTerms = 5;
+constexpr float kTanh[kTanhTerms] = {0.9999997020f,   -0.3333213031f, 0.1331958324f, -0.05326583609f,
+                                     0.01997328177f, -0.005951280240f, 0.0009637721814f};
+constexpr float kTanhNear[kTanhNearTerms] = {0.9999996424f, -0.3333120942f, 0.1329921037f, -0.05169674382f, 0.01497695968f};
 
 struct WinArgs {
     CUtensorMap tmap;  // {line, rows (block, plane, token), panels, heads}
@@ -64,7 +66,7 @@ struct WinArgs {
     float sl2;        // scale * log2(e) (times k_scale of a per-tensor e4m3 cache)
     float out_scale;  // v_scale of a per-tensor e4m3 cache, else 1
     float cap2, inv_cap2;  // softcap * log2(e) and its reciprocal, or 0 (shaped logits only, like the next)
-    float tanh_c[6];       // cap2 times kTanh
+    float tanh_c[kTanhTerms];  // cap2 times kTanh
     const float* slopes;   // [Hq], or null
     int batch, q_len, Hq, Hkv, grp, rows;  // rows = q_len * grp: query rows of a KV head
     int num_blocks, page, max_blocks;
@@ -82,7 +84,7 @@ struct WinArgs {
 
 // cap2 tanh(y) for |y| > 1: 1 - 2 / (1 + e^{2y}) (infinities become +-cap2, a NaN
 // stays one).  Its error is absolute, 2^-23 of the cap: near 0 the polynomial's is
-// relative, 2^-18 of the logit, which is what a cap far above the logits needs.
+// relative, 2^-21 of the logit, which is what a cap far above the logits needs.
 __device__ __forceinline__ float tanh_far(float cap2, float y) {
     return cap2 - __fdividef(2.f * cap2, 1.f + ex2(2.f * kLog2e * y));
 }

@@ -283,9 +283,9 @@ constexpr int kSteps2 = 22;  // bits 22 + 2j: scales from the box's first to tha
 // A base-2 logit x capped.
 __device__ __forceinline__ float capped(const WinArgs& a, float x) {
     const float y = x * a.inv_cap2, z = y * y;
-    float w = a.tanh_c[5];
+    float w = a.tanh_c[kTanhTerms - 1];
 #pragma unroll
-    for (int k = 4; k >= 0; --k) w = fmaf(w, z, a.tanh_c[k]);
+    for (int k = kTanhTerms - 2; k >= 0; --k) w = fmaf(w, z, a.tanh_c[k]);
     return fabsf(y) <= 1.f ? y * w : tanh_far(a.cap2, y);
 }
 
