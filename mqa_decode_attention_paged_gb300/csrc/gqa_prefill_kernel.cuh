@@ -545,6 +545,20 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8], boo
     }
 }
 
+// O's columns of a warp's rows times f.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t o_at, float f) {
+#pragma unroll 1
+    for (int k = 0; k < D; k += 16) {
+        uint32_t o[16];
+        tmem_ld16(o_at + k, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st16(o_at + k, o);
+    }
+}
+
 // Four lanes' rows of 128 bytes, v[8 u ..] the 32 bytes u of the lane's own row: after
 // it v[8 j ..] are bytes 32 q .. of row j of the four, q = lane % 4.
 __device__ __forceinline__ void transpose4(uint32_t (&v)[32]) {
@@ -618,6 +632,59 @@ __device__ __forceinline__ void write_rows(const PreArgs& a, uint32_t o_at, bool
             }
         }
     }
+}
+
+// A row's softmax of one block whatever the shaping, in chunks through TMEM: the
+// logits take S's place, then P theirs (that of chunk k in columns 16 k .. 16 k + 15,
+// of chunks that were read before).  A function of its own, so that its code lies
+// apart from what usually runs.
+struct RareRow {
+    uint32_t s_at, o_at;    // the row's warp's S and O
+    const float* scales;    // [2][8], of K's and V's groups, or null
+    uint32_t seen[4];       // keys that count
+    float slope2;
+    int d;                  // distance of the first key
+    bool mid, rescale;      // as of shape_any; whether O holds anything yet
+    float m, l[2];          // reference and sum, in and out
+    uint64_t* o_done;       // O's last product, and its phase
+    int o_phase;
+    float f;                // out: what other sums of the row are to be multiplied by
+};
+template <int D, bool TIMES>
+__device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t y[32];
+        tmem_ld32(q.s_at + 32 * k, y);
+        tmem_wait_ld();
+        shape_any(a, y, q.scales ? make_float2(q.scales[2 * k], q.scales[2 * k + 1]) : both(1.f), q.mid, q.slope2, q.d - 32 * k, q.seen[k]);
+        mx = fmaxf(mx, chunk_max(y));
+        tmem_st32(q.s_at + 32 * k, y);
+    }
+    tmem_wait_st();
+    const bool move = mx > q.m + 8.f;
+    q.f = move && q.rescale ? ex2(q.m - mx) : 1.f;
+    if (move) q.m = mx;
+    float2 l[2] = {make_float2(q.l[0] * q.f, q.l[1] * q.f), both(0.f)};
+    if (q.rescale && __any_sync(0xffffffffu, move)) {
+        if (!warp_wait(q.o_done, q.o_phase)) return false;
+        tc_fence_after();
+        rescale<D>(q.o_at, q.f);
+    }
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t y[32], o[16];
+        tmem_ld32(q.s_at + 32 * k, y);
+        tmem_wait_ld();
+        float2 v = both(1.f);
+        if (TIMES && q.scales) v = make_float2(q.seen[k] & 0xffffu ? q.scales[8 + 2 * k] : 0.f, q.seen[k] >> 16 ? q.scales[8 + 2 * k + 1] : 0.f);
+        numerators<false, TIMES>(y, both(1.f), -q.m, 0.f, v, l, o);
+        tmem_st16(q.s_at + 16 * k, o);
+    }
+    q.l[0] = l[0].x + l[1].x;
+    q.l[1] = l[0].y + l[1].y;
+    return true;
 }
 
 // MODE: kPlain (one positive scale), kScaled (non-negative scales of token blocks),
@@ -1100,15 +1167,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         // the product before must be in O
                         if (!warp_wait(&s.o_done[i], (sn - 1) & 1)) return false;
                         tc_fence_after();
-#pragma unroll 1
-                        for (int k = 0; k < D; k += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(my_o + k, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(my_o + k, o);
-                        }
+                        rescale<D>(my_o, f);
                     }
                     return true;
                 };
@@ -1131,28 +1190,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
                 if constexpr (kCap || kBias) rare |= !(a.sl2 > 0.f);
                 if (__builtin_expect(rare, 0)) {
-                    // in chunks through TMEM: the logits take S's place, then P theirs (that of
-                    // chunk k in columns 16 k .. 16 k + 15, of chunks that were read before)
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t y[32];
-                        tmem_ld32(my_s + 32 * k, y);
-                        tmem_wait_ld();
-                        shape_any(a, y, scaled ? make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]) : both(1.f), mid, slope2, p - t0 - 32 * k, edge ? seen(k) : 0xffffffffu);
-                        mx = fmaxf(mx, chunk_max(y));
-                        tmem_st32(my_s + 32 * k, y);
-                    }
-                    tmem_wait_st();
-                    ok = refer(mx);
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t y[32], o[16];
-                        tmem_ld32(my_s + 32 * k, y);
-                        tmem_wait_ld();
-                        numerators<false, kTimes>(y, both(1.f), -m, 0.f, v_scales(k), l, o);
-                        tmem_st16(my_s + 16 * k, o);
-                    }
+                    RareRow q = {my_s, my_o, scaled ? &ex.scale[kvb % C::kInfo][0][0] : nullptr, {0, 0, 0, 0}, slope2, p - t0, mid, nact > 0, m,
+                                 {l[0].x, l[0].y}, &s.o_done[i], (sn - 1) & 1};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q.seen[k] = edge ? seen(k) : 0xffffffffu;
+                    ok = rare_row<D, kTimes>(a, q);
+                    m = q.m;
+                    l[1] = mul2(l[1], both(q.f));
+                    l[0] = make_float2(q.l[0], q.l[1]);
                 } else {
                     float b[4];
                     if (!kCap && edge) {
