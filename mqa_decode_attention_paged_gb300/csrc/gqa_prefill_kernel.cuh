@@ -634,6 +634,21 @@ __device__ __forceinline__ void write_rows(const PreArgs& a, uint32_t o_at, bool
     }
 }
 
+// -inf in a row's products of keys whose bit is not set (32 to a word).  A function of
+// its own, like rare_row, for the edges of what rows see.
+static __device__ __noinline__ void mask_row(uint32_t s_at, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+    const uint32_t bits[4] = {b0, b1, b2, b3};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t x[32];
+        tmem_ld32(s_at + 32 * k, x);
+        tmem_wait_ld();
+        keep(x, bits[k], -INFINITY);
+        tmem_st32(s_at + 32 * k, x);
+    }
+    tmem_wait_st();
+}
+
 // A row's softmax of one block whatever the shaping, in chunks through TMEM: the
 // logits take S's place, then P theirs (that of chunk k in columns 16 k .. 16 k + 15,
 // of chunks that were read before).  A function of its own, so that its code lies
@@ -1018,6 +1033,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         ok = false;
                         break;
                     }
+                    // (a K scale of 0, whose codes are 0: their products stay 0, and -inf where nothing is seen stays that)
+                    if (scaled && plane == 0 && w == 0 && lane < 8 && ex.scale[slot][0][lane] < 0x1p-100f) ex.scale[slot][0][lane] = 0x1p-100f;
                     const uint32_t groups = s.valid[slot];
                     const bool all = groups == 0xffu && t0 + kPreBlock <= hi && (t0 >= lo || t0 + kPreBlock <= se);
                     auto seen = [&](int r) {
@@ -1130,10 +1147,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     ks[0] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][0]);
                     ks[1] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][4]);
                 }
+                if (scaled && !kCap && __builtin_expect(edge, 0)) {  // those of groups that the row does not see may be anything
+                    const uint32_t b0 = seen(0), b1 = seen(1), b2 = seen(2), b3 = seen(3);
+                    ks[0] = make_float4(b0 & 0xffffu ? ks[0].x : 1.f, b0 >> 16 ? ks[0].y : 1.f, b1 & 0xffffu ? ks[0].z : 1.f, b1 >> 16 ? ks[0].w : 1.f);
+                    ks[1] = make_float4(b2 & 0xffffu ? ks[1].x : 1.f, b2 >> 16 ? ks[1].y : 1.f, b3 & 0xffffu ? ks[1].z : 1.f, b3 >> 16 ? ks[1].w : 1.f);
+                }
                 auto scales = [&](int k) {  // of the two groups of chunk k (with a cap from shared memory: registers)
                     if (kCap && scaled) return make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]);
                     return k & 1 ? make_float2(ks[k >> 1].z, ks[k >> 1].w) : make_float2(ks[k >> 1].x, ks[k >> 1].y);
                 };
+                if (!kCap && __builtin_expect(edge, 0)) mask_row(my_s, seen(0), seen(1), seen(2), seen(3));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 tmem_wait_ld();
@@ -1200,17 +1223,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     l[0] = make_float2(q.l[0], q.l[1]);
                 } else {
                     float b[4];
-                    if (!kCap && edge) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (MODE != kPlain) {  // scaled first: a scale of 0 times -inf is no logit
-                                const float2 f = mul2(scales(k), both(a.sl2));
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
-                            }
-                            keep(x[k], seen(k), -INFINITY);
-                        }
-                    }
                     if (kCap && edge) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -1221,15 +1233,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if constexpr (C::kCodes && MODE != kPlain) {
-                                const float2 f = !kCap && edge ? both(1.f) : scales(k), top = group_max(x[k]);
+                                const float2 f = scales(k), top = group_max(x[k]);
                                 b[k] = fmaxf(top.x * f.x, top.y * f.y);
                             } else {
                                 b[k] = chunk_max(x[k]);
                             }
                         }
                     }
-                    // (of logits, and of products that are not scaled yet; with a cap of what it takes)
-                    const float unit = MODE == kPlain || kCap || !edge ? a.sl2 : 1.f;
                     float mx;
                     if constexpr (kBias) {
                         // Instead of the largest logit a bound of it: the largest product of
@@ -1238,13 +1248,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         const float d = static_cast<float>(p - t0);  // distance of the block's first key
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            b[k] *= unit;
+                            b[k] *= a.sl2;
                             if (kCap && b[k] > -INFINITY) b[k] = b[k] * a.inv_cap2 * tanh_over(a.tanh_near, both(b[k] * a.inv_cap2)).x;
                             b[k] = fmaf(-slope2, fmaxf(0.f, d - (32.f * k + 31.f)), b[k]);
                         }
                         mx = max3(fmaxf(b[0], b[1]), b[2], b[3]);
                     } else {
-                        mx = max3(fmaxf(b[0], b[1]), b[2], b[3]) * unit;
+                        mx = max3(fmaxf(b[0], b[1]), b[2], b[3]) * a.sl2;
                         if (kCap && mx > -INFINITY) mx = mx * a.inv_cap2 * tanh_over(a.tanh_near, both(mx * a.inv_cap2)).x;
                     }
                     ok = refer(mx);
@@ -1269,8 +1279,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         float2 f = both(a.sl2);
                         if constexpr (kCap)
                             f = both(1.f);
-                        else if constexpr (MODE != kPlain)
-                            f = edge ? both(1.f) : C::kCodes ? mul2(scales(k), both(a.sl2)) : f;
+                        else if constexpr (kTimes)
+                            f = mul2(scales(k), both(a.sl2));
                         // With a bias: every key that is seen lies at or before the query, slope2 e -
                         // slope2 d (a row sees its own key at distance 0, beside which the rounding
                         // of a far key's bias is nothing).
