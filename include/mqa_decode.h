@@ -620,10 +620,10 @@ size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_s
  * over the keys seen; out = 0, lse = -inf where there are none.  Rows of
  * tokens outside [query_start[0], query_start[batch]) are padding: not written.
  * Blocks that no new token sees are not read, nor are their block-table
- * entries.  Bytes of tokens that none of the request's new tokens sees never
- * reach a result, whatever they hold, nor do those of other requests; an Inf
- * or NaN among the values of a token that one of them sees may reach all of
- * the request's new tokens.
+ * entries.  Bytes of tokens that a new token does not see never reach its
+ * result, whatever they hold; an Inf or NaN at a key, or in a scale, makes the
+ * results of the queries that see that key, or a key of that scale, undefined
+ * (an Inf or NaN in most cases).
  *
  *   q          bf16 [num_tokens, num_q_heads, head_size], with a token stride in
  *              elements (a multiple of 8, at least a token's row).

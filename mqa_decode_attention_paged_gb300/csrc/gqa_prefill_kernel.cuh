@@ -70,6 +70,20 @@ struct Piece {
 };
 constexpr int kPieces = 4;  // described ahead
 
+// Tokens of a piece whose V row holds an Inf or NaN, in blocks that not every row of
+// the cell sees all of: that row counts as zeros in the products (0 * NaN would reach
+// the rows that do not see it), and the rows that see it become NaN at the end.
+struct BadTokens {
+    int any;  // 1 where a bit below is set, 2 where there was no room for one
+    int first[8];
+    uint32_t bits[8][4];
+    // Row r of the piece's block number e of those looked over.
+    __device__ __forceinline__ void found(int e, int r) {
+        if (e < 8) atomicOr(&bits[e][r >> 5], 1u << (r & 31));
+        atomicOr(&any, e < 8 ? 1 : 2);
+    }
+};
+
 struct alignas(16) Shared {  // (what follows it is read 16 bytes at a time)
     uint64_t kv_full[8];   // copies landed (a raw stage's for codes)
     uint64_t kv_free[8];   // codes: read by the helpers; bf16: see ready / used
@@ -83,6 +97,7 @@ struct alignas(16) Shared {  // (what follows it is read 16 bytes at a time)
     int b[2], u[2], h[2], j[2];  // start and end of the block's share
     uint32_t tmem;
     Piece piece[kPieces];
+    BadTokens bad[kPieces];
     uint32_t valid[16];      // 16-token groups of a block that were copied
 };
 // What block-scaled caches have beside: K and V scales of the groups.
@@ -114,6 +129,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void st_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+// Two bf16 values times zero, added to sum.
+__device__ __forceinline__ uint32_t times_zero(uint32_t v, uint32_t sum) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(sum));
+    return d;
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
     uint4 v;
@@ -634,6 +655,81 @@ __device__ __forceinline__ void write_rows(const PreArgs& a, uint32_t o_at, bool
     }
 }
 
+// A bf16 block's rows at the edges of what the cell sees, by one warp.  If `some`:
+// rows that no row of the cell sees become zeros; if lim < hi: rows that some see and
+// some do not, [lim, hi) and [lo, lo_last), are looked over for an Inf or NaN.
+template <int D>
+__device__ __forceinline__ void edge_rows(BadTokens& bad, int edge, uint32_t dst, uint32_t groups, int t0, int hi, int lo, int se, bool some,
+                                       int lim, int lo_last) {
+    // 16-byte chunks of rows from r0 to r1, a lane each (the swizzle only permutes a row's chunks)
+    constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // chunks of a row, rows at a time
+    const int lane = threadIdx.x & 31, my_row = lane / kChunks;
+    const uint32_t my_at = dst + ((lane % kChunks) >> 3) * (kPreBlock * 128) + (lane & 7) * 16;
+    bool wrote = some;
+    auto clear = [&](int r0, int r1) {
+        for (int r = max(r0, 0) + my_row; r < min(r1, kPreBlock); r += kRows) st_zero16(my_at + r * 128);
+    };
+    if (some) {
+        if (groups == 0xffu) {
+            clear(hi - t0, kPreBlock);
+            clear(se - t0, lo - t0);
+        } else {
+            for (int r = my_row; r < kPreBlock; r += kRows) {
+                const int t = t0 + r;
+                if (!(((groups >> (r >> 4)) & 1u) && t < hi && (t >= lo || t < se))) st_zero16(my_at + r * 128);
+            }
+        }
+        __syncwarp();
+    }
+    auto look = [&](int r0, int r1) {
+        // 0 times an Inf or NaN is a NaN, which stays in the sum
+        uint32_t sum[4] = {0u, 0u, 0u, 0u};
+        r0 = max(r0, 0) + my_row;
+        r1 = min(r1, kPreBlock);
+#pragma unroll 1
+        for (int r = r0; r < r1; r += 4 * kRows) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = r + u * kRows < r1 ? ld_shared16(my_at + (r + u * kRows) * 128) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                sum[0] = times_zero(v[u].x, sum[0]);
+                sum[1] = times_zero(v[u].y, sum[1]);
+                sum[2] = times_zero(v[u].z, sum[2]);
+                sum[3] = times_zero(v[u].w, sum[3]);
+            }
+        }
+        if (!__any_sync(0xffffffffu, (sum[0] | sum[1] | sum[2] | sum[3]) != 0)) return;
+        wrote = true;
+        for (int r = r0; r < r1; r += kRows) {
+            // an exponent of ones in a half of a word carries into its sign
+            auto full = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+            const uint4 v = ld_shared16(my_at + r * 128);
+            if ((full(v.x) | full(v.y) | full(v.z) | full(v.w)) != 0) {
+                bad.found(edge, r);
+                st_zero16(my_at + r * 128);
+            }
+        }
+    };
+    if (lim < INT32_MAX) {
+        look(lim - t0, hi - t0);
+        look(lo - t0, lo_last - t0);
+    }
+    if (wrote) fence_proxy_async_smem();
+}
+
+// NaN where a row that sees t < lim, t >= lo or t < sinks sees one of the tokens, else 0.
+static __device__ __noinline__ float bad_tokens(const BadTokens& bad, int lim, int lo, int sinks) {
+    bool sees = (bad.any & 2) && lim > 0;
+    for (int e = 0; e < 8; ++e)
+        for (int k = 0; k < 4; ++k)
+            for (uint32_t bits = bad.bits[e][k]; bits; bits &= bits - 1) {
+                const int t = bad.first[e] + 32 * k + __ffs(bits) - 1;
+                sees |= t < lim && (t >= lo || t < sinks);
+            }
+    return sees ? NAN : 0.f;
+}
+
 // -inf in a row's products of keys whose bit is not set (32 to a word).  A function of
 // its own, like rare_row, for the edges of what rows see.
 static __device__ __noinline__ void mask_row(uint32_t s_at, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
@@ -887,6 +983,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 }
                 Piece& pc = s.piece[n % kPieces];
                 const PreCell& c = pw.cell;
+                s.bad[n % kPieces] = {};
                 pc = {c.row0, c.cnt, c.p0, c.pre, c.hi, c.lo, c.s_end, c.ns, c.w0, c.nt, pw.j0, pw.j1, pw.b < a.batch ? pw.b : pw.eb, pw.h, more, 0};
                 mbar_arrive(&s.piece_full[n % kPieces]);
                 if (!more) break;
@@ -922,8 +1019,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         const uint32_t on = elect_lane();
         int st = 0, ph = 0;          // stage and phase of the next K or V block that is waited for
         int qn = 0, qs = 0;          // pieces with blocks, where the queries of this one lie
-        int pn0 = 0, pn1 = 0;        // P blocks of each tile
-        int on0 = 0, on1 = 0;        // pieces with a product of each tile
+        uint32_t pn0 = 0, pn1 = 0;   // P blocks of each tile
+        uint32_t on0 = 0, on1 = 0;   // pieces with a product of each tile
         auto wait_block = [&](int& at) {  // the next K or V block
             at = st;
             ok = warp_wait(&s.ready[st], ph);
@@ -962,51 +1059,42 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             qs = qn % C::kQ;
             ok = warp_wait(&s.q_full[qs], qn++ / C::kQ & 1);
             if (!ok) break;
-            int kst = 0, vst = 0;
-            wait_block(kst);
-            if (!ok) break;
-            int t = pc.block(pc.j0) * kPreBlock;
-            bool a0 = v0.active(a, t), a1 = v1.active(a, t);  // tiles that the block has to do with
-            bool begun0 = false, begun1 = false;
-            if (a0) qk(0, kst);
-            if (a1) qk(1, kst);
-            umma_done(on, &s.used[kst]);
-            if (pc.j1 - pc.j0 == 1) umma_done(on, &s.q_free[qs]);
-            for (int j = pc.j0; j < pc.j1; ++j) {
-                const bool more = j + 1 < pc.j1;
-                t = more ? pc.block(j + 1) * kPreBlock : 0;
-                const bool n0 = more && v0.active(a, t), n1 = more && v1.active(a, t);
-                wait_block(vst);  // V of this block
+            uint32_t act = 0, begun = 0;  // tiles that the block has to do with; tiles with a product in this piece
+            // P V of a block and Q K^T of the next one, tile by tile, so that one tile's
+            // softmax runs beside the other's products
+#pragma unroll 1
+            for (int j = pc.j0 - 1; j < pc.j1 && ok; ++j) {
+                const bool have = j >= pc.j0, more = j + 1 < pc.j1;
+                const int t = more ? pc.block(j + 1) * kPreBlock : 0;
+                const uint32_t next = more ? (v0.active(a, t) ? 1u : 0u) | (v1.active(a, t) ? 2u : 0u) : 0u;
+                int kst = 0, vst = 0;
+                if (have) wait_block(vst);
                 if (!ok) break;
-                if (a0) {
-                    ok = warp_wait(&s.p_full[0], pn0++ & 1) && (begun0 || on0 == 0 || warp_wait(&s.o_free[0], (on0 - 1) & 1));
-                    if (!ok) break;
-                    on0 += !begun0;
-                    tc_fence_after();
-                    pv(0, vst, begun0);
-                    begun0 = true;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    if ((act >> i) & 1u) {
+                        const uint32_t pn = i ? pn1++ : pn0++;
+                        ok = warp_wait(&s.p_full[i], pn & 1u);
+                        if (ok && !((begun >> i) & 1u)) {
+                            const uint32_t n_o = i ? on1++ : on0++;
+                            if (n_o > 0) ok = warp_wait(&s.o_free[i], (n_o - 1) & 1u);
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(i, vst, (begun >> i) & 1u);
+                        begun |= 1u << i;
+                    }
+                    if (more) {
+                        if (i == 0) wait_block(kst);
+                        if (!ok) break;
+                        if ((next >> i) & 1u) qk(i, kst);
+                    }
                 }
-                if (more) {
-                    wait_block(kst);  // K of the next one
-                    if (!ok) break;
-                    if (n0) qk(0, kst);
-                }
-                if (a1) {
-                    ok = warp_wait(&s.p_full[1], pn1++ & 1) && (begun1 || on1 == 0 || warp_wait(&s.o_free[1], (on1 - 1) & 1));
-                    if (!ok) break;
-                    on1 += !begun1;
-                    tc_fence_after();
-                    pv(1, vst, begun1);
-                    begun1 = true;
-                }
-                umma_done(on, &s.used[vst]);
-                if (more) {
-                    if (n1) qk(1, kst);
-                    umma_done(on, &s.used[kst]);
-                    if (j + 2 == pc.j1) umma_done(on, &s.q_free[qs]);
-                }
-                a0 = n0;
-                a1 = n1;
+                if (!ok) break;
+                if (have) umma_done(on, &s.used[vst]);
+                if (more) umma_done(on, &s.used[kst]);
+                if (j + 2 == pc.j1) umma_done(on, &s.q_free[qs]);
+                act = next;
             }
         }
         if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
@@ -1022,8 +1110,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             const Piece* pp = piece(n);
             if (!pp) break;
             const Piece pc = *pp;
-            __syncwarp();
-            if (lane == 0) piece_done(n);
+            // what some rows of the cell see and some do not: [lim, hi) and [lo, lo_last)
+            const int lim = pc.p0 < 0 ? 0 : max(pc.p0 + 1, pc.pre), lo_last = pc.p0 + pc.cnt - a.window;
+            BadTokens& bad = s.bad[n % kPieces];
+            int edges = 0;
             for (int j = pc.j0; j < pc.j1 && ok; ++j) {
                 const int t0 = pc.block(j) * kPreBlock, hi = pc.hi, lo = pc.lo, se = pc.s_end;
                 for (int plane = 0; plane < 2; ++plane, ++kvc) {
@@ -1037,21 +1127,22 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     if (scaled && plane == 0 && w == 0 && lane < 8 && ex.scale[slot][0][lane] < 0x1p-100f) ex.scale[slot][0][lane] = 0x1p-100f;
                     const uint32_t groups = s.valid[slot];
                     const bool all = groups == 0xffu && t0 + kPreBlock <= hi && (t0 >= lo || t0 + kPreBlock <= se);
+                    // V rows that not every row of the cell sees are looked over
+                    const bool look = plane == 1 && KIND != kWinInt8 &&
+                                      ((t0 < hi && t0 + kPreBlock > lim && lim < hi) || (t0 < lo_last && t0 + kPreBlock > lo && lo < lo_last));
+                    const int edge = edges;
+                    if (look) {
+                        ++edges;
+                        if (edge < 8 && w == 0 && lane == 0) bad.first[edge] = t0;
+                    }
                     auto seen = [&](int r) {
                         const int t = t0 + r;
                         return ((groups >> (r >> 4)) & 1u) && t < hi && (t >= lo || t < se);
                     };
                     const uint32_t dst = kv_s + st * C::kTile;
                     if constexpr (!C::kCodes) {
-                        if ((plane == 1 || kCap) && !all) {  // (K too where its products choose the cap's formula)
-                            // two rows at a time, a 16-byte chunk a lane (the swizzle only permutes a row's chunks)
-                            constexpr int kChunks = D / 8;  // chunks of a row
-                            for (int i = lane; i < kPreBlock * kChunks; i += 32) {
-                                const int r = i / kChunks, ch = i % kChunks;
-                                if (!seen(r)) st_zero16(dst + (ch >> 3) * C::kPanel + r * 128 + (ch & 7) * 16);
-                            }
-                            fence_proxy_async_smem();
-                        }
+                        if (__builtin_expect(look || ((plane == 1 || kCap) && !all), 0))
+                            edge_rows<D>(bad, edge, dst, groups, t0, hi, lo, se, !all, look ? lim : INT32_MAX, lo_last);
                     } else {
                         // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one; four at a time
                         constexpr int kQ4 = D / 64, kUnits = kPreBlock / 8 * kQ4 / C::kHelpers;
@@ -1065,6 +1156,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                     const int i = (u0 + u) * C::kHelpers + w, r = i / kQ4 * 8 + (lane & 7), q = i % kQ4 * 4 + (lane >> 3);
                                     const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
                                     c[u] = decltype(whole)::value || seen(r) ? ld_shared16(src + at) : make_uint4(0, 0, 0, 0);
+                                    if (!decltype(whole)::value && look) {  // (e4m3: a NaN's seven ones carry into the sign)
+                                        auto full = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+                                        if ((full(c[u].x) | full(c[u].y) | full(c[u].z) | full(c[u].w)) != 0) {
+                                            bad.found(edge, r);
+                                            c[u] = make_uint4(0, 0, 0, 0);
+                                        }
+                                    }
                                 }
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
@@ -1084,7 +1182,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                 }
                             }
                         };
-                        if ((plane == 1 || kCap) && !all)
+                        if (look || ((plane == 1 || kCap) && !all))
                             widen(std::false_type{});
                         else
                             widen(std::true_type{});
@@ -1097,6 +1195,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) piece_done(n);
         }
         if (!ok) report(a.status, MQA_ERR_DEVICE_TIMEOUT);
     } else if (warp == 11) {
@@ -1298,7 +1398,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
             }
             if (!ok) break;
             // ---- the piece's result
-            const float sum = l[0].x + l[0].y + l[1].x + l[1].y;
+            if (nact > 0 && !warp_wait(&s.o_done[i], (sn - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float sum = l[0].x + l[0].y + l[1].x + l[1].y;
+            if (__builtin_expect(s.bad[n % kPieces].any != 0, 0)) sum += bad_tokens(s.bad[n % kPieces], lim, lo, a.sinks);
             const int j0 = pc->j0;
             const bool part = j0 > 0 || j1 < pc->nt;
             const long long orow = static_cast<long long>(pc->row0 + i * a.tile_tok + tk) * a.Hq + pc->h * a.grp + g;
@@ -1312,11 +1418,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     a.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
                 }
             }
-            if (nact > 0 && !warp_wait(&s.o_done[i], (sn - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
             write_rows<D>(a, my_o, part, f, !row ? -1 : part ? prow : orow);
             __syncwarp();
             if (lane == 0) piece_done(n);

@@ -232,3 +232,42 @@ def test_a_wait_that_runs_out(monkeypatch):
     torch.cuda.synchronize()
     assert rc == 0 and int(status) == 6
     run([37], [10])  # the context goes on
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "fp8_e4m3_block", "int8_block"])
+@pytest.mark.parametrize("what", ["key", "value", "scale"])
+@pytest.mark.parametrize("shape", [dict(), dict(window=50, sinks=3), dict(prefix=[130, 0]), dict(cap=30.0), dict(slopes=True)])
+def test_non_finite_tokens_reach_those_that_see_them_alone(kv, what, shape):
+    if (what == "scale") != kv.endswith("block") and what == "scale":
+        pytest.skip("no scales")
+    if kv == "int8_block" and what != "scale":
+        pytest.skip("int8 codes are finite")
+    new, old = [150, 40], [70, 300]
+    q, starts, lens = batch(new, old, 8, 128)
+    c = Paged(lens, 2, 128, 16, kv, 1, 16)
+    cap, window, sinks = shape.get("cap", 0.0), shape.get("window", NO_WINDOW), shape.get("sinks", 0)
+    sl = slopes_of(8) if shape.get("slopes") else None
+    pre = shape.get("prefix")
+    kw = dict(softcap=cap, slopes=sl, window=window, sinks=sinks, kv_scales=c.scales, k_scale=c.k_scale, v_scale=c.v_scale,
+              prefix_lens=torch.tensor(pre, dtype=torch.int32, device="cuda") if pre else None)
+    spots = [1, 90, 131, 200]  # tokens of the first request
+    codes = c.cache.view(torch.int16 if kv == "bf16" else torch.uint8)
+    for t in spots:
+        block, slot = int(c.table[0, t // 16]), t % 16
+        if what == "scale":
+            c.scales[block, :, 0, 1] = float("nan")
+        else:
+            codes[block, 0 if what == "key" else 1, slot, 1, 5] = (0x7f80 if t % 2 else 0x7fc0) if kv == "bf16" else 0x7f
+    for splits in (1, None):
+        out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, num_kv_splits=splits, **kw)
+        ref = attention(q[150:], c.K[1], c.V[1], 300, 0.1, cap, sl, window, sinks, 0)
+        judge(out[150:], lse[150:], ref, "the other request")
+        p = 70 + torch.arange(150, device="cuda")[:, None]
+        t = torch.tensor(sum(([*range(s // 16 * 16, s // 16 * 16 + 16)] for s in spots), []) if what == "scale" else spots, device="cuda")
+        sees = (((t <= p) | (t < (pre[0] if pre else 0))) & ((t < sinks) | (t > p - window))).any(1)
+        ref = attention(q[:150], c.K[0], c.V[0], 70, 0.1, cap, sl, window, sinks, pre[0] if pre else 0)
+        for heads in (slice(0, 4), slice(4, 8)):  # the first KV head is clean
+            rows = ~sees if heads.start else torch.ones_like(sees)
+            judge(out[:150][rows][:, heads], lse[:150][rows][:, heads], tuple(x[rows][:, heads] for x in ref), f"{heads}")
+        if what != "key" or kv != "bf16":  # (of an infinite key the logit may be -inf: no weight at all)
+            assert not bool(torch.isfinite(out[:150][sees][:, 4:].float()).all(-1).any()), "rows that see one say so"
