@@ -633,7 +633,8 @@ size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_s
  *   prefix_lens int32 [batch] or NULL; taken within [0, seq_lens[b]].
  *   softcap, slopes, window, sinks  as for gqa_score_decode.
  *   out        bf16 [num_tokens, num_q_heads, head_size] (contiguous).
- *   lse        fp32 [num_tokens, num_q_heads] or NULL.
+ *   lse        fp32 [num_tokens, num_q_heads] or NULL.  out, lse and the workspace
+ *              overlap no other argument.
  *   num_kv_splits  1: no request's keys are cut (a token's result does not
  *              depend on the rest of the batch); more: work is cut into one
  *              share for each multiprocessor, which needs the workspace.

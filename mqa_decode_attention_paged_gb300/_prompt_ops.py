@@ -111,7 +111,7 @@ def _pools(caches, num_blocks, index):
                 raise ValueError(f"caches[{i}] must have {num_blocks} pages in its first dimension, got {tuple(s)}")
             raise ValueError(f"caches[{i}] is on {t.device}, the call runs on cuda:{index}")
         addresses.append(t.data_ptr())
-        sizes.append(t.nbytes // num_blocks)
+        sizes.append(t.nbytes // max(1, num_blocks))  # (no pages: refused by the call)
     return addresses, sizes
 
 

@@ -27,4 +27,10 @@ inline bool api_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<u
 // and its reciprocal are normal numbers.
 inline bool api_softcap_ok(float cap) { return cap == 0.f || (cap >= 0x1p-20f && cap <= 0x1p60f); }
 
+// Whether nx bytes at x and ny bytes at y overlap.
+inline bool api_overlap(const void* x, size_t nx, const void* y, size_t ny) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return x && y && a < b + ny && b < a + nx;
+}
+
 }  // namespace mqa

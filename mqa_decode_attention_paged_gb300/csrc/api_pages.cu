@@ -10,6 +10,7 @@ namespace {
 
 using mqa::api_aligned;
 using mqa::api_cuda_fail;
+using mqa::api_overlap;
 
 // The caches as pools.
 mqa_status pools_of(mqa::PagePools& p, void* const* caches, const size_t* page_bytes, int n, int num_blocks) {
@@ -34,11 +35,6 @@ mqa_status pools_of(mqa::PagePools& p, void* const* caches, const size_t* page_b
     p.first[n] = static_cast<int>(chunks);
     p.n = n;
     return MQA_OK;
-}
-
-bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-    return a < b + ny && b < a + nx;
 }
 
 mqa_status sizes_ok(int rows, int new_rows, int max_blocks, int num_blocks, int page_size) {
@@ -74,8 +70,8 @@ mqa_status mqa_pages_fork(const int32_t* block_table, const int32_t* seq_lens, c
         if (!api_aligned(p, 4)) return MQA_ERR_INVALID_ARG;
     if (const mqa_status s = sizes_ok(rows, new_rows, max_blocks, num_blocks, page_size); s != MQA_OK) return s;
     const size_t old_table = static_cast<size_t>(rows) * max_blocks * 4, table = static_cast<size_t>(new_rows) * max_blocks * 4;
-    if (overlap(block_table, old_table, new_table, table) || overlap(seq_lens, rows * 4ull, new_lens, new_rows * 4ull) ||
-        (refs != new_refs && overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)))
+    if (api_overlap(block_table, old_table, new_table, table) || api_overlap(seq_lens, rows * 4ull, new_lens, new_rows * 4ull) ||
+        (refs != new_refs && api_overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)))
         return MQA_ERR_INVALID_ARG;
     mqa::PagePools pools{};
     if (const mqa_status s = pools_of(pools, caches, page_bytes, num_caches, num_blocks); s != MQA_OK) return s;
@@ -115,9 +111,9 @@ mqa_status mqa_pages_compact(const int32_t* block_table, const int32_t* seq_lens
         if (!api_aligned(p, 4)) return MQA_ERR_INVALID_ARG;
     if (const mqa_status s = sizes_ok(rows, rows, max_blocks, num_blocks, page_size); s != MQA_OK) return s;
     const size_t table = static_cast<size_t>(rows) * max_blocks * 4;
-    if ((block_table != new_table && overlap(block_table, table, new_table, table)) ||
-        (refs != new_refs && overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)) ||
-        overlap(moved, num_blocks * 4ull, refs, num_blocks * 4ull) || overlap(moved, num_blocks * 4ull, new_refs, num_blocks * 4ull))
+    if ((block_table != new_table && api_overlap(block_table, table, new_table, table)) ||
+        (refs != new_refs && api_overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)) ||
+        api_overlap(moved, num_blocks * 4ull, refs, num_blocks * 4ull) || api_overlap(moved, num_blocks * 4ull, new_refs, num_blocks * 4ull))
         return MQA_ERR_INVALID_ARG;
     mqa::PagePools pools{};
     if (const mqa_status s = pools_of(pools, caches, page_bytes, num_caches, num_blocks); s != MQA_OK) return s;

@@ -66,6 +66,15 @@ def test_prefill_validation(kw, code):
     assert _prefill(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(), dict(out=FAKE + 4 * 2048 + 2032), dict(out=FAKE - 5 * 2048 + 16), dict(out=FAKE + 0x100000, lse=FAKE + 0x100000 + 5 * 2048 - 4),
+    dict(out=FAKE + 0x100000, lse=FAKE + 16), dict(out=FAKE + 0x100000, S=2, ws=FAKE + 9216, wsb=1 << 30),
+    dict(out=FAKE + 0x100000, stride=2048, lse=FAKE + 4 * 4096 + 2044)])
+def test_prefill_overlap(kw):
+    """A row of q is read while results of others are written."""
+    assert _prefill(**kw) == INV
+
+
 def test_prefill_workspace_sizes():
     assert mqa.gqa_prefill_workspace_bytes(9, 2, 128) == 0 and mqa.gqa_prefill_workspace_bytes(8, 2, 96) == 0
 
@@ -157,6 +166,13 @@ def test_prefill_optional_tensors(name, value):
     t = _tensors()
     with pytest.raises((TypeError, ValueError)):
         pkg.gqa_prefill(t["q"], t["kv"], t["bt"], t["sl"], t["qs"], 0.1, **{name: value})
+
+
+def test_no_pages():
+    """Caches of no pages reach the call, which refuses them."""
+    from mqa_decode_attention_paged_gb300 import _prompt_ops
+    assert list(_prompt_ops._pools([torch.zeros(0, 4)], 0, -1)[1]) == [0]
+    assert _fork(nb=0) == INV and _compact(nb=0) == INV
 
 
 def test_score_slopes():
