@@ -73,7 +73,7 @@ mqa_status mqa_pages_fork(const int32_t* block_table, const int32_t* seq_lens, c
     if (api_overlap(block_table, old_table, new_table, table) || api_overlap(seq_lens, rows * 4ull, new_lens, new_rows * 4ull) ||
         (refs != new_refs && api_overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)))
         return MQA_ERR_INVALID_ARG;
-    mqa::PagePools pools{};
+    mqa::PagePools pools;
     if (const mqa_status s = pools_of(pools, caches, page_bytes, num_caches, num_blocks); s != MQA_OK) return s;
     if (!workspace || workspace_bytes < mqa::fork_workspace_bytes(new_rows)) return MQA_ERR_WORKSPACE_TOO_SMALL;
     if (!api_aligned(workspace, 16)) return MQA_ERR_INVALID_ARG;
@@ -115,7 +115,7 @@ mqa_status mqa_pages_compact(const int32_t* block_table, const int32_t* seq_lens
         (refs != new_refs && api_overlap(refs, num_blocks * 4ull, new_refs, num_blocks * 4ull)) ||
         api_overlap(moved, num_blocks * 4ull, refs, num_blocks * 4ull) || api_overlap(moved, num_blocks * 4ull, new_refs, num_blocks * 4ull))
         return MQA_ERR_INVALID_ARG;
-    mqa::PagePools pools{};
+    mqa::PagePools pools;
     if (const mqa_status s = pools_of(pools, caches, page_bytes, num_caches, num_blocks); s != MQA_OK) return s;
     if (!workspace || workspace_bytes < mqa::compact_workspace_bytes(num_blocks)) return MQA_ERR_WORKSPACE_TOO_SMALL;
     if (!api_aligned(workspace, 16)) return MQA_ERR_INVALID_ARG;

@@ -283,7 +283,8 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyCtasPerSm = 4;
 
 // The pairs' pages in every pool, chunk by chunk.
-__device__ __forceinline__ void copy_pairs(const PagePools& pools, const int32_t* src, const int32_t* dst, int pairs) {
+template <int N>
+__device__ __forceinline__ void copy_pairs(const PoolsOf<N>& pools, const int32_t* src, const int32_t* dst, int pairs) {
     const int per = pools.first[pools.n];
     const long long items = static_cast<long long>(pairs) * per;
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
@@ -320,9 +321,9 @@ __device__ __forceinline__ void copy_pairs(const PagePools& pools, const int32_t
     }
 }
 
-template <bool FORK>
+template <bool FORK, int N>
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtasPerSm)
-    pages_copy_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PagePools pools) {
+    pages_copy_kernel(const __grid_constant__ PagesArgs a, const __grid_constant__ PoolsOf<N> pools) {
     pdl_wait();
     pdl_launch_dependents();
     const int32_t* src = a.ws + kPagesHeader;
@@ -375,6 +376,17 @@ cudaError_t launch_plan(void (*kern)(PagesArgs), const PagesArgs& a, size_t smem
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <bool FORK>
+cudaError_t launch_copy(const PagesArgs& a, const PagePools& pools, int sms, cudaStream_t stream) {
+    const dim3 grid(sms * kCopyCtasPerSm), block(kCopyThreads);
+    if (pools.n > kFewPools) return launch_with_pdl(pages_copy_kernel<FORK, kMaxPools>, grid, block, 0, stream, a, pools);
+    PoolsOf<kFewPools> few;
+    for (int i = 0; i < pools.n; ++i) few.pool[i] = {pools.pool[i].base, pools.pool[i].bytes};
+    for (int i = 0; i <= pools.n; ++i) few.first[i] = pools.first[i];
+    few.n = pools.n;
+    return launch_with_pdl(pages_copy_kernel<FORK, kFewPools>, grid, block, 0, stream, a, few);
+}
+
 }  // namespace
 
 cudaError_t pages_fork(const PagesArgs& a, const PagePools& pools, int sms, cudaStream_t stream) {
@@ -390,12 +402,12 @@ cudaError_t pages_fork(const PagesArgs& a, const PagePools& pools, int sms, cuda
         if (known) done[dev].store(true, std::memory_order_relaxed);
     }
     if (cudaError_t e = launch_plan(fork_plan_kernel, a, 2 * sizeof(int) * a.rows, stream); e != cudaSuccess) return e;
-    return launch_with_pdl(pages_copy_kernel<true>, dim3(sms * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream, a, pools);
+    return launch_copy<true>(a, pools, sms, stream);
 }
 
 cudaError_t pages_compact(const PagesArgs& a, const PagePools& pools, int sms, cudaStream_t stream) {
     if (cudaError_t e = launch_plan(compact_plan_kernel, a, 0, stream); e != cudaSuccess) return e;
-    return launch_with_pdl(pages_copy_kernel<false>, dim3(sms * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream, a, pools);
+    return launch_copy<false>(a, pools, sms, stream);
 }
 
 }  // namespace mqa

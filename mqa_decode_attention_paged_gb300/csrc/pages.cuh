@@ -10,14 +10,19 @@ constexpr int kMaxPools = 256;
 constexpr int kPagesMaxRows = 8192;
 
 // The tensors whose first dimension is a page, one after the other in chunks.
-struct PagePools {
+// They go to the kernel by value; kFewPools of them in a structure of their own,
+// as a launch with the 5 KB of the large one takes 4 us longer on the host.
+constexpr int kFewPools = 16;
+template <int N>
+struct PoolsOf {
     struct Pool {
         char* base;
         long long bytes;  // of a page, a multiple of 4
-    } pool[kMaxPools];
-    int first[kMaxPools + 1];  // chunks of a page before each
+    } pool[N];
+    int first[N + 1];  // chunks of a page before each
     int n;
 };
+using PagePools = PoolsOf<kMaxPools>;
 
 struct PagesArgs {
     const int32_t* table;    // [rows, width]

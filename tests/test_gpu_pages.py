@@ -99,6 +99,13 @@ def test_fork_formats(kinds):
     check_fork([40, 17, 100], [0, 0, 1, 2, 2, 2, 0], kinds=kinds)
 
 
+@pytest.mark.parametrize("count", [16, 17, 61, 256])
+def test_caches_of_many_layers(count):
+    kinds = (("bf16", "scale", "mla", "pth") * 64)[:count]
+    check_fork([40, 17, 100], [0, 0, 1, 2, 2, 2, 0], kinds=kinds)
+    check_compact([40, 17, 100], kinds=kinds)
+
+
 @pytest.mark.parametrize("lens,parents", [
     ([5], [0]), ([5], [0, 0, 0, 0]), ([16], [0, 0]), ([0], [0, 0]), ([5], [-1]), ([1, 2, 3], [-1, 2, -1, 2, 0]),
     ([33, 47], [1, 0]), ([33, 47], [1, 1]), ([15, 16, 17], [2, 2, 1, 1, 0, 0, -1]), ([300], [0] * 50)])
