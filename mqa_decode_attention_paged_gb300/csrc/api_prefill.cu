@@ -153,6 +153,7 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = kv_dtype == MQA_KV_BF16        ? mqa::pre_stage1_bf16(a, head_size, st)
                           : kv_dtype == MQA_KV_INT8_BLOCK ? mqa::pre_stage1_int8(a, head_size, st)
+                          : block                         ? mqa::pre_stage1_e4m3_block(a, head_size, st)
                                                           : mqa::pre_stage1_e4m3(a, head_size, st);
     if (e != cudaSuccess) return api_cuda_fail(e);
     if (a.cut)

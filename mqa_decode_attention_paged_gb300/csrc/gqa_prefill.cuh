@@ -35,7 +35,13 @@ struct PreArgs {
     const int32_t* prefix_lens;  // [batch], or null
     __nv_bfloat16* out;          // [num_tokens, Hq, D]
     float* lse;                  // [num_tokens, Hq], or null
-    int4* ws_meta;               // [grid][2], see PreMeta
+    // [grid][2], what thread block c leaves for the merge.  Its first piece uses partial slot 2c
+    // where it continues a (cell, head) that an earlier block began, its last one slot 2c + 1
+    // where it begins one that it does not end.
+    //   x  whether the last piece does;  y  the first piece: 0 continues nothing, 1 ends what it
+    //   continues, 2 does not, 3 there is no piece at all;  z, w  first row and tokens of the
+    //   begun cell;  second x  its KV head
+    int4* ws_meta;
     float* ws_ml;                // [2 grid][256][2]: reference (base 2) and sum of each row
     float* ws_o;                 // [2 grid][256][D]
     int* status;
@@ -110,16 +116,6 @@ __device__ __forceinline__ PreCell pre_cell(const PreArgs& a, const PreReq& r, i
     return c;
 }
 
-// What a thread block leaves for the merge.  Its first piece uses partial slot
-// 2c where it continues a (cell, head) that an earlier block began; its last
-// one slot 2c + 1 where it begins one that it does not end.
-struct PreMeta {
-    int begun;     // whether the last piece begins a (cell, head) and does not end it
-    int head;      // first piece: 0 continues nothing, 1 ends what it continues, 2 does not; 3: no piece at all
-    int row0, rows;  // of the begun cell: first token's row, tokens
-    int h;           // its KV head
-};
-
 // Partials: [2 grid] slots of two tiles.
 constexpr int kPreSlotRows = 2 * kPreTile;
 inline size_t pre_workspace_bytes(int grid, int D) {
@@ -129,6 +125,7 @@ inline size_t pre_workspace_bytes(int grid, int D) {
 
 cudaError_t pre_stage1_bf16(const PreArgs& a, int D, cudaStream_t stream);
 cudaError_t pre_stage1_e4m3(const PreArgs& a, int D, cudaStream_t stream);
+cudaError_t pre_stage1_e4m3_block(const PreArgs& a, int D, cudaStream_t stream);
 cudaError_t pre_stage1_int8(const PreArgs& a, int D, cudaStream_t stream);
 cudaError_t pre_merge(const PreArgs& a, int D, cudaStream_t stream);
 

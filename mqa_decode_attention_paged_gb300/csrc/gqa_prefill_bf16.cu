@@ -1,8 +1,8 @@
-// Prompt attention over bf16 caches (gqa_prefill_kernel.cuh).
+// Prompt attention over caches in bf16 (gqa_prefill_kernel.cuh).
 #include "gqa_prefill_kernel.cuh"
 
 namespace mqa {
 
-cudaError_t pre_stage1_bf16(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinBf16>(a, D, stream); }
+cudaError_t pre_stage1_bf16(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinBf16, false>(a, D, stream); }
 
 }  // namespace mqa

@@ -3,6 +3,6 @@
 
 namespace mqa {
 
-cudaError_t pre_stage1_e4m3(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinE4m3>(a, D, stream); }
+cudaError_t pre_stage1_e4m3(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinE4m3, false>(a, D, stream); }
 
 }  // namespace mqa

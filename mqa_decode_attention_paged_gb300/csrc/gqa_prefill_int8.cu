@@ -3,6 +3,6 @@
 
 namespace mqa {
 
-cudaError_t pre_stage1_int8(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinInt8>(a, D, stream); }
+cudaError_t pre_stage1_int8(const PreArgs& a, int D, cudaStream_t stream) { return pre::dispatch<kWinInt8, true>(a, D, stream); }
 
 }  // namespace mqa

@@ -39,7 +39,7 @@
 namespace mqa {
 namespace pre {
 
-enum Mode { kPlain, kScaled, kCapped, kBiased, kBoth };
+enum Mode { kPlain, kCapped, kBiased, kBoth };
 
 constexpr float kNone = -3e38f;  // reference before the first logit
 
@@ -65,7 +65,7 @@ struct Piece {
     int row0, cnt, p0, pre;
     int hi, lo, s_end, ns;
     int w0, nt, j0, j1;
-    int b, h, more, unused;  // more: 0 behind the last piece
+    int b, h, more;  // more: 0 behind the last piece
     __device__ __forceinline__ int block(int j) const { return j < ns ? j : w0 + j - ns; }
 };
 constexpr int kPieces = 4;  // described ahead
@@ -798,13 +798,14 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
     return true;
 }
 
-// MODE: kPlain (one positive scale), kScaled (non-negative scales of token blocks),
+// SCALED: whether token blocks have scales (they cost a per-tensor cache with slopes
+// 40 %: 154 us instead of 110, three chunks of 64 tokens).  MODE: kPlain (positive scale),
 // kCapped, kBiased (slopes, or a scale <= 0), kBoth.  All keep a row's 128 products
 // in registers; what is rare (a product beyond 0.6 of its cap, keys behind the query,
 // steep biases, scales <= 0) is shaped in a loop of its own through TMEM, so that
 // the code that runs stays short: with every case in line a capped prompt of 15999
 // tokens took 3509 us, a biased one 3728, a third of it waits for instructions.
-template <int D, int KIND, int MODE>
+template <int D, int KIND, bool SCALED, int MODE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
     using C = Cfg<D, KIND>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -812,16 +813,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     Shared& s = *reinterpret_cast<Shared*>(smem + (2 * C::kQ + C::kStages) * C::kTile + C::kRawStages * C::kRaw);
     Extra& ex = *reinterpret_cast<Extra*>(&s + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool scaled = C::kCodes && MODE != kPlain && a.kv_scales != nullptr;
     constexpr bool kCap = MODE == kCapped || MODE == kBoth, kBias = MODE == kBiased || MODE == kBoth;
-    constexpr bool kTimes = C::kCodes && MODE != kPlain;
     constexpr int kCopyStages = C::kCodes ? C::kRawStages : C::kStages;
 
     if (threadIdx.x == 0) {
         prefetch_tmap(&a.q_map);
         prefetch_tmap(&a.kv_map);
         for (int i = 0; i < 8; ++i) {
-            mbar_init(&s.kv_full[i], scaled ? 9 : 1);
+            mbar_init(&s.kv_full[i], SCALED ? 9 : 1);
             mbar_init(&s.kv_free[i], C::kHelpers);
             mbar_init(&s.ready[i], C::kHelpers);
             mbar_init(&s.used[i], 1);
@@ -899,7 +898,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         if ((have >> k) & 1u) groups |= ((1u << per) - 1u) << (k * per);
                 }
                 int g_id = 0, g_off = 0;
-                if (scaled) {
+                if (SCALED) {
                     g_id = __shfl_sync(0xffffffffu, id, lane / per);
                     g_off = __shfl_sync(0xffffffffu, off, lane / per) + lane % per * 16;
                 }
@@ -927,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                          &s.kv_full[st]);
                         }
                     }
-                    if (scaled && lane < 8) {
+                    if (SCALED && lane < 8) {
                         // (V's with K's: the softmax wants both)
                         if (plane == 0 && g_id >= 0) {
                             const float* from = a.kv_scales + (static_cast<long long>(g_id * 2) * a.scale_groups + a.scale_div(g_off)) * a.Hkv + pc.h;
@@ -984,7 +983,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 Piece& pc = s.piece[n % kPieces];
                 const PreCell& c = pw.cell;
                 s.bad[n % kPieces] = {};
-                pc = {c.row0, c.cnt, c.p0, c.pre, c.hi, c.lo, c.s_end, c.ns, c.w0, c.nt, pw.j0, pw.j1, pw.b < a.batch ? pw.b : pw.eb, pw.h, more, 0};
+                pc = {c.row0, c.cnt, c.p0, c.pre, c.hi, c.lo, c.s_end, c.ns, c.w0, c.nt, pw.j0, pw.j1, pw.b < a.batch ? pw.b : pw.eb, pw.h, more};
                 mbar_arrive(&s.piece_full[n % kPieces]);
                 if (!more) break;
                 if (n == 0) head = pw.j0 == 0 ? 0 : pw.j1 < c.nt ? 2 : 1;
@@ -1124,7 +1123,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         break;
                     }
                     // (a K scale of 0, whose codes are 0: their products stay 0, and -inf where nothing is seen stays that)
-                    if (scaled && plane == 0 && w == 0 && lane < 8 && ex.scale[slot][0][lane] < 0x1p-100f) ex.scale[slot][0][lane] = 0x1p-100f;
+                    if (SCALED && plane == 0 && w == 0 && lane < 8 && ex.scale[slot][0][lane] < 0x1p-100f) ex.scale[slot][0][lane] = 0x1p-100f;
                     const uint32_t groups = s.valid[slot];
                     const bool all = groups == 0xffu && t0 + kPreBlock <= hi && (t0 >= lo || t0 + kPreBlock <= se);
                     // V rows that not every row of the cell sees are looked over
@@ -1243,17 +1242,17 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 };
                 uint32_t x[4][32];
                 float4 ks[2] = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
-                if (scaled && !kCap) {
+                if (SCALED && !kCap) {
                     ks[0] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][0]);
                     ks[1] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][4]);
                 }
-                if (scaled && !kCap && __builtin_expect(edge, 0)) {  // those of groups that the row does not see may be anything
+                if (SCALED && !kCap && __builtin_expect(edge, 0)) {  // those of groups that the row does not see may be anything
                     const uint32_t b0 = seen(0), b1 = seen(1), b2 = seen(2), b3 = seen(3);
                     ks[0] = make_float4(b0 & 0xffffu ? ks[0].x : 1.f, b0 >> 16 ? ks[0].y : 1.f, b1 & 0xffffu ? ks[0].z : 1.f, b1 >> 16 ? ks[0].w : 1.f);
                     ks[1] = make_float4(b2 & 0xffffu ? ks[1].x : 1.f, b2 >> 16 ? ks[1].y : 1.f, b3 & 0xffffu ? ks[1].z : 1.f, b3 >> 16 ? ks[1].w : 1.f);
                 }
                 auto scales = [&](int k) {  // of the two groups of chunk k (with a cap from shared memory: registers)
-                    if (kCap && scaled) return make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]);
+                    if (kCap && SCALED) return make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]);
                     return k & 1 ? make_float2(ks[k >> 1].z, ks[k >> 1].w) : make_float2(ks[k >> 1].x, ks[k >> 1].y);
                 };
                 if (!kCap && __builtin_expect(edge, 0)) mask_row(my_s, seen(0), seen(1), seen(2), seen(3));
@@ -1264,7 +1263,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 // (an Inf or NaN scale reaches the rows that see a key of it)
                 auto v_scales = [&](int k) {
                     float2 v = both(1.f);
-                    if (kTimes && scaled) {
+                    if (SCALED) {
                         v = *reinterpret_cast<const float2*>(&ex.scale[kvb % C::kInfo][1][2 * k]);
                         if (edge) {
                             const uint32_t bits = seen(k);
@@ -1313,11 +1312,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
                 if constexpr (kCap || kBias) rare |= !(a.sl2 > 0.f);
                 if (__builtin_expect(rare, 0)) {
-                    RareRow q = {my_s, my_o, scaled ? &ex.scale[kvb % C::kInfo][0][0] : nullptr, {0, 0, 0, 0}, slope2, p - t0, mid, nact > 0, m,
+                    RareRow q = {my_s, my_o, SCALED ? &ex.scale[kvb % C::kInfo][0][0] : nullptr, {0, 0, 0, 0}, slope2, p - t0, mid, nact > 0, m,
                                  {l[0].x, l[0].y}, &s.o_done[i], (sn - 1) & 1};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) q.seen[k] = edge ? seen(k) : 0xffffffffu;
-                    ok = rare_row<D, kTimes>(a, q);
+                    ok = rare_row<D, SCALED>(a, q);
                     m = q.m;
                     l[1] = mul2(l[1], both(q.f));
                     l[0] = make_float2(q.l[0], q.l[1]);
@@ -1332,7 +1331,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if constexpr (C::kCodes && MODE != kPlain) {
+                            if constexpr (SCALED) {
                                 const float2 f = scales(k), top = group_max(x[k]);
                                 b[k] = fmaxf(top.x * f.x, top.y * f.y);
                             } else {
@@ -1361,7 +1360,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     if constexpr (kCap) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if (scaled) {
+                            if (SCALED) {
                                 const float2 f = scales(k);
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
@@ -1379,13 +1378,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         float2 f = both(a.sl2);
                         if constexpr (kCap)
                             f = both(1.f);
-                        else if constexpr (kTimes)
+                        else if constexpr (SCALED)
                             f = mul2(scales(k), both(a.sl2));
                         // With a bias: every key that is seen lies at or before the query, slope2 e -
                         // slope2 d (a row sees its own key at distance 0, beside which the rounding
                         // of a far key's bias is nothing).
                         const float add = kBias ? fmaf(-slope2, static_cast<float>(p - t0 - 32 * k), -m) : -m;
-                        numerators<kBias, kTimes>(x[k], f, add, slope2, v_scales(k), l, o);
+                        numerators<kBias, SCALED>(x[k], f, add, slope2, v_scales(k), l, o);
                         tmem_st16(my_s + 16 * k, o);
                     }
                 }
@@ -1437,13 +1436,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     }
 }
 
-template <int D, int KIND, int MODE>
+template <int D, int KIND, bool SCALED, int MODE>
 cudaError_t launch(const PreArgs& a, cudaStream_t stream) {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[kDevices];
     constexpr int bytes = smem_bytes<D, KIND>();
     static_assert(bytes <= 227 * 1024, "shared memory");
-    auto kern = gqa_prefill_kernel<D, KIND, MODE>;
+    auto kern = gqa_prefill_kernel<D, KIND, SCALED, MODE>;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const bool known = dev >= 0 && dev < kDevices;
@@ -1454,19 +1453,17 @@ cudaError_t launch(const PreArgs& a, cudaStream_t stream) {
     return launch_with_pdl(kern, dim3(a.grid), dim3(Cfg<D, KIND>::kThreads), bytes, stream, a);
 }
 
-template <int KIND, int MODE>
+template <int KIND, bool SCALED, int MODE>
 cudaError_t dispatch_size(const PreArgs& a, int D, cudaStream_t stream) {
-    return D == 128 ? launch<128, KIND, MODE>(a, stream) : launch<64, KIND, MODE>(a, stream);
+    return D == 128 ? launch<128, KIND, SCALED, MODE>(a, stream) : launch<64, KIND, SCALED, MODE>(a, stream);
 }
 
-template <int KIND>
+template <int KIND, bool SCALED>
 cudaError_t dispatch(const PreArgs& a, int D, cudaStream_t stream) {
-    if (a.cap2 > 0.f) return a.slopes ? dispatch_size<KIND, kBoth>(a, D, stream) : dispatch_size<KIND, kCapped>(a, D, stream);
-    if (a.slopes || !(a.sl2 > 0.f)) return dispatch_size<KIND, kBiased>(a, D, stream);
-    if constexpr (KIND != kWinBf16)
-        if (a.kv_scales) return dispatch_size<KIND, kScaled>(a, D, stream);
-    if constexpr (KIND != kWinInt8) return dispatch_size<KIND, kPlain>(a, D, stream);
-    return cudaErrorInvalidValue;  // (int8 codes always have scales)
+    if (a.cap2 > 0.f)
+        return a.slopes ? dispatch_size<KIND, SCALED, kBoth>(a, D, stream) : dispatch_size<KIND, SCALED, kCapped>(a, D, stream);
+    if (a.slopes || !(a.sl2 > 0.f)) return dispatch_size<KIND, SCALED, kBiased>(a, D, stream);
+    return dispatch_size<KIND, SCALED, kPlain>(a, D, stream);
 }
 
 }  // namespace pre
