@@ -68,7 +68,7 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kHelper + kHelpers);
     // registers a thread: 64 K by the launch, moved between the warpgroups
     static constexpr int kRegsSoftmax = kCodes ? 200 : 216, kRegsRest = kCodes ? 56 : 72;
-    static constexpr int kInfo = 16;  // blocks whose validity and scales are kept
+    static constexpr int kInfo = 8;  // blocks whose validity and scales are kept (at most 6 are between copy and softmax)
 };
 
 // A piece: blocks [j0, j1) of a cell's keys for one KV head (see PreCell).
@@ -109,11 +109,14 @@ struct alignas(16) Shared {  // (what follows it is read 16 bytes at a time)
     uint32_t tmem;
     Piece piece[kPieces];
     BadTokens bad[kPieces];
-    uint32_t valid[16];      // 16-token groups of a block that were copied
+    uint32_t valid[8];       // 16-token groups of a block that were copied
 };
-// What block-scaled caches have beside: K and V scales of the groups.
+// What block-scaled caches have beside: K and V scales of the groups, logarithms and
+// reciprocals of V's, and whether one of K's leaves 2^-100 .. 2^100, one of V's 2^-40 ..
+// 2^40 (or is a NaN): such blocks are rare.
 struct alignas(16) Extra {
-    float scale[16][2][8];
+    float scale[8][4][8];
+    uint32_t far[8];
 };
 
 template <int D, int KIND>
@@ -549,18 +552,35 @@ __device__ __forceinline__ void shape_any(const PreArgs& a, uint32_t (&x)[32], f
 }
 
 // P of 32 keys as bf16 pairs from x f + add, a scale f for each 16 of them, and +
-// slope2 e for key e if BIAS.  Their sum is added to l; with TIMES P is multiplied
-// by V's scales v of the two groups after that (codes are V's operand then, so that
-// there is one rounding, of P v: bf16 has the range of any scale).
+// slope2 e for key e if BIAS.  Their sum is added to l.  With TIMES P is multiplied by
+// V's scales v of the two groups (codes are V's operand then, so that there is one
+// rounding, of P v: bf16 has the range of any scale): by adding their logarithms before
+// the exponential, and the sums of each 16 are multiplied by the reciprocals.
 template <bool BIAS, bool TIMES>
-__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float add, float slope2, float2 v, float2 (&l)[2], uint32_t (&p)[16]) {
+__device__ __forceinline__ void numerators(const uint32_t (&x)[32], float2 f, float add, float slope2, float2 log_v, float2 rcp_v, float2 (&l)[2], uint32_t (&p)[16]) {
+    float2 group = both(0.f);
+    const float2 start = TIMES ? make_float2(add + log_v.x, add + log_v.y) : both(add);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        float2 y = fma2(get2(x, 2 * k), both(k < 8 ? f.x : f.y), both(add));
+        float2 y = fma2(get2(x, 2 * k), both(k < 8 ? f.x : f.y), both(k < 8 ? start.x : start.y));
         if (BIAS) y = make_float2(fmaf(slope2, 2.f * k, y.x), fmaf(slope2, 2.f * k + 1.f, y.y));
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        if (TIMES)
+            group = k % 8 == 0 ? e : add2(group, e);
+        else
+            l[k & 1] = add2(l[k & 1], e);
+        p[k] = pack_bf16x2(e.x, e.y);
+        if (TIMES && k % 8 == 7) l[k >> 3] = fma2(group, both(k < 8 ? rcp_v.x : rcp_v.y), l[k >> 3]);
+    }
+}
+// The same of finished logits less their reference, multiplied by v as it is.
+__device__ __forceinline__ void numerators_times(const uint32_t (&x)[32], float add, float2 v, float2 (&l)[2], uint32_t (&p)[16]) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float2 y = add2(get2(x, 2 * k), both(add));
         float2 e = make_float2(ex2(y.x), ex2(y.y));
         l[k & 1] = add2(l[k & 1], e);
-        if (TIMES) e = mul2(e, both(k < 8 ? v.x : v.y));
+        e = mul2(e, both(k < 8 ? v.x : v.y));
         p[k] = pack_bf16x2(e.x, e.y);
     }
 }
@@ -801,7 +821,7 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
         tmem_wait_ld();
         float2 v = both(1.f);
         if (TIMES && q.scales) v = make_float2(q.seen[k] & 0xffffu ? q.scales[8 + 2 * k] : 0.f, q.seen[k] >> 16 ? q.scales[8 + 2 * k + 1] : 0.f);
-        numerators<false, TIMES>(y, both(1.f), -q.m, 0.f, v, l, o);
+        numerators_times(y, -q.m, v, l, o);
         tmem_st16(q.s_at + 16 * k, o);
     }
     q.l[0] = l[0].x + l[1].x;
@@ -945,7 +965,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                             cp_async_4(&ex.scale[slot][1][lane], from + a.scale_groups * a.Hkv);
                             cp_async_arrive(&s.kv_full[st]);
                         } else {
-                            if (plane == 0) ex.scale[slot][0][lane] = ex.scale[slot][1][lane] = 0.f;
+                            if (plane == 0) ex.scale[slot][0][lane] = ex.scale[slot][1][lane] = 1.f;
                             mbar_arrive(&s.kv_full[st]);
                         }
                     }
@@ -1133,8 +1153,19 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         ok = false;
                         break;
                     }
-                    // (a K scale of 0, whose codes are 0: their products stay 0, and -inf where nothing is seen stays that)
-                    if (SCALED && plane == 0 && w == 0 && lane < 8 && ex.scale[slot][0][lane] < 0x1p-100f) ex.scale[slot][0][lane] = 0x1p-100f;
+                    if (SCALED && plane == 0 && w == 0) {
+                        // (a K scale of 0, whose codes are 0: their products stay 0, and -inf where nothing is seen stays that)
+                        float k = 1.f, v = 1.f;
+                        if (lane < 8) {
+                            k = ex.scale[slot][0][lane];
+                            v = ex.scale[slot][1][lane];
+                            if (k >= 0.f && k < 0x1p-100f) ex.scale[slot][0][lane] = k = 0x1p-100f;
+                            ex.scale[slot][2][lane] = log2f(v);
+                            ex.scale[slot][3][lane] = 1.f / v;
+                        }
+                        const uint32_t far = __any_sync(0xffffffffu, !(k >= 0x1p-100f && k <= 0x1p100f && v >= 0x1p-40f && v <= 0x1p40f));
+                        if (lane == 0) ex.far[slot] = far;
+                    }
                     const uint32_t groups = s.valid[slot];
                     const bool all = groups == 0xffu && t0 + kPreBlock <= hi && (t0 >= lo || t0 + kPreBlock <= se);
                     // V rows that not every row of the cell sees are looked over
@@ -1154,15 +1185,19 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         if (__builtin_expect(look || ((plane == 1 || kCap) && !all), 0))
                             edge_rows<D>(bad, edge, dst, groups, t0, hi, lo, se, !all, look ? lim : INT32_MAX, lo_last);
                     } else {
-                        // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one; four at a time
-                        constexpr int kQ4 = D / 64, kUnits = kPreBlock / 8 * kQ4 / C::kHelpers;
+                        // a lane takes 16 codes of row r: chunk q of the raw row, two chunks of the wide one.  How many at
+                        // a time: where this bounds the block, four (e4m3 without scales or a cap: 1707 us where two take 1876, one
+                        // prompt of 15999 tokens); else two, as short code counts (capped 2539 where four take 2817, 24 chunks over
+                        // int8 blocks 229 and 243); at edges one (six prompts with a window over e4m3 184, four 211)
+                        constexpr int kQ4 = D / 64, kUnits = kPreBlock / 8 * kQ4 / C::kHelpers, kAtOnce = kCap || SCALED ? 2 : 4;
                         const uint32_t src = raw_s + rst * C::kRaw;
                         auto widen = [&](auto whole) {
 #pragma unroll 1
-                            for (int u0 = 0; u0 < kUnits; u0 += 4) {
-                                uint4 c[4];
+                            for (int u0 = 0; u0 < kUnits; u0 += decltype(whole)::value ? kAtOnce : 1) {
+                                constexpr int kAt = decltype(whole)::value ? kAtOnce : 1;
+                                uint4 c[kAt];
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
+                                for (int u = 0; u < kAt; ++u) {
                                     const int i = (u0 + u) * C::kHelpers + w, r = i / kQ4 * 8 + (lane & 7), q = i % kQ4 * 4 + (lane >> 3);
                                     const uint32_t at = D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
                                     c[u] = decltype(whole)::value || seen(r) ? ld_shared16(src + at) : make_uint4(0, 0, 0, 0);
@@ -1175,7 +1210,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                     }
                                 }
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
+                                for (int u = 0; u < kAt; ++u) {
                                     const int i = (u0 + u) * C::kHelpers + w, r = i / kQ4 * 8 + (lane & 7), q = i % kQ4 * 4 + (lane >> 3);
                                     const uint32_t in[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
                                     uint32_t o[8];
@@ -1257,11 +1292,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     ks[0] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][0]);
                     ks[1] = *reinterpret_cast<const float4*>(&ex.scale[kvb % C::kInfo][0][4]);
                 }
-                if (SCALED && !kCap && __builtin_expect(edge, 0)) {  // those of groups that the row does not see may be anything
-                    const uint32_t b0 = seen(0), b1 = seen(1), b2 = seen(2), b3 = seen(3);
-                    ks[0] = make_float4(b0 & 0xffffu ? ks[0].x : 1.f, b0 >> 16 ? ks[0].y : 1.f, b1 & 0xffffu ? ks[0].z : 1.f, b1 >> 16 ? ks[0].w : 1.f);
-                    ks[1] = make_float4(b2 & 0xffffu ? ks[1].x : 1.f, b2 >> 16 ? ks[1].y : 1.f, b3 & 0xffffu ? ks[1].z : 1.f, b3 >> 16 ? ks[1].w : 1.f);
-                }
                 auto scales = [&](int k) {  // of the two groups of chunk k (with a cap from shared memory: registers)
                     if (kCap && SCALED) return make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]);
                     return k & 1 ? make_float2(ks[k >> 1].z, ks[k >> 1].w) : make_float2(ks[k >> 1].x, ks[k >> 1].y);
@@ -1270,19 +1300,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 tmem_wait_ld();
-                // V's scales of the two groups of chunk k; 1 where there are none, 0 where no key of a group is seen by the row
-                // (an Inf or NaN scale reaches the rows that see a key of it)
-                auto v_scales = [&](int k) {
-                    float2 v = both(1.f);
-                    if (SCALED) {
-                        v = *reinterpret_cast<const float2*>(&ex.scale[kvb % C::kInfo][1][2 * k]);
-                        if (edge) {
-                            const uint32_t bits = seen(k);
-                            if (!(bits & 0xffffu)) v.x = 0.f;
-                            if (!(bits >> 16)) v.y = 0.f;
-                        }
-                    }
-                    return v;
+                // Logarithms and reciprocals of V's scales of the two groups of chunk k (the row's keys of groups that
+                // it does not see are -inf, whatever is added)
+                auto v_scales = [&](int k, int which) {
+                    return SCALED ? *reinterpret_cast<const float2*>(&ex.scale[kvb % C::kInfo][which][2 * k]) : both(0.f);
                 };
                 // The row's reference after a block whose largest logit is mx (or less); false if a wait ran out.
                 auto refer = [&](float mx) {
@@ -1304,7 +1325,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     }
                     return true;
                 };
-                bool rare = false, mid = false;
+                // (scales of 0, infinite ones and NaN reach the rows that see a key of theirs)
+                bool rare = SCALED && ex.far[kvb % C::kInfo] != 0, mid = false;
                 if constexpr (kCap) {
                     float size = 0.f;
 #pragma unroll
@@ -1317,7 +1339,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         size = max3(size, wide[0] * f.x, wide[1] * f.y);
                     }
                     size *= fabsf(a.sl2) * a.inv_cap2;  // (a NaN passes the comparisons of the others and stays one)
-                    rare = a.tiny_unit || __any_sync(0xffffffffu, row && size > 0.6f);
+                    rare |= a.tiny_unit || __any_sync(0xffffffffu, row && size > 0.6f);
                     mid = !__any_sync(0xffffffffu, row && size > 1.f);
                 }
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
@@ -1395,7 +1417,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                         // slope2 d (a row sees its own key at distance 0, beside which the rounding
                         // of a far key's bias is nothing).
                         const float add = kBias ? fmaf(-slope2, static_cast<float>(p - t0 - 32 * k), -m) : -m;
-                        numerators<kBias, SCALED>(x[k], f, add, slope2, v_scales(k), l, o);
+                        numerators<kBias, SCALED>(x[k], f, add, slope2, v_scales(k, 2), v_scales(k, 3), l, o);
                         tmem_st16(my_s + 16 * k, o);
                     }
                 }
