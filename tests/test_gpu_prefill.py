@@ -234,6 +234,30 @@ def test_a_wait_that_runs_out(monkeypatch):
     run([37], [10])  # the context goes on
 
 
+@pytest.mark.parametrize("kv", ["fp8_e4m3_block", "int8_block"])
+@pytest.mark.parametrize("shape", [dict(), dict(window=50, sinks=3), dict(cap=30.0), dict(slopes=True), dict(cap=30.0, slopes=True)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_unusual_block_scales(kv, shape, D):
+    """Scales of 0, far below and far above what caches hold, in blocks of their own and among others."""
+    new, old = [300, 40], [170, 300]
+    q, starts, lens = batch(new, old, 8, D)
+    c = Paged(lens, 2, D, 16, kv, 1, 16)
+    cap, window, sinks = shape.get("cap", 0.0), shape.get("window", NO_WINDOW), shape.get("sinks", 0)
+    sl = slopes_of(8) if shape.get("slopes") else None
+    for b, group, plane, h, factor in [(0, 0, 1, 0, 0.0), (0, 3, 0, 1, 0.0), (0, 9, 1, 1, 2.0 ** -60), (0, 12, 0, 0, 2.0 ** -110),
+                                       (0, 17, 1, 0, 2.0 ** 50), (0, 20, 1, 1, 2.0 ** -39), (0, 28, 1, 1, 0.0),
+                                       *((1, k, 1, 0, 0.0) for k in range(22)), (1, 5, 1, 1, 2.0 ** 39)]:
+        c.scales[int(c.table[b, group]), plane, 0, h] *= factor
+        (c.V if plane else c.K)[b][16 * group:16 * group + 16, h] *= factor
+    for splits in (1, None):
+        out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, D ** -0.5, softcap=cap, slopes=sl, window=window,
+                                   sinks=sinks, kv_scales=c.scales, num_kv_splits=splits)
+        for b, at in ((0, 0), (1, 300)):
+            k = new[b]
+            judge(out[at:at + k], lse[at:at + k], attention(q[at:at + k], c.K[b], c.V[b], old[b], D ** -0.5, cap, sl, window, sinks, 0),
+                  f"request {b}")
+
+
 @pytest.mark.parametrize("kv,what", [(kv, what) for kv in ("bf16", "fp8_e4m3", "fp8_e4m3_block") for what in ("key", "value")]
                          + [("fp8_e4m3_block", "scale"), ("int8_block", "scale")])  # (int8 codes are finite)
 @pytest.mark.parametrize("shape", [dict(), dict(window=50, sinks=3), dict(prefix=[130, 0]), dict(cap=30.0), dict(slopes=True)])
