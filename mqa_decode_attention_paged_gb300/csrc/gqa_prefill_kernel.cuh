@@ -492,7 +492,7 @@ __device__ __forceinline__ void keep(uint32_t (&x)[32], uint32_t bits, float v) 
     for (int e = 0; e < 32; ++e)
         if (!((bits >> e) & 1u)) x[e] = __float_as_uint(v);
 }
-// The largest value of each 16 whose bit is set.
+// The largest value of each 16 (whose bit is set).
 __device__ __forceinline__ float2 group_max(const uint32_t (&x)[32], uint32_t bits) {
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -761,16 +761,30 @@ static __device__ __noinline__ float bad_tokens(const BadTokens& bad, int lim, i
     return sees ? NAN : 0.f;
 }
 
-// -inf in a row's products of keys whose bit is not set (32 to a word).  A function of
-// its own, like rare_row, for the edges of what rows see.
-static __device__ __noinline__ void mask_row(uint32_t s_at, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
-    const uint32_t bits[4] = {b0, b1, b2, b3};
-#pragma unroll
+// The keys of a block that a row sees, relative to the block's first one: key e where e <
+// lim and (e >= lo or e < sinks), if its group of 16 was copied.
+struct Seen {
+    int lim, lo, sinks;
+    uint32_t groups;
+    // of keys 32 k ..: bit e for key 32 k + e
+    __device__ __forceinline__ uint32_t bits(int k) const {
+        auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
+        const int t = 32 * k;
+        return below(lim - t) & (~below(lo - t) | below(sinks - t)) &
+               (((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u));
+    }
+};
+
+// -inf in a row's products of keys that it does not see.  A function of its own, like
+// rare_row, for the edges of what rows see.
+static __device__ __noinline__ void mask_row(uint32_t s_at, int lim, int lo, int sinks, uint32_t groups) {
+    const Seen seen = {lim, lo, sinks, groups};
+#pragma unroll 1
     for (int k = 0; k < 4; ++k) {
         uint32_t x[32];
         tmem_ld32(s_at + 32 * k, x);
         tmem_wait_ld();
-        keep(x, bits[k], -INFINITY);
+        keep(x, seen.bits(k), -INFINITY);
         tmem_st32(s_at + 32 * k, x);
     }
     tmem_wait_st();
@@ -783,7 +797,7 @@ static __device__ __noinline__ void mask_row(uint32_t s_at, uint32_t b0, uint32_
 struct RareRow {
     uint32_t s_at, o_at;    // the row's warp's S and O
     const float* scales;    // [2][8], of K's and V's groups, or null
-    uint32_t seen[4];       // keys that count
+    Seen seen;              // keys that count
     float slope2;
     int d;                  // distance of the first key
     bool mid, rescale;      // as of shape_any; whether O holds anything yet
@@ -800,7 +814,7 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
         uint32_t y[32];
         tmem_ld32(q.s_at + 32 * k, y);
         tmem_wait_ld();
-        shape_any(a, y, q.scales ? make_float2(q.scales[2 * k], q.scales[2 * k + 1]) : both(1.f), q.mid, q.slope2, q.d - 32 * k, q.seen[k]);
+        shape_any(a, y, q.scales ? make_float2(q.scales[2 * k], q.scales[2 * k + 1]) : both(1.f), q.mid, q.slope2, q.d - 32 * k, q.seen.bits(k));
         mx = fmaxf(mx, chunk_max(y));
         tmem_st32(q.s_at + 32 * k, y);
     }
@@ -820,7 +834,10 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
         tmem_ld32(q.s_at + 32 * k, y);
         tmem_wait_ld();
         float2 v = both(1.f);
-        if (TIMES && q.scales) v = make_float2(q.seen[k] & 0xffffu ? q.scales[8 + 2 * k] : 0.f, q.seen[k] >> 16 ? q.scales[8 + 2 * k + 1] : 0.f);
+        if (TIMES && q.scales) {
+            const uint32_t bits = q.seen.bits(k);
+            v = make_float2(bits & 0xffffu ? q.scales[8 + 2 * k] : 0.f, bits >> 16 ? q.scales[8 + 2 * k + 1] : 0.f);
+        }
         numerators_times(y, -q.m, v, l, o);
         tmem_st16(q.s_at + 16 * k, o);
     }
@@ -1279,13 +1296,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 tc_fence_after();
                 const uint32_t groups = s.valid[kvb % C::kInfo];
                 const bool edge = groups != 0xffu || !view.whole(a, t0);
-                // of keys t0 + 32 k + e, e < 32: bit e set where it counts, t < lim and (t >= lo or t < sinks), its group copied
-                auto seen = [&](int k) {
-                    auto below = [](int e) { return e <= 0 ? 0u : e >= 32 ? 0xffffffffu : (1u << e) - 1u; };
-                    const int t = t0 + 32 * k;
-                    return below(lim - t) & (~below(lo - t) | below(a.sinks - t)) &
-                           (((groups >> (2 * k)) & 1u ? 0xffffu : 0u) | ((groups >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u));
-                };
+                // (a block may lie 2^30 before a row's window and more: relative positions do not leave the range)
+                const Seen seen = {lim - t0, lo - t0, a.sinks - t0, groups};
                 uint32_t x[4][32];
                 float4 ks[2] = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
                 if (SCALED && !kCap) {
@@ -1296,7 +1308,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     if (kCap && SCALED) return make_float2(ex.scale[kvb % C::kInfo][0][2 * k], ex.scale[kvb % C::kInfo][0][2 * k + 1]);
                     return k & 1 ? make_float2(ks[k >> 1].z, ks[k >> 1].w) : make_float2(ks[k >> 1].x, ks[k >> 1].y);
                 };
-                if (!kCap && __builtin_expect(edge, 0)) mask_row(my_s, seen(0), seen(1), seen(2), seen(3));
+                if (!kCap && __builtin_expect(edge, 0)) mask_row(my_s, seen.lim, seen.lo, seen.sinks, seen.groups);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
                 tmem_wait_ld();
@@ -1345,31 +1357,34 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
                 if constexpr (kCap || kBias) rare |= !(a.sl2 > 0.f);
                 if (__builtin_expect(rare, 0)) {
-                    RareRow q = {my_s, my_o, SCALED ? &ex.scale[kvb % C::kInfo][0][0] : nullptr, {0, 0, 0, 0}, slope2, p - t0, mid, nact > 0, m,
+                    RareRow q = {my_s, my_o, SCALED ? &ex.scale[kvb % C::kInfo][0][0] : nullptr, seen, slope2, p - t0, mid, nact > 0, m,
                                  {l[0].x, l[0].y}, &s.o_done[i], (sn - 1) & 1};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) q.seen[k] = edge ? seen(k) : 0xffffffffu;
                     ok = rare_row<D, SCALED>(a, q);
                     m = q.m;
                     l[1] = mul2(l[1], both(q.f));
                     l[0] = make_float2(q.l[0], q.l[1]);
                 } else {
                     float b[4];
-                    if (kCap && edge) {
+                    // Masked keys' -inf stay that under the cap: its leading coefficient is positive.
+                    // (kBoth masks maxima and capped logits in registers: with the call bf16 spills, 4743
+                    // us for one prompt of 15999 tokens where it takes 3207; with -inf put in before the
+                    // maxima bf16 takes 2681, but e4m3 5157 where it takes 3681.)
+                    if (kCap && !kBias && __builtin_expect(edge, 0)) {
+                        mask_row(my_s, seen.lim, seen.lo, seen.sinks, seen.groups);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = scales(k), top = group_max(x[k], seen(k));
+                        for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, x[k]);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (kCap && kBias && edge) {
+                            const float2 f = scales(k), top = group_max(x[k], seen.bits(k));
                             b[k] = fmaxf(top.x * f.x, top.y * f.y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (SCALED) {
-                                const float2 f = scales(k), top = group_max(x[k]);
-                                b[k] = fmaxf(top.x * f.x, top.y * f.y);
-                            } else {
-                                b[k] = chunk_max(x[k]);
-                            }
+                        } else if constexpr (SCALED) {
+                            const float2 f = scales(k), top = group_max(x[k]);
+                            b[k] = fmaxf(top.x * f.x, top.y * f.y);
+                        } else {
+                            b[k] = chunk_max(x[k]);
                         }
                     }
                     float mx;
@@ -1400,9 +1415,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                             }
                             cap_chunk(a.tanh_raw, x[k]);
                         }
-                        if (edge) {
+                        if (kBias && edge) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) keep(x[k], seen(k), -INFINITY);
+                            for (int k = 0; k < 4; ++k) keep(x[k], seen.bits(k), -INFINITY);
                         }
                     }
 #pragma unroll
