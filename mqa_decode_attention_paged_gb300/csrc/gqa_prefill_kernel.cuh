@@ -32,13 +32,13 @@
 // What bounds it, measured with 32/8 heads x 128 (64/8 x 64) on one prompt of 15999
 // tokens unless said: the tensor cores over bf16 (1268 us, 1654 TFLOP/s of the 1952 of
 // a library's matrix product; a cell's start and end, and 4 % for looking V rows over
-// for an Inf or NaN, are the rest); the softmax's instructions with head size 64 (2074
-// us: half the products for as many exponentials), with slopes (1787) and with a cap
-// (2195); the widening over codes (e4m3 1725, its block scales 2157, int8 x 64 3227).
+// for an Inf or NaN, are the rest); the softmax's instructions with head size 64 (2058
+// us: half the products for as many exponentials), with slopes (1767) and with a cap
+// (1813); the widening over codes (e4m3 1716, its block scales 2096, int8 x 64 2888).
 // Short rows by the starts and ends of cells and by masked edges: six prompts of 500 to
-// 2600 tokens 154 us, 151 with a window of 1024 (10 blocks for 8 seen).  Few tokens
-// behind long contexts (three chunks of 64 behind 20 to 40 thousand) 99 us, 110 over
-// e4m3, 126 with slopes.
+// 2600 tokens 152 us, 141 with a window of 1024 (10 blocks for 8 seen).  Few tokens
+// behind long contexts (three chunks of 64 behind 20 to 40 thousand) 98 us, 112 over
+// e4m3, 125 with slopes.
 #pragma once
 
 #include <atomic>
