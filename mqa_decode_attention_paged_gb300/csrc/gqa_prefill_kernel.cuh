@@ -847,7 +847,7 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
 }
 
 // SCALED: whether token blocks have scales (they cost a per-tensor cache with slopes
-// 40 %: 154 us instead of 110, three chunks of 64 tokens).  MODE: kPlain (positive scale),
+// 22 %: 154 us instead of 126, three chunks of 64 tokens).  MODE: kPlain (positive scale),
 // kCapped, kBiased (slopes, or a scale <= 0), kBoth.  All keep a row's 128 products
 // in registers; what is rare (a product beyond 0.6 of its cap, keys behind the query,
 // steep biases, scales <= 0) is shaped in a loop of its own through TMEM, so that
