@@ -617,7 +617,8 @@ size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_s
  * (a prefix whose tokens see each other in both directions; none: causal), and
  * a query with p < 0 sees none.  x_t as for gqa_score_decode;
  *   lse = ln sum_t e^{x_t},  out = sum_t e^{x_t - lse} V_t
- * over the keys seen; out = 0, lse = -inf where there are none.  Rows of
+ * over the keys seen; out = 0, lse = -inf where there are none.  (Logits are
+ * fp32: without a cap results are finite up to 2^30 in magnitude.)  Rows of
  * tokens outside [query_start[0], query_start[batch]) are padding: not written.
  * Blocks that no new token sees are not read, nor are their block-table
  * entries.  Bytes of tokens that a new token does not see never reach its

@@ -50,7 +50,7 @@ struct PreArgs {
     float cap2, inv_cap2;    // softcap * log2(e) and its reciprocal, or 0
     float tanh_c[kTanhTerms], tanh_near[kTanhNearTerms];  // cap2 times kTanh and kTanhNear
     float tanh_raw[kTanhNearTerms];             // the latter in products: coefficient k times (sl2 / cap2)^(2 k + 1)
-    bool tiny_unit;                 // .. where these leave the fp32 range
+    bool tiny_unit;                 // .. where these leave the fp32 range, or the cap 2^20
     int num_tokens, batch, Hq, Hkv, grp;
     int tile_tok, tile_rows;  // tokens and rows of a tile: rows = tokens * grp <= 128
     int num_blocks, page, max_blocks;

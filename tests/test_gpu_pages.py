@@ -229,3 +229,22 @@ def test_captured_and_replayed():
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert int(more[3]) == int((want[2] > 0).sum())
+
+
+def test_pages_far_into_a_large_cache():
+    """Copies between pages on both sides of 2^32 bytes of their cache."""
+    nb, words = 140000, 32768 // 4
+    cache = torch.empty(nb, words, dtype=I32, device="cuda")
+    row = torch.arange(words, dtype=I32, device="cuda")
+    refs = torch.ones(nb, dtype=I32, device="cuda")
+    refs[[5, nb - 2]] = 0
+    cache[[nb - 1, 7]] = torch.stack([row + 1, row + 2])
+    table = torch.tensor([[nb - 1], [7]], dtype=I32, device="cuda")
+    got, lens, after = mqa.pages_fork(table, torch.tensor([3, 3], dtype=I32, device="cuda"),
+                                      torch.tensor([0, 0, 1, 1], dtype=I32, device="cuda"), refs, [cache], 16)
+    assert got.tolist() == [[nb - 1], [5], [7], [nb - 2]] and lens.tolist() == [3] * 4
+    assert torch.equal(cache[5], row + 1) and torch.equal(cache[nb - 2], row + 2) and int(after.sum()) == nb
+    after[:nb - 4] = 0  # live: the last four
+    got, after, moved, live = mqa.pages_compact(got[[0, 3]].contiguous(), lens[:2].contiguous(), after, [cache], 16)
+    assert int(live) == 4 and got.tolist() == [[3], [2]]
+    assert torch.equal(cache[3], row + 1) and torch.equal(cache[2], row + 2)

@@ -291,3 +291,70 @@ def test_non_finite_tokens_reach_those_that_see_them_alone(kv, what, shape):
             judge(out[:150][rows][:, heads], lse[:150][rows][:, heads], tuple(x[rows][:, heads] for x in ref), f"{heads}")
         if what != "key" or kv != "bf16":  # (of an infinite key the logit may be -inf: no weight at all)
             assert not bool(torch.isfinite(out[:150][sees][:, 4:].float()).all(-1).any()), "rows that see one say so"
+
+
+@pytest.mark.parametrize("cap,scale", [(4e-6, 4.4e-10), (4e-6, 1e-6), (2.0 ** -20, 0.1), (2.0 ** 60, 0.1), (2.0 ** 60, 2.0 ** 48)])
+def test_ends_of_the_range_of_caps(cap, scale):
+    run([200, 1], [60, 300], cap=cap, scale=scale, window=150)
+    run([200, 1], [60, 300], cap=cap, scale=scale, slopes=True, kv="int8_block")
+
+
+def test_replayed_with_other_lengths():
+    """A captured call reads lengths and starts when it runs; the workspace holds what the run before left."""
+    lens = [[300, 40, 700], [20, 600, 1], [700, 700, 700]]
+    new = [[300, 0, 64], [20, 90, 0], [1, 200, 129]]
+    c = Paged([700] * 3, 2, 128, 16, "bf16")
+    q = batch([400], [0], 8, 128)[0]
+    sl, starts = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros(400, 8, device="cuda")
+    workspace = torch.full((mqa.gqa_prefill_workspace_bytes(8, 2, 128),), 0xff, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mqa.gqa_prefill(q, c.cache, c.table, sl, starts, 0.1, out=out, lse=lse, workspace=workspace)
+    for n, k in zip(lens, new):
+        sl.copy_(torch.tensor(n, dtype=torch.int32))
+        starts.copy_(torch.tensor([0, *itertools.accumulate(k)], dtype=torch.int32))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for b in range(3):
+            if k[b]:
+                judge(out[at:at + k[b]], lse[at:at + k[b]],
+                      attention(q[at:at + k[b]], c.K[b][:n[b]], c.V[b][:n[b]], n[b] - k[b], 0.1), f"request {b}")
+            at += k[b]
+        assert bool((out[at:] == 7.0).all())
+
+
+@pytest.mark.parametrize("splits", [1, None])
+def test_results_at_odd_addresses(splits):
+    q, starts, lens = batch([150, 7], [40, 900], 6, 64)
+    c = Paged(lens, 3, 64, 16, "bf16")
+    want = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, num_kv_splits=splits)
+    buffer = torch.zeros(q.numel() + 16, dtype=torch.bfloat16, device="cuda")
+    words = torch.zeros(157 * 6 + 3, device="cuda")
+    room = torch.zeros(mqa.gqa_prefill_workspace_bytes(6, 3, 64) + 16, dtype=torch.uint8, device="cuda")
+    got = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, num_kv_splits=splits,
+                          out=buffer[8:8 + q.numel()].view(q.shape), lse=words[1:1 + 157 * 6].view(157, 6), workspace=room[16:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((buffer[:8] == 0).all()) and bool((buffer[-8:] == 0).all()) and float(words[0]) == float(words[-1]) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8_block"])
+def test_pages_far_into_a_large_cache(kv):
+    """Pages whose addresses lie past 2^32 bytes, and past 2^31 values, of their cache."""
+    new, old, page, Hkv, D = [70, 5], [100, 300], 16, 8, 128
+    q, starts, lens = batch(new, old, 8, D)
+    c = Paged(lens, Hkv, D, page, kv, 1, 16 if "block" in kv else 0)
+    small = c.cache.shape[0]
+    nb = 2 ** 31 // (2 * page * Hkv * D) + 1000
+    big = torch.empty((nb, *c.cache.shape[1:]), dtype=c.cache.dtype, device="cuda")
+    big[-small:] = c.cache
+    scales = None
+    if c.scales is not None:
+        scales = torch.ones(nb, *c.scales.shape[1:], device="cuda")
+        scales[-small:] = c.scales
+    table = torch.where((c.table >= 0) & (c.table < small), c.table + (nb - small), c.table)
+    want = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, kv_scales=c.scales)
+    got = mqa.gqa_prefill(q, big, table, c.seq_lens, starts, 0.1, kv_scales=scales)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
