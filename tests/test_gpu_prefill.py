@@ -33,6 +33,8 @@ def run(new, old, Hq=8, Hkv=2, D=128, page=16, kv="bf16", group=0, window=NO_WIN
     c = Paged(lens, Hkv, D, page, kv, seed, group, value=value)
     scale = D ** -0.5 if scale is None else scale
     sl = slopes_of(Hq) if slopes else None
+    if isinstance(slopes, list):
+        sl = torch.tensor(slopes, device="cuda")
     pre = None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device="cuda")
     out = torch.full((q.shape[0], Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((q.shape[0], Hq), 7.0, device="cuda")
@@ -358,3 +360,10 @@ def test_pages_far_into_a_large_cache(kv):
     want = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, kv_scales=c.scales)
     got = mqa.gqa_prefill(q, big, table, c.seq_lens, starts, 0.1, kv_scales=scales)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8_block"])
+def test_slopes_of_any_size_and_sign(kv, cap):
+    run([200, 1, 5], [60, 3000, 9], slopes=[0.0, -0.05, 5.0, 1e4, 1.4, 1.5, -3.0, 1e-6], cap=cap, kv=kv)
+    run([200, 40], [60, 0], slopes=[1.42, 0.3, 2.0, -1.0, 0.0, 0.0, 64.0, 1.0], cap=cap, kv=kv, Hq=8, Hkv=8, window=50, sinks=3, D=64)

@@ -9,20 +9,23 @@ pytestmark = pytest.mark.gpu
 
 
 def run(lens, L=1, Hq=8, Hkv=2, D=128, page=16, kv="bf16", group=0, window=None, sinks=0, cap=0.0, slopes=False, splits=None,
-        size=1.0, seed=3):
+        size=1.0, seed=3, scale=None):
     g = torch.Generator(device="cuda").manual_seed(seed)
     shape = (len(lens), Hq, D) if L == 1 else (len(lens), L, Hq, D)
     q = (torch.randn(*shape, generator=g, device="cuda") * size).to(torch.bfloat16)
     c = Paged(lens, Hkv, D, page, kv, seed, group)
     sl = torch.exp2(-8.0 * torch.arange(1, Hq + 1, device="cuda") / Hq).float() if slopes else None
+    if isinstance(slopes, list):
+        sl = torch.tensor(slopes, device="cuda")
+    scale = D ** -0.5 if scale is None else scale
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = mqa.gqa_score_decode(q, c.cache, c.table, c.seq_lens, D ** -0.5, softcap=cap, slopes=sl, window=window,
+    out, lse = mqa.gqa_score_decode(q, c.cache, c.table, c.seq_lens, scale, softcap=cap, slopes=sl, window=window,
                                     sinks=sinks, kv_scales=c.scales, k_scale=c.k_scale, v_scale=c.v_scale,
                                     num_kv_splits=splits, device_status=status)
     torch.cuda.synchronize()
     assert int(status) == 0 and out.shape == q.shape and lse.shape == q.shape[:-1]
     for b, n in enumerate(lens):
-        ref = attention(q[b].view(L, Hq, D), c.K[b], c.V[b], n - L, D ** -0.5, cap, sl,
+        ref = attention(q[b].view(L, Hq, D), c.K[b], c.V[b], n - L, scale, cap, sl,
                         NO_WINDOW if window is None else window, sinks, half_codes=c.codes[b])
         judge(out[b].view(L, Hq, D), lse[b].view(L, Hq), ref, f"request {b}")
     return q, c, out, lse
@@ -72,3 +75,15 @@ def test_captured_and_replayed():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
+@pytest.mark.parametrize("cap,scale", [(4e-6, 4.4e-10), (2.0 ** -20, 0.1), (2.0 ** 60, 0.1), (2.0 ** 60, 2.0 ** 48), (30.0, -0.2), (30.0, 0.0)])
+def test_ends_of_the_range_of_caps(cap, scale):
+    run([300, 70], cap=cap, scale=scale)
+    run([300, 70], cap=cap, scale=scale, slopes=True, kv="int8_block", L=3)
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8_block"])
+def test_slopes_of_any_size_and_sign(kv, cap):
+    run([300, 70, 3000], slopes=[0.0, -0.05, 5.0, 1e4, 1.4, 1.5, -3.0, 1e-6], cap=cap, kv=kv)
