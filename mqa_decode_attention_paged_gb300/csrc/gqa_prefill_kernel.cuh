@@ -1039,7 +1039,12 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 row0 = c.row0;
                 cnt = c.cnt;
                 h = pw.h;
-                if (pw.j1 <= pw.j0) continue;
+                if (pw.j1 <= pw.j0) {
+                    // (queries held back over pieces without blocks would be waited for by a piece whose place in the
+                    // ring is wanted next)
+                    copy_queries();
+                    continue;
+                }
                 if (queries > 0)
                     for (int i = 0; i < (cnt > a.tile_tok ? 2 : 1); ++i)
                         for (int p = 0; p < C::kPanels; ++p) tma_prefetch(&a.q_map, p * 64, h * a.grp, row0 + i * a.tile_tok);

@@ -367,3 +367,36 @@ def test_pages_far_into_a_large_cache(kv):
 def test_slopes_of_any_size_and_sign(kv, cap):
     run([200, 1, 5], [60, 3000, 9], slopes=[0.0, -0.05, 5.0, 1e4, 1.4, 1.5, -3.0, 1e-6], cap=cap, kv=kv)
     run([200, 40], [60, 0], slopes=[1.42, 0.3, 2.0, -1.0, 0.0, 0.0, 64.0, 1.0], cap=cap, kv=kv, Hq=8, Hkv=8, window=50, sinks=3, D=64)
+
+
+# ---- rows that see nothing among others that do: each of their (cell, KV head) pairs is a piece without blocks
+
+@pytest.mark.parametrize("splits", [1, None])
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("bf16", 64), ("fp8_e4m3", 128), ("fp8_e4m3_block", 64), ("int8_block", 128)])
+@pytest.mark.parametrize("empty", ["last 4", "last 16", "last 64", "every other", "all but one"])
+def test_single_tokens_some_without_a_sequence(empty, kv, D, splits):
+    none = {"last 4": range(252, 256), "last 16": range(240, 256), "last 64": range(192, 256), "every other": range(1, 256, 2),
+            "all but one": [i for i in range(256) if i != 77]}[empty]
+    run([1] * 256, [-1 if i in none else 199 for i in range(256)], Hq=32, Hkv=8, D=D, page=32, kv=kv, splits=splits)
+
+
+@pytest.mark.parametrize("splits", [1, None])
+@pytest.mark.parametrize("at", [0, 11, 23])
+@pytest.mark.parametrize("shape", [dict(), dict(kv="int8_block", D=64), dict(window=100, sinks=3, kv="fp8_e4m3"),
+                                   dict(cap=20.0, slopes=True)])
+def test_prompts_one_of_them_longer_than_its_sequence(shape, at, splits):
+    new = [100 + 20 * i for i in range(24)]
+    new[at] = 500
+    run(new, [-460 if i == at else i % 3 * 40 for i in range(24)], Hq=32, Hkv=8, splits=splits, pad=2, **shape)
+
+
+def test_pieces_without_blocks_in_runs_of_any_length():
+    """Between requests with keys 0 to 11 requests without, several heads each, in an order of their own for each share."""
+    new, old = [], []
+    for k in range(12):
+        for i in range(12):
+            new += [1 + (7 * i + k) % 300] + [1 + j % 3 for j in range(k)]
+            old += [(50 * i + 11 * k) % 400] + [-(1 + j % 3) for j in range(k)]
+    for Hkv in (1, 3):
+        for splits in (1, None):
+            run(new, old, Hq=2 * Hkv, Hkv=Hkv, splits=splits, D=64 if Hkv == 3 else 128)
