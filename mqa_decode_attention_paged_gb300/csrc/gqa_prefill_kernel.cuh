@@ -84,10 +84,17 @@ constexpr int kPieces = 4;  // described ahead
 // Tokens of a piece whose V row holds an Inf or NaN, in blocks that not every row of
 // the cell sees all of: that row counts as zeros in the products (0 * NaN would reach
 // the rows that do not see it), and the rows that see it become NaN at the end.
+// The softmax of a tile reads them while blocks behind its last one, which it has not
+// waited for, are still looked over: a block's tokens lie behind every row's limit
+// until its first one is stored, and are not seen by the tile's rows after that.
 struct BadTokens {
     int any;  // 1 where a bit below is set, 2 where there was no room for one
     int first[8];
     uint32_t bits[8][4];
+    __device__ __forceinline__ void clear() {
+        *this = {};
+        for (int& t : first) t = kPreNoWindow;
+    }
     // Row r of the piece's block number e of those looked over.
     __device__ __forceinline__ void found(int e, int r) {
         if (e < 8) atomicOr(&bits[e][r >> 5], 1u << (r & 31));
@@ -1030,7 +1037,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 }
                 Piece& pc = s.piece[n % kPieces];
                 const PreCell& c = pw.cell;
-                s.bad[n % kPieces] = {};
+                s.bad[n % kPieces].clear();
                 pc = {c.row0, c.cnt, c.p0, c.pre, c.hi, c.lo, c.s_end, c.ns, c.w0, c.nt, pw.j0, pw.j1, pw.b < a.batch ? pw.b : pw.eb, pw.h, more};
                 mbar_arrive(&s.piece_full[n % kPieces]);
                 if (!more) break;

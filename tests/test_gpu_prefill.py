@@ -400,3 +400,22 @@ def test_pieces_without_blocks_in_runs_of_any_length():
     for Hkv in (1, 3):
         for splits in (1, None):
             run(new, old, Hq=2 * Hkv, Hkv=Hkv, splits=splits, D=64 if Hkv == 3 else 128)
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "bf16", "fp8_e4m3_block"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_bad_value_of_the_second_tiles_block_stays_there(kv, D):
+    """Cells of two tiles of 128 tokens: the first one is done a block before the second, in whose block values are NaN."""
+    B, H = 48, 4
+    q, starts, lens = batch([256] * B, [0] * B, H, D)
+    c = Paged(lens, H, D, 64, kv)
+    codes = c.cache.view(torch.int16 if kv == "bf16" else torch.uint8)
+    kw = dict(kv_scales=c.scales, k_scale=c.k_scale, v_scale=c.v_scale, num_kv_splits=1)
+    want = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, **kw)
+    for t in (130, 170, 230, 255):
+        codes[c.table[:, t // 64].long(), 1, t % 64, :, 5] = 0x7fc0 if kv == "bf16" else 0x7f
+    sees = (torch.arange(256, device="cuda") >= 130).repeat(B)
+    for i in range(40):
+        out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, **kw)
+        assert torch.equal(out[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees]), f"call {i}"
+        assert bool(torch.isnan(out[sees].float()).any(-1).all())
