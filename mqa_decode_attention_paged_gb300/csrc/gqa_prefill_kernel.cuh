@@ -908,10 +908,12 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
     const uint32_t t_o = tmem, t_s = tmem + 2 * D;  // tile i: t_o + i D, t_s + 128 i
 
     bool ok = true;
-    // Piece number n, once it is described; false behind the last one (or where the wait ran out).
+    // Piece number n, once it is described; null behind the last one (or where the wait ran out).  The whole warp calls
+    // it, and every wait below but those of warp 10's lane: code after them meets at full masks, so that a warp's lanes
+    // have to give up together.
     auto piece = [&](int n) -> const Piece* {
         const Piece* pc = &s.piece[n % kPieces];
-        if (!mbar_wait(&s.piece_full[n % kPieces], n / kPieces & 1)) {
+        if (!warp_wait(&s.piece_full[n % kPieces], n / kPieces & 1)) {
             ok = false;
             return nullptr;
         }
@@ -961,7 +963,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 for (int plane = 0; plane < 2; ++plane, ++kvc) {
                     const int st = kvc % kCopyStages;
                     uint64_t* free = C::kCodes ? &s.kv_free[st] : &s.used[st];
-                    if (!mbar_wait(free, (kvc / kCopyStages & 1) ^ 1)) {
+                    if (!warp_wait(free, (kvc / kCopyStages & 1) ^ 1)) {
                         ok = false;
                         break;
                     }
@@ -1107,8 +1109,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
         };
         for (int n = 0; ok; ++n) {
             const Piece* pp = piece(n);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !pp) break;
+            if (!pp) break;
             const Piece pc = *pp;
             __syncwarp();
             if (lane == 0) piece_done(n);
@@ -1177,8 +1178,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                 const int t0 = pc.block(j) * kPreBlock, hi = pc.hi, lo = pc.lo, se = pc.s_end;
                 for (int plane = 0; plane < 2; ++plane, ++kvc) {
                     const int st = kvc % C::kStages, rst = kvc % kCopyStages, slot = (kvc >> 1) % C::kInfo;
-                    if (!mbar_wait(&s.kv_full[rst], kvc / kCopyStages & 1) ||
-                        (C::kCodes && !mbar_wait(&s.used[st], (kvc / C::kStages & 1) ^ 1))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&s.kv_full[rst], kvc / kCopyStages & 1) &&
+                                                     (!C::kCodes || mbar_wait(&s.used[st], (kvc / C::kStages & 1) ^ 1)))) {
                         ok = false;
                         break;
                     }
