@@ -396,7 +396,7 @@ __device__ __forceinline__ long long block_scan(Shared& s, long long v, long lon
 __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
     const int tid = threadIdx.x, nthr = blockDim.x, c = blockIdx.x;
     // first[b]: cells of the requests before b
-    int before = 0;
+    long long before = 0;
     for (int base = 0; base < a.batch; base += nthr) {
         const int b = base + tid;
         int k = 0;
@@ -405,16 +405,19 @@ __device__ __forceinline__ void plan(const PreArgs& a, Shared& s, int* first) {
             k = a.cell_div(r.cnt + 2 * a.tile_tok - 1);
         }
         long long all;
-        const int at = before + static_cast<int>(block_scan(s, k, all));
-        if (b < a.batch) first[b] = at;
-        before += static_cast<int>(all);
+        const long long at = before + block_scan(s, k, all);
+        if (b < a.batch) first[b] = static_cast<int>(at);
+        before += all;
     }
+    // Requests that ascend have at most this many cells.  Starts that go down and up again can claim every token once
+    // a request: far more work than the call's, and more cells than an int holds.  Nothing is done for them.
+    if (before > a.num_tokens + a.batch) before = 0;
     if (tid < 2) {
         s.b[tid] = a.batch;
         s.u[tid] = s.h[tid] = s.j[tid] = 0;
     }
     __syncthreads();
-    const int cells = before;
+    const int cells = static_cast<int>(before);
     auto find = [&](int i, int& b, int& u, int& nt) {
         int lo = 0, hi = a.batch - 1;  // the last request whose cells begin at or before i (empty ones lie before)
         while (lo < hi) {

@@ -419,3 +419,18 @@ def test_a_bad_value_of_the_second_tiles_block_stays_there(kv, D):
         out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, **kw)
         assert torch.equal(out[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees]), f"call {i}"
         assert bool(torch.isnan(out[sees].float()).any(-1).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 8, 64), (16, 2, 128), (128, 1, 64)])
+def test_starts_that_go_up_and_down(Hq, Hkv, D):
+    """Every second request claims all tokens: no work is done for them, and the call says so."""
+    T, B = 3000, 8192
+    q, _, _ = batch([T], [0], Hq, D)
+    c = Paged([T], Hkv, D, 64, "bf16")
+    starts = torch.tensor([0, T] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+    for splits in (1, None):
+        out, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+        mqa.gqa_prefill(q, c.cache, c.table.expand(B, -1).contiguous(), c.seq_lens.expand(B).contiguous(), starts, 0.1, out=out,
+                        num_kv_splits=splits, device_status=status)
+        assert int(status) == 5 and bool((out == 7.0).all())
+    run([37], [10])
