@@ -341,8 +341,15 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtasPerSm)
             const int n = p < 0 ? 0 : row_len(a, p, nullptr), k = pages_of(a, n);
             const int own = dst[a.new_rows + r];  // own pages lie after the destinations
             const int32_t* in = a.table + static_cast<long long>(p < 0 ? 0 : p) * a.width;
-            for (int j = threadIdx.x; j < a.width; j += kCopyThreads)
-                out[j] = j >= k ? -1 : j == k - 1 && own != -2 ? own : __ldg(in + j);
+            for (int j = threadIdx.x; j < a.width; j += kCopyThreads) {
+                int id = -1;
+                if (j < k) {
+                    id = __ldg(in + j);
+                    if (!is_page(a, id)) report(a.status, MQA_ERR_DEVICE_CHECK);  // (kept; the plan does not look at rows with one child)
+                    if (j == k - 1 && own != -2) id = own;
+                }
+                out[j] = id;
+            }
         } else {
             const int k = pages_of(a, row_len(a, r, a.status));
             const int32_t* in = a.table + static_cast<long long>(r) * a.width;

@@ -248,3 +248,35 @@ def test_pages_far_into_a_large_cache():
     got, after, moved, live = mqa.pages_compact(got[[0, 3]].contiguous(), lens[:2].contiguous(), after, [cache], 16)
     assert int(live) == 4 and got.tolist() == [[3], [2]]
     assert torch.equal(cache[3], row + 1) and torch.equal(cache[2], row + 2)
+
+
+@pytest.mark.parametrize("bad", [-1, -7, "nb", 2 ** 31 - 1])
+@pytest.mark.parametrize("lens,at", [([40, 17], (1, 0)), ([40, 17], (1, 1)), ([40, 32], (1, 1)), ([40, 17], (0, 2))])
+@pytest.mark.parametrize("parents", [[0, 1], [1, 0], [0, 1, -1], [0, 1, 0], [0, 1, 1]])
+def test_fork_reports_bad_ids_whatever_the_number_of_children(parents, lens, at, bad):
+    table, n, refs = state(lens, 16, 6)
+    held = table.clone()
+    bad = len(refs) if bad == "nb" else bad
+    table[at] = bad
+    cache = caches_of(len(refs), 16, ("scale",))[0]
+    before, status = cache.clone(), torch.zeros(1, dtype=I32, device="cuda")
+    nt, nl, nr = mqa.pages_fork(table.cuda(), n.cuda(), torch.tensor(parents, dtype=I32, device="cuda"), refs.cuda(), [cache], 16,
+                                device_status=status)
+    assert int(status) == 5
+    count = [parents.count(r) for r in range(2)]
+    want = refs.clone()
+    for r in range(2):
+        for j in range(-(-lens[r] // 16)):
+            tail = lens[r] % 16 and j == lens[r] // 16
+            if (r, j) != at:
+                want[held[r, j]] += (count[r] > 0) - 1 if tail else count[r] - 1
+    copied = [(parents.index(p), r) for r, p in enumerate(parents) if p >= 0 and p in parents[:r] and lens[p] % 16 and at != (p, lens[p] // 16)]
+    free = [i for i, c in enumerate(want.tolist()) if c == 0]
+    for (first, r), f in zip(copied, free):
+        want[f] = 1
+        before[f] = before[int(nt[first, lens[parents[r]] // 16])]
+        assert int(nt[r, lens[parents[r]] // 16]) == f
+    assert torch.equal(nr.cpu(), want) and torch.equal(cache, before)
+    for r, p in enumerate(parents):
+        if p >= 0 and r not in [x for _, x in copied]:
+            assert torch.equal(nt[r, :-(-lens[p] // 16)].cpu(), table[p, :-(-lens[p] // 16)])
