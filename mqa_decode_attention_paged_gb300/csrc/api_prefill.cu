@@ -11,7 +11,7 @@ namespace {
 
 using mqa::api_aligned;
 using mqa::api_cuda_fail;
-using mqa::api_overlap;
+using mqa::ApiSpan;
 
 constexpr int kMaxGrid = 256;  // thread blocks that the merge looks over
 constexpr int kMaxTokens = 1 << 24;
@@ -75,13 +75,17 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     if (q_stride % 8 != 0 || q_stride < static_cast<long long>(num_q_heads) * head_size || q_stride > (1LL << 36))
         return MQA_ERR_INVALID_ARG;
     if (num_kv_splits > 1 && !workspace) return MQA_ERR_WORKSPACE_TOO_SMALL;
-    // (rows of q are read while others' results are written)
+    // (rows of q and the rest are read while others' results are written)
     const size_t q_bytes = num_tokens > 0 ? 2 * ((num_tokens - 1) * static_cast<size_t>(q_stride) + static_cast<size_t>(num_q_heads) * head_size) : 0;
-    const size_t rows = static_cast<size_t>(num_tokens) * num_q_heads, out_bytes = rows * head_size * 2, lse_bytes = rows * 4;
-    if (api_overlap(q, q_bytes, out, out_bytes) || api_overlap(q, q_bytes, lse, lse_bytes) || api_overlap(out, out_bytes, lse, lse_bytes) ||
-        (num_kv_splits > 1 && (api_overlap(workspace, workspace_bytes, q, q_bytes) || api_overlap(workspace, workspace_bytes, out, out_bytes) ||
-                               api_overlap(workspace, workspace_bytes, lse, lse_bytes))))
-        return MQA_ERR_INVALID_ARG;
+    const size_t rows = static_cast<size_t>(num_tokens) * num_q_heads;
+    const size_t lines = 2ull * num_blocks * page_size * num_kv_heads;  // rows of head_size codes of the cache
+    const ApiSpan writes[] = {{out, rows * head_size * 2}, {lse, rows * 4}, {device_status, 4},
+                              {num_kv_splits > 1 ? workspace : nullptr, workspace_bytes}};
+    const ApiSpan reads[] = {{q, q_bytes}, {kv_cache, lines * head_size * (kv_dtype == MQA_KV_BF16 ? 2 : 1)},
+                             {block ? kv_scales : nullptr, block ? lines / scale_block * 4 : 0},
+                             {block_table, static_cast<size_t>(batch) * max_blocks * 4}, {seq_lens, batch * 4ull},
+                             {query_start, (batch + 1) * 4ull}, {prefix_lens, batch * 4ull}, {slopes, num_q_heads * 4ull}};
+    if (mqa::api_clash(writes, reads)) return MQA_ERR_INVALID_ARG;
     const int grid = grid_of();
     if (grid < 1) return MQA_ERR_CUDA;
     const size_t need = num_kv_splits > 1 ? mqa::pre_workspace_bytes(grid, head_size) : 0;

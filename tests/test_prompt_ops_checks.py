@@ -195,3 +195,59 @@ def test_page_tensors(change):
         pkg.pages_compact(t["bt"], t["sl"], t["refs"], t["caches"], 16)
     with pytest.raises((TypeError, ValueError)):
         pkg.pages_fork(t["bt"], t["sl"], torch.zeros(3), t["refs"], t["caches"], 16)
+
+
+# ---- outputs on other arguments (refused; each call has what it wants but for that)
+
+M = 0x10000000  # so far apart that nothing else overlaps
+FORK = dict(bt=M, sl=2 * M, pa=3 * M, refs=4 * M, nt=5 * M, nl=6 * M, nr=7 * M, ws=8 * M, wsb=1 << 20, st=9 * M,
+            caches=[10 * M, 11 * M], sizes=[4096, 64])
+COMPACT = dict(bt=M, sl=2 * M, refs=4 * M, nt=5 * M, nr=7 * M, mv=12 * M, nl=6 * M, ws=8 * M, wsb=1 << 20, st=9 * M,
+               caches=[10 * M, 11 * M], sizes=[4096, 64])
+FORK_BYTES = dict(bt=128, sl=16, pa=32, refs=400, nt=256, nl=32, nr=400, ws=(64 + 24) * 4, st=4)
+COMPACT_BYTES = dict(bt=128, sl=16, refs=400, nt=128, nr=400, mv=400, nl=4, ws=(64 + 300) * 4, st=4)
+
+
+def _clashes(sizes, written):
+    """Each written argument, each other one, and whether it is to be placed on that one's last or first word."""
+    return [(w, o, end) for w in written for o in sizes if o != w for end in (0, 1)]
+
+
+def _at(start, size, own, end, align):
+    """An address, aligned, at which `own` bytes touch the first or last ones of [start, start + size)."""
+    return (start + size - 4) // align * align if end else -(-(start + 4 - own) // align) * align
+
+
+@pytest.mark.parametrize("w,o,end", _clashes(FORK_BYTES, ("nt", "nl", "nr", "ws", "st")))
+def test_fork_writes_on_nothing_else(w, o, end):
+    at = _at(FORK[o], FORK_BYTES[o], FORK_BYTES[w], end, 16 if w in ("out", "ws") else 4)
+    assert _fork(**{**FORK, w: at}) == INV
+
+
+@pytest.mark.parametrize("w,o,end", _clashes(COMPACT_BYTES, ("nt", "nr", "mv", "nl", "ws", "st")))
+def test_compact_writes_on_nothing_else(w, o, end):
+    at = _at(COMPACT[o], COMPACT_BYTES[o], COMPACT_BYTES[w], end, 16 if w in ("out", "ws") else 4)
+    assert _compact(**{**COMPACT, w: at}) == INV
+
+
+@pytest.mark.parametrize("name", [*FORK_BYTES, "mv"])
+@pytest.mark.parametrize("cache", [0, 1])
+def test_pages_of_caches_hold_no_argument(name, cache):
+    first, last = FORK["caches"][cache], FORK["caches"][cache] + 100 * FORK["sizes"][cache] - 16
+    for at in (first, last):
+        if name in FORK_BYTES:
+            assert _fork(**{**FORK, name: at}) == INV
+        if name in COMPACT_BYTES:
+            assert _compact(**{**COMPACT, name: at}) == INV
+
+
+PREFILL = dict(q=M, kv=2 * M, sc=3 * M, bt=4 * M, sl=5 * M, qs=6 * M, pre=7 * M, slopes=8 * M, out=9 * M, lse=10 * M, st=11 * M,
+               ws=12 * M, wsb=0x8000000, S=2, kvd=6, G=16, ks=1.0)
+PREFILL_BYTES = dict(q=5 * 2048, kv=10 * 2 * 16 * 2 * 128, sc=10 * 2 * 2 * 4, bt=64, sl=8, qs=12, pre=8, slopes=32, out=5 * 2048,
+                     lse=160, st=4, ws=0x8000000)
+
+
+@pytest.mark.parametrize("w,o,end", _clashes(PREFILL_BYTES, ("out", "lse", "st", "ws")))
+def test_prefill_writes_on_nothing_else(w, o, end):
+    at = _at(PREFILL[o], PREFILL_BYTES[o], PREFILL_BYTES[w], end, 16 if w in ("out", "ws") else 4)
+    assert _prefill(**{**PREFILL, w: at}) == INV
