@@ -687,7 +687,8 @@ size_t mqa_pages_compact_workspace_bytes(int num_blocks);
  *   new_table  int32 [new_rows, max_blocks], fully written, -1 behind a row's last
  *              page; new_lens int32 [new_rows]; new_refs int32 [num_blocks] (may
  *              be refs itself).  Outputs overlap nothing else.
- *   rows, new_rows up to 8192; page_size a multiple of 16.
+ *   rows, new_rows 1 to 8192 (where no row goes on: one parent of -1); page_size a
+ *              multiple of 16.
  *   MQA_ERR_DEVICE_CHECK in *device_status: a parent or length out of range
  *   (an empty row; the length is taken into range), a block id outside
  *   [0, num_blocks) (kept, not counted), or too few free pages (the last rows that

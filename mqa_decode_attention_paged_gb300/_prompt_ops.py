@@ -145,8 +145,8 @@ def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_t
     gets the lowest free page with a copy of its data.  block_table int32 [rows, max_blocks], seq_lens int32 [rows],
     parents int32 [new_rows], refs int32 [num_blocks] (holders of each page, 0: free); caches: the tensors
     [num_blocks, ...] whose pages are copied, in place (of every layer; block scales are tensors of their own).
-    Returns new_table [new_rows, max_blocks], new_lens [new_rows] and new_refs [num_blocks] (new_refs may be refs
-    itself; allocated with torch when not given)."""
+    No parents: every row ends.  Returns new_table [new_rows, max_blocks], new_lens [new_rows] and new_refs
+    [num_blocks] (new_refs may be refs itself; allocated with torch when not given)."""
     if parents.dim() != 1:
         raise ValueError("parents must be int32 [new_rows]")
     shape, N, index = block_table.shape, parents.shape[0], block_table.get_device()
@@ -168,6 +168,10 @@ def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_t
                               new_lens=new_lens, new_refs=new_refs, workspace=workspace, device_status=device_status,
                               stream=stream)
     fresh = []
+    no_rows = (new_table, new_lens) if N == 0 else None
+    if no_rows:  # every row ends: one empty row in the place of none, which the C call does not take
+        parents, N, new_table, new_lens, workspace = torch.full((1,), -1, dtype=_I32, device=refs.device), 1, None, None, None
+        fresh.append(parents)
 
     def given(t, *size):
         if t is None:
@@ -184,6 +188,8 @@ def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_t
                             _call_stream(stream, index, fresh))
     if rc != OK:
         raise MqaError(rc, "mqa_pages_fork")
+    if no_rows:
+        new_table, new_lens = (made[:0] if t is None else t for t, made in zip(no_rows, (new_table, new_lens)))
     return new_table, new_lens, new_refs
 
 

@@ -280,3 +280,25 @@ def test_fork_reports_bad_ids_whatever_the_number_of_children(parents, lens, at,
     for r, p in enumerate(parents):
         if p >= 0 and r not in [x for _, x in copied]:
             assert torch.equal(nt[r, :-(-lens[p] // 16)].cpu(), table[p, :-(-lens[p] // 16)])
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_fork_without_new_rows(given):
+    """Every row ends: the counts fall, pages that something else holds stay."""
+    table, n, refs = state([40, 16, 0, 17], 16, 5, share=((3, 0, 1),))
+    refs[table[0, 1]] += 1
+    want = refs.clone()
+    for r, k in enumerate((3, 1, 0, 2)):
+        for i in table[r, :k].tolist():
+            want[i] -= 1
+    cache = caches_of(len(refs), 16, ("scale",))[0]
+    before, status = cache.clone(), torch.zeros(1, dtype=I32, device="cuda")
+    none, d_refs, W = torch.zeros(0, dtype=I32, device="cuda"), refs.cuda(), table.shape[1]
+    kw = dict(new_table=torch.zeros(0, W, dtype=I32, device="cuda"), new_lens=none.clone(), new_refs=d_refs,
+              workspace=torch.zeros(mqa.pages_fork_workspace_bytes(0), device="cuda")) if given else {}
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    nt, nl, nr = mqa.pages_fork(table.cuda(), n.cuda(), none, d_refs, [cache], 16, device_status=status, stream=stream, **kw)
+    stream.synchronize()
+    assert nt.shape == (0, W) and nl.shape == (0,) and int(status) == 0
+    assert torch.equal(nr.cpu(), want) and torch.equal(cache, before) and torch.equal(d_refs.cpu(), want if given else refs)
