@@ -53,6 +53,9 @@ namespace pre {
 enum Mode { kPlain, kCapped, kBiased, kBoth };
 
 constexpr float kNone = -3e38f;  // reference before the first logit
+// Below it a logit's factor could vanish beside a block's K scale (2^-100 at least), and a masked key's -inf times it be
+// a NaN: such calls, and scales <= 0, multiply before they mask.
+constexpr float kLeastScale = 0x1p-40f;
 
 template <int D, int KIND>
 struct Cfg {
@@ -857,8 +860,8 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
 }
 
 // SCALED: whether token blocks have scales (they cost a per-tensor cache with slopes
-// 22 %: 154 us instead of 126, three chunks of 64 tokens).  MODE: kPlain (positive scale),
-// kCapped, kBiased (slopes, or a scale <= 0), kBoth.  All keep a row's 128 products
+// 22 %: 154 us instead of 126, three chunks of 64 tokens).  MODE: kPlain (a scale that is
+// no smaller than kLeastScale), kCapped, kBiased (slopes, or another scale), kBoth.  All keep a row's 128 products
 // in registers; what is rare (a product beyond 0.6 of its cap, keys behind the query,
 // steep biases, scales <= 0) is shaped in a loop of its own through TMEM, so that
 // the code that runs stays short: with every case in line a capped prompt of 15999
@@ -1373,7 +1376,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                     mid = !__any_sync(0xffffffffu, row && size > 1.f);
                 }
                 if constexpr (kBias) rare |= steep || (pc->pre > 0 && t0 + kPreBlock > pc->p0 + i * a.tile_tok);
-                if constexpr (kCap || kBias) rare |= !(a.sl2 > 0.f);
+                if constexpr (kCap || kBias) rare |= !(a.sl2 >= kLeastScale);
                 if (__builtin_expect(rare, 0)) {
                     RareRow q = {my_s, my_o, SCALED ? &ex.scale[kvb % C::kInfo][0][0] : nullptr, seen, slope2, p - t0, mid, nact > 0, m,
                                  {l[0].x, l[0].y}, &s.o_done[i], (sn - 1) & 1};
@@ -1528,7 +1531,7 @@ template <int KIND, bool SCALED>
 cudaError_t dispatch(const PreArgs& a, int D, cudaStream_t stream) {
     if (a.cap2 > 0.f)
         return a.slopes ? dispatch_size<KIND, SCALED, kBoth>(a, D, stream) : dispatch_size<KIND, SCALED, kCapped>(a, D, stream);
-    if (a.slopes || !(a.sl2 > 0.f)) return dispatch_size<KIND, SCALED, kBiased>(a, D, stream);
+    if (a.slopes || !(a.sl2 >= kLeastScale)) return dispatch_size<KIND, SCALED, kBiased>(a, D, stream);
     return dispatch_size<KIND, SCALED, kPlain>(a, D, stream);
 }
 

@@ -434,3 +434,23 @@ def test_starts_that_go_up_and_down(Hq, Hkv, D):
                         num_kv_splits=splits, device_status=status)
         assert int(status) == 5 and bool((out == 7.0).all())
     run([37], [10])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -39, 2.0 ** -42, 2.0 ** -60, 2.0 ** -120])
+@pytest.mark.parametrize("kv,D", [("int8_block", 64), ("fp8_e4m3_block", 128)])
+@pytest.mark.parametrize("shape", [dict(), dict(slopes=True), dict(cap=30.0)])
+def test_tiny_scales_over_blocks_whose_keys_scale_is_zero(shape, kv, D, scale):
+    new, old = [300, 40], [170, 300]
+    q, starts, lens = batch(new, old, 8, D)
+    c = Paged(lens, 2, D, 16, kv, 1, 16)
+    for b in (0, 1):
+        for group in (0, 3, 4, 10, 20):
+            c.scales[int(c.table[b, group]), 0, 0, :] = 0.0
+            c.K[b][16 * group:16 * group + 16] = 0.0
+    sl = slopes_of(8) if shape.get("slopes") else None
+    out, lse = mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, scale, softcap=shape.get("cap", 0.0), slopes=sl,
+                               window=150, sinks=3, kv_scales=c.scales)
+    for b, at in ((0, 0), (1, 300)):
+        k = new[b]
+        judge(out[at:at + k], lse[at:at + k], attention(q[at:at + k], c.K[b], c.V[b], old[b], scale, shape.get("cap", 0.0), sl, 150, 3, 0),
+              f"request {b}")
