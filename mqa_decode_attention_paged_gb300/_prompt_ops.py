@@ -79,7 +79,7 @@ def gqa_prefill(q, kv_cache, block_table, seq_lens, query_start, scale, *, softc
         fresh.append(lse)
     if T == 0:  # (an empty tensor has no address)
         return out, lse
-    splits = 2 if num_kv_splits is None else int(num_kv_splits)
+    splits = 2 if num_kv_splits is None else _c_int(num_kv_splits)
     ws_bytes = 0
     if workspace is not None:
         ws_bytes = workspace.nbytes
@@ -183,7 +183,7 @@ def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_t
     workspace = given(workspace, max(16, lib.mqa_pages_fork_workspace_bytes(N) // 4))
     rc = lib.mqa_pages_fork(block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(), refs.data_ptr(),
                             new_table.data_ptr(), new_lens.data_ptr(), new_refs.data_ptr(), shape[0], N, width, nb,
-                            int(page_size), addresses.buffer_info()[0], sizes.buffer_info()[0], len(addresses),
+                            _c_int(page_size), addresses.buffer_info()[0], sizes.buffer_info()[0], len(addresses),
                             workspace.data_ptr(), workspace.nbytes, _raw(device_status),
                             _call_stream(stream, index, fresh))
     if rc != OK:
@@ -229,7 +229,7 @@ def pages_compact(block_table, seq_lens, refs, caches, page_size, *, new_table=N
     workspace = given(workspace, max(16, lib.mqa_pages_compact_workspace_bytes(nb) // 4))
     rc = lib.mqa_pages_compact(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), new_table.data_ptr(),
                                new_refs.data_ptr(), moved.data_ptr(), num_live.data_ptr(), shape[0], shape[1], nb,
-                               int(page_size), addresses.buffer_info()[0], sizes.buffer_info()[0], len(addresses),
+                               _c_int(page_size), addresses.buffer_info()[0], sizes.buffer_info()[0], len(addresses),
                                workspace.data_ptr(), workspace.nbytes, _raw(device_status),
                                _call_stream(stream, index, fresh))
     if rc != OK:

@@ -302,3 +302,13 @@ def test_fork_without_new_rows(given):
     stream.synchronize()
     assert nt.shape == (0, W) and nl.shape == (0,) and int(status) == 0
     assert torch.equal(nr.cpu(), want) and torch.equal(cache, before) and torch.equal(d_refs.cpu(), want if given else refs)
+
+
+def test_page_sizes_beyond_a_c_int_are_taken_at_their_value():
+    table, n, refs = (x.cuda() for x in state([40, 17], 16, 5))
+    parents = torch.tensor([0, 1], dtype=I32, device="cuda")
+    for page in (2 ** 32 + 16, -2 ** 32 + 16, 2 ** 33):
+        with pytest.raises(mqa.MqaError):
+            mqa.pages_fork(table, n, parents, refs, [], page)
+        with pytest.raises(mqa.MqaError):
+            mqa.pages_compact(table, n, refs, [], page)

@@ -454,3 +454,15 @@ def test_tiny_scales_over_blocks_whose_keys_scale_is_zero(shape, kv, D, scale):
         k = new[b]
         judge(out[at:at + k], lse[at:at + k], attention(q[at:at + k], c.K[b], c.V[b], old[b], scale, shape.get("cap", 0.0), sl, 150, 3, 0),
               f"request {b}")
+
+
+def test_splits_beyond_a_c_int_are_taken_at_their_value():
+    q, starts, lens = batch([64, 1], [9000, 4000], 32, 128)
+    c = Paged(lens, 8, 128, 64, "bf16")
+    call = lambda n: mqa.gqa_prefill(q, c.cache, c.table, c.seq_lens, starts, 0.1, num_kv_splits=n)  # noqa: E731
+    want = call(2)
+    for n in (2 ** 32, 2 ** 32 + 1):
+        out, lse = call(n)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(mqa.MqaError):
+        call(1 - 2 ** 32)
