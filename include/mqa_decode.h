@@ -589,6 +589,10 @@ mqa_status mla_rope_append(const void* kv_c, const void* k_pe, const void* q_pe,
  * gqa_window_decode with shaped logits: of query head h at position p and key t
  *   x_t = cap tanh(scale <q, K_t> / cap) - slopes[h] |p - t|
  * (softcap = cap; 0: the scaled product itself; slopes NULL: no bias).
+ * Logits are fp32: where the largest one is x, a key's weight may be off by
+ * 2^-22 |x| of itself beside the errors of the products, and over 8-bit codes,
+ * whose scales join the exponent, the outputs as a whole (10 % at a logit of
+ * 400 thousand).
  *
  *   softcap    0, or 2^-20 .. 2^60.
  *   slopes     fp32 [num_q_heads] or NULL.
@@ -618,7 +622,8 @@ size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_s
  * a query with p < 0 sees none.  x_t as for gqa_score_decode;
  *   lse = ln sum_t e^{x_t},  out = sum_t e^{x_t - lse} V_t
  * over the keys seen; out = 0, lse = -inf where there are none.  (Logits are
- * fp32: without a cap results are finite up to 2^30 in magnitude.)  Rows of
+ * fp32: without a cap results are finite up to 2^30 in magnitude, over block
+ * scales or with slopes up to 2^26.)  Rows of
  * tokens outside [query_start[0], query_start[batch]) are padding: not written.
  * Blocks that no new token sees are not read, nor are their block-table
  * entries.  Bytes of tokens that a new token does not see never reach its
