@@ -686,6 +686,13 @@ size_t mqa_pages_compact_workspace_bytes(int num_blocks);
  * (c(p) > 0) - 1; a fresh page's is 1.  Pages that become free in this call may
  * be taken by it.  (A row without children is freed: parents of -1 free.)
  *
+ * Counts say who holds a page, not who writes it.  A row's next tokens go behind
+ * its last one, into a partly filled last page, which is therefore the row's
+ * alone to write: of the rows given, only one may end in it, and whatever else
+ * holds it (a store of prefixes) reads no more than the tokens that were there.
+ * The first child keeps such a page, and the right to write it, whatever its
+ * count.
+ *
  *   block_table int32 [rows, max_blocks], seq_lens int32 [rows], refs int32
  *              [num_blocks]; entries behind a row's last page are not read.
  *   parents    int32 [new_rows] in [-1, rows).

@@ -141,10 +141,10 @@ def _check_pages(block_table, seq_lens, refs, named, workspace, device_status):
 def pages_fork(block_table, seq_lens, parents, refs, caches, page_size, *, new_table=None, new_lens=None,
                new_refs=None, workspace=None, device_status=None, stream=None):
     """New rows of a block table from parents through the C ABI (``mqa_pages_fork``): row r of the result shares the
-    pages of row parents[r] (-1: an empty row); a partly filled last page stays with the first child, every other one
-    gets the lowest free page with a copy of its data.  block_table int32 [rows, max_blocks], seq_lens int32 [rows],
-    parents int32 [new_rows], refs int32 [num_blocks] (holders of each page, 0: free); caches: the tensors
-    [num_blocks, ...] whose pages are copied, in place (of every layer; block scales are tensors of their own).
+    pages of row parents[r] (-1: an empty row); a partly filled last page, in which only one row may end, stays with the
+    first child, every other one gets the lowest free page with a copy of its data.  block_table int32 [rows, max_blocks],
+    seq_lens int32 [rows], parents int32 [new_rows], refs int32 [num_blocks] (holders of each page, 0: free); caches: the
+    tensors [num_blocks, ...] whose pages are copied, in place (of every layer; block scales are tensors of their own).
     No parents: every row ends.  Returns new_table [new_rows, max_blocks], new_lens [new_rows] and new_refs
     [num_blocks] (new_refs may be refs itself; allocated with torch when not given)."""
     if parents.dim() != 1:

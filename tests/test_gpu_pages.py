@@ -312,3 +312,20 @@ def test_page_sizes_beyond_a_c_int_are_taken_at_their_value():
             mqa.pages_fork(table, n, parents, refs, [], page)
         with pytest.raises(mqa.MqaError):
             mqa.pages_compact(table, n, refs, [], page)
+
+
+@pytest.mark.parametrize("parents", [[0], [0, 0, 0], [-1], [1, 0, 1]])
+def test_fork_of_a_partly_filled_page_that_something_else_holds(parents):
+    """The page stays with the first child, further ones get copies; the other holder keeps its count."""
+    table, n, refs = state([40, 21], 16, 6)
+    tail = int(table[0, 2])
+    refs[tail] += 2
+    caches = caches_of(len(refs), 16, ("bf16",))
+    want_caches = [x.clone() for x in caches]
+    want = plain_fork(table, n, refs, parents, 16, want_caches)
+    got = mqa.pages_fork(table.cuda(), n.cuda(), torch.tensor(parents, dtype=I32, device="cuda"), refs.cuda(), caches, 16)
+    for a, b in zip(got, want[:3]):
+        assert torch.equal(a.cpu(), b)
+    assert torch.equal(caches[0], want_caches[0]) and int(got[2][tail]) == 2 + (0 in parents)
+    if 0 in parents:
+        assert int(got[0][parents.index(0), 2]) == tail
