@@ -466,3 +466,11 @@ def test_splits_beyond_a_c_int_are_taken_at_their_value():
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     with pytest.raises(mqa.MqaError):
         call(1 - 2 ** 32)
+
+
+@pytest.mark.parametrize("cap", [20.0, 34.0, 36.0, 50.0, 57.0, 58.0, 59.0, 60.0, 90.0])
+@pytest.mark.parametrize("size", [1.0, 8.0])
+def test_caps_over_small_scales_of_the_cache(cap, size):
+    """scale k_scale / cap from 1.8e-4 to 3.9e-5, either side of where its ninth power times the cap stops being normal."""
+    run([200, 1], [60, 300], cap=cap, size=size, kv="fp8_e4m3")
+    run([200, 1], [60, 300], cap=cap, size=size, kv="fp8_e4m3", slopes=True, window=150)
