@@ -29,16 +29,25 @@
 // exactly; K scales multiply the logits, V scales the numerators before they are
 // rounded.
 //
-// What bounds it, measured with 32/8 heads x 128 (64/8 x 64) on one prompt of 15999
-// tokens unless said: the tensor cores over bf16 (1268 us, 1654 TFLOP/s of the 1952 of
-// a library's matrix product; a cell's start and end, and 4 % for looking V rows over
-// for an Inf or NaN, are the rest); the softmax's instructions with head size 64 (2058
-// us: half the products for as many exponentials), with slopes (1767) and with a cap
-// (1813); the widening over codes (e4m3 1716, its block scales 2096, int8 x 64 2888).
-// Short rows by the starts and ends of cells and by masked edges: six prompts of 500 to
-// 2600 tokens 152 us, 141 with a window of 1024 (10 blocks for 8 seen).  Few tokens
-// behind long contexts (three chunks of 64 behind 20 to 40 thousand) 98 us, 112 over
-// e4m3, 125 with slopes.
+// What bounds it, measured on the prompts of perf/more_operators.py and changes of them
+// (us a call, 12 calls in a row; 32/8 heads x 128 unless said).  One prompt of 15999
+// tokens: 1315, the tensor cores (1595 TFLOP/s, 1627 where a call stands alone, of the 1952
+// of a library's matrix product; a cell's start and end, and 4 % for looking V rows over
+// for an Inf or NaN, are the rest).  Else the chain from product to softmax to product of
+// each tile, as P lies where S did; where it was profiled no unit is full (64/8 heads x 64
+// 2075: half the products for as many exponentials; slopes 1765, a cap of 50 1859, both
+// 3198; e4m3 1716, block scales 2109, int8 64/8 x 64 2745, e4m3 with a cap 2673).  Blocks
+// that take the slow form (see MODE below) take four to five times as long: caps of 20 and
+// 15, which these logits of deviation 3 reach, 8533 and 8399, slopes up to 17 6028, a
+// negative scale 6249.
+// Short rows are bound by the starts and ends of cells and by masked edges: six prompts of
+// 500 to 2600 tokens 122, 120 with a window of 1024 (10 blocks for 8 seen), capped at 50
+// too 174, at 20 537.  Few tokens behind long contexts (three chunks of 64 behind 20 to 40
+// thousand): 90, over e4m3 101, with slopes 114.
+//
+// Figures of steps below are of like batches: the prompt of 15999 tokens; six prompts of
+// 522, 1400, 2600, 900, 1800 and 1500 tokens behind 3, 100, 50, 20, 0 and 77; three chunks
+// of 64 behind 20, 30 and 40 thousand; 24 chunks of 1 to 700 tokens behind up to 900.
 #pragma once
 
 #include <atomic>
@@ -860,12 +869,13 @@ __device__ __noinline__ bool rare_row(const PreArgs& a, RareRow& q) {
 }
 
 // SCALED: whether token blocks have scales (they cost a per-tensor cache with slopes
-// 22 %: 154 us instead of 126, three chunks of 64 tokens).  MODE: kPlain (a scale that is
-// no smaller than kLeastScale), kCapped, kBiased (slopes, or another scale), kBoth.  All keep a row's 128 products
-// in registers; what is rare (a product beyond 0.6 of its cap, keys behind the query,
-// steep biases, scales <= 0) is shaped in a loop of its own through TMEM, so that
-// the code that runs stays short: with every case in line a capped prompt of 15999
-// tokens took 3509 us, a biased one 3728, a third of it waits for instructions.
+// 22 %: 154 us instead of 126, three chunks of 64 tokens).  MODE: kPlain (a scale that is no
+// smaller than kLeastScale), kCapped, kBiased (slopes, or another scale), kBoth.  All keep
+// a row's 128 products in registers; what is rare (a product beyond 0.6 of its cap in any
+// row of a warp, a scale far below the cap, keys behind the query under slopes, steep
+// biases, scales <= 0) is shaped in a loop of its own through TMEM, four to five times as
+// slow, so that the code that runs stays short: with every case in line a capped prompt of
+// 15999 tokens took 3509 us, a biased one 3728, a third of it waits for instructions.
 template <int D, int KIND, bool SCALED, int MODE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(const __grid_constant__ PreArgs a) {
     using C = Cfg<D, KIND>;

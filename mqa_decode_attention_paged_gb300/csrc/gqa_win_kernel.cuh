@@ -292,9 +292,10 @@ __device__ __forceinline__ float capped(const WinArgs& a, float x) {
 // MULTI: more than one query position per request.  SHAPED: logits capped by
 // a.cap2 (if > 0) and biased by -slope |p - t| (if a.slopes), in that order, on the
 // accumulators where they lie; instances of their own, so that the others keep their
-// code and registers.  256 lognormal lengths over bf16 with a cap: 496 us, 7.0 TB/s
-// (HBM hides the polynomial); 32 windows of 4096 x 4 positions over e4m3 blocks with
-// slopes: 75 us where the unshaped call takes 69.
+// code and registers.  256 lognormal lengths, one position: over bf16 495 us with a cap,
+// slopes, both or neither, 7.0 TB/s (HBM hides the polynomial); over e4m3 272 (both: 277);
+// over e4m3 / int8 blocks of 16 271, slopes 274 / 272, a cap 281 / 283, both 288 / 294.  32
+// windows of 4096 x 4 positions over e4m3 blocks: unshaped 67, slopes 76, a cap 85.
 template <int D, int KIND, int NHB, bool MULTI, bool SHAPED>
 __global__ void __launch_bounds__(256, win_ctas_per_sm(NHB, D)) gqa_win_kernel(const __grid_constant__ WinArgs a) {
     using C = Cfg<D, KIND, NHB>;

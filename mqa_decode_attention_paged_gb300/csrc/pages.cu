@@ -17,10 +17,10 @@
 // writes the table as well.  Counts are changed by integer atomics and free
 // pages numbered by prefix sums: the result does not depend on any order.
 //
-// Measured: 64 prompts forked 8 ways over 6 layers of e4m3 caches (352 MB written) 86
+// Measured: 64 prompts forked 8 ways over 6 layers of e4m3 caches (352 MB written) 85
 // us, of them 12 the plan; compacting 256 rows over two layers of bf16 caches (318 MB
-// moved) 109 us, 86 % of a copy's rate.  8 beams of 4 over one layer 11.2 us on the GPU and 25
-// to 29 from Python, which is the host's part (allocation 10, the C call 5).
+// moved) 112 us, 84 % of a copy's rate.  8 beams of 4 over one layer 10 us on the GPU and 25
+// to 30 from Python, which is the host's part (allocation 10, the C call 5).
 #include "pages.cuh"
 
 #include <atomic>
