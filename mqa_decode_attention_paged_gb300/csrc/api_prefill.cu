@@ -143,14 +143,25 @@ mqa_status prefill(const void* q, const void* kv_cache, const float* kv_scales, 
     // a block takes longer, 2 and 3 are within 2 % of each other.
     a.cell_cost = 3;
     const double unit = softcap > 0.f ? static_cast<double>(a.sl2) * a.inv_cap2 : 0.0;
-    double power = unit;
-    for (int k = 0; k < mqa::kTanhNearTerms; ++k, power *= unit * unit) a.tanh_raw[k] = static_cast<float>(a.cap2 * mqa::kTanhNear[k] * power);
-    // The slow form for every block where these coefficients would not do: the last one is to be a normal number (full
-    // precision, and infinite times a masked key's infinity; over per-tensor e4m3 k_scale is part of the unit, and with cap
-    // 50 and head size 128 a k_scale of 0.035 or more is fast).  Logits beyond 2^20 are taken relative to the largest
-    // of the same capped values, not to the cap of the largest product, whose rounding they may exceed by more than an
-    // exponential holds.  One prompt of 15999 tokens over e4m3, cap 50, k_scale 0.05: 2673 us, 8499 in the slow form.
-    a.tiny_unit = std::fabs(unit) > 1.0 || !(std::fabs(a.tanh_raw[mqa::kTanhNearTerms - 1]) >= 0x1p-126f) || a.cap2 > 0x1p20f;
+    auto coefficients = [&](double of) {
+        double power = of;
+        for (int k = 0; k < mqa::kTanhNearTerms; ++k, power *= of * of) a.tanh_raw[k] = static_cast<float>(a.cap2 * mqa::kTanhNear[k] * power);
+        // normal numbers (full precision, and infinite times a masked key's infinity)
+        return std::fabs(a.tanh_raw[mqa::kTanhNearTerms - 1]) >= 0x1p-126f;
+    };
+    // Over per-tensor e4m3 k_scale is part of the unit (cap 50, head size 128: k_scales below 0.035): small units leave a power of
+    // two to the products there.  One prompt of 15999 tokens, cap 50: 2600 us, with k_scale 0.02 2536, in the slow form 8450.
+    // (With the same multiplication bf16 takes 2077 instead of 1854, and e4m3 with slopes too 4151 instead of 3784.)
+    a.raw_unit = 1.f;
+    bool fit = coefficients(unit);
+    if (!fit && per_tensor && !slopes && std::fabs(unit) >= 0x1p-60) {
+        a.raw_unit = static_cast<float>(std::ldexp(1.0, std::ilogb(unit)));
+        fit = coefficients(unit / a.raw_unit);
+    }
+    // The slow form for every block where they do not fit.  Logits beyond 2^20 are taken relative to the largest of the same
+    // capped values, not to the cap of the largest product, whose rounding they may exceed by more than an exponential
+    // holds.
+    a.tiny_unit = std::fabs(unit) > 1.0 || !fit || a.cap2 > 0x1p20f;
     a.grid = grid;
     a.cut = num_kv_splits > 1;
     a.withhold = withhold;

@@ -49,7 +49,8 @@ struct PreArgs {
     float out_scale;         // v_scale of a per-tensor e4m3 cache, else 1
     float cap2, inv_cap2;    // softcap * log2(e) and its reciprocal, or 0
     float tanh_c[kTanhTerms], tanh_near[kTanhNearTerms];  // cap2 times kTanh and kTanhNear
-    float tanh_raw[kTanhNearTerms];             // the latter in products: coefficient k times (sl2 / cap2)^(2 k + 1)
+    float tanh_raw[kTanhNearTerms];             // the latter in products times raw_unit: coefficient k times (sl2 / cap2 / raw_unit)^(2 k + 1)
+    float raw_unit;                 // a power of two (1 but over per-tensor e4m3 without slopes)
     bool tiny_unit;                 // .. where these leave the fp32 range, or the cap 2^20
     int num_tokens, batch, Hq, Hkv, grp;
     int tile_tok, tile_rows;  // tokens and rows of a tile: rows = tokens * grp <= 128

@@ -36,7 +36,7 @@
 // for an Inf or NaN, are the rest).  Else the chain from product to softmax to product of
 // each tile, as P lies where S did; where it was profiled no unit is full (64/8 heads x 64
 // 2075: half the products for as many exponentials; slopes 1765, a cap of 50 1859, both
-// 3198; e4m3 1716, block scales 2109, int8 64/8 x 64 2745, e4m3 with a cap 2673).  Blocks
+// 3198; e4m3 1716, block scales 2109, int8 64/8 x 64 2745, e4m3 with a cap 2602).  Blocks
 // that take the slow form (see MODE below) take four to five times as long: caps of 20 and
 // 15, which these logits of deviation 3 reach, 8533 and 8399, slopes up to 17 6028, a
 // negative scale 6249.
@@ -1443,6 +1443,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) gqa_prefill_kernel(
                                 const float2 f = scales(k);
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(e < 16 ? f.x : f.y)));
+                            } else if (KIND == kWinE4m3 && !kBias) {
+                                if (a.raw_unit != 1.f) {
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) put2(x[k], e, mul2(get2(x[k], e), both(a.raw_unit)));
+                                }
                             }
                             cap_chunk(a.tanh_raw, x[k]);
                         }

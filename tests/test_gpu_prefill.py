@@ -474,3 +474,14 @@ def test_caps_over_small_scales_of_the_cache(cap, size):
     """scale k_scale / cap from 1.8e-4 to 3.9e-5, either side of where its ninth power times the cap stops being normal."""
     run([200, 1], [60, 300], cap=cap, size=size, kv="fp8_e4m3")
     run([200, 1], [60, 300], cap=cap, size=size, kv="fp8_e4m3", slopes=True, window=150)
+
+
+@pytest.mark.parametrize("cap", [1e2, 1e3, 1e5, 3e5, 1e9])
+@pytest.mark.parametrize("size", [0.1, 1.0, 30.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_far_above_the_scale_of_the_cache(cap, size, D, monkeypatch):
+    run([200, 1], [60, 300], cap=cap, size=size, kv="fp8_e4m3", D=D, window=200, sinks=3)
+    # With a scale of 1e-5 all weights are alike, and a row's denominator is a sum of up to 300 numbers of one size in four
+    # fp32 chains: 75 additions, each rounded by up to 2^-24 of the sum, 300 2^-26 in lse beside what judge() counts.
+    monkeypatch.setitem(globals(), "judge", lambda out, lse, ref, what, plain=judge: plain(out, lse, (*ref[:3], ref[3] + 300 * 2.0 ** -26), what))
+    run([150, 300], [60, 0], cap=cap, size=size, kv="fp8_e4m3", D=D, prefix=[90, 0], scale=1e-5)
