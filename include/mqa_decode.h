@@ -650,12 +650,15 @@ size_t gqa_prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_s
  *              need one each.
  *   head_size in {64, 128}; num_kv_heads and query heads per KV head up to 128;
  *   num_tokens 0 .. 2^24; batch up to 8192; page_size a multiple of 16;
- *   max_blocks * page_size and num_blocks * page_size < 2^30.  query_start that
- *   descends or leaves [0, num_tokens], or a length out of range, raises
- *   MQA_ERR_DEVICE_CHECK (values are then taken into range; rows that several
- *   requests claim are undefined, and where requests claim more tokens in all
- *   than num_tokens the call may write no row), as does a block id outside
- *   [0, num_blocks) (its tokens are not seen). */
+ *   max_blocks * page_size and num_blocks * page_size < 2^30.  (A request's keys
+ *   are walked by one thread block where they are not cut: from some 2^24 of
+ *   them on, several such walks in a row may outlast a wait of 2 s,
+ *   MQA_ERR_DEVICE_TIMEOUT.)  query_start that descends or leaves
+ *   [0, num_tokens], or a length out of range, raises MQA_ERR_DEVICE_CHECK
+ *   (values are then taken into range; rows that several requests claim are
+ *   undefined, and where requests claim more tokens in all than num_tokens the
+ *   call may write no row), as does a block id outside [0, num_blocks) (its
+ *   tokens are not seen). */
 mqa_status gqa_prefill(const void* q, const void* kv_cache, const float* kv_scales, const int32_t* block_table,
                        const int32_t* seq_lens, const int32_t* query_start, const int32_t* prefix_lens, float scale,
                        float k_scale, float v_scale, float softcap, const float* slopes, int window, int sinks,
